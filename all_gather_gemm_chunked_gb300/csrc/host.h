@@ -1,0 +1,40 @@
+// host.h -- what the host sides of the library share: the thread's last error,
+// the log, TMA descriptor encoding and the current-device guard (host.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace agg {
+
+int log_level();  // AG_GEMM_LOG=0..3 (read once): 1 errors, 2 plans, 3 runs
+void log_msg(int level, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+// Records the thread's last error and returns its code.
+int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int cuda_fail(cudaError_t e, const char* what);
+int last_error();
+const char* last_error_message();
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Tensor of rank 2 to 5, innermost dimension first; zero fill out of bounds.
+int encode_tiled(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank,
+                 const cuuint64_t* dims, const cuuint64_t* strides_bytes, const cuuint32_t* box,
+                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+
+// Makes `dev` current; restores the caller's current device on scope exit.
+struct DeviceGuard {
+  int prev = -1;
+  bool ok = true;
+  explicit DeviceGuard(int dev) {
+    if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
+    if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
+  }
+  ~DeviceGuard() {
+    int cur = -1;
+    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+  }
+};
+
+}  // namespace agg

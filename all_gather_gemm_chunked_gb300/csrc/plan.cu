@@ -5,9 +5,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cstdarg>
-#include <cstdio>
-#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <new>
@@ -15,88 +12,20 @@
 
 #include "ag_gemm.h"
 #include "fused_kernel.cuh"
+#include "host.h"
 #include "schedule.h"
 
 using agg::Geometry;
 
-// ------------------------------------------------------------------ errors, log
+using agg::aligned16;
+using agg::cuda_fail;
+using agg::DeviceGuard;
+using agg::encode_tiled;
+using agg::fail;
+using agg::log_msg;
+
 namespace {
-thread_local int g_last_error = AG_GEMM_OK;
-thread_local char g_last_msg[512] = "";
-
-// AG_GEMM_LOG=0..3 in the environment (read once): 1 errors, 2 plans, 3 runs.
-int log_level() {
-  static const int level = [] {
-    const char* v = std::getenv("AG_GEMM_LOG");
-    if (!v || !*v) return 0;
-    const int l = std::atoi(v);
-    return l < 0 ? 0 : (l > 3 ? 3 : l);
-  }();
-  return level;
-}
-
-void log_msg(int level, const char* fmt, ...) {
-  if (log_level() < level) return;
-  char buf[640];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  std::fprintf(stderr, "[ag_gemm] %s\n", buf);
-}
-
-int fail(int code, const char* fmt, ...) {
-  g_last_error = code;
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_last_msg, sizeof(g_last_msg), fmt, ap);
-  va_end(ap);
-  log_msg(1, "error %d: %s", code, g_last_msg);
-  return code;
-}
-
-int cuda_fail(cudaError_t e, const char* what) {
-  return fail(e == cudaErrorMemoryAllocation ? AG_GEMM_ERR_OOM : AG_GEMM_ERR_CUDA, "%s: %s",
-              what, cudaGetErrorString(e));
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // ------------------------------------------------------------------ TMA descriptors
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
-}
-
-// Tensor, innermost dimension first; 128-byte swizzle, zero fill out of bounds.
-int encode_tiled(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank,
-                 const cuuint64_t* dims, const cuuint64_t* strides_bytes, const cuuint32_t* box,
-                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return fail(AG_GEMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  cuuint32_t estride[3] = {1, 1, 1};
-  CUresult r = fn(map, type, static_cast<cuuint32_t>(rank),
-                  const_cast<void*>(base), dims, strides_bytes, box, estride,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(AG_GEMM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
-  return AG_GEMM_OK;
-}
-
 // 2-byte operands.  bf16 plans use the same descriptors: TMA copies bytes, the
 // element type only fixes the element size, and the zero fill is +0 in both.
 int encode_f16(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
@@ -257,20 +186,6 @@ bool from_public(const ag_gemm_geometry* in, Geometry& g) {
   agg::make_geometry(g, in->n_shards, in->M, in->K, in->N, in->dtype, in->chunk_rows);
   return true;
 }
-
-// Restores the caller's current device on scope exit.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-    if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
-};
 
 }  // namespace
 
@@ -1171,9 +1086,9 @@ int64_t ag_gemm_plan_trace(ag_gemm_plan* plan, ag_gemm_trace_event* out, int64_t
   return static_cast<int64_t>(kept + dropped);
 }
 
-int ag_gemm_last_error(void) { return g_last_error; }
+int ag_gemm_last_error(void) { return agg::last_error(); }
 
-const char* ag_gemm_last_error_message(void) { return g_last_msg; }
+const char* ag_gemm_last_error_message(void) { return agg::last_error_message(); }
 
 }  // extern "C"
 
