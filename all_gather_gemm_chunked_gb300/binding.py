@@ -1,4 +1,4 @@
-"""ctypes binding of libaggemm.so (include/ag_gemm.h).
+"""ctypes binding of libaggemm.so (include/ag_gemm.h, include/ag_moe.h).
 
 Argument marshalling only: every step of the path runs in the CUDA library.
 The functions keep the C names; pointers are passed as Python ints (device
@@ -28,8 +28,12 @@ OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_OOM, ERR_TIMEOUT, ERR_STATE = 0,
 ERROR_NAMES = {ERR_INVALID: "INVALID", ERR_UNSUPPORTED: "UNSUPPORTED", ERR_CUDA: "CUDA",
                ERR_OOM: "OOM", ERR_TIMEOUT: "TIMEOUT", ERR_STATE: "STATE"}
 
+F32, E4M3 = 3, 4  # AG_MOE_F32, AG_MOE_E4M3: beside F16, I8 and BF16
+MAX_EXPERTS, MAX_TOP_K, SCALE_BLOCK = 1024, 32, 128
+
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                       "include", "ag_gemm.h")
+HEADER_MOE = os.path.join(os.path.dirname(HEADER), "ag_moe.h")
 
 
 class AgGemmError(RuntimeError):
@@ -99,6 +103,24 @@ def _load():
         "ag_gemm_plan_set_trace": (i32, [vp, i64]),
         "ag_gemm_plan_set_grid": (i32, [vp, i32]),
         "ag_gemm_plan_trace": (i64, [vp, ctypes.POINTER(TraceEvent), i64]),
+        "ag_moe_route_workspace": (i64, [i64, i32, i32]),
+        "ag_moe_route": (i32, [i64, i32, i32, i32, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp]),
+        "ag_moe_route_backward": (i32, [i64, i32, i32, i32, vp, i64, i32, vp, vp, vp, vp, vp]),
+        "ag_moe_gather": (i32, [i64, i32, i64, i32, vp, i64, vp, vp, vp]),
+        "ag_moe_combine": (i32, [i64, i32, i64, i32, vp, i64, vp, vp, vp, vp]),
+        "ag_moe_combine_backward": (i32, [i64, i32, i64, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp]),
+        "ag_fp8_quantize_rows": (i32, [i64, i64, i32, vp, i64, i64, vp, i32, vp, vp, vp]),
+        "ag_fp8_quantize_weights": (i32, [i32, i64, i64, i32, vp, vp, vp, vp]),
+        "ag_moe_plan_create": (vp, [i32, i64, i64, i32]),
+        "ag_moe_plan_destroy": (None, [vp]),
+        "ag_moe_plan_status": (i32, [vp]),
+        "ag_moe_plan_status_word": (i64, [vp]),
+        "ag_moe_plan_reset": (i32, [vp, vp]),
+        "ag_moe_plan_set_timeout_ns": (i32, [vp, i64]),
+        "ag_moe_forward": (i32, [vp, i64, vp, i64, vp, vp, i64, i64, vp, i64, i32, vp]),
+        "ag_moe_backward_input": (i32, [vp, i64, vp, i64, vp, vp, i64, i64, vp, i64, i32, vp]),
+        "ag_moe_backward_weight": (i32, [vp, i64, vp, i64, vp, i64, vp, vp, i32, vp]),
+        "ag_fp8_forward": (i32, [vp, i64, vp, vp, vp, vp, vp, vp, i64, i32, vp]),
         "ag_gemm_last_error": (i32, []),
         "ag_gemm_last_error_message": (ctypes.c_char_p, []),
     }
@@ -113,10 +135,10 @@ _lib = _load()
 
 
 def header_functions(path: str = HEADER):
-    """Names of the functions include/ag_gemm.h declares."""
+    """Names of the functions a header (include/ag_gemm.h) declares."""
     text = open(path).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(ag_gemm_\w+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(ag_(?:gemm|moe|fp8)_\w+)\s*\(", text)))
 
 
 def library_handle():
@@ -286,3 +308,46 @@ def ag_gemm_last_error() -> int:
 
 def ag_gemm_last_error_message() -> str:
     return (_lib.ag_gemm_last_error_message() or b"").decode()
+
+
+# -- include/ag_moe.h ---------------------------------------------------------
+# The front ends (moe.py, fp8.py) call the library's functions through these: a
+# negative code raises, the others are returned.
+
+def _wrapped(name):
+    fn = getattr(_lib, name)
+
+    def call(*args):
+        rc = fn(*args)
+        if rc < 0:
+            raise _err()
+        return rc
+
+    call.__name__ = name
+    return call
+
+
+(ag_moe_route_workspace, ag_moe_route, ag_moe_route_backward, ag_moe_gather, ag_moe_combine,
+ ag_moe_combine_backward, ag_fp8_quantize_rows, ag_fp8_quantize_weights, ag_moe_plan_reset,
+ ag_moe_plan_set_timeout_ns, ag_moe_plan_status_word, ag_moe_forward, ag_moe_backward_input,
+ ag_moe_backward_weight, ag_fp8_forward) = (_wrapped("ag_" + n) for n in (
+     "moe_route_workspace", "moe_route", "moe_route_backward", "moe_gather", "moe_combine",
+     "moe_combine_backward", "fp8_quantize_rows", "fp8_quantize_weights", "moe_plan_reset",
+     "moe_plan_set_timeout_ns", "moe_plan_status_word", "moe_forward", "moe_backward_input",
+     "moe_backward_weight", "fp8_forward"))
+
+
+def ag_moe_plan_create(E: int, K: int, N: int, dtype: int) -> int:
+    h = _lib.ag_moe_plan_create(E, K, N, dtype)
+    if not h:
+        raise _err()
+    return h
+
+
+def ag_moe_plan_destroy(plan: int) -> None:
+    _lib.ag_moe_plan_destroy(plan)
+
+
+def ag_moe_plan_status(plan: int) -> int:
+    """AG_GEMM_OK or a negative code (not raised, as ag_gemm_plan_status)."""
+    return _lib.ag_moe_plan_status(plan)

@@ -1,0 +1,62 @@
+// experts_kernel.cuh -- parameters shared by the host side (moe.cu) and the
+// kernel of the products grouped by expert (experts_kernel.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace agg {
+
+// The four products of the kernel.  "Wide" is the output's contiguous dimension,
+// the MMA's M; "rows" its N.
+enum ExpertsOp : int {
+  kOpForward = 0,   // y[r][n]  = sum_k x[r][k] w[e][k][n]     wide n, rows r, over k
+  kOpInput = 1,     // dx[r][k] = sum_n dy[r][n] w[e][k][n]    wide k, rows r, over n
+  kOpWeight = 2,    // dw[e][k][n] = sum_r x[r][k] dy[r][n]    wide n, rows k, over e's rows r
+  kOpFp8 = 3,       // y[r][n] with e4m3 operands and scales   wide n, rows r, over k
+};
+
+constexpr int kXWide = 256;    // a pair's tile: 256 of the wide dimension
+constexpr int kXRows = 256;    // and up to 256 rows,
+constexpr int kXFewRows = 64;  // or up to 64 where groups are short
+constexpr int kXRowBoxes = 4;  // box heights of the row operand: 1/4 to 4/4 of half a tile
+constexpr int kXThreads = 320; // TMA warp, MMA warp, 8 epilogue warps
+constexpr int kXGroup = 8;     // row tiles that share the weights they read (tile order)
+
+struct ExpertsParams {
+  CUtensorMap tm_w;              // the wide operand
+  CUtensorMap tm_r[kXRowBoxes];  // the row operand, by box height (weight gradient: the first only)
+  const int32_t* offsets;        // [E + 1], or null: one group of all rows
+  int32_t E;
+  int32_t rows;                  // rows of the inputs
+  int32_t wide;                  // extent of the wide dimension
+  int32_t red;                   // length of the sums (weight gradient: unused)
+  int32_t out_rows;              // weight gradient: output rows per expert (K)
+  int32_t w_blk, r_blk;          // MN-major operand described in blocks of 64 columns (one load), or not (two)
+  int32_t bf16;                  // operands are bfloat16 (otherwise fp16)
+  int32_t out_type;              // ElemType of the output
+  void* out;
+  int64_t ldo;
+  const float* xs;               // e4m3: row scales [KB][rows]
+  const float* ws;               // e4m3: weight scales [E][NB][KB]
+  float* partials;               // split sums: [unit][16 warps][columns][32 lanes]
+  uint32_t* arrivals;            // [tile][16 warps], zero between runs
+  int32_t max_units;             // units the workspace holds (0: never split)
+  uint32_t* status;              // [2]: status word, detail
+  uint64_t timeout_ns;
+};
+
+// A warp's part of a split sum: columns x 32 lanes of floats.
+constexpr int64_t split_unit_bytes(bool few) {
+  return 16 * static_cast<int64_t>(few ? kXFewRows : kXRows) / 2 * 32 * 4;
+}
+
+constexpr uint32_t kStatusOffsets = 16;  // status word: offsets decrease or leave [0, rows]
+
+// Kernel attributes; the number of CTA pairs that are resident at once.
+cudaError_t experts_prepare(int* pairs);
+cudaError_t launch_experts(const ExpertsParams& p, int op, bool few, int grid,
+                           cudaStream_t stream);
+
+}  // namespace agg

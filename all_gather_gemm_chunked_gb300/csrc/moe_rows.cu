@@ -1,0 +1,573 @@
+// moe_rows.cu -- the router (top-k, softmax, expert-sorted layout) and the moves
+// of rows between tokens and experts, with their gradients.
+//
+// All of it is bound by memory, or by latency where the batch is small, so each
+// kernel reads its inputs once, with 16-byte accesses where rows are aligned, and
+// keeps sums in 32-bit registers.  No atomic decides an order: the layout comes
+// from counts and prefix sums, and every sum has a fixed order.
+
+#include <math_constants.h>
+
+#include "moe_rows.cuh"
+#include "moe_types.cuh"
+
+namespace agg {
+
+namespace {
+constexpr uint32_t kAll = 0xffffffffu;
+
+// ------------------------------------------------------------------ router
+// Logits as unsigned keys in the same order; 0 for what is not there.  -0 counts
+// as +0.  Keys up to kKeyNegInf are never chosen.
+constexpr uint32_t kKeyNegInf = 0x007fffffu;
+__device__ __forceinline__ uint32_t logit_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float key_logit(uint32_t key) {
+  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+// One token by one warp: lane holds experts lane, lane + 32, ...; each of the k
+// rounds takes the largest key left (one warp reduction) and the lowest expert
+// that has it (a second one).  Returns, for lane j < k, the j-th choice's expert
+// (-1: none) and writes its weight.
+template <typename T, int VPL>
+__device__ __forceinline__ int choose(const RouteArgs& a, int64_t t, int lane) {
+  const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+  uint32_t key[VPL];
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = i * 32 + lane;
+    float v = -CUDART_INF_F;
+    if (e < a.E) v = Elem<T>::get(row[e]);
+    nan |= v != v;
+    key[i] = (e < a.E && v == v) ? logit_key(v) : 0u;
+  }
+  nan = __any_sync(kAll, nan);
+  float all = 0.0f;  // sum of exp(logit - largest) over all experts
+  uint32_t mine = 0;
+  int expert = -1;
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t best = key[0];
+    int bi = lane;
+#pragma unroll
+    for (int i = 1; i < VPL; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        bi = i * 32 + lane;
+      }
+    const uint32_t top = __reduce_max_sync(kAll, best);
+    if (top <= kKeyNegInf) break;
+    if (j == 0 && !a.normalize) {
+      const float m = key_logit(top);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (key[i] != 0u) all += expf(key_logit(key[i]) - m);
+      all = warp_sum(all);
+    }
+    const int e = static_cast<int>(__reduce_min_sync(
+        kAll, best == top ? static_cast<uint32_t>(bi) : 0xffffffffu));
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (i * 32 + lane == e) key[i] = 0u;
+    if (lane == j) {
+      mine = top;
+      expert = e;
+    }
+  }
+  const float l = key_logit(mine);
+  const float m = __shfl_sync(kAll, l, 0);
+  const float p = expert >= 0 ? expf(l - m) : 0.0f;
+  const float sum = a.normalize ? warp_sum(p) : all;
+  float w = expert >= 0 ? p / sum : 0.0f;
+  if (nan && expert >= 0) w = CUDART_NAN_F;
+  if (lane < a.k) {
+    a.weights[t * a.k + lane] = w;
+    a.experts[t * a.k + lane] = expert;
+  }
+  return expert;
+}
+
+// The tokens of block b and of its warps: contiguous, in order.
+struct Share {
+  int64_t t0, t1;
+};
+__device__ __forceinline__ Share share_of(int64_t first, int64_t end, int64_t part, int64_t parts) {
+  const int64_t n = end - first, per = (n + parts - 1) / parts;
+  const int64_t a = first + part * per, b = a + per;
+  return {a < end ? a : end, b < end ? b : end};
+}
+
+constexpr int kRouteThreads = 1024;
+constexpr int kRouteWarps = kRouteThreads / 32;
+
+// Sum over the block's threads before this one (value of thread e at e).
+__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_sums, int warp,
+                                                    int lane) {
+  uint32_t s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(kAll, s, o);
+    if (lane >= o) s += u;
+  }
+  if (lane == 31) warp_sums[warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    const uint32_t own = warp_sums[lane];
+    uint32_t w = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(kAll, w, o);
+      if (lane >= o) w += u;
+    }
+    warp_sums[lane] = w - own;
+  }
+  __syncthreads();
+  return warp_sums[warp] + s - v;
+}
+
+// Place the block's choices.  A row's place is its expert's first row, plus the
+// expert's choices in earlier blocks, in earlier warps of this block, and in this
+// warp's earlier tokens (a token chooses an expert at most once): counts and
+// prefix sums alone, so the order within an expert is the tokens'.
+// smem: [kRouteWarps][E] uint16 counts (a warp has fewer than 2^16 tokens: T is at
+// most 2^28), then E uint32 first rows, 32 warp sums and the number of rows in use.
+__device__ void place(const RouteArgs& a, int64_t T0, int64_t T1, uint8_t* smem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(smem);
+  uint32_t* base = reinterpret_cast<uint32_t*>(smem + ((kRouteWarps * a.E * 2 + 15) & ~15));
+  uint32_t* sums = base + a.E;
+  for (int i = threadIdx.x; i < kRouteWarps * a.E; i += kRouteThreads) cnt[i] = 0;
+  for (int e = threadIdx.x; e < a.E; e += kRouteThreads) base[e] = 0;
+  __syncthreads();
+  const Share own = share_of(T0, T1, warp, kRouteWarps);
+  for (int64_t t = own.t0; t < own.t1; ++t) {
+    const int e = lane < a.k ? a.experts[t * a.k + lane] : -1;
+    if (e >= 0) cnt[warp * a.E + e] += 1;
+    __syncwarp();
+  }
+  __syncthreads();
+  const int e = threadIdx.x;
+  uint32_t total = 0, before = 0;
+  if (gridDim.x == 1) {
+    if (e < a.E)
+      for (int w = 0; w < kRouteWarps; ++w) total += cnt[w * a.E + e];
+  } else {
+    // groups of E threads read the blocks' counts side by side
+    uint32_t* acc = base;  // total, then the earlier blocks' part
+    const int groups = kRouteThreads / a.E > 0 ? kRouteThreads / a.E : 1;
+    const int g = e / a.E, x = e - g * a.E;
+    uint32_t all = 0, early = 0;
+    if (g < groups && x < a.E)
+#pragma unroll 8
+      for (int b = g; b < static_cast<int>(gridDim.x); b += groups) {
+        const uint32_t c = static_cast<uint32_t>(a.counts[static_cast<int64_t>(b) * a.E + x]);
+        all += c;
+        if (b < static_cast<int>(blockIdx.x)) early += c;
+      }
+    // integer additions: the same in any order
+    if (all) atomicAdd(&acc[x], all);
+    __syncthreads();
+    if (e < a.E) total = acc[e];
+    __syncthreads();
+    if (e < a.E) acc[e] = 0;
+    __syncthreads();
+    if (early) atomicAdd(&acc[x], early);
+    __syncthreads();
+    if (e < a.E) before = acc[e];
+    __syncthreads();
+  }
+  const uint32_t first = block_exclusive(e < a.E ? total : 0u, sums, warp, lane);
+  if (e < a.E) {
+    base[e] = first + before;
+    if (blockIdx.x == 0) a.offsets[e + 1] = static_cast<int32_t>(first + total);
+    if (blockIdx.x == 0 && e == 0) a.offsets[0] = 0;
+    uint32_t run = 0;  // counts to the counts of earlier warps
+    for (int w = 0; w < kRouteWarps; ++w) {
+      const uint32_t c = cnt[w * a.E + e];
+      cnt[w * a.E + e] = static_cast<uint16_t>(run);
+      run += c;
+    }
+    if (e == a.E - 1) sums[32] = first + total;  // rows in use
+  }
+  __syncthreads();
+  for (int64_t t = own.t0; t < own.t1; ++t) {
+    const int x = lane < a.k ? a.experts[t * a.k + lane] : -1;
+    if (lane < a.k) {
+      int32_t place = -1;
+      if (x >= 0) {
+        place = static_cast<int32_t>(base[x] + cnt[warp * a.E + x]);
+        cnt[warp * a.E + x] += 1;
+        a.order[place] = static_cast<int32_t>(t * a.k + lane);
+      }
+      a.slots[t * a.k + lane] = place;
+    }
+    __syncwarp();
+  }
+  for (int64_t s = sums[32] + static_cast<int64_t>(blockIdx.x) * kRouteThreads + threadIdx.x;
+       s < a.T * a.k; s += static_cast<int64_t>(gridDim.x) * kRouteThreads)
+    a.order[s] = -1;
+}
+
+size_t place_smem(int E) { return ((static_cast<size_t>(kRouteWarps) * E * 2 + 15) & ~size_t{15}) + E * 4 + 33 * 4; }
+
+// Up to kOneBlockTokens tokens: choices and layout by one block, one launch.
+template <typename T, int VPL>
+__global__ void __launch_bounds__(kRouteThreads) route_one_kernel(const RouteArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Share own = share_of(0, a.T, warp, kRouteWarps);
+  for (int64_t t = own.t0; t < own.t1; ++t) choose<T, VPL>(a, t, lane);
+  __syncthreads();
+  place(a, 0, a.T, smem);
+}
+
+// More: one kernel chooses and counts the choices of each block's tokens, the
+// next places them.
+template <typename T, int VPL>
+__global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
+  __shared__ uint32_t cnt[kMaxExperts];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < a.E; e += kRouteThreads) cnt[e] = 0;
+  __syncthreads();
+  const Share blk = share_of(0, a.T, blockIdx.x, gridDim.x);
+  const Share own = share_of(blk.t0, blk.t1, warp, kRouteWarps);
+  for (int64_t t = own.t0; t < own.t1; ++t) {
+    const int e = choose<T, VPL>(a, t, lane);
+    if (e >= 0) atomicAdd(&cnt[e], 1u);  // (integer counts: any order)
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kRouteThreads)
+    a.counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = static_cast<int32_t>(cnt[e]);
+}
+
+__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const Share blk = share_of(0, a.T, blockIdx.x, gridDim.x);
+  place(a, blk.t0, blk.t1, smem);
+}
+
+// Gradient of the logits, one warp per token.  normalize: w_j (dw_j - sum w dw) at
+// the chosen experts, 0 elsewhere.  Otherwise p_e ([e chosen] dw - sum w dw) with
+// the softmax p over all experts, which is computed again from the logits.
+template <typename T>
+__global__ void __launch_bounds__(256) route_backward_kernel(const RouteArgs a,
+                                                             const float* __restrict__ dweights,
+                                                             T* __restrict__ dlogits) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x / 32);
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
+       t < a.T; t += warps) {
+    float w = 0.0f, dw = 0.0f;
+    int expert = -1;
+    if (lane < a.k) {
+      w = a.weights[t * a.k + lane];
+      expert = a.experts[t * a.k + lane];
+      dw = expert >= 0 ? dweights[t * a.k + lane] : 0.0f;
+    }
+    const float dot = warp_sum(expert >= 0 ? w * dw : 0.0f);
+    const float d = w * (dw - dot);
+    T* out = dlogits + t * a.E;
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    float m = 0.0f, inv = 0.0f;
+    if (!a.normalize) {
+      m = -CUDART_INF_F;
+      for (int e = lane; e < a.E; e += 32) m = fmaxf(m, Elem<T>::get(row[e]));
+      m = warp_max(m);
+      float s = 0.0f;
+      // (a token with no finite logit has no choices: its gradient is zero)
+      if (m != -CUDART_INF_F)
+        for (int e = lane; e < a.E; e += 32) s += expf(Elem<T>::get(row[e]) - m);
+      s = warp_sum(s);
+      inv = m != -CUDART_INF_F ? 1.0f / s : 0.0f;
+    }
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      float v = 0.0f;
+      if (!a.normalize && e < a.E && m != -CUDART_INF_F)
+        v = -(expf(Elem<T>::get(row[e]) - m) * inv) * dot;
+      for (int j = 0; j < a.k; ++j) {
+        const int ej = __shfl_sync(kAll, expert, j);
+        const float dj = __shfl_sync(kAll, d, j);
+        if (e == ej) v = dj;
+      }
+      if (e < a.E) out[e] = Elem<T>::put(v);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ rows
+constexpr int kRowThreads = 256;
+
+// One block per row of out and kRowThreads * V columns.
+template <typename T, int V>
+__global__ void __launch_bounds__(kRowThreads) gather_kernel(int64_t T_, int k, int64_t H,
+                                                             const T* __restrict__ x, int64_t ldx,
+                                                             const int32_t* __restrict__ order,
+                                                             T* __restrict__ out) {
+  const int64_t s = blockIdx.x;
+  const int64_t c = (static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x) * V;
+  if (c >= H) return;
+  const int32_t o = order[s];
+  const int64_t t = o / k;
+  float f[V] = {};
+  if (o >= 0 && t < T_) load_elems<T, V>(x + t * ldx + c, f);
+  store_elems<T, V>(out + s * H + c, f);
+}
+
+// One block per token and kRowThreads * V columns: the k rows are read with four
+// loads in flight per thread and summed in registers in the order of j.
+template <typename T, int V>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(int64_t T_, int k, int64_t H,
+                                                              const T* __restrict__ y, int64_t ldy,
+                                                              const int32_t* __restrict__ slots,
+                                                              const float* __restrict__ weights,
+                                                              T* __restrict__ out) {
+  const int64_t t = blockIdx.x, S = T_ * k;
+  const int64_t c = (static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x) * V;
+  if (c >= H) return;
+  float acc[V] = {};
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    float f[4][V], w[4];
+    bool in[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u;
+      const int32_t s = j < k ? slots[t * k + j] : -1;
+      in[u] = s >= 0 && s < S;
+      w[u] = in[u] && weights ? weights[t * k + j] : 1.0f;
+      if (in[u]) load_elems<T, V>(y + s * ldy + c, f[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (in[u])
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(w[u], f[u][v], acc[v]);
+  }
+  store_elems<T, V>(out + t * H + c, acc);
+}
+
+// One block per token: dy rows and, over the whole row, the dot products.  Four
+// choices at a time; dout is read again for the next four.
+template <typename T, int V>
+__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(
+    int64_t T_, int k, int64_t H, const T* __restrict__ dout, int64_t ldd,
+    const T* __restrict__ y, int64_t ldy, const int32_t* __restrict__ slots,
+    const float* __restrict__ weights, const int32_t* __restrict__ offsets_end,
+    T* __restrict__ dy, float* __restrict__ dweights) {
+  __shared__ float part[kRowThreads / 32][4];
+  const int64_t t = blockIdx.x, S = T_ * k;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    int64_t s[4];
+    float w[4], dot[4] = {};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u;
+      s[u] = j < k ? slots[t * k + j] : -1;
+      if (s[u] >= S) s[u] = -1;
+      w[u] = s[u] >= 0 ? weights[t * k + j] : 0.0f;
+    }
+    for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < H; c += kRowThreads * V) {
+      float g[V], f[4][V];
+      load_elems<T, V>(dout + t * ldd + c, g);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (s[u] >= 0) load_elems<T, V>(y + s[u] * ldy + c, f[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (s[u] >= 0) {
+          float d[V];
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            dot[u] = fmaf(g[v], f[u][v], dot[u]);
+            d[v] = w[u] * g[v];
+          }
+          store_elems<T, V>(dy + s[u] * H + c, d);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      dot[u] = warp_sum(dot[u]);
+      if (lane == 0) part[warp][u] = dot[u];
+    }
+    __syncthreads();
+    if (threadIdx.x < 4 && j0 + static_cast<int>(threadIdx.x) < k) {
+      float sum = 0.0f;
+      for (int i = 0; i < kRowThreads / 32; ++i) sum += part[i][threadIdx.x];
+      dweights[t * k + j0 + threadIdx.x] = sum;
+    }
+    __syncthreads();
+  }
+  if (offsets_end) {  // rows that belong to no choice
+    const int64_t end = *offsets_end;
+    const float zero[V] = {};
+    for (int64_t r = (end < 0 ? 0 : end) + t; r < S; r += gridDim.x)
+      for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < H; c += kRowThreads * V)
+        store_elems<T, V>(dy + r * H + c, zero);
+  }
+}
+
+bool aligned(const void* p, int64_t ld, int esize) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * esize) % 16 == 0;
+}
+
+template <typename T>
+const void* route_one_fn(int vpl) {
+  switch (vpl) {
+    case 1: return reinterpret_cast<const void*>(&route_one_kernel<T, 1>);
+    case 2: return reinterpret_cast<const void*>(&route_one_kernel<T, 2>);
+    case 4: return reinterpret_cast<const void*>(&route_one_kernel<T, 4>);
+    case 8: return reinterpret_cast<const void*>(&route_one_kernel<T, 8>);
+    case 16: return reinterpret_cast<const void*>(&route_one_kernel<T, 16>);
+    default: return reinterpret_cast<const void*>(&route_one_kernel<T, 32>);
+  }
+}
+template <typename T>
+const void* route_choose_fn(int vpl) {
+  switch (vpl) {
+    case 1: return reinterpret_cast<const void*>(&route_choose_kernel<T, 1>);
+    case 2: return reinterpret_cast<const void*>(&route_choose_kernel<T, 2>);
+    case 4: return reinterpret_cast<const void*>(&route_choose_kernel<T, 4>);
+    case 8: return reinterpret_cast<const void*>(&route_choose_kernel<T, 8>);
+    case 16: return reinterpret_cast<const void*>(&route_choose_kernel<T, 16>);
+    default: return reinterpret_cast<const void*>(&route_choose_kernel<T, 32>);
+  }
+}
+int values_per_lane(int E) { return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
+
+// Calls F<T>() for the element type.
+#define AGG_FOR_TYPE(dtype, ...)                    \
+  [&]() -> cudaError_t {                            \
+    if ((dtype) == kTypeF32) {                      \
+      using T = float;                              \
+      __VA_ARGS__                                   \
+    }                                               \
+    if ((dtype) == kTypeF16) {                      \
+      using T = __half;                             \
+      __VA_ARGS__                                   \
+    }                                               \
+    using T = __nv_bfloat16;                        \
+    __VA_ARGS__                                     \
+  }()
+
+}  // namespace
+
+// One block serves as many tokens as its warps take in four turns; beyond that
+// blocks of at least 32 tokens, one per SM at most.
+constexpr int64_t kOneBlockTokens = 4 * kRouteWarps;
+int route_blocks(int64_t T) {
+  if (T <= kOneBlockTokens) return 1;
+  const int64_t b = (T + 31) / 32;
+  return static_cast<int>(b < 152 ? b : 152);
+}
+
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
+  const int vpl = values_per_lane(a.E), blocks = route_blocks(a.T);
+  const size_t smem = place_smem(a.E);
+  void* args[] = {const_cast<RouteArgs*>(&a)};
+  return AGG_FOR_TYPE(a.dtype, {
+    if (blocks == 1) {
+      const void* fn = route_one_fn<T>(vpl);
+      if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+      }
+      return cudaLaunchKernel(fn, dim3(1), dim3(kRouteThreads), args, smem, stream);
+    }
+    cudaError_t e = cudaLaunchKernel(route_choose_fn<T>(vpl), dim3(blocks), dim3(kRouteThreads),
+                                     args, 0, stream);
+    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024 &&
+        (e = cudaFuncSetAttribute(route_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(smem))) != cudaSuccess)
+      return e;
+    return cudaLaunchKernel(reinterpret_cast<const void*>(&route_place_kernel), dim3(blocks),
+                            dim3(kRouteThreads), args, smem, stream);
+  });
+}
+
+cudaError_t launch_route_backward(const RouteArgs& a, const float* dweights, void* dlogits,
+                                  cudaStream_t stream) {
+  if (a.T == 0) return cudaSuccess;
+  const int64_t want = (a.T + 7) / 8;
+  const int grid = static_cast<int>(want < 152 * 8 ? want : 152 * 8);
+  return AGG_FOR_TYPE(a.dtype, {
+    route_backward_kernel<T><<<grid, 256, 0, stream>>>(a, dweights, static_cast<T*>(dlogits));
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_gather(int64_t T_, int k, int64_t H, int dtype, const void* x, int64_t ldx,
+                          const int32_t* order, void* out, cudaStream_t stream) {
+  if (T_ == 0) return cudaSuccess;
+  return AGG_FOR_TYPE(dtype, {
+    constexpr int V = Elem<T>::kVec;
+    const bool vec = H % V == 0 && aligned(x, ldx, sizeof(T)) && aligned(out, H, sizeof(T));
+    const int64_t per = kRowThreads * (vec ? V : 1);
+    const dim3 grid(static_cast<unsigned>(T_ * k), static_cast<unsigned>((H + per - 1) / per));
+    if (vec)
+      gather_kernel<T, V><<<grid, kRowThreads, 0, stream>>>(T_, k, H, static_cast<const T*>(x),
+                                                            ldx, order, static_cast<T*>(out));
+    else
+      gather_kernel<T, 1><<<grid, kRowThreads, 0, stream>>>(T_, k, H, static_cast<const T*>(x),
+                                                            ldx, order, static_cast<T*>(out));
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_combine(int64_t T_, int k, int64_t H, int dtype, const void* y, int64_t ldy,
+                           const int32_t* slots, const float* weights, void* out,
+                           cudaStream_t stream) {
+  if (T_ == 0) return cudaSuccess;
+  return AGG_FOR_TYPE(dtype, {
+    constexpr int V = Elem<T>::kVec;
+    const bool vec = H % V == 0 && aligned(y, ldy, sizeof(T)) && aligned(out, H, sizeof(T));
+    const int64_t per = kRowThreads * (vec ? V : 1);
+    const dim3 grid(static_cast<unsigned>(T_), static_cast<unsigned>((H + per - 1) / per));
+    if (vec)
+      combine_kernel<T, V><<<grid, kRowThreads, 0, stream>>>(
+          T_, k, H, static_cast<const T*>(y), ldy, slots, weights, static_cast<T*>(out));
+    else
+      combine_kernel<T, 1><<<grid, kRowThreads, 0, stream>>>(
+          T_, k, H, static_cast<const T*>(y), ldy, slots, weights, static_cast<T*>(out));
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_combine_backward(int64_t T_, int k, int64_t H, int dtype, const void* dout,
+                                    int64_t ldd, const void* y, int64_t ldy, const int32_t* slots,
+                                    const float* weights, const int32_t* offsets_end, void* dy,
+                                    float* dweights, cudaStream_t stream) {
+  if (T_ == 0) return cudaSuccess;
+  return AGG_FOR_TYPE(dtype, {
+    constexpr int V = Elem<T>::kVec;
+    const bool vec = H % V == 0 && aligned(y, ldy, sizeof(T)) && aligned(dout, ldd, sizeof(T)) &&
+                     aligned(dy, H, sizeof(T));
+    if (vec)
+      combine_backward_kernel<T, V><<<static_cast<unsigned>(T_), kRowThreads, 0, stream>>>(
+          T_, k, H, static_cast<const T*>(dout), ldd, static_cast<const T*>(y), ldy, slots,
+          weights, offsets_end, static_cast<T*>(dy), dweights);
+    else
+      combine_backward_kernel<T, 1><<<static_cast<unsigned>(T_), kRowThreads, 0, stream>>>(
+          T_, k, H, static_cast<const T*>(dout), ldd, static_cast<const T*>(y), ldy, slots,
+          weights, offsets_end, static_cast<T*>(dy), dweights);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace agg

@@ -1,0 +1,48 @@
+// moe_rows.cuh -- launchers of the router and of the kernels that move rows
+// between tokens and experts (moe_rows.cu), and of the 8-bit quantisation
+// (fp8_quant.cu).  Arguments as in ag_moe.h, checked by the caller.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace agg {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 32;
+constexpr int kScaleBlock = 128;
+enum ElemType : int { kTypeF16 = 0, kTypeBf16 = 2, kTypeF32 = 3, kTypeE4m3 = 4 };
+
+struct RouteArgs {
+  const void* logits;
+  int64_t T, ld;
+  int E, k, dtype, normalize;
+  float* weights;
+  int32_t* experts;
+  int32_t* offsets;
+  int32_t* order;
+  int32_t* slots;
+  int32_t* counts;  // [blocks][E], of more than one block
+};
+int route_blocks(int64_t T);
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
+cudaError_t launch_route_backward(const RouteArgs& a, const float* dweights, void* dlogits,
+                                  cudaStream_t stream);
+
+cudaError_t launch_gather(int64_t T, int k, int64_t H, int dtype, const void* x, int64_t ldx,
+                          const int32_t* order, void* out, cudaStream_t stream);
+cudaError_t launch_combine(int64_t T, int k, int64_t H, int dtype, const void* y, int64_t ldy,
+                           const int32_t* slots, const float* weights, void* out,
+                           cudaStream_t stream);
+cudaError_t launch_combine_backward(int64_t T, int k, int64_t H, int dtype, const void* dout,
+                                    int64_t ldd, const void* y, int64_t ldy, const int32_t* slots,
+                                    const float* weights, const int32_t* offsets_end, void* dy,
+                                    float* dweights, cudaStream_t stream);
+
+cudaError_t launch_quantize_rows(int64_t rows, int64_t K, int dtype, const void* x, int64_t ldx,
+                                 int64_t src_rows, const int32_t* order, int k, void* q,
+                                 float* scales, cudaStream_t stream);
+cudaError_t launch_quantize_weights(int E, int64_t K, int64_t N, int dtype, const void* w,
+                                    void* q, float* scales, cudaStream_t stream);
+
+}  // namespace agg
