@@ -93,6 +93,14 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// Arrive on a barrier of either CTA of the pair without a cluster-scope release:
+// for arrivals that publish no memory writes (an accumulator that has been read:
+// tcgen05 fences order that).  The release waits for the warp's earlier stores and
+// loads, about a microsecond under load: too long once per k-block.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // ------------------------------------------------------------------ work
 // A unit of work, the same for every role of both CTAs.
 struct Unit {
@@ -296,7 +304,7 @@ __device__ void tma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
         } else if (rank == 0) {
           mbar_arrive_expect_tx(&ring.full[stage], 2 * (kWBytes + r_tx));
         } else if (OP == kOpWeight) {
-          mbar_arrive_cluster(bar);
+          mbar_arrive_pair(bar);
         }
         if constexpr (OP == kOpForward) {
           load_mn(wd, &p.tm_w, bar, p.w_blk, n, kb * 64, u.e, 2);
@@ -521,7 +529,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Schedule<OP, BN>& sc
             if (c == c_n - 1) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(tempty0 + (acc & 1u) * 8);
+              if (lane == 0) mbar_arrive_pair(tempty0 + (acc & 1u) * 8);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -563,7 +571,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Schedule<OP, BN>& sc
         if (c == c_n - 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty0 + (acc & 1u) * 8);
+          if (lane == 0) mbar_arrive_pair(tempty0 + (acc & 1u) * 8);
         }
         float v[16];
 #pragma unroll

@@ -129,15 +129,14 @@ cudaError_t launch_quantize_rows(int64_t rows, int64_t K, int dtype, const void*
                   static_cast<unsigned>((K + 256 * kQuantSteps - 1) / (256 * kQuantSteps)));
   uint8_t* out = static_cast<uint8_t*>(q);
   if (dtype == kTypeF32)
-    quantize_rows_kernel<float><<<grid, 256, 0, stream>>>(
+    return launch(quantize_rows_kernel<float>, dim3(grid), 256, stream, 
         rows, K, static_cast<const float*>(x), ldx, src_rows, order, k, out, scales);
   else if (dtype == kTypeF16)
-    quantize_rows_kernel<__half><<<grid, 256, 0, stream>>>(
+    return launch(quantize_rows_kernel<__half>, dim3(grid), 256, stream, 
         rows, K, static_cast<const __half*>(x), ldx, src_rows, order, k, out, scales);
   else
-    quantize_rows_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(
+    return launch(quantize_rows_kernel<__nv_bfloat16>, dim3(grid), 256, stream, 
         rows, K, static_cast<const __nv_bfloat16*>(x), ldx, src_rows, order, k, out, scales);
-  return cudaGetLastError();
 }
 
 cudaError_t launch_quantize_weights(int E, int64_t K, int64_t N, int dtype, const void* w,
@@ -146,13 +145,12 @@ cudaError_t launch_quantize_weights(int E, int64_t K, int64_t N, int dtype, cons
   uint8_t* out = static_cast<uint8_t*>(q);
   const unsigned grid = static_cast<unsigned>(blocks);
   if (dtype == kTypeF32)
-    quantize_weights_kernel<float><<<grid, 256, 0, stream>>>(K, N, static_cast<const float*>(w), out, scales);
+    return launch(quantize_weights_kernel<float>, dim3(grid), 256, stream, K, N, static_cast<const float*>(w), out, scales);
   else if (dtype == kTypeF16)
-    quantize_weights_kernel<__half><<<grid, 256, 0, stream>>>(K, N, static_cast<const __half*>(w), out, scales);
+    return launch(quantize_weights_kernel<__half>, dim3(grid), 256, stream, K, N, static_cast<const __half*>(w), out, scales);
   else
-    quantize_weights_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(
+    return launch(quantize_weights_kernel<__nv_bfloat16>, dim3(grid), 256, stream, 
         K, N, static_cast<const __nv_bfloat16*>(w), out, scales);
-  return cudaGetLastError();
 }
 
 }  // namespace agg

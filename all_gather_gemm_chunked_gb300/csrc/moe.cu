@@ -209,15 +209,22 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   const int64_t wide_tiles = (x.wide + agg::kXWide - 1) / agg::kXWide;
   if (row_tiles * wide_tiles >= (1LL << 30))
     return fail(AG_GEMM_ERR_UNSUPPORTED, "more than 2^30 tiles");
-  cudaError_t e;
-  if (p->has_run && p->last_stream != stream &&
+  // A captured run is ordered by its graph: an event of the stream outside cannot be
+  // waited on there, nor one of the graph outside.
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(stream, &capture);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+  const bool captured = capture != cudaStreamCaptureStatusNone;
+  if (!captured && p->has_run && p->last_stream != stream &&
       (e = cudaStreamWaitEvent(stream, p->done, 0)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamWaitEvent");
   if ((e = agg::launch_experts(x, op, few, 2 * p->pairs, stream)) != cudaSuccess)
     return cuda_fail(e, "experts kernel launch");
-  if ((e = cudaEventRecord(p->done, stream)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
-  p->last_stream = stream;
-  p->has_run = true;
+  if (!captured) {
+    if ((e = cudaEventRecord(p->done, stream)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
+    p->last_stream = stream;
+    p->has_run = true;
+  }
   log_msg(3, "plan %p: experts product %d enqueued, %d rows", static_cast<void*>(p), op, x.rows);
   return AG_GEMM_OK;
 }

@@ -507,8 +507,7 @@ cudaError_t launch_route_backward(const RouteArgs& a, const float* dweights, voi
   const int64_t want = (a.T + 7) / 8;
   const int grid = static_cast<int>(want < 152 * 8 ? want : 152 * 8);
   return AGG_FOR_TYPE(a.dtype, {
-    route_backward_kernel<T><<<grid, 256, 0, stream>>>(a, dweights, static_cast<T*>(dlogits));
-    return cudaGetLastError();
+    return launch(route_backward_kernel<T>, dim3(grid), 256, stream, a, dweights, static_cast<T*>(dlogits));
   });
 }
 
@@ -521,12 +520,11 @@ cudaError_t launch_gather(int64_t T_, int k, int64_t H, int dtype, const void* x
     const int64_t per = kRowThreads * (vec ? V : 1);
     const dim3 grid(static_cast<unsigned>(T_ * k), static_cast<unsigned>((H + per - 1) / per));
     if (vec)
-      gather_kernel<T, V><<<grid, kRowThreads, 0, stream>>>(T_, k, H, static_cast<const T*>(x),
+      return launch(gather_kernel<T, V>, dim3(grid), kRowThreads, stream, T_, k, H, static_cast<const T*>(x),
                                                             ldx, order, static_cast<T*>(out));
     else
-      gather_kernel<T, 1><<<grid, kRowThreads, 0, stream>>>(T_, k, H, static_cast<const T*>(x),
+      return launch(gather_kernel<T, 1>, dim3(grid), kRowThreads, stream, T_, k, H, static_cast<const T*>(x),
                                                             ldx, order, static_cast<T*>(out));
-    return cudaGetLastError();
   });
 }
 
@@ -540,12 +538,11 @@ cudaError_t launch_combine(int64_t T_, int k, int64_t H, int dtype, const void* 
     const int64_t per = kRowThreads * (vec ? V : 1);
     const dim3 grid(static_cast<unsigned>(T_), static_cast<unsigned>((H + per - 1) / per));
     if (vec)
-      combine_kernel<T, V><<<grid, kRowThreads, 0, stream>>>(
+      return launch(combine_kernel<T, V>, dim3(grid), kRowThreads, stream, 
           T_, k, H, static_cast<const T*>(y), ldy, slots, weights, static_cast<T*>(out));
     else
-      combine_kernel<T, 1><<<grid, kRowThreads, 0, stream>>>(
+      return launch(combine_kernel<T, 1>, dim3(grid), kRowThreads, stream, 
           T_, k, H, static_cast<const T*>(y), ldy, slots, weights, static_cast<T*>(out));
-    return cudaGetLastError();
   });
 }
 
@@ -559,14 +556,13 @@ cudaError_t launch_combine_backward(int64_t T_, int k, int64_t H, int dtype, con
     const bool vec = H % V == 0 && aligned(y, ldy, sizeof(T)) && aligned(dout, ldd, sizeof(T)) &&
                      aligned(dy, H, sizeof(T));
     if (vec)
-      combine_backward_kernel<T, V><<<static_cast<unsigned>(T_), kRowThreads, 0, stream>>>(
+      return launch(combine_backward_kernel<T, V>, dim3(static_cast<unsigned>(T_)), kRowThreads, stream, 
           T_, k, H, static_cast<const T*>(dout), ldd, static_cast<const T*>(y), ldy, slots,
           weights, offsets_end, static_cast<T*>(dy), dweights);
     else
-      combine_backward_kernel<T, 1><<<static_cast<unsigned>(T_), kRowThreads, 0, stream>>>(
+      return launch(combine_backward_kernel<T, 1>, dim3(static_cast<unsigned>(T_)), kRowThreads, stream, 
           T_, k, H, static_cast<const T*>(dout), ldd, static_cast<const T*>(y), ldy, slots,
           weights, offsets_end, static_cast<T*>(dy), dweights);
-    return cudaGetLastError();
   });
 }
 

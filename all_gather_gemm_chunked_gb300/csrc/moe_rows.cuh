@@ -13,6 +13,17 @@ constexpr int kMaxTopK = 32;
 constexpr int kScaleBlock = 128;
 enum ElemType : int { kTypeF16 = 0, kTypeBf16 = 2, kTypeF32 = 3, kTypeE4m3 = 4 };
 
+// A launch whose own error is returned (cudaGetLastError would also return an
+// earlier one's).
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 struct RouteArgs {
   const void* logits;
   int64_t T, ld;

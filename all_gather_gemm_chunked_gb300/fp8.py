@@ -14,7 +14,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B_
-from .moe import _ExpertsPlan, _on, _plain, _raw_stream, _rows, _type, _TYPES
+from .moe import _current_stream, _ExpertsPlan, _on, _plain, _rows, _type, _TYPES
 
 E4M3 = torch.float8_e4m3fn
 
@@ -28,6 +28,8 @@ def quantize_rows(x: torch.Tensor, routing=None, stream=None):
     each 128 columns s = max(largest magnitude / 448, 2^-126) and code = e4m3(x * (1 / s)),
     rounded to float at each step, the code to the nearest, ties to even.  With a
     ``moe.Routing`` the rows are the experts' rows of x, as ``moe.gather`` gives them."""
+    if stream is not None:
+        return _on(stream, quantize_rows, x, routing)
     code, ld = _type(x, "x"), _rows(x, "x")
     src, K = x.shape
     rows, order, k = src, None, 1
@@ -35,11 +37,10 @@ def quantize_rows(x: torch.Tensor, routing=None, stream=None):
         k = routing.slots.shape[1]
         rows = src * k
         order = _plain(routing.order, "routing.order", torch.int32, (rows,))
-    with _on(stream):
-        q = torch.empty((rows, K), dtype=E4M3, device=x.device)
-        s = torch.empty((_blocks(K), rows), dtype=torch.float32, device=x.device)
-        B_.ag_fp8_quantize_rows(rows, K, code, x.data_ptr(), ld, src, order, k, q.data_ptr(),
-                                s.data_ptr(), _raw_stream(stream))
+    q = torch.empty((rows, K), dtype=E4M3, device=x.device)
+    s = torch.empty((_blocks(K), rows), dtype=torch.float32, device=x.device)
+    B_.ag_fp8_quantize_rows(rows, K, code, x.data_ptr(), ld, src, order, k, q.data_ptr(), s.data_ptr(),
+                            _current_stream(x.get_device()))
     return q, s
 
 
@@ -47,17 +48,18 @@ def quantize_weights(w: torch.Tensor, stream=None):
     """(codes (..., N, K) e4m3, scales (..., ceil(N / 128), ceil(K / 128)) float32) of
     weights (E, K, N) or (K, N): one scale for each 128 x 128 block, the codes laid out
     along K as the product reads them."""
+    if stream is not None:
+        return _on(stream, quantize_weights, w)
     code = _type(w, "w")
     if w.dim() not in (2, 3) or not w.is_contiguous():
         raise ValueError("w must be a contiguous (E, K, N) or (K, N) tensor")
     E = w.shape[0] if w.dim() == 3 else 1
     K, N = w.shape[-2:]
     lead = tuple(w.shape[:-2])
-    with _on(stream):
-        q = torch.empty(lead + (N, K), dtype=E4M3, device=w.device)
-        s = torch.empty(lead + (_blocks(N), _blocks(K)), dtype=torch.float32, device=w.device)
-        B_.ag_fp8_quantize_weights(E, K, N, code, w.data_ptr(), q.data_ptr(), s.data_ptr(),
-                                   _raw_stream(stream))
+    q = torch.empty(lead + (N, K), dtype=E4M3, device=w.device)
+    s = torch.empty(lead + (_blocks(N), _blocks(K)), dtype=torch.float32, device=w.device)
+    B_.ag_fp8_quantize_weights(E, K, N, code, w.data_ptr(), q.data_ptr(), s.data_ptr(),
+                               _current_stream(w.get_device()))
     return q, s
 
 
@@ -68,21 +70,26 @@ class Fp8Linear(_ExpertsPlan):
     blocks in 32-bit registers.  Forward only: training goes through moe.Experts."""
 
     def __init__(self, K: int, N: int, n_experts: int = 1):
+        self._xs_blocks = _blocks(K)
+        self._w_shape, self._ws_shape = (N, K), (_blocks(N), _blocks(K))
         super().__init__(n_experts, K, N, B_.E4M3)
 
     def forward(self, xq, xs, wq, ws, offsets=None, out=None, out_dtype=torch.bfloat16,
                 stream=None) -> torch.Tensor:
-        rows, E, K, N = xq.shape[0], self.n_experts, self.K, self.N
-        lead = (E,) if wq.dim() == 3 else ()
-        if not lead and E != 1:
-            raise ValueError(f"wq must have shape {(E, N, K)}, got {tuple(wq.shape)}")
-        a = _plain(xq, "xq", E4M3, (rows, K))
-        b = _plain(xs, "xs", torch.float32, (_blocks(K), rows))
-        c = _plain(wq, "wq", E4M3, lead + (N, K))
-        d = _plain(ws, "ws", torch.float32, lead + (_blocks(N), _blocks(K)))
+        if stream is not None:
+            return _on(stream, self.forward, xq, xs, wq, ws, offsets, out, out_dtype)
+        rows, N = xq.shape[0], self.N
+        lead = () if self.n_experts == 1 and wq.dim() == 2 else (self.n_experts,)
+        a = _plain(xq, "xq", E4M3, (rows, self.K))
+        b = _plain(xs, "xs", torch.float32, (self._xs_blocks, rows))
+        c = _plain(wq, "wq", E4M3, lead + self._w_shape)
+        d = _plain(ws, "ws", torch.float32, lead + self._ws_shape)
         off = self._offsets(offsets)
-        with _on(stream):
-            out = self._out(out, (rows, N), out_dtype, xq.device, "out")
-            B_.ag_fp8_forward(self.handle, rows, a, b, off, c, d, out.data_ptr(),
-                              _rows(out, "out"), _TYPES.get(out_dtype, -1), _raw_stream(stream))
+        if out is None:
+            out, ldo = torch.empty((rows, N), dtype=out_dtype, device=xq.device), N
+        else:
+            out = self._out(out, (rows, N), out_dtype, xq.device)
+            ldo = _rows(out, "out")
+        B_.ag_fp8_forward(self.handle, rows, a, b, off, c, d, out.data_ptr(), ldo,
+                          _TYPES.get(out_dtype, -1), _current_stream(xq.get_device()))
         return out

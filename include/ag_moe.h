@@ -109,7 +109,9 @@ int ag_fp8_quantize_weights(int E, int64_t K, int64_t N, int dtype, const void *
  * A plan serves the products of one layer's experts: E weight matrices K x N.
  * dtype AG_GEMM_F16 or AG_GEMM_BF16 (K, N multiples of 8), or AG_MOE_E4M3 (K % 16
  * == 0, N % 8 == 0).  It owns the workspace of the products that split K and the
- * status word; runs on one plan are serialised as those of ag_gemm.h are.
+ * status word; runs on one plan are serialised as those of ag_gemm.h are.  Runs may be
+ * captured into a CUDA graph; a replay is then the caller's to keep apart from the
+ * plan's other runs, and to wait for before the status is read.
  *
  * offsets are the E + 1 row offsets on the device (NULL: one group of all rows,
  * E must be 1).  They must not decrease and must lie within [0, rows]; otherwise
