@@ -20,7 +20,9 @@
 //
 //   warp 0      TMA: streams k-blocks of both operands into a ring of stages
 //   warp 1      MMA (even CTA, one thread); owns the TMEM allocation
-//   warps 2-9   epilogue: TMEM lane quadrant warp % 4, half of the tile's columns
+//   warps 2-17  epilogue: TMEM lane quadrant warp % 4, a quarter of the tile's columns
+//   warp 18     weight gradient: zeros over the rows behind a group's end;
+//               e4m3: the scales of each k-block into shared memory
 //
 // Work: tiles in expert order, and inside an expert in groups of 8 row tiles by all
 // wide tiles, so that the tiles in flight share operands in L2.  Unit u of pair p is
@@ -30,9 +32,13 @@
 // and the warp that arrives last adds the S parts in their order, so that nobody
 // waits and the result does not depend on the order of arrival.
 //
-// e4m3: scales differ per 128 along the sum, so each k-block's sum leaves TMEM and
-// is multiplied and added into 32-bit registers (128 columns a thread); two
-// accumulators alternate, and the MMA runs on meanwhile.
+// Sums leave TMEM in segments and are added in 32-bit registers (64 columns a
+// thread); two accumulators alternate, and the MMA runs on meanwhile.  A segment is
+//   e4m3           one k-block: its sum is multiplied by both operands' scales,
+//   fp32 outputs   8 k-blocks: the tensor core's additions lose about a last bit
+//                  each, so the error of one long accumulation grows with its length
+//                  (1.1e-6 of the result over 1024 terms, %ERR% in segments),
+//   16-bit outputs the whole sum (the rounding of the output hides that error).
 //
 // Rows beyond a group's end belong to the next group: they are multiplied along and
 // not stored (rows on the N side do not mix).  In the weight gradient they would
@@ -61,10 +67,11 @@ __host__ __device__ constexpr int r_bytes(int BN) { return rows_per_cta(BN) * 12
 // Stages that fit: 6 of 32 KB, or 10 of 20 KB for short row tiles, where the bytes
 // in flight are the weights' alone.
 __host__ __device__ constexpr int stages_of(int BN) { return BN == kXRows ? 6 : 10; }
-constexpr int kScaleBytes = 8 * 2 * 128 * 4;  // e4m3: each epilogue warp's row scales, two k-blocks
+constexpr int kScaleSlots = 4;  // e4m3: k-blocks whose scales are held
+constexpr int kScaleBytes = kScaleSlots * kXRows * 4;
 constexpr int kTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) & ~15;
 __host__ __device__ constexpr int smem_bytes(int BN, bool fp8) {
-  return stages_of(BN) * (kWBytes + r_bytes(BN)) + (fp8 ? kScaleBytes : 0) + kTableBytes + 512 +
+  return stages_of(BN) * (kWBytes + r_bytes(BN)) + (fp8 ? kScaleBytes : 0) + kTableBytes + 512 /*barriers*/ +
          1024 /*alignment*/;
 }
 static_assert(smem_bytes(kXRows, true) <= 227 * 1024 && smem_bytes(kXFewRows, true) <= 227 * 1024,
@@ -99,6 +106,36 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m
 // loads, about a microsecond under load: too long once per k-block.
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Two 32-bit sums in one instruction (the epilogue issues one per two columns).
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  lo = __uint_as_float(a);
+  hi = __uint_as_float(b);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 32 TMEM lanes x 8 columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 
 // ------------------------------------------------------------------ work
@@ -223,10 +260,10 @@ struct Schedule {
 template <int BN>
 __device__ bool load_table(const ExpertsParams& p, int32_t* off, int32_t* pre, int32_t* flag) {
   if (threadIdx.x == 0) *flag = 0;
-  for (int e = threadIdx.x; e <= p.E; e += kXThreads)
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
     off[e] = p.offsets ? p.offsets[e] : (e == 0 ? 0 : p.rows);
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kXThreads)
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x)
     if (off[e] < 0 || off[e + 1] < off[e] || off[e + 1] > p.rows) *flag = 1;
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
@@ -255,8 +292,11 @@ struct Ring {
   uint64_t* full;   // the pair's bytes are counted on the even CTA's
   uint64_t* empty;
   uint64_t* tfull;  // accumulators, on both CTAs
-  uint64_t* tempty; // on the even CTA: 16 epilogue warps
-  uint64_t* tail;   // weight gradient: this CTA's last k-block of a group
+  uint64_t* tempty; // on the even CTA: the epilogue warps of both
+  uint64_t* tail;   // weight gradient, by stage: this CTA's last k-block of a group
+  uint64_t* sfull;  // e4m3: scales of a k-block, by slot
+  uint64_t* sempty; // e4m3: this CTA's epilogue warps are through with them
+  float* scales;    // [kScaleSlots][kXRows]
   volatile int* abort;
 };
 
@@ -278,9 +318,9 @@ __device__ void tma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
                          uint32_t rank, int lane) {
   constexpr int kStagesX = stages_of(BN);
   const uint32_t full0 = mapa_shared(smem_u32(ring.full), 0);
-  const uint32_t tail_bar = mapa_shared(smem_u32(ring.tail), rank);
+  const uint32_t tail0 = mapa_shared(smem_u32(ring.tail), rank);
   int stage = 0;
-  uint32_t phase = 0, tails = 0, issued = 0, issued_phase = 0;
+  uint32_t phase = 0, issued = 0, issued_phase = 0;
   bool ok = true;
   Unit u;
   for (int32_t i = 0; ok && sch.get(i, u); ++i) {
@@ -299,8 +339,8 @@ __device__ void tma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
       uint8_t* rd = ring.r + stage * r_bytes(BN);
       if (lane == 0) {
         if (tail) {
-          bar = tail_bar;
-          mbar_arrive_expect_tx(ring.tail, kWBytes + r_tx);
+          bar = tail0 + stage * 8;  // counted here: zero_role passes it on
+          mbar_arrive_expect_tx(&ring.tail[stage], kWBytes + r_tx);
         } else if (rank == 0) {
           mbar_arrive_expect_tx(&ring.full[stage], 2 * (kWBytes + r_tx));
         } else if (OP == kOpWeight) {
@@ -324,25 +364,6 @@ __device__ void tma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
         }
       }
-      if (OP == kOpWeight && tail) {
-        // this CTA's rows have landed: zeros over the rows of the next group, up
-        // to the end of the last 16 that the MMA reads
-        ok = mbar_wait(ring.tail, tails & 1u, p.timeout_ns, ring.abort, p.status);
-        ++tails;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const int valid = u.red_rows - kb * 64, end = (valid + 15) & ~15;
-        const int n16 = (end - valid) * 8;  // 16-byte pieces per block of 64 columns
-        for (int j = lane; j < 4 * n16; j += 32) {
-          const int blk = j / n16, o = valid * 128 + (j - blk * n16) * 16;
-          uint8_t* base = blk < 2 ? wd + blk * (64 * 128) : rd + (blk - 2) * (64 * 128);
-          *reinterpret_cast<uint4*>(base + o) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(full0 + stage * 8);
-        __syncwarp();
-      }
       if (++stage == kStagesX) {
         stage = 0;
         phase ^= 1u;
@@ -361,6 +382,88 @@ __device__ void tma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
   __syncwarp();
 }
 
+// ------------------------------------------------------------------ zeros (weight gradient)
+// The last k-block of a group that ends inside it: once this CTA's part has landed,
+// zeros over the rows of the next group, up to the end of the last 16 that the MMA
+// reads; then the k-block is passed on.  A warp of its own: the TMA warp, waiting for
+// its own loads here, would leave the ring to run dry once per tile.
+template <int BN>
+__device__ void zero_role(const ExpertsParams& p, const Schedule<kOpWeight, BN>& sch,
+                          const Ring& ring, uint32_t rank, int lane) {
+  constexpr int kStagesX = stages_of(BN);
+  const uint32_t full0 = mapa_shared(smem_u32(ring.full), 0);
+  uint32_t blocks = 0, used = 0;  // k-blocks so far; bit s: parity of stage s's tails
+  Unit u;
+  for (int32_t i = 0; sch.get(i, u); ++i) {
+    blocks += static_cast<uint32_t>(u.kb1);
+    const int valid = u.red_rows & 63;
+    if (valid == 0) continue;
+    const uint32_t stage = (blocks - 1) % kStagesX;
+    bool ok = mbar_wait(&ring.tail[stage], (used >> stage) & 1u, p.timeout_ns, ring.abort, p.status);
+    used ^= 1u << stage;
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) {
+      if (lane == 0) {
+        set_status(p.status, kStatusPipelineTimeout, 0x400u | rank);
+        *ring.abort = 1;
+      }
+      break;
+    }
+    const int n16 = (((valid + 15) & ~15) - valid) * 8;  // 16-byte pieces per block of 64 columns
+    for (int j = lane; j < 4 * n16; j += 32) {
+      const int blk = j / n16, o = valid * 128 + (j - blk * n16) * 16;
+      uint8_t* base = blk < 2 ? ring.w + stage * kWBytes + blk * (64 * 128)
+                              : ring.r + stage * r_bytes(BN) + (blk - 2) * (64 * 128);
+      *reinterpret_cast<uint4*>(base + o) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(full0 + stage * 8);
+    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------------ scales (e4m3)
+// For each k-block the scales of the tile's rows times this CTA's weights' scale (its
+// 128 of the wide dimension are one block), a few k-blocks ahead of the epilogue.
+template <int BN>
+__device__ void scale_role(const ExpertsParams& p, const Schedule<kOpFp8, BN>& sch,
+                           const Ring& ring, uint32_t rank, int lane) {
+  constexpr int kPer = BN / 32;
+  uint32_t n = 0;  // k-blocks so far
+  bool ok = true;
+  Unit u;
+  for (int32_t i = 0; ok && sch.get(i, u); ++i) {
+    const int32_t NB = (p.wide + 127) / 128, nb = u.n0 / 128 + static_cast<int>(rank);
+    const float* ws = p.ws + (static_cast<int64_t>(u.e) * NB + (nb < NB ? nb : NB - 1)) * sch.KB;
+    const float* xs = p.xs + u.row0 + lane;
+    float x[kPer], w = 0.0f;
+    auto fetch = [&](int32_t kb) {
+      w = __ldg(ws + kb);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        x[j] = j * 32 + lane < u.cnt ? __ldg(xs + static_cast<int64_t>(kb) * p.rows + j * 32) : 0.0f;
+    };
+    fetch(u.kb0);
+    for (int32_t kb = u.kb0; kb < u.kb1; ++kb, ++n) {
+      const uint32_t slot = n % kScaleSlots;
+      ok = mbar_wait(&ring.sempty[slot], ((n / kScaleSlots) & 1u) ^ 1u, p.timeout_ns, ring.abort,
+                     p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) ring.scales[slot * kXRows + j * 32 + lane] = x[j] * w;
+      if (kb + 1 < u.kb1) fetch(kb + 1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.sfull[slot]);
+    }
+  }
+  if (!ok && lane == 0) {
+    set_status(p.status, kStatusPipelineTimeout, 0x500u | rank);
+    *ring.abort = 1;
+  }
+}
+
 // ------------------------------------------------------------------ MMA (one thread)
 template <int OP, int BN>
 __device__ void mma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, const Ring& ring,
@@ -376,10 +479,12 @@ __device__ void mma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
   for (int32_t i = 0; ok && sch.get(i, u); ++i) {
     const uint32_t idesc = idesc_f16_f32(kXWide, u.w, kWMn, kRMn) |
                            (OP != kOpFp8 && p.bf16 ? kIdescAbBf16 : 0u);
+    int32_t left = 0;  // k-blocks left of the segment
     for (int32_t kb = u.kb0; kb < u.kb1; ++kb) {
       const uint32_t d = tmem + (acc & 1u) * 256u;
-      const bool first = OP == kOpFp8 || kb == u.kb0;
+      const bool first = OP == kOpFp8 || left == 0;
       if (first) {
+        left = p.segment;
         if (!(ok = mbar_wait(&ring.tempty[acc & 1u], ((acc >> 1) & 1u) ^ 1u, p.timeout_ns,
                              ring.abort, p.status)))
           break;
@@ -419,7 +524,8 @@ __device__ void mma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
         stage = 0;
         phase ^= 1u;
       }
-      if (OP == kOpFp8 || kb == u.kb1 - 1) {
+      if (OP == kOpFp8 || --left == 0 || kb == u.kb1 - 1) {
+        left = 0;
         mma_commit_pair_both(&ring.tfull[acc & 1u]);
         ++acc;
       }
@@ -432,32 +538,30 @@ __device__ void mma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
 }
 
 // ------------------------------------------------------------------ epilogue
-// 16 rows of one output column per lane.
+// 8 rows of one output column per lane.
 struct Out {
   void* base;
-  int64_t ldo;
+  int64_t ldo, row0, col;
   int type;
   bool col_ok;
-  int64_t row0;
   int32_t cnt;
-  int64_t col;
-  __device__ __forceinline__ void store(int32_t c0, const float (&v)[16]) const {
+  __device__ __forceinline__ void store(int32_t c0, const float (&v)[8]) const {
     if (!col_ok) return;
-    const int32_t n = cnt - c0 < 16 ? cnt - c0 : 16;
+    const int32_t n = cnt - c0;
     if (type == kTypeF32) {
       float* o = static_cast<float*>(base) + (row0 + c0) * ldo + col;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < 8; ++i)
         if (i < n) o[i * ldo] = v[i];
     } else if (type == kTypeF16) {
       __half* o = static_cast<__half*>(base) + (row0 + c0) * ldo + col;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < 8; ++i)
         if (i < n) o[i * ldo] = __float2half_rn(v[i]);
     } else {
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(base) + (row0 + c0) * ldo + col;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < 8; ++i)
         if (i < n) o[i * ldo] = __float2bfloat16_rn(v[i]);
     }
   }
@@ -465,146 +569,119 @@ struct Out {
 
 template <int OP, int BN>
 __device__ void epilogue_role(const ExpertsParams& p, const Schedule<OP, BN>& sch,
-                              const Ring& ring, uint32_t rank, int ew, int lane, uint32_t tmem,
-                              float* scale_buf) {
-  constexpr int kCols = BN / 2;  // columns of a warp, at most
-  const int quad = (threadIdx.x >> 5) & 3, half = ew >> 2;
-  const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-  const uint32_t tempty0 = mapa_shared(smem_u32(ring.tempty), 0);
+                              const Ring& ring, uint32_t rank, int ew, int lane, uint32_t tmem) {
+  constexpr int kCols = BN / 4;  // columns of a warp, at most
+  const int quad = (threadIdx.x >> 5) & 3, quarter = ew >> 2;
   uint32_t acc = 0;
-  Unit u;
-  for (int32_t i = 0; sch.get(i, u); ++i) {
-    const int c_n = u.w / 32, c_first = half * c_n;  // this warp's 16-column chunks
-    const int64_t col = static_cast<int64_t>(u.n0) + rank * 128 + quad * 32 + lane;
-    const Out out{p.out, p.ldo, p.out_type, col < p.wide,
-                  OP == kOpWeight ? static_cast<int64_t>(u.e) * p.out_rows + u.kt0 : u.row0, u.cnt, col};
-    const bool split = sch.split > 1;
-    // this warp's part of a split sum: [columns][32 lanes]
-    const int64_t slab = static_cast<int64_t>(kCols) * 32;
-    float* part = nullptr;
-    if (split)
-      part = p.partials + ((static_cast<int64_t>(u.tile) * sch.split + u.part) * 16 + rank * 8 + ew) * slab + lane;
-
-    if (u.kb0 == u.kb1) {  // an expert without rows: its weights' gradient is zero
-      const float zero[16] = {};
-      for (int c = 0; c < c_n; ++c) out.store((c_first + c) * 16, zero);
-      continue;
-    }
-    if constexpr (OP == kOpFp8) {
-      float sums[kCols];
+  for (int32_t i = 0;; ++i) {
+    uint64_t sums[kCols / 2];
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) sums[c] = 0.0f;
-      const int32_t KB = sch.KB, NB = (p.wide + 127) / 128, nb = u.n0 / 128 + static_cast<int>(rank);
-      const float* ws = p.ws + (static_cast<int64_t>(u.e) * NB + (nb < NB ? nb : NB - 1)) * KB;
-      const float* xs = p.xs + u.row0 + c_first * 16;
-      const int32_t left = u.cnt - c_first * 16;  // rows from this warp's first column on
-      constexpr int kPer = (kCols + 31) / 32;
-      float nx[kPer], nw;
-      auto fetch = [&](int32_t kb) {
-        nw = __ldg(ws + kb);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          nx[j] = j * 32 + lane < left && j * 32 + lane < c_n * 16
-                      ? __ldg(xs + static_cast<int64_t>(kb) * p.rows + j * 32 + lane) : 0.0f;
-      };
-      fetch(u.kb0);
-      for (int32_t kb = u.kb0; kb < u.kb1; ++kb) {
-        float* buf = scale_buf + (kb & 1) * 128;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) buf[j * 32 + lane] = nx[j] * nw;
-        if (kb + 1 < u.kb1) fetch(kb + 1);
-        __syncwarp();
-        if (!mbar_wait(&ring.tfull[acc & 1u], (acc >> 1) & 1u, p.timeout_ns, ring.abort, p.status)) {
+    for (int c = 0; c < kCols / 2; ++c) sums[c] = 0;
+    {
+      Unit u;
+      if (!sch.get(i, u)) break;
+      const int n8 = u.w / 32, c_first = quarter * n8 * 8;  // this warp's columns, in eights
+      const uint32_t from0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c_first;
+      const uint32_t tempty0 = mapa_shared(smem_u32(ring.tempty), 0);
+      const int32_t seg = OP == kOpFp8 ? 1 : p.segment;
+      for (int32_t left = u.kb1 - u.kb0; left > 0; left -= seg) {
+        [[maybe_unused]] const float* scale = ring.scales + (acc % kScaleSlots) * kXRows + c_first;
+        bool ok = true;
+        if constexpr (OP == kOpFp8)
+          ok = mbar_wait(&ring.sfull[acc % kScaleSlots], (acc / kScaleSlots) & 1u, p.timeout_ns,
+                         ring.abort, p.status);
+        if (!ok || !mbar_wait(&ring.tfull[acc & 1u], (acc >> 1) & 1u, p.timeout_ns, ring.abort, p.status)) {
           set_status(p.status, kStatusPipelineTimeout, 0x300u | rank);
           *ring.abort = 1;
           return;
         }
         tc_fence_after();
+        const uint32_t from = from0 + (acc & 1u) * 256u;
 #pragma unroll
-        for (int c = 0; c < kCols / 16; ++c) {
-          if (c < c_n) {
-            uint32_t v[16];
-            tmem_ld16(lane_base + (acc & 1u) * 256u + (c_first + c) * 16, v);
+        for (int c = 0; c < kCols / 8; ++c) {
+          if (c < n8) {
+            uint32_t v[8];
+            tmem_ld8(from + c * 8, v);
             tmem_ld_wait();
-            if (c == c_n - 1) {
+            if (c == n8 - 1) {  // the accumulator has been read
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive_pair(tempty0 + (acc & 1u) * 8);
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float4 s = *reinterpret_cast<const float4*>(buf + c * 16 + q * 4);
-              sums[c * 16 + q * 4 + 0] = fmaf(__uint_as_float(v[q * 4 + 0]), s.x, sums[c * 16 + q * 4 + 0]);
-              sums[c * 16 + q * 4 + 1] = fmaf(__uint_as_float(v[q * 4 + 1]), s.y, sums[c * 16 + q * 4 + 1]);
-              sums[c * 16 + q * 4 + 2] = fmaf(__uint_as_float(v[q * 4 + 2]), s.z, sums[c * 16 + q * 4 + 2]);
-              sums[c * 16 + q * 4 + 3] = fmaf(__uint_as_float(v[q * 4 + 3]), s.w, sums[c * 16 + q * 4 + 3]);
+            for (int q = 0; q < 2; ++q) {
+              uint64_t* s = sums + c * 4 + q * 2;
+              const uint64_t lo = pack2(v[q * 4], v[q * 4 + 1]), hi = pack2(v[q * 4 + 2], v[q * 4 + 3]);
+              if constexpr (OP == kOpFp8) {
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scale + c * 8 + q * 4);
+                s[0] = fma2(lo, f.x, s[0]);
+                s[1] = fma2(hi, f.y, s[1]);
+              } else {
+                s[0] = add2(lo, s[0]);
+                s[1] = add2(hi, s[1]);
+              }
             }
           }
         }
+        if constexpr (OP == kOpFp8) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ring.sempty[acc % kScaleSlots]);
+        }
         ++acc;
       }
-#pragma unroll
-      for (int c = 0; c < kCols / 16; ++c) {
-        if (c < c_n) {
-          float v[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = sums[c * 16 + j];
-          if (split) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) __stcg(part + (c * 16 + j) * 32, v[j]);
-          } else {
-            out.store((c_first + c) * 16, v);
-          }
-        }
-      }
-    } else {
-      if (!mbar_wait(&ring.tfull[acc & 1u], (acc >> 1) & 1u, p.timeout_ns, ring.abort, p.status)) {
-        set_status(p.status, kStatusPipelineTimeout, 0x300u | rank);
-        *ring.abort = 1;
-        return;
-      }
-      tc_fence_after();
-      for (int c = 0; c < c_n; ++c) {
-        uint32_t r[16];
-        tmem_ld16(lane_base + (acc & 1u) * 256u + (c_first + c) * 16, r);
-        tmem_ld_wait();
-        if (c == c_n - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_pair(tempty0 + (acc & 1u) * 8);
-        }
-        float v[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-        if (split) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) __stcg(part + (c * 16 + j) * 32, v[j]);
-        } else {
-          out.store((c_first + c) * 16, v);
-        }
-      }
-      ++acc;
     }
-    if (split) {
-      // the warp that comes last adds the parts, in their order
-      __threadfence();
-      __syncwarp();
-      uint32_t* count = p.arrivals + static_cast<int64_t>(u.tile) * 16 + rank * 8 + ew;
-      uint32_t before = 0;
-      if (lane == 0) before = atomicAdd(count, 1u);
-      before = __shfl_sync(0xffffffffu, before, 0);
-      if (before == static_cast<uint32_t>(sch.split - 1)) {
-        __threadfence();
-        if (lane == 0) *count = 0;  // for the next run
-        const float* first = p.partials + (static_cast<int64_t>(u.tile) * sch.split * 16 + rank * 8 + ew) * slab + lane;
-        for (int c = 0; c < c_n; ++c) {
-          float v[16] = {};
-          for (int s = 0; s < sch.split; ++s)
+    // (the unit again: its fields would take the registers of the loop above)
+    Unit u;
+    sch.get(i, u);
+    const int n8 = u.w / 32, c_first = quarter * n8 * 8;
+    const int64_t col = static_cast<int64_t>(u.n0) + rank * 128 + quad * 32 + lane;
+    const Out out{p.out, p.ldo,
+                  OP == kOpWeight ? static_cast<int64_t>(u.e) * p.out_rows + u.kt0 : u.row0, col,
+                  p.out_type, col < p.wide, u.cnt};
+    auto eight = [&](int c, float (&v)[8]) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              v[j] += __ldcg(first + s * 16 * slab + (c * 16 + j) * 32);
-          out.store((c_first + c) * 16, v);
+      for (int j = 0; j < 4; ++j) unpack2(sums[c * 4 + j], v[2 * j], v[2 * j + 1]);
+    };
+    if (sch.split == 1) {
+#pragma unroll
+      for (int c = 0; c < kCols / 8; ++c)
+        if (c < n8) {
+          float v[8];
+          eight(c, v);
+          out.store(c_first + c * 8, v);
         }
+      continue;
+    }
+    // this warp's part, [columns][32 lanes]; the warp that comes last adds the parts,
+    // in their order
+    constexpr int64_t kSlab = static_cast<int64_t>(kCols) * 32;
+    constexpr int64_t kNext = 2 * kXEpiWarps * kSlab;
+    float* first = p.partials +
+                   ((static_cast<int64_t>(u.tile) * sch.split * 2 + rank) * kXEpiWarps + ew) * kSlab + lane;
+    float* part = first + u.part * kNext;
+#pragma unroll
+    for (int c = 0; c < kCols / 8; ++c)
+      if (c < n8) {
+        float v[8];
+        eight(c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) __stcg(part + (c * 8 + j) * 32, v[j]);
+      }
+    __threadfence();
+    __syncwarp();
+    uint32_t* count = p.arrivals + (static_cast<int64_t>(u.tile) * 2 + rank) * kXEpiWarps + ew;
+    uint32_t before = 0;
+    if (lane == 0) before = atomicAdd(count, 1u);
+    before = __shfl_sync(0xffffffffu, before, 0);
+    if (before == static_cast<uint32_t>(sch.split - 1)) {
+      __threadfence();
+      if (lane == 0) *count = 0;  // for the next run
+      for (int c = 0; c < n8; ++c) {
+        float v[8] = {};
+        for (int s = 0; s < sch.split; ++s)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] += __ldcg(first + s * kNext + (c * 8 + j) * 32);
+        out.store(c_first + c * 8, v);
       }
     }
   }
@@ -612,7 +689,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Schedule<OP, BN>& sc
 
 // ------------------------------------------------------------------ kernel
 template <int OP, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     experts_kernel(const __grid_constant__ ExpertsParams p) {
   constexpr int kStagesX = stages_of(BN);
   extern __shared__ uint8_t smem_raw[];
@@ -621,8 +698,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
   Ring ring;
   ring.w = smem;
   ring.r = smem + kStagesX * kWBytes;
-  float* scales = reinterpret_cast<float*>(ring.r + kStagesX * r_bytes(BN));
-  int32_t* off = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(scales) +
+  ring.scales = reinterpret_cast<float*>(ring.r + kStagesX * r_bytes(BN));
+  int32_t* off = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(ring.scales) +
                                             (OP == kOpFp8 ? kScaleBytes : 0));
   int32_t* pre = off + kMaxExperts + 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(off) + kTableBytes);
@@ -631,7 +708,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
   ring.tfull = bars + 2 * kStagesX;
   ring.tempty = ring.tfull + 2;
   ring.tail = ring.tempty + 2;
-  uint64_t* drain = ring.tail + 1;
+  ring.sfull = ring.tail + kStagesX;
+  ring.sempty = ring.sfull + kScaleSlots;
+  uint64_t* drain = ring.sempty + kScaleSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   ring.abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* flag = reinterpret_cast<int32_t*>(tmem_slot + 2);
@@ -642,12 +721,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
     for (int s = 0; s < kStagesX; ++s) {
       mbar_init(&ring.full[s], OP == kOpWeight ? 2 : 1);
       mbar_init(&ring.empty[s], 1);
+      mbar_init(&ring.tail[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ring.tfull[b], 1);
-      mbar_init(&ring.tempty[b], 16);
+      mbar_init(&ring.tempty[b], 2 * kXEpiWarps);
     }
-    mbar_init(ring.tail, 1);
+    for (int s = 0; s < kScaleSlots; ++s) {
+      mbar_init(&ring.sfull[s], 1);
+      mbar_init(&ring.sempty[s], kXEpiWarps);
+    }
     mbar_init(drain, 1);
     *tmem_slot = 0;
     *ring.abort = 0;
@@ -668,8 +751,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
       tma_role<OP, BN>(p, sch, ring, rank, lane);
     } else if (warp == 1) {
       if (rank == 0 && lane == 0) mma_role<OP, BN>(p, sch, ring, tmem);
-    } else {
-      epilogue_role<OP, BN>(p, sch, ring, rank, warp - 2, lane, tmem, scales + (warp - 2) * 256);
+    } else if (warp < 2 + kXEpiWarps) {
+      epilogue_role<OP, BN>(p, sch, ring, rank, warp - 2, lane, tmem);
+    } else if constexpr (OP == kOpWeight) {
+      zero_role<BN>(p, sch, ring, rank, lane);
+    } else if constexpr (OP == kOpFp8) {
+      scale_role<BN>(p, sch, ring, rank, lane);
     }
   } else if (threadIdx.x == 0) {
     set_status(p.status, kStatusOffsets, 0);
@@ -725,7 +812,7 @@ cudaError_t experts_prepare(int* pairs) {
       if (e != cudaSuccess) break;
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
-      cfg.blockDim = dim3(kXThreads);
+      cfg.blockDim = dim3(static_cast<unsigned>(threads_of(op)));
       cfg.dynamicSmemBytes = static_cast<size_t>(smem);
       int clusters = 0;
       e = cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg);
@@ -739,7 +826,7 @@ cudaError_t launch_experts(const ExpertsParams& p, int op, bool few, int grid,
                            cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kXThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads_of(op)));
   cfg.dynamicSmemBytes =
       static_cast<size_t>(smem_bytes(few && op != kOpWeight ? kXFewRows : kXRows, op == kOpFp8));
   cfg.stream = stream;

@@ -21,7 +21,12 @@ constexpr int kXWide = 256;    // a pair's tile: 256 of the wide dimension
 constexpr int kXRows = 256;    // and up to 256 rows,
 constexpr int kXFewRows = 64;  // or up to 64 where groups are short
 constexpr int kXRowBoxes = 4;  // box heights of the row operand: 1/4 to 4/4 of half a tile
-constexpr int kXThreads = 320; // TMA warp, MMA warp, 8 epilogue warps
+constexpr int kXEpiWarps = 16;
+// TMA warp, MMA warp, epilogue warps; the weight gradient's zeroing warp, or the
+// scale warp of e4m3.
+__host__ __device__ constexpr int threads_of(int op) {
+  return 32 * (2 + kXEpiWarps + (op == kOpWeight || op == kOpFp8 ? 1 : 0));
+}
 constexpr int kXGroup = 8;     // row tiles that share the weights they read (tile order)
 
 struct ExpertsParams {
@@ -34,22 +39,23 @@ struct ExpertsParams {
   int32_t red;                   // length of the sums (weight gradient: unused)
   int32_t out_rows;              // weight gradient: output rows per expert (K)
   int32_t w_blk, r_blk;          // MN-major operand described in blocks of 64 columns (one load), or not (two)
+  int32_t segment;               // k-blocks per accumulator (e4m3: 1)
   int32_t bf16;                  // operands are bfloat16 (otherwise fp16)
   int32_t out_type;              // ElemType of the output
   void* out;
   int64_t ldo;
   const float* xs;               // e4m3: row scales [KB][rows]
   const float* ws;               // e4m3: weight scales [E][NB][KB]
-  float* partials;               // split sums: [unit][16 warps][columns][32 lanes]
-  uint32_t* arrivals;            // [tile][16 warps], zero between runs
+  float* partials;               // split sums: [unit][warps of the pair][columns][32 lanes]
+  uint32_t* arrivals;            // [tile][warps of the pair], zero between runs
   int32_t max_units;             // units the workspace holds (0: never split)
   uint32_t* status;              // [2]: status word, detail
   uint64_t timeout_ns;
 };
 
-// A warp's part of a split sum: columns x 32 lanes of floats.
+// A unit of a split sum: each warp's columns x 32 lanes of floats.
 constexpr int64_t split_unit_bytes(bool few) {
-  return 16 * static_cast<int64_t>(few ? kXFewRows : kXRows) / 2 * 32 * 4;
+  return 2 * kXEpiWarps * (static_cast<int64_t>(few ? kXFewRows : kXRows) / 4) * 32 * 4;
 }
 
 constexpr uint32_t kStatusOffsets = 16;  // status word: offsets decrease or leave [0, rows]

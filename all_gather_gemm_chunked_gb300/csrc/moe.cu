@@ -106,6 +106,9 @@ constexpr int64_t kPartialBytes = 608 * agg::split_unit_bytes(true);
 static_assert(kPartialBytes == 152 * agg::split_unit_bytes(false), "both tile heights");
 int max_units(bool few) { return static_cast<int>(kPartialBytes / agg::split_unit_bytes(few)); }
 
+// k-blocks of a segment where the output is fp32.
+constexpr int kSegment = 8;
+
 struct Prepared {
   cudaError_t e;
   int pairs;
@@ -201,6 +204,7 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
   x.E = p->E;
   x.bf16 = p->dtype == AG_GEMM_BF16;
+  x.segment = x.out_type == AG_MOE_F32 ? kSegment : 1 << 30;
   x.partials = p->partials;
   x.arrivals = p->arrivals;
   x.max_units = max_units(few);
@@ -440,7 +444,7 @@ ag_moe_plan* ag_moe_plan_create(int E, int64_t K, int64_t N, int dtype) {
   p->dtype = dtype;
   p->device = device;
   p->pairs = pre.pairs;
-  p->arrival_count = static_cast<int64_t>(max_units(true)) * 16;
+  p->arrival_count = static_cast<int64_t>(max_units(true)) * 2 * agg::kXEpiWarps;
   const size_t words = static_cast<size_t>(4 + p->arrival_count) * sizeof(uint32_t);
   if ((e = cudaMalloc(&p->status, words)) != cudaSuccess ||
       (e = cudaMemset(p->status, 0, words)) != cudaSuccess ||
