@@ -7,7 +7,8 @@
 //   forward          W = w[e] (K x N, wide contiguous: MN-major),  R = x rows (K-major)
 //   input gradient   W = w[e] (red contiguous: K-major),           R = dy rows (K-major)
 //   weight gradient  W = dy^T (MN-major), R = x^T (MN-major), red = the expert's rows
-//   e4m3             W = wq[e] (N x K: K-major), R = xq rows (K-major)
+//   e4m3             W = wq[e] (N x K: K-major), R = xq rows (K-major); for long
+//                    groups the other way round, rows on the M side
 //
 // Rows on the N side: a pair's N takes any multiple of 32 up to 256 where its M is
 // 256, so a group of 300 rows costs two tiles of 160 and one of 7 rows a tile of 32,
@@ -55,23 +56,28 @@
 #include "experts_kernel.cuh"
 #include "fused_kernel.cuh"
 #include "moe_rows.cuh"
+#include "moe_types.cuh"
 #include "sm103.cuh"
 
 namespace agg {
 
 namespace {
 constexpr int kWBytes = 128 * 128;  // a CTA's wide operand per k-block: 128 x 128 bytes
+// k-blocks per stage of the ring.  The MMA thread's work around a stage (a wait, a
+// fence, a commit) took about 0.2 us, as long as the MMAs of one k-block; two k-blocks
+// a stage halve it.
+constexpr int kSub = 2;
 
 __host__ __device__ constexpr int rows_per_cta(int BN) { return BN / 2; }
 __host__ __device__ constexpr int r_bytes(int BN) { return rows_per_cta(BN) * 128; }
-// Stages that fit: 6 of 32 KB, or 10 of 20 KB for short row tiles, where the bytes
-// in flight are the weights' alone.
-__host__ __device__ constexpr int stages_of(int BN) { return BN == kXRows ? 6 : 10; }
+// Stages that fit: 3 of 64 KB, or 5 of 40 KB for short row tiles, where the bytes in
+// flight are nearly the weights' alone.
+__host__ __device__ constexpr int stages_of(int BN) { return BN == kXRows ? 3 : 5; }
 constexpr int kScaleSlots = 4;  // e4m3: k-blocks whose scales are held
 constexpr int kScaleBytes = kScaleSlots * kXRows * 4;
 constexpr int kTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) & ~15;
 __host__ __device__ constexpr int smem_bytes(int BN, bool fp8) {
-  return stages_of(BN) * (kWBytes + r_bytes(BN)) + (fp8 ? kScaleBytes : 0) + kTableBytes + 512 /*barriers*/ +
+  return stages_of(BN) * kSub * (kWBytes + r_bytes(BN)) + (fp8 ? kScaleBytes : 0) + kTableBytes + 512 /*barriers*/ +
          1024 /*alignment*/;
 }
 static_assert(smem_bytes(kXRows, true) <= 227 * 1024 && smem_bytes(kXFewRows, true) <= 227 * 1024,
@@ -152,8 +158,9 @@ struct Unit {
   int32_t tile, part;
 };
 
+__host__ __device__ constexpr bool is_fp8(int op) { return op == kOpFp8 || op == kOpFp8Long; }
 template <int OP>
-__host__ __device__ constexpr int block_k() { return OP == kOpFp8 ? 128 : 64; }
+__host__ __device__ constexpr int block_k() { return is_fp8(OP) ? 128 : 64; }
 
 template <int OP, int BN>
 struct Schedule {
@@ -241,11 +248,20 @@ struct Schedule {
       const int32_t gw = nt - g * kXGroup < kXGroup ? nt - g * kXGroup : kXGroup;
       const int32_t x = r / gw;
       u.n0 = x * kXWide;
-      // the group's rows in nt tiles of equal width, a multiple of 32
-      u.w = ((cnt + nt - 1) / nt + 31) & ~31;
-      const int32_t first = (g * kXGroup + r - x * gw) * u.w;
+      const int32_t tile = g * kXGroup + r - x * gw;
+      int32_t height;
+      if constexpr (OP == kOpFp8Long) {
+        height = BN;
+        const int32_t cols = p.wide - u.n0;
+        u.w = cols < kXWide ? (cols + 31) & ~31 : kXWide;
+      } else {
+        // the group's rows in nt tiles of equal width, a multiple of 32
+        u.w = ((cnt + nt - 1) / nt + 31) & ~31;
+        height = u.w;
+      }
+      const int32_t first = tile * height;
       u.row0 = off[lo] + first;
-      u.cnt = cnt - first < u.w ? cnt - first : u.w;
+      u.cnt = cnt - first < height ? cnt - first : height;
       u.kt0 = 0;
       u.red_rows = 0;
       u.kb0 = static_cast<int32_t>(static_cast<int64_t>(KB) * u.part / split);
@@ -293,7 +309,8 @@ struct Ring {
   uint64_t* empty;
   uint64_t* tfull;  // accumulators, on both CTAs
   uint64_t* tempty; // on the even CTA: the epilogue warps of both
-  uint64_t* tail;   // weight gradient, by stage: this CTA's last k-block of a group
+  uint64_t* tail;   // weight gradient, by stage: this CTA's part of a group's last k-block
+  uint64_t* zfull;  // and, on the even CTA: both CTAs' parts zeroed behind the group's end
   uint64_t* sfull;  // e4m3: scales of a k-block, by slot
   uint64_t* sempty; // e4m3: this CTA's epilogue warps are through with them
   float* scales;    // [kScaleSlots][kXRows]
@@ -320,50 +337,55 @@ __device__ void tma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
   const uint32_t full0 = mapa_shared(smem_u32(ring.full), 0);
   const uint32_t tail0 = mapa_shared(smem_u32(ring.tail), rank);
   int stage = 0;
-  uint32_t phase = 0, issued = 0, issued_phase = 0;
+  uint32_t phase = 0, issued = 0, filled = 0;  // bit s: stage s used; its loads' parity
   bool ok = true;
   Unit u;
   for (int32_t i = 0; ok && sch.get(i, u); ++i) {
     const int32_t half = u.w / 2;
     const int box = OP == kOpWeight ? 0 : (half + BN / 8 - 1) / (BN / 8) - 1;
-    const uint32_t r_tx =
-        OP == kOpWeight ? static_cast<uint32_t>(2 * 64 * 128) : static_cast<uint32_t>((box + 1) * (BN / 8) * 128);
+    const uint32_t r_tx = OP == kOpWeight || OP == kOpFp8Long
+                              ? static_cast<uint32_t>(r_bytes(BN))
+                              : static_cast<uint32_t>((box + 1) * (BN / 8) * 128);
     const int32_t n = u.n0 + static_cast<int32_t>(rank) * 128;
-    for (int32_t kb = u.kb0; kb < u.kb1; ++kb) {
+    for (int32_t kb0 = u.kb0; kb0 < u.kb1; kb0 += kSub) {
+      const int n_sub = u.kb1 - kb0 < kSub ? u.kb1 - kb0 : kSub;
       ok = mbar_wait(&ring.empty[stage], phase ^ 1u, p.timeout_ns, ring.abort, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const bool tail = OP == kOpWeight && u.red_rows - kb * 64 < 64;
-      uint32_t bar = full0 + stage * 8;
-      uint8_t* wd = ring.w + stage * kWBytes;
-      uint8_t* rd = ring.r + stage * r_bytes(BN);
       if (lane == 0) {
+        const bool tail = OP == kOpWeight && u.red_rows - (kb0 + n_sub) * 64 < 0;
+        uint32_t bar = full0 + stage * 8;
         if (tail) {
           bar = tail0 + stage * 8;  // counted here: zero_role passes it on
-          mbar_arrive_expect_tx(&ring.tail[stage], kWBytes + r_tx);
-        } else if (rank == 0) {
-          mbar_arrive_expect_tx(&ring.full[stage], 2 * (kWBytes + r_tx));
-        } else if (OP == kOpWeight) {
-          mbar_arrive_pair(bar);
-        }
-        if constexpr (OP == kOpForward) {
-          load_mn(wd, &p.tm_w, bar, p.w_blk, n, kb * 64, u.e, 2);
-        } else if constexpr (OP == kOpWeight) {
-          load_mn(wd, &p.tm_w, bar, p.w_blk, n, u.row0 + kb * 64, 0, 2);
+          mbar_arrive_expect_tx(&ring.tail[stage], n_sub * (kWBytes + r_tx));
         } else {
-          tma_load_3d_pair(wd, &p.tm_w, bar, kb * block_k<OP>(), n, u.e);
-        }
-        if constexpr (OP == kOpWeight)
-          load_mn(rd, &p.tm_r[0], bar, p.r_blk, u.kt0 + static_cast<int32_t>(rank) * half,
-                  u.row0 + kb * 64, 0, 2);
-        else
-          tma_load_2d_pair(rd, &p.tm_r[box], bar, kb * block_k<OP>(),
-                           u.row0 + static_cast<int32_t>(rank) * half);
-        if (!tail) {
+          if (rank == 0) mbar_arrive_expect_tx(&ring.full[stage], 2 * n_sub * (kWBytes + r_tx));
           issued |= 1u << stage;
-          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          filled ^= 1u << stage;
+        }
+        for (int s = 0; s < n_sub; ++s) {
+          const int32_t kb = kb0 + s;
+          uint8_t* wd = ring.w + (stage * kSub + s) * kWBytes;
+          uint8_t* rd = ring.r + (stage * kSub + s) * r_bytes(BN);
+          if constexpr (OP == kOpFp8Long) {
+            tma_load_2d_pair(wd, &p.tm_r[kXRowBoxes - 1], bar, kb * 128,
+                             u.row0 + static_cast<int32_t>(rank) * 128);
+            tma_load_3d_pair(rd, &p.tm_w, bar, kb * 128, u.n0 + static_cast<int32_t>(rank) * half, u.e);
+          } else if constexpr (OP == kOpForward) {
+            load_mn(wd, &p.tm_w, bar, p.w_blk, n, kb * 64, u.e, 2);
+          } else if constexpr (OP == kOpWeight) {
+            load_mn(wd, &p.tm_w, bar, p.w_blk, n, u.row0 + kb * 64, 0, 2);
+            load_mn(rd, &p.tm_r[0], bar, p.r_blk, u.kt0 + static_cast<int32_t>(rank) * half,
+                    u.row0 + kb * 64, 0, 2);
+          } else {
+            tma_load_3d_pair(wd, &p.tm_w, bar, kb * block_k<OP>(), n, u.e);
+          }
+          if constexpr (OP == kOpForward || OP == kOpInput || OP == kOpFp8)
+            tma_load_2d_pair(rd, &p.tm_r[box], bar, kb * block_k<OP>(),
+                             u.row0 + static_cast<int32_t>(rank) * half);
         }
       }
+      __syncwarp();
       if (++stage == kStagesX) {
         stage = 0;
         phase ^= 1u;
@@ -376,7 +398,7 @@ __device__ void tma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
     if (rank == 0) {
       volatile int never = 0;
       for (int s = 0; s < kStagesX; ++s)
-        if (issued & (1u << s)) mbar_wait(&ring.full[s], (issued_phase >> s) & 1u, 20000000ull, &never);
+        if (issued & (1u << s)) mbar_wait(&ring.full[s], ((filled >> s) & 1u) ^ 1u, 20000000ull, &never);
     }
   }
   __syncwarp();
@@ -391,14 +413,15 @@ template <int BN>
 __device__ void zero_role(const ExpertsParams& p, const Schedule<kOpWeight, BN>& sch,
                           const Ring& ring, uint32_t rank, int lane) {
   constexpr int kStagesX = stages_of(BN);
-  const uint32_t full0 = mapa_shared(smem_u32(ring.full), 0);
-  uint32_t blocks = 0, used = 0;  // k-blocks so far; bit s: parity of stage s's tails
+  const uint32_t zfull0 = mapa_shared(smem_u32(ring.zfull), 0);
+  uint32_t stages = 0, used = 0;  // stages so far; bit s: parity of stage s's tails
   Unit u;
   for (int32_t i = 0; sch.get(i, u); ++i) {
-    blocks += static_cast<uint32_t>(u.kb1);
+    stages += static_cast<uint32_t>((u.kb1 + kSub - 1) / kSub);
     const int valid = u.red_rows & 63;
     if (valid == 0) continue;
-    const uint32_t stage = (blocks - 1) % kStagesX;
+    const uint32_t stage = (stages - 1) % kStagesX;
+    const uint32_t block = stage * kSub + (u.kb1 - 1) % kSub;
     bool ok = mbar_wait(&ring.tail[stage], (used >> stage) & 1u, p.timeout_ns, ring.abort, p.status);
     used ^= 1u << stage;
     ok = __all_sync(0xffffffffu, ok);
@@ -412,13 +435,13 @@ __device__ void zero_role(const ExpertsParams& p, const Schedule<kOpWeight, BN>&
     const int n16 = (((valid + 15) & ~15) - valid) * 8;  // 16-byte pieces per block of 64 columns
     for (int j = lane; j < 4 * n16; j += 32) {
       const int blk = j / n16, o = valid * 128 + (j - blk * n16) * 16;
-      uint8_t* base = blk < 2 ? ring.w + stage * kWBytes + blk * (64 * 128)
-                              : ring.r + stage * r_bytes(BN) + (blk - 2) * (64 * 128);
+      uint8_t* base = blk < 2 ? ring.w + block * kWBytes + blk * (64 * 128)
+                              : ring.r + block * r_bytes(BN) + (blk - 2) * (64 * 128);
       *reinterpret_cast<uint4*>(base + o) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_shared();
     __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(full0 + stage * 8);
+    if (lane == 0) mbar_arrive_cluster(zfull0 + stage * 8);
     __syncwarp();
   }
 }
@@ -471,63 +494,82 @@ __device__ void mma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
   constexpr int kStagesX = stages_of(BN);
   constexpr bool kWMn = OP == kOpForward || OP == kOpWeight;
   constexpr bool kRMn = OP == kOpWeight;
-  const uint32_t w0 = smem_u32(ring.w), r0 = smem_u32(ring.r);
+  // 128-byte swizzle.  K-major: groups of 8 rows 1024 B apart, 32 B further per step.
+  // MN-major: blocks of 64 columns 8 KB apart, groups of 8 rows 1024 B apart, 16 rows
+  // (2 KB) per step.  (The address is the descriptor's lowest field, in units of 16.)
+  const uint64_t w0 = kWMn ? smem_desc_sw128(smem_u32(ring.w), 64 * 128, 1024)
+                           : smem_desc_sw128(smem_u32(ring.w), 16, 1024);
+  const uint64_t r0 = kRMn ? smem_desc_sw128(smem_u32(ring.r), 64 * 128, 1024)
+                           : smem_desc_sw128(smem_u32(ring.r), 16, 1024);
+  constexpr uint32_t kWStep = (kWMn ? 2048 : 32) / 16, kRStep = (kRMn ? 2048 : 32) / 16;
   int stage = 0;
-  uint32_t phase = 0, acc = 0;
+  uint32_t acc = 0, full_phase = 0, zeroed = 0;  // bit s: parity of stage s's barriers
   bool ok = true;
+  auto accumulator = [&] {  // wait until it has been read
+    const bool r = mbar_wait(&ring.tempty[acc & 1u], ((acc >> 1) & 1u) ^ 1u, p.timeout_ns,
+                             ring.abort, p.status);
+    tc_fence_after();
+    return r;
+  };
   Unit u;
   for (int32_t i = 0; ok && sch.get(i, u); ++i) {
     const uint32_t idesc = idesc_f16_f32(kXWide, u.w, kWMn, kRMn) |
-                           (OP != kOpFp8 && p.bf16 ? kIdescAbBf16 : 0u);
+                           (!is_fp8(OP) && p.bf16 ? kIdescAbBf16 : 0u);
     int32_t left = 0;  // k-blocks left of the segment
-    for (int32_t kb = u.kb0; kb < u.kb1; ++kb) {
-      const uint32_t d = tmem + (acc & 1u) * 256u;
-      const bool first = OP == kOpFp8 || left == 0;
-      if (first) {
+    for (int32_t kb0 = u.kb0; kb0 < u.kb1; kb0 += kSub) {
+      const int n_sub = u.kb1 - kb0 < kSub ? u.kb1 - kb0 : kSub;
+      bool first = false;
+      if (!is_fp8(OP) && left <= 0) {
+        if (!(ok = accumulator())) break;
         left = p.segment;
-        if (!(ok = mbar_wait(&ring.tempty[acc & 1u], ((acc >> 1) & 1u) ^ 1u, p.timeout_ns,
-                             ring.abort, p.status)))
-          break;
-        tc_fence_after();
+        first = true;
       }
-      // (the weight gradient's last k-block is zeroed by both CTAs' threads)
-      if (OP == kOpWeight)
-        ok = mbar_wait_cluster(&ring.full[stage], phase, p.timeout_ns, ring.abort, p.status);
-      else
-        ok = mbar_wait(&ring.full[stage], phase, p.timeout_ns, ring.abort, p.status);
+      int last_steps = 4;  // of the stage's last k-block
+      if (OP == kOpWeight && u.red_rows - (kb0 + n_sub) * 64 < 0) {
+        // a group's last k-block comes through both CTAs' zeroing warps
+        last_steps = (u.red_rows - (kb0 + n_sub - 1) * 64 + 15) / 16;
+        ok = mbar_wait_cluster(&ring.zfull[stage], (zeroed >> stage) & 1u, p.timeout_ns, ring.abort,
+                               p.status);
+        zeroed ^= 1u << stage;
+      } else {
+        ok = mbar_wait(&ring.full[stage], (full_phase >> stage) & 1u, p.timeout_ns, ring.abort,
+                       p.status);
+        full_phase ^= 1u << stage;
+      }
       if (!ok) break;
       tc_fence_after();
-      const uint32_t ws = w0 + stage * kWBytes, rs = r0 + stage * r_bytes(BN);
-      int steps = 4;
-      if (OP == kOpWeight) {
-        const int valid = u.red_rows - kb * 64;
-        if (valid < 64) steps = (valid + 15) / 16;
-      }
+      const uint64_t ws = w0 + static_cast<uint32_t>(stage * (kSub * kWBytes / 16));
+      const uint64_t rs = r0 + static_cast<uint32_t>(stage * (kSub * r_bytes(BN) / 16));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (OP == kOpWeight && k >= steps) break;
-        // 128-byte swizzle.  K-major: groups of 8 rows 1024 B apart, 32 B further
-        // per step.  MN-major: blocks of 64 columns 8 KB apart, groups of 8 rows
-        // 1024 B apart, 16 rows (2 KB) per step.
-        const uint64_t wd = kWMn ? smem_desc_sw128(ws + k * 2048, 64 * 128, 1024)
-                                 : smem_desc_sw128(ws + k * 32, 16, 1024);
-        const uint64_t rd = kRMn ? smem_desc_sw128(rs + k * 2048, 64 * 128, 1024)
-                                 : smem_desc_sw128(rs + k * 32, 16, 1024);
-        const uint32_t add = (!first || k > 0) ? 1u : 0u;
-        if constexpr (OP == kOpFp8)
-          mma_f8_pair(d, wd, rd, idesc, add);
-        else
-          mma_f16_pair(d, wd, rd, idesc, add);
+      for (int s = 0; s < kSub; ++s) {
+        if (s >= n_sub) break;
+        if (is_fp8(OP) && !(ok = accumulator())) break;
+        const uint32_t d = tmem + (acc & 1u) * 256u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (OP == kOpWeight && s == n_sub - 1 && k >= last_steps) break;
+          const uint64_t wd = ws + (s * kWBytes / 16 + k * kWStep);
+          const uint64_t rd = rs + (s * r_bytes(BN) / 16 + k * kRStep);
+          if constexpr (is_fp8(OP))
+            mma_f8_pair(d, wd, rd, idesc, k > 0 ? 1u : 0u);
+          else
+            mma_f16_pair(d, wd, rd, idesc, (!first || s > 0 || k > 0) ? 1u : 0u);
+        }
+        if (is_fp8(OP)) {
+          mma_commit_pair_both(&ring.tfull[acc & 1u]);
+          ++acc;
+        }
       }
+      if (!ok) break;
       mma_commit_pair_both(&ring.empty[stage]);
-      if (++stage == kStagesX) {
-        stage = 0;
-        phase ^= 1u;
-      }
-      if (OP == kOpFp8 || --left == 0 || kb == u.kb1 - 1) {
-        left = 0;
-        mma_commit_pair_both(&ring.tfull[acc & 1u]);
-        ++acc;
+      if (++stage == kStagesX) stage = 0;
+      if (!is_fp8(OP)) {
+        left -= n_sub;
+        if (left <= 0 || kb0 + kSub >= u.kb1) {
+          left = 0;
+          mma_commit_pair_both(&ring.tfull[acc & 1u]);
+          ++acc;
+        }
       }
     }
   }
@@ -566,6 +608,161 @@ struct Out {
     }
   }
 };
+
+// After this warp has stored its part of a split sum: true for the warp that comes
+// last and adds the parts.
+__device__ __forceinline__ bool last_part(const ExpertsParams& p, const Unit& u, int32_t split,
+                                          uint32_t rank, int ew, int lane) {
+  __threadfence();
+  __syncwarp();
+  uint32_t* count = p.arrivals + (static_cast<int64_t>(u.tile) * 2 + rank) * kXEpiWarps + ew;
+  uint32_t before = 0;
+  if (lane == 0) before = atomicAdd(count, 1u);
+  before = __shfl_sync(0xffffffffu, before, 0);
+  if (before != static_cast<uint32_t>(split - 1)) return false;
+  __threadfence();
+  if (lane == 0) *count = 0;  // for the next run
+  return true;
+}
+
+// 8 columns of one output row per lane (N % 8 == 0: all inside or none).
+__device__ __forceinline__ void store_row8(void* base, int type, int64_t at, const float (&v)[8]) {
+  if (type == kTypeF32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else if (type == kTypeF16) {
+    *reinterpret_cast<uint4*>(static_cast<__half*>(base) + at) = Elem<__half>::pack(v);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at) = Elem<__nv_bfloat16>::pack(v);
+  }
+}
+
+// e4m3, long groups: a lane is a row here, so a k-block's scale is one number per
+// thread (the row's times that of the warp's 64 columns, which lie in one block), with
+// no shared memory in the loop: with the scales on the columns, reading them took as
+// much of the shared memory's time as the MMA's operands.
+template <int BN>
+__device__ void epilogue_long(const ExpertsParams& p, const Schedule<kOpFp8Long, BN>& sch,
+                              const Ring& ring, uint32_t rank, int ew, int lane, uint32_t tmem) {
+  const int quad = (threadIdx.x >> 5) & 3, c_first = (ew >> 2) * 64;
+  uint32_t acc = 0;
+  for (int32_t i = 0;; ++i) {
+    uint64_t sums[32];
+#pragma unroll
+    for (int c = 0; c < 32; ++c) sums[c] = 0;
+    {
+      Unit u;
+      if (!sch.get(i, u)) break;
+      const int cols = u.w - c_first;
+      const int n8 = cols <= 0 ? 0 : cols >= 64 ? 8 : cols / 8;
+      const uint32_t from0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c_first;
+      const uint32_t tempty0 = mapa_shared(smem_u32(ring.tempty), 0);
+      const int32_t row = static_cast<int32_t>(rank) * 128 + quad * 32 + lane;
+      const int32_t NB = (p.wide + 127) / 128, nb = (u.n0 + c_first) / 128;
+      const float* ws = p.ws + (static_cast<int64_t>(u.e) * NB + (nb < NB ? nb : NB - 1)) * sch.KB + u.kb0;
+      const float* xs = p.xs + static_cast<int64_t>(u.kb0) * p.rows + u.row0 + (row < u.cnt ? row : 0);
+      const int32_t kbs = u.kb1 - u.kb0;
+      // two k-blocks ahead (pointers at the next one to fetch)
+      float xa = __ldg(xs), wa = __ldg(ws), xb = 0.0f, wb = 0.0f;
+      if (kbs > 1) xb = __ldg(xs + p.rows), wb = __ldg(ws + 1);
+      xs += 2 * static_cast<int64_t>(p.rows);
+      ws += 2;
+      for (int32_t j = 0; j < kbs; ++j) {
+        const float s = xa * wa;
+        xa = xb;
+        wa = wb;
+        if (j + 2 < kbs) {
+          xb = __ldg(xs);
+          wb = __ldg(ws);
+          xs += p.rows;
+          ++ws;
+        }
+        const uint64_t s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+        if (!mbar_wait(&ring.tfull[acc & 1u], (acc >> 1) & 1u, p.timeout_ns, ring.abort, p.status)) {
+          set_status(p.status, kStatusPipelineTimeout, 0x300u | rank);
+          *ring.abort = 1;
+          return;
+        }
+        tc_fence_after();
+        const uint32_t from = from0 + (acc & 1u) * 256u;
+        if (n8 == 8) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[16];
+            tmem_ld16(from + c * 16, v);
+            tmem_ld_wait();
+            if (c == 3) {  // the accumulator has been read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_pair(tempty0 + (acc & 1u) * 8);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              sums[c * 8 + q] = fma2(pack2(v[2 * q], v[2 * q + 1]), s2, sums[c * 8 + q]);
+          }
+        } else {  // the last columns
+#pragma unroll
+          for (int c = 0; c < 7; ++c) {
+            if (c < n8) {
+              uint32_t v[8];
+              tmem_ld8(from + c * 8, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                sums[c * 4 + q] = fma2(pack2(v[2 * q], v[2 * q + 1]), s2, sums[c * 4 + q]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_pair(tempty0 + (acc & 1u) * 8);
+        }
+        ++acc;
+      }
+    }
+    Unit u;
+    sch.get(i, u);
+    const int64_t col = static_cast<int64_t>(u.n0) + c_first;
+    const int32_t row = static_cast<int32_t>(rank) * 128 + quad * 32 + lane;
+    const int64_t at = (static_cast<int64_t>(u.row0) + row) * p.ldo + col;
+    const int32_t left = p.wide - static_cast<int32_t>(col);  // columns of the output from here
+    const int n = left <= 0 ? 0 : left >= 64 ? 8 : left / 8;
+    auto eight = [&](int c, float (&v)[8]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) unpack2(sums[c * 4 + j], v[2 * j], v[2 * j + 1]);
+    };
+    if (sch.split == 1) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < n && row < u.cnt) {
+          float v[8];
+          eight(c, v);
+          store_row8(p.out, p.out_type, at + c * 8, v);
+        }
+      continue;
+    }
+    constexpr int64_t kSlab = 64 * 32, kNext = 2 * kXEpiWarps * kSlab;
+    float* first = p.partials +
+                   ((static_cast<int64_t>(u.tile) * sch.split * 2 + rank) * kXEpiWarps + ew) * kSlab + lane;
+    float* part = first + u.part * kNext;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < n) {
+        float v[8];
+        eight(c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) __stcg(part + (c * 8 + j) * 32, v[j]);
+      }
+    if (last_part(p, u, sch.split, rank, ew, lane))
+      for (int c = 0; c < n; ++c) {
+        float v[8] = {};
+        for (int s = 0; s < sch.split; ++s)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] += __ldcg(first + s * kNext + (c * 8 + j) * 32);
+        if (row < u.cnt) store_row8(p.out, p.out_type, at + c * 8, v);
+      }
+  }
+}
 
 template <int OP, int BN>
 __device__ void epilogue_role(const ExpertsParams& p, const Schedule<OP, BN>& sch,
@@ -667,15 +864,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Schedule<OP, BN>& sc
 #pragma unroll
         for (int j = 0; j < 8; ++j) __stcg(part + (c * 8 + j) * 32, v[j]);
       }
-    __threadfence();
-    __syncwarp();
-    uint32_t* count = p.arrivals + (static_cast<int64_t>(u.tile) * 2 + rank) * kXEpiWarps + ew;
-    uint32_t before = 0;
-    if (lane == 0) before = atomicAdd(count, 1u);
-    before = __shfl_sync(0xffffffffu, before, 0);
-    if (before == static_cast<uint32_t>(sch.split - 1)) {
-      __threadfence();
-      if (lane == 0) *count = 0;  // for the next run
+    if (last_part(p, u, sch.split, rank, ew, lane))
       for (int c = 0; c < n8; ++c) {
         float v[8] = {};
         for (int s = 0; s < sch.split; ++s)
@@ -683,7 +872,6 @@ __device__ void epilogue_role(const ExpertsParams& p, const Schedule<OP, BN>& sc
           for (int j = 0; j < 8; ++j) v[j] += __ldcg(first + s * kNext + (c * 8 + j) * 32);
         out.store(c_first + c * 8, v);
       }
-    }
   }
 }
 
@@ -697,8 +885,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
                                              ~static_cast<uintptr_t>(1023));
   Ring ring;
   ring.w = smem;
-  ring.r = smem + kStagesX * kWBytes;
-  ring.scales = reinterpret_cast<float*>(ring.r + kStagesX * r_bytes(BN));
+  ring.r = smem + kStagesX * kSub * kWBytes;
+  ring.scales = reinterpret_cast<float*>(ring.r + kStagesX * kSub * r_bytes(BN));
   int32_t* off = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(ring.scales) +
                                             (OP == kOpFp8 ? kScaleBytes : 0));
   int32_t* pre = off + kMaxExperts + 1;
@@ -708,7 +896,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   ring.tfull = bars + 2 * kStagesX;
   ring.tempty = ring.tfull + 2;
   ring.tail = ring.tempty + 2;
-  ring.sfull = ring.tail + kStagesX;
+  ring.zfull = ring.tail + kStagesX;
+  ring.sfull = ring.zfull + kStagesX;
   ring.sempty = ring.sfull + kScaleSlots;
   uint64_t* drain = ring.sempty + kScaleSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -719,9 +908,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStagesX; ++s) {
-      mbar_init(&ring.full[s], OP == kOpWeight ? 2 : 1);
+      mbar_init(&ring.full[s], 1);
       mbar_init(&ring.empty[s], 1);
       mbar_init(&ring.tail[s], 1);
+      mbar_init(&ring.zfull[s], 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ring.tfull[b], 1);
@@ -752,7 +942,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     } else if (warp == 1) {
       if (rank == 0 && lane == 0) mma_role<OP, BN>(p, sch, ring, tmem);
     } else if (warp < 2 + kXEpiWarps) {
-      epilogue_role<OP, BN>(p, sch, ring, rank, warp - 2, lane, tmem);
+      if constexpr (OP == kOpFp8Long)
+        epilogue_long<BN>(p, sch, ring, rank, warp - 2, lane, tmem);
+      else
+        epilogue_role<OP, BN>(p, sch, ring, rank, warp - 2, lane, tmem);
     } else if constexpr (OP == kOpWeight) {
       zero_role<BN>(p, sch, ring, rank, lane);
     } else if constexpr (OP == kOpFp8) {
@@ -781,20 +974,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   }
 }
 
-template <int OP>
-const void* fn_of(bool few) {
-  if constexpr (OP == kOpWeight)
-    return reinterpret_cast<const void*>(&experts_kernel<OP, kXRows>);
-  else
-    return few ? reinterpret_cast<const void*>(&experts_kernel<OP, kXFewRows>)
-               : reinterpret_cast<const void*>(&experts_kernel<OP, kXRows>);
+// The kernel of a product: its variant, threads and shared memory.
+struct Variant {
+  const void* fn;
+  int threads, smem;
+};
+template <int OP, int BN>
+Variant variant_of() {
+  return {reinterpret_cast<const void*>(&experts_kernel<OP, BN>), threads_of(OP),
+          smem_bytes(BN, OP == kOpFp8)};
 }
-const void* kernel_of(int op, bool few) {
+Variant variant(int op, bool few) {
   switch (op) {
-    case kOpForward: return fn_of<kOpForward>(few);
-    case kOpInput: return fn_of<kOpInput>(few);
-    case kOpWeight: return fn_of<kOpWeight>(few);
-    default: return fn_of<kOpFp8>(few);
+    case kOpForward: return few ? variant_of<kOpForward, kXFewRows>() : variant_of<kOpForward, kXRows>();
+    case kOpInput: return few ? variant_of<kOpInput, kXFewRows>() : variant_of<kOpInput, kXRows>();
+    case kOpWeight: return variant_of<kOpWeight, kXRows>();
+    default: return few ? variant_of<kOpFp8, kXFewRows>() : variant_of<kOpFp8Long, kXRows>();
   }
 }
 }  // namespace
@@ -806,16 +1001,15 @@ cudaError_t experts_prepare(int* pairs) {
   int least = sms / 2;
   for (int op = 0; op < 4 && e == cudaSuccess; ++op)
     for (int few = 0; few < 2 && e == cudaSuccess; ++few) {
-      const void* fn = kernel_of(op, few != 0);
-      const int smem = smem_bytes(few && op != kOpWeight ? kXFewRows : kXRows, op == kOpFp8);
-      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      const Variant v = variant(op, few != 0);
+      e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
       if (e != cudaSuccess) break;
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
-      cfg.blockDim = dim3(static_cast<unsigned>(threads_of(op)));
-      cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+      cfg.blockDim = dim3(static_cast<unsigned>(v.threads));
+      cfg.dynamicSmemBytes = static_cast<size_t>(v.smem);
       int clusters = 0;
-      e = cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&clusters, v.fn, &cfg);
       if (clusters < least) least = clusters;
     }
   *pairs = least;
@@ -824,14 +1018,14 @@ cudaError_t experts_prepare(int* pairs) {
 
 cudaError_t launch_experts(const ExpertsParams& p, int op, bool few, int grid,
                            cudaStream_t stream) {
+  const Variant v = variant(op, few);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads_of(op)));
-  cfg.dynamicSmemBytes =
-      static_cast<size_t>(smem_bytes(few && op != kOpWeight ? kXFewRows : kXRows, op == kOpFp8));
+  cfg.blockDim = dim3(static_cast<unsigned>(v.threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(v.smem);
   cfg.stream = stream;
   void* args[] = {const_cast<ExpertsParams*>(&p)};
-  return cudaLaunchKernelExC(&cfg, kernel_of(op, few), args);
+  return cudaLaunchKernelExC(&cfg, v.fn, args);
 }
 
 }  // namespace agg

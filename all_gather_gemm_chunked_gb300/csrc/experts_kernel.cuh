@@ -15,6 +15,7 @@ enum ExpertsOp : int {
   kOpInput = 1,     // dx[r][k] = sum_n dy[r][n] w[e][k][n]    wide k, rows r, over n
   kOpWeight = 2,    // dw[e][k][n] = sum_r x[r][k] dy[r][n]    wide n, rows k, over e's rows r
   kOpFp8 = 3,       // y[r][n] with e4m3 operands and scales   wide n, rows r, over k
+  kOpFp8Long = 4,   // the same with rows as the MMA's M (chosen by the launcher)
 };
 
 constexpr int kXWide = 256;    // a pair's tile: 256 of the wide dimension
