@@ -74,13 +74,14 @@ __host__ __device__ constexpr int r_bytes(int BN) { return rows_per_cta(BN) * 12
 // flight are nearly the weights' alone.
 __host__ __device__ constexpr int stages_of(int BN) { return BN == kXRows ? 3 : 5; }
 constexpr int kScaleSlots = 4;  // e4m3: k-blocks whose scales are held
-constexpr int kScaleBytes = kScaleSlots * kXRows * 4;
+__host__ __device__ constexpr int scale_bytes(int op, int BN) { return op == kOpFp8 ? kScaleSlots * BN * 4 : 0; }
+constexpr int kOutBytes = 1024;  // an epilogue warp's buffer for 8 rows of output
 constexpr int kTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) & ~15;
-__host__ __device__ constexpr int smem_bytes(int BN, bool fp8) {
-  return stages_of(BN) * kSub * (kWBytes + r_bytes(BN)) + (fp8 ? kScaleBytes : 0) + kTableBytes + 512 /*barriers*/ +
-         1024 /*alignment*/;
+__host__ __device__ constexpr int smem_bytes(int op, int BN) {
+  return stages_of(BN) * kSub * (kWBytes + r_bytes(BN)) + scale_bytes(op, BN) +
+         kXEpiWarps * kOutBytes + kTableBytes + 512 /*barriers*/ + 1024 /*alignment*/;
 }
-static_assert(smem_bytes(kXRows, true) <= 227 * 1024 && smem_bytes(kXFewRows, true) <= 227 * 1024,
+static_assert(smem_bytes(kOpForward, kXRows) <= 227 * 1024 && smem_bytes(kOpFp8, kXFewRows) <= 227 * 1024,
               "shared memory of an SM");
 
 __device__ __forceinline__ void set_status(uint32_t* status, uint32_t kind, uint32_t detail) {
@@ -162,6 +163,28 @@ __host__ __device__ constexpr bool is_fp8(int op) { return op == kOpFp8 || op ==
 template <int OP>
 __host__ __device__ constexpr int block_k() { return is_fp8(OP) ? 128 : 64; }
 
+// Division by a number that stays: n < 2^31; floor(2^32 / d) gives the quotient or one
+// less.  (A hardware division takes about a hundred cycles; a role that decodes its
+// next unit with five of them holds the ring up at every tile.)
+struct Divisor {
+  uint32_t d, m;
+  __device__ __forceinline__ explicit Divisor(uint32_t d_) : d(d_), m(0xffffffffu / d_) {}
+  __device__ __forceinline__ uint32_t div(uint32_t n, uint32_t& rest) const {
+    uint32_t q = __umulhi(n, m);
+    rest = n - q * d;
+    if (rest >= d) {
+      ++q;
+      rest -= d;
+    }
+    return q;
+  }
+};
+__constant__ uint32_t kInverse[kXGroup + 1] = {0, 0xffffffffu, 0xffffffffu / 2, 0xffffffffu / 3,
+                                               0xffffffffu / 4, 0xffffffffu / 5, 0xffffffffu / 6,
+                                               0xffffffffu / 7, 0xffffffffu / 8};
+
+// The units of a pair in order: unit i is number pair + i * pairs of the list.  A role
+// asks for them one after the other (or the same one again).
 template <int OP, int BN>
 struct Schedule {
   const ExpertsParams& p;
@@ -172,23 +195,25 @@ struct Schedule {
   int32_t KB;           // k-blocks of a whole sum
   int32_t split;        // parts of each tile's sum
   int32_t units, pair, pairs;
+  Divisor by_split, by_group, by_expert;  // parts; tiles of 8 row tiles; weight gradient: of an expert
+  // the expert of the last unit, its first tile, row tiles and their height
+  int32_t e, tile0, nt, height;
 
   __device__ __forceinline__ Schedule(const ExpertsParams& p_, const int32_t* off_,
                                       const int32_t* pre_)
-      : p(p_), off(off_), pre(pre_) {
-    wt = (p.wide + kXWide - 1) / kXWide;
-    pair = blockIdx.x / 2;
-    pairs = gridDim.x / 2;
+      : p(p_), off(off_), pre(pre_), wt((p_.wide + kXWide - 1) / kXWide),
+        kt(OP == kOpWeight ? (p_.out_rows + BN - 1) / BN : 0),
+        KB(OP == kOpWeight ? 0 : (p_.red + block_k<OP>() - 1) / block_k<OP>()),
+        pair(static_cast<int32_t>(blockIdx.x / 2)), pairs(static_cast<int32_t>(gridDim.x / 2)),
+        split(1), by_split(1), by_group(static_cast<uint32_t>(kXGroup * wt)),
+        by_expert(OP == kOpWeight ? static_cast<uint32_t>(wt * kt) : 1u), e(-1), tile0(0), nt(0),
+        height(0) {
     if constexpr (OP == kOpWeight) {
-      kt = (p.out_rows + BN - 1) / BN;
-      KB = 0;
-      split = 1;
       units = p.E * wt * kt;
     } else {
-      kt = 0;
-      KB = (p.red + block_k<OP>() - 1) / block_k<OP>();
       const int32_t tiles = pre[p.E] * wt;
       split = choose_split(tiles);
+      if (split > 1) by_split = Divisor(static_cast<uint32_t>(split));
       units = tiles * split;
     }
   }
@@ -208,20 +233,46 @@ struct Schedule {
     return best;
   }
 
-  __device__ __forceinline__ bool get(int32_t i, Unit& u) const {
+  // Tile `r` of an expert with n row tiles: groups of 8 row tiles, in a group all wide
+  // tiles, the row tiles innermost.
+  __device__ __forceinline__ void place(uint32_t r, int32_t n, int32_t& x, int32_t& row_tile) const {
+    uint32_t rest;
+    const int32_t g = static_cast<int32_t>(by_group.div(r, rest));
+    const uint32_t gw = static_cast<uint32_t>(n - g * kXGroup < kXGroup ? n - g * kXGroup : kXGroup);
+    uint32_t q = __umulhi(rest, kInverse[gw]);
+    rest -= q * gw;
+    if (rest >= gw) {
+      ++q;
+      rest -= gw;
+    }
+    x = static_cast<int32_t>(q);
+    row_tile = g * kXGroup + static_cast<int32_t>(rest);
+  }
+
+  __device__ __forceinline__ void enter(int32_t tile) {
+    int32_t lo = e < 0 ? 0 : e, hi = p.E;
+    while (hi - lo > 1) {  // the expert whose row tiles hold this one
+      const int32_t mid = (lo + hi) >> 1;
+      if (pre[mid] * wt <= tile) lo = mid; else hi = mid;
+    }
+    e = lo;
+    tile0 = pre[lo] * wt;
+    nt = pre[lo + 1] - pre[lo];
+    // its rows in nt tiles of equal height, a multiple of 32 (rows on the M side: 256)
+    height = OP == kOpFp8Long ? BN : ((off[lo + 1] - off[lo] + nt - 1) / nt + 31) & ~31;
+  }
+
+  __device__ __forceinline__ bool get(int32_t i, Unit& u) {
     const int64_t id = static_cast<int64_t>(i) * pairs + pair;
     if (id >= units) return false;
-    const int32_t unit = static_cast<int32_t>(id);
+    const uint32_t unit = static_cast<uint32_t>(id);
+    int32_t x, row_tile;
     if constexpr (OP == kOpWeight) {
-      const int32_t per = wt * kt;
-      u.e = unit / per;
-      int32_t r = unit - u.e * per;
-      const int32_t g = r / (kXGroup * wt);
-      r -= g * (kXGroup * wt);
-      const int32_t gw = kt - g * kXGroup < kXGroup ? kt - g * kXGroup : kXGroup;
-      const int32_t x = r / gw;
+      uint32_t r;
+      u.e = static_cast<int32_t>(by_expert.div(unit, r));
+      place(r, kt, x, row_tile);
       u.n0 = x * kXWide;
-      u.kt0 = (g * kXGroup + r - x * gw) * BN;
+      u.kt0 = row_tile * BN;
       u.cnt = p.out_rows - u.kt0 < BN ? p.out_rows - u.kt0 : BN;
       // (the halves of the two CTAs start at multiples of 64 columns)
       u.w = (u.cnt + 127) & ~127;
@@ -229,43 +280,30 @@ struct Schedule {
       u.red_rows = off[u.e + 1] - u.row0;
       u.kb0 = 0;
       u.kb1 = (u.red_rows + 63) / 64;
-      u.tile = unit;
+      u.tile = static_cast<int32_t>(unit);
       u.part = 0;
     } else {
-      u.tile = unit / split;
-      u.part = unit - u.tile * split;
-      // the expert whose row tiles hold this one
-      int32_t lo = 0, hi = p.E;
-      while (hi - lo > 1) {
-        const int32_t mid = (lo + hi) >> 1;
-        if (pre[mid] * wt <= u.tile) lo = mid; else hi = mid;
-      }
-      u.e = lo;
-      const int32_t nt = pre[lo + 1] - pre[lo], cnt = off[lo + 1] - off[lo];
-      int32_t r = u.tile - pre[lo] * wt;
-      const int32_t g = r / (kXGroup * wt);
-      r -= g * (kXGroup * wt);
-      const int32_t gw = nt - g * kXGroup < kXGroup ? nt - g * kXGroup : kXGroup;
-      const int32_t x = r / gw;
+      uint32_t part;
+      u.tile = static_cast<int32_t>(by_split.div(unit, part));
+      u.part = static_cast<int32_t>(part);
+      if (e < 0 || u.tile >= tile0 + nt * wt) enter(u.tile);
+      u.e = e;
+      place(static_cast<uint32_t>(u.tile - tile0), nt, x, row_tile);
       u.n0 = x * kXWide;
-      const int32_t tile = g * kXGroup + r - x * gw;
-      int32_t height;
-      if constexpr (OP == kOpFp8Long) {
-        height = BN;
-        const int32_t cols = p.wide - u.n0;
-        u.w = cols < kXWide ? (cols + 31) & ~31 : kXWide;
-      } else {
-        // the group's rows in nt tiles of equal width, a multiple of 32
-        u.w = ((cnt + nt - 1) / nt + 31) & ~31;
-        height = u.w;
-      }
-      const int32_t first = tile * height;
-      u.row0 = off[lo] + first;
-      u.cnt = cnt - first < height ? cnt - first : height;
+      const int32_t cols = p.wide - u.n0;
+      u.w = OP != kOpFp8Long ? height : cols < kXWide ? (cols + 31) & ~31 : kXWide;
+      const int32_t first = row_tile * height, left = off[e + 1] - off[e] - first;
+      u.row0 = off[e] + first;
+      u.cnt = left < height ? left : height;
       u.kt0 = 0;
       u.red_rows = 0;
-      u.kb0 = static_cast<int32_t>(static_cast<int64_t>(KB) * u.part / split);
-      u.kb1 = static_cast<int32_t>(static_cast<int64_t>(KB) * (u.part + 1) / split);
+      u.kb0 = 0;
+      u.kb1 = KB;
+      if (split > 1) {
+        uint32_t rest;
+        u.kb0 = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(KB * u.part), rest));
+        u.kb1 = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(KB * (u.part + 1)), rest));
+      }
     }
     return true;
   }
@@ -313,7 +351,8 @@ struct Ring {
   uint64_t* zfull;  // and, on the even CTA: both CTAs' parts zeroed behind the group's end
   uint64_t* sfull;  // e4m3: scales of a k-block, by slot
   uint64_t* sempty; // e4m3: this CTA's epilogue warps are through with them
-  float* scales;    // [kScaleSlots][kXRows]
+  float* scales;    // [kScaleSlots][BN]
+  uint8_t* stage_out;  // a buffer of kOutBytes for each epilogue warp
   volatile int* abort;
 };
 
@@ -331,7 +370,7 @@ __device__ __forceinline__ void load_mn(uint8_t* dst, const CUtensorMap* map, ui
 }
 
 template <int OP, int BN>
-__device__ void tma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, const Ring& ring,
+__device__ void tma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ring& ring,
                          uint32_t rank, int lane) {
   constexpr int kStagesX = stages_of(BN);
   const uint32_t full0 = mapa_shared(smem_u32(ring.full), 0);
@@ -410,7 +449,7 @@ __device__ void tma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
 // reads; then the k-block is passed on.  A warp of its own: the TMA warp, waiting for
 // its own loads here, would leave the ring to run dry once per tile.
 template <int BN>
-__device__ void zero_role(const ExpertsParams& p, const Schedule<kOpWeight, BN>& sch,
+__device__ void zero_role(const ExpertsParams& p, Schedule<kOpWeight, BN>& sch,
                           const Ring& ring, uint32_t rank, int lane) {
   constexpr int kStagesX = stages_of(BN);
   const uint32_t zfull0 = mapa_shared(smem_u32(ring.zfull), 0);
@@ -450,7 +489,7 @@ __device__ void zero_role(const ExpertsParams& p, const Schedule<kOpWeight, BN>&
 // For each k-block the scales of the tile's rows times this CTA's weights' scale (its
 // 128 of the wide dimension are one block), a few k-blocks ahead of the epilogue.
 template <int BN>
-__device__ void scale_role(const ExpertsParams& p, const Schedule<kOpFp8, BN>& sch,
+__device__ void scale_role(const ExpertsParams& p, Schedule<kOpFp8, BN>& sch,
                            const Ring& ring, uint32_t rank, int lane) {
   constexpr int kPer = BN / 32;
   uint32_t n = 0;  // k-blocks so far
@@ -475,7 +514,7 @@ __device__ void scale_role(const ExpertsParams& p, const Schedule<kOpFp8, BN>& s
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) ring.scales[slot * kXRows + j * 32 + lane] = x[j] * w;
+      for (int j = 0; j < kPer; ++j) ring.scales[slot * BN + j * 32 + lane] = x[j] * w;
       if (kb + 1 < u.kb1) fetch(kb + 1);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.sfull[slot]);
@@ -489,7 +528,7 @@ __device__ void scale_role(const ExpertsParams& p, const Schedule<kOpFp8, BN>& s
 
 // ------------------------------------------------------------------ MMA (one thread)
 template <int OP, int BN>
-__device__ void mma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, const Ring& ring,
+__device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ring& ring,
                          uint32_t tmem) {
   constexpr int kStagesX = stages_of(BN);
   constexpr bool kWMn = OP == kOpForward || OP == kOpWeight;
@@ -580,31 +619,44 @@ __device__ void mma_role(const ExpertsParams& p, const Schedule<OP, BN>& sch, co
 }
 
 // ------------------------------------------------------------------ epilogue
-// 8 rows of one output column per lane.
+// 8 rows of one output column per lane, 32 columns a warp.  They are turned in shared
+// memory (a buffer per warp) so that a store instruction writes 16 bytes a lane, 64 or
+// 128 contiguous bytes of each row: stores of one element a lane, at the LSU's rate of
+// one instruction per about 7 cycles, took 7000 cycles for a 256 x 256 tile.
 struct Out {
   void* base;
-  int64_t ldo, row0, col;
+  int64_t ldo, row0, col;  // col: the warp's first
   int type;
-  bool col_ok;
-  int32_t cnt;
-  __device__ __forceinline__ void store(int32_t c0, const float (&v)[8]) const {
-    if (!col_ok) return;
-    const int32_t n = cnt - c0;
+  int32_t cnt, cols;       // rows of the tile; columns of the output from col on
+  uint8_t* stage;          // 1 KB
+  __device__ __forceinline__ void store(int32_t c0, const float (&v)[8], int lane) const {
+    __syncwarp();  // the buffer has been read
     if (type == kTypeF32) {
-      float* o = static_cast<float*>(base) + (row0 + c0) * ldo + col;
+      float* s = reinterpret_cast<float*>(stage) + lane;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) o[i * ldo] = v[i];
-    } else if (type == kTypeF16) {
-      __half* o = static_cast<__half*>(base) + (row0 + c0) * ldo + col;
+      for (int i = 0; i < 8; ++i) s[i * 32] = v[i];
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) o[i * ldo] = __float2half_rn(v[i]);
+      for (int h = 0; h < 2; ++h) {
+        const int row = h * 4 + (lane >> 3), part = (lane & 7) * 4;
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 128 + part * 4);
+        if (c0 + row < cnt && part < cols)
+          *reinterpret_cast<uint4*>(static_cast<float*>(base) + (row0 + c0 + row) * ldo + col + part) = x;
+      }
     } else {
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(base) + (row0 + c0) * ldo + col;
+      uint16_t* s = reinterpret_cast<uint16_t*>(stage) + lane;
+      if (type == kTypeF16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) o[i * ldo] = __float2bfloat16_rn(v[i]);
+        for (int i = 0; i < 8; ++i) s[i * 32] = __half_as_ushort(__float2half_rn(v[i]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i * 32] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+      }
+      __syncwarp();
+      const int row = lane >> 2, part = (lane & 3) * 8;
+      const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 64 + part * 2);
+      if (c0 + row < cnt && part < cols)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + (row0 + c0 + row) * ldo + col + part) = x;
     }
   }
 };
@@ -643,7 +695,7 @@ __device__ __forceinline__ void store_row8(void* base, int type, int64_t at, con
 // no shared memory in the loop: with the scales on the columns, reading them took as
 // much of the shared memory's time as the MMA's operands.
 template <int BN>
-__device__ void epilogue_long(const ExpertsParams& p, const Schedule<kOpFp8Long, BN>& sch,
+__device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& sch,
                               const Ring& ring, uint32_t rank, int ew, int lane, uint32_t tmem) {
   const int quad = (threadIdx.x >> 5) & 3, c_first = (ew >> 2) * 64;
   uint32_t acc = 0;
@@ -765,7 +817,7 @@ __device__ void epilogue_long(const ExpertsParams& p, const Schedule<kOpFp8Long,
 }
 
 template <int OP, int BN>
-__device__ void epilogue_role(const ExpertsParams& p, const Schedule<OP, BN>& sch,
+__device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
                               const Ring& ring, uint32_t rank, int ew, int lane, uint32_t tmem) {
   constexpr int kCols = BN / 4;  // columns of a warp, at most
   const int quad = (threadIdx.x >> 5) & 3, quarter = ew >> 2;
@@ -782,7 +834,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Schedule<OP, BN>& sc
       const uint32_t tempty0 = mapa_shared(smem_u32(ring.tempty), 0);
       const int32_t seg = OP == kOpFp8 ? 1 : p.segment;
       for (int32_t left = u.kb1 - u.kb0; left > 0; left -= seg) {
-        [[maybe_unused]] const float* scale = ring.scales + (acc % kScaleSlots) * kXRows + c_first;
+        [[maybe_unused]] const float* scale = ring.scales + (acc % kScaleSlots) * BN + c_first;
         bool ok = true;
         if constexpr (OP == kOpFp8)
           ok = mbar_wait(&ring.sfull[acc % kScaleSlots], (acc / kScaleSlots) & 1u, p.timeout_ns,
@@ -831,10 +883,10 @@ __device__ void epilogue_role(const ExpertsParams& p, const Schedule<OP, BN>& sc
     Unit u;
     sch.get(i, u);
     const int n8 = u.w / 32, c_first = quarter * n8 * 8;
-    const int64_t col = static_cast<int64_t>(u.n0) + rank * 128 + quad * 32 + lane;
+    const int32_t col = u.n0 + static_cast<int32_t>(rank) * 128 + quad * 32;
     const Out out{p.out, p.ldo,
                   OP == kOpWeight ? static_cast<int64_t>(u.e) * p.out_rows + u.kt0 : u.row0, col,
-                  p.out_type, col < p.wide, u.cnt};
+                  p.out_type, u.cnt, p.wide - col, ring.stage_out + ew * kOutBytes};
     auto eight = [&](int c, float (&v)[8]) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) unpack2(sums[c * 4 + j], v[2 * j], v[2 * j + 1]);
@@ -845,7 +897,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Schedule<OP, BN>& sc
         if (c < n8) {
           float v[8];
           eight(c, v);
-          out.store(c_first + c * 8, v);
+          out.store(c_first + c * 8, v, lane);
         }
       continue;
     }
@@ -870,7 +922,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Schedule<OP, BN>& sc
         for (int s = 0; s < sch.split; ++s)
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] += __ldcg(first + s * kNext + (c * 8 + j) * 32);
-        out.store(c_first + c * 8, v);
+        out.store(c_first + c * 8, v, lane);
       }
   }
 }
@@ -887,8 +939,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   ring.w = smem;
   ring.r = smem + kStagesX * kSub * kWBytes;
   ring.scales = reinterpret_cast<float*>(ring.r + kStagesX * kSub * r_bytes(BN));
-  int32_t* off = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(ring.scales) +
-                                            (OP == kOpFp8 ? kScaleBytes : 0));
+  ring.stage_out = reinterpret_cast<uint8_t*>(ring.scales) + scale_bytes(OP, BN);
+  int32_t* off = reinterpret_cast<int32_t*>(ring.stage_out + kXEpiWarps * kOutBytes);
   int32_t* pre = off + kMaxExperts + 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(off) + kTableBytes);
   ring.full = bars;
@@ -936,7 +988,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (valid) {
-    const Schedule<OP, BN> sch(p, off, pre);
+    Schedule<OP, BN> sch(p, off, pre);
     if (warp == 0) {
       tma_role<OP, BN>(p, sch, ring, rank, lane);
     } else if (warp == 1) {
@@ -982,7 +1034,7 @@ struct Variant {
 template <int OP, int BN>
 Variant variant_of() {
   return {reinterpret_cast<const void*>(&experts_kernel<OP, BN>), threads_of(OP),
-          smem_bytes(BN, OP == kOpFp8)};
+          smem_bytes(OP, BN)};
 }
 Variant variant(int op, bool few) {
   switch (op) {
