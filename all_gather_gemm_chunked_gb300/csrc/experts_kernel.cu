@@ -115,6 +115,14 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// A wait of a whole warp: the vote keeps its control flow uniform, so that what the
+// warp computes around it (the MMA's descriptors) stays in uniform registers.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
+                                          volatile int* abort, const volatile uint32_t* gstatus) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, timeout_ns, abort, gstatus));
+}
+
 // Two 32-bit sums in one instruction (the epilogue issues one per two columns).
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
   uint64_t r;
@@ -526,10 +534,11 @@ __device__ void scale_role(const ExpertsParams& p, Schedule<kOpFp8, BN>& sch,
   }
 }
 
-// ------------------------------------------------------------------ MMA (one thread)
+// ------------------------------------------------------------------ MMA (one warp)
+// The warp waits and computes together; lane 0 issues.
 template <int OP, int BN>
 __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ring& ring,
-                         uint32_t tmem) {
+                         int lane, uint32_t tmem) {
   constexpr int kStagesX = stages_of(BN);
   constexpr bool kWMn = OP == kOpForward || OP == kOpWeight;
   constexpr bool kRMn = OP == kOpWeight;
@@ -545,7 +554,7 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
   uint32_t acc = 0, full_phase = 0, zeroed = 0;  // bit s: parity of stage s's barriers
   bool ok = true;
   auto accumulator = [&] {  // wait until it has been read
-    const bool r = mbar_wait(&ring.tempty[acc & 1u], ((acc >> 1) & 1u) ^ 1u, p.timeout_ns,
+    const bool r = warp_wait(&ring.tempty[acc & 1u], ((acc >> 1) & 1u) ^ 1u, p.timeout_ns,
                              ring.abort, p.status);
     tc_fence_after();
     return r;
@@ -567,11 +576,11 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
       if (OP == kOpWeight && u.red_rows - (kb0 + n_sub) * 64 < 0) {
         // a group's last k-block comes through both CTAs' zeroing warps
         last_steps = (u.red_rows - (kb0 + n_sub - 1) * 64 + 15) / 16;
-        ok = mbar_wait_cluster(&ring.zfull[stage], (zeroed >> stage) & 1u, p.timeout_ns, ring.abort,
-                               p.status);
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&ring.zfull[stage], (zeroed >> stage) & 1u,
+                                                       p.timeout_ns, ring.abort, p.status));
         zeroed ^= 1u << stage;
       } else {
-        ok = mbar_wait(&ring.full[stage], (full_phase >> stage) & 1u, p.timeout_ns, ring.abort,
+        ok = warp_wait(&ring.full[stage], (full_phase >> stage) & 1u, p.timeout_ns, ring.abort,
                        p.status);
         full_phase ^= 1u << stage;
       }
@@ -584,35 +593,36 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
         if (s >= n_sub) break;
         if (is_fp8(OP) && !(ok = accumulator())) break;
         const uint32_t d = tmem + (acc & 1u) * 256u;
+        if (lane == 0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (OP == kOpWeight && s == n_sub - 1 && k >= last_steps) break;
-          const uint64_t wd = ws + (s * kWBytes / 16 + k * kWStep);
-          const uint64_t rd = rs + (s * r_bytes(BN) / 16 + k * kRStep);
-          if constexpr (is_fp8(OP))
-            mma_f8_pair(d, wd, rd, idesc, k > 0 ? 1u : 0u);
-          else
-            mma_f16_pair(d, wd, rd, idesc, (!first || s > 0 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < 4; ++k) {
+            if (OP == kOpWeight && s == n_sub - 1 && k >= last_steps) break;
+            const uint64_t wd = ws + (s * kWBytes / 16 + k * kWStep);
+            const uint64_t rd = rs + (s * r_bytes(BN) / 16 + k * kRStep);
+            if constexpr (is_fp8(OP))
+              mma_f8_pair(d, wd, rd, idesc, k > 0 ? 1u : 0u);
+            else
+              mma_f16_pair(d, wd, rd, idesc, (!first || s > 0 || k > 0) ? 1u : 0u);
+          }
+          if (is_fp8(OP)) mma_commit_pair_both(&ring.tfull[acc & 1u]);
         }
-        if (is_fp8(OP)) {
-          mma_commit_pair_both(&ring.tfull[acc & 1u]);
-          ++acc;
-        }
+        if (is_fp8(OP)) ++acc;
       }
       if (!ok) break;
-      mma_commit_pair_both(&ring.empty[stage]);
+      if (lane == 0) mma_commit_pair_both(&ring.empty[stage]);
       if (++stage == kStagesX) stage = 0;
       if (!is_fp8(OP)) {
         left -= n_sub;
         if (left <= 0 || kb0 + kSub >= u.kb1) {
           left = 0;
-          mma_commit_pair_both(&ring.tfull[acc & 1u]);
+          if (lane == 0) mma_commit_pair_both(&ring.tfull[acc & 1u]);
           ++acc;
         }
       }
+      __syncwarp();
     }
   }
-  if (!ok) {
+  if (!ok && lane == 0) {
     set_status(p.status, kStatusPipelineTimeout, 0x200u);
     *ring.abort = 1;
   }
@@ -992,7 +1002,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     if (warp == 0) {
       tma_role<OP, BN>(p, sch, ring, rank, lane);
     } else if (warp == 1) {
-      if (rank == 0 && lane == 0) mma_role<OP, BN>(p, sch, ring, tmem);
+      if (rank == 0) mma_role<OP, BN>(p, sch, ring, lane, tmem);
     } else if (warp < 2 + kXEpiWarps) {
       if constexpr (OP == kOpFp8Long)
         epilogue_long<BN>(p, sch, ring, rank, warp - 2, lane, tmem);
