@@ -66,13 +66,14 @@ constexpr int kWBytes = 128 * 128;  // a CTA's wide operand per k-block: 128 x 1
 // k-blocks per stage of the ring.  The MMA thread's work around a stage (a wait, a
 // fence, a commit) took about 0.2 us, as long as the MMAs of one k-block; two k-blocks
 // a stage halve it.
-constexpr int kSub = 2;
+constexpr int kSub = kXSub;
+constexpr int kGroupBytes = kSub * 64 * 128;  // MN-major: 64 columns of a stage
 
 __host__ __device__ constexpr int rows_per_cta(int BN) { return BN / 2; }
 __host__ __device__ constexpr int r_bytes(int BN) { return rows_per_cta(BN) * 128; }
 // Stages that fit: 3 of 64 KB, or 5 of 40 KB for short row tiles, where the bytes in
 // flight are nearly the weights' alone.
-__host__ __device__ constexpr int stages_of(int BN) { return BN == kXRows ? 3 : 5; }
+__host__ __device__ constexpr int stages_of(int BN) { return (BN == kXRows ? 6 : 10) / kSub; }
 constexpr int kScaleSlots = 4;  // e4m3: k-blocks whose scales are held
 __host__ __device__ constexpr int scale_bytes(int op, int BN) { return op == kOpFp8 ? kScaleSlots * BN * 4 : 0; }
 constexpr int kOutBytes = 1024;  // an epilogue warp's buffer for 8 rows of output
@@ -365,16 +366,36 @@ struct Ring {
 };
 
 // ------------------------------------------------------------------ TMA warp
-// Two loads of 64 columns, or one of both where the operand is described in blocks.
+// The loads of a stage's two k-blocks of one operand: one TMA instruction where the
+// operand's extent allows a view in blocks of 128 bytes, two otherwise.  (The TMA
+// unit's time per instruction counts: an instruction for each k-block instead took
+// %TMA%.)
+// MN-major: 128 columns from col by 128 rows of the sum's dimension from row.
 __device__ __forceinline__ void load_mn(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
-                                        int32_t blk, int32_t col, int32_t row, int32_t e,
-                                        int groups) {
+                                        int32_t blk, int32_t col, int32_t row, int32_t e) {
   if (blk) {
     tma_load_4d_pair(dst, map, bar, 0, row, col / 64, e);
   } else {
-    for (int i = 0; i < groups; ++i)
-      tma_load_3d_pair(dst + i * (64 * 128), map, bar, col + i * 64, row, e);
+    tma_load_3d_pair(dst, map, bar, col, row, e);
+    tma_load_3d_pair(dst + kGroupBytes, map, bar, col + 64, row, e);
   }
+}
+// K-major: rows of e from row, k-blocks kb and kb + 1 (bk elements each).
+__device__ __forceinline__ void load_k(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
+                                       int32_t blk, int32_t kb, int32_t bk, int32_t row, int32_t e,
+                                       int32_t second) {
+  if (blk) {
+    tma_load_4d_pair(dst, map, bar, 0, row, kb, e);
+  } else {
+    for (int s = 0; s < kSub; ++s)
+      tma_load_3d_pair(dst + s * second, map, bar, (kb + s) * bk, row, e);
+  }
+}
+
+// Box height of the row operand's loads (rows of a CTA, rounded up to its four sizes).
+template <int BN>
+__device__ __forceinline__ int32_t box_of(int32_t half) {
+  return (half + BN / 8 - 1) / (BN / 8);
 }
 
 template <int OP, int BN>
@@ -382,17 +403,16 @@ __device__ void tma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
                          uint32_t rank, int lane) {
   constexpr int kStagesX = stages_of(BN);
   const uint32_t full0 = mapa_shared(smem_u32(ring.full), 0);
-  const uint32_t tail0 = mapa_shared(smem_u32(ring.tail), rank);
+  [[maybe_unused]] const uint32_t tail0 = mapa_shared(smem_u32(ring.tail), rank);
   int stage = 0;
   uint32_t phase = 0, issued = 0, filled = 0;  // bit s: stage s used; its loads' parity
   bool ok = true;
   Unit u;
   for (int32_t i = 0; ok && sch.get(i, u); ++i) {
     const int32_t half = u.w / 2;
-    const int box = OP == kOpWeight ? 0 : (half + BN / 8 - 1) / (BN / 8) - 1;
-    const uint32_t r_tx = OP == kOpWeight || OP == kOpFp8Long
-                              ? static_cast<uint32_t>(r_bytes(BN))
-                              : static_cast<uint32_t>((box + 1) * (BN / 8) * 128);
+    const int32_t boxes = OP == kOpWeight || OP == kOpFp8Long ? kXRowBoxes : box_of<BN>(half);
+    const int32_t height = boxes * (BN / 8);
+    const uint32_t tx = static_cast<uint32_t>(kSub * (kWBytes + height * 128));
     const int32_t n = u.n0 + static_cast<int32_t>(rank) * 128;
     for (int32_t kb0 = u.kb0; kb0 < u.kb1; kb0 += kSub) {
       const int n_sub = u.kb1 - kb0 < kSub ? u.kb1 - kb0 : kSub;
@@ -404,32 +424,29 @@ __device__ void tma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
         uint32_t bar = full0 + stage * 8;
         if (tail) {
           bar = tail0 + stage * 8;  // counted here: zero_role passes it on
-          mbar_arrive_expect_tx(&ring.tail[stage], n_sub * (kWBytes + r_tx));
+          mbar_arrive_expect_tx(&ring.tail[stage], tx);
         } else {
-          if (rank == 0) mbar_arrive_expect_tx(&ring.full[stage], 2 * n_sub * (kWBytes + r_tx));
+          if (rank == 0) mbar_arrive_expect_tx(&ring.full[stage], 2 * tx);
           issued |= 1u << stage;
           filled ^= 1u << stage;
         }
-        for (int s = 0; s < n_sub; ++s) {
-          const int32_t kb = kb0 + s;
-          uint8_t* wd = ring.w + (stage * kSub + s) * kWBytes;
-          uint8_t* rd = ring.r + (stage * kSub + s) * r_bytes(BN);
-          if constexpr (OP == kOpFp8Long) {
-            tma_load_2d_pair(wd, &p.tm_r[kXRowBoxes - 1], bar, kb * 128,
-                             u.row0 + static_cast<int32_t>(rank) * 128);
-            tma_load_3d_pair(rd, &p.tm_w, bar, kb * 128, u.n0 + static_cast<int32_t>(rank) * half, u.e);
-          } else if constexpr (OP == kOpForward) {
-            load_mn(wd, &p.tm_w, bar, p.w_blk, n, kb * 64, u.e, 2);
-          } else if constexpr (OP == kOpWeight) {
-            load_mn(wd, &p.tm_w, bar, p.w_blk, n, u.row0 + kb * 64, 0, 2);
-            load_mn(rd, &p.tm_r[0], bar, p.r_blk, u.kt0 + static_cast<int32_t>(rank) * half,
-                    u.row0 + kb * 64, 0, 2);
-          } else {
-            tma_load_3d_pair(wd, &p.tm_w, bar, kb * block_k<OP>(), n, u.e);
-          }
-          if constexpr (OP == kOpForward || OP == kOpInput || OP == kOpFp8)
-            tma_load_2d_pair(rd, &p.tm_r[box], bar, kb * block_k<OP>(),
-                             u.row0 + static_cast<int32_t>(rank) * half);
+        uint8_t* wd = ring.w + stage * (kSub * kWBytes);
+        uint8_t* rd = ring.r + stage * (kSub * r_bytes(BN));
+        const int32_t mine = static_cast<int32_t>(rank) * half;
+        if constexpr (OP == kOpFp8Long) {
+          load_k(wd, &p.tm_r[kXRowBoxes - 1], bar, p.r_blk, kb0, 128,
+                 u.row0 + static_cast<int32_t>(rank) * 128, 0, kWBytes);
+          load_k(rd, &p.tm_w, bar, p.w_blk, kb0, 128, u.n0 + mine, u.e, r_bytes(BN));
+        } else if constexpr (OP == kOpWeight) {
+          load_mn(wd, &p.tm_w, bar, p.w_blk, n, u.row0 + kb0 * 64, 0);
+          load_mn(rd, &p.tm_r[0], bar, p.r_blk, u.kt0 + mine, u.row0 + kb0 * 64, 0);
+        } else {
+          if constexpr (OP == kOpForward)
+            load_mn(wd, &p.tm_w, bar, p.w_blk, n, kb0 * 64, u.e);
+          else
+            load_k(wd, &p.tm_w, bar, p.w_blk, kb0, block_k<OP>(), n, u.e, kWBytes);
+          load_k(rd, &p.tm_r[boxes - 1], bar, p.r_blk, kb0, block_k<OP>(), u.row0 + mine, 0,
+                 height * 128);
         }
       }
       __syncwarp();
@@ -468,7 +485,7 @@ __device__ void zero_role(const ExpertsParams& p, Schedule<kOpWeight, BN>& sch,
     const int valid = u.red_rows & 63;
     if (valid == 0) continue;
     const uint32_t stage = (stages - 1) % kStagesX;
-    const uint32_t block = stage * kSub + (u.kb1 - 1) % kSub;
+    const int first = ((u.kb1 - 1) % kSub) * 64 + valid;  // of the stage's 128 rows
     bool ok = mbar_wait(&ring.tail[stage], (used >> stage) & 1u, p.timeout_ns, ring.abort, p.status);
     used ^= 1u << stage;
     ok = __all_sync(0xffffffffu, ok);
@@ -481,9 +498,9 @@ __device__ void zero_role(const ExpertsParams& p, Schedule<kOpWeight, BN>& sch,
     }
     const int n16 = (((valid + 15) & ~15) - valid) * 8;  // 16-byte pieces per block of 64 columns
     for (int j = lane; j < 4 * n16; j += 32) {
-      const int blk = j / n16, o = valid * 128 + (j - blk * n16) * 16;
-      uint8_t* base = blk < 2 ? ring.w + block * kWBytes + blk * (64 * 128)
-                              : ring.r + block * r_bytes(BN) + (blk - 2) * (64 * 128);
+      const int blk = j / n16, o = first * 128 + (j - blk * n16) * 16;
+      uint8_t* base = blk < 2 ? ring.w + stage * (kSub * kWBytes) + blk * kGroupBytes
+                              : ring.r + stage * (kSub * r_bytes(BN)) + (blk - 2) * kGroupBytes;
       *reinterpret_cast<uint4*>(base + o) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_shared();
@@ -543,13 +560,14 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
   constexpr bool kWMn = OP == kOpForward || OP == kOpWeight;
   constexpr bool kRMn = OP == kOpWeight;
   // 128-byte swizzle.  K-major: groups of 8 rows 1024 B apart, 32 B further per step.
-  // MN-major: blocks of 64 columns 8 KB apart, groups of 8 rows 1024 B apart, 16 rows
+  // MN-major: blocks of 64 columns kGroupBytes apart, groups of 8 rows 1024 B apart, 16 rows
   // (2 KB) per step.  (The address is the descriptor's lowest field, in units of 16.)
-  const uint64_t w0 = kWMn ? smem_desc_sw128(smem_u32(ring.w), 64 * 128, 1024)
+  const uint64_t w0 = kWMn ? smem_desc_sw128(smem_u32(ring.w), kGroupBytes, 1024)
                            : smem_desc_sw128(smem_u32(ring.w), 16, 1024);
-  const uint64_t r0 = kRMn ? smem_desc_sw128(smem_u32(ring.r), 64 * 128, 1024)
+  const uint64_t r0 = kRMn ? smem_desc_sw128(smem_u32(ring.r), kGroupBytes, 1024)
                            : smem_desc_sw128(smem_u32(ring.r), 16, 1024);
   constexpr uint32_t kWStep = (kWMn ? 2048 : 32) / 16, kRStep = (kRMn ? 2048 : 32) / 16;
+  constexpr uint32_t kWSecond = (kWMn ? 64 * 128 : kWBytes) / 16;  // the second k-block
   int stage = 0;
   uint32_t acc = 0, full_phase = 0, zeroed = 0;  // bit s: parity of stage s's barriers
   bool ok = true;
@@ -563,6 +581,9 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
   for (int32_t i = 0; ok && sch.get(i, u); ++i) {
     const uint32_t idesc = idesc_f16_f32(kXWide, u.w, kWMn, kRMn) |
                            (!is_fp8(OP) && p.bf16 ? kIdescAbBf16 : 0u);
+    const uint32_t r_second = kRMn ? 64 * 128 / 16
+                              : OP == kOpFp8Long ? r_bytes(BN) / 16
+                                                 : static_cast<uint32_t>(box_of<BN>(u.w / 2) * (BN / 8) * 128 / 16);
     int32_t left = 0;  // k-blocks left of the segment
     for (int32_t kb0 = u.kb0; kb0 < u.kb1; kb0 += kSub) {
       const int n_sub = u.kb1 - kb0 < kSub ? u.kb1 - kb0 : kSub;
@@ -597,8 +618,8 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (OP == kOpWeight && s == n_sub - 1 && k >= last_steps) break;
-            const uint64_t wd = ws + (s * kWBytes / 16 + k * kWStep);
-            const uint64_t rd = rs + (s * r_bytes(BN) / 16 + k * kRStep);
+            const uint64_t wd = ws + (s * kWSecond + k * kWStep);
+            const uint64_t rd = rs + (s * r_second + k * kRStep);
             if constexpr (is_fp8(OP))
               mma_f8_pair(d, wd, rd, idesc, k > 0 ? 1u : 0u);
             else

@@ -22,6 +22,7 @@ constexpr int kXWide = 256;    // a pair's tile: 256 of the wide dimension
 constexpr int kXRows = 256;    // and up to 256 rows,
 constexpr int kXFewRows = 64;  // or up to 64 where groups are short
 constexpr int kXRowBoxes = 4;  // box heights of the row operand: 1/4 to 4/4 of half a tile
+constexpr int kXSub = 2;       // k-blocks of 128 bytes per stage of the ring
 constexpr int kXEpiWarps = 16;
 // TMA warp, MMA warp, epilogue warps; the weight gradient's zeroing warp, or the
 // scale warp of e4m3.
@@ -39,7 +40,7 @@ struct ExpertsParams {
   int32_t wide;                  // extent of the wide dimension
   int32_t red;                   // length of the sums (weight gradient: unused)
   int32_t out_rows;              // weight gradient: output rows per expert (K)
-  int32_t w_blk, r_blk;          // MN-major operand described in blocks of 64 columns (one load), or not (two)
+  int32_t w_blk, r_blk;          // operand described in blocks of 128 bytes (one load a stage), or not (two)
   int32_t segment;               // k-blocks per accumulator (e4m3: 1)
   int32_t bf16;                  // operands are bfloat16 (otherwise fp16)
   int32_t out_type;              // ElemType of the output

@@ -138,32 +138,40 @@ CUtensorMapDataType map_type(int dtype) {
   return dtype == AG_MOE_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
-// An operand whose sum runs along the memory rows' length: box of 128 bytes by
-// `height` rows of one of E matrices (extent len x rows; 2D for the row operand).
+// An operand whose sum runs along the memory rows' length: two k-blocks of 128 bytes by
+// `height` rows of one of E matrices (extent len x rows).  With whole blocks the length
+// is described in blocks and one box brings both.
+bool whole_blocks(int dtype, int64_t len) { return len * esize(dtype) % 128 == 0; }
 int encode_k_major(CUtensorMap* map, int dtype, const void* base, int64_t len, int64_t rows,
-                   int64_t ld, int64_t E, int64_t ld_e, int height, bool three_d) {
+                   int64_t ld, int64_t E, int64_t ld_e, int height) {
   const int es = esize(dtype);
+  const cuuint64_t in = 128 / es;
+  if (whole_blocks(dtype, len)) {
+    const cuuint64_t dims[4] = {in, (cuuint64_t)rows, (cuuint64_t)len / in, (cuuint64_t)E};
+    const cuuint64_t strides[3] = {(cuuint64_t)ld * es, 128, (cuuint64_t)ld_e * es};
+    const cuuint32_t box[4] = {(cuuint32_t)in, (cuuint32_t)height, agg::kXSub, 1};
+    return encode_tiled(map, map_type(dtype), base, 4, dims, strides, box);
+  }
   const cuuint64_t dims[3] = {(cuuint64_t)len, (cuuint64_t)rows, (cuuint64_t)E};
   const cuuint64_t strides[2] = {(cuuint64_t)ld * es, (cuuint64_t)ld_e * es};
-  const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)height, 1};
-  return encode_tiled(map, map_type(dtype), base, three_d ? 3 : 2, dims, strides, box);
+  const cuuint32_t box[3] = {(cuuint32_t)in, (cuuint32_t)height, 1};
+  return encode_tiled(map, map_type(dtype), base, 3, dims, strides, box);
 }
 
-// An operand whose sum runs across the memory rows (2-byte elements): 64 columns
-// by 64 rows; with cols % 64 == 0 in blocks of 64 columns, two of them a box, so
-// that a CTA's 128 columns are one load.
-bool in_blocks(int64_t cols) { return cols % 64 == 0; }
+// An operand whose sum runs across the memory rows (2-byte elements): 128 rows (two
+// k-blocks) by 64 columns; with cols % 64 == 0 in blocks of 64 columns, two of them a
+// box, so that a CTA's 128 columns are one load.
 int encode_mn_major(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld,
                     int64_t E, int64_t ld_e) {
-  if (in_blocks(cols)) {
+  if (whole_blocks(AG_GEMM_F16, cols)) {
     const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)cols / 64, (cuuint64_t)E};
     const cuuint64_t strides[3] = {(cuuint64_t)ld * 2, 128, (cuuint64_t)ld_e * 2};
-    const cuuint32_t box[4] = {64, 64, 2, 1};
+    const cuuint32_t box[4] = {64, 64 * agg::kXSub, 2, 1};
     return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, 4, dims, strides, box);
   }
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)E};
   const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld_e * 2};
-  const cuuint32_t box[3] = {64, 64, 1};
+  const cuuint32_t box[3] = {64, 64 * agg::kXSub, 1};
   return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, 3, dims, strides, box);
 }
 
@@ -236,13 +244,14 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
 int encode_rows(agg::ExpertsParams& x, int dtype, const void* base, int64_t len, int64_t rows,
                 int64_t ld, bool few) {
   const int step = (few ? agg::kXFewRows : agg::kXRows) / 8;
+  x.r_blk = whole_blocks(dtype, len);
   for (int i = 0; i < agg::kXRowBoxes; ++i)
-    if (int rc = encode_k_major(&x.tm_r[i], dtype, base, len, rows, ld, 1, 0, (i + 1) * step, false))
+    if (int rc = encode_k_major(&x.tm_r[i], dtype, base, len, rows, ld, 1, rows * ld, (i + 1) * step))
       return rc;
   return AG_GEMM_OK;
 }
 
-// forward (transposed: false) and input gradient: out rows x wide over red.
+// Forward and input gradient: out rows x wide over red.
 int run_rows(ag_moe_plan* p, int op, int64_t rows, const void* in, int64_t ld_in,
              const int32_t* offsets, const void* w, int64_t ldw, int64_t ldw_e, void* out,
              int64_t ld_out, int out_dtype, void* stream) {
@@ -265,13 +274,13 @@ int run_rows(ag_moe_plan* p, int op, int64_t rows, const void* in, int64_t ld_in
   if (fwd)
     rc = encode_mn_major(&x.tm_w, w, p->N, p->K, ldw, p->E, ldw_e);
   else
-    rc = encode_k_major(&x.tm_w, p->dtype, w, p->N, p->K, ldw, p->E, ldw_e, 128, true);
+    rc = encode_k_major(&x.tm_w, p->dtype, w, p->N, p->K, ldw, p->E, ldw_e, 128);
   if (rc || (rc = encode_rows(x, p->dtype, in, red, rows, ld_in, few))) return rc;
   x.offsets = offsets;
   x.rows = static_cast<int32_t>(rows);
   x.wide = static_cast<int32_t>(wide);
   x.red = static_cast<int32_t>(red);
-  x.w_blk = in_blocks(p->N);
+  x.w_blk = whole_blocks(p->dtype, p->N);
   x.out_type = out_dtype;
   x.out = out;
   x.ldo = ld_out;
@@ -548,8 +557,8 @@ int ag_moe_backward_weight(ag_moe_plan* plan, int64_t rows, const void* x, int64
   p.rows = static_cast<int32_t>(rows);
   p.wide = static_cast<int32_t>(plan->N);
   p.out_rows = static_cast<int32_t>(plan->K);
-  p.w_blk = in_blocks(plan->N);
-  p.r_blk = in_blocks(plan->K);
+  p.w_blk = whole_blocks(plan->dtype, plan->N);
+  p.r_blk = whole_blocks(plan->dtype, plan->K);
   p.out_type = out_dtype;
   p.out = dw;
   p.ldo = plan->N;
@@ -570,7 +579,7 @@ int ag_fp8_forward(ag_moe_plan* plan, int64_t rows, const void* xq, const float*
   std::memset(&p, 0, sizeof(p));
   const bool few = few_rows(plan, rows);
   int rc;
-  if ((rc = encode_k_major(&p.tm_w, AG_MOE_E4M3, wq, plan->K, plan->N, plan->K, plan->E, plan->K * plan->N, 128, true)) ||
+  if ((rc = encode_k_major(&p.tm_w, AG_MOE_E4M3, wq, plan->K, plan->N, plan->K, plan->E, plan->K * plan->N, 128)) ||
       (rc = encode_rows(p, AG_MOE_E4M3, xq, plan->K, rows, plan->K, few)))
     return rc;
   p.offsets = offsets;
@@ -580,6 +589,7 @@ int ag_fp8_forward(ag_moe_plan* plan, int64_t rows, const void* xq, const float*
   p.out_type = out_dtype;
   p.out = y;
   p.ldo = ldy;
+  p.w_blk = whole_blocks(AG_MOE_E4M3, plan->K);
   p.xs = xs;
   p.ws = ws;
   return run(plan, p, agg::kOpFp8, few, rows / (few ? agg::kXFewRows : agg::kXRows) + plan->E, stream);
