@@ -75,14 +75,19 @@ __host__ __device__ constexpr int r_bytes(int BN) { return rows_per_cta(BN) * 12
 // flight are nearly the weights' alone.
 __host__ __device__ constexpr int stages_of(int BN) { return (BN == kXRows ? 6 : 10) / kSub; }
 constexpr int kScaleSlots = 4;  // e4m3: k-blocks whose scales are held
-__host__ __device__ constexpr int scale_bytes(int op, int BN) { return op == kOpFp8 ? kScaleSlots * BN * 4 : 0; }
+constexpr int kScaleBatch = 4;  // and for long groups: two batches of four, for both column blocks
+__host__ __device__ constexpr int scale_bytes(int op, int BN) {
+  return op == kOpFp8 ? kScaleSlots * BN * 4 : op == kOpFp8Long ? 2 * kScaleBatch * 2 * 128 * 4 : 0;
+}
 constexpr int kOutBytes = 1024;  // an epilogue warp's buffer for 8 rows of output
+__host__ __device__ constexpr int out_bytes(int op) { return op == kOpFp8Long ? 0 : kXEpiWarps * kOutBytes; }
 constexpr int kTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) & ~15;
 __host__ __device__ constexpr int smem_bytes(int op, int BN) {
   return stages_of(BN) * kSub * (kWBytes + r_bytes(BN)) + scale_bytes(op, BN) +
-         kXEpiWarps * kOutBytes + kTableBytes + 512 /*barriers*/ + 1024 /*alignment*/;
+         out_bytes(op) + kTableBytes + 512 /*barriers*/ + 1024 /*alignment*/;
 }
-static_assert(smem_bytes(kOpForward, kXRows) <= 227 * 1024 && smem_bytes(kOpFp8, kXFewRows) <= 227 * 1024,
+static_assert(smem_bytes(kOpForward, kXRows) <= 227 * 1024 && smem_bytes(kOpFp8, kXFewRows) <= 227 * 1024 &&
+                  smem_bytes(kOpFp8Long, kXRows) <= 227 * 1024,
               "shared memory of an SM");
 
 __device__ __forceinline__ void set_status(uint32_t* status, uint32_t kind, uint32_t detail) {
@@ -153,6 +158,14 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                  "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
+
+// Accumulators in TMEM's 512 columns: 2 of 256, or 8 of 64, which keep the MMA going
+// while the epilogue's answers for short row tiles (a k-block each, e4m3) are on their way.
+__host__ __device__ constexpr int accs_of(int BN) { return 512 / BN; }
+template <int BN>
+__device__ __forceinline__ uint32_t acc_slot(uint32_t acc) { return acc % accs_of(BN); }
+template <int BN>
+__device__ __forceinline__ uint32_t acc_phase(uint32_t acc) { return acc / accs_of(BN) & 1u; }
 
 // ------------------------------------------------------------------ work
 // A unit of work, the same for every role of both CTAs.
@@ -551,6 +564,57 @@ __device__ void scale_role(const ExpertsParams& p, Schedule<kOpFp8, BN>& sch,
   }
 }
 
+// Long groups: this CTA's 128 rows' scales times those of the tile's two column blocks,
+// [k-block][column block][row], a batch of k-blocks per hand-over.
+template <int BN>
+__device__ void scale_long_role(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& sch,
+                                const Ring& ring, uint32_t rank, int lane) {
+  uint32_t batch = 0;
+  bool ok = true;
+  Unit u;
+  for (int32_t i = 0; ok && sch.get(i, u); ++i) {
+    const int32_t NB = (p.wide + 127) / 128, nb = u.n0 / 128;
+    const float* w0 = p.ws + (static_cast<int64_t>(u.e) * NB + nb) * sch.KB;
+    const float* w1 = nb + 1 < NB ? w0 + sch.KB : w0;
+    const int32_t first = static_cast<int32_t>(rank) * 128 + lane;
+    const float* xs = p.xs + u.row0 + first;
+    for (int32_t kb0 = u.kb0; kb0 < u.kb1; kb0 += kScaleBatch, ++batch) {
+      const int32_t n = u.kb1 - kb0 < kScaleBatch ? u.kb1 - kb0 : kScaleBatch;
+      float x[kScaleBatch][4], a[kScaleBatch], b[kScaleBatch];
+#pragma unroll
+      for (int j = 0; j < kScaleBatch; ++j) {
+        if (j < n) {
+          a[j] = __ldg(w0 + kb0 + j);
+          b[j] = __ldg(w1 + kb0 + j);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          x[j][r] = j < n && first + r * 32 < u.cnt
+                        ? __ldg(xs + static_cast<int64_t>(kb0 + j) * p.rows + r * 32) : 0.0f;
+      }
+      const uint32_t slot = batch & 1u;
+      ok = mbar_wait(&ring.sempty[slot], ((batch >> 1) & 1u) ^ 1u, p.timeout_ns, ring.abort, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      float* out = ring.scales + slot * (kScaleBatch * 256) + lane;
+#pragma unroll
+      for (int j = 0; j < kScaleBatch; ++j)
+        if (j < n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            out[j * 256 + r * 32] = x[j][r] * a[j];
+            out[j * 256 + 128 + r * 32] = x[j][r] * b[j];
+          }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.sfull[slot]);
+    }
+  }
+  if (!ok && lane == 0) {
+    set_status(p.status, kStatusPipelineTimeout, 0x500u | rank);
+    *ring.abort = 1;
+  }
+}
+
 // ------------------------------------------------------------------ MMA (one warp)
 // The warp waits and computes together; lane 0 issues.
 template <int OP, int BN>
@@ -572,7 +636,7 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
   uint32_t acc = 0, full_phase = 0, zeroed = 0;  // bit s: parity of stage s's barriers
   bool ok = true;
   auto accumulator = [&] {  // wait until it has been read
-    const bool r = warp_wait(&ring.tempty[acc & 1u], ((acc >> 1) & 1u) ^ 1u, p.timeout_ns,
+    const bool r = warp_wait(&ring.tempty[acc_slot<BN>(acc)], acc_phase<BN>(acc) ^ 1u, p.timeout_ns,
                              ring.abort, p.status);
     tc_fence_after();
     return r;
@@ -613,7 +677,7 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
       for (int s = 0; s < kSub; ++s) {
         if (s >= n_sub) break;
         if (is_fp8(OP) && !(ok = accumulator())) break;
-        const uint32_t d = tmem + (acc & 1u) * 256u;
+        const uint32_t d = tmem + acc_slot<BN>(acc) * BN;
         if (lane == 0) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -625,7 +689,7 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
             else
               mma_f16_pair(d, wd, rd, idesc, (!first || s > 0 || k > 0) ? 1u : 0u);
           }
-          if (is_fp8(OP)) mma_commit_pair_both(&ring.tfull[acc & 1u]);
+          if (is_fp8(OP)) mma_commit_pair_both(&ring.tfull[acc_slot<BN>(acc)]);
         }
         if (is_fp8(OP)) ++acc;
       }
@@ -636,7 +700,7 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
         left -= n_sub;
         if (left <= 0 || kb0 + kSub >= u.kb1) {
           left = 0;
-          if (lane == 0) mma_commit_pair_both(&ring.tfull[acc & 1u]);
+          if (lane == 0) mma_commit_pair_both(&ring.tfull[acc_slot<BN>(acc)]);
           ++acc;
         }
       }
@@ -694,11 +758,12 @@ struct Out {
 
 // After this warp has stored its part of a split sum: true for the warp that comes
 // last and adds the parts.
+template <int kWarps>
 __device__ __forceinline__ bool last_part(const ExpertsParams& p, const Unit& u, int32_t split,
                                           uint32_t rank, int ew, int lane) {
   __threadfence();
   __syncwarp();
-  uint32_t* count = p.arrivals + (static_cast<int64_t>(u.tile) * 2 + rank) * kXEpiWarps + ew;
+  uint32_t* count = p.arrivals + (static_cast<int64_t>(u.tile) * 2 + rank) * kWarps + ew;
   uint32_t before = 0;
   if (lane == 0) before = atomicAdd(count, 1u);
   before = __shfl_sync(0xffffffffu, before, 0);
@@ -722,101 +787,94 @@ __device__ __forceinline__ void store_row8(void* base, int type, int64_t at, con
 }
 
 // e4m3, long groups: a lane is a row here, so a k-block's scale is one number per
-// thread (the row's times that of the warp's 64 columns, which lie in one block), with
-// no shared memory in the loop: with the scales on the columns, reading them took as
-// much of the shared memory's time as the MMA's operands.
+// thread (the row's times that of the warp's 64 columns, which lie in one block).  With
+// the scales on the columns, reading them took as much of the shared memory's time as
+// the MMA's operands.  scale_long_role prepares them, four k-blocks at a time: loads
+// from global memory in this loop stalled it for half of its time.
 template <int BN>
 __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& sch,
                               const Ring& ring, uint32_t rank, int ew, int lane, uint32_t tmem) {
-  const int quad = (threadIdx.x >> 5) & 3, c_first = (ew >> 2) * 64;
-  uint32_t acc = 0;
+  constexpr int kCols = 64;
+  const int quad = (threadIdx.x >> 5) & 3, c_first = (ew >> 2) * kCols;
+  uint32_t acc = 0, batch = 0;
   for (int32_t i = 0;; ++i) {
-    uint64_t sums[32];
+    uint64_t sums[kCols / 2];
 #pragma unroll
-    for (int c = 0; c < 32; ++c) sums[c] = 0;
+    for (int c = 0; c < kCols / 2; ++c) sums[c] = 0;
     {
       Unit u;
       if (!sch.get(i, u)) break;
-      const int cols = u.w - c_first;
-      const int n8 = cols <= 0 ? 0 : cols >= 64 ? 8 : cols / 8;
+      const int cols = u.w - c_first;  // a multiple of 32
+      const int n16 = cols <= 0 ? 0 : cols >= kCols ? kCols / 16 : cols / 16;
       const uint32_t from0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c_first;
       const uint32_t tempty0 = mapa_shared(smem_u32(ring.tempty), 0);
-      const int32_t row = static_cast<int32_t>(rank) * 128 + quad * 32 + lane;
-      const int32_t NB = (p.wide + 127) / 128, nb = (u.n0 + c_first) / 128;
-      const float* ws = p.ws + (static_cast<int64_t>(u.e) * NB + (nb < NB ? nb : NB - 1)) * sch.KB + u.kb0;
-      const float* xs = p.xs + static_cast<int64_t>(u.kb0) * p.rows + u.row0 + (row < u.cnt ? row : 0);
-      const int32_t kbs = u.kb1 - u.kb0;
-      // two k-blocks ahead (pointers at the next one to fetch)
-      float xa = __ldg(xs), wa = __ldg(ws), xb = 0.0f, wb = 0.0f;
-      if (kbs > 1) xb = __ldg(xs + p.rows), wb = __ldg(ws + 1);
-      xs += 2 * static_cast<int64_t>(p.rows);
-      ws += 2;
-      for (int32_t j = 0; j < kbs; ++j) {
-        const float s = xa * wa;
-        xa = xb;
-        wa = wb;
-        if (j + 2 < kbs) {
-          xb = __ldg(xs);
-          wb = __ldg(ws);
-          xs += p.rows;
-          ++ws;
+      const float* scale0 = ring.scales + (c_first >> 7) * 128 + quad * 32 + lane;
+      for (int32_t left = u.kb1 - u.kb0; left > 0; left -= kScaleBatch, ++batch) {
+        const uint32_t slot = batch & 1u;
+        bool ok = mbar_wait(&ring.sfull[slot], (batch >> 1) & 1u, p.timeout_ns, ring.abort, p.status);
+        const int32_t n = left < kScaleBatch ? left : kScaleBatch;
+        for (int32_t j = 0; ok && j < n; ++j) {
+          const float s = scale0[(slot * kScaleBatch + j) * 256];
+          const uint64_t s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+          ok = mbar_wait(&ring.tfull[acc_slot<BN>(acc)], acc_phase<BN>(acc), p.timeout_ns, ring.abort,
+                         p.status);
+          tc_fence_after();
+          const uint32_t from = from0 + acc_slot<BN>(acc) * BN;
+          if (n16 == kCols / 16) {
+#pragma unroll
+            for (int c = 0; c < kCols / 16; ++c) {
+              uint32_t v[16];
+              tmem_ld16(from + c * 16, v);
+              tmem_ld_wait();
+              if (c == kCols / 16 - 1) {  // the accumulator has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(tempty0 + acc_slot<BN>(acc) * 8);
+              }
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                sums[c * 8 + q] = fma2(pack2(v[2 * q], v[2 * q + 1]), s2, sums[c * 8 + q]);
+            }
+          } else {  // the last columns
+#pragma unroll
+            for (int c = 0; c < kCols / 16 - 1; ++c)
+              if (c < n16) {
+                uint32_t v[16];
+                tmem_ld16(from + c * 16, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                  sums[c * 8 + q] = fma2(pack2(v[2 * q], v[2 * q + 1]), s2, sums[c * 8 + q]);
+              }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(tempty0 + acc_slot<BN>(acc) * 8);
+          }
+          ++acc;
         }
-        const uint64_t s2 = pack2(__float_as_uint(s), __float_as_uint(s));
-        if (!mbar_wait(&ring.tfull[acc & 1u], (acc >> 1) & 1u, p.timeout_ns, ring.abort, p.status)) {
+        if (!ok) {
           set_status(p.status, kStatusPipelineTimeout, 0x300u | rank);
           *ring.abort = 1;
           return;
         }
-        tc_fence_after();
-        const uint32_t from = from0 + (acc & 1u) * 256u;
-        if (n8 == 8) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[16];
-            tmem_ld16(from + c * 16, v);
-            tmem_ld_wait();
-            if (c == 3) {  // the accumulator has been read
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_pair(tempty0 + (acc & 1u) * 8);
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              sums[c * 8 + q] = fma2(pack2(v[2 * q], v[2 * q + 1]), s2, sums[c * 8 + q]);
-          }
-        } else {  // the last columns
-#pragma unroll
-          for (int c = 0; c < 7; ++c) {
-            if (c < n8) {
-              uint32_t v[8];
-              tmem_ld8(from + c * 8, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                sums[c * 4 + q] = fma2(pack2(v[2 * q], v[2 * q + 1]), s2, sums[c * 4 + q]);
-            }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_pair(tempty0 + (acc & 1u) * 8);
-        }
-        ++acc;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ring.sempty[slot]);
       }
     }
     Unit u;
     sch.get(i, u);
-    const int64_t col = static_cast<int64_t>(u.n0) + c_first;
     const int32_t row = static_cast<int32_t>(rank) * 128 + quad * 32 + lane;
+    const int64_t col = static_cast<int64_t>(u.n0) + c_first;
     const int64_t at = (static_cast<int64_t>(u.row0) + row) * p.ldo + col;
     const int32_t left = p.wide - static_cast<int32_t>(col);  // columns of the output from here
-    const int n = left <= 0 ? 0 : left >= 64 ? 8 : left / 8;
+    const int n = left <= 0 ? 0 : left >= kCols ? kCols / 8 : left / 8;
     auto eight = [&](int c, float (&v)[8]) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) unpack2(sums[c * 4 + j], v[2 * j], v[2 * j + 1]);
     };
     if (sch.split == 1) {
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
+      for (int c = 0; c < kCols / 8; ++c)
         if (c < n && row < u.cnt) {
           float v[8];
           eight(c, v);
@@ -824,19 +882,20 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
         }
       continue;
     }
-    constexpr int64_t kSlab = 64 * 32, kNext = 2 * kXEpiWarps * kSlab;
+    constexpr int kWarps = kXEpiWarps;
+    constexpr int64_t kSlab = kCols * 32, kNext = 2 * kWarps * kSlab;
     float* first = p.partials +
-                   ((static_cast<int64_t>(u.tile) * sch.split * 2 + rank) * kXEpiWarps + ew) * kSlab + lane;
+                   ((static_cast<int64_t>(u.tile) * sch.split * 2 + rank) * kWarps + ew) * kSlab + lane;
     float* part = first + u.part * kNext;
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
+    for (int c = 0; c < kCols / 8; ++c)
       if (c < n) {
         float v[8];
         eight(c, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) __stcg(part + (c * 8 + j) * 32, v[j]);
       }
-    if (last_part(p, u, sch.split, rank, ew, lane))
+    if (last_part<kWarps>(p, u, sch.split, rank, ew, lane))
       for (int c = 0; c < n; ++c) {
         float v[8] = {};
         for (int s = 0; s < sch.split; ++s)
@@ -870,13 +929,14 @@ __device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
         if constexpr (OP == kOpFp8)
           ok = mbar_wait(&ring.sfull[acc % kScaleSlots], (acc / kScaleSlots) & 1u, p.timeout_ns,
                          ring.abort, p.status);
-        if (!ok || !mbar_wait(&ring.tfull[acc & 1u], (acc >> 1) & 1u, p.timeout_ns, ring.abort, p.status)) {
+        if (!ok || !mbar_wait(&ring.tfull[acc_slot<BN>(acc)], acc_phase<BN>(acc), p.timeout_ns, ring.abort,
+                              p.status)) {
           set_status(p.status, kStatusPipelineTimeout, 0x300u | rank);
           *ring.abort = 1;
           return;
         }
         tc_fence_after();
-        const uint32_t from = from0 + (acc & 1u) * 256u;
+        const uint32_t from = from0 + acc_slot<BN>(acc) * BN;
 #pragma unroll
         for (int c = 0; c < kCols / 8; ++c) {
           if (c < n8) {
@@ -886,7 +946,7 @@ __device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
             if (c == n8 - 1) {  // the accumulator has been read
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_pair(tempty0 + (acc & 1u) * 8);
+              if (lane == 0) mbar_arrive_pair(tempty0 + acc_slot<BN>(acc) * 8);
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -947,7 +1007,7 @@ __device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
 #pragma unroll
         for (int j = 0; j < 8; ++j) __stcg(part + (c * 8 + j) * 32, v[j]);
       }
-    if (last_part(p, u, sch.split, rank, ew, lane))
+    if (last_part<kXEpiWarps>(p, u, sch.split, rank, ew, lane))
       for (int c = 0; c < n8; ++c) {
         float v[8] = {};
         for (int s = 0; s < sch.split; ++s)
@@ -971,14 +1031,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   ring.r = smem + kStagesX * kSub * kWBytes;
   ring.scales = reinterpret_cast<float*>(ring.r + kStagesX * kSub * r_bytes(BN));
   ring.stage_out = reinterpret_cast<uint8_t*>(ring.scales) + scale_bytes(OP, BN);
-  int32_t* off = reinterpret_cast<int32_t*>(ring.stage_out + kXEpiWarps * kOutBytes);
+  int32_t* off = reinterpret_cast<int32_t*>(ring.stage_out + out_bytes(OP));
   int32_t* pre = off + kMaxExperts + 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(off) + kTableBytes);
   ring.full = bars;
   ring.empty = bars + kStagesX;
   ring.tfull = bars + 2 * kStagesX;
-  ring.tempty = ring.tfull + 2;
-  ring.tail = ring.tempty + 2;
+  ring.tempty = ring.tfull + accs_of(BN);
+  ring.tail = ring.tempty + accs_of(BN);
   ring.zfull = ring.tail + kStagesX;
   ring.sfull = ring.zfull + kStagesX;
   ring.sempty = ring.sfull + kScaleSlots;
@@ -996,7 +1056,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       mbar_init(&ring.tail[s], 1);
       mbar_init(&ring.zfull[s], 2);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < accs_of(BN); ++b) {
       mbar_init(&ring.tfull[b], 1);
       mbar_init(&ring.tempty[b], 2 * kXEpiWarps);
     }
@@ -1033,6 +1093,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       zero_role<BN>(p, sch, ring, rank, lane);
     } else if constexpr (OP == kOpFp8) {
       scale_role<BN>(p, sch, ring, rank, lane);
+    } else if constexpr (OP == kOpFp8Long) {
+      scale_long_role<BN>(p, sch, ring, rank, lane);
     }
   } else if (threadIdx.x == 0) {
     set_status(p.status, kStatusOffsets, 0);

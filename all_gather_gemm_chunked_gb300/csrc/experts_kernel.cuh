@@ -27,7 +27,7 @@ constexpr int kXEpiWarps = 16;
 // TMA warp, MMA warp, epilogue warps; the weight gradient's zeroing warp, or the
 // scale warp of e4m3.
 __host__ __device__ constexpr int threads_of(int op) {
-  return 32 * (2 + kXEpiWarps + (op == kOpWeight || op == kOpFp8 ? 1 : 0));
+  return 32 * (2 + kXEpiWarps + (op == kOpWeight || op == kOpFp8 || op == kOpFp8Long ? 1 : 0));
 }
 constexpr int kXGroup = 8;     // row tiles that share the weights they read (tile order)
 
