@@ -129,28 +129,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, timeout_ns, abort, gstatus));
 }
 
-// Two 32-bit sums in one instruction (the epilogue issues one per two columns).
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  uint32_t a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-  lo = __uint_as_float(a);
-  hi = __uint_as_float(b);
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // 32 TMEM lanes x 8 columns.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -798,9 +776,9 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
   const int quad = (threadIdx.x >> 5) & 3, c_first = (ew >> 2) * kCols;
   uint32_t acc = 0, batch = 0;
   for (int32_t i = 0;; ++i) {
-    uint64_t sums[kCols / 2];
+    float sums[kCols];
 #pragma unroll
-    for (int c = 0; c < kCols / 2; ++c) sums[c] = 0;
+    for (int c = 0; c < kCols; ++c) sums[c] = 0.0f;
     {
       Unit u;
       if (!sch.get(i, u)) break;
@@ -815,7 +793,6 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
         const int32_t n = left < kScaleBatch ? left : kScaleBatch;
         for (int32_t j = 0; ok && j < n; ++j) {
           const float s = scale0[(slot * kScaleBatch + j) * 256];
-          const uint64_t s2 = pack2(__float_as_uint(s), __float_as_uint(s));
           ok = mbar_wait(&ring.tfull[acc_slot<BN>(acc)], acc_phase<BN>(acc), p.timeout_ns, ring.abort,
                          p.status);
           tc_fence_after();
@@ -832,8 +809,8 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
                 if (lane == 0) mbar_arrive_pair(tempty0 + acc_slot<BN>(acc) * 8);
               }
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                sums[c * 8 + q] = fma2(pack2(v[2 * q], v[2 * q + 1]), s2, sums[c * 8 + q]);
+              for (int q = 0; q < 16; ++q)
+                sums[c * 16 + q] = fmaf(__uint_as_float(v[q]), s, sums[c * 16 + q]);
             }
           } else {  // the last columns
 #pragma unroll
@@ -843,8 +820,8 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
                 tmem_ld16(from + c * 16, v);
                 tmem_ld_wait();
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  sums[c * 8 + q] = fma2(pack2(v[2 * q], v[2 * q + 1]), s2, sums[c * 8 + q]);
+                for (int q = 0; q < 16; ++q)
+                  sums[c * 16 + q] = fmaf(__uint_as_float(v[q]), s, sums[c * 16 + q]);
               }
             tc_fence_before();
             __syncwarp();
@@ -870,7 +847,7 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
     const int n = left <= 0 ? 0 : left >= kCols ? kCols / 8 : left / 8;
     auto eight = [&](int c, float (&v)[8]) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) unpack2(sums[c * 4 + j], v[2 * j], v[2 * j + 1]);
+      for (int j = 0; j < 8; ++j) v[j] = sums[c * 8 + j];
     };
     if (sch.split == 1) {
 #pragma unroll
@@ -913,9 +890,9 @@ __device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
   const int quad = (threadIdx.x >> 5) & 3, quarter = ew >> 2;
   uint32_t acc = 0;
   for (int32_t i = 0;; ++i) {
-    uint64_t sums[kCols / 2];
+    float sums[kCols];
 #pragma unroll
-    for (int c = 0; c < kCols / 2; ++c) sums[c] = 0;
+    for (int c = 0; c < kCols; ++c) sums[c] = 0.0f;
     {
       Unit u;
       if (!sch.get(i, u)) break;
@@ -949,16 +926,17 @@ __device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
               if (lane == 0) mbar_arrive_pair(tempty0 + acc_slot<BN>(acc) * 8);
             }
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint64_t* s = sums + c * 4 + q * 2;
-              const uint64_t lo = pack2(v[q * 4], v[q * 4 + 1]), hi = pack2(v[q * 4 + 2], v[q * 4 + 3]);
+            for (int q = 0; q < 8; q += 4) {
+              float* s = sums + c * 8 + q;
               if constexpr (OP == kOpFp8) {
-                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scale + c * 8 + q * 4);
-                s[0] = fma2(lo, f.x, s[0]);
-                s[1] = fma2(hi, f.y, s[1]);
+                const float4 f = *reinterpret_cast<const float4*>(scale + c * 8 + q);
+                s[0] = fmaf(__uint_as_float(v[q]), f.x, s[0]);
+                s[1] = fmaf(__uint_as_float(v[q + 1]), f.y, s[1]);
+                s[2] = fmaf(__uint_as_float(v[q + 2]), f.z, s[2]);
+                s[3] = fmaf(__uint_as_float(v[q + 3]), f.w, s[3]);
               } else {
-                s[0] = add2(lo, s[0]);
-                s[1] = add2(hi, s[1]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[j] += __uint_as_float(v[q + j]);
               }
             }
           }
@@ -980,7 +958,7 @@ __device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
                   p.out_type, u.cnt, p.wide - col, ring.stage_out + ew * kOutBytes};
     auto eight = [&](int c, float (&v)[8]) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) unpack2(sums[c * 4 + j], v[2 * j], v[2 * j + 1]);
+      for (int j = 0; j < 8; ++j) v[j] = sums[c * 8 + j];
     };
     if (sch.split == 1) {
 #pragma unroll
