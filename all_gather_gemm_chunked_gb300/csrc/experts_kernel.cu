@@ -121,6 +121,14 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// A value that is the same in all lanes, so that the compiler knows it: what it
+// computes from such values stays in uniform registers, where the MMA and TMA
+// instructions take their operands.
+template <typename T>
+__device__ __forceinline__ T uniform(T v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
 // A wait of a whole warp: the vote keeps its control flow uniform, so that what the
 // warp computes around it (the MMA's descriptors) stays in uniform registers.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
@@ -621,14 +629,16 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
   };
   Unit u;
   for (int32_t i = 0; ok && sch.get(i, u); ++i) {
-    const uint32_t idesc = idesc_f16_f32(kXWide, u.w, kWMn, kRMn) |
+    const int32_t kb_end = uniform(u.kb1), kb_begin = uniform(u.kb0), width = uniform(u.w);
+    [[maybe_unused]] const int32_t red_rows = uniform(u.red_rows);
+    const uint32_t idesc = idesc_f16_f32(kXWide, width, kWMn, kRMn) |
                            (!is_fp8(OP) && p.bf16 ? kIdescAbBf16 : 0u);
     const uint32_t r_second = kRMn ? 64 * 128 / 16
                               : OP == kOpFp8Long ? r_bytes(BN) / 16
-                                                 : static_cast<uint32_t>(box_of<BN>(u.w / 2) * (BN / 8) * 128 / 16);
+                                                 : static_cast<uint32_t>(box_of<BN>(width / 2) * (BN / 8) * 128 / 16);
     int32_t left = 0;  // k-blocks left of the segment
-    for (int32_t kb0 = u.kb0; kb0 < u.kb1; kb0 += kSub) {
-      const int n_sub = u.kb1 - kb0 < kSub ? u.kb1 - kb0 : kSub;
+    for (int32_t kb0 = kb_begin; kb0 < kb_end; kb0 += kSub) {
+      const int n_sub = kb_end - kb0 < kSub ? kb_end - kb0 : kSub;
       bool first = false;
       if (!is_fp8(OP) && left <= 0) {
         if (!(ok = accumulator())) break;
@@ -636,9 +646,9 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
         first = true;
       }
       int last_steps = 4;  // of the stage's last k-block
-      if (OP == kOpWeight && u.red_rows - (kb0 + n_sub) * 64 < 0) {
+      if (OP == kOpWeight && red_rows - (kb0 + n_sub) * 64 < 0) {
         // a group's last k-block comes through both CTAs' zeroing warps
-        last_steps = (u.red_rows - (kb0 + n_sub - 1) * 64 + 15) / 16;
+        last_steps = (red_rows - (kb0 + n_sub - 1) * 64 + 15) / 16;
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(&ring.zfull[stage], (zeroed >> stage) & 1u,
                                                        p.timeout_ns, ring.abort, p.status));
         zeroed ^= 1u << stage;
@@ -676,7 +686,7 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
       if (++stage == kStagesX) stage = 0;
       if (!is_fp8(OP)) {
         left -= n_sub;
-        if (left <= 0 || kb0 + kSub >= u.kb1) {
+        if (left <= 0 || kb0 + kSub >= kb_end) {
           left = 0;
           if (lane == 0) mma_commit_pair_both(&ring.tfull[acc_slot<BN>(acc)]);
           ++acc;
@@ -1025,7 +1035,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   ring.abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* flag = reinterpret_cast<int32_t*>(tmem_slot + 2);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStagesX; ++s) {
@@ -1055,7 +1065,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   if (valid) {
     Schedule<OP, BN> sch(p, off, pre);
     if (warp == 0) {

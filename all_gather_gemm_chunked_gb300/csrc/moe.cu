@@ -82,6 +82,32 @@ int launched(cudaError_t e, const char* what) {
 }  // namespace
 
 // ------------------------------------------------------------------ plan
+// The operands of a product as the last run of its kind described them; a run on the
+// same matrices (a pointer, its pitch, the rows) takes the descriptors from here.
+struct OperandCache {
+  bool valid = false;
+  const void* w = nullptr;
+  const void* r = nullptr;
+  int64_t ldw = 0, ldw_e = 0, ldr = 0, rows = 0;
+  agg::ExpertsParams x{};
+  // The parameters if they are these operands', otherwise null after taking them down
+  // (valid again once the caller has encoded them).
+  agg::ExpertsParams* find(const void* w_, int64_t ldw_, int64_t ldw_e_, const void* r_, int64_t ldr_,
+                           int64_t rows_) {
+    if (valid && w == w_ && ldw == ldw_ && ldw_e == ldw_e_ && r == r_ && ldr == ldr_ && rows == rows_)
+      return &x;
+    valid = false;
+    w = w_;
+    ldw = ldw_;
+    ldw_e = ldw_e_;
+    r = r_;
+    ldr = ldr_;
+    rows = rows_;
+    std::memset(&x, 0, sizeof(x));
+    return nullptr;
+  }
+};
+
 struct ag_moe_plan {
   int E = 0;
   int64_t K = 0, N = 0;
@@ -96,6 +122,7 @@ struct ag_moe_plan {
   cudaEvent_t done = nullptr;
   cudaStream_t last_stream = nullptr;
   bool has_run = false;
+  OperandCache cache[4];  // by ExpertsOp
 };
 
 namespace {
@@ -267,20 +294,23 @@ int run_rows(ag_moe_plan* p, int op, int64_t rows, const void* in, int64_t ld_in
                 (long long)ldw_e);
   if (p->E == 1) ldw_e = p->K * ldw;
   DeviceGuard dg(p->device);
-  agg::ExpertsParams x;
-  std::memset(&x, 0, sizeof(x));
   const bool few = few_rows(p, rows);
-  int rc;
-  if (fwd)
-    rc = encode_mn_major(&x.tm_w, w, p->N, p->K, ldw, p->E, ldw_e);
-  else
-    rc = encode_k_major(&x.tm_w, p->dtype, w, p->N, p->K, ldw, p->E, ldw_e, 128);
-  if (rc || (rc = encode_rows(x, p->dtype, in, red, rows, ld_in, few))) return rc;
+  OperandCache& c = p->cache[op];
+  if (!c.find(w, ldw, ldw_e, in, ld_in, rows)) {
+    int rc;
+    if (fwd)
+      rc = encode_mn_major(&c.x.tm_w, w, p->N, p->K, ldw, p->E, ldw_e);
+    else
+      rc = encode_k_major(&c.x.tm_w, p->dtype, w, p->N, p->K, ldw, p->E, ldw_e, 128);
+    if (rc || (rc = encode_rows(c.x, p->dtype, in, red, rows, ld_in, few))) return rc;
+    c.x.w_blk = whole_blocks(p->dtype, p->N);
+    c.valid = true;
+  }
+  agg::ExpertsParams& x = c.x;
   x.offsets = offsets;
   x.rows = static_cast<int32_t>(rows);
   x.wide = static_cast<int32_t>(wide);
   x.red = static_cast<int32_t>(red);
-  x.w_blk = whole_blocks(p->dtype, p->N);
   x.out_type = out_dtype;
   x.out = out;
   x.ldo = ld_out;
@@ -547,18 +577,21 @@ int ag_moe_backward_weight(ag_moe_plan* plan, int64_t rows, const void* x, int64
   }
   if (int rc = check_matrix("x", x, ldx, plan->K, plan->dtype)) return rc;
   if (int rc = check_matrix("dy", dy, lddy, plan->N, plan->dtype)) return rc;
-  agg::ExpertsParams p;
-  std::memset(&p, 0, sizeof(p));
-  int rc;
-  if ((rc = encode_mn_major(&p.tm_w, dy, plan->N, rows, lddy, 1, rows * lddy)) ||
-      (rc = encode_mn_major(&p.tm_r[0], x, plan->K, rows, ldx, 1, rows * ldx)))
-    return rc;
+  OperandCache& c = plan->cache[agg::kOpWeight];
+  if (!c.find(dy, lddy, 0, x, ldx, rows)) {
+    int rc;
+    if ((rc = encode_mn_major(&c.x.tm_w, dy, plan->N, rows, lddy, 1, rows * lddy)) ||
+        (rc = encode_mn_major(&c.x.tm_r[0], x, plan->K, rows, ldx, 1, rows * ldx)))
+      return rc;
+    c.x.w_blk = whole_blocks(plan->dtype, plan->N);
+    c.x.r_blk = whole_blocks(plan->dtype, plan->K);
+    c.valid = true;
+  }
+  agg::ExpertsParams& p = c.x;
   p.offsets = offsets;
   p.rows = static_cast<int32_t>(rows);
   p.wide = static_cast<int32_t>(plan->N);
   p.out_rows = static_cast<int32_t>(plan->K);
-  p.w_blk = whole_blocks(plan->dtype, plan->N);
-  p.r_blk = whole_blocks(plan->dtype, plan->K);
   p.out_type = out_dtype;
   p.out = dw;
   p.ldo = plan->N;
@@ -575,13 +608,18 @@ int ag_fp8_forward(ag_moe_plan* plan, int64_t rows, const void* xq, const float*
   if (int rc = check_matrix("y", y, ldy, plan->N, out_dtype)) return rc;
   if (!xs || !ws) return fail(AG_GEMM_ERR_INVALID, "scales are NULL");
   DeviceGuard dg(plan->device);
-  agg::ExpertsParams p;
-  std::memset(&p, 0, sizeof(p));
   const bool few = few_rows(plan, rows);
-  int rc;
-  if ((rc = encode_k_major(&p.tm_w, AG_MOE_E4M3, wq, plan->K, plan->N, plan->K, plan->E, plan->K * plan->N, 128)) ||
-      (rc = encode_rows(p, AG_MOE_E4M3, xq, plan->K, rows, plan->K, few)))
-    return rc;
+  OperandCache& c = plan->cache[agg::kOpFp8];
+  if (!c.find(wq, plan->K, plan->K * plan->N, xq, plan->K, rows)) {
+    int rc;
+    if ((rc = encode_k_major(&c.x.tm_w, AG_MOE_E4M3, wq, plan->K, plan->N, plan->K, plan->E,
+                             plan->K * plan->N, 128)) ||
+        (rc = encode_rows(c.x, AG_MOE_E4M3, xq, plan->K, rows, plan->K, few)))
+      return rc;
+    c.x.w_blk = whole_blocks(AG_MOE_E4M3, plan->K);
+    c.valid = true;
+  }
+  agg::ExpertsParams& p = c.x;
   p.offsets = offsets;
   p.rows = static_cast<int32_t>(rows);
   p.wide = static_cast<int32_t>(plan->N);
@@ -589,7 +627,6 @@ int ag_fp8_forward(ag_moe_plan* plan, int64_t rows, const void* xq, const float*
   p.out_type = out_dtype;
   p.out = y;
   p.ldo = ldy;
-  p.w_blk = whole_blocks(AG_MOE_E4M3, plan->K);
   p.xs = xs;
   p.ws = ws;
   return run(plan, p, agg::kOpFp8, few, rows / (few ? agg::kXFewRows : agg::kXRows) + plan->E, stream);
