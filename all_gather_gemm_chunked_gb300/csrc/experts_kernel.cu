@@ -129,6 +129,19 @@ __device__ __forceinline__ T uniform(T v) {
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
+// True in one lane of a converged warp, the same one every time.  (Not lane == 0: of a
+// branch on this the compiler knows that one thread runs it, and issues MMAs and loads
+// from uniform registers; on a lane number it moved every operand there first.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // A wait of a whole warp: the vote keeps its control flow uniform, so that what the
 // warp computes around it (the MMA's descriptors) stays in uniform registers.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
@@ -418,7 +431,7 @@ __device__ void tma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
       ok = mbar_wait(&ring.empty[stage], phase ^ 1u, p.timeout_ns, ring.abort, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (lane == 0) {
+      if (elect_one()) {
         const bool tail = OP == kOpWeight && u.red_rows - (kb0 + n_sub) * 64 < 0;
         uint32_t bar = full0 + stage * 8;
         if (tail) {
@@ -455,7 +468,7 @@ __device__ void tma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
       }
     }
   }
-  if (!ok && lane == 0) {
+  if (!ok && elect_one()) {  // (the lane that counted its loads)
     set_status(p.status, kStatusPipelineTimeout, 0x100u | rank);
     *ring.abort = 1;
     if (rank == 0) {
@@ -666,7 +679,7 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
         if (s >= n_sub) break;
         if (is_fp8(OP) && !(ok = accumulator())) break;
         const uint32_t d = tmem + acc_slot<BN>(acc) * BN;
-        if (lane == 0) {
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (OP == kOpWeight && s == n_sub - 1 && k >= last_steps) break;
@@ -682,13 +695,13 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
         if (is_fp8(OP)) ++acc;
       }
       if (!ok) break;
-      if (lane == 0) mma_commit_pair_both(&ring.empty[stage]);
+      if (elect_one()) mma_commit_pair_both(&ring.empty[stage]);
       if (++stage == kStagesX) stage = 0;
       if (!is_fp8(OP)) {
         left -= n_sub;
         if (left <= 0 || kb0 + kSub >= kb_end) {
           left = 0;
-          if (lane == 0) mma_commit_pair_both(&ring.tfull[acc_slot<BN>(acc)]);
+          if (elect_one()) mma_commit_pair_both(&ring.tfull[acc_slot<BN>(acc)]);
           ++acc;
         }
       }
@@ -1089,7 +1102,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (rank == 0 && warp == 1 && lane == 0) {
+  if (rank == 0 && warp == 1 && elect_one()) {  // the thread that issued the MMAs
     mma_commit_pair_local(drain);
     volatile int never = 0;
     mbar_wait(drain, 0, p.timeout_ns, &never);
