@@ -239,19 +239,17 @@ struct Schedule {
     }
   }
 
-  // Parts that make the longest pair's share shortest: a round of the pairs costs
-  // its k-blocks and about three more for a tile's start and end.
+  // Parts that make the longest pair's share shortest: a round of the pairs costs its
+  // k-blocks and about six more for a tile's start and end.  Each lane tries one number.
   __device__ __forceinline__ int32_t choose_split(int32_t tiles) const {
     if (tiles == 0 || tiles >= 2 * pairs || p.max_units == 0) return 1;
-    int32_t best = 1, cost = 0x7fffffff;
-    for (int32_t s = 1; s <= 16 && (s == 1 || (KB >= 4 * s && tiles * s <= p.max_units)); ++s) {
-      const int32_t c = ((tiles * s + pairs - 1) / pairs) * ((KB + s - 1) / s + 3);
-      if (c < cost) {
-        cost = c;
-        best = s;
-      }
-    }
-    return best;
+    const int32_t s = static_cast<int32_t>(threadIdx.x & 31) + 1;
+    const bool can = s == 1 || (s <= 16 && KB >= 4 * s && tiles * s <= p.max_units);
+    const int32_t rounds = (tiles * s + pairs - 1) / pairs;
+    const uint32_t cost = can ? static_cast<uint32_t>(rounds * ((KB + s - 1) / s + 6)) : 0x03ffffffu;
+    // (the smallest number among the cheapest)
+    const uint32_t best = __reduce_min_sync(0xffffffffu, min(cost, 0x03ffffffu) * 32 + (s - 1));
+    return static_cast<int32_t>(best & 31u) + 1;
   }
 
   // Tile `r` of an expert with n row tiles: groups of 8 row tiles, in a group all wide
@@ -634,9 +632,9 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
   int stage = 0;
   uint32_t acc = 0, full_phase = 0, zeroed = 0;  // bit s: parity of stage s's barriers
   bool ok = true;
-  auto accumulator = [&] {  // wait until it has been read
-    const bool r = warp_wait(&ring.tempty[acc_slot<BN>(acc)], acc_phase<BN>(acc) ^ 1u, p.timeout_ns,
-                             ring.abort, p.status);
+  auto accumulator = [&](uint32_t n = 0) {  // wait until the n-th from here has been read
+    const bool r = warp_wait(&ring.tempty[acc_slot<BN>(acc + n)], acc_phase<BN>(acc + n) ^ 1u,
+                             p.timeout_ns, ring.abort, p.status);
     tc_fence_after();
     return r;
   };
@@ -677,7 +675,10 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
 #pragma unroll
       for (int s = 0; s < kSub; ++s) {
         if (s >= n_sub) break;
-        if (is_fp8(OP) && !(ok = accumulator())) break;
+        // (the epilogue reads them in order: with many, one wait serves the stage's)
+        if (is_fp8(OP) && (accs_of(BN) < 4 || s == 0) &&
+            !(ok = accumulator(accs_of(BN) < 4 ? 0 : n_sub - 1)))
+          break;
         const uint32_t d = tmem + acc_slot<BN>(acc) * BN;
         if (elect_one()) {
 #pragma unroll
@@ -784,6 +785,25 @@ __device__ __forceinline__ void store_row8(void* base, int type, int64_t at, con
     *reinterpret_cast<uint4*>(static_cast<__half*>(base) + at) = Elem<__half>::pack(v);
   } else {
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at) = Elem<__nv_bfloat16>::pack(v);
+  }
+}
+
+// The sum of a split tile's parts for 8 columns, in the order of the parts, the loads of
+// four parts in flight.
+__device__ __forceinline__ void add_parts(const float* first, int64_t next, int32_t parts, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  for (int32_t s0 = 0; s0 < parts; s0 += 4) {
+    float x[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[u][j] = s0 + u < parts ? __ldcg(first + (s0 + u) * next + j * 32) : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (s0 + u < parts)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += x[u][j];
   }
 }
 
@@ -897,10 +917,8 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
       }
     if (last_part<kWarps>(p, u, sch.split, rank, ew, lane))
       for (int c = 0; c < n; ++c) {
-        float v[8] = {};
-        for (int s = 0; s < sch.split; ++s)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] += __ldcg(first + s * kNext + (c * 8 + j) * 32);
+        float v[8];
+        add_parts(first + c * 8 * 32, kNext, sch.split, v);
         if (row < u.cnt) store_row8(p.out, p.out_type, at + c * 8, v);
       }
   }
@@ -1010,10 +1028,8 @@ __device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
       }
     if (last_part<kXEpiWarps>(p, u, sch.split, rank, ew, lane))
       for (int c = 0; c < n8; ++c) {
-        float v[8] = {};
-        for (int s = 0; s < sch.split; ++s)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] += __ldcg(first + s * kNext + (c * 8 + j) * 32);
+        float v[8];
+        add_parts(first + c * 8 * 32, kNext, sch.split, v);
         out.store(c_first + c * 8, v, lane);
       }
   }
@@ -1074,6 +1090,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
+  if (warp == 2 && lane <= kXRowBoxes)  // the descriptors' first use would wait for them
+    tma_prefetch_desc(lane == kXRowBoxes ? &p.tm_w : &p.tm_r[OP == kOpWeight ? 0 : lane]);
   const bool valid = load_table<BN>(p, off, pre, flag);
   tc_fence_before();
   cluster_sync();
