@@ -1066,6 +1066,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
+  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStagesX; ++s) {
       mbar_init(&ring.full[s], 1);
@@ -1092,6 +1093,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   }
   if (warp == 2 && lane <= kXRowBoxes)  // the descriptors' first use would wait for them
     tma_prefetch_desc(lane == kXRowBoxes ? &p.tm_w : &p.tm_r[OP == kOpWeight ? 0 : lane]);
+  pdl_wait();  // from here on global memory is read
   const bool valid = load_table<BN>(p, off, pre, flag);
   tc_fence_before();
   cluster_sync();
@@ -1183,13 +1185,8 @@ cudaError_t experts_prepare(int* pairs) {
 cudaError_t launch_experts(const ExpertsParams& p, int op, bool few, int grid,
                            cudaStream_t stream) {
   const Variant v = variant(op, few);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(v.threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(v.smem);
-  cfg.stream = stream;
   void* args[] = {const_cast<ExpertsParams*>(&p)};
-  return cudaLaunchKernelExC(&cfg, v.fn, args);
+  return launch_args(v.fn, dim3(static_cast<unsigned>(grid)), v.threads, static_cast<size_t>(v.smem), stream, args);
 }
 
 }  // namespace agg

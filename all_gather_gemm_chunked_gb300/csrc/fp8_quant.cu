@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int64_
                                                             const int32_t* __restrict__ order,
                                                             int k, uint8_t* __restrict__ q,
                                                             float* __restrict__ scales) {
+  pdl_enter();
   constexpr int V = Elem<T>::kVec;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + warp;
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(int64_t K, int64_
                                                                const T* __restrict__ w,
                                                                uint8_t* __restrict__ q,
                                                                float* __restrict__ scales) {
+  pdl_enter();
   __shared__ uint8_t tile[kScaleBlock][kTilePitch];
   __shared__ float red[8];
   const int64_t KB = (K + kScaleBlock - 1) / kScaleBlock, NB = (N + kScaleBlock - 1) / kScaleBlock;

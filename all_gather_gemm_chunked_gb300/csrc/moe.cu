@@ -234,6 +234,11 @@ bool few_rows(const ag_moe_plan* p, int64_t rows) {
   return rows <= static_cast<int64_t>(agg::kXFewRows) * p->E;
 }
 
+// Row tiles that the groups of so many rows can make.
+int64_t most_row_tiles(const ag_moe_plan* p, int64_t rows, bool few) {
+  return rows / (few ? agg::kXFewRows : agg::kXRows) + (rows < p->E ? rows : p->E);
+}
+
 int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_tiles,
         void* stream_v) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
@@ -257,7 +262,11 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   if (!captured && p->has_run && p->last_stream != stream &&
       (e = cudaStreamWaitEvent(stream, p->done, 0)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamWaitEvent");
-  if ((e = agg::launch_experts(x, op, few, 2 * p->pairs, stream)) != cudaSuccess)
+  // no more pairs than there can be units: split sums have up to 16 parts of 4 k-blocks
+  const int64_t kb = op == agg::kOpWeight ? 0 : x.red / (op == agg::kOpFp8 ? 128 : 64);
+  const int64_t units = row_tiles * wide_tiles * (kb < 8 ? 1 : kb < 64 ? (kb + 1) / 4 : 16);
+  const int pairs = static_cast<int>(units < p->pairs ? units : p->pairs);
+  if ((e = agg::launch_experts(x, op, few, 2 * pairs, stream)) != cudaSuccess)
     return cuda_fail(e, "experts kernel launch");
   if (!captured) {
     if ((e = cudaEventRecord(p->done, stream)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
@@ -314,7 +323,7 @@ int run_rows(ag_moe_plan* p, int op, int64_t rows, const void* in, int64_t ld_in
   x.out_type = out_dtype;
   x.out = out;
   x.ldo = ld_out;
-  return run(p, x, op, few, rows / (few ? agg::kXFewRows : agg::kXRows) + p->E, stream);
+  return run(p, x, op, few, most_row_tiles(p, rows, few), stream);
 }
 
 }  // namespace
@@ -629,7 +638,7 @@ int ag_fp8_forward(ag_moe_plan* plan, int64_t rows, const void* xq, const float*
   p.ldo = ldy;
   p.xs = xs;
   p.ws = ws;
-  return run(plan, p, agg::kOpFp8, few, rows / (few ? agg::kXFewRows : agg::kXRows) + plan->E, stream);
+  return run(plan, p, agg::kOpFp8, few, most_row_tiles(plan, rows, few), stream);
 }
 
 }  // extern "C"

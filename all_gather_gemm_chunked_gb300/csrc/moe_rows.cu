@@ -227,6 +227,7 @@ size_t place_smem(int E) { return ((static_cast<size_t>(kRouteWarps) * E * 2 + 1
 // Up to kOneBlockTokens tokens: choices and layout by one block, one launch.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kRouteThreads) route_one_kernel(const RouteArgs a) {
+  pdl_enter();
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Share own = share_of(0, a.T, warp, kRouteWarps);
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_one_kernel(const RouteArg
 // next places them.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
+  pdl_enter();
   __shared__ uint32_t cnt[kMaxExperts];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < a.E; e += kRouteThreads) cnt[e] = 0;
@@ -255,6 +257,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
 }
 
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteArgs a) {
+  pdl_enter();
   extern __shared__ __align__(16) uint8_t smem[];
   const Share blk = share_of(0, a.T, blockIdx.x, gridDim.x);
   place(a, blk.t0, blk.t1, smem);
@@ -267,6 +270,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) route_backward_kernel(const RouteArgs a,
                                                              const float* __restrict__ dweights,
                                                              T* __restrict__ dlogits) {
+  pdl_enter();
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x / 32);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
@@ -318,6 +322,7 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(int64_t T_, int k, 
                                                              const T* __restrict__ x, int64_t ldx,
                                                              const int32_t* __restrict__ order,
                                                              T* __restrict__ out) {
+  pdl_enter();
   const int64_t s = blockIdx.x;
   const int64_t c = (static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x) * V;
   if (c >= H) return;
@@ -336,6 +341,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(int64_t T_, int k,
                                                               const int32_t* __restrict__ slots,
                                                               const float* __restrict__ weights,
                                                               T* __restrict__ out) {
+  pdl_enter();
   const int64_t t = blockIdx.x, S = T_ * k;
   const int64_t c = (static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x) * V;
   if (c >= H) return;
@@ -368,6 +374,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(
     const T* __restrict__ y, int64_t ldy, const int32_t* __restrict__ slots,
     const float* __restrict__ weights, const int32_t* __restrict__ offsets_end,
     T* __restrict__ dy, float* __restrict__ dweights) {
+  pdl_enter();
   __shared__ float part[kRowThreads / 32][4];
   const int64_t t = blockIdx.x, S = T_ * k;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -487,17 +494,16 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
                                              static_cast<int>(smem));
         if (e != cudaSuccess) return e;
       }
-      return cudaLaunchKernel(fn, dim3(1), dim3(kRouteThreads), args, smem, stream);
+      return launch_args(fn, dim3(1), kRouteThreads, smem, stream, args);
     }
-    cudaError_t e = cudaLaunchKernel(route_choose_fn<T>(vpl), dim3(blocks), dim3(kRouteThreads),
-                                     args, 0, stream);
+    cudaError_t e = launch_args(route_choose_fn<T>(vpl), dim3(blocks), kRouteThreads, 0, stream, args);
     if (e != cudaSuccess) return e;
     if (smem > 48 * 1024 &&
         (e = cudaFuncSetAttribute(route_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   static_cast<int>(smem))) != cudaSuccess)
       return e;
-    return cudaLaunchKernel(reinterpret_cast<const void*>(&route_place_kernel), dim3(blocks),
-                            dim3(kRouteThreads), args, smem, stream);
+    return launch_args(reinterpret_cast<const void*>(&route_place_kernel), dim3(blocks), kRouteThreads,
+                       smem, stream, args);
   });
 }
 

@@ -13,15 +13,39 @@ constexpr int kMaxTopK = 32;
 constexpr int kScaleBlock = 128;
 enum ElemType : int { kTypeF16 = 0, kTypeBf16 = 2, kTypeF32 = 3, kTypeE4m3 = 4 };
 
-// A launch whose own error is returned (cudaGetLastError would also return an
-// earlier one's).
-template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+// Programmatic dependent launch: a kernel of this library may start while the kernel
+// before it in the stream is still running (launch latency and set-up overlap it) and
+// waits for that one's end, and its writes, before it touches global memory.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// First in every kernel that touches global memory at once.
+__device__ __forceinline__ void pdl_enter() {
+  pdl_trigger();
+  pdl_wait();
+}
+
+// A launch with that attribute.  Its own error is returned (cudaGetLastError would also
+// return an earlier one's).
+inline cudaError_t launch_args(const void* kernel, dim3 grid, int threads, size_t smem,
+                               cudaStream_t stream, void** args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+  return [&](P... p) {
+    void* list[] = {static_cast<void*>(&p)...};
+    return launch_args(reinterpret_cast<const void*>(kernel), grid, threads, 0, stream, list);
+  }(static_cast<P>(args)...);
 }
 
 struct RouteArgs {
