@@ -28,6 +28,32 @@ __device__ __forceinline__ float key_logit(uint32_t key) {
   return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
+// Keys of 16-bit logits: the value's bits in the same order above, 0xffff - expert below,
+// so that one reduction finds the largest logit's lowest expert.  -0 counts as +0.
+template <typename T>
+__host__ __device__ constexpr uint32_t packed_neg_inf() {
+  return (sizeof(T) == 2 && Elem<T>::kNegInf != 0 ? (0xffffu ^ Elem<T>::kNegInf) << 16 : 0u) | 0xffffu;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack_key(T v, int expert) {
+  uint32_t b = 0;
+  if constexpr (sizeof(T) == 2) b = *reinterpret_cast<const uint16_t*>(&v);
+  if (b == 0x8000u) b = 0;
+  return ((b ^ ((b >> 15) ? 0xffffu : 0x8000u)) << 16) | (0xffffu - static_cast<uint32_t>(expert));
+}
+template <typename T>
+__device__ __forceinline__ float packed_logit(uint32_t key) {
+  const uint32_t k = key >> 16;
+  const uint16_t b = static_cast<uint16_t>(k ^ ((k >> 15) ? 0x8000u : 0xffffu));
+  if constexpr (sizeof(T) == 2)
+    return Elem<T>::get(*reinterpret_cast<const T*>(&b));
+  else
+    return 0.0f;
+}
+__device__ __forceinline__ int packed_expert(uint32_t key) {
+  return static_cast<int>(0xffffu - (key & 0xffffu));
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
@@ -39,66 +65,115 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// One token by one warp: lane holds experts lane, lane + 32, ...; each of the k
-// rounds takes the largest key left (one warp reduction) and the lowest expert
-// that has it (a second one).  Returns, for lane j < k, the j-th choice's expert
-// (-1: none) and writes its weight.
+// Two tokens by one warp (side by side: a token's rounds are a chain of warp
+// reductions, and two chains take little longer than one): lane holds experts lane,
+// lane + 32, ...; each of the k rounds takes the largest key left (one reduction) and
+// the lowest expert that has it (a second one).  Writes the choices and their weights;
+// `chosen` gets, in lane j < k, the j-th choice's expert (-1: none).  A token from
+// `end` on is left out.
+__host__ __device__ constexpr int tokens_of(int VPL) { return VPL <= 8 ? 2 : 1; }
 template <typename T, int VPL>
-__device__ __forceinline__ int choose(const RouteArgs& a, int64_t t, int lane) {
-  const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-  uint32_t key[VPL];
-  bool nan = false;
+__device__ __forceinline__ void choose(const RouteArgs& a, int64_t t0, int64_t end, int lane,
+                                       int (&chosen)[tokens_of(VPL)]) {
+  constexpr int kTokens = tokens_of(VPL);
+  // 16-bit logits: value and expert in one key (16 bits of either), so that a round is
+  // one reduction: the largest key is the largest logit's lowest expert.
+  constexpr bool kPacked = sizeof(T) == 2;
+  uint32_t key[kTokens][VPL];
+  bool nan[kTokens];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * 32 + lane;
-    float v = -CUDART_INF_F;
-    if (e < a.E) v = Elem<T>::get(row[e]);
-    nan |= v != v;
-    key[i] = (e < a.E && v == v) ? logit_key(v) : 0u;
+  for (int n = 0; n < kTokens; ++n) {
+    const T* row = static_cast<const T*>(a.logits) + (t0 + n) * a.ld;
+    T v[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = i * 32 + lane;
+      v[i] = e < a.E && t0 + n < end ? row[e] : Elem<T>::put(-CUDART_INF_F);
+    }
+    nan[n] = false;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const float f = Elem<T>::get(v[i]);
+      const bool is_nan = f != f;
+      nan[n] |= is_nan;
+      key[n][i] = kPacked ? pack_key<T>(v[i], i * 32 + lane) : logit_key(f);
+      if (i * 32 + lane >= a.E || is_nan) key[n][i] = 0u;
+    }
   }
-  nan = __any_sync(kAll, nan);
-  float all = 0.0f;  // sum of exp(logit - largest) over all experts
-  uint32_t mine = 0;
-  int expert = -1;
+  float all[kTokens] = {};  // sum of exp(logit - largest) over all experts
+  uint32_t mine[kTokens] = {};
+#pragma unroll
+  for (int n = 0; n < kTokens; ++n) {
+    nan[n] = __any_sync(kAll, nan[n]);
+    chosen[n] = -1;
+  }
   for (int j = 0; j < a.k; ++j) {
-    uint32_t best = key[0];
-    int bi = lane;
+    uint32_t best[kTokens], top[kTokens];
+    int bi[kTokens];
+    bool any = false;
 #pragma unroll
-    for (int i = 1; i < VPL; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        bi = i * 32 + lane;
+    for (int n = 0; n < kTokens; ++n) {
+      best[n] = key[n][0];
+      bi[n] = lane;
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) {
+        if (kPacked) {
+          best[n] = max(best[n], key[n][i]);
+        } else if (key[n][i] > best[n]) {
+          best[n] = key[n][i];
+          bi[n] = i * 32 + lane;
+        }
       }
-    const uint32_t top = __reduce_max_sync(kAll, best);
-    if (top <= kKeyNegInf) break;
+      top[n] = __reduce_max_sync(kAll, best[n]);
+      any |= top[n] > (kPacked ? packed_neg_inf<T>() : kKeyNegInf);
+    }
+    if (!any) break;
     if (j == 0 && !a.normalize) {
-      const float m = key_logit(top);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (key[i] != 0u) all += expf(key_logit(key[i]) - m);
-      all = warp_sum(all);
+      for (int n = 0; n < kTokens; ++n) {
+        const float m = kPacked ? packed_logit<T>(top[n]) : key_logit(top[n]);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (key[n][i] != 0u)
+            all[n] += expf((kPacked ? packed_logit<T>(key[n][i]) : key_logit(key[n][i])) - m);
+        all[n] = warp_sum(all[n]);
+      }
     }
-    const int e = static_cast<int>(__reduce_min_sync(
-        kAll, best == top ? static_cast<uint32_t>(bi) : 0xffffffffu));
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (i * 32 + lane == e) key[i] = 0u;
-    if (lane == j) {
-      mine = top;
-      expert = e;
+    for (int n = 0; n < kTokens; ++n) {
+      const bool real = top[n] > (kPacked ? packed_neg_inf<T>() : kKeyNegInf);
+      int e;
+      if (kPacked) {
+        e = real ? packed_expert(top[n]) : -1;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (key[n][i] == top[n]) key[n][i] = 0u;
+      } else {
+        e = static_cast<int>(__reduce_min_sync(
+            kAll, real && best[n] == top[n] ? static_cast<uint32_t>(bi[n]) : 0xffffffffu));
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (i * 32 + lane == e) key[n][i] = 0u;
+      }
+      if (lane == j && real) {
+        mine[n] = top[n];
+        chosen[n] = e;
+      }
     }
   }
-  const float l = key_logit(mine);
-  const float m = __shfl_sync(kAll, l, 0);
-  const float p = expert >= 0 ? expf(l - m) : 0.0f;
-  const float sum = a.normalize ? warp_sum(p) : all;
-  float w = expert >= 0 ? p / sum : 0.0f;
-  if (nan && expert >= 0) w = CUDART_NAN_F;
-  if (lane < a.k) {
-    a.weights[t * a.k + lane] = w;
-    a.experts[t * a.k + lane] = expert;
+#pragma unroll
+  for (int n = 0; n < kTokens; ++n) {
+    const float l = kPacked ? packed_logit<T>(mine[n]) : key_logit(mine[n]);
+    const float m = __shfl_sync(kAll, l, 0);
+    const float p = chosen[n] >= 0 ? expf(l - m) : 0.0f;
+    const float sum = a.normalize ? warp_sum(p) : all[n];
+    float w = chosen[n] >= 0 ? p / sum : 0.0f;
+    if (nan[n] && chosen[n] >= 0) w = CUDART_NAN_F;
+    if (lane < a.k && t0 + n < end) {
+      a.weights[(t0 + n) * a.k + lane] = w;
+      a.experts[(t0 + n) * a.k + lane] = chosen[n];
+    }
   }
-  return expert;
 }
 
 // The tokens of block b and of its warps: contiguous, in order.
@@ -154,10 +229,17 @@ __device__ void place(const RouteArgs& a, int64_t T0, int64_t T1, uint8_t* smem)
   for (int e = threadIdx.x; e < a.E; e += kRouteThreads) base[e] = 0;
   __syncthreads();
   const Share own = share_of(T0, T1, warp, kRouteWarps);
-  for (int64_t t = own.t0; t < own.t1; ++t) {
-    const int e = lane < a.k ? a.experts[t * a.k + lane] : -1;
-    if (e >= 0) cnt[warp * a.E + e] += 1;
-    __syncwarp();
+  // (four tokens' choices in flight)
+  for (int64_t t0 = own.t0; t0 < own.t1; t0 += 4) {
+    int x[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      x[n] = lane < a.k && t0 + n < own.t1 ? a.experts[(t0 + n) * a.k + lane] : -1;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      if (x[n] >= 0) cnt[warp * a.E + x[n]] += 1;
+      __syncwarp();
+    }
   }
   __syncthreads();
   const int e = threadIdx.x;
@@ -172,7 +254,7 @@ __device__ void place(const RouteArgs& a, int64_t T0, int64_t T1, uint8_t* smem)
     const int g = e / a.E, x = e - g * a.E;
     uint32_t all = 0, early = 0;
     if (g < groups && x < a.E)
-#pragma unroll 8
+#pragma unroll 20
       for (int b = g; b < static_cast<int>(gridDim.x); b += groups) {
         const uint32_t c = static_cast<uint32_t>(a.counts[static_cast<int64_t>(b) * a.E + x]);
         all += c;
@@ -196,26 +278,37 @@ __device__ void place(const RouteArgs& a, int64_t T0, int64_t T1, uint8_t* smem)
     if (blockIdx.x == 0) a.offsets[e + 1] = static_cast<int32_t>(first + total);
     if (blockIdx.x == 0 && e == 0) a.offsets[0] = 0;
     uint32_t run = 0;  // counts to the counts of earlier warps
-    for (int w = 0; w < kRouteWarps; ++w) {
-      const uint32_t c = cnt[w * a.E + e];
-      cnt[w * a.E + e] = static_cast<uint16_t>(run);
-      run += c;
+#pragma unroll
+    for (int w0 = 0; w0 < kRouteWarps; w0 += 8) {
+      uint32_t c[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) c[w] = cnt[(w0 + w) * a.E + e];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        cnt[(w0 + w) * a.E + e] = static_cast<uint16_t>(run);
+        run += c[w];
+      }
     }
     if (e == a.E - 1) sums[32] = first + total;  // rows in use
   }
   __syncthreads();
-  for (int64_t t = own.t0; t < own.t1; ++t) {
-    const int x = lane < a.k ? a.experts[t * a.k + lane] : -1;
-    if (lane < a.k) {
+  for (int64_t t0 = own.t0; t0 < own.t1; t0 += 4) {
+    int x[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      x[n] = lane < a.k && t0 + n < own.t1 ? a.experts[(t0 + n) * a.k + lane] : -1;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int64_t t = t0 + n;
       int32_t place = -1;
-      if (x >= 0) {
-        place = static_cast<int32_t>(base[x] + cnt[warp * a.E + x]);
-        cnt[warp * a.E + x] += 1;
+      if (x[n] >= 0) {
+        place = static_cast<int32_t>(base[x[n]] + cnt[warp * a.E + x[n]]);
+        cnt[warp * a.E + x[n]] += 1;
         a.order[place] = static_cast<int32_t>(t * a.k + lane);
       }
-      a.slots[t * a.k + lane] = place;
+      if (lane < a.k && t < own.t1) a.slots[t * a.k + lane] = place;
+      __syncwarp();
     }
-    __syncwarp();
   }
   for (int64_t s = sums[32] + static_cast<int64_t>(blockIdx.x) * kRouteThreads + threadIdx.x;
        s < a.T * a.k; s += static_cast<int64_t>(gridDim.x) * kRouteThreads)
@@ -231,7 +324,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_one_kernel(const RouteArg
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Share own = share_of(0, a.T, warp, kRouteWarps);
-  for (int64_t t = own.t0; t < own.t1; ++t) choose<T, VPL>(a, t, lane);
+  constexpr int kTokens = tokens_of(VPL);
+  int chosen[kTokens];
+  for (int64_t t = own.t0; t < own.t1; t += kTokens) choose<T, VPL>(a, t, own.t1, lane, chosen);
   __syncthreads();
   place(a, 0, a.T, smem);
 }
@@ -240,16 +335,20 @@ __global__ void __launch_bounds__(kRouteThreads) route_one_kernel(const RouteArg
 // next places them.
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
-  pdl_enter();
+  pdl_wait();
   __shared__ uint32_t cnt[kMaxExperts];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < a.E; e += kRouteThreads) cnt[e] = 0;
   __syncthreads();
   const Share blk = share_of(0, a.T, blockIdx.x, gridDim.x);
   const Share own = share_of(blk.t0, blk.t1, warp, kRouteWarps);
-  for (int64_t t = own.t0; t < own.t1; ++t) {
-    const int e = choose<T, VPL>(a, t, lane);
-    if (e >= 0) atomicAdd(&cnt[e], 1u);  // (integer counts: any order)
+  constexpr int kTokens = tokens_of(VPL);
+  for (int64_t t = own.t0; t < own.t1; t += kTokens) {
+    int chosen[kTokens];
+    choose<T, VPL>(a, t, own.t1, lane, chosen);
+#pragma unroll
+    for (int n = 0; n < kTokens; ++n)
+      if (chosen[n] >= 0) atomicAdd(&cnt[chosen[n]], 1u);  // (integer counts: any order)
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += kRouteThreads)
@@ -257,21 +356,24 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
 }
 
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteArgs a) {
-  pdl_enter();
+  pdl_wait();
   extern __shared__ __align__(16) uint8_t smem[];
   const Share blk = share_of(0, a.T, blockIdx.x, gridDim.x);
   place(a, blk.t0, blk.t1, smem);
 }
 
-// Gradient of the logits, one warp per token.  normalize: w_j (dw_j - sum w dw) at
-// the chosen experts, 0 elsewhere.  Otherwise p_e ([e chosen] dw - sum w dw) with
-// the softmax p over all experts, which is computed again from the logits.
+// Gradient of the logits, one warp per token.  normalize: w_j (dw_j - sum w dw) at the
+// chosen experts, 0 elsewhere.  Otherwise p_e ([e chosen] dw - sum w dw) with the softmax
+// p over all experts, which is computed again from the logits.  The row is written as
+// for experts that were not chosen first, then, behind a warp barrier, the k choices.
 template <typename T>
 __global__ void __launch_bounds__(256) route_backward_kernel(const RouteArgs a,
                                                              const float* __restrict__ dweights,
-                                                             T* __restrict__ dlogits) {
+                                                             T* dlogits) {
   pdl_enter();
+  constexpr int V = Elem<T>::kVec;
   const int lane = threadIdx.x & 31;
+  const bool vec = a.E % V == 0 && (reinterpret_cast<uintptr_t>(dlogits) & 15u) == 0;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x / 32);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
        t < a.T; t += warps) {
@@ -280,36 +382,33 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteArgs a,
     if (lane < a.k) {
       w = a.weights[t * a.k + lane];
       expert = a.experts[t * a.k + lane];
-      dw = expert >= 0 ? dweights[t * a.k + lane] : 0.0f;
+      dw = dweights[t * a.k + lane];
     }
-    const float dot = warp_sum(expert >= 0 ? w * dw : 0.0f);
-    const float d = w * (dw - dot);
     T* out = dlogits + t * a.E;
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    float m = 0.0f, inv = 0.0f;
-    if (!a.normalize) {
-      m = -CUDART_INF_F;
+    const bool chosen = expert >= 0 && expert < a.E;
+    const float dot = warp_sum(chosen ? w * dw : 0.0f);
+    if (a.normalize) {
+      if (vec) {
+        for (int e = lane * V; e < a.E; e += 32 * V)
+          *reinterpret_cast<uint4*>(out + e) = make_uint4(0, 0, 0, 0);
+      } else {
+        for (int e = lane; e < a.E; e += 32) out[e] = Elem<T>::put(0.0f);
+      }
+    } else {
+      const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+      float m = -CUDART_INF_F, s = 0.0f;
       for (int e = lane; e < a.E; e += 32) m = fmaxf(m, Elem<T>::get(row[e]));
       m = warp_max(m);
-      float s = 0.0f;
       // (a token with no finite logit has no choices: its gradient is zero)
-      if (m != -CUDART_INF_F)
+      const bool some = m != -CUDART_INF_F;
+      if (some)
         for (int e = lane; e < a.E; e += 32) s += expf(Elem<T>::get(row[e]) - m);
-      s = warp_sum(s);
-      inv = m != -CUDART_INF_F ? 1.0f / s : 0.0f;
+      const float scale = some ? -dot / warp_sum(s) : 0.0f;
+      for (int e = lane; e < a.E; e += 32)
+        out[e] = Elem<T>::put(some ? expf(Elem<T>::get(row[e]) - m) * scale : 0.0f);
     }
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      float v = 0.0f;
-      if (!a.normalize && e < a.E && m != -CUDART_INF_F)
-        v = -(expf(Elem<T>::get(row[e]) - m) * inv) * dot;
-      for (int j = 0; j < a.k; ++j) {
-        const int ej = __shfl_sync(kAll, expert, j);
-        const float dj = __shfl_sync(kAll, d, j);
-        if (e == ej) v = dj;
-      }
-      if (e < a.E) out[e] = Elem<T>::put(v);
-    }
+    __syncwarp();
+    if (chosen) out[expert] = Elem<T>::put(w * (dw - dot));
   }
 }
 

@@ -15,6 +15,7 @@ struct Elem;
 template <>
 struct Elem<float> {
   static constexpr int kVec = 4;
+  static constexpr uint32_t kNegInf = 0;  // (16-bit types only)
   static __device__ __forceinline__ float get(float v) { return v; }
   static __device__ __forceinline__ float put(float v) { return v; }
   static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
@@ -32,6 +33,7 @@ struct Elem<float> {
 template <>
 struct Elem<__half> {
   static constexpr int kVec = 8;
+  static constexpr uint32_t kNegInf = 0xfc00u;
   static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
   static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
   static __device__ __forceinline__ uint32_t pair(float lo, float hi) {
@@ -58,6 +60,7 @@ struct Elem<__half> {
 template <>
 struct Elem<__nv_bfloat16> {
   static constexpr int kVec = 8;
+  static constexpr uint32_t kNegInf = 0xff80u;
   static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
   static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
   static __device__ __forceinline__ uint32_t pair(float lo, float hi) {
