@@ -97,6 +97,21 @@ __device__ __forceinline__ void store_elems(T* p, const float (&f)[V]) {
     *reinterpret_cast<uint4*>(p) = Elem<T>::pack(f);
 }
 
+// The same as it is loaded, in half (16-bit types) of the registers of its floats:
+// for loads that wait in flight.
+template <typename T, int V>
+struct Raw {
+  uint4 u;
+  __device__ __forceinline__ void load(const T* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&f)[V]) const { Elem<T>::unpack(u, f); }
+};
+template <typename T>
+struct Raw<T, 1> {
+  T u;
+  __device__ __forceinline__ void load(const T* p) { u = *p; }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = Elem<T>::get(u); }
+};
+
 // Two floats to e4m3 codes (nearest, ties to even, clipped to +-448; NaN stays
 // NaN), lo in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
