@@ -74,13 +74,13 @@ __host__ __device__ constexpr int r_bytes(int BN) { return rows_per_cta(BN) * 12
 // Stages that fit: 3 of 64 KB, or 5 of 40 KB for short row tiles, where the bytes in
 // flight are nearly the weights' alone.
 __host__ __device__ constexpr int stages_of(int BN) { return (BN == kXRows ? 6 : 10) / kSub; }
-constexpr int kScaleSlots = 4;  // e4m3: k-blocks whose scales are held
-constexpr int kScaleBatch = 4;  // and for long groups: two batches of four, for both column blocks
+constexpr int kScaleBatch = 4;  // e4m3: k-blocks whose scales are handed over at once; two such batches
 __host__ __device__ constexpr int scale_bytes(int op, int BN) {
-  return op == kOpFp8 ? kScaleSlots * BN * 4 : op == kOpFp8Long ? 2 * kScaleBatch * 2 * 128 * 4 : 0;
+  return op == kOpFp8 ? 2 * kScaleBatch * BN * 4 : op == kOpFp8Long ? 2 * kScaleBatch * 2 * 128 * 4 : 0;
 }
-constexpr int kOutBytes = 1024;  // an epilogue warp's buffer for 8 rows of output
-__host__ __device__ constexpr int out_bytes(int op) { return op == kOpFp8Long ? 0 : kXEpiWarps * kOutBytes; }
+// An epilogue warp's buffer for rows of output on their way: 8 of 128 bytes, or 4.
+__host__ __device__ constexpr int out_buffer(int op) { return op == kOpFp8Long ? 0 : op == kOpFp8 ? 512 : 1024; }
+__host__ __device__ constexpr int out_bytes(int op) { return kXEpiWarps * out_buffer(op); }
 constexpr int kTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) & ~15;
 __host__ __device__ constexpr int smem_bytes(int op, int BN) {
   return stages_of(BN) * kSub * (kWBytes + r_bytes(BN)) + scale_bytes(op, BN) +
@@ -158,13 +158,12 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "r"(taddr));
 }
 
-// Accumulators in TMEM's 512 columns: 2 of 256, or 8 of 64, which keep the MMA going
-// while the epilogue's answers for short row tiles (a k-block each, e4m3) are on their way.
-__host__ __device__ constexpr int accs_of(int BN) { return 512 / BN; }
-template <int BN>
-__device__ __forceinline__ uint32_t acc_slot(uint32_t acc) { return acc % accs_of(BN); }
-template <int BN>
-__device__ __forceinline__ uint32_t acc_phase(uint32_t acc) { return acc / accs_of(BN) & 1u; }
+// Accumulators: two of 256 TMEM columns.  For e4m3 with short row tiles one holds four
+// k-blocks of 64 columns side by side, so that they are handed over together: a
+// hand-over costs the epilogue about 300 cycles, as much as a k-block's sums.
+constexpr int kAccCols = 256;
+constexpr int kFewBlocks = kAccCols / kXFewRows;
+static_assert(kScaleBatch == kFewBlocks, "scales are handed over with the accumulators");
 
 // ------------------------------------------------------------------ work
 // A unit of work, the same for every role of both CTAs.
@@ -370,8 +369,8 @@ struct Ring {
   uint64_t* zfull;  // and, on the even CTA: both CTAs' parts zeroed behind the group's end
   uint64_t* sfull;  // e4m3: scales of a k-block, by slot
   uint64_t* sempty; // e4m3: this CTA's epilogue warps are through with them
-  float* scales;    // [kScaleSlots][BN]
-  uint8_t* stage_out;  // a buffer of kOutBytes for each epilogue warp
+  float* scales;    // two batches: [k-block][BN], long groups [k-block][column block][128]
+  uint8_t* stage_out;  // a buffer of out_buffer(OP) bytes for each epilogue warp
   volatile int* abort;
 };
 
@@ -522,35 +521,38 @@ __device__ void zero_role(const ExpertsParams& p, Schedule<kOpWeight, BN>& sch,
 
 // ------------------------------------------------------------------ scales (e4m3)
 // For each k-block the scales of the tile's rows times this CTA's weights' scale (its
-// 128 of the wide dimension are one block), a few k-blocks ahead of the epilogue.
+// 128 of the wide dimension are one block), a batch of k-blocks per hand-over.
 template <int BN>
 __device__ void scale_role(const ExpertsParams& p, Schedule<kOpFp8, BN>& sch,
                            const Ring& ring, uint32_t rank, int lane) {
   constexpr int kPer = BN / 32;
-  uint32_t n = 0;  // k-blocks so far
+  uint32_t batch = 0;
   bool ok = true;
   Unit u;
   for (int32_t i = 0; ok && sch.get(i, u); ++i) {
     const int32_t NB = (p.wide + 127) / 128, nb = u.n0 / 128 + static_cast<int>(rank);
     const float* ws = p.ws + (static_cast<int64_t>(u.e) * NB + (nb < NB ? nb : NB - 1)) * sch.KB;
     const float* xs = p.xs + u.row0 + lane;
-    float x[kPer], w = 0.0f;
-    auto fetch = [&](int32_t kb) {
-      w = __ldg(ws + kb);
+    for (int32_t kb0 = u.kb0; kb0 < u.kb1; kb0 += kScaleBatch, ++batch) {
+      const int32_t n = u.kb1 - kb0 < kScaleBatch ? u.kb1 - kb0 : kScaleBatch;
+      float x[kScaleBatch][kPer], w[kScaleBatch];
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        x[j] = j * 32 + lane < u.cnt ? __ldg(xs + static_cast<int64_t>(kb) * p.rows + j * 32) : 0.0f;
-    };
-    fetch(u.kb0);
-    for (int32_t kb = u.kb0; kb < u.kb1; ++kb, ++n) {
-      const uint32_t slot = n % kScaleSlots;
-      ok = mbar_wait(&ring.sempty[slot], ((n / kScaleSlots) & 1u) ^ 1u, p.timeout_ns, ring.abort,
-                     p.status);
+      for (int j = 0; j < kScaleBatch; ++j) {
+        w[j] = j < n ? __ldg(ws + kb0 + j) : 0.0f;
+#pragma unroll
+        for (int r = 0; r < kPer; ++r)
+          x[j][r] = j < n && r * 32 + lane < u.cnt
+                        ? __ldg(xs + static_cast<int64_t>(kb0 + j) * p.rows + r * 32) : 0.0f;
+      }
+      const uint32_t slot = batch & 1u;
+      ok = mbar_wait(&ring.sempty[slot], ((batch >> 1) & 1u) ^ 1u, p.timeout_ns, ring.abort, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) ring.scales[slot * BN + j * 32 + lane] = x[j] * w;
-      if (kb + 1 < u.kb1) fetch(kb + 1);
+      for (int j = 0; j < kScaleBatch; ++j)
+#pragma unroll
+        for (int r = 0; r < kPer; ++r)
+          ring.scales[(slot * kScaleBatch + j) * BN + r * 32 + lane] = x[j][r] * w[j];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.sfull[slot]);
     }
@@ -632,9 +634,9 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
   int stage = 0;
   uint32_t acc = 0, full_phase = 0, zeroed = 0;  // bit s: parity of stage s's barriers
   bool ok = true;
-  auto accumulator = [&](uint32_t n = 0) {  // wait until the n-th from here has been read
-    const bool r = warp_wait(&ring.tempty[acc_slot<BN>(acc + n)], acc_phase<BN>(acc + n) ^ 1u,
-                             p.timeout_ns, ring.abort, p.status);
+  auto accumulator = [&] {  // wait until it has been read
+    const bool r = warp_wait(&ring.tempty[acc & 1u], ((acc >> 1) & 1u) ^ 1u, p.timeout_ns, ring.abort,
+                             p.status);
     tc_fence_after();
     return r;
   };
@@ -647,13 +649,14 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
     const uint32_t r_second = kRMn ? 64 * 128 / 16
                               : OP == kOpFp8Long ? r_bytes(BN) / 16
                                                  : static_cast<uint32_t>(box_of<BN>(width / 2) * (BN / 8) * 128 / 16);
+    const int32_t segment = OP == kOpFp8Long ? 1 : OP == kOpFp8 ? kFewBlocks : p.segment;
     int32_t left = 0;  // k-blocks left of the segment
     for (int32_t kb0 = kb_begin; kb0 < kb_end; kb0 += kSub) {
       const int n_sub = kb_end - kb0 < kSub ? kb_end - kb0 : kSub;
       bool first = false;
-      if (!is_fp8(OP) && left <= 0) {
+      if (OP != kOpFp8Long && left <= 0) {
         if (!(ok = accumulator())) break;
-        left = p.segment;
+        left = segment;
         first = true;
       }
       int last_steps = 4;  // of the stage's last k-block
@@ -675,11 +678,9 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
 #pragma unroll
       for (int s = 0; s < kSub; ++s) {
         if (s >= n_sub) break;
-        // (the epilogue reads them in order: with many, one wait serves the stage's)
-        if (is_fp8(OP) && (accs_of(BN) < 4 || s == 0) &&
-            !(ok = accumulator(accs_of(BN) < 4 ? 0 : n_sub - 1)))
-          break;
-        const uint32_t d = tmem + acc_slot<BN>(acc) * BN;
+        if (OP == kOpFp8Long && !(ok = accumulator())) break;
+        const uint32_t d = tmem + (acc & 1u) * kAccCols +
+                           (OP == kOpFp8 ? (kFewBlocks - left + s) * kXFewRows : 0);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -691,18 +692,18 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
             else
               mma_f16_pair(d, wd, rd, idesc, (!first || s > 0 || k > 0) ? 1u : 0u);
           }
-          if (is_fp8(OP)) mma_commit_pair_both(&ring.tfull[acc_slot<BN>(acc)]);
+          if (OP == kOpFp8Long) mma_commit_pair_both(&ring.tfull[acc & 1u]);
         }
-        if (is_fp8(OP)) ++acc;
+        if (OP == kOpFp8Long) ++acc;
       }
       if (!ok) break;
       if (elect_one()) mma_commit_pair_both(&ring.empty[stage]);
       if (++stage == kStagesX) stage = 0;
-      if (!is_fp8(OP)) {
+      if (OP != kOpFp8Long) {
         left -= n_sub;
         if (left <= 0 || kb0 + kSub >= kb_end) {
           left = 0;
-          if (elect_one()) mma_commit_pair_both(&ring.tfull[acc_slot<BN>(acc)]);
+          if (elect_one()) mma_commit_pair_both(&ring.tfull[acc & 1u]);
           ++acc;
         }
       }
@@ -720,25 +721,31 @@ __device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
 // memory (a buffer per warp) so that a store instruction writes 16 bytes a lane, 64 or
 // 128 contiguous bytes of each row: stores of one element a lane, at the LSU's rate of
 // one instruction per about 7 cycles, took 7000 cycles for a 256 x 256 tile.
+template <int kBytes>  // of the buffer
 struct Out {
   void* base;
   int64_t ldo, row0, col;  // col: the warp's first
   int type;
   int32_t cnt, cols;       // rows of the tile; columns of the output from col on
-  uint8_t* stage;          // 1 KB
+  uint8_t* stage;
   __device__ __forceinline__ void store(int32_t c0, const float (&v)[8], int lane) const {
     __syncwarp();  // the buffer has been read
     if (type == kTypeF32) {
+      constexpr int kRows = kBytes / 128;  // rows at a time
       float* s = reinterpret_cast<float*>(stage) + lane;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i * 32] = v[i];
-      __syncwarp();
+      for (int r0 = 0; r0 < 8; r0 += kRows) {
+        if (r0 > 0) __syncwarp();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = h * 4 + (lane >> 3), part = (lane & 7) * 4;
-        const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 128 + part * 4);
-        if (c0 + row < cnt && part < cols)
-          *reinterpret_cast<uint4*>(static_cast<float*>(base) + (row0 + c0 + row) * ldo + col + part) = x;
+        for (int i = 0; i < kRows; ++i) s[i * 32] = v[r0 + i];
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < kRows; h += 4) {
+          const int r = h + (lane >> 3), row = r0 + r, part = (lane & 7) * 4;
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 128 + part * 4);
+          if (c0 + row < cnt && part < cols)
+            *reinterpret_cast<uint4*>(static_cast<float*>(base) + (row0 + c0 + row) * ldo + col + part) = x;
+        }
       }
     } else {
       uint16_t* s = reinterpret_cast<uint16_t*>(stage) + lane;
@@ -757,6 +764,20 @@ struct Out {
     }
   }
 };
+
+// 16 columns of an output row in one store of 32 bytes (16-bit outputs whose rows are
+// 32-byte aligned): whole sectors, half the instructions.
+__device__ __forceinline__ void store_row16(void* base, int type, int64_t at, const float (&v)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i] = type == kTypeF16 ? Elem<__half>::pair(v[2 * i], v[2 * i + 1])
+                            : Elem<__nv_bfloat16>::pair(v[2 * i], v[2 * i + 1]);
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                   static_cast<uint16_t*>(base) + at),
+               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 
 // After this warp has stored its part of a split sum: true for the warp that comes
 // last and adds the parts.
@@ -830,16 +851,22 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
       const uint32_t from0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c_first;
       const uint32_t tempty0 = mapa_shared(smem_u32(ring.tempty), 0);
       const float* scale0 = ring.scales + (c_first >> 7) * 128 + quad * 32 + lane;
-      for (int32_t left = u.kb1 - u.kb0; left > 0; left -= kScaleBatch, ++batch) {
+      bool ok = true;
+      for (int32_t left = u.kb1 - u.kb0; ok && left > 0; left -= kScaleBatch, ++batch) {
         const uint32_t slot = batch & 1u;
-        bool ok = mbar_wait(&ring.sfull[slot], (batch >> 1) & 1u, p.timeout_ns, ring.abort, p.status);
-        const int32_t n = left < kScaleBatch ? left : kScaleBatch;
-        for (int32_t j = 0; ok && j < n; ++j) {
-          const float s = scale0[(slot * kScaleBatch + j) * 256];
-          ok = mbar_wait(&ring.tfull[acc_slot<BN>(acc)], acc_phase<BN>(acc), p.timeout_ns, ring.abort,
-                         p.status);
+        ok = mbar_wait(&ring.sfull[slot], (batch >> 1) & 1u, p.timeout_ns, ring.abort, p.status);
+        // the batch's scales to registers: a load in the loop would be waited for
+        float s[kScaleBatch];
+#pragma unroll
+        for (int j = 0; j < kScaleBatch; ++j) s[j] = scale0[(slot * kScaleBatch + j) * 256];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ring.sempty[slot]);
+#pragma unroll
+        for (int j = 0; j < kScaleBatch; ++j) {
+          if (!ok || j >= left) break;
+          ok = mbar_wait(&ring.tfull[acc & 1u], (acc >> 1) & 1u, p.timeout_ns, ring.abort, p.status);
           tc_fence_after();
-          const uint32_t from = from0 + acc_slot<BN>(acc) * BN;
+          const uint32_t from = from0 + (acc & 1u) * kAccCols;
           if (n16 == kCols / 16) {
 #pragma unroll
             for (int c = 0; c < kCols / 16; ++c) {
@@ -849,11 +876,11 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
               if (c == kCols / 16 - 1) {  // the accumulator has been read
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_pair(tempty0 + acc_slot<BN>(acc) * 8);
+                if (lane == 0) mbar_arrive_pair(tempty0 + (acc & 1u) * 8);
               }
 #pragma unroll
               for (int q = 0; q < 16; ++q)
-                sums[c * 16 + q] = fmaf(__uint_as_float(v[q]), s, sums[c * 16 + q]);
+                sums[c * 16 + q] = fmaf(__uint_as_float(v[q]), s[j], sums[c * 16 + q]);
             }
           } else {  // the last columns
 #pragma unroll
@@ -864,21 +891,19 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
                 tmem_ld_wait();
 #pragma unroll
                 for (int q = 0; q < 16; ++q)
-                  sums[c * 16 + q] = fmaf(__uint_as_float(v[q]), s, sums[c * 16 + q]);
+                  sums[c * 16 + q] = fmaf(__uint_as_float(v[q]), s[j], sums[c * 16 + q]);
               }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair(tempty0 + acc_slot<BN>(acc) * 8);
+            if (lane == 0) mbar_arrive_pair(tempty0 + (acc & 1u) * 8);
           }
           ++acc;
         }
-        if (!ok) {
-          set_status(p.status, kStatusPipelineTimeout, 0x300u | rank);
-          *ring.abort = 1;
-          return;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ring.sempty[slot]);
+      }
+      if (!ok) {
+        set_status(p.status, kStatusPipelineTimeout, 0x300u | rank);
+        *ring.abort = 1;
+        return;
       }
     }
     Unit u;
@@ -892,6 +917,17 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = sums[c * 8 + j];
     };
+    if (sch.split == 1 && n == kCols / 8 && p.rows32) {
+      if (row < u.cnt)
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = sums[c + j];
+          store_row16(p.out, p.out_type, at + c, v);
+        }
+      continue;
+    }
     if (sch.split == 1) {
 #pragma unroll
       for (int c = 0; c < kCols / 8; ++c)
@@ -940,53 +976,65 @@ __device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
       const int n8 = u.w / 32, c_first = quarter * n8 * 8;  // this warp's columns, in eights
       const uint32_t from0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c_first;
       const uint32_t tempty0 = mapa_shared(smem_u32(ring.tempty), 0);
-      const int32_t seg = OP == kOpFp8 ? 1 : p.segment;
-      for (int32_t left = u.kb1 - u.kb0; left > 0; left -= seg) {
-        [[maybe_unused]] const float* scale = ring.scales + (acc % kScaleSlots) * BN + c_first;
+      const int32_t seg = OP == kOpFp8 ? kFewBlocks : p.segment;
+      for (int32_t left = u.kb1 - u.kb0; left > 0; left -= seg, ++acc) {
+        const uint32_t slot = acc & 1u, phase = (acc >> 1) & 1u;
         bool ok = true;
         if constexpr (OP == kOpFp8)
-          ok = mbar_wait(&ring.sfull[acc % kScaleSlots], (acc / kScaleSlots) & 1u, p.timeout_ns,
-                         ring.abort, p.status);
-        if (!ok || !mbar_wait(&ring.tfull[acc_slot<BN>(acc)], acc_phase<BN>(acc), p.timeout_ns, ring.abort,
-                              p.status)) {
+          ok = mbar_wait(&ring.sfull[slot], phase, p.timeout_ns, ring.abort, p.status);
+        if (!ok || !mbar_wait(&ring.tfull[slot], phase, p.timeout_ns, ring.abort, p.status)) {
           set_status(p.status, kStatusPipelineTimeout, 0x300u | rank);
           *ring.abort = 1;
           return;
         }
         tc_fence_after();
-        const uint32_t from = from0 + acc_slot<BN>(acc) * BN;
+        const uint32_t from = from0 + slot * kAccCols;
+        if constexpr (OP == kOpFp8) {
+          // four k-blocks side by side: this warp's columns of each, times their scales
+          const float* scale = ring.scales + slot * (kFewBlocks * BN) + c_first;
 #pragma unroll
-        for (int c = 0; c < kCols / 8; ++c) {
-          if (c < n8) {
-            uint32_t v[8];
-            tmem_ld8(from + c * 8, v);
-            tmem_ld_wait();
-            if (c == n8 - 1) {  // the accumulator has been read
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_pair(tempty0 + acc_slot<BN>(acc) * 8);
+          for (int j = 0; j < kFewBlocks; ++j) {
+            if (j < left) {
+              uint32_t v[kCols];
+              if (n8 == kCols / 8)
+                tmem_ld16(from + j * BN, v);
+              else
+                tmem_ld8(from + j * BN, *reinterpret_cast<uint32_t(*)[8]>(v));
+              tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < kCols; q += 4)
+                if (q < n8 * 8) {
+                  const float4 f = *reinterpret_cast<const float4*>(scale + j * BN + q);
+                  sums[q] = fmaf(__uint_as_float(v[q]), f.x, sums[q]);
+                  sums[q + 1] = fmaf(__uint_as_float(v[q + 1]), f.y, sums[q + 1]);
+                  sums[q + 2] = fmaf(__uint_as_float(v[q + 2]), f.z, sums[q + 2]);
+                  sums[q + 3] = fmaf(__uint_as_float(v[q + 3]), f.w, sums[q + 3]);
+                }
             }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_pair(tempty0 + slot * 8);
+            mbar_arrive(&ring.sempty[slot]);
+          }
+        } else {
 #pragma unroll
-            for (int q = 0; q < 8; q += 4) {
-              float* s = sums + c * 8 + q;
-              if constexpr (OP == kOpFp8) {
-                const float4 f = *reinterpret_cast<const float4*>(scale + c * 8 + q);
-                s[0] = fmaf(__uint_as_float(v[q]), f.x, s[0]);
-                s[1] = fmaf(__uint_as_float(v[q + 1]), f.y, s[1]);
-                s[2] = fmaf(__uint_as_float(v[q + 2]), f.z, s[2]);
-                s[3] = fmaf(__uint_as_float(v[q + 3]), f.w, s[3]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[j] += __uint_as_float(v[q + j]);
+          for (int c = 0; c < kCols / 8; ++c) {
+            if (c < n8) {
+              uint32_t v[8];
+              tmem_ld8(from + c * 8, v);
+              tmem_ld_wait();
+              if (c == n8 - 1) {  // the accumulator has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(tempty0 + slot * 8);
               }
+#pragma unroll
+              for (int q = 0; q < 8; ++q) sums[c * 8 + q] += __uint_as_float(v[q]);
             }
           }
         }
-        if constexpr (OP == kOpFp8) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ring.sempty[acc % kScaleSlots]);
-        }
-        ++acc;
       }
     }
     // (the unit again: its fields would take the registers of the loop above)
@@ -994,9 +1042,9 @@ __device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
     sch.get(i, u);
     const int n8 = u.w / 32, c_first = quarter * n8 * 8;
     const int32_t col = u.n0 + static_cast<int32_t>(rank) * 128 + quad * 32;
-    const Out out{p.out, p.ldo,
+    const Out<out_buffer(OP)> out{p.out, p.ldo,
                   OP == kOpWeight ? static_cast<int64_t>(u.e) * p.out_rows + u.kt0 : u.row0, col,
-                  p.out_type, u.cnt, p.wide - col, ring.stage_out + ew * kOutBytes};
+                  p.out_type, u.cnt, p.wide - col, ring.stage_out + ew * out_buffer(OP)};
     auto eight = [&](int c, float (&v)[8]) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = sums[c * 8 + j];
@@ -1054,12 +1102,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   ring.full = bars;
   ring.empty = bars + kStagesX;
   ring.tfull = bars + 2 * kStagesX;
-  ring.tempty = ring.tfull + accs_of(BN);
-  ring.tail = ring.tempty + accs_of(BN);
+  ring.tempty = ring.tfull + 2;
+  ring.tail = ring.tempty + 2;
   ring.zfull = ring.tail + kStagesX;
   ring.sfull = ring.zfull + kStagesX;
-  ring.sempty = ring.sfull + kScaleSlots;
-  uint64_t* drain = ring.sempty + kScaleSlots;
+  ring.sempty = ring.sfull + 2;
+  uint64_t* drain = ring.sempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   ring.abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* flag = reinterpret_cast<int32_t*>(tmem_slot + 2);
@@ -1074,13 +1122,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       mbar_init(&ring.tail[s], 1);
       mbar_init(&ring.zfull[s], 2);
     }
-    for (int b = 0; b < accs_of(BN); ++b) {
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&ring.tfull[b], 1);
       mbar_init(&ring.tempty[b], 2 * kXEpiWarps);
-    }
-    for (int s = 0; s < kScaleSlots; ++s) {
-      mbar_init(&ring.sfull[s], 1);
-      mbar_init(&ring.sempty[s], kXEpiWarps);
+      mbar_init(&ring.sfull[b], 1);
+      mbar_init(&ring.sempty[b], kXEpiWarps);
     }
     mbar_init(drain, 1);
     *tmem_slot = 0;

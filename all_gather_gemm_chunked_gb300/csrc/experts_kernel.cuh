@@ -44,6 +44,7 @@ struct ExpertsParams {
   int32_t segment;               // k-blocks per accumulator (e4m3: 1)
   int32_t bf16;                  // operands are bfloat16 (otherwise fp16)
   int32_t out_type;              // ElemType of the output
+  int32_t rows32;                // 16-bit output whose rows start at multiples of 32 bytes
   void* out;
   int64_t ldo;
   const float* xs;               // e4m3: row scales [KB][rows]

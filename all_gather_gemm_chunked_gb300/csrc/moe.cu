@@ -249,6 +249,7 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   x.arrivals = p->arrivals;
   x.max_units = max_units(few);
   x.status = p->status;
+  x.rows32 = x.out_type != AG_MOE_F32 && (reinterpret_cast<uintptr_t>(x.out) & 31u) == 0 && x.ldo % 16 == 0;
   x.timeout_ns = p->timeout_ns;
   const int64_t wide_tiles = (x.wide + agg::kXWide - 1) / agg::kXWide;
   if (row_tiles * wide_tiles >= (1LL << 30))
