@@ -239,13 +239,14 @@ struct Schedule {
   }
 
   // Parts that make the longest pair's share shortest: a round of the pairs costs its
-  // k-blocks and about six more for a tile's start and end.  Each lane tries one number.
+  // k-blocks and about six more for a tile's start and end, parts about eight more once,
+  // for the sums' way through memory.  Each lane tries one number.
   __device__ __forceinline__ int32_t choose_split(int32_t tiles) const {
     if (tiles == 0 || tiles >= 2 * pairs || p.max_units == 0) return 1;
     const int32_t s = static_cast<int32_t>(threadIdx.x & 31) + 1;
     const bool can = s == 1 || (s <= 16 && KB >= 4 * s && tiles * s <= p.max_units);
     const int32_t rounds = (tiles * s + pairs - 1) / pairs;
-    const uint32_t cost = can ? static_cast<uint32_t>(rounds * ((KB + s - 1) / s + 6)) : 0x03ffffffu;
+    const uint32_t cost = can ? static_cast<uint32_t>(rounds * ((KB + s - 1) / s + 6) + (s > 1 ? 8 : 0)) : 0x03ffffffu;
     // (the smallest number among the cheapest)
     const uint32_t best = __reduce_min_sync(0xffffffffu, min(cost, 0x03ffffffu) * 32 + (s - 1));
     return static_cast<int32_t>(best & 31u) + 1;

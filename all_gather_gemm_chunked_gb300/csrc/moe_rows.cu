@@ -214,29 +214,46 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_s
   return warp_sums[warp] + s - v;
 }
 
+// A warp's first tokens' choices are held in registers.
+constexpr int kHeld = 4;
+// The choices (lane j's) of the tokens t0 .. t0 + 3 below end.
+__device__ __forceinline__ void load_choices(const RouteArgs& a, int64_t t0, int64_t end, int lane,
+                                             int (&x)[kHeld]) {
+#pragma unroll
+  for (int n = 0; n < kHeld; ++n)
+    x[n] = lane < a.k && t0 + n < end ? a.experts[(t0 + n) * a.k + lane] : -1;
+}
+
 // Place the block's choices.  A row's place is its expert's first row, plus the
 // expert's choices in earlier blocks, in earlier warps of this block, and in this
 // warp's earlier tokens (a token chooses an expert at most once): counts and
 // prefix sums alone, so the order within an expert is the tokens'.
 // smem: [kRouteWarps][E] uint16 counts (a warp has fewer than 2^16 tokens: T is at
-// most 2^28), then E uint32 first rows, 32 warp sums and the number of rows in use.
-__device__ void place(const RouteArgs& a, int64_t T0, int64_t T1, uint8_t* smem) {
+// most 2^28), then E uint32 first rows, 32 warp sums, the number of rows in use, E counts of
+// earlier blocks.
+__device__ void place(const RouteArgs& a, int64_t T0, int64_t T1, uint8_t* smem,
+                      const int (&held)[kHeld]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint16_t* cnt = reinterpret_cast<uint16_t*>(smem);
   uint32_t* base = reinterpret_cast<uint32_t*>(smem + ((kRouteWarps * a.E * 2 + 15) & ~15));
   uint32_t* sums = base + a.E;
   for (int i = threadIdx.x; i < kRouteWarps * a.E; i += kRouteThreads) cnt[i] = 0;
-  for (int e = threadIdx.x; e < a.E; e += kRouteThreads) base[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += kRouteThreads) base[e] = sums[33 + e] = 0;
   __syncthreads();
   const Share own = share_of(T0, T1, warp, kRouteWarps);
-  // (four tokens' choices in flight)
-  for (int64_t t0 = own.t0; t0 < own.t1; t0 += 4) {
-    int x[4];
+  auto choices_at = [&](int64_t t0, int (&x)[kHeld]) {
+    if (t0 == own.t0) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
-      x[n] = lane < a.k && t0 + n < own.t1 ? a.experts[(t0 + n) * a.k + lane] : -1;
+      for (int n = 0; n < kHeld; ++n) x[n] = held[n];
+    } else {
+      load_choices(a, t0, own.t1, lane, x);
+    }
+  };
+  for (int64_t t0 = own.t0; t0 < own.t1; t0 += kHeld) {
+    int x[kHeld];
+    choices_at(t0, x);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int n = 0; n < kHeld; ++n) {
       if (x[n] >= 0) cnt[warp * a.E + x[n]] += 1;
       __syncwarp();
     }
@@ -246,30 +263,29 @@ __device__ void place(const RouteArgs& a, int64_t T0, int64_t T1, uint8_t* smem)
   uint32_t total = 0, before = 0;
   if (gridDim.x == 1) {
     if (e < a.E)
+#pragma unroll 16
       for (int w = 0; w < kRouteWarps; ++w) total += cnt[w * a.E + e];
   } else {
     // groups of E threads read the blocks' counts side by side
-    uint32_t* acc = base;  // total, then the earlier blocks' part
-    const int groups = kRouteThreads / a.E > 0 ? kRouteThreads / a.E : 1;
+    uint32_t* early = sums + 33;  // the earlier blocks' part (base holds the totals)
+    const int groups = kRouteThreads / a.E;
     const int g = e / a.E, x = e - g * a.E;
-    uint32_t all = 0, early = 0;
-    if (g < groups && x < a.E)
+    uint32_t all = 0, mine = 0;
+    if (g < groups)
 #pragma unroll 20
       for (int b = g; b < static_cast<int>(gridDim.x); b += groups) {
         const uint32_t c = static_cast<uint32_t>(a.counts[static_cast<int64_t>(b) * a.E + x]);
         all += c;
-        if (b < static_cast<int>(blockIdx.x)) early += c;
+        if (b < static_cast<int>(blockIdx.x)) mine += c;
       }
     // integer additions: the same in any order
-    if (all) atomicAdd(&acc[x], all);
+    if (all) atomicAdd(&base[x], all);
+    if (mine) atomicAdd(&early[x], mine);
     __syncthreads();
-    if (e < a.E) total = acc[e];
-    __syncthreads();
-    if (e < a.E) acc[e] = 0;
-    __syncthreads();
-    if (early) atomicAdd(&acc[x], early);
-    __syncthreads();
-    if (e < a.E) before = acc[e];
+    if (e < a.E) {
+      total = base[e];
+      before = early[e];
+    }
     __syncthreads();
   }
   const uint32_t first = block_exclusive(e < a.E ? total : 0u, sums, warp, lane);
@@ -292,13 +308,11 @@ __device__ void place(const RouteArgs& a, int64_t T0, int64_t T1, uint8_t* smem)
     if (e == a.E - 1) sums[32] = first + total;  // rows in use
   }
   __syncthreads();
-  for (int64_t t0 = own.t0; t0 < own.t1; t0 += 4) {
-    int x[4];
+  for (int64_t t0 = own.t0; t0 < own.t1; t0 += kHeld) {
+    int x[kHeld];
+    choices_at(t0, x);
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
-      x[n] = lane < a.k && t0 + n < own.t1 ? a.experts[(t0 + n) * a.k + lane] : -1;
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int n = 0; n < kHeld; ++n) {
       const int64_t t = t0 + n;
       int32_t place = -1;
       if (x[n] >= 0) {
@@ -315,7 +329,7 @@ __device__ void place(const RouteArgs& a, int64_t T0, int64_t T1, uint8_t* smem)
     a.order[s] = -1;
 }
 
-size_t place_smem(int E) { return ((static_cast<size_t>(kRouteWarps) * E * 2 + 15) & ~size_t{15}) + E * 4 + 33 * 4; }
+size_t place_smem(int E) { return ((static_cast<size_t>(kRouteWarps) * E * 2 + 15) & ~size_t{15}) + 2 * E * 4 + 33 * 4; }
 
 // Up to kOneBlockTokens tokens: choices and layout by one block, one launch.
 template <typename T, int VPL>
@@ -325,10 +339,18 @@ __global__ void __launch_bounds__(kRouteThreads) route_one_kernel(const RouteArg
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Share own = share_of(0, a.T, warp, kRouteWarps);
   constexpr int kTokens = tokens_of(VPL);
-  int chosen[kTokens];
-  for (int64_t t = own.t0; t < own.t1; t += kTokens) choose<T, VPL>(a, t, own.t1, lane, chosen);
-  __syncthreads();
-  place(a, 0, a.T, smem);
+  int held[kHeld] = {-1, -1, -1, -1};  // (a warp has at most kHeld tokens here)
+#pragma unroll
+  for (int n = 0; n < kHeld; n += kTokens) {
+    int chosen[kTokens];
+    if (own.t0 + n < own.t1) {
+      choose<T, VPL>(a, own.t0 + n, own.t1, lane, chosen);
+#pragma unroll
+      for (int i = 0; i < kTokens; ++i)
+        if (own.t0 + n + i < own.t1) held[n + i] = chosen[i];
+    }
+  }
+  place(a, 0, a.T, smem, held);
 }
 
 // More: one kernel chooses and counts the choices of each block's tokens, the
@@ -359,7 +381,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteA
   pdl_wait();
   extern __shared__ __align__(16) uint8_t smem[];
   const Share blk = share_of(0, a.T, blockIdx.x, gridDim.x);
-  place(a, blk.t0, blk.t1, smem);
+  const Share own = share_of(blk.t0, blk.t1, threadIdx.x >> 5, kRouteWarps);
+  int held[kHeld];
+  load_choices(a, own.t0, own.t1, threadIdx.x & 31, held);
+  place(a, blk.t0, blk.t1, smem, held);
 }
 
 // Gradient of the logits, one warp per token.  normalize: w_j (dw_j - sum w dw) at the
@@ -586,7 +611,7 @@ int values_per_lane(int E) { return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E
 
 // One block serves as many tokens as its warps take in four turns; beyond that
 // blocks of at least 32 tokens, one per SM at most.
-constexpr int64_t kOneBlockTokens = 4 * kRouteWarps;
+constexpr int64_t kOneBlockTokens = kHeld * kRouteWarps;
 int route_blocks(int64_t T) {
   if (T <= kOneBlockTokens) return 1;
   const int64_t b = (T + 31) / 32;
