@@ -90,6 +90,9 @@ static_assert(smem_bytes(kOpForward, kXRows) <= 227 * 1024 && smem_bytes(kOpFp8,
                   smem_bytes(kOpFp8Long, kXRows) <= 227 * 1024,
               "shared memory of an SM");
 
+// After a wait has run out: how long what is in flight is waited for.
+constexpr uint64_t kDrainNs = 20000000;
+
 __device__ __forceinline__ void set_status(uint32_t* status, uint32_t kind, uint32_t detail) {
   if (atomicCAS(status, 0u, kind) == 0u) atomicExch(status + 1, detail);
 }
@@ -111,6 +114,17 @@ __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* m
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
+}
+
+// cluster_sync in two steps, and an arrival that publishes no memory writes.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Arrive on a barrier of either CTA of the pair without a cluster-scope release:
@@ -142,8 +156,9 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// A wait of a whole warp: the vote keeps its control flow uniform, so that what the
-// warp computes around it (the MMA's descriptors) stays in uniform registers.
+// A wait of a whole warp.  The vote keeps its control flow uniform: the warp goes on, or
+// gives up, together (TMEM loads are a warp's), and what it computes around the wait (the
+// MMA's descriptors) stays in uniform registers.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
                                           volatile int* abort, const volatile uint32_t* gstatus) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
@@ -189,6 +204,7 @@ __host__ __device__ constexpr int block_k() { return is_fp8(OP) ? 128 : 64; }
 struct Divisor {
   uint32_t d, m;
   __device__ __forceinline__ explicit Divisor(uint32_t d_) : d(d_), m(0xffffffffu / d_) {}
+  __device__ __forceinline__ Divisor(uint32_t d_, uint32_t m_) : d(d_), m(m_) {}
   __device__ __forceinline__ uint32_t div(uint32_t n, uint32_t& rest) const {
     uint32_t q = __umulhi(n, m);
     rest = n - q * d;
@@ -203,14 +219,37 @@ __constant__ uint32_t kInverse[kXGroup + 1] = {0, 0xffffffffu, 0xffffffffu / 2, 
                                                0xffffffffu / 4, 0xffffffffu / 5, 0xffffffffu / 6,
                                                0xffffffffu / 7, 0xffffffffu / 8};
 
+// The work of a launch, in shared memory.
+struct Table {
+  const int32_t* off;   // [E + 1] row offsets
+  const int32_t* pre;   // [E + 1] row tiles before each expert
+  const int32_t* head;  // parts of each tile's sum, floor((2^32 - 1) / parts), units
+};
+
+// Parts of a sum that make the longest pair's share shortest: a round of the pairs costs
+// its k-blocks and about six more for a tile's start and end, parts about eight more
+// once, for the sums' way through memory.  Each lane of a warp tries one number.
+__device__ __forceinline__ int32_t choose_split(int32_t tiles, int32_t KB, int32_t max_units) {
+  const int32_t pairs = static_cast<int32_t>(gridDim.x / 2);
+  if (tiles == 0 || tiles >= 2 * pairs || KB < 8) return 1;
+  const int32_t s = static_cast<int32_t>(threadIdx.x & 31) + 1;
+  const bool can = s == 1 || (s <= 16 && KB >= 4 * s && tiles * s <= max_units);
+  const int32_t rounds = (tiles * s + pairs - 1) / pairs;
+  const uint32_t cost = can ? static_cast<uint32_t>(rounds * ((KB + s - 1) / s + 6) + (s > 1 ? 8 : 0)) : 0x03ffffffu;
+  // (the smallest number among the cheapest)
+  const uint32_t best = __reduce_min_sync(0xffffffffu, min(cost, 0x03ffffffu) * 32 + (s - 1));
+  return static_cast<int32_t>(best & 31u) + 1;
+}
+
 // The units of a pair in order: unit i is number pair + i * pairs of the list.  A role
-// asks for them one after the other (or the same one again).
+// asks for them one after the other.  (Cheap to make: the epilogue makes it anew for
+// each tile, so that nothing of it takes registers while sums are added.)
 template <int OP, int BN>
 struct Schedule {
   const ExpertsParams& p;
-  const int32_t* off;   // [E + 1] row offsets
-  const int32_t* pre;   // [E + 1] row tiles before each expert
-  int32_t wt;           // wide tiles
+  const int32_t* off;
+  const int32_t* pre;
+  int32_t wt;           // tiles of the wide dimension
   int32_t kt;           // weight gradient: output row tiles per expert
   int32_t KB;           // k-blocks of a whole sum
   int32_t split;        // parts of each tile's sum
@@ -219,38 +258,34 @@ struct Schedule {
   // the expert of the last unit, its first tile, row tiles and their height
   int32_t e, tile0, nt, height;
 
-  __device__ __forceinline__ Schedule(const ExpertsParams& p_, const int32_t* off_,
-                                      const int32_t* pre_)
-      : p(p_), off(off_), pre(pre_), wt((p_.wide + kXWide - 1) / kXWide),
-        kt(OP == kOpWeight ? (p_.out_rows + BN - 1) / BN : 0),
-        KB(OP == kOpWeight ? 0 : (p_.red + block_k<OP>() - 1) / block_k<OP>()),
-        pair(static_cast<int32_t>(blockIdx.x / 2)), pairs(static_cast<int32_t>(gridDim.x / 2)),
-        split(1), by_split(1), by_group(static_cast<uint32_t>(kXGroup * wt)),
-        by_expert(OP == kOpWeight ? static_cast<uint32_t>(wt * kt) : 1u), e(-1), tile0(0), nt(0),
-        height(0) {
-    if constexpr (OP == kOpWeight) {
-      units = p.E * wt * kt;
-    } else {
-      const int32_t tiles = pre[p.E] * wt;
-      split = choose_split(tiles);
-      if (split > 1) by_split = Divisor(static_cast<uint32_t>(split));
-      units = tiles * split;
+  static __device__ __forceinline__ int32_t wide_tiles(const ExpertsParams& p) {
+    return (p.wide + kXWide - 1) / kXWide;
+  }
+  static __device__ __forceinline__ int32_t row_tiles(const ExpertsParams& p) {
+    return OP == kOpWeight ? (p.out_rows + BN - 1) / BN : 0;
+  }
+  static __device__ __forceinline__ int32_t k_blocks(const ExpertsParams& p) {
+    return OP == kOpWeight ? 0 : (p.red + block_k<OP>() - 1) / block_k<OP>();
+  }
+  // By one warp, once the table's `tiles` row tiles are known: its head.
+  static __device__ __forceinline__ void fill_head(const ExpertsParams& p, int32_t tiles, int32_t* head) {
+    const int32_t wt = wide_tiles(p);
+    const int32_t split = OP == kOpWeight ? 1 : choose_split(tiles * wt, k_blocks(p), p.max_units);
+    if ((threadIdx.x & 31) == 0) {
+      head[0] = split;
+      head[1] = static_cast<int32_t>(split == 1 ? 0xffffffffu : 0xffffffffu / static_cast<uint32_t>(split));
+      head[2] = OP == kOpWeight ? p.E * wt * row_tiles(p) : tiles * wt * split;
     }
   }
 
-  // Parts that make the longest pair's share shortest: a round of the pairs costs its
-  // k-blocks and about six more for a tile's start and end, parts about eight more once,
-  // for the sums' way through memory.  Each lane tries one number.
-  __device__ __forceinline__ int32_t choose_split(int32_t tiles) const {
-    if (tiles == 0 || tiles >= 2 * pairs || p.max_units == 0) return 1;
-    const int32_t s = static_cast<int32_t>(threadIdx.x & 31) + 1;
-    const bool can = s == 1 || (s <= 16 && KB >= 4 * s && tiles * s <= p.max_units);
-    const int32_t rounds = (tiles * s + pairs - 1) / pairs;
-    const uint32_t cost = can ? static_cast<uint32_t>(rounds * ((KB + s - 1) / s + 6) + (s > 1 ? 8 : 0)) : 0x03ffffffu;
-    // (the smallest number among the cheapest)
-    const uint32_t best = __reduce_min_sync(0xffffffffu, min(cost, 0x03ffffffu) * 32 + (s - 1));
-    return static_cast<int32_t>(best & 31u) + 1;
-  }
+  __device__ __forceinline__ Schedule(const ExpertsParams& p_, const Table& t)
+      : p(p_), off(t.off), pre(t.pre), wt(wide_tiles(p_)), kt(row_tiles(p_)), KB(k_blocks(p_)),
+        split(t.head[0]), units(t.head[2]), pair(static_cast<int32_t>(blockIdx.x / 2)),
+        pairs(static_cast<int32_t>(gridDim.x / 2)),
+        by_split(static_cast<uint32_t>(split), static_cast<uint32_t>(t.head[1])),
+        by_group(static_cast<uint32_t>(kXGroup * wt), p_.inv_group),
+        by_expert(OP == kOpWeight ? static_cast<uint32_t>(wt * kt) : 1u, p_.inv_expert), e(-1), tile0(0),
+        nt(0), height(0) {}
 
   // Tile `r` of an expert with n row tiles: groups of 8 row tiles, in a group all wide
   // tiles, the row tiles innermost.
@@ -278,7 +313,8 @@ struct Schedule {
     tile0 = pre[lo] * wt;
     nt = pre[lo + 1] - pre[lo];
     // its rows in nt tiles of equal height, a multiple of 32 (rows on the M side: 256)
-    height = OP == kOpFp8Long ? BN : ((off[lo + 1] - off[lo] + nt - 1) / nt + 31) & ~31;
+    const int32_t cnt = off[lo + 1] - off[lo];
+    height = OP == kOpFp8Long ? BN : ((nt == 1 ? cnt : (cnt + nt - 1) / nt) + 31) & ~31;
   }
 
   __device__ __forceinline__ bool get(int32_t i, Unit& u) {
@@ -330,8 +366,8 @@ struct Schedule {
 
 // Offsets to shared memory, checked, and the row tiles before each expert.
 // Returns false (to every thread) if the offsets are no layout of the rows.
-template <int BN>
-__device__ bool load_table(const ExpertsParams& p, int32_t* off, int32_t* pre, int32_t* flag) {
+template <int OP, int BN>
+__device__ bool load_table(const ExpertsParams& p, int32_t* off, int32_t* pre, int32_t* head, int32_t* flag) {
   if (threadIdx.x == 0) *flag = 0;
   for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
     off[e] = p.offsets ? p.offsets[e] : (e == 0 ? 0 : p.rows);
@@ -354,6 +390,7 @@ __device__ bool load_table(const ExpertsParams& p, int32_t* off, int32_t* pre, i
       carry += __shfl_sync(0xffffffffu, s, 31);
     }
     if (lane == 0) pre[0] = 0;
+    Schedule<OP, BN>::fill_head(p, carry, head);
   }
   __syncthreads();
   return *flag == 0;
@@ -409,8 +446,9 @@ __device__ __forceinline__ int32_t box_of(int32_t half) {
 }
 
 template <int OP, int BN>
-__device__ void tma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ring& ring,
+__device__ void tma_role(const ExpertsParams& p, const Table& table, const Ring& ring,
                          uint32_t rank, int lane) {
+  Schedule<OP, BN> sch(p, table);
   constexpr int kStagesX = stages_of(BN);
   const uint32_t full0 = mapa_shared(smem_u32(ring.full), 0);
   [[maybe_unused]] const uint32_t tail0 = mapa_shared(smem_u32(ring.tail), rank);
@@ -472,7 +510,7 @@ __device__ void tma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
     if (rank == 0) {
       volatile int never = 0;
       for (int s = 0; s < kStagesX; ++s)
-        if (issued & (1u << s)) mbar_wait(&ring.full[s], ((filled >> s) & 1u) ^ 1u, 20000000ull, &never);
+        if (issued & (1u << s)) mbar_wait(&ring.full[s], ((filled >> s) & 1u) ^ 1u, kDrainNs, &never);
     }
   }
   __syncwarp();
@@ -484,8 +522,9 @@ __device__ void tma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ri
 // reads; then the k-block is passed on.  A warp of its own: the TMA warp, waiting for
 // its own loads here, would leave the ring to run dry once per tile.
 template <int BN>
-__device__ void zero_role(const ExpertsParams& p, Schedule<kOpWeight, BN>& sch,
+__device__ void zero_role(const ExpertsParams& p, const Table& table,
                           const Ring& ring, uint32_t rank, int lane) {
+  Schedule<kOpWeight, BN> sch(p, table);
   constexpr int kStagesX = stages_of(BN);
   const uint32_t zfull0 = mapa_shared(smem_u32(ring.zfull), 0);
   uint32_t stages = 0, used = 0;  // stages so far; bit s: parity of stage s's tails
@@ -524,8 +563,9 @@ __device__ void zero_role(const ExpertsParams& p, Schedule<kOpWeight, BN>& sch,
 // For each k-block the scales of the tile's rows times this CTA's weights' scale (its
 // 128 of the wide dimension are one block), a batch of k-blocks per hand-over.
 template <int BN>
-__device__ void scale_role(const ExpertsParams& p, Schedule<kOpFp8, BN>& sch,
+__device__ void scale_role(const ExpertsParams& p, const Table& table,
                            const Ring& ring, uint32_t rank, int lane) {
+  Schedule<kOpFp8, BN> sch(p, table);
   constexpr int kPer = BN / 32;
   uint32_t batch = 0;
   bool ok = true;
@@ -567,8 +607,9 @@ __device__ void scale_role(const ExpertsParams& p, Schedule<kOpFp8, BN>& sch,
 // Long groups: this CTA's 128 rows' scales times those of the tile's two column blocks,
 // [k-block][column block][row], a batch of k-blocks per hand-over.
 template <int BN>
-__device__ void scale_long_role(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& sch,
+__device__ void scale_long_role(const ExpertsParams& p, const Table& table,
                                 const Ring& ring, uint32_t rank, int lane) {
+  Schedule<kOpFp8Long, BN> sch(p, table);
   uint32_t batch = 0;
   bool ok = true;
   Unit u;
@@ -618,8 +659,9 @@ __device__ void scale_long_role(const ExpertsParams& p, Schedule<kOpFp8Long, BN>
 // ------------------------------------------------------------------ MMA (one warp)
 // The warp waits and computes together; lane 0 issues.
 template <int OP, int BN>
-__device__ void mma_role(const ExpertsParams& p, Schedule<OP, BN>& sch, const Ring& ring,
+__device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring& ring,
                          int lane, uint32_t tmem) {
+  Schedule<OP, BN> sch(p, table);
   constexpr int kStagesX = stages_of(BN);
   constexpr bool kWMn = OP == kOpForward || OP == kOpWeight;
   constexpr bool kRMn = OP == kOpWeight;
@@ -835,7 +877,7 @@ __device__ __forceinline__ void add_parts(const float* first, int64_t next, int3
 // the MMA's operands.  scale_long_role prepares them, four k-blocks at a time: loads
 // from global memory in this loop stalled it for half of its time.
 template <int BN>
-__device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& sch,
+__device__ void epilogue_long(const ExpertsParams& p, const Table& table,
                               const Ring& ring, uint32_t rank, int ew, int lane, uint32_t tmem) {
   constexpr int kCols = 64;
   const int quad = (threadIdx.x >> 5) & 3, c_first = (ew >> 2) * kCols;
@@ -846,7 +888,7 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
     for (int c = 0; c < kCols; ++c) sums[c] = 0.0f;
     {
       Unit u;
-      if (!sch.get(i, u)) break;
+      if (!Schedule<kOpFp8Long, BN>(p, table).get(i, u)) break;
       const int cols = u.w - c_first;  // a multiple of 32
       const int n16 = cols <= 0 ? 0 : cols >= kCols ? kCols / 16 : cols / 16;
       const uint32_t from0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c_first;
@@ -855,7 +897,7 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
       bool ok = true;
       for (int32_t left = u.kb1 - u.kb0; ok && left > 0; left -= kScaleBatch, ++batch) {
         const uint32_t slot = batch & 1u;
-        ok = mbar_wait(&ring.sfull[slot], (batch >> 1) & 1u, p.timeout_ns, ring.abort, p.status);
+        ok = warp_wait(&ring.sfull[slot], (batch >> 1) & 1u, p.timeout_ns, ring.abort, p.status);
         // the batch's scales to registers: a load in the loop would be waited for
         float s[kScaleBatch];
 #pragma unroll
@@ -865,7 +907,7 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
 #pragma unroll
         for (int j = 0; j < kScaleBatch; ++j) {
           if (!ok || j >= left) break;
-          ok = mbar_wait(&ring.tfull[acc & 1u], (acc >> 1) & 1u, p.timeout_ns, ring.abort, p.status);
+          ok = warp_wait(&ring.tfull[acc & 1u], (acc >> 1) & 1u, p.timeout_ns, ring.abort, p.status);
           tc_fence_after();
           const uint32_t from = from0 + (acc & 1u) * kAccCols;
           if (n16 == kCols / 16) {
@@ -908,6 +950,7 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
       }
     }
     Unit u;
+    Schedule<kOpFp8Long, BN> sch(p, table);
     sch.get(i, u);
     const int32_t row = static_cast<int32_t>(rank) * 128 + quad * 32 + lane;
     const int64_t col = static_cast<int64_t>(u.n0) + c_first;
@@ -962,7 +1005,7 @@ __device__ void epilogue_long(const ExpertsParams& p, Schedule<kOpFp8Long, BN>& 
 }
 
 template <int OP, int BN>
-__device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
+__device__ void epilogue_role(const ExpertsParams& p, const Table& table,
                               const Ring& ring, uint32_t rank, int ew, int lane, uint32_t tmem) {
   constexpr int kCols = BN / 4;  // columns of a warp, at most
   const int quad = (threadIdx.x >> 5) & 3, quarter = ew >> 2;
@@ -973,7 +1016,7 @@ __device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
     for (int c = 0; c < kCols; ++c) sums[c] = 0.0f;
     {
       Unit u;
-      if (!sch.get(i, u)) break;
+      if (!Schedule<OP, BN>(p, table).get(i, u)) break;
       const int n8 = u.w / 32, c_first = quarter * n8 * 8;  // this warp's columns, in eights
       const uint32_t from0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c_first;
       const uint32_t tempty0 = mapa_shared(smem_u32(ring.tempty), 0);
@@ -982,8 +1025,8 @@ __device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
         const uint32_t slot = acc & 1u, phase = (acc >> 1) & 1u;
         bool ok = true;
         if constexpr (OP == kOpFp8)
-          ok = mbar_wait(&ring.sfull[slot], phase, p.timeout_ns, ring.abort, p.status);
-        if (!ok || !mbar_wait(&ring.tfull[slot], phase, p.timeout_ns, ring.abort, p.status)) {
+          ok = warp_wait(&ring.sfull[slot], phase, p.timeout_ns, ring.abort, p.status);
+        if (!ok || !warp_wait(&ring.tfull[slot], phase, p.timeout_ns, ring.abort, p.status)) {
           set_status(p.status, kStatusPipelineTimeout, 0x300u | rank);
           *ring.abort = 1;
           return;
@@ -1040,6 +1083,7 @@ __device__ void epilogue_role(const ExpertsParams& p, Schedule<OP, BN>& sch,
     }
     // (the unit again: its fields would take the registers of the loop above)
     Unit u;
+    Schedule<OP, BN> sch(p, table);
     sch.get(i, u);
     const int n8 = u.w / 32, c_first = quarter * n8 * 8;
     const int32_t col = u.n0 + static_cast<int32_t>(rank) * 128 + quad * 32;
@@ -1112,6 +1156,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   ring.abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* flag = reinterpret_cast<int32_t*>(tmem_slot + 2);
+  int32_t* head = flag + 1;  // [3]
+  const Table table{off, pre, head};
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -1140,47 +1186,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   }
   if (warp == 2 && lane <= kXRowBoxes)  // the descriptors' first use would wait for them
     tma_prefetch_desc(lane == kXRowBoxes ? &p.tm_w : &p.tm_r[OP == kOpWeight ? 0 : lane]);
-  pdl_wait();  // from here on global memory is read
-  const bool valid = load_table<BN>(p, off, pre, flag);
   tc_fence_before();
-  cluster_sync();
+  cluster_arrive();  // barriers initialised, TMEM allocated; the table is read meanwhile
+  pdl_wait();        // from here on global memory is read
+  const bool valid = load_table<OP, BN>(p, off, pre, head, flag);
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
   if (valid) {
-    Schedule<OP, BN> sch(p, off, pre);
     if (warp == 0) {
-      tma_role<OP, BN>(p, sch, ring, rank, lane);
+      tma_role<OP, BN>(p, table, ring, rank, lane);
     } else if (warp == 1) {
-      if (rank == 0) mma_role<OP, BN>(p, sch, ring, lane, tmem);
+      if (rank == 0) mma_role<OP, BN>(p, table, ring, lane, tmem);
     } else if (warp < 2 + kXEpiWarps) {
       if constexpr (OP == kOpFp8Long)
-        epilogue_long<BN>(p, sch, ring, rank, warp - 2, lane, tmem);
+        epilogue_long<BN>(p, table, ring, rank, warp - 2, lane, tmem);
       else
-        epilogue_role<OP, BN>(p, sch, ring, rank, warp - 2, lane, tmem);
+        epilogue_role<OP, BN>(p, table, ring, rank, warp - 2, lane, tmem);
     } else if constexpr (OP == kOpWeight) {
-      zero_role<BN>(p, sch, ring, rank, lane);
+      zero_role<BN>(p, table, ring, rank, lane);
     } else if constexpr (OP == kOpFp8) {
-      scale_role<BN>(p, sch, ring, rank, lane);
+      scale_role<BN>(p, table, ring, rank, lane);
     } else if constexpr (OP == kOpFp8Long) {
-      scale_long_role<BN>(p, sch, ring, rank, lane);
+      scale_long_role<BN>(p, table, ring, rank, lane);
     }
   } else if (threadIdx.x == 0) {
     set_status(p.status, kStatusOffsets, 0);
   }
   tc_fence_before();
-  __syncthreads();
-  if (rank == 0 && warp == 1 && elect_one()) {  // the thread that issued the MMAs
-    mma_commit_pair_local(drain);
-    volatile int never = 0;
-    mbar_wait(drain, 0, p.timeout_ns, &never);
-  }
-  if (*ring.abort || *reinterpret_cast<volatile uint32_t*>(p.status) != 0u) {
-    // after a timeout loads that no barrier of ours counts may still be landing
+  // Every accumulator has been waited for, so every MMA and load of the pair is through,
+  // unless a wait ran out (the whole block's verdict: the status word may change meanwhile):
+  if (__syncthreads_or(*ring.abort || *reinterpret_cast<volatile uint32_t*>(p.status) != 0u)) {
+    if (rank == 0 && warp == 1 && elect_one()) {  // the thread that issued the MMAs
+      mma_commit_pair_local(drain);
+      volatile int never = 0;
+      mbar_wait(drain, 0, kDrainNs, &never);
+    }
+    // loads that no barrier of ours counts may still be landing
     if (threadIdx.x == 0) __nanosleep(100000);
+    __syncthreads();
   }
-  __syncthreads();
+  // (relaxed: the pair only leaves together, what it wrote is published by its end)
   tc_fence_before();
-  cluster_sync();
+  cluster_arrive_relaxed();
+  cluster_wait();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);

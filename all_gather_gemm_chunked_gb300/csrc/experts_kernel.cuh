@@ -40,6 +40,7 @@ struct ExpertsParams {
   int32_t wide;                  // extent of the wide dimension
   int32_t red;                   // length of the sums (weight gradient: unused)
   int32_t out_rows;              // weight gradient: output rows per expert (K)
+  uint32_t inv_group, inv_expert;  // floor((2^32 - 1) / n): n tiles of 8 row tiles, n of an expert (weight gradient)
   int32_t w_blk, r_blk;          // operand described in blocks of 128 bytes (one load a stage), or not (two)
   int32_t segment;               // k-blocks per accumulator (e4m3: 1)
   int32_t bf16;                  // operands are bfloat16 (otherwise fp16)

@@ -252,8 +252,11 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   x.rows32 = x.out_type != AG_MOE_F32 && (reinterpret_cast<uintptr_t>(x.out) & 31u) == 0 && x.ldo % 16 == 0;
   x.timeout_ns = p->timeout_ns;
   const int64_t wide_tiles = (x.wide + agg::kXWide - 1) / agg::kXWide;
-  if (row_tiles * wide_tiles >= (1LL << 30))
+  if ((row_tiles + agg::kXGroup) * wide_tiles >= (1LL << 30))
     return fail(AG_GEMM_ERR_UNSUPPORTED, "more than 2^30 tiles");
+  x.inv_group = 0xffffffffu / static_cast<uint32_t>(agg::kXGroup * wide_tiles);
+  x.inv_expert = 0xffffffffu / static_cast<uint32_t>(
+                                   wide_tiles * ((x.out_rows + agg::kXRows - 1) / agg::kXRows) + (x.out_rows == 0));
   // A captured run is ordered by its graph: an event of the stream outside cannot be
   // waited on there, nor one of the graph outside.
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;

@@ -262,3 +262,52 @@ def test_refusals():
         lib = B_.library_handle()
         assert lib.ag_moe_forward(None, 1, None, 0, None, None, 0, 0, None, 0, 0, None) == B_.ERR_INVALID
         assert lib.ag_fp8_forward(p.handle, 1, None, None, None, None, None, None, 0, 0, None) == B_.ERR_INVALID
+
+
+def test_runs_in_a_cuda_graph():
+    """A plan's runs can be captured, whatever stream ran before, and replayed on new inputs."""
+    from all_gather_gemm_chunked_gb300 import fp8
+    g = rng(31)
+    T, E, k, K, N = 24, 6, 2, 256, 320
+    x, logits = randn(g, (T, K), torch.bfloat16), randn(g, (T, E))
+    w = randn(g, (E, K, N), torch.bfloat16, K ** -0.5)
+    wq, ws = fp8.quantize_weights(w)
+
+    def step():
+        r = moe.route(logits, k)
+        y = up.forward(moe.gather(x, r), r.offsets, w)
+        z = low.forward(*fp8.quantize_rows(x, r), wq, ws, r.offsets)
+        return moe.combine(y, r.slots, r.weights), moe.combine(z, r.slots, r.weights)
+
+    with moe.Experts(E, K, N) as up, fp8.Fp8Linear(K, N, n_experts=E) as low:
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        for seed in (32, 33):
+            x.copy_(randn(rng(seed), (T, K), torch.bfloat16))
+            logits.copy_(randn(rng(seed + 5), (T, E)))
+            graph.replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in out]
+            for a, b in zip(got, step()):
+                assert torch.equal(a, b)
+        assert up.status() == B_.OK and low.status() == B_.OK
+
+
+def test_rows_counts_around_the_tile_heights():
+    """Short and long row tiles, chosen by the mean rows of a group, agree with 64 bits at
+    the change-over (64 rows a group) and at tile edges."""
+    K, N, E = 128, 64, 2
+    g = rng(41)
+    w = randn(g, (E, K, N), torch.float16, K ** -0.5)
+    for sizes in ([64, 64], [65, 64], [0, 128], [129, 0], [1, 255], [257, 1], [512, 31]):
+        x, off = randn(g, (sum(sizes), K), torch.float16), offsets_of(sizes)
+        with moe.Experts(E, K, N, "f16") as p:
+            y = p.forward(x, off, w)
+        at = 0
+        for e, n in enumerate(sizes):
+            a, b = x[at:at + n].double(), w[e].double()
+            check(y[at:at + n], a @ b, product_bound(a, b, K, torch.float16), f"{sizes} {e}")
+            at += n
