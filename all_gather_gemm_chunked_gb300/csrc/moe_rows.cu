@@ -214,54 +214,43 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_s
   return warp_sums[warp] + s - v;
 }
 
-// A warp's first tokens' choices are held in registers.
-constexpr int kHeld = 4;
-// The choices (lane j's) of the tokens t0 .. t0 + 3 below end.
-__device__ __forceinline__ void load_choices(const RouteArgs& a, int64_t t0, int64_t end, int lane,
-                                             int (&x)[kHeld]) {
-#pragma unroll
-  for (int n = 0; n < kHeld; ++n)
-    x[n] = lane < a.k && t0 + n < end ? a.experts[(t0 + n) * a.k + lane] : -1;
-}
-
-// Place the block's choices.  A row's place is its expert's first row, plus the
-// expert's choices in earlier blocks, in earlier warps of this block, and in this
-// warp's earlier tokens (a token chooses an expert at most once): counts and
-// prefix sums alone, so the order within an expert is the tokens'.
-// smem: [kRouteWarps][E] uint16 counts (a warp has fewer than 2^16 tokens: T is at
-// most 2^28), then E uint32 first rows, 32 warp sums, the number of rows in use, E counts of
-// earlier blocks.
-__device__ void place(const RouteArgs& a, int64_t T0, int64_t T1, uint8_t* smem,
-                      const int (&held)[kHeld]) {
+// Place a block's choices c0 .. c1 - 1 (token * k + j), 32 a warp at a time.  A row's
+// place is its expert's first row, plus the expert's choices in earlier blocks, in
+// earlier warps of this block, in this warp's earlier steps and in earlier lanes (a
+// match of the experts over the warp): counts and prefix sums alone, so the order
+// within an expert is the tokens' (a token chooses an expert at most once).
+// smem: [kRouteWarps][E] uint16 counts (a warp has fewer than 2^16 tokens: T is at most
+// 2^28), then E uint32 first rows, 32 warp sums, the number of rows in use, E counts of
+// earlier blocks.  `blocks`: blocks that place, with their counts if more than one.
+__device__ void place(const RouteArgs& a, int64_t c0, int64_t c1, int blocks, uint8_t* smem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint16_t* cnt = reinterpret_cast<uint16_t*>(smem);
   uint32_t* base = reinterpret_cast<uint32_t*>(smem + ((kRouteWarps * a.E * 2 + 15) & ~15));
   uint32_t* sums = base + a.E;
-  for (int i = threadIdx.x; i < kRouteWarps * a.E; i += kRouteThreads) cnt[i] = 0;
+  // this warp's choices: a multiple of 32, the first 64 of them held in registers
+  const int64_t per = ((c1 - c0 + kRouteThreads - 1) / kRouteThreads) * 32;
+  const int64_t w0 = c0 + warp * per, w1 = w0 + per < c1 ? w0 + per : c1;
+  auto load = [&](int64_t c) { return c < w1 ? __ldcg(a.experts + c) : -1; };
+  const int held0 = load(w0 + lane), held1 = load(w0 + 32 + lane);
+  auto expert_at = [&](int64_t c) { return c == w0 ? held0 : c == w0 + 32 ? held1 : load(c + lane); };
+  for (int i = threadIdx.x; i < kRouteWarps * a.E / 2; i += kRouteThreads)
+    reinterpret_cast<uint32_t*>(cnt)[i] = 0;
   for (int e = threadIdx.x; e < a.E; e += kRouteThreads) base[e] = sums[33 + e] = 0;
   __syncthreads();
-  const Share own = share_of(T0, T1, warp, kRouteWarps);
-  auto choices_at = [&](int64_t t0, int (&x)[kHeld]) {
-    if (t0 == own.t0) {
-#pragma unroll
-      for (int n = 0; n < kHeld; ++n) x[n] = held[n];
-    } else {
-      load_choices(a, t0, own.t1, lane, x);
-    }
-  };
-  for (int64_t t0 = own.t0; t0 < own.t1; t0 += kHeld) {
-    int x[kHeld];
-    choices_at(t0, x);
-#pragma unroll
-    for (int n = 0; n < kHeld; ++n) {
-      if (x[n] >= 0) cnt[warp * a.E + x[n]] += 1;
-      __syncwarp();
-    }
+  uint16_t* mine = cnt + warp * a.E;
+  uint32_t match0 = 0, match1 = 0;  // held too: a match takes a step for each distinct expert
+  for (int64_t c = w0; c < w1; c += 32) {
+    const int x = expert_at(c);
+    const uint32_t same = __match_any_sync(kAll, x);
+    if (c == w0) match0 = same;
+    if (c == w0 + 32) match1 = same;
+    if (x >= 0 && lane == __ffs(same) - 1) mine[x] = static_cast<uint16_t>(mine[x] + __popc(same));
+    __syncwarp();
   }
   __syncthreads();
   const int e = threadIdx.x;
   uint32_t total = 0, before = 0;
-  if (gridDim.x == 1) {
+  if (blocks == 1) {
     if (e < a.E)
 #pragma unroll 16
       for (int w = 0; w < kRouteWarps; ++w) total += cnt[w * a.E + e];
@@ -270,17 +259,17 @@ __device__ void place(const RouteArgs& a, int64_t T0, int64_t T1, uint8_t* smem,
     uint32_t* early = sums + 33;  // the earlier blocks' part (base holds the totals)
     const int groups = kRouteThreads / a.E;
     const int g = e / a.E, x = e - g * a.E;
-    uint32_t all = 0, mine = 0;
+    uint32_t all = 0, own = 0;
     if (g < groups)
 #pragma unroll 20
-      for (int b = g; b < static_cast<int>(gridDim.x); b += groups) {
+      for (int b = g; b < blocks; b += groups) {
         const uint32_t c = static_cast<uint32_t>(a.counts[static_cast<int64_t>(b) * a.E + x]);
         all += c;
-        if (b < static_cast<int>(blockIdx.x)) mine += c;
+        if (b < static_cast<int>(blockIdx.x)) own += c;
       }
     // integer additions: the same in any order
     if (all) atomicAdd(&base[x], all);
-    if (mine) atomicAdd(&early[x], mine);
+    if (own) atomicAdd(&early[x], own);
     __syncthreads();
     if (e < a.E) {
       total = base[e];
@@ -295,62 +284,58 @@ __device__ void place(const RouteArgs& a, int64_t T0, int64_t T1, uint8_t* smem,
     if (blockIdx.x == 0 && e == 0) a.offsets[0] = 0;
     uint32_t run = 0;  // counts to the counts of earlier warps
 #pragma unroll
-    for (int w0 = 0; w0 < kRouteWarps; w0 += 8) {
+    for (int v0 = 0; v0 < kRouteWarps; v0 += 8) {
       uint32_t c[8];
 #pragma unroll
-      for (int w = 0; w < 8; ++w) c[w] = cnt[(w0 + w) * a.E + e];
+      for (int w = 0; w < 8; ++w) c[w] = cnt[(v0 + w) * a.E + e];
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
-        cnt[(w0 + w) * a.E + e] = static_cast<uint16_t>(run);
+        cnt[(v0 + w) * a.E + e] = static_cast<uint16_t>(run);
         run += c[w];
       }
     }
     if (e == a.E - 1) sums[32] = first + total;  // rows in use
   }
   __syncthreads();
-  for (int64_t t0 = own.t0; t0 < own.t1; t0 += kHeld) {
-    int x[kHeld];
-    choices_at(t0, x);
-#pragma unroll
-    for (int n = 0; n < kHeld; ++n) {
-      const int64_t t = t0 + n;
-      int32_t place = -1;
-      if (x[n] >= 0) {
-        place = static_cast<int32_t>(base[x[n]] + cnt[warp * a.E + x[n]]);
-        cnt[warp * a.E + x[n]] += 1;
-        a.order[place] = static_cast<int32_t>(t * a.k + lane);
-      }
-      if (lane < a.k && t < own.t1) a.slots[t * a.k + lane] = place;
-      __syncwarp();
+  for (int64_t c = w0; c < w1; c += 32) {
+    const int x = expert_at(c);
+    const uint32_t same = c == w0 ? match0 : c == w0 + 32 ? match1 : __match_any_sync(kAll, x);
+    int32_t row = -1;
+    if (x >= 0) {
+      row = static_cast<int32_t>(base[x] + mine[x] + __popc(same & ((1u << lane) - 1u)));
+      a.order[row] = static_cast<int32_t>(c + lane);
     }
+    __syncwarp();
+    if (x >= 0 && lane == __ffs(same) - 1) mine[x] = static_cast<uint16_t>(mine[x] + __popc(same));
+    if (c + lane < w1) a.slots[c + lane] = row;
+    __syncwarp();
   }
-  for (int64_t s = sums[32] + static_cast<int64_t>(blockIdx.x) * kRouteThreads + threadIdx.x;
-       s < a.T * a.k; s += static_cast<int64_t>(gridDim.x) * kRouteThreads)
+  for (int64_t s = sums[32] + static_cast<int64_t>(blocks == 1 ? 0 : blockIdx.x) * kRouteThreads + threadIdx.x;
+       s < a.T * a.k; s += static_cast<int64_t>(blocks) * kRouteThreads)
     a.order[s] = -1;
 }
 
-size_t place_smem(int E) { return ((static_cast<size_t>(kRouteWarps) * E * 2 + 15) & ~size_t{15}) + 2 * E * 4 + 33 * 4; }
+size_t place_smem(int E) {
+  return ((static_cast<size_t>(kRouteWarps) * E * 2 + 15) & ~size_t{15}) + 2 * E * 4 + 33 * 4;
+}
 
-// Up to kOneBlockTokens tokens: choices and layout by one block, one launch.
+// Few tokens: a cluster of blocks chooses, its first block places, one launch.
+// (Choosing is bound by instructions: 75 tokens of 182 experts on one SM took 8 us.)
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kRouteThreads) route_one_kernel(const RouteArgs a) {
   pdl_enter();
   extern __shared__ __align__(16) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Share own = share_of(0, a.T, warp, kRouteWarps);
+  const int lane = threadIdx.x & 31;
   constexpr int kTokens = tokens_of(VPL);
-  int held[kHeld] = {-1, -1, -1, -1};  // (a warp has at most kHeld tokens here)
-#pragma unroll
-  for (int n = 0; n < kHeld; n += kTokens) {
+  // tokens go round the blocks, so that a block's warps are few where tokens are
+  for (int64_t t = (static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x) * kTokens; t < a.T;
+       t += static_cast<int64_t>(kRouteWarps) * gridDim.x * kTokens) {
     int chosen[kTokens];
-    if (own.t0 + n < own.t1) {
-      choose<T, VPL>(a, own.t0 + n, own.t1, lane, chosen);
-#pragma unroll
-      for (int i = 0; i < kTokens; ++i)
-        if (own.t0 + n + i < own.t1) held[n + i] = chosen[i];
-    }
+    choose<T, VPL>(a, t, a.T, lane, chosen);
   }
-  place(a, 0, a.T, smem, held);
+  // the choices of all blocks are written
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (blockIdx.x == 0) place(a, 0, a.T * a.k, 1, smem);
 }
 
 // More: one kernel chooses and counts the choices of each block's tokens, the
@@ -381,10 +366,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteA
   pdl_wait();
   extern __shared__ __align__(16) uint8_t smem[];
   const Share blk = share_of(0, a.T, blockIdx.x, gridDim.x);
-  const Share own = share_of(blk.t0, blk.t1, threadIdx.x >> 5, kRouteWarps);
-  int held[kHeld];
-  load_choices(a, own.t0, own.t1, threadIdx.x & 31, held);
-  place(a, blk.t0, blk.t1, smem, held);
+  place(a, blk.t0 * a.k, blk.t1 * a.k, static_cast<int>(gridDim.x), smem);
 }
 
 // Gradient of the logits, one warp per token.  normalize: w_j (dw_j - sum w dw) at the
@@ -609,11 +591,17 @@ int values_per_lane(int E) { return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E
 
 }  // namespace
 
-// One block serves as many tokens as its warps take in four turns; beyond that
-// blocks of at least 32 tokens, one per SM at most.
-constexpr int64_t kOneBlockTokens = kHeld * kRouteWarps;
+// One cluster serves as many tokens as its warps take in one step each, two tokens a
+// warp; beyond that blocks of at least 32 tokens, one per SM at most.
+// (64 experts, k 4: 256 tokens 7.1 us against 7.6 by two kernels, 384 tokens 8.2
+// against 7.6; 256 experts, k 8: 11.4 against 12.3, 15.1 against 12.7.)
+constexpr int64_t kOneClusterTokens = 256;
+// Its blocks: one for as few tokens as it takes, else eight.
+// (64 experts, k 4: 16 tokens 3.7 us by one block, 4.0 by eight, 32 tokens 4.1 and 4.0;
+// 256 experts, k 8: 5.2 and 5.1, 6.4 and 5.3.)
+int cluster_blocks(int64_t T) { return T <= 16 ? 1 : 8; }
 int route_blocks(int64_t T) {
-  if (T <= kOneBlockTokens) return 1;
+  if (T <= kOneClusterTokens) return 1;
   const int64_t b = (T + 31) / 32;
   return static_cast<int>(b < 152 ? b : 152);
 }
@@ -630,7 +618,8 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
                                              static_cast<int>(smem));
         if (e != cudaSuccess) return e;
       }
-      return launch_args(fn, dim3(1), kRouteThreads, smem, stream, args);
+      const int cluster = cluster_blocks(a.T);
+      return launch_args(fn, dim3(cluster), kRouteThreads, smem, stream, args, cluster);
     }
     cudaError_t e = launch_args(route_choose_fn<T>(vpl), dim3(blocks), kRouteThreads, 0, stream, args);
     if (e != cudaSuccess) return e;
