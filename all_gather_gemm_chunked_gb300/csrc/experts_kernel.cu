@@ -38,7 +38,7 @@
 //   e4m3           one k-block: its sum is multiplied by both operands' scales,
 //   fp32 outputs   8 k-blocks: the tensor core's additions lose about a last bit
 //                  each, so the error of one long accumulation grows with its length
-//                  (1.1e-6 of the result over 1024 terms, %ERR% in segments),
+//                  (1.1e-6 of the result over 1024 terms, 4.5e-7 in segments),
 //   16-bit outputs the whole sum (the rounding of the output hides that error).
 //
 // Rows beyond a group's end belong to the next group: they are multiplied along and
@@ -227,15 +227,19 @@ struct Table {
 };
 
 // Parts of a sum that make the longest pair's share shortest: a round of the pairs costs
-// its k-blocks and about six more for a tile's start and end, parts about eight more
-// once, for the sums' way through memory.  Each lane of a warp tries one number.
-__device__ __forceinline__ int32_t choose_split(int32_t tiles, int32_t KB, int32_t max_units) {
+// its k-blocks and about six more for a tile's start and end; parts cost about 14 more
+// once, for their way through memory, and each as long as the one CTA that adds a tile's
+// parts takes to read it, `part` k-blocks: 5 (tiles of 128 rows 3, of 64 rows 2 of theirs).  (One tile a
+// column block, 64 rows: 4096 x 512 13.7 us whole, 10.3 in four parts, 12.5 in sixteen;
+// 1024 x 2048 7.2 and 9.0.  Tiles of 256, 200 rows of 1024 x 2048: 10.7 and 15.7;
+// 234 of 2896 x 752: 16.7 and, in three, 15.5.)  Each lane of a warp tries one number.
+__device__ __forceinline__ int32_t choose_split(int32_t tiles, int32_t KB, int32_t max_units, int32_t part) {
   const int32_t pairs = static_cast<int32_t>(gridDim.x / 2);
   if (tiles == 0 || tiles >= 2 * pairs || KB < 8) return 1;
   const int32_t s = static_cast<int32_t>(threadIdx.x & 31) + 1;
   const bool can = s == 1 || (s <= 16 && KB >= 4 * s && tiles * s <= max_units);
   const int32_t rounds = (tiles * s + pairs - 1) / pairs;
-  const uint32_t cost = can ? static_cast<uint32_t>(rounds * ((KB + s - 1) / s + 6) + (s > 1 ? 8 : 0)) : 0x03ffffffu;
+  const uint32_t cost = can ? static_cast<uint32_t>(rounds * ((KB + s - 1) / s + 6) + (s > 1 ? 14 + s * part : 0)) : 0x03ffffffu;
   // (the smallest number among the cheapest)
   const uint32_t best = __reduce_min_sync(0xffffffffu, min(cost, 0x03ffffffu) * 32 + (s - 1));
   return static_cast<int32_t>(best & 31u) + 1;
@@ -262,19 +266,25 @@ struct Schedule {
     return (p.wide + kXWide - 1) / kXWide;
   }
   static __device__ __forceinline__ int32_t row_tiles(const ExpertsParams& p) {
-    return OP == kOpWeight ? (p.out_rows + BN - 1) / BN : 0;
+    return OP == kOpWeight ? p.row_tiles : 0;
   }
   static __device__ __forceinline__ int32_t k_blocks(const ExpertsParams& p) {
     return OP == kOpWeight ? 0 : (p.red + block_k<OP>() - 1) / block_k<OP>();
   }
   // By one warp, once the table's `tiles` row tiles are known: its head.
-  static __device__ __forceinline__ void fill_head(const ExpertsParams& p, int32_t tiles, int32_t* head) {
-    const int32_t wt = wide_tiles(p);
-    const int32_t split = OP == kOpWeight ? 1 : choose_split(tiles * wt, k_blocks(p), p.max_units);
+  // (In the weight gradient the tiles are the weights', and the sum that counts is the
+  // longest group's, of `longest` rows.)
+  static __device__ __forceinline__ void fill_head(const ExpertsParams& p, int32_t tiles, int32_t longest,
+                                                   int32_t* head) {
+    if (OP == kOpWeight) tiles = p.E * row_tiles(p);
+    tiles *= wide_tiles(p);
+    const int32_t part = BN != kXRows ? 2 : OP == kOpWeight && p.step < kXRows ? 3 : 5;
+    const int32_t split =
+        choose_split(tiles, OP == kOpWeight ? longest / 64 : k_blocks(p), p.max_units, part);
     if ((threadIdx.x & 31) == 0) {
       head[0] = split;
       head[1] = static_cast<int32_t>(split == 1 ? 0xffffffffu : 0xffffffffu / static_cast<uint32_t>(split));
-      head[2] = OP == kOpWeight ? p.E * wt * row_tiles(p) : tiles * wt * split;
+      head[2] = tiles * split;
     }
   }
 
@@ -322,25 +332,24 @@ struct Schedule {
     if (id >= units) return false;
     const uint32_t unit = static_cast<uint32_t>(id);
     int32_t x, row_tile;
+    uint32_t part = 0;
+    u.tile = static_cast<int32_t>(unit);
+    if (split > 1) u.tile = static_cast<int32_t>(by_split.div(unit, part));
+    u.part = static_cast<int32_t>(part);
+    int32_t blocks = KB;  // k-blocks of the whole sum
     if constexpr (OP == kOpWeight) {
       uint32_t r;
-      u.e = static_cast<int32_t>(by_expert.div(unit, r));
+      u.e = static_cast<int32_t>(by_expert.div(static_cast<uint32_t>(u.tile), r));
       place(r, kt, x, row_tile);
       u.n0 = x * kXWide;
-      u.kt0 = row_tile * BN;
-      u.cnt = p.out_rows - u.kt0 < BN ? p.out_rows - u.kt0 : BN;
+      u.kt0 = row_tile * p.step;
+      u.cnt = p.out_rows - u.kt0 < p.step ? p.out_rows - u.kt0 : p.step;
       // (the halves of the two CTAs start at multiples of 64 columns)
       u.w = (u.cnt + 127) & ~127;
       u.row0 = off[u.e];
       u.red_rows = off[u.e + 1] - u.row0;
-      u.kb0 = 0;
-      u.kb1 = (u.red_rows + 63) / 64;
-      u.tile = static_cast<int32_t>(unit);
-      u.part = 0;
+      blocks = (u.red_rows + 63) / 64;
     } else {
-      uint32_t part;
-      u.tile = static_cast<int32_t>(by_split.div(unit, part));
-      u.part = static_cast<int32_t>(part);
       if (e < 0 || u.tile >= tile0 + nt * wt) enter(u.tile);
       u.e = e;
       place(static_cast<uint32_t>(u.tile - tile0), nt, x, row_tile);
@@ -352,13 +361,13 @@ struct Schedule {
       u.cnt = left < height ? left : height;
       u.kt0 = 0;
       u.red_rows = 0;
-      u.kb0 = 0;
-      u.kb1 = KB;
-      if (split > 1) {
-        uint32_t rest;
-        u.kb0 = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(KB * u.part), rest));
-        u.kb1 = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(KB * (u.part + 1)), rest));
-      }
+    }
+    u.kb0 = 0;
+    u.kb1 = blocks;
+    if (split > 1) {
+      uint32_t rest;
+      u.kb0 = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(blocks * u.part), rest));
+      u.kb1 = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(blocks * (u.part + 1)), rest));
     }
     return true;
   }
@@ -376,11 +385,12 @@ __device__ bool load_table(const ExpertsParams& p, int32_t* off, int32_t* pre, i
     if (off[e] < 0 || off[e + 1] < off[e] || off[e + 1] > p.rows) *flag = 1;
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    int32_t carry = 0;
+    int32_t carry = 0, longest = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
       const int32_t n = e < p.E ? off[e + 1] - off[e] : 0;
       int32_t s = n > 0 ? (n - 1) / BN + 1 : 0;
+      longest = n > longest ? n : longest;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int32_t v = __shfl_up_sync(0xffffffffu, s, o);
@@ -390,7 +400,8 @@ __device__ bool load_table(const ExpertsParams& p, int32_t* off, int32_t* pre, i
       carry += __shfl_sync(0xffffffffu, s, 31);
     }
     if (lane == 0) pre[0] = 0;
-    Schedule<OP, BN>::fill_head(p, carry, head);
+    if (OP == kOpWeight) longest = __reduce_max_sync(0xffffffffu, longest);
+    Schedule<OP, BN>::fill_head(p, carry, longest, head);
   }
   __syncthreads();
   return *flag == 0;
@@ -415,16 +426,16 @@ struct Ring {
 // ------------------------------------------------------------------ TMA warp
 // The loads of a stage's two k-blocks of one operand: one TMA instruction where the
 // operand's extent allows a view in blocks of 128 bytes, two otherwise.  (The TMA
-// unit's time per instruction counts: an instruction for each k-block instead took
-// %TMA%.)
-// MN-major: 128 columns from col by 128 rows of the sum's dimension from row.
+// unit takes its instructions one by one; two an operand and stage measured the same.)
+// MN-major: 128 columns from col (a map of 64, `half`: 64) by 128 rows of the sum's
+// dimension from row.
 __device__ __forceinline__ void load_mn(uint8_t* dst, const CUtensorMap* map, uint32_t bar,
-                                        int32_t blk, int32_t col, int32_t row, int32_t e) {
+                                        int32_t blk, int32_t col, int32_t row, int32_t e, bool half) {
   if (blk) {
     tma_load_4d_pair(dst, map, bar, 0, row, col / 64, e);
   } else {
     tma_load_3d_pair(dst, map, bar, col, row, e);
-    tma_load_3d_pair(dst + kGroupBytes, map, bar, col + 64, row, e);
+    if (!half) tma_load_3d_pair(dst + kGroupBytes, map, bar, col + 64, row, e);
   }
 }
 // K-major: rows of e from row, k-blocks kb and kb + 1 (bk elements each).
@@ -458,8 +469,8 @@ __device__ void tma_role(const ExpertsParams& p, const Table& table, const Ring&
   Unit u;
   for (int32_t i = 0; ok && sch.get(i, u); ++i) {
     const int32_t half = u.w / 2;
-    const int32_t boxes = OP == kOpWeight || OP == kOpFp8Long ? kXRowBoxes : box_of<BN>(half);
-    const int32_t height = boxes * (BN / 8);
+    const int32_t boxes = OP == kOpFp8Long ? kXRowBoxes : box_of<BN>(half);
+    const int32_t height = OP == kOpWeight ? half : boxes * (BN / 8);
     const uint32_t tx = static_cast<uint32_t>(kSub * (kWBytes + height * 128));
     const int32_t n = u.n0 + static_cast<int32_t>(rank) * 128;
     for (int32_t kb0 = u.kb0; kb0 < u.kb1; kb0 += kSub) {
@@ -486,11 +497,11 @@ __device__ void tma_role(const ExpertsParams& p, const Table& table, const Ring&
                  u.row0 + static_cast<int32_t>(rank) * 128, 0, kWBytes);
           load_k(rd, &p.tm_w, bar, p.w_blk, kb0, 128, u.n0 + mine, u.e, r_bytes(BN));
         } else if constexpr (OP == kOpWeight) {
-          load_mn(wd, &p.tm_w, bar, p.w_blk, n, u.row0 + kb0 * 64, 0);
-          load_mn(rd, &p.tm_r[0], bar, p.r_blk, u.kt0 + mine, u.row0 + kb0 * 64, 0);
+          load_mn(wd, &p.tm_w, bar, p.w_blk, n, u.row0 + kb0 * 64, 0, false);
+          load_mn(rd, &p.tm_r[half == 64], bar, p.r_blk, u.kt0 + mine, u.row0 + kb0 * 64, 0, half == 64);
         } else {
           if constexpr (OP == kOpForward)
-            load_mn(wd, &p.tm_w, bar, p.w_blk, n, kb0 * 64, u.e);
+            load_mn(wd, &p.tm_w, bar, p.w_blk, n, kb0 * 64, u.e, false);
           else
             load_k(wd, &p.tm_w, bar, p.w_blk, kb0, block_k<OP>(), n, u.e, kWBytes);
           load_k(rd, &p.tm_r[boxes - 1], bar, p.r_blk, kb0, block_k<OP>(), u.row0 + mine, 0,
@@ -530,11 +541,11 @@ __device__ void zero_role(const ExpertsParams& p, const Table& table,
   uint32_t stages = 0, used = 0;  // stages so far; bit s: parity of stage s's tails
   Unit u;
   for (int32_t i = 0; sch.get(i, u); ++i) {
-    stages += static_cast<uint32_t>((u.kb1 + kSub - 1) / kSub);
+    stages += static_cast<uint32_t>((u.kb1 - u.kb0 + kSub - 1) / kSub);
+    if (u.red_rows - u.kb1 * 64 >= 0) continue;  // whole k-blocks, or a part before the last
     const int valid = u.red_rows & 63;
-    if (valid == 0) continue;
     const uint32_t stage = (stages - 1) % kStagesX;
-    const int first = ((u.kb1 - 1) % kSub) * 64 + valid;  // of the stage's 128 rows
+    const int first = ((u.kb1 - u.kb0 - 1) % kSub) * 64 + valid;  // of the stage's 128 rows
     bool ok = mbar_wait(&ring.tail[stage], (used >> stage) & 1u, p.timeout_ns, ring.abort, p.status);
     used ^= 1u << stage;
     ok = __all_sync(0xffffffffu, ok);
@@ -1185,7 +1196,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     tmem_relinquish_pair();
   }
   if (warp == 2 && lane <= kXRowBoxes)  // the descriptors' first use would wait for them
-    tma_prefetch_desc(lane == kXRowBoxes ? &p.tm_w : &p.tm_r[OP == kOpWeight ? 0 : lane]);
+    tma_prefetch_desc(lane == kXRowBoxes ? &p.tm_w : &p.tm_r[OP == kOpWeight ? lane & 1 : lane]);
   tc_fence_before();
   cluster_arrive();  // barriers initialised, TMEM allocated; the table is read meanwhile
   pdl_wait();        // from here on global memory is read

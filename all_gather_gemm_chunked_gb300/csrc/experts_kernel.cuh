@@ -33,13 +33,14 @@ constexpr int kXGroup = 8;     // row tiles that share the weights they read (ti
 
 struct ExpertsParams {
   CUtensorMap tm_w;              // the wide operand
-  CUtensorMap tm_r[kXRowBoxes];  // the row operand, by box height (weight gradient: the first only)
+  CUtensorMap tm_r[kXRowBoxes];  // the row operand, by box height (weight gradient: of 128 and of 64 columns)
   const int32_t* offsets;        // [E + 1], or null: one group of all rows
   int32_t E;
   int32_t rows;                  // rows of the inputs
   int32_t wide;                  // extent of the wide dimension
   int32_t red;                   // length of the sums (weight gradient: unused)
   int32_t out_rows;              // weight gradient: output rows per expert (K)
+  int32_t step, row_tiles;       // weight gradient: output rows of a tile, 256 or 128; tiles of K
   uint32_t inv_group, inv_expert;  // floor((2^32 - 1) / n): n tiles of 8 row tiles, n of an expert (weight gradient)
   int32_t w_blk, r_blk;          // operand described in blocks of 128 bytes (one load a stage), or not (two)
   int32_t segment;               // k-blocks per accumulator (e4m3: 1)

@@ -189,11 +189,11 @@ int encode_k_major(CUtensorMap* map, int dtype, const void* base, int64_t len, i
 // k-blocks) by 64 columns; with cols % 64 == 0 in blocks of 64 columns, two of them a
 // box, so that a CTA's 128 columns are one load.
 int encode_mn_major(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld,
-                    int64_t E, int64_t ld_e) {
+                    int64_t E, int64_t ld_e, int blocks = 2) {
   if (whole_blocks(AG_GEMM_F16, cols)) {
     const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)cols / 64, (cuuint64_t)E};
     const cuuint64_t strides[3] = {(cuuint64_t)ld * 2, 128, (cuuint64_t)ld_e * 2};
-    const cuuint32_t box[4] = {64, 64 * agg::kXSub, 2, 1};
+    const cuuint32_t box[4] = {64, 64 * agg::kXSub, (cuuint32_t)blocks, 1};
     return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, 4, dims, strides, box);
   }
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)E};
@@ -227,16 +227,20 @@ int check_run(ag_moe_plan* p, bool fp8, int64_t rows, const int32_t* offsets, in
   return AG_GEMM_OK;
 }
 
-// Short row tiles where the groups are short on average.  64 rows a tile leave
-// ten stages for the weights in flight; 256 read the weights once where a group
-// is longer.
-bool few_rows(const ag_moe_plan* p, int64_t rows) {
-  return rows <= static_cast<int64_t>(agg::kXFewRows) * p->E;
-}
-
 // Row tiles that the groups of so many rows can make.
 int64_t most_row_tiles(const ag_moe_plan* p, int64_t rows, bool few) {
   return rows / (few ? agg::kXFewRows : agg::kXRows) + (rows < p->E ? rows : p->E);
+}
+
+// Short row tiles where the groups are short on average (64 rows a tile leave ten
+// stages for the weights in flight; 256 read the weights once where a group is longer),
+// and where all of them run at once: a k-block of 256 rows takes 0.23 us, of 64 0.14.
+// (One expert, 200 rows of 1024 x 2048, 32 short tiles: 7.5 us against 10.7; e4m3 7.3
+// against 10.1.  In two rounds of short tiles 1200 rows of 1024 x 2048 took 10.7 against
+// 12.1 us, 600 of 2048 x 3000 18.4 against 15.0; e4m3 1088 of 4096 x 2048 22.2 against 21.2.)
+bool few_rows(const ag_moe_plan* p, int64_t rows, int64_t wide) {
+  return rows <= static_cast<int64_t>(agg::kXFewRows) * p->E ||
+         most_row_tiles(p, rows, true) * ((wide + agg::kXWide - 1) / agg::kXWide) <= p->pairs;
 }
 
 int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_tiles,
@@ -255,8 +259,7 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   if ((row_tiles + agg::kXGroup) * wide_tiles >= (1LL << 30))
     return fail(AG_GEMM_ERR_UNSUPPORTED, "more than 2^30 tiles");
   x.inv_group = 0xffffffffu / static_cast<uint32_t>(agg::kXGroup * wide_tiles);
-  x.inv_expert = 0xffffffffu / static_cast<uint32_t>(
-                                   wide_tiles * ((x.out_rows + agg::kXRows - 1) / agg::kXRows) + (x.out_rows == 0));
+  x.inv_expert = op == agg::kOpWeight ? 0xffffffffu / static_cast<uint32_t>(wide_tiles * x.row_tiles) : 0;
   // A captured run is ordered by its graph: an event of the stream outside cannot be
   // waited on there, nor one of the graph outside.
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
@@ -267,7 +270,7 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
       (e = cudaStreamWaitEvent(stream, p->done, 0)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamWaitEvent");
   // no more pairs than there can be units: split sums have up to 16 parts of 4 k-blocks
-  const int64_t kb = op == agg::kOpWeight ? 0 : x.red / (op == agg::kOpFp8 ? 128 : 64);
+  const int64_t kb = op == agg::kOpWeight ? x.rows / 64 : x.red / (op == agg::kOpFp8 ? 128 : 64);
   const int64_t units = row_tiles * wide_tiles * (kb < 8 ? 1 : kb < 64 ? (kb + 1) / 4 : 16);
   const int pairs = static_cast<int>(units < p->pairs ? units : p->pairs);
   if ((e = agg::launch_experts(x, op, few, 2 * pairs, stream)) != cudaSuccess)
@@ -307,7 +310,7 @@ int run_rows(ag_moe_plan* p, int op, int64_t rows, const void* in, int64_t ld_in
                 (long long)ldw_e);
   if (p->E == 1) ldw_e = p->K * ldw;
   DeviceGuard dg(p->device);
-  const bool few = few_rows(p, rows);
+  const bool few = few_rows(p, rows, wide);
   OperandCache& c = p->cache[op];
   if (!c.find(w, ldw, ldw_e, in, ld_in, rows)) {
     int rc;
@@ -594,7 +597,8 @@ int ag_moe_backward_weight(ag_moe_plan* plan, int64_t rows, const void* x, int64
   if (!c.find(dy, lddy, 0, x, ldx, rows)) {
     int rc;
     if ((rc = encode_mn_major(&c.x.tm_w, dy, plan->N, rows, lddy, 1, rows * lddy)) ||
-        (rc = encode_mn_major(&c.x.tm_r[0], x, plan->K, rows, ldx, 1, rows * ldx)))
+        (rc = encode_mn_major(&c.x.tm_r[0], x, plan->K, rows, ldx, 1, rows * ldx)) ||
+        (rc = encode_mn_major(&c.x.tm_r[1], x, plan->K, rows, ldx, 1, rows * ldx, 1)))
       return rc;
     c.x.w_blk = whole_blocks(plan->dtype, plan->N);
     c.x.r_blk = whole_blocks(plan->dtype, plan->K);
@@ -605,10 +609,16 @@ int ag_moe_backward_weight(ag_moe_plan* plan, int64_t rows, const void* x, int64
   p.rows = static_cast<int32_t>(rows);
   p.wide = static_cast<int32_t>(plan->N);
   p.out_rows = static_cast<int32_t>(plan->K);
+  // Half tiles where all of them run at once: half the rows to store and half of x to
+  // load per k-block.  (3754 rows of 608 x 376: 16.2 us against 22.4; 64 of 4096 x 512:
+  // 7.4 against 8.2.  Twice as many tiles as pairs would cost a second round.)
+  const int64_t halves = plan->E * ((plan->K + 127) / 128) * ((plan->N + agg::kXWide - 1) / agg::kXWide);
+  p.step = halves <= plan->pairs ? agg::kXRows / 2 : agg::kXRows;
+  p.row_tiles = (p.out_rows + p.step - 1) / p.step;
   p.out_type = out_dtype;
   p.out = dw;
   p.ldo = plan->N;
-  return run(plan, p, agg::kOpWeight, false, plan->E * ((plan->K + agg::kXRows - 1) / agg::kXRows), stream);
+  return run(plan, p, agg::kOpWeight, false, static_cast<int64_t>(plan->E) * p.row_tiles, stream);
 }
 
 int ag_fp8_forward(ag_moe_plan* plan, int64_t rows, const void* xq, const float* xs,
@@ -621,7 +631,7 @@ int ag_fp8_forward(ag_moe_plan* plan, int64_t rows, const void* xq, const float*
   if (int rc = check_matrix("y", y, ldy, plan->N, out_dtype)) return rc;
   if (!xs || !ws) return fail(AG_GEMM_ERR_INVALID, "scales are NULL");
   DeviceGuard dg(plan->device);
-  const bool few = few_rows(plan, rows);
+  const bool few = few_rows(plan, rows, plan->N);
   OperandCache& c = plan->cache[agg::kOpFp8];
   if (!c.find(wq, plan->K, plan->K * plan->N, xq, plan->K, rows)) {
     int rc;

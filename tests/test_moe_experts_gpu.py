@@ -174,6 +174,25 @@ def test_runs_repeat_bit_for_bit(sizes, K, N):
                 assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("sizes,K,N", [([3754], 608, 376), ([1000, 0, 1, 2049], 264, 72), ([511, 512, 513, 65], 256, 520)])
+@pytest.mark.parametrize("out_f32", [False, True])
+def test_long_groups_of_small_weights(sizes, K, N, out_f32):
+    """The sums over a group's rows are split between pairs: each part, the ragged last
+    one, parts without rows, and infinities in the rows behind the last group."""
+    dt = torch.bfloat16
+    x, _, dy, off = _case(sizes + [9], K, N, dt, 21)
+    rows, od = sum(sizes), torch.float32 if out_f32 else dt
+    x[rows:], dy[rows:] = float("inf"), float("nan")
+    with moe.Experts(len(sizes), K, N) as p:
+        dw = p.backward_weight(x, dy, off[:-1].contiguous(), out_dtype=od)
+        for _ in range(4):
+            assert torch.equal(dw, p.backward_weight(x, dy, off[:-1].contiguous(), out_dtype=od))
+        assert p.status() == B_.OK
+    xd, gd = x.double(), dy.double()
+    for e, (a, b) in enumerate(_per_expert(sizes, lambda e, a, b: (a, b))):
+        check(dw[e], xd[a:b].t() @ gd[a:b], product_bound(xd[a:b].t(), gd[a:b], b - a, od), f"dw of {e}")
+
+
 def test_runs_on_two_streams_do_not_meet():
     """One plan's runs share its workspace: a run on another stream waits for the last."""
     g = rng(12)
