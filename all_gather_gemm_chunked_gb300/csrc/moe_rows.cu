@@ -261,11 +261,18 @@ __device__ void place(const RouteArgs& a, int64_t c0, int64_t c1, int blocks, ui
     const int g = e / a.E, x = e - g * a.E;
     uint32_t all = 0, own = 0;
     if (g < groups)
-#pragma unroll 20
-      for (int b = g; b < blocks; b += groups) {
-        const uint32_t c = static_cast<uint32_t>(a.counts[static_cast<int64_t>(b) * a.E + x]);
-        all += c;
-        if (b < static_cast<int>(blockIdx.x)) own += c;
+      for (int b0 = g; b0 < blocks; b0 += 8 * groups) {
+        uint32_t c[8];  // eight loads in flight, whatever is left
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int b = b0 + i * groups;
+          c[i] = b < blocks ? static_cast<uint32_t>(__ldcg(a.counts + b * a.E + x)) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          all += c[i];
+          if (b0 + i * groups < static_cast<int>(blockIdx.x)) own += c[i];
+        }
       }
     // integer additions: the same in any order
     if (all) atomicAdd(&base[x], all);
@@ -339,7 +346,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_one_kernel(const RouteArg
 }
 
 // More: one kernel chooses and counts the choices of each block's tokens, the
-// next places them.
+// next places them.  Warps take tokens in pairs (one each cost as much as two).
+// (2048 tokens of 64 experts, k 4: 6.9 us; 16384 of 256, k 8: 20.7 us.)
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
   pdl_wait();
@@ -348,11 +356,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
   for (int e = threadIdx.x; e < a.E; e += kRouteThreads) cnt[e] = 0;
   __syncthreads();
   const Share blk = share_of(0, a.T, blockIdx.x, gridDim.x);
-  const Share own = share_of(blk.t0, blk.t1, warp, kRouteWarps);
   constexpr int kTokens = tokens_of(VPL);
-  for (int64_t t = own.t0; t < own.t1; t += kTokens) {
+  for (int64_t t = blk.t0 + warp * kTokens; t < blk.t1; t += kRouteWarps * kTokens) {
     int chosen[kTokens];
-    choose<T, VPL>(a, t, own.t1, lane, chosen);
+    choose<T, VPL>(a, t, blk.t1, lane, chosen);
 #pragma unroll
     for (int n = 0; n < kTokens; ++n)
       if (chosen[n] >= 0) atomicAdd(&cnt[chosen[n]], 1u);  // (integer counts: any order)
@@ -591,10 +598,11 @@ int values_per_lane(int E) { return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E
 
 }  // namespace
 
-// One cluster serves as many tokens as its warps take in one step each, two tokens a
-// warp; beyond that blocks of at least 32 tokens, one per SM at most.
-// (64 experts, k 4: 256 tokens 7.1 us against 7.6 by two kernels, 384 tokens 8.2
-// against 7.6; 256 experts, k 8: 11.4 against 12.3, 15.1 against 12.7.)
+// One cluster serves up to 256 tokens; beyond that blocks of at least 32 tokens, sixteen
+// warps' pairs, one block per SM at most.  (64 experts, k 4: 256 tokens 5.9 us, 6.5 by
+// two kernels, 384 tokens 7.0 and 6.6; 256 experts, k 8: 192 tokens 8.6 and 9.1, 256
+// tokens 10.0 and 9.2; 8 experts, k 2: 256 tokens 4.3 and 6.0.  Blocks of 16 tokens
+// took 7.8 us against 7.2 for 2048 tokens of 64 experts, of 64 tokens 7.7.)
 constexpr int64_t kOneClusterTokens = 256;
 // Its blocks: one for as few tokens as it takes, else eight.
 // (64 experts, k 4: 16 tokens 3.7 us by one block, 4.0 by eight, 32 tokens 4.1 and 4.0;
