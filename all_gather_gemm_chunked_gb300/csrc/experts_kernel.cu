@@ -227,19 +227,22 @@ struct Table {
 };
 
 // Parts of a sum that make the longest pair's share shortest: a round of the pairs costs
-// its k-blocks and about six more for a tile's start and end; parts cost about 14 more
-// once, for their way through memory, and each as long as the one CTA that adds a tile's
-// parts takes to read it, `part` k-blocks: 5 (tiles of 128 rows 3, of 64 rows 2 of theirs).  (One tile a
-// column block, 64 rows: 4096 x 512 13.7 us whole, 10.3 in four parts, 12.5 in sixteen;
-// 1024 x 2048 7.2 and 9.0.  Tiles of 256, 200 rows of 1024 x 2048: 10.7 and 15.7;
-// 234 of 2896 x 752: 16.7 and, in three, 15.5.)  Each lane of a warp tries one number.
-__device__ __forceinline__ int32_t choose_split(int32_t tiles, int32_t KB, int32_t max_units, int32_t part) {
+// its k-blocks and about six more for a tile's start and end; with parts `once` more, for
+// their way through memory, and at the end each part as long as the one CTA that adds a
+// tile's parts takes to read it, `part` k-blocks.  (Rows of 64, one expert, bf16: 4096 x
+// 512 13.7 us whole, 10.3 in four parts, 12.5 in sixteen; 1024 x 2048 7.2 and, in four,
+// 9.0.  Tiles of 256: 200 rows of 1024 x 2048 10.7 and 15.7; 234 of 2896 x 752 16.7 and,
+// in three, 15.5.  e4m3: 1 row of 3472 x 952 10.5 and, in four, 9.1; 64 of 16384 x 7168
+// 28.2 in two parts and one round, 34.4 in five parts and two rounds.)  Each lane of a
+// warp tries one number.
+__device__ __forceinline__ int32_t choose_split(int32_t tiles, int32_t KB, int32_t max_units, int32_t once, int32_t part) {
   const int32_t pairs = static_cast<int32_t>(gridDim.x / 2);
   if (tiles == 0 || tiles >= 2 * pairs || KB < 8) return 1;
   const int32_t s = static_cast<int32_t>(threadIdx.x & 31) + 1;
   const bool can = s == 1 || (s <= 16 && KB >= 4 * s && tiles * s <= max_units);
   const int32_t rounds = (tiles * s + pairs - 1) / pairs;
-  const uint32_t cost = can ? static_cast<uint32_t>(rounds * ((KB + s - 1) / s + 6) + (s > 1 ? 14 + s * part : 0)) : 0x03ffffffu;
+  const uint32_t cost = can ? static_cast<uint32_t>(rounds * ((KB + s - 1) / s + 6 + (s > 1 ? once : 0)) + (s > 1 ? s * part : 0))
+                            : 0x03ffffffu;
   // (the smallest number among the cheapest)
   const uint32_t best = __reduce_min_sync(0xffffffffu, min(cost, 0x03ffffffu) * 32 + (s - 1));
   return static_cast<int32_t>(best & 31u) + 1;
@@ -278,9 +281,10 @@ struct Schedule {
                                                    int32_t* head) {
     if (OP == kOpWeight) tiles = p.E * row_tiles(p);
     tiles *= wide_tiles(p);
-    const int32_t part = BN != kXRows ? 2 : OP == kOpWeight && p.step < kXRows ? 3 : 5;
-    const int32_t split =
-        choose_split(tiles, OP == kOpWeight ? longest / 64 : k_blocks(p), p.max_units, part);
+    const int32_t part = OP == kOpFp8 ? 1 : OP == kOpFp8Long ? 3 : BN != kXRows ? 2
+                         : OP == kOpWeight && p.step < kXRows ? 3 : 5;
+    const int32_t split = choose_split(tiles, OP == kOpWeight ? longest / 64 : k_blocks(p), p.max_units,
+                                       is_fp8(OP) ? 9 : 14, part);
     if ((threadIdx.x & 31) == 0) {
       head[0] = split;
       head[1] = static_cast<int32_t>(split == 1 ? 0xffffffffu : 0xffffffffu / static_cast<uint32_t>(split));
@@ -1047,24 +1051,30 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
         if constexpr (OP == kOpFp8) {
           // four k-blocks side by side: this warp's columns of each, times their scales
           const float* scale = ring.scales + slot * (kFewBlocks * BN) + c_first;
+          // (two at a time: a wait for the loads costs as much as the sums of a k-block)
 #pragma unroll
-          for (int j = 0; j < kFewBlocks; ++j) {
-            if (j < left) {
-              uint32_t v[kCols];
-              if (n8 == kCols / 8)
-                tmem_ld16(from + j * BN, v);
-              else
-                tmem_ld8(from + j * BN, *reinterpret_cast<uint32_t(*)[8]>(v));
+          for (int j0 = 0; j0 < kFewBlocks; j0 += 2) {
+            if (j0 < left) {
+              uint32_t v[2][kCols];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                if (n8 == kCols / 8)
+                  tmem_ld16(from + (j0 + j) * BN, v[j]);
+                else
+                  tmem_ld8(from + (j0 + j) * BN, *reinterpret_cast<uint32_t(*)[8]>(v[j]));
+              }
               tmem_ld_wait();
 #pragma unroll
-              for (int q = 0; q < kCols; q += 4)
-                if (q < n8 * 8) {
-                  const float4 f = *reinterpret_cast<const float4*>(scale + j * BN + q);
-                  sums[q] = fmaf(__uint_as_float(v[q]), f.x, sums[q]);
-                  sums[q + 1] = fmaf(__uint_as_float(v[q + 1]), f.y, sums[q + 1]);
-                  sums[q + 2] = fmaf(__uint_as_float(v[q + 2]), f.z, sums[q + 2]);
-                  sums[q + 3] = fmaf(__uint_as_float(v[q + 3]), f.w, sums[q + 3]);
-                }
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int q = 0; q < kCols; q += 4)
+                  if (q < n8 * 8 && j0 + j < left) {
+                    const float4 f = *reinterpret_cast<const float4*>(scale + (j0 + j) * BN + q);
+                    sums[q] = fmaf(__uint_as_float(v[j][q]), f.x, sums[q]);
+                    sums[q + 1] = fmaf(__uint_as_float(v[j][q + 1]), f.y, sums[q + 1]);
+                    sums[q + 2] = fmaf(__uint_as_float(v[j][q + 2]), f.z, sums[q + 2]);
+                    sums[q + 3] = fmaf(__uint_as_float(v[j][q + 3]), f.w, sums[q + 3]);
+                  }
             }
           }
           tc_fence_before();
