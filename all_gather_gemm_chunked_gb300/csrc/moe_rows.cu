@@ -427,45 +427,86 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteArgs a,
 }
 
 // ------------------------------------------------------------------ rows
-constexpr int kRowThreads = 256;
+constexpr int kRowLog = 8, kRowThreads = 1 << kRowLog;
 
-// One block per row of out and kRowThreads * V columns.
-template <typename T, int V>
-__global__ void __launch_bounds__(kRowThreads) gather_kernel(int64_t T_, int k, int64_t H,
+// A thread moves pieces of V elements, a row's threads apart: of 16 bytes, or where rows
+// are not 16-byte aligned single elements, several of them, so that as many bytes are in
+// flight.  (8192 tokens, k 4, H 4096, bf16: aligned rows combine in 52 us, their gradient
+// takes 92, gather 66; with odd pitches 81, 123 and 97, one element a thread 182, 220 and
+// 528.)
+constexpr int kPieces = 4;
+constexpr int kGatherPieces = 8, kGatherVec = 4;  // (gather with one 16-byte piece 80 us)
+// Short rows share a block, each with the warps that it fills: a block a row is bound by
+// the time a block lives.  (5317 tokens, k 3, H 118: combine 3.8 us against 6.7, gradient
+// 6.4 and 12.6, gather 5.5 and 17.0; 8192 tokens, k 8, H 1000: gradient 50 and 66.  Rows
+// that fill a block keep their number of threads as a constant: as a variable it cost
+// combine registers, 60 us against 52 for 8192 tokens, k 4, H 4096.)
+struct RowShape {
+  int log;       // threads of a row, a power of two from 32 on
+  unsigned x, y; // blocks over the rows, blocks over a row
+};
+RowShape row_shape(int64_t rows, int64_t H, int per_thread) {
+  RowShape s{kRowLog, 0, 0};
+  while (s.log > 5 && (H + per_thread - 1) / per_thread <= (1 << (s.log - 1))) --s.log;
+  const int64_t per = kRowThreads >> s.log, span = static_cast<int64_t>(per_thread) << s.log;
+  s.x = static_cast<unsigned>((rows + per - 1) / per);
+  s.y = static_cast<unsigned>((H + span - 1) / span);
+  return s;
+}
+
+// 2^log threads per row of out and as many times V * N columns.  (32768 rows of 4096: 66 us,
+// 5.1 TB/s of reads and writes.)
+template <typename T, int V, int N, bool kShort>
+__global__ void __launch_bounds__(kRowThreads) gather_kernel(int64_t T_, int k, int64_t H, int log_,
                                                              const T* __restrict__ x, int64_t ldx,
                                                              const int32_t* __restrict__ order,
                                                              T* __restrict__ out) {
   pdl_enter();
-  const int64_t s = blockIdx.x;
-  const int64_t c = (static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x) * V;
-  if (c >= H) return;
+  const int log = kShort ? log_ : kRowLog, step = V << log;
+  const int64_t s = static_cast<int64_t>(blockIdx.x) * (kRowThreads >> log) + (threadIdx.x >> log);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * step * N + (threadIdx.x & ((1 << log) - 1)) * V;
+  if (c0 >= H || s >= T_ * k) return;
   const int32_t o = order[s];
   const int64_t t = o / k;
-  float f[V] = {};
-  if (o >= 0 && t < T_) load_elems<T, V>(x + t * ldx + c, f);
-  store_elems<T, V>(out + s * H + c, f);
+  const bool in = o >= 0 && t < T_;
+  Raw<T, V> r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t c = c0 + i * step;
+    if (in && c < H) r[i].load(x + t * ldx + c);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t c = c0 + i * step;
+    float f[V] = {};
+    if (in) r[i].get(f);
+    if (c < H) store_elems<T, V>(out + s * H + c, f);
+  }
 }
 
-// One block per token and kRowThreads * V columns: the k rows are read with four loads
-// in flight per thread and summed in registers in the order of j.  Bound by the bytes in
-// flight (a token's slots come first, then its rows): the loads wait as they came and
-// six blocks share an SM (8192 tokens, k 4, H 4096: 51 us; as floats, four blocks, 92).
-template <typename T, int V>
-__global__ void __launch_bounds__(kRowThreads, 6) combine_kernel(int64_t T_, int k, int64_t H,
+// 2^log threads per token and as many times V * N columns: the k rows are read with four
+// loads a piece in flight per thread and summed in registers in the order of j.  Bound by
+// the bytes in flight (a token's slots come first, then its rows): the loads wait as they
+// came and six blocks share an SM (8192 tokens, k 4, H 4096: 51 us, 6.6 TB/s; as floats,
+// four blocks, 92).
+template <typename T, int V, int N, bool kShort>
+__global__ void __launch_bounds__(kRowThreads, kShort ? 5 : 6) combine_kernel(int64_t T_, int k, int64_t H, int log_,
                                                                  const T* __restrict__ y, int64_t ldy,
                                                                  const int32_t* __restrict__ slots,
                                                                  const float* __restrict__ weights,
                                                                  T* __restrict__ out) {
   pdl_enter();
-  const int64_t t = blockIdx.x;
+  const int log = kShort ? log_ : kRowLog, step = V << log;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRowThreads >> log) + (threadIdx.x >> log);
   const int S = static_cast<int>(T_ * k);
-  const int64_t c = (static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x) * V;
-  if (c >= H) return;
-  float acc[V] = {};
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * step * N + (threadIdx.x & ((1 << log) - 1)) * V;
+  if (c >= H || t >= T_) return;
+  const int64_t left = H - c;  // pieces from there on are outside
+  float acc[N][V] = {};
   slots += t * k;
   if (weights) weights += t * k;
   for (int j0 = 0; j0 < k; j0 += 4) {
-    Raw<T, V> r[4];
+    Raw<T, V> r[4][N];
     int s[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -474,62 +515,83 @@ __global__ void __launch_bounds__(kRowThreads, 6) combine_kernel(int64_t T_, int
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (s[u] >= 0) r[u].load(y + s[u] * ldy + c);
+      if (s[u] >= 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (i * step < left) r[u][i].load(y + s[u] * ldy + c + i * step);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (s[u] >= 0) {
         const float w = weights ? weights[j0 + u] : 1.0f;
-        float f[V];
-        r[u].get(f);
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = fmaf(w, f[v], acc[v]);
+        for (int i = 0; i < N; ++i) {
+          float f[V];
+          r[u][i].get(f);
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[i][v] = fmaf(w, f[v], acc[i][v]);
+        }
       }
   }
-  store_elems<T, V>(out + t * H + c, acc);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i * step < left) store_elems<T, V>(out + t * H + c + i * step, acc[i]);
 }
 
-// One block per token: dy rows and, over the whole row, the dot products.  Four
-// choices at a time; dout is read again for the next four.
-template <typename T, int V>
+// 2^log threads per token: dy rows and, over the whole row, the dot products.  Four
+// choices at a time; dout is read again for the next four.  (8192 tokens, k 4, H 4096:
+// 90 us, 6.7 TB/s.)
+template <typename T, int V, int N, bool kShort>
 __global__ void __launch_bounds__(kRowThreads, 4) combine_backward_kernel(
-    int64_t T_, int k, int64_t H, const T* __restrict__ dout, int64_t ldd,
+    int64_t T_, int k, int64_t H, int log_, const T* __restrict__ dout, int64_t ldd,
     const T* __restrict__ y, int64_t ldy, const int32_t* __restrict__ slots,
     const float* __restrict__ weights, const int32_t* __restrict__ offsets_end,
     T* __restrict__ dy, float* __restrict__ dweights) {
   pdl_enter();
   __shared__ float part[kRowThreads / 32][4];
-  const int64_t t = blockIdx.x, S = T_ * k;
+  const int log = kShort ? log_ : kRowLog, step = V << log;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int thread = threadIdx.x & ((1 << log) - 1);  // of the token
+  const int64_t per = kRowThreads >> log, S = T_ * k;
+  const int64_t t = blockIdx.x * per + (threadIdx.x >> log);
   for (int j0 = 0; j0 < k; j0 += 4) {
     int64_t s[4];
     float w[4], dot[4] = {};
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int j = j0 + u;
-      s[u] = j < k ? slots[t * k + j] : -1;
+      s[u] = j < k && t < T_ ? slots[t * k + j] : -1;
       if (s[u] >= S) s[u] = -1;
       w[u] = s[u] >= 0 ? weights[t * k + j] : 0.0f;
     }
-    for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < H; c += kRowThreads * V) {
-      Raw<T, V> r[4], rg;
-      rg.load(dout + t * ldd + c);
+    for (int64_t c = thread * V; c < H && t < T_; c += step * N) {
+      Raw<T, V> r[4][N], rg[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i * step < H - c) rg[i].load(dout + t * ldd + c + i * step);
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (s[u] >= 0) r[u].load(y + s[u] * ldy + c);
-      float g[V];
-      rg.get(g);
+        if (s[u] >= 0)
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (s[u] >= 0) {
-          float d[V], f[V];
-          r[u].get(f);
+          for (int i = 0; i < N; ++i)
+            if (i * step < H - c) r[u][i].load(y + s[u] * ldy + c + i * step);
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            dot[u] = fmaf(g[v], f[v], dot[u]);
-            d[v] = w[u] * g[v];
+      for (int i = 0; i < N; ++i) {
+        if (i * step >= H - c) break;
+        float g[V];
+        rg[i].get(g);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (s[u] >= 0) {
+            float d[V], f[V];
+            r[u][i].get(f);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              dot[u] = fmaf(g[v], f[v], dot[u]);
+              d[v] = w[u] * g[v];
+            }
+            store_elems<T, V>(dy + s[u] * H + c + i * step, d);
           }
-          store_elems<T, V>(dy + s[u] * H + c, d);
-        }
+      }
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -537,18 +599,18 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_backward_kernel(
       if (lane == 0) part[warp][u] = dot[u];
     }
     __syncthreads();
-    if (threadIdx.x < 4 && j0 + static_cast<int>(threadIdx.x) < k) {
+    if (thread < 4 && j0 + thread < k && t < T_) {
       float sum = 0.0f;
-      for (int i = 0; i < kRowThreads / 32; ++i) sum += part[i][threadIdx.x];
-      dweights[t * k + j0 + threadIdx.x] = sum;
+      for (int i = 0; i < (1 << log) / 32; ++i) sum += part[warp + i][thread];
+      dweights[t * k + j0 + thread] = sum;
     }
     __syncthreads();
   }
   if (offsets_end) {  // rows that belong to no choice
     const int64_t end = *offsets_end;
     const float zero[V] = {};
-    for (int64_t r = (end < 0 ? 0 : end) + t; r < S; r += gridDim.x)
-      for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < H; c += kRowThreads * V)
+    for (int64_t r = (end < 0 ? 0 : end) + t; r < S; r += gridDim.x * per)
+      for (int64_t c = thread * V; c < H; c += step)
         store_elems<T, V>(dy + r * H + c, zero);
   }
 }
@@ -656,14 +718,15 @@ cudaError_t launch_gather(int64_t T_, int k, int64_t H, int dtype, const void* x
   return AGG_FOR_TYPE(dtype, {
     constexpr int V = Elem<T>::kVec;
     const bool vec = H % V == 0 && aligned(x, ldx, sizeof(T)) && aligned(out, H, sizeof(T));
-    const int64_t per = kRowThreads * (vec ? V : 1);
-    const dim3 grid(static_cast<unsigned>(T_ * k), static_cast<unsigned>((H + per - 1) / per));
-    if (vec)
-      return launch(gather_kernel<T, V>, dim3(grid), kRowThreads, stream, T_, k, H, static_cast<const T*>(x),
-                                                            ldx, order, static_cast<T*>(out));
-    else
-      return launch(gather_kernel<T, 1>, dim3(grid), kRowThreads, stream, T_, k, H, static_cast<const T*>(x),
-                                                            ldx, order, static_cast<T*>(out));
+    const RowShape s = row_shape(T_ * k, H, vec ? kGatherVec * V : kGatherPieces);
+    const dim3 grid(s.x, s.y);
+    auto go = [&](auto kernel) {
+      return launch(kernel, grid, kRowThreads, stream, T_, k, H, s.log, static_cast<const T*>(x), ldx, order,
+                    static_cast<T*>(out));
+    };
+    if (s.log == kRowLog)
+      return vec ? go(gather_kernel<T, V, kGatherVec, false>) : go(gather_kernel<T, 1, kGatherPieces, false>);
+    return vec ? go(gather_kernel<T, V, kGatherVec, true>) : go(gather_kernel<T, 1, kGatherPieces, true>);
   });
 }
 
@@ -674,14 +737,14 @@ cudaError_t launch_combine(int64_t T_, int k, int64_t H, int dtype, const void* 
   return AGG_FOR_TYPE(dtype, {
     constexpr int V = Elem<T>::kVec;
     const bool vec = H % V == 0 && aligned(y, ldy, sizeof(T)) && aligned(out, H, sizeof(T));
-    const int64_t per = kRowThreads * (vec ? V : 1);
-    const dim3 grid(static_cast<unsigned>(T_), static_cast<unsigned>((H + per - 1) / per));
-    if (vec)
-      return launch(combine_kernel<T, V>, dim3(grid), kRowThreads, stream, 
-          T_, k, H, static_cast<const T*>(y), ldy, slots, weights, static_cast<T*>(out));
-    else
-      return launch(combine_kernel<T, 1>, dim3(grid), kRowThreads, stream, 
-          T_, k, H, static_cast<const T*>(y), ldy, slots, weights, static_cast<T*>(out));
+    const RowShape s = row_shape(T_, H, vec ? V : kPieces);
+    const dim3 grid(s.x, s.y);
+    auto go = [&](auto kernel) {
+      return launch(kernel, grid, kRowThreads, stream, T_, k, H, s.log, static_cast<const T*>(y), ldy, slots,
+                    weights, static_cast<T*>(out));
+    };
+    if (s.log == kRowLog) return vec ? go(combine_kernel<T, V, 1, false>) : go(combine_kernel<T, 1, kPieces, false>);
+    return vec ? go(combine_kernel<T, V, 1, true>) : go(combine_kernel<T, 1, kPieces, true>);
   });
 }
 
@@ -694,14 +757,14 @@ cudaError_t launch_combine_backward(int64_t T_, int k, int64_t H, int dtype, con
     constexpr int V = Elem<T>::kVec;
     const bool vec = H % V == 0 && aligned(y, ldy, sizeof(T)) && aligned(dout, ldd, sizeof(T)) &&
                      aligned(dy, H, sizeof(T));
-    if (vec)
-      return launch(combine_backward_kernel<T, V>, dim3(static_cast<unsigned>(T_)), kRowThreads, stream, 
-          T_, k, H, static_cast<const T*>(dout), ldd, static_cast<const T*>(y), ldy, slots,
-          weights, offsets_end, static_cast<T*>(dy), dweights);
-    else
-      return launch(combine_backward_kernel<T, 1>, dim3(static_cast<unsigned>(T_)), kRowThreads, stream, 
-          T_, k, H, static_cast<const T*>(dout), ldd, static_cast<const T*>(y), ldy, slots,
-          weights, offsets_end, static_cast<T*>(dy), dweights);
+    const RowShape s = row_shape(T_, H, vec ? V : kPieces);
+    auto go = [&](auto kernel) {
+      return launch(kernel, dim3(s.x), kRowThreads, stream, T_, k, H, s.log, static_cast<const T*>(dout), ldd,
+                    static_cast<const T*>(y), ldy, slots, weights, offsets_end, static_cast<T*>(dy), dweights);
+    };
+    if (s.log == kRowLog)
+      return vec ? go(combine_backward_kernel<T, V, 1, false>) : go(combine_backward_kernel<T, 1, kPieces, false>);
+    return vec ? go(combine_backward_kernel<T, V, 1, true>) : go(combine_backward_kernel<T, 1, kPieces, true>);
   });
 }
 

@@ -175,6 +175,13 @@ def test_gather_and_combine(T, k, H, dtype, masked):
     check(dw, (g_ * yr).sum(-1), (H + 1) * 2.0 ** -24 * (g_ * yr).abs().sum(-1) + 1e-30)
 
 
+# rows that share a block, pieces that the end of a row cuts, rows beyond the last block's
+@pytest.mark.parametrize("T,k,H", [(13, 3, 118), (7, 2, 255), (9, 2, 257), (11, 4, 1025), (5, 3, 2191), (6, 5, 520), (19, 1, 2048)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_of_any_length(T, k, H, dtype):
+    test_gather_and_combine(T, k, H, dtype, True)
+
+
 def test_combine_without_offsets_and_pitched():
     g = rng(23)
     T, k, H = 21, 4, 64
