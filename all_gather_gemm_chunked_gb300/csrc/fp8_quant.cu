@@ -18,7 +18,8 @@ __device__ __forceinline__ float block_scale(float amax) {
 // a row per step, 8 per lane: 16 lanes make one scale block, whose maximum takes
 // four shuffles.  All of a lane's loads are issued before the first use.  The
 // eight warps of a block take eight neighbouring rows, so that the scales they
-// write ([K block][row]) fill 32-byte sectors.
+// write ([K block][row]) fill 32-byte sectors.  (32768 rows of 4096, bf16: 69 us,
+// 5.9 TB/s; 64 rows of 16384: 2.3 us.)
 constexpr int kQuantSteps = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int64_t K,
@@ -78,8 +79,27 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int64_
   }
 }
 
-// One block per 128 x 128 block of an expert's weights (done once per model):
-// maximum, then the codes transposed through shared memory.
+// Two neighbouring elements, and as floats.
+template <typename T>
+struct Two {
+  uint32_t u;
+  __device__ __forceinline__ void load(const T* p) { u = __ldg(reinterpret_cast<const uint32_t*>(p)); }
+  __device__ __forceinline__ float2 get() const {
+    const T* v = reinterpret_cast<const T*>(&u);
+    return make_float2(Elem<T>::get(v[0]), Elem<T>::get(v[1]));
+  }
+};
+template <>
+struct Two<float> {
+  float2 u;
+  __device__ __forceinline__ void load(const float* p) { u = __ldg(reinterpret_cast<const float2*>(p)); }
+  __device__ __forceinline__ float2 get() const { return u; }
+};
+
+// One block per 128 x 128 block of an expert's weights (done once per model): a thread
+// holds two columns of 32 rows in registers, all its loads in flight; maximum, then the
+// codes transposed through shared memory.  Bound by memory
+// (16 x 4096 x 4096 bf16: 201 us, 4.0 TB/s).
 constexpr int kTilePitch = kScaleBlock + 4;
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_weights_kernel(int64_t K, int64_t N,
@@ -87,17 +107,26 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(int64_t K, int64_
                                                                uint8_t* __restrict__ q,
                                                                float* __restrict__ scales) {
   pdl_enter();
-  __shared__ uint8_t tile[kScaleBlock][kTilePitch];
+  __shared__ __align__(16) uint8_t tile[kScaleBlock][kTilePitch];
   __shared__ float red[8];
   const int64_t KB = (K + kScaleBlock - 1) / kScaleBlock, NB = (N + kScaleBlock - 1) / kScaleBlock;
   const int64_t kb = blockIdx.x % KB, nb = (blockIdx.x / KB) % NB, e = blockIdx.x / (KB * NB);
-  const int64_t n = nb * kScaleBlock + (threadIdx.x & 127);
-  const int k0 = threadIdx.x >> 7;  // two threads per column, every second row
-  const T* src = w + (e * K + kb * kScaleBlock) * N + n;
+  const int col = (threadIdx.x & 63) * 2, row0 = (threadIdx.x >> 6) * 32;
+  const int64_t n = nb * kScaleBlock + col;  // (N is even: both columns are there, or none)
+  const T* src = w + (e * K + kb * kScaleBlock + row0) * N + n;
   const int rows = static_cast<int>(K - kb * kScaleBlock < kScaleBlock ? K - kb * kScaleBlock : kScaleBlock);
+  Two<T> v[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[i] = Two<T>{};
+    if (n < N && row0 + i < rows) v[i].load(src + i * N);
+  }
   float amax = 0.0f;
-  if (n < N)
-    for (int i = k0; i < rows; i += 2) amax = fmaxf(amax, fabsf(Elem<T>::get(src[i * N])));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float2 f = v[i].get();
+    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
@@ -105,14 +134,22 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(int64_t K, int64_
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = fmaxf(amax, red[i]);
   const float s = block_scale(amax), inv = __frcp_rn(s);
-  for (int i = k0; i < kScaleBlock; i += 2) {
-    float v = 0.0f;
-    if (n < N && i < rows) v = Elem<T>::get(src[i * N]);
-    tile[threadIdx.x & 127][i] = static_cast<uint8_t>(e4m3x2(__fmul_rn(v, inv), 0.0f));
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    float2 f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = v[i + j].get();
+      f[j].x = __fmul_rn(f[j].x, inv);
+      f[j].y = __fmul_rn(f[j].y, inv);
+    }
+    *reinterpret_cast<uint32_t*>(&tile[col][row0 + i]) = e4m3x2(f[0].x, f[1].x) | (e4m3x2(f[2].x, f[3].x) << 16);
+    *reinterpret_cast<uint32_t*>(&tile[col + 1][row0 + i]) = e4m3x2(f[0].y, f[1].y) | (e4m3x2(f[2].y, f[3].y) << 16);
   }
   if (threadIdx.x == 0) scales[(e * NB + nb) * KB + kb] = s;
   __syncthreads();
   // rows n of q: 128 codes along K, 4 per thread and step
+#pragma unroll
   for (int i = threadIdx.x; i < kScaleBlock * (kScaleBlock / 4); i += 256) {
     const int row = i >> 5, c = (i & 31) * 4;
     const int64_t nn = nb * kScaleBlock + row;

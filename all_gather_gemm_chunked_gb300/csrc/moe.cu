@@ -255,6 +255,7 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   x.arrivals = p->arrivals;
   x.max_units = max_units(few);
   x.status = p->status;
+  // (8192 x 4096 x 4096, e4m3: 125 us with 32-byte stores, 134 with rows 16 bytes off)
   x.rows32 = x.out_type != AG_MOE_F32 && (reinterpret_cast<uintptr_t>(x.out) & 31u) == 0 && x.ldo % 16 == 0;
   x.timeout_ns = p->timeout_ns;
   const int64_t wide_tiles = (x.wide + agg::kXWide - 1) / agg::kXWide;

