@@ -234,21 +234,21 @@ struct Table {
 };
 
 // Parts of a sum that make the longest pair's share shortest: a round of the pairs costs
-// its k-blocks and about six more for a tile's start and end; with parts `once` more, for
+// its k-blocks and about six more for a tile's start and end; with parts price.once more, for
 // their way through memory, and at the end each part as long as the one CTA that adds a
-// tile's parts takes to read it, `part` k-blocks.  (Rows of 64, one expert, bf16: 4096 x
+// tile's parts takes to read it, price.part.  (Rows of 64, one expert, bf16: 4096 x
 // 512 13.7 us whole, 10.3 in four parts, 12.5 in sixteen; 1024 x 2048 7.2 and, in four,
 // 9.0.  Tiles of 256: 200 rows of 1024 x 2048 10.7 and 15.7; 234 of 2896 x 752 16.7 and,
 // in three, 15.5.  e4m3: 1 row of 3472 x 952 10.5 and, in four, 9.1; 64 of 16384 x 7168
 // 28.2 in two parts and one round, 34.4 in five parts and two rounds.)  Each lane of a
 // warp tries one number.
-__device__ __forceinline__ int32_t choose_split(int32_t tiles, int32_t KB, int32_t max_units, int32_t once, int32_t part) {
+__device__ __forceinline__ int32_t choose_split(int32_t tiles, int32_t KB, int32_t max_units, SplitPrice price) {
   const int32_t pairs = static_cast<int32_t>(gridDim.x / 2);
-  if (tiles == 0 || tiles >= 2 * pairs || KB < 8) return 1;
+  if (tiles == 0 || tiles >= 2 * pairs || max_units == 0) return 1;
   const int32_t s = static_cast<int32_t>(threadIdx.x & 31) + 1;
-  const bool can = s == 1 || (s <= 16 && KB >= 4 * s && tiles * s <= max_units);
+  const bool can = s == 1 || (s <= kMaxSplit && KB >= kMinPart * s && tiles * s <= max_units);
   const int32_t rounds = (tiles * s + pairs - 1) / pairs;
-  const uint32_t cost = can ? static_cast<uint32_t>(rounds * ((KB + s - 1) / s + 6 + (s > 1 ? once : 0)) + (s > 1 ? s * part : 0))
+  const uint32_t cost = can ? static_cast<uint32_t>(rounds * ((KB + s - 1) / s + 6 + (s > 1 ? price.once : 0)) + (s > 1 ? s * price.part : 0))
                             : 0x03ffffffu;
   // (the smallest number among the cheapest)
   const uint32_t best = __reduce_min_sync(0xffffffffu, min(cost, 0x03ffffffu) * 32 + (s - 1));
@@ -288,10 +288,8 @@ struct Schedule {
                                                    int32_t* head) {
     if (OP == kOpWeight) tiles = p.E * row_tiles(p);
     tiles *= wide_tiles(p);
-    const int32_t part = OP == kOpFp8 ? 1 : OP == kOpFp8Long ? 3 : BN != kXRows ? 2
-                         : OP == kOpWeight && p.step < kXRows ? 3 : 5;
     const int32_t split = choose_split(tiles, OP == kOpWeight ? longest / 64 : k_blocks(p), p.max_units,
-                                       is_fp8(OP) ? 9 : 14, part);
+                                       split_price(OP, OP == kOpWeight ? p.step < kXRows : BN != kXRows));
     if ((threadIdx.x & 31) == 0) {
       head[0] = split;
       head[1] = static_cast<int32_t>(split == 1 ? 0xffffffffu : 0xffffffffu / static_cast<uint32_t>(split));

@@ -63,6 +63,19 @@ constexpr int64_t split_unit_bytes(bool few) {
   return 2 * kXEpiWarps * (static_cast<int64_t>(few ? kXFewRows : kXRows) / 4) * 32 * 4;
 }
 
+// Prices of splitting a sum, in k-blocks of its variant: once a round, and for each part
+// (choose_split says what they stand for).
+struct SplitPrice {
+  int32_t once, part;
+};
+__host__ __device__ constexpr SplitPrice split_price(int op, bool short_tiles) {
+  return op == kOpFp8 ? SplitPrice{9, 1}
+         : op == kOpFp8Long ? SplitPrice{9, 3}
+         : op == kOpWeight ? SplitPrice{14, short_tiles ? 3 : 5}  // half tiles, whole ones
+                           : SplitPrice{14, short_tiles ? 2 : 5};
+}
+constexpr int kMaxSplit = 16, kMinPart = 4;  // parts of a sum; k-blocks of a part
+
 constexpr uint32_t kStatusOffsets = 16;  // status word: offsets decrease or leave [0, rows]
 
 // Kernel attributes; the number of CTA pairs that are resident at once.

@@ -134,19 +134,20 @@ at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& li
   return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), c10::nullopt));
 }
 
-// Tensors of 4-byte elements that share one allocation, one after the other (an
+// Tensors that share one allocation, one after the other from 256-byte boundaries (an
 // allocation takes about half a microsecond of host time, and as much to give back).
 struct Pieces {
   at::Tensor all;
   int64_t used = 0;
-  static int64_t room(int64_t n) { return (n + 63) & ~int64_t{63}; }
-  Pieces(int64_t elements, const at::Tensor& like) : all(make({elements}, at::ScalarType::Int, like)) {}
+  static int64_t room(int64_t bytes) { return (bytes + 255) & ~int64_t{255}; }
+  Pieces(int64_t bytes, const at::Tensor& like) : all(make({bytes}, at::ScalarType::Byte, like)) {}
   at::Tensor take(at::IntArrayRef shape, at::ScalarType type) {
+    const int64_t size = static_cast<int64_t>(c10::elementSize(type));
     at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
                                                             c10::scalarTypeToTypeMeta(type));
-    t.unsafeGetTensorImpl()->set_storage_offset(used);
+    t.unsafeGetTensorImpl()->set_storage_offset(used / size);
     t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-    used += room(t.numel());
+    used += room(t.numel() * size);
     return t;
   }
 };
@@ -193,7 +194,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int k = to_int32(a[1], "top_k");
   if (E > AG_MOE_MAX_EXPERTS) check_rc(ag_moe_route_workspace(T, AG_MOE_MAX_EXPERTS + 1, k));
   const int64_t size = check_rc(ag_moe_route_workspace(T, static_cast<int>(E), k));
-  Pieces pieces(4 * Pieces::room(T * k) + Pieces::room(E + 1), z);
+  Pieces pieces(4 * Pieces::room(T * k * 4) + Pieces::room((E + 1) * 4), z);
   at::Tensor w = pieces.take({T, k}, kF32), e = pieces.take({T, k}, kI32), off = pieces.take({E + 1}, kI32),
              order = pieces.take({T * k}, kI32), slots = pieces.take({T, k}, kI32), ws;
   if (size > 0) ws = make({size}, at::ScalarType::Byte, z);
@@ -314,7 +315,8 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     rows = src * k;
     order = plain<int32_t>(a[1], "routing.order", kI32, {rows});
   }
-  at::Tensor q = make({rows, K}, kE4m3, x), s = make({blocks(K), rows}, kF32, x);
+  Pieces pieces(Pieces::room(rows * K) + Pieces::room(blocks(K) * rows * 4), x);
+  at::Tensor q = pieces.take({rows, K}, kE4m3), s = pieces.take({blocks(K), rows}, kF32);
   check_rc(ag_fp8_quantize_rows(rows, K, type, x.data_ptr(), ld, src, order, static_cast<int>(k), q.data_ptr(),
                                 static_cast<float*>(s.data_ptr()), stream_of(x)));
   return tuple_of(q, s);

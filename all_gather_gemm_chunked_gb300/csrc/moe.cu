@@ -120,8 +120,13 @@ struct ag_moe_plan {
   float* partials = nullptr;
   uint64_t timeout_ns = 2000000000ull;
   cudaEvent_t done = nullptr;
+  // The last run that may split its sums, and so use the workspace: `done` is recorded
+  // behind it, and the next such run on another stream waits for it.  Others share
+  // nothing with it but the status word; an event behind each would cost a call a
+  // quarter of its host time (4.5 us against 3.4).
   cudaStream_t last_stream = nullptr;
   bool has_run = false;
+  bool loose = false;  // a run without an event since the last status or reset
   OperandCache cache[4];  // by ExpertsOp
 };
 
@@ -132,6 +137,15 @@ namespace {
 constexpr int64_t kPartialBytes = 608 * agg::split_unit_bytes(true);
 static_assert(kPartialBytes == 152 * agg::split_unit_bytes(false), "both tile heights");
 int max_units(bool few) { return static_cast<int>(kPartialBytes / agg::split_unit_bytes(few)); }
+
+// Whether a sum of so many k-blocks can be split: whether that pays in the best case, all
+// parts running at once.  (More tiles than pairs make it pay less: the parts' rounds
+// then save no more of the k-blocks, and cost more.)
+bool may_split(int64_t KB, agg::SplitPrice price) {
+  for (int64_t s = 2; s <= agg::kMaxSplit && s * agg::kMinPart <= KB; ++s)
+    if ((KB + s - 1) / s + price.once + s * price.part < KB) return true;
+  return false;
+}
 
 // k-blocks of a segment where the output is fp32.
 constexpr int kSegment = 8;
@@ -253,7 +267,6 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   x.segment = x.out_type == AG_MOE_F32 ? kSegment : 1 << 30;
   x.partials = p->partials;
   x.arrivals = p->arrivals;
-  x.max_units = max_units(few);
   x.status = p->status;
   // (8192 x 4096 x 4096, e4m3: 125 us with 32-byte stores, 134 with rows 16 bytes off)
   x.rows32 = x.out_type != AG_MOE_F32 && (reinterpret_cast<uintptr_t>(x.out) & 31u) == 0 && x.ldo % 16 == 0;
@@ -263,22 +276,31 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
     return fail(AG_GEMM_ERR_UNSUPPORTED, "more than 2^30 tiles");
   x.inv_group = 0xffffffffu / static_cast<uint32_t>(agg::kXGroup * wide_tiles);
   x.inv_expert = op == agg::kOpWeight ? 0xffffffffu / static_cast<uint32_t>(wide_tiles * x.row_tiles) : 0;
+  const bool fp8 = op == agg::kOpFp8;
+  const int64_t kb = op == agg::kOpWeight ? x.rows / 64 : (x.red + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
+  // (where the tiles' number does not depend on offsets, two rounds of them never split)
+  const bool plenty = (op == agg::kOpWeight || !x.offsets) && (row_tiles - 1) * wide_tiles >= 2 * p->pairs;
+  const bool split = !plenty && may_split(kb, agg::split_price(fp8 && !few ? agg::kOpFp8Long : op,
+                                                    op == agg::kOpWeight ? x.step < agg::kXRows : few));
+  x.max_units = split ? max_units(few) : 0;
   // A captured run is ordered by its graph: an event of the stream outside cannot be
   // waited on there, nor one of the graph outside.
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(stream, &capture);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
   const bool captured = capture != cudaStreamCaptureStatusNone;
-  if (!captured && p->has_run && p->last_stream != stream &&
+  if (split && !captured && p->has_run && p->last_stream != stream &&
       (e = cudaStreamWaitEvent(stream, p->done, 0)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamWaitEvent");
-  // no more pairs than there can be units: split sums have up to 16 parts of 4 k-blocks
-  const int64_t kb = op == agg::kOpWeight ? x.rows / 64 : x.red / (op == agg::kOpFp8 ? 128 : 64);
-  const int64_t units = row_tiles * wide_tiles * (kb < 8 ? 1 : kb < 64 ? (kb + 1) / 4 : 16);
+  // no more pairs than there can be units
+  const int64_t parts = !split ? 1 : kb / agg::kMinPart < agg::kMaxSplit ? kb / agg::kMinPart : agg::kMaxSplit;
+  const int64_t units = row_tiles * wide_tiles * parts;
   const int pairs = static_cast<int>(units < p->pairs ? units : p->pairs);
   if ((e = agg::launch_experts(x, op, few, 2 * pairs, stream)) != cudaSuccess)
     return cuda_fail(e, "experts kernel launch");
-  if (!captured) {
+  if (!split) {
+    p->loose = true;
+  } else if (!captured) {
     if ((e = cudaEventRecord(p->done, stream)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
     p->last_stream = stream;
     p->has_run = true;
@@ -529,8 +551,10 @@ int64_t ag_moe_plan_status_word(ag_moe_plan* plan) {
   if (!plan) return fail(AG_GEMM_ERR_INVALID, "plan is NULL");
   DeviceGuard dg(plan->device);
   cudaError_t e;
-  if (plan->has_run && (e = cudaEventSynchronize(plan->done)) != cudaSuccess)
+  if (plan->loose && (e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
+  if (!plan->loose && plan->has_run && (e = cudaEventSynchronize(plan->done)) != cudaSuccess)
     return cuda_fail(e, "cudaEventSynchronize");
+  plan->loose = false;
   uint32_t w[2] = {0, 0};
   if ((e = cudaMemcpy(w, plan->status, sizeof(w), cudaMemcpyDeviceToHost)) != cudaSuccess)
     return cuda_fail(e, "status read");
@@ -552,9 +576,11 @@ int ag_moe_plan_reset(ag_moe_plan* plan, void* stream_v) {
   DeviceGuard dg(plan->device);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
   cudaError_t e;
-  if (plan->has_run && plan->last_stream != stream &&
+  if (plan->loose && (e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
+  if (!plan->loose && plan->has_run && plan->last_stream != stream &&
       (e = cudaStreamWaitEvent(stream, plan->done, 0)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamWaitEvent");
+  plan->loose = false;
   if ((e = cudaMemsetAsync(plan->status, 0, static_cast<size_t>(4 + plan->arrival_count) * sizeof(uint32_t),
                            stream)) != cudaSuccess ||
       (e = cudaEventRecord(plan->done, stream)) != cudaSuccess)

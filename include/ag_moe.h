@@ -108,8 +108,9 @@ int ag_fp8_quantize_weights(int E, int64_t K, int64_t N, int dtype, const void *
 /*
  * A plan serves the products of one layer's experts: E weight matrices K x N.
  * dtype AG_GEMM_F16 or AG_GEMM_BF16 (K, N multiples of 8), or AG_MOE_E4M3 (K % 16
- * == 0, N % 8 == 0).  It owns the workspace of the products that split K and the
- * status word; runs on one plan are serialised as those of ag_gemm.h are.  Runs may be
+ * == 0, N % 8 == 0).  It owns the workspace of the products that split their sums and
+ * the status word; runs on one plan that may use the workspace are serialised as those
+ * of ag_gemm.h are, others may overlap where their streams let them.  Runs may be
  * captured into a CUDA graph; a replay is then the caller's to keep apart from the
  * plan's other runs, and to wait for before the status is read.
  *
@@ -124,7 +125,7 @@ typedef struct ag_moe_plan ag_moe_plan;
 
 ag_moe_plan *ag_moe_plan_create(int E, int64_t K, int64_t N, int dtype);
 void ag_moe_plan_destroy(ag_moe_plan *plan);
-/* Waits for the plan's last run; AG_GEMM_OK, AG_GEMM_ERR_TIMEOUT (a bounded wait in
+/* Waits for the plan's runs (for the device, if some left no event); AG_GEMM_OK, AG_GEMM_ERR_TIMEOUT (a bounded wait in
  * the kernel ran out) or AG_GEMM_ERR_INVALID (offsets, see above). */
 int ag_moe_plan_status(ag_moe_plan *plan);
 int64_t ag_moe_plan_status_word(ag_moe_plan *plan);
