@@ -82,32 +82,6 @@ int launched(cudaError_t e, const char* what) {
 }  // namespace
 
 // ------------------------------------------------------------------ plan
-// The operands of a product as the last run of its kind described them; a run on the
-// same matrices (a pointer, its pitch, the rows) takes the descriptors from here.
-struct OperandCache {
-  bool valid = false;
-  const void* w = nullptr;
-  const void* r = nullptr;
-  int64_t ldw = 0, ldw_e = 0, ldr = 0, rows = 0;
-  agg::ExpertsParams x{};
-  // The parameters if they are these operands', otherwise null after taking them down
-  // (valid again once the caller has encoded them).
-  agg::ExpertsParams* find(const void* w_, int64_t ldw_, int64_t ldw_e_, const void* r_, int64_t ldr_,
-                           int64_t rows_) {
-    if (valid && w == w_ && ldw == ldw_ && ldw_e == ldw_e_ && r == r_ && ldr == ldr_ && rows == rows_)
-      return &x;
-    valid = false;
-    w = w_;
-    ldw = ldw_;
-    ldw_e = ldw_e_;
-    r = r_;
-    ldr = ldr_;
-    rows = rows_;
-    std::memset(&x, 0, sizeof(x));
-    return nullptr;
-  }
-};
-
 struct ag_moe_plan {
   int E = 0;
   int64_t K = 0, N = 0;
@@ -127,7 +101,6 @@ struct ag_moe_plan {
   cudaStream_t last_stream = nullptr;
   bool has_run = false;
   bool loose = false;  // a run without an event since the last status or reset
-  OperandCache cache[4];  // by ExpertsOp
 };
 
 namespace {
@@ -309,13 +282,21 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   return AG_GEMM_OK;
 }
 
+// The row operand, once for each height of box that its tiles can have.
 int encode_rows(agg::ExpertsParams& x, int dtype, const void* base, int64_t len, int64_t rows,
                 int64_t ld, bool few) {
   const int step = (few ? agg::kXFewRows : agg::kXRows) / 8;
+  const int64_t half = (rows + 31) / 32 * 16;  // of a CTA, in a tile of all rows
+  const int most = (dtype == AG_MOE_E4M3 && !few) || half >= 4 * step ? agg::kXRowBoxes
+                                                                   : static_cast<int>((half + step - 1) / step);
   x.r_blk = whole_blocks(dtype, len);
-  for (int i = 0; i < agg::kXRowBoxes; ++i)
-    if (int rc = encode_k_major(&x.tm_r[i], dtype, base, len, rows, ld, 1, rows * ld, (i + 1) * step))
-      return rc;
+  for (int i = 0; i < agg::kXRowBoxes; ++i) {
+    if (i >= most) {
+      x.tm_r[i] = x.tm_r[i - 1];
+      continue;
+    }
+    if (int rc = encode_k_major(&x.tm_r[i], dtype, base, len, rows, ld, 1, rows * ld, (i + 1) * step)) return rc;
+  }
   return AG_GEMM_OK;
 }
 
@@ -336,18 +317,11 @@ int run_rows(ag_moe_plan* p, int op, int64_t rows, const void* in, int64_t ld_in
   if (p->E == 1) ldw_e = p->K * ldw;
   DeviceGuard dg(p->device);
   const bool few = few_rows(p, rows, wide);
-  OperandCache& c = p->cache[op];
-  if (!c.find(w, ldw, ldw_e, in, ld_in, rows)) {
-    int rc;
-    if (fwd)
-      rc = encode_mn_major(&c.x.tm_w, w, p->N, p->K, ldw, p->E, ldw_e);
-    else
-      rc = encode_k_major(&c.x.tm_w, p->dtype, w, p->N, p->K, ldw, p->E, ldw_e, 128);
-    if (rc || (rc = encode_rows(c.x, p->dtype, in, red, rows, ld_in, few))) return rc;
-    c.x.w_blk = whole_blocks(p->dtype, p->N);
-    c.valid = true;
-  }
-  agg::ExpertsParams& x = c.x;
+  agg::ExpertsParams x{};
+  int rc = fwd ? encode_mn_major(&x.tm_w, w, p->N, p->K, ldw, p->E, ldw_e)
+               : encode_k_major(&x.tm_w, p->dtype, w, p->N, p->K, ldw, p->E, ldw_e, 128);
+  if (rc || (rc = encode_rows(x, p->dtype, in, red, rows, ld_in, few))) return rc;
+  x.w_blk = whole_blocks(p->dtype, p->N);
   x.offsets = offsets;
   x.rows = static_cast<int32_t>(rows);
   x.wide = static_cast<int32_t>(wide);
@@ -622,18 +596,14 @@ int ag_moe_backward_weight(ag_moe_plan* plan, int64_t rows, const void* x, int64
   }
   if (int rc = check_matrix("x", x, ldx, plan->K, plan->dtype)) return rc;
   if (int rc = check_matrix("dy", dy, lddy, plan->N, plan->dtype)) return rc;
-  OperandCache& c = plan->cache[agg::kOpWeight];
-  if (!c.find(dy, lddy, 0, x, ldx, rows)) {
-    int rc;
-    if ((rc = encode_mn_major(&c.x.tm_w, dy, plan->N, rows, lddy, 1, rows * lddy)) ||
-        (rc = encode_mn_major(&c.x.tm_r[0], x, plan->K, rows, ldx, 1, rows * ldx)) ||
-        (rc = encode_mn_major(&c.x.tm_r[1], x, plan->K, rows, ldx, 1, rows * ldx, 1)))
-      return rc;
-    c.x.w_blk = whole_blocks(plan->dtype, plan->N);
-    c.x.r_blk = whole_blocks(plan->dtype, plan->K);
-    c.valid = true;
-  }
-  agg::ExpertsParams& p = c.x;
+  agg::ExpertsParams p{};
+  int rc;
+  if ((rc = encode_mn_major(&p.tm_w, dy, plan->N, rows, lddy, 1, rows * lddy)) ||
+      (rc = encode_mn_major(&p.tm_r[0], x, plan->K, rows, ldx, 1, rows * ldx)) ||
+      (rc = encode_mn_major(&p.tm_r[1], x, plan->K, rows, ldx, 1, rows * ldx, 1)))
+    return rc;
+  p.w_blk = whole_blocks(plan->dtype, plan->N);
+  p.r_blk = whole_blocks(plan->dtype, plan->K);
   p.offsets = offsets;
   p.rows = static_cast<int32_t>(rows);
   p.wide = static_cast<int32_t>(plan->N);
@@ -661,17 +631,12 @@ int ag_fp8_forward(ag_moe_plan* plan, int64_t rows, const void* xq, const float*
   if (!xs || !ws) return fail(AG_GEMM_ERR_INVALID, "scales are NULL");
   DeviceGuard dg(plan->device);
   const bool few = few_rows(plan, rows, plan->N);
-  OperandCache& c = plan->cache[agg::kOpFp8];
-  if (!c.find(wq, plan->K, plan->K * plan->N, xq, plan->K, rows)) {
-    int rc;
-    if ((rc = encode_k_major(&c.x.tm_w, AG_MOE_E4M3, wq, plan->K, plan->N, plan->K, plan->E,
-                             plan->K * plan->N, 128)) ||
-        (rc = encode_rows(c.x, AG_MOE_E4M3, xq, plan->K, rows, plan->K, few)))
-      return rc;
-    c.x.w_blk = whole_blocks(AG_MOE_E4M3, plan->K);
-    c.valid = true;
-  }
-  agg::ExpertsParams& p = c.x;
+  agg::ExpertsParams p{};
+  int rc;
+  if ((rc = encode_k_major(&p.tm_w, AG_MOE_E4M3, wq, plan->K, plan->N, plan->K, plan->E, plan->K * plan->N, 128)) ||
+      (rc = encode_rows(p, AG_MOE_E4M3, xq, plan->K, rows, plan->K, few)))
+    return rc;
+  p.w_blk = whole_blocks(AG_MOE_E4M3, plan->K);
   p.offsets = offsets;
   p.rows = static_cast<int32_t>(rows);
   p.wide = static_cast<int32_t>(plan->N);
