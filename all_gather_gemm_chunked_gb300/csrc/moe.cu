@@ -1,5 +1,5 @@
 // moe.cu -- host side of include/ag_moe.h: argument checks, the plan of the
-// products by expert (workspace, status, TMA descriptors) and the launches.
+// products by expert (workspace, status) and the launches.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -338,7 +338,7 @@ extern "C" {
 
 int64_t ag_moe_route_workspace(int64_t T, int E, int top_k) {
   if (int rc = check_route(T, E, top_k, AG_MOE_F32)) return rc;
-  const int blocks = agg::route_blocks(T);
+  const int blocks = agg::route_blocks(T, top_k);
   return blocks == 1 ? 0 : static_cast<int64_t>(blocks) * E * 4;
 }
 
@@ -349,7 +349,7 @@ int ag_moe_route(int64_t T, int E, int top_k, int dtype, const void* logits, int
   if (!offsets || (T > 0 && (!logits || !weights || !experts || !order || !slots)))
     return fail(AG_GEMM_ERR_INVALID, "a pointer is NULL");
   if (ld < E) return fail(AG_GEMM_ERR_INVALID, "row pitch %lld is less than %d experts", (long long)ld, E);
-  if (agg::route_blocks(T) > 1 && !workspace)
+  if (agg::route_blocks(T, top_k) > 1 && !workspace)
     return fail(AG_GEMM_ERR_INVALID, "workspace is NULL (see ag_moe_route_workspace)");
   agg::RouteArgs a = route_args(T, E, top_k, dtype, logits, ld, normalize);
   a.weights = weights;

@@ -65,6 +65,24 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// Sorts a lane's keys, largest first (Batcher's odd-even merge sort).
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = j; i < j + k; ++i)
+          if (i + k < N && i / (2 * p) == (i + k) / (2 * p)) {
+            const uint32_t hi = max(key[i], key[i + k]);
+            key[i + k] = min(key[i], key[i + k]);
+            key[i] = hi;
+          }
+}
+
 // Two tokens by one warp (side by side: a token's rounds are a chain of warp
 // reductions, and two chains take little longer than one): lane holds experts lane,
 // lane + 32, ...; each of the k rounds takes the largest key left (one reduction) and
@@ -79,6 +97,10 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t t0, int64_t e
   // 16-bit logits: value and expert in one key (16 bits of either), so that a round is
   // one reduction: the largest key is the largest logit's lowest expert.
   constexpr bool kPacked = sizeof(T) == 2;
+  // Such a lane's keys are sorted first: a round then looks at its largest alone (16384
+  // tokens of 256 experts, k 8: 18.3 us, 20.7 with all keys in each round; 128 experts,
+  // k 1: 11.3 and 11.1).
+  constexpr bool kSorted = kPacked && VPL <= 8;
   uint32_t key[kTokens][VPL];
   bool nan[kTokens];
 #pragma unroll
@@ -104,6 +126,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t t0, int64_t e
   uint32_t mine[kTokens] = {};
 #pragma unroll
   for (int n = 0; n < kTokens; ++n) {
+    if constexpr (kSorted) sort_keys(key[n]);
     nan[n] = __any_sync(kAll, nan[n]);
     chosen[n] = -1;
   }
@@ -116,7 +139,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t t0, int64_t e
       best[n] = key[n][0];
       bi[n] = lane;
 #pragma unroll
-      for (int i = 1; i < VPL; ++i) {
+      for (int i = 1; i < (kSorted ? 1 : VPL); ++i) {
         if (kPacked) {
           best[n] = max(best[n], key[n][i]);
         } else if (key[n][i] > best[n]) {
@@ -145,9 +168,16 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t t0, int64_t e
       int e;
       if (kPacked) {
         e = real ? packed_expert(top[n]) : -1;
+        if constexpr (kSorted) {
+          const bool taken = key[n][0] == top[n];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (key[n][i] == top[n]) key[n][i] = 0u;
+          for (int i = 0; i < VPL; ++i)
+            if (taken) key[n][i] = i + 1 < VPL ? key[n][i + 1] : 0u;
+        } else {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i)
+            if (key[n][i] == top[n]) key[n][i] = 0u;
+        }
       } else {
         e = static_cast<int>(__reduce_min_sync(
             kAll, real && best[n] == top[n] ? static_cast<uint32_t>(bi[n]) : 0xffffffffu));
@@ -347,7 +377,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_one_kernel(const RouteArg
 
 // More: one kernel chooses and counts the choices of each block's tokens, the
 // next places them.  Warps take tokens in pairs (one each cost as much as two).
-// (2048 tokens of 64 experts, k 4: 6.9 us; 16384 of 256, k 8: 20.7 us.)
+// (2048 tokens of 64 experts, k 4: 6.9 us; 16384 of 256, k 8: 18.3 us.)
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
   pdl_wait();
@@ -661,24 +691,24 @@ int values_per_lane(int E) { return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E
 
 }  // namespace
 
-// One cluster serves up to 256 tokens; beyond that blocks of at least 32 tokens, sixteen
-// warps' pairs, one block per SM at most.  (64 experts, k 4: 256 tokens 5.9 us, 6.5 by
-// two kernels, 384 tokens 7.0 and 6.6; 256 experts, k 8: 192 tokens 8.6 and 9.1, 256
-// tokens 10.0 and 9.2; 8 experts, k 2: 256 tokens 4.3 and 6.0.  Blocks of 16 tokens
-// took 7.8 us against 7.2 for 2048 tokens of 64 experts, of 64 tokens 7.7.)
-constexpr int64_t kOneClusterTokens = 256;
-// Its blocks: one for as few tokens as it takes, else eight.
-// (64 experts, k 4: 16 tokens 3.7 us by one block, 4.0 by eight, 32 tokens 4.1 and 4.0;
-// 256 experts, k 8: 5.2 and 5.1, 6.4 and 5.3.)
-int cluster_blocks(int64_t T) { return T <= 16 ? 1 : 8; }
-int route_blocks(int64_t T) {
-  if (T <= kOneClusterTokens) return 1;
+// One cluster serves up to 512 tokens and 1536 choices (one block places them all);
+// beyond that blocks of at least 32 tokens, sixteen warps' pairs, one block per SM at most.
+// (One cluster and two kernels: 64 experts, k 4: 256 tokens 5.9 us and 6.4, 384 7.0 and
+// 6.6; 256 experts, k 8: 192 tokens 8.1 and 8.5, 256 tokens 9.4 and 8.6; 128 experts, k 1:
+// 384 tokens 5.3 and 6.9.  Blocks of 16 tokens took 7.8 us against 7.2 for 2048 tokens of
+// 64 experts, of 64 tokens 7.7.)
+int route_blocks(int64_t T, int k) {
+  if (T <= 512 && T * k <= 1536) return 1;
   const int64_t b = (T + 31) / 32;
   return static_cast<int>(b < 152 ? b : 152);
 }
+// A cluster's blocks: one for as few tokens as it takes, else eight.
+// (64 experts, k 4: 16 tokens 3.7 us by one block, 4.0 by eight, 32 tokens 4.1 and 4.0;
+// 256 experts, k 8: 4.8 and 4.8, 5.8 and 5.0.)
+int cluster_blocks(int64_t T) { return T <= 16 ? 1 : 8; }
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
-  const int vpl = values_per_lane(a.E), blocks = route_blocks(a.T);
+  const int vpl = values_per_lane(a.E), blocks = route_blocks(a.T, a.k);
   const size_t smem = place_smem(a.E);
   void* args[] = {const_cast<RouteArgs*>(&a)};
   return AGG_FOR_TYPE(a.dtype, {

@@ -62,7 +62,7 @@ struct RouteArgs {
   int32_t* slots;
   int32_t* counts;  // [blocks][E], of more than one block
 };
-int route_blocks(int64_t T);
+int route_blocks(int64_t T, int k);
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
 cudaError_t launch_route_backward(const RouteArgs& a, const float* dweights, void* dlogits,
                                   cudaStream_t stream);
