@@ -89,9 +89,10 @@ __host__ __device__ constexpr int scale_bytes(int op, int BN) {
 __host__ __device__ constexpr int out_buffer(int op) { return op == kOpFp8Long ? 0 : op == kOpFp8 ? 512 : 1024; }
 __host__ __device__ constexpr int out_bytes(int op) { return kXEpiWarps * out_buffer(op); }
 constexpr int kTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) & ~15;
+constexpr int kUnitBytes = kXEpiWarps * 48;  // the epilogue warps' units
 __host__ __device__ constexpr int smem_bytes(int op, int BN) {
   return stages_of(BN) * kSub * (kWBytes + r_bytes(BN)) + scale_bytes(op, BN) +
-         out_bytes(op) + kTableBytes + 512 /*barriers*/ + 1024 /*alignment*/;
+         out_bytes(op) + kTableBytes + kUnitBytes + 512 /*barriers*/ + 1024 /*alignment*/;
 }
 static_assert(smem_bytes(kOpForward, kXRows) <= 227 * 1024 && smem_bytes(kOpFp8, kXFewRows) <= 227 * 1024 &&
                   smem_bytes(kOpFp8Long, kXRows) <= 227 * 1024,
@@ -202,6 +203,7 @@ struct Unit {
                      // (the inputs' last row) or the 16 rows of an MMA step end with the group
   int32_t tile, part;
 };
+static_assert(sizeof(Unit) <= kUnitBytes / kXEpiWarps, "an epilogue warp's unit");
 
 __host__ __device__ constexpr bool is_fp8(int op) { return op == kOpFp8 || op == kOpFp8Long; }
 template <int OP>
@@ -432,6 +434,7 @@ struct Ring {
   uint64_t* sempty; // e4m3: this CTA's epilogue warps are through with them
   float* scales;    // two batches: [k-block][BN], long groups [k-block][column block][128]
   uint8_t* stage_out;  // a buffer of out_buffer(OP) bytes for each epilogue warp
+  Unit* units;         // an epilogue warp's unit, beside the sums that fill its registers
   volatile int* abort;
 };
 
@@ -985,9 +988,11 @@ __device__ void epilogue_long(const ExpertsParams& p, const Table& table,
         return;
       }
     }
-    Unit u;
+    Unit u;  // (found anew: kept in shared memory as by epilogue_role, 8192 x 4096 x 4096 took
+             // 130 us against 126, from other registers in the loop above)
     Schedule<kOpFp8Long, BN> sch(p, table);
     sch.get(i, u);
+    const int32_t split = sch.split;
     const int32_t row = static_cast<int32_t>(rank) * 128 + quad * 32 + lane;
     const int64_t col = static_cast<int64_t>(u.n0) + c_first;
     const int64_t at = (static_cast<int64_t>(u.row0) + row) * p.ldo + col;
@@ -997,7 +1002,7 @@ __device__ void epilogue_long(const ExpertsParams& p, const Table& table,
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = sums[c * 8 + j];
     };
-    if (sch.split == 1 && n == kCols / 8 && p.rows32) {
+    if (split == 1 && n == kCols / 8 && p.rows32) {
       if (row < u.cnt)
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {
@@ -1008,7 +1013,7 @@ __device__ void epilogue_long(const ExpertsParams& p, const Table& table,
         }
       continue;
     }
-    if (sch.split == 1) {
+    if (split == 1) {
 #pragma unroll
       for (int c = 0; c < kCols / 8; ++c)
         if (c < n && row < u.cnt) {
@@ -1021,7 +1026,7 @@ __device__ void epilogue_long(const ExpertsParams& p, const Table& table,
     constexpr int kWarps = kXEpiWarps;
     constexpr int64_t kSlab = kCols * 32, kNext = 2 * kWarps * kSlab;
     float* first = p.partials +
-                   ((static_cast<int64_t>(u.tile) * sch.split * 2 + rank) * kWarps + ew) * kSlab + lane;
+                   ((static_cast<int64_t>(u.tile) * split * 2 + rank) * kWarps + ew) * kSlab + lane;
     float* part = first + u.part * kNext;
 #pragma unroll
     for (int c = 0; c < kCols / 8; ++c)
@@ -1031,10 +1036,10 @@ __device__ void epilogue_long(const ExpertsParams& p, const Table& table,
 #pragma unroll
         for (int j = 0; j < 8; ++j) __stcg(part + (c * 8 + j) * 32, v[j]);
       }
-    if (last_part<kWarps>(p, u, sch.split, rank, ew, lane))
+    if (last_part<kWarps>(p, u, split, rank, ew, lane))
       for (int c = 0; c < n; ++c) {
         float v[8];
-        add_parts(first + c * 8 * 32, kNext, sch.split, v);
+        add_parts(first + c * 8 * 32, kNext, split, v);
         if (row < u.cnt) store_row8(p.out, p.out_type, at + c * 8, v);
       }
   }
@@ -1053,6 +1058,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
     {
       Unit u;
       if (!Schedule<OP, BN>(p, table).get(i, u)) break;
+      if (lane == 0) ring.units[ew] = u;
       const int n8 = u.w / 32, c_first = quarter * n8 * 8;  // this warp's columns, in eights
       if (OP == kOpWeight && u.red_rows == 0 && table.head[0] == 1) {
         // an expert without rows (2 rows, 61 experts of 864 x 352: 21 us, by the sums 26)
@@ -1130,10 +1136,12 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
         }
       }
     }
-    // (the unit again: its fields would take the registers of the loop above)
-    Unit u;
-    Schedule<OP, BN> sch(p, table);
-    sch.get(i, u);
+    // (the unit again: its fields would take the registers of the loop above.  Finding it
+    // anew cost about 0.3 us a tile: weight gradient of 4096 rows, 16 experts of 4096 x 4096,
+    // 206 us, so 194; e4m3 of 4085 rows, 47 experts of 784 x 2664, 47.8 and 43.5.)
+    __syncwarp();
+    const Unit u = ring.units[ew];
+    const int32_t split = table.head[0];
     const int n8 = u.w / 32, c_first = quarter * n8 * 8;
     const int32_t col = u.n0 + static_cast<int32_t>(rank) * 128 + quad * 32;
     const Out<out_buffer(OP)> out{p.out, p.ldo,
@@ -1143,7 +1151,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = sums[c * 8 + j];
     };
-    if (sch.split == 1) {
+    if (split == 1) {
 #pragma unroll
       for (int c = 0; c < kCols / 8; ++c)
         if (c < n8) {
@@ -1158,7 +1166,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
     constexpr int64_t kSlab = static_cast<int64_t>(kCols) * 32;
     constexpr int64_t kNext = 2 * kXEpiWarps * kSlab;
     float* first = p.partials +
-                   ((static_cast<int64_t>(u.tile) * sch.split * 2 + rank) * kXEpiWarps + ew) * kSlab + lane;
+                   ((static_cast<int64_t>(u.tile) * split * 2 + rank) * kXEpiWarps + ew) * kSlab + lane;
     float* part = first + u.part * kNext;
 #pragma unroll
     for (int c = 0; c < kCols / 8; ++c)
@@ -1168,10 +1176,10 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
 #pragma unroll
         for (int j = 0; j < 8; ++j) __stcg(part + (c * 8 + j) * 32, v[j]);
       }
-    if (last_part<kXEpiWarps>(p, u, sch.split, rank, ew, lane))
+    if (last_part<kXEpiWarps>(p, u, split, rank, ew, lane))
       for (int c = 0; c < n8; ++c) {
         float v[8];
-        add_parts(first + c * 8 * 32, kNext, sch.split, v);
+        add_parts(first + c * 8 * 32, kNext, split, v);
         out.store(c_first + c * 8, v, lane);
       }
   }
@@ -1192,7 +1200,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   ring.stage_out = reinterpret_cast<uint8_t*>(ring.scales) + scale_bytes(OP, BN);
   int32_t* off = reinterpret_cast<int32_t*>(ring.stage_out + out_bytes(OP));
   int32_t* pre = off + kMaxExperts + 1;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(off) + kTableBytes);
+  ring.units = reinterpret_cast<Unit*>(reinterpret_cast<uint8_t*>(off) + kTableBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ring.units) + kUnitBytes);
   ring.full = bars;
   ring.empty = bars + kStagesX;
   ring.tfull = bars + 2 * kStagesX;
