@@ -52,7 +52,7 @@ enum {
  *   weights T x top_k float, experts T x top_k int32, offsets, order, slots as above.
  * workspace: ag_moe_route_workspace(T, E, top_k) bytes (may be NULL if that is 0),
  * not in use by another call.  T may be 0: offsets become zeros.
- * 1 <= E <= 1024, 1 <= top_k <= min(E, 32), T * top_k < 2^31.
+ * 1 <= E <= 1024, 1 <= top_k <= min(E, 32), T <= 2^28, T * top_k < 2^31.
  */
 int64_t ag_moe_route_workspace(int64_t T, int E, int top_k);
 int ag_moe_route(int64_t T, int E, int top_k, int dtype, const void *logits, int64_t ld,
