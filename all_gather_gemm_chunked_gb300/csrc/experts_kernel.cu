@@ -94,7 +94,8 @@ __host__ __device__ constexpr int smem_bytes(int op, int BN) {
   return stages_of(BN) * kSub * (kWBytes + r_bytes(BN)) + scale_bytes(op, BN) +
          out_bytes(op) + kTableBytes + kUnitBytes + 512 /*barriers*/ + 1024 /*alignment*/;
 }
-static_assert(smem_bytes(kOpForward, kXRows) <= 227 * 1024 && smem_bytes(kOpFp8, kXFewRows) <= 227 * 1024 &&
+static_assert(smem_bytes(kOpForward, kXRows) <= 227 * 1024 && smem_bytes(kOpForward, kXFewRows) <= 227 * 1024 &&
+                  smem_bytes(kOpWeight, kXRows) <= 227 * 1024 && smem_bytes(kOpFp8, kXFewRows) <= 227 * 1024 &&
                   smem_bytes(kOpFp8Long, kXRows) <= 227 * 1024,
               "shared memory of an SM");
 
@@ -226,15 +227,14 @@ struct Divisor {
     return q;
   }
 };
-__constant__ uint32_t kInverse[kXGroup + 1] = {0, 0xffffffffu, 0xffffffffu / 2, 0xffffffffu / 3,
-                                               0xffffffffu / 4, 0xffffffffu / 5, 0xffffffffu / 6,
-                                               0xffffffffu / 7, 0xffffffffu / 8};
 
 // The work of a launch, in shared memory.
 struct Table {
   const int32_t* off;   // [E + 1] row offsets
   const int32_t* pre;   // [E + 1] row tiles before each expert
-  const int32_t* head;  // parts of each tile's sum, floor((2^32 - 1) / parts), units
+  const int32_t* head;  // parts of each tile's sum, floor((2^32 - 1) / parts), units; and from
+                        // kInverse on floor((2^32 - 1) / n) for n up to 8
+  static constexpr int kInverse = 3;
 };
 
 // Parts of a sum that make the longest pair's share shortest: a round of the pairs costs
@@ -272,6 +272,7 @@ struct Schedule {
   int32_t KB;           // k-blocks of a whole sum
   int32_t split;        // parts of each tile's sum
   int32_t units, pair, pairs;
+  const int32_t* inverse;
   Divisor by_split, by_group, by_expert;  // parts; tiles of 8 row tiles; weight gradient: of an expert
   // the expert of the last unit, its first tile, row tiles and their height
   int32_t e, tile0, nt, height;
@@ -304,7 +305,7 @@ struct Schedule {
   __device__ __forceinline__ Schedule(const ExpertsParams& p_, const Table& t)
       : p(p_), off(t.off), pre(t.pre), wt(wide_tiles(p_)), kt(row_tiles(p_)), KB(k_blocks(p_)),
         split(t.head[0]), units(t.head[2]), pair(static_cast<int32_t>(blockIdx.x / 2)),
-        pairs(static_cast<int32_t>(gridDim.x / 2)),
+        pairs(static_cast<int32_t>(gridDim.x / 2)), inverse(t.head + Table::kInverse),
         by_split(static_cast<uint32_t>(split), static_cast<uint32_t>(t.head[1])),
         by_group(static_cast<uint32_t>(kXGroup * wt), p_.inv_group),
         by_expert(OP == kOpWeight ? static_cast<uint32_t>(wt * kt) : 1u, p_.inv_expert), e(-1), tile0(0),
@@ -316,7 +317,7 @@ struct Schedule {
     uint32_t rest;
     const int32_t g = static_cast<int32_t>(by_group.div(r, rest));
     const uint32_t gw = static_cast<uint32_t>(n - g * kXGroup < kXGroup ? n - g * kXGroup : kXGroup);
-    uint32_t q = __umulhi(rest, kInverse[gw]);
+    uint32_t q = __umulhi(rest, inverse[gw]);
     rest -= q * gw;
     if (rest >= gw) {
       ++q;
@@ -1214,7 +1215,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   ring.abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* flag = reinterpret_cast<int32_t*>(tmem_slot + 2);
-  int32_t* head = flag + 1;  // [3]
+  int32_t* head = flag + 1;  // [Table::kInverse + kXGroup + 1]
   const Table table{off, pre, head};
 
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -1242,6 +1243,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
+  if (warp == 3 && lane <= kXGroup)
+    head[Table::kInverse + lane] = static_cast<int32_t>(lane ? 0xffffffffu / static_cast<uint32_t>(lane) : 0u);
   if (warp == 2 && lane <= kXRowBoxes)  // the descriptors' first use would wait for them
     tma_prefetch_desc(lane == kXRowBoxes ? &p.tm_w : &p.tm_r[OP == kOpWeight ? lane & 1 : lane]);
   tc_fence_before();
@@ -1273,7 +1276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   }
   tc_fence_before();
   // Every accumulator has been waited for, so every MMA and load of the pair is through,
-  // unless a wait ran out (the whole block's verdict: the status word may change meanwhile):
+  // unless a wait ran out (decided by the whole block: the status word may change meanwhile):
   if (__syncthreads_or(*ring.abort || *reinterpret_cast<volatile uint32_t*>(p.status) != 0u)) {
     if (rank == 0 && warp == 1 && elect_one()) {  // the thread that issued the MMAs
       mma_commit_pair_local(drain);
