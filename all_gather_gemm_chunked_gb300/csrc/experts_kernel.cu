@@ -52,7 +52,7 @@
 // as long as its MMAs take the tensor cores); weight gradient to fp32 175 us; 64 rows on
 // 32 experts of 4096 x 4096 131 us (the hit weights at 6.9 TB/s).  e4m3: the same product
 // 126 us (2.2 PFLOP/s; bound by the epilogue's work on each k-block), 64 rows of 16384 x
-// 7168 28 us (a bare read of the weights 27.6).  A call of one tile takes 5 us.
+// 7168 28 us (a bare read of the weights 27.6).  A call of one tile takes 4.4 us.
 //
 // Every wait is bounded; on a timeout the kernel records a status word, drains what
 // it has in flight, frees TMEM and returns.
@@ -1275,9 +1275,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     set_status(p.status, kStatusOffsets, 0);
   }
   tc_fence_before();
-  // Every accumulator has been waited for, so every MMA and load of the pair is through,
-  // unless a wait ran out (decided by the whole block: the status word may change meanwhile):
-  if (__syncthreads_or(*ring.abort || *reinterpret_cast<volatile uint32_t*>(p.status) != 0u)) {
+  // This CTA's epilogue has waited for every accumulator of the pair, so every MMA and load
+  // of the pair is through, unless a wait of this CTA ran out (a wait of the peer's alone
+  // leaves nothing of the pair's in flight then):
+  if (__syncthreads_or(*ring.abort)) {
     if (rank == 0 && warp == 1 && elect_one()) {  // the thread that issued the MMAs
       mma_commit_pair_local(drain);
       volatile int never = 0;
