@@ -184,7 +184,7 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   AGG_END
 }
 
-// route(logits, top_k, normalize) -> weights, experts, offsets, order, slots
+// route(logits, top_k, normalize) -> weights, experts, offsets, order, slots, normalize
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   AGG_BEGIN
   check_args(n, 3);
@@ -203,7 +203,13 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
                         static_cast<int32_t*>(off.data_ptr()), static_cast<int32_t*>(order.data_ptr()),
                         static_cast<int32_t*>(slots.data_ptr()), size > 0 ? ws.data_ptr() : nullptr,
                         stream_of(z)));
-  return tuple_of(w, e, off, order, slots);
+  // (the fields of moe.Routing, which takes the tuple as it is)
+  PyObject* r = PyTuple_New(6);
+  if (!r) throw Raised();
+  Py_ssize_t i = 0;
+  for (at::Tensor* t : {&w, &e, &off, &order, &slots}) PyTuple_SET_ITEM(r, i++, wrap(std::move(*t)));
+  PyTuple_SET_ITEM(r, i, Py_NewRef(a[2]));
+  return r;
   AGG_END
 }
 

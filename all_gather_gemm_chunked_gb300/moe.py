@@ -52,7 +52,7 @@ def route(logits: torch.Tensor, top_k: int, normalize: bool = True, stream=None)
     layout of the rows sorted by expert."""
     if stream is not None:
         return _on(stream, route, logits, top_k, normalize)
-    return Routing(*_front.route(logits, top_k, normalize), normalize)
+    return tuple.__new__(Routing, _front.route(logits, top_k, normalize))
 
 
 def route_backward(logits: torch.Tensor, routing: Routing, dweights: torch.Tensor,
