@@ -89,6 +89,27 @@ def test_neighbours_with_infinities_and_nan_stay_out():
         check(dw[e], xd.t() @ gd, product_bound(xd.t(), gd, b - a, torch.float32), f"dw of {e}")
 
 
+@pytest.mark.parametrize("sizes,bad", [([16, 7, 48, 5, 96, 3, 64], [1, 3, 5]), ([80, 300, 112], [1]), ([33, 0, 16, 9], [0, 3])])
+def test_groups_that_end_with_a_step_next_to_poison(sizes, bad):
+    """Groups of whole steps of 16 rows, and an empty one, before rows of NaN."""
+    K, N = 264, 136
+    x, _, dy, off = _case(sizes, K, N, torch.bfloat16, 31)
+    at = 0
+    for e, n in enumerate(sizes):
+        if e in bad:
+            x[at:at + n] = float("nan")
+            dy[at:at + n] = float("inf")
+        at += n
+    with moe.Experts(len(sizes), K, N) as p:
+        dw = p.backward_weight(x, dy, off)
+        assert p.status() == B_.OK
+    for e, (a, b) in enumerate(_per_expert(sizes, lambda e, a, b: (a, b))):
+        if e not in bad:
+            xd, gd = x[a:b].double(), dy[a:b].double()
+            check(dw[e], xd.t() @ gd, product_bound(xd.t(), gd, b - a, torch.float32), f"dw of {e}")
+            assert a < b or not bool(dw[e].any())
+
+
 def test_gradients_are_the_differences_of_the_product():
     """The product is linear: with small whole numbers every value is exact, and
     <dy, y(x + v) - y(x - v)> / 2 = <dx, v>, the same for the weights."""
