@@ -28,7 +28,7 @@ static_assert(AG_MOE_F32 == agg::kTypeF32 && AG_MOE_E4M3 == agg::kTypeE4m3 &&
 
 namespace {
 
-constexpr int64_t kMaxTokens = 1LL << 28;   // a warp's 16-bit counts of the router hold this many
+constexpr int64_t kMaxTokens = 1LL << 28;   // (the router then takes 4097 blocks)
 constexpr int64_t kMaxRowLen = 1LL << 24;   // columns of a moved row (grid limit)
 
 bool float_type(int dtype) {

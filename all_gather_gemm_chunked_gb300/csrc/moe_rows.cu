@@ -218,6 +218,9 @@ __device__ __forceinline__ Share share_of(int64_t first, int64_t end, int64_t pa
 
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWarps = kRouteThreads / 32;
+// Tokens of a block: place() holds prefixes of its choices of an expert in 16 bits (in 32
+// bits 1024 experts would take 128 KB of shared memory instead of 64).
+constexpr int64_t kBlockTokens = 65535;
 
 // Sum over the block's threads before this one (value of thread e at e).
 __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_sums, int warp,
@@ -249,8 +252,8 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_s
 // earlier warps of this block, in this warp's earlier steps and in earlier lanes (a
 // match of the experts over the warp): counts and prefix sums alone, so the order
 // within an expert is the tokens' (a token chooses an expert at most once).
-// smem: [kRouteWarps][E] uint16 counts (a warp has fewer than 2^16 tokens: T is at most
-// 2^28), then E uint32 first rows, 32 warp sums, the number of rows in use, E counts of
+// smem: [kRouteWarps][E] uint16 counts and, later, counts of this block's earlier choices
+// (a block has at most kBlockTokens tokens, see route_blocks), then E uint32 first rows, 32 warp sums, the number of rows in use, E counts of
 // earlier blocks.  `blocks`: blocks that place, with their counts if more than one.
 __device__ void place(const RouteArgs& a, int64_t c0, int64_t c1, int blocks, uint8_t* smem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -692,15 +695,16 @@ int values_per_lane(int E) { return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E
 }  // namespace
 
 // One cluster serves up to 512 tokens and 1536 choices (one block places them all);
-// beyond that blocks of at least 32 tokens, sixteen warps' pairs, one block per SM at most.
+// beyond that blocks of at least 32 tokens, sixteen warps' pairs, one block per SM, and
+// from 152 * kBlockTokens tokens on as many as hold them.
 // (One cluster and two kernels: 64 experts, k 4: 256 tokens 5.9 us and 6.4, 384 7.0 and
 // 6.6; 256 experts, k 8: 192 tokens 8.1 and 8.5, 256 tokens 9.4 and 8.6; 128 experts, k 1:
 // 384 tokens 5.3 and 6.9.  Blocks of 16 tokens took 7.8 us against 7.2 for 2048 tokens of
 // 64 experts, of 64 tokens 7.7.)
 int route_blocks(int64_t T, int k) {
   if (T <= 512 && T * k <= 1536) return 1;
-  const int64_t b = (T + 31) / 32;
-  return static_cast<int>(b < 152 ? b : 152);
+  const int64_t b = (T + 31) / 32, least = (T + kBlockTokens - 1) / kBlockTokens;
+  return static_cast<int>(b < 152 ? b : least < 152 ? 152 : least);
 }
 // A cluster's blocks: one for as few tokens as it takes, else eight.
 // (64 experts, k 4: 16 tokens 3.7 us by one block, 4.0 by eight, 32 tokens 4.1 and 4.0;
