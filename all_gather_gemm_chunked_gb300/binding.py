@@ -113,6 +113,7 @@ def _load():
         "ag_fp8_quantize_weights": (i32, [i32, i64, i64, i32, vp, vp, vp, vp]),
         "ag_moe_plan_create": (vp, [i32, i64, i64, i32]),
         "ag_moe_plan_destroy": (None, [vp]),
+        "ag_moe_plan_device": (i32, [vp]),
         "ag_moe_plan_status": (i32, [vp]),
         "ag_moe_plan_status_word": (i64, [vp]),
         "ag_moe_plan_reset": (i32, [vp, vp]),

@@ -4,11 +4,13 @@
 // the allocation and the foreign call took 10 to 18 us a call, longer than the kernels.
 //
 // Wrong tensors raise TypeError or ValueError; a negative code of the library raises
-// what the error function given to init() returns.
+// what the error function given to init() returns.  The tensors of a call, and its plan,
+// are on one device, which is current while it allocates and launches.
 
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -70,10 +72,19 @@ ag_moe_plan* to_plan(PyObject* o) {
   return reinterpret_cast<ag_moe_plan*>(static_cast<uintptr_t>(to_int(o)));
 }
 
+// A call's first tensor.
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) raise(PyExc_TypeError, "%s must be a torch.Tensor", name);
   const at::Tensor& t = THPVariable_Unpack(o);
   if (!t.is_cuda()) raise(PyExc_ValueError, "%s must be on a CUDA device", name);
+  return t;
+}
+// Any other: on the first one's device.
+const at::Tensor& tensor(PyObject* o, const char* name, const at::Tensor& first) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.device() != first.device())
+    raise(PyExc_ValueError, "%s is on device %s, the call's first tensor on %s", name, t.device().str().c_str(),
+          first.device().str().c_str());
   return t;
 }
 
@@ -120,10 +131,10 @@ int64_t pitch(const at::Tensor& t, const char* name, int64_t cols = -1) {
   return t.stride(0);
 }
 
-// Pointer of a contiguous tensor of this type and shape.
+// Pointer of a contiguous tensor of this type and shape, on the first one's device.
 template <typename T = void>
-T* plain(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape) {
-  const at::Tensor& t = tensor(o, name);
+T* plain(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, const at::Tensor& first) {
+  const at::Tensor& t = tensor(o, name, first);
   want_type(t, name, type);
   want_shape(t, name, shape);
   if (!t.is_contiguous()) raise(PyExc_ValueError, "%s must be contiguous", name);
@@ -194,6 +205,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int k = to_int32(a[1], "top_k");
   if (E > AG_MOE_MAX_EXPERTS) check_rc(ag_moe_route_workspace(T, AG_MOE_MAX_EXPERTS + 1, k));
   const int64_t size = check_rc(ag_moe_route_workspace(T, static_cast<int>(E), k));
+  const c10::cuda::CUDAGuard guard(z.device());
   Pieces pieces(4 * Pieces::room(T * k * 4) + Pieces::room((E + 1) * 4), z);
   at::Tensor w = pieces.take({T, k}, kF32), e = pieces.take({T, k}, kI32), off = pieces.take({E + 1}, kI32),
              order = pieces.take({T * k}, kI32), slots = pieces.take({T, k}, kI32), ws;
@@ -220,11 +232,12 @@ PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& z = tensor(a[0], "logits");
   const int type = float_type(z, "logits");
   const int64_t ld = pitch(z, "logits"), T = z.size(0), E = z.size(1);
-  const at::Tensor& wt = tensor(a[1], "routing.weights");
+  const at::Tensor& wt = tensor(a[1], "routing.weights", z);
   const int64_t k = wt.dim() == 2 ? wt.size(1) : 0;
-  const float* w = plain<float>(a[1], "routing.weights", kF32, {T, k});
-  const int32_t* e = plain<int32_t>(a[2], "routing.experts", kI32, {T, k});
-  const float* dw = plain<float>(a[3], "dweights", kF32, {T, k});
+  const float* w = plain<float>(a[1], "routing.weights", kF32, {T, k}, z);
+  const int32_t* e = plain<int32_t>(a[2], "routing.experts", kI32, {T, k}, z);
+  const float* dw = plain<float>(a[3], "dweights", kF32, {T, k}, z);
+  const c10::cuda::CUDAGuard guard(z.device());
   at::Tensor out = make({T, E}, z.scalar_type(), z);
   check_rc(ag_moe_route_backward(T, static_cast<int>(E), static_cast<int>(k), type, z.data_ptr(), ld,
                                  PyObject_IsTrue(a[4]), w, e, dw, out.data_ptr(), stream_of(z)));
@@ -239,9 +252,10 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& x = tensor(a[0], "x");
   const int type = float_type(x, "x");
   const int64_t ld = pitch(x, "x"), T = x.size(0), H = x.size(1);
-  const at::Tensor& slots = tensor(a[2], "routing.slots");
+  const at::Tensor& slots = tensor(a[2], "routing.slots", x);
   const int64_t k = slots.dim() == 2 ? slots.size(1) : 0;
-  const int32_t* order = plain<int32_t>(a[1], "routing.order", kI32, {T * k});
+  const int32_t* order = plain<int32_t>(a[1], "routing.order", kI32, {T * k}, x);
+  const c10::cuda::CUDAGuard guard(x.device());
   at::Tensor out = make({T * k, H}, x.scalar_type(), x);
   check_rc(ag_moe_gather(T, static_cast<int>(k), H, type, x.data_ptr(), ld, order, out.data_ptr(), stream_of(x)));
   return wrap(out);
@@ -254,13 +268,13 @@ struct Choices {
   const int32_t* slots;
 };
 Choices choices(PyObject* slots_o, const at::Tensor& y) {
-  const at::Tensor& s = tensor(slots_o, "slots");
+  const at::Tensor& s = tensor(slots_o, "slots", y);
   if (s.dim() != 2) raise(PyExc_ValueError, "slots must have shape (tokens, top_k), got %s", shape_of(s.sizes()).c_str());
   const int64_t T = s.size(0), k = s.size(1);
   if (y.size(0) != T * k)
     raise(PyExc_ValueError, "y must have %lld rows, got %lld", static_cast<long long>(T * k),
           static_cast<long long>(y.size(0)));
-  return {T, k, plain<int32_t>(slots_o, "slots", kI32, {T, k})};
+  return {T, k, plain<int32_t>(slots_o, "slots", kI32, {T, k}, y)};
 }
 
 // combine(y, slots, weights or None) -> out
@@ -271,7 +285,8 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int type = float_type(y, "y");
   const int64_t ld = pitch(y, "y"), H = y.size(1);
   const Choices c = choices(a[1], y);
-  const float* w = a[2] == Py_None ? nullptr : plain<float>(a[2], "weights", kF32, {c.T, c.k});
+  const float* w = a[2] == Py_None ? nullptr : plain<float>(a[2], "weights", kF32, {c.T, c.k}, y);
+  const c10::cuda::CUDAGuard guard(y.device());
   at::Tensor out = make({c.T, H}, y.scalar_type(), y);
   check_rc(ag_moe_combine(c.T, static_cast<int>(c.k), H, type, y.data_ptr(), ld, c.slots, w, out.data_ptr(),
                           stream_of(y)));
@@ -283,7 +298,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   AGG_BEGIN
   check_args(n, 5);
-  const at::Tensor &d = tensor(a[0], "dout"), &y = tensor(a[1], "y");
+  const at::Tensor &d = tensor(a[0], "dout"), &y = tensor(a[1], "y", d);
   const int type = float_type(y, "y");
   want_type(d, "dout", y.scalar_type());
   const int64_t ld = pitch(y, "y"), H = y.size(1), ldd = pitch(d, "dout", H);
@@ -291,13 +306,14 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (d.size(0) != c.T)
     raise(PyExc_ValueError, "dout must have %lld rows, got %lld", static_cast<long long>(c.T),
           static_cast<long long>(d.size(0)));
-  const float* w = plain<float>(a[3], "weights", kF32, {c.T, c.k});
+  const float* w = plain<float>(a[3], "weights", kF32, {c.T, c.k}, y);
   const int32_t* end = nullptr;
   if (a[4] != Py_None) {
-    const int64_t m = tensor(a[4], "offsets").numel();
+    const int64_t m = tensor(a[4], "offsets", y).numel();
     if (m < 1) raise(PyExc_ValueError, "offsets must not be empty");
-    end = plain<int32_t>(a[4], "offsets", kI32, {m}) + m - 1;
+    end = plain<int32_t>(a[4], "offsets", kI32, {m}, y) + m - 1;
   }
+  const c10::cuda::CUDAGuard guard(y.device());
   at::Tensor dy = make({c.T * c.k, H}, y.scalar_type(), y), dw = make({c.T, c.k}, kF32, y);
   check_rc(ag_moe_combine_backward(c.T, static_cast<int>(c.k), H, type, d.data_ptr(), ldd, y.data_ptr(), ld,
                                    c.slots, w, end, dy.data_ptr(), static_cast<float*>(dw.data_ptr()),
@@ -316,11 +332,12 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t rows = src, k = 1;
   const int32_t* order = nullptr;
   if (a[1] != Py_None) {
-    const at::Tensor& slots = tensor(a[2], "routing.slots");
+    const at::Tensor& slots = tensor(a[2], "routing.slots", x);
     k = slots.dim() == 2 ? slots.size(1) : 0;
     rows = src * k;
-    order = plain<int32_t>(a[1], "routing.order", kI32, {rows});
+    order = plain<int32_t>(a[1], "routing.order", kI32, {rows}, x);
   }
+  const c10::cuda::CUDAGuard guard(x.device());
   Pieces pieces(Pieces::room(rows * K) + Pieces::room(blocks(K) * rows * 4), x);
   at::Tensor q = pieces.take({rows, K}, kE4m3), s = pieces.take({blocks(K), rows}, kF32);
   check_rc(ag_fp8_quantize_rows(rows, K, type, x.data_ptr(), ld, src, order, static_cast<int>(k), q.data_ptr(),
@@ -339,6 +356,7 @@ PyObject* quantize_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
     raise(PyExc_ValueError, "w must be a contiguous (E, K, N) or (K, N) tensor");
   const bool many = w.dim() == 3;
   const int64_t E = many ? w.size(0) : 1, K = w.size(-2), N = w.size(-1);
+  const c10::cuda::CUDAGuard guard(w.device());
   at::Tensor q = make({E, N, K}, kE4m3, w), s = make({E, blocks(N), blocks(K)}, kF32, w);
   if (E > AG_MOE_MAX_EXPERTS) raise(PyExc_ValueError, "w has too many experts");
   check_rc(ag_fp8_quantize_weights(static_cast<int>(E), K, N, type, w.data_ptr(), q.data_ptr(),
@@ -358,8 +376,18 @@ struct PlanArgs {
 };
 PlanArgs plan_args(PyObject* const* a) { return {to_plan(a[0]), to_int(a[1]), to_int(a[2]), to_int(a[3])}; }
 
-const int32_t* offsets_of(PyObject* o, int64_t E) {
-  return o == Py_None ? nullptr : plain<int32_t>(o, "offsets", kI32, {E + 1});
+// A product's first tensor, on its plan's device.
+const at::Tensor& tensor(PyObject* o, const char* name, const PlanArgs& p) {
+  const at::Tensor& t = tensor(o, name);
+  const int64_t device = check_rc(ag_moe_plan_device(p.plan));
+  if (t.device().index() != device)
+    raise(PyExc_ValueError, "%s is on device %s, the plan on cuda:%d", name, t.device().str().c_str(),
+          static_cast<int>(device));
+  return t;
+}
+
+const int32_t* offsets_of(PyObject* o, int64_t E, const at::Tensor& first) {
+  return o == Py_None ? nullptr : plain<int32_t>(o, "offsets", kI32, {E + 1}, first);
 }
 
 at::ScalarType dtype_of(PyObject* o) {
@@ -369,7 +397,7 @@ at::ScalarType dtype_of(PyObject* o) {
 
 at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
   if (o == Py_None) return make(shape, type, like);
-  const at::Tensor& t = tensor(o, "out");
+  const at::Tensor& t = tensor(o, "out", like);
   want_type(t, "out", type);
   want_shape(t, "out", shape);
   return t;
@@ -383,11 +411,11 @@ PyObject* rows_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::ScalarType type = dtype_of(a[4]);
   const bool back = a[5] == Py_True;
   const char* name = back ? "dy" : "x";
-  const at::Tensor& x = tensor(a[6], name);
+  const at::Tensor& x = tensor(a[6], name, p);
   want_type(x, name, type);
   const int64_t ld = pitch(x, name, back ? p.N : p.K), rows = x.size(0), wide = back ? p.K : p.N;
-  const int32_t* off = offsets_of(a[7], p.E);
-  const at::Tensor& w = tensor(a[8], "w");
+  const int32_t* off = offsets_of(a[7], p.E, x);
+  const at::Tensor& w = tensor(a[8], "w", x);
   want_type(w, "w", type);
   want_shape(w, "w", {p.E, p.K, p.N});
   int64_t ldw = p.N, ldw_e = p.K * p.N;
@@ -397,6 +425,7 @@ PyObject* rows_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ldw_e = w.stride(0);
   }
   const at::ScalarType ot = a[10] == Py_None ? type : dtype_of(a[10]);
+  const c10::cuda::CUDAGuard guard(x.device());
   at::Tensor out = output(a[9], {rows, wide}, ot, x);
   const int64_t ldo = pitch(out, "out");
   check_rc((back ? ag_moe_backward_input : ag_moe_forward)(p.plan, rows, x.data_ptr(), ld, off, w.data_ptr(), ldw,
@@ -412,15 +441,16 @@ PyObject* weight_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check_args(n, 10);
   const PlanArgs p = plan_args(a);
   const at::ScalarType type = dtype_of(a[4]);
-  const at::Tensor &x = tensor(a[5], "x"), &dy = tensor(a[6], "dy");
+  const at::Tensor &x = tensor(a[5], "x", p), &dy = tensor(a[6], "dy", x);
   want_type(x, "x", type);
   want_type(dy, "dy", type);
   const int64_t ldx = pitch(x, "x", p.K), ldd = pitch(dy, "dy", p.N), rows = x.size(0);
   if (dy.size(0) != rows)
     raise(PyExc_ValueError, "x and dy must have the same rows, got %lld and %lld", static_cast<long long>(rows),
           static_cast<long long>(dy.size(0)));
-  const int32_t* off = offsets_of(a[7], p.E);
+  const int32_t* off = offsets_of(a[7], p.E, x);
   const at::ScalarType ot = dtype_of(a[9]);
+  const c10::cuda::CUDAGuard guard(x.device());
   at::Tensor out = output(a[8], {p.E, p.K, p.N}, ot, x);
   if (!out.is_contiguous()) raise(PyExc_ValueError, "out must be contiguous");
   check_rc(ag_moe_backward_weight(p.plan, rows, x.data_ptr(), ldx, dy.data_ptr(), ldd, off, out.data_ptr(),
@@ -434,21 +464,22 @@ PyObject* fp8_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   AGG_BEGIN
   check_args(n, 11);
   const PlanArgs p = plan_args(a);
-  const at::Tensor &x = tensor(a[4], "xq"), &w = tensor(a[6], "wq");
+  const at::Tensor &x = tensor(a[4], "xq", p), &w = tensor(a[6], "wq", x);
   const int64_t rows = x.dim() > 0 ? x.size(0) : 0, kb = blocks(p.K), nb = blocks(p.N);
-  const void* xq = plain(a[4], "xq", kE4m3, {rows, p.K});
-  const float* xs = plain<float>(a[5], "xs", kF32, {kb, rows});
+  const void* xq = plain(a[4], "xq", kE4m3, {rows, p.K}, x);
+  const float* xs = plain<float>(a[5], "xs", kF32, {kb, rows}, x);
   const void* wq;
   const float* ws;
   if (p.E == 1 && w.dim() == 2) {
-    wq = plain(a[6], "wq", kE4m3, {p.N, p.K});
-    ws = plain<float>(a[7], "ws", kF32, {nb, kb});
+    wq = plain(a[6], "wq", kE4m3, {p.N, p.K}, x);
+    ws = plain<float>(a[7], "ws", kF32, {nb, kb}, x);
   } else {
-    wq = plain(a[6], "wq", kE4m3, {p.E, p.N, p.K});
-    ws = plain<float>(a[7], "ws", kF32, {p.E, nb, kb});
+    wq = plain(a[6], "wq", kE4m3, {p.E, p.N, p.K}, x);
+    ws = plain<float>(a[7], "ws", kF32, {p.E, nb, kb}, x);
   }
-  const int32_t* off = offsets_of(a[8], p.E);
+  const int32_t* off = offsets_of(a[8], p.E, x);
   const at::ScalarType ot = dtype_of(a[10]);
+  const c10::cuda::CUDAGuard guard(x.device());
   at::Tensor out = output(a[9], {rows, p.N}, ot, x);
   const int64_t ldo = pitch(out, "out");
   check_rc(ag_fp8_forward(p.plan, rows, xq, xs, off, wq, ws, out.data_ptr(), ldo, type_code(ot), stream_of(x)));

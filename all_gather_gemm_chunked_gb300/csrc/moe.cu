@@ -521,6 +521,11 @@ void ag_moe_plan_destroy(ag_moe_plan* plan) {
   free_plan(plan);
 }
 
+int ag_moe_plan_device(const ag_moe_plan* plan) {
+  if (!plan) return fail(AG_GEMM_ERR_INVALID, "plan is NULL");
+  return plan->device;
+}
+
 int64_t ag_moe_plan_status_word(ag_moe_plan* plan) {
   if (!plan) return fail(AG_GEMM_ERR_INVALID, "plan is NULL");
   DeviceGuard dg(plan->device);

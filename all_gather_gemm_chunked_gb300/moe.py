@@ -11,6 +11,9 @@ A layer's forward pass::
     y = down.forward(act(h), r.offsets, w_down)
     out = combine(y, r.slots, r.weights)
 
+The tensors of a call, its plan and its stream are on one device, which need not be the
+current one.
+
 ``stream`` (every function): a torch stream, None for the current one.  Outputs are
 allocated on it; inputs written on another stream need the caller's event, as in any
 torch program.
@@ -40,6 +43,9 @@ class Routing(NamedTuple):
 
 def _on(stream, fn, *args):
     """fn(*args) with `stream` current: outputs are allocated on it."""
+    first = next((a for a in args if isinstance(a, torch.Tensor)), None)
+    if first is not None and first.is_cuda and first.device != stream.device:
+        raise ValueError(f"stream is on device {stream.device}, the call's first tensor on {first.device}")
     with torch.cuda.stream(stream):
         return fn(*args)
 
