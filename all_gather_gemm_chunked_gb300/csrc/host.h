@@ -23,6 +23,31 @@ int encode_tiled(CUtensorMap* map, CUtensorMapDataType type, const void* base, i
                  const cuuint64_t* dims, const cuuint64_t* strides_bytes, const cuuint32_t* box,
                  CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
+// Clears a new plan's memory on a stream of its own and waits for that: a memset on the
+// default stream would come behind that stream's work, and so perhaps behind (or into) the
+// plan's first run on a stream that does not wait for the default one.
+class Clearer {
+ public:
+  Clearer() : e_(cudaStreamCreateWithFlags(&stream_, cudaStreamNonBlocking)) {}
+  ~Clearer() {
+    if (stream_) cudaStreamDestroy(stream_);
+  }
+  Clearer(const Clearer&) = delete;
+  Clearer& operator=(const Clearer&) = delete;
+  cudaError_t clear(void* p, size_t bytes) {
+    if (e_ == cudaSuccess) e_ = cudaMemsetAsync(p, 0, bytes, stream_);
+    return e_;
+  }
+  cudaError_t finish() {
+    if (e_ == cudaSuccess) e_ = cudaStreamSynchronize(stream_);
+    return e_;
+  }
+
+ private:
+  cudaStream_t stream_ = nullptr;
+  cudaError_t e_;
+};
+
 // Makes `dev` current; restores the caller's current device on scope exit.
 struct DeviceGuard {
   int prev = -1;

@@ -500,10 +500,12 @@ ag_moe_plan* ag_moe_plan_create(int E, int64_t K, int64_t N, int dtype) {
   p->pairs = pre.pairs;
   p->arrival_count = static_cast<int64_t>(max_units(true)) * 2 * agg::kXEpiWarps;
   const size_t words = static_cast<size_t>(4 + p->arrival_count) * sizeof(uint32_t);
+  agg::Clearer clearer;
   if ((e = cudaMalloc(&p->status, words)) != cudaSuccess ||
-      (e = cudaMemset(p->status, 0, words)) != cudaSuccess ||
+      (e = clearer.clear(p->status, words)) != cudaSuccess ||
       (e = cudaMalloc(&p->partials, static_cast<size_t>(kPartialBytes))) != cudaSuccess ||
-      (e = cudaEventCreateWithFlags(&p->done, cudaEventDisableTiming)) != cudaSuccess) {
+      (e = cudaEventCreateWithFlags(&p->done, cudaEventDisableTiming)) != cudaSuccess ||
+      (e = clearer.finish()) != cudaSuccess) {
     cuda_fail(e, "plan allocation");
     free_plan(p);
     return nullptr;
