@@ -35,7 +35,7 @@ class Clearer {
   Clearer(const Clearer&) = delete;
   Clearer& operator=(const Clearer&) = delete;
   cudaError_t clear(void* p, size_t bytes) {
-    if (e_ == cudaSuccess) e_ = cudaMemsetAsync(p, 0, bytes, stream_);
+    if (e_ == cudaSuccess && bytes > 0) e_ = cudaMemsetAsync(p, 0, bytes, stream_);
     return e_;
   }
   cudaError_t finish() {

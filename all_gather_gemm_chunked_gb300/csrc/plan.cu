@@ -752,28 +752,30 @@ ag_gemm_plan* create_plan(int n_shards, int64_t M, int64_t K, int64_t N, int dty
   }
   // one counter per chunk; on the skinny path one per (k-part, chunk)
   p->counter_count = slots * g.Q * (skinny ? p->sk_np : 1);
+  agg::Clearer clearer;
   if ((e = cudaMalloc(&p->staging, p->staging_bytes)) != cudaSuccess ||
       (e = cudaMalloc(&p->counters, sizeof(uint32_t) * p->counter_count)) != cudaSuccess ||
       (e = cudaMalloc(&p->item_counter, sizeof(unsigned long long))) != cudaSuccess ||
-      (e = cudaMemset(p->item_counter, 0, sizeof(unsigned long long))) != cudaSuccess ||
+      (e = clearer.clear(p->item_counter, sizeof(unsigned long long))) != cudaSuccess ||
       (e = cudaMalloc(&p->tile_counter, sizeof(unsigned long long))) != cudaSuccess ||
-      (e = cudaMemset(p->tile_counter, 0, sizeof(unsigned long long))) != cudaSuccess ||
+      (e = clearer.clear(p->tile_counter, sizeof(unsigned long long))) != cudaSuccess ||
       (e = cudaMalloc(&p->status, 2 * sizeof(uint32_t))) != cudaSuccess ||
-      (e = cudaMemset(p->counters, 0, sizeof(uint32_t) * p->counter_count)) != cudaSuccess ||
-      (e = cudaMemset(p->status, 0, 2 * sizeof(uint32_t))) != cudaSuccess ||
+      (e = clearer.clear(p->counters, sizeof(uint32_t) * p->counter_count)) != cudaSuccess ||
+      (e = clearer.clear(p->status, 2 * sizeof(uint32_t))) != cudaSuccess ||
       (e = cudaEventCreateWithFlags(&p->done, cudaEventDisableTiming)) != cudaSuccess ||
       (p->window > 0 &&
        ((e = cudaMalloc(&p->credits, sizeof(uint32_t) * p->window)) != cudaSuccess ||
-        (e = cudaMemset(p->credits, 0, sizeof(uint32_t) * p->window)) != cudaSuccess)) ||
+        (e = clearer.clear(p->credits, sizeof(uint32_t) * p->window)) != cudaSuccess)) ||
       (p->partials_bytes > 0 &&
        ((e = cudaMalloc(&p->partials, static_cast<size_t>(p->partials_bytes))) != cudaSuccess ||
         (e = cudaMalloc(&p->part_flags, sizeof(uint32_t) * tail)) != cudaSuccess ||
-        (e = cudaMemset(p->part_flags, 0, sizeof(uint32_t) * tail)) != cudaSuccess)) ||
+        (e = clearer.clear(p->part_flags, sizeof(uint32_t) * tail)) != cudaSuccess)) ||
       (p->zero_tasks > 0 &&
        ((e = cudaMalloc(&p->zero_ticket, sizeof(unsigned long long))) != cudaSuccess ||
-        (e = cudaMemset(p->zero_ticket, 0, sizeof(unsigned long long))) != cudaSuccess ||
+        (e = clearer.clear(p->zero_ticket, sizeof(unsigned long long))) != cudaSuccess ||
         (e = cudaMalloc(&p->zero_done, sizeof(uint32_t))) != cudaSuccess ||
-        (e = cudaMemset(p->zero_done, 0, sizeof(uint32_t))) != cudaSuccess))) {
+        (e = clearer.clear(p->zero_done, sizeof(uint32_t))) != cudaSuccess)) ||
+      (e = clearer.finish()) != cudaSuccess) {
     cuda_fail(e, "plan allocation");
     free_plan(p);
     return nullptr;
@@ -1044,7 +1046,8 @@ int ag_gemm_plan_set_trace(ag_gemm_plan* plan, int64_t capacity) {
   void* buf = nullptr;
   const size_t bytes = 32 + static_cast<size_t>(capacity) * sizeof(agg::TraceEvent);
   if ((e = cudaMalloc(&buf, bytes)) != cudaSuccess) return cuda_fail(e, "trace allocation");
-  if ((e = cudaMemset(buf, 0, 32)) != cudaSuccess) {
+  agg::Clearer clearer;
+  if ((e = clearer.clear(buf, 32)) != cudaSuccess || (e = clearer.finish()) != cudaSuccess) {
     cudaFree(buf);
     return cuda_fail(e, "trace allocation");
   }

@@ -1,0 +1,40 @@
+"""AllGather+GEMM plans and streams: a new plan's cleared counters, runs from several
+threads' default streams."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from all_gather_gemm_chunked_gb300 import binding as B_  # noqa: E402
+from all_gather_gemm_chunked_gb300.plan import Plan  # noqa: E402
+
+CYCLES_PER_MS = 2_000_000  # at about 2 GHz
+
+
+def _problem(M=512, K=256, N=256):
+    g = torch.Generator(device="cuda").manual_seed(5)
+    a = torch.randint(-3, 4, (M, K), generator=g, device="cuda").half()  # exact sums
+    b = torch.randint(-3, 4, (K, N), generator=g, device="cuda").half()
+    return list(a.chunk(2)), b, (a.double() @ b.double()).float()
+
+
+def test_a_new_plan_is_clean_on_any_stream():
+    """Work waits on the default stream while a plan is made and used on a stream that does
+    not wait for it: the counters are clear before the first run, and stay after it."""
+    shards, b, want = _problem()
+    s = torch.cuda.Stream()
+    for wait_ms in (0, 300):  # (the first time loads the kernels, which waits for the device)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(wait_ms * CYCLES_PER_MS)
+        with Plan(2, 512, 256, 256) as p, torch.cuda.stream(s):
+            first = p.run(shards, b)
+            s.synchronize()
+            torch.cuda.synchronize()
+            second = p.run(shards, b)
+            s.synchronize()
+            assert p.status() == B_.OK
+        assert torch.equal(first, want) and torch.equal(second, want)
