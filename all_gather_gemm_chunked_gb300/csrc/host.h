@@ -48,6 +48,23 @@ class Clearer {
   cudaError_t e_;
 };
 
+// The stream of a plan's last run, by the number that no other stream has: one handle
+// stands for every thread's own default stream, and a destroyed stream's may be given to a
+// new one while its work is pending.
+class LastStream {
+ public:
+  // Whether `stream` has to wait for the last run's event: it is another, or cannot be told.
+  bool other(cudaStream_t stream) const { return id_ == 0 || number(stream) != id_; }
+  void set(cudaStream_t stream) { id_ = number(stream); }
+
+ private:
+  static unsigned long long number(cudaStream_t stream) {
+    unsigned long long n = 0;
+    return cudaStreamGetId(stream, &n) == cudaSuccess ? n + 1 : 0;
+  }
+  unsigned long long id_ = 0;  // the number plus 1
+};
+
 // Makes `dev` current; restores the caller's current device on scope exit.
 struct DeviceGuard {
   int prev = -1;

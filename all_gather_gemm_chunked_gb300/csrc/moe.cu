@@ -98,7 +98,7 @@ struct ag_moe_plan {
   // behind it, and the next such run on another stream waits for it.  Others share
   // nothing with it but the status word; an event behind each would cost a call a
   // quarter of its host time (4.5 us against 3.4).
-  cudaStream_t last_stream = nullptr;
+  agg::LastStream last_stream;
   bool has_run = false;
   bool loose = false;  // a run without an event since the last status or reset
 };
@@ -262,7 +262,7 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   cudaError_t e = cudaStreamIsCapturing(stream, &capture);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
   const bool captured = capture != cudaStreamCaptureStatusNone;
-  if (split && !captured && p->has_run && p->last_stream != stream &&
+  if (split && !captured && p->has_run && p->last_stream.other(stream) &&
       (e = cudaStreamWaitEvent(stream, p->done, 0)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamWaitEvent");
   // no more pairs than there can be units
@@ -275,7 +275,7 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
     p->loose = true;
   } else if (!captured) {
     if ((e = cudaEventRecord(p->done, stream)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
-    p->last_stream = stream;
+    p->last_stream.set(stream);
     p->has_run = true;
   }
   log_msg(3, "plan %p: experts product %d enqueued, %d rows", static_cast<void*>(p), op, x.rows);
@@ -558,7 +558,7 @@ int ag_moe_plan_reset(ag_moe_plan* plan, void* stream_v) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
   cudaError_t e;
   if (plan->loose && (e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-  if (!plan->loose && plan->has_run && plan->last_stream != stream &&
+  if (!plan->loose && plan->has_run && plan->last_stream.other(stream) &&
       (e = cudaStreamWaitEvent(stream, plan->done, 0)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamWaitEvent");
   plan->loose = false;
@@ -566,7 +566,7 @@ int ag_moe_plan_reset(ag_moe_plan* plan, void* stream_v) {
                            stream)) != cudaSuccess ||
       (e = cudaEventRecord(plan->done, stream)) != cudaSuccess)
     return cuda_fail(e, "plan reset");
-  plan->last_stream = stream;
+  plan->last_stream.set(stream);
   plan->has_run = true;
   return AG_GEMM_OK;
 }

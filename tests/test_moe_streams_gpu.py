@@ -17,6 +17,7 @@ from all_gather_gemm_chunked_gb300 import moe  # noqa: E402
 from moe_util import randn, rng  # noqa: E402
 
 CYCLES_PER_MS = 2_000_000  # at about 2 GHz
+PER_THREAD = 2             # the handle of a host thread's own default stream
 
 
 def test_a_new_plan_is_clean_on_any_stream():
@@ -33,3 +34,58 @@ def test_a_new_plan_is_clean_on_any_stream():
             s.synchronize()
             torch.cuda.synchronize()
             assert p.status() == B_.ERR_INVALID
+
+
+def _split_product():
+    """One expert whose sums are split, and its operands."""
+    g = rng(3)
+    return randn(g, (48, 4096), torch.bfloat16), randn(g, (1, 4096, 512), torch.bfloat16, 1 / 64)
+
+
+def test_runs_on_two_threads_default_streams_are_ordered():
+    """The per-thread default stream has one handle in every thread, but is not one stream:
+    a run that shares the workspace with one of another thread waits for it."""
+    x, w = _split_product()
+    s = torch.cuda.ExternalStream(PER_THREAD)
+    queued, over = threading.Event(), threading.Event()
+    with moe.Experts(1, 4096, 512) as p:
+        want = p.forward(x, None, w)
+        p.forward(x, None, w, stream=s)
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(0)
+        torch.cuda.synchronize()
+
+        def first():
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(400 * CYCLES_PER_MS)
+                p.forward(x, None, w)
+            queued.set()
+            over.wait()  # (a thread's stream ends with it)
+
+        t = threading.Thread(target=first)
+        t.start()
+        queued.wait()
+        try:
+            got = p.forward(x, None, w, stream=s)
+            done = torch.cuda.Event()
+            done.record(s)
+            time.sleep(0.05)
+            early = done.query()
+            torch.cuda.synchronize()
+        finally:
+            over.set()
+            t.join()
+        assert not early
+        assert torch.equal(got, want) and p.status() == B_.OK
+
+
+def test_a_run_behind_its_own_stream_and_a_reset():
+    x, w = _split_product()
+    s = torch.cuda.Stream()
+    with moe.Experts(1, 4096, 512) as p:
+        want = p.forward(x, None, w)
+        for stream in (s, None, s):
+            p.reset(stream)
+            got = [p.forward(x, None, w, stream=s) for _ in range(3)] + [p.forward(x, None, w)]
+            torch.cuda.synchronize()
+            assert p.status() == B_.OK and all(torch.equal(g, want) for g in got)
