@@ -1,5 +1,8 @@
 """AllGather+GEMM plans and streams: a new plan's cleared counters, runs from several
 threads' default streams."""
+import threading
+import time
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -13,6 +16,7 @@ from all_gather_gemm_chunked_gb300 import binding as B_  # noqa: E402
 from all_gather_gemm_chunked_gb300.plan import Plan  # noqa: E402
 
 CYCLES_PER_MS = 2_000_000  # at about 2 GHz
+PER_THREAD = 2             # the handle of a host thread's own default stream
 
 
 def _problem(M=512, K=256, N=256):
@@ -38,3 +42,40 @@ def test_a_new_plan_is_clean_on_any_stream():
             s.synchronize()
             assert p.status() == B_.OK
         assert torch.equal(first, want) and torch.equal(second, want)
+
+
+def test_runs_on_two_threads_default_streams_are_ordered():
+    """The per-thread default stream has one handle in every thread, but is not one stream."""
+    shards, b, want = _problem()
+    s = torch.cuda.ExternalStream(PER_THREAD)
+    queued, over = threading.Event(), threading.Event()
+    with Plan(2, 512, 256, 256) as p:
+        with torch.cuda.stream(s):
+            p.run(shards, b)
+            torch.cuda._sleep(0)
+        torch.cuda.synchronize()
+        got = []
+
+        def first():
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(400 * CYCLES_PER_MS)
+                got.append(p.run(shards, b))
+            queued.set()
+            over.wait()  # (a thread's stream ends with it)
+
+        t = threading.Thread(target=first)
+        t.start()
+        queued.wait()
+        try:
+            with torch.cuda.stream(s):
+                got.append(p.run(shards, b))
+                done = torch.cuda.Event()
+                done.record(s)
+            time.sleep(0.05)
+            early = done.query()
+            torch.cuda.synchronize()
+        finally:
+            over.set()
+            t.join()
+        assert not early and p.status() == B_.OK
+        assert all(torch.equal(c, want) for c in got)
