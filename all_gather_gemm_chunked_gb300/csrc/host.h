@@ -53,16 +53,26 @@ class Clearer {
 // new one while its work is pending.
 class LastStream {
  public:
-  // Whether `stream` has to wait for the last run's event: it is another, or cannot be told.
-  bool other(cudaStream_t stream) const { return id_ == 0 || number(stream) != id_; }
-  void set(cudaStream_t stream) { id_ = number(stream); }
+  bool other(cudaStream_t stream) const {
+    const unsigned long long n = id_ ? number(stream) : 0;
+    return n ? n != id_ : stream != handle_;
+  }
+  void set(cudaStream_t stream) {
+    handle_ = stream;
+    id_ = number(stream);
+  }
 
  private:
+  // The number plus 1; 0 while the stream is captured (to ask for it would end the
+  // capture): handles are compared then.
   static unsigned long long number(cudaStream_t stream) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     unsigned long long n = 0;
+    if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) return 0;
     return cudaStreamGetId(stream, &n) == cudaSuccess ? n + 1 : 0;
   }
-  unsigned long long id_ = 0;  // the number plus 1
+  cudaStream_t handle_ = nullptr;
+  unsigned long long id_ = 0;
 };
 
 // Makes `dev` current; restores the caller's current device on scope exit.

@@ -79,3 +79,23 @@ def test_runs_on_two_threads_default_streams_are_ordered():
             t.join()
         assert not early and p.status() == B_.OK
         assert all(torch.equal(c, want) for c in got)
+
+
+def test_a_run_in_a_cuda_graph():
+    """A run behind another on the capturing stream, captured and replayed once."""
+    shards, b, want = _problem()
+    s = torch.cuda.Stream()
+    out = torch.empty_like(want)
+    for mode in (B_.MODE_PIPELINED, B_.MODE_COMPUTE_ONLY):
+        with Plan(2, 512, 256, 256) as p:
+            with torch.cuda.stream(s):
+                p.run(shards, b, out)
+            torch.cuda.synchronize()
+            p.set_mode(mode)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                p.run(shards, b, out)
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
