@@ -101,6 +101,10 @@ struct ag_moe_plan {
   agg::LastStream last_stream;
   bool has_run = false;
   bool loose = false;  // a run without an event since the last status or reset
+  // The same inside a graph capture: branches of one capture are put in order.
+  cudaEvent_t captured = nullptr;
+  agg::LastStream captured_stream;
+  unsigned long long capture_id = 0;
 };
 
 namespace {
@@ -143,6 +147,7 @@ Prepared prepare_once(int device) {
 
 void free_plan(ag_moe_plan* p) {
   if (p->done) cudaEventDestroy(p->done);
+  if (p->captured) cudaEventDestroy(p->captured);
   if (p->status) cudaFree(p->status);
   if (p->partials) cudaFree(p->partials);
   delete p;
@@ -256,14 +261,16 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   const bool split = !plenty && may_split(kb, agg::split_price(fp8 && !few ? agg::kOpFp8Long : op,
                                                     op == agg::kOpWeight ? x.step < agg::kXRows : few));
   x.max_units = split ? max_units(few) : 0;
-  // A captured run is ordered by its graph: an event of the stream outside cannot be
+  // A captured run is ordered by its graph: an event of the streams outside cannot be
   // waited on there, nor one of the graph outside.
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-  cudaError_t e = cudaStreamIsCapturing(stream, &capture);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+  unsigned long long capture_id = 0;
+  cudaError_t e = cudaStreamGetCaptureInfo(stream, &capture, &capture_id);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetCaptureInfo");
   const bool captured = capture != cudaStreamCaptureStatusNone;
-  if (split && !captured && p->has_run && p->last_stream.other(stream) &&
-      (e = cudaStreamWaitEvent(stream, p->done, 0)) != cudaSuccess)
+  const bool wait = captured ? p->capture_id == capture_id && p->captured_stream.other(stream)
+                             : p->has_run && p->last_stream.other(stream);
+  if (split && wait && (e = cudaStreamWaitEvent(stream, captured ? p->captured : p->done, 0)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamWaitEvent");
   // no more pairs than there can be units
   const int64_t parts = !split ? 1 : kb / agg::kMinPart < agg::kMaxSplit ? kb / agg::kMinPart : agg::kMaxSplit;
@@ -273,8 +280,12 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
     return cuda_fail(e, "experts kernel launch");
   if (!split) {
     p->loose = true;
-  } else if (!captured) {
-    if ((e = cudaEventRecord(p->done, stream)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
+  } else if ((e = cudaEventRecord(captured ? p->captured : p->done, stream)) != cudaSuccess) {
+    return cuda_fail(e, "cudaEventRecord");
+  } else if (captured) {
+    p->captured_stream.set(stream);
+    p->capture_id = capture_id;
+  } else {
     p->last_stream.set(stream);
     p->has_run = true;
   }
@@ -505,6 +516,7 @@ ag_moe_plan* ag_moe_plan_create(int E, int64_t K, int64_t N, int dtype) {
       (e = clearer.clear(p->status, words)) != cudaSuccess ||
       (e = cudaMalloc(&p->partials, static_cast<size_t>(kPartialBytes))) != cudaSuccess ||
       (e = cudaEventCreateWithFlags(&p->done, cudaEventDisableTiming)) != cudaSuccess ||
+      (e = cudaEventCreateWithFlags(&p->captured, cudaEventDisableTiming)) != cudaSuccess ||
       (e = clearer.finish()) != cudaSuccess) {
     cuda_fail(e, "plan allocation");
     free_plan(p);

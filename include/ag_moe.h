@@ -111,8 +111,8 @@ int ag_fp8_quantize_weights(int E, int64_t K, int64_t N, int dtype, const void *
  * == 0, N % 8 == 0).  It owns the workspace of the products that split their sums and
  * the status word; runs on one plan that may use the workspace are serialised as those
  * of ag_gemm.h are, others may overlap where their streams let them.  Runs may be
- * captured into a CUDA graph; a replay is then the caller's to keep apart from the
- * plan's other runs, and to wait for before the status is read.
+ * captured into a CUDA graph, on several branches of it too; a replay is then the caller's
+ * to keep apart from the plan's other runs, and to wait for before the status is read.
  *
  * offsets are the E + 1 row offsets on the device (NULL: one group of all rows,
  * E must be 1).  They must not decrease and must lie within [0, rows]; otherwise

@@ -89,3 +89,27 @@ def test_a_run_behind_its_own_stream_and_a_reset():
             got = [p.forward(x, None, w, stream=s) for _ in range(3)] + [p.forward(x, None, w)]
             torch.cuda.synchronize()
             assert p.status() == B_.OK and all(torch.equal(g, want) for g in got)
+
+
+def test_branches_of_a_captured_graph_are_ordered():
+    """Two streams of one capture run products that share the plan's workspace."""
+    x, w = _split_product()
+    xs = [x, x * 2, x * 3, x * 4]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    with moe.Experts(1, 4096, 512) as p:
+        want = [p.forward(t, None, w) for t in xs]
+        torch.cuda.synchronize()
+        for _ in range(2):  # (a second capture knows nothing of the first one's events)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=a):
+                b.wait_stream(a)
+                got = [p.forward(t, None, w, stream=s) for t, s in zip(xs, (a, b, a, b))]
+                a.wait_stream(b)
+            for _ in range(20):
+                for t in got:
+                    t.zero_()
+                graph.replay()
+                torch.cuda.synchronize()
+                assert all(torch.equal(g, t) for g, t in zip(got, want))
+        assert all(torch.equal(p.forward(t, None, w), y) for t, y in zip(xs, want))
+        assert p.status() == B_.OK
