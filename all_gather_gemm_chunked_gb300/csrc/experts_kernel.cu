@@ -1272,7 +1272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       scale_long_role<BN>(p, table, ring, rank, lane);
     }
   } else if (threadIdx.x == 0) {
-    set_status(p.status, kStatusOffsets, 0);
+    set_status(p.status + 2, kStatusOffsets, 0);
   }
   tc_fence_before();
   // This CTA's epilogue has waited for every accumulator of the pair, so every MMA and load

@@ -54,7 +54,8 @@ struct ExpertsParams {
   float* partials;               // split sums: [unit][warps of the pair][columns][32 lanes]
   uint32_t* arrivals;            // [tile][warps of the pair], zero between runs
   int32_t max_units;             // units the workspace holds (0: never split)
-  uint32_t* status;              // [2]: status word, detail
+  uint32_t* status;              // [4]: status word and detail of a wait that ran out, which ends the waits
+                                 // of later runs too; the same of bad offsets, which concern their run alone
   uint64_t timeout_ns;
 };
 

@@ -88,7 +88,7 @@ struct ag_moe_plan {
   int dtype = 0;
   int device = 0;
   int pairs = 0;
-  uint32_t* status = nullptr;    // [2], then the arrival counters
+  uint32_t* status = nullptr;    // [4], then the arrival counters
   uint32_t* arrivals = nullptr;
   int64_t arrival_count = 0;
   float* partials = nullptr;
@@ -548,10 +548,11 @@ int64_t ag_moe_plan_status_word(ag_moe_plan* plan) {
   if (!plan->loose && plan->has_run && (e = cudaEventSynchronize(plan->done)) != cudaSuccess)
     return cuda_fail(e, "cudaEventSynchronize");
   plan->loose = false;
-  uint32_t w[2] = {0, 0};
+  uint32_t w[4] = {0, 0, 0, 0};
   if ((e = cudaMemcpy(w, plan->status, sizeof(w), cudaMemcpyDeviceToHost)) != cudaSuccess)
     return cuda_fail(e, "status read");
-  return static_cast<int64_t>(w[0]) | (static_cast<int64_t>(w[1]) << 32);
+  const int i = w[0] != agg::kStatusOk ? 0 : 2;
+  return static_cast<int64_t>(w[i]) | (static_cast<int64_t>(w[i + 1]) << 32);
 }
 
 int ag_moe_plan_status(ag_moe_plan* plan) {

@@ -127,8 +127,11 @@ ag_moe_plan *ag_moe_plan_create(int E, int64_t K, int64_t N, int dtype);
 void ag_moe_plan_destroy(ag_moe_plan *plan);
 /* The device that was current when the plan was made, and that its runs take place on. */
 int ag_moe_plan_device(const ag_moe_plan *plan);
-/* Waits for the plan's runs (for the device, if some left no event); AG_GEMM_OK, AG_GEMM_ERR_TIMEOUT (a bounded wait in
- * the kernel ran out) or AG_GEMM_ERR_INVALID (offsets, see above). */
+/* Waits for the plan's runs (for the device, if some left no event).  AG_GEMM_OK;
+ * AG_GEMM_ERR_TIMEOUT: a bounded wait in the kernel ran out, the results of that run and
+ * of all runs until ag_moe_plan_reset are undefined; AG_GEMM_ERR_INVALID: a run had offsets
+ * that are none (see above) and wrote nothing, other runs are not affected.  Both stay
+ * until ag_moe_plan_reset. */
 int ag_moe_plan_status(ag_moe_plan *plan);
 int64_t ag_moe_plan_status_word(ag_moe_plan *plan);
 /* Back to AG_GEMM_OK and a clean workspace after a failed run. */
