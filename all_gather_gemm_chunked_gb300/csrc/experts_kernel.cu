@@ -338,7 +338,9 @@ struct Schedule {
     nt = pre[lo + 1] - pre[lo];
     // its rows in nt tiles of equal height, a multiple of 32 (rows on the M side: 256)
     const int32_t cnt = off[lo + 1] - off[lo];
-    height = OP == kOpFp8Long ? BN : ((nt == 1 ? cnt : (cnt + nt - 1) / nt) + 31) & ~31;
+    // (unsigned: the sum passes 2^31 for a group of more than 2.139e9 rows)
+    const uint32_t most = nt == 1 ? cnt : (static_cast<uint32_t>(cnt) + nt - 1u) / static_cast<uint32_t>(nt);
+    height = OP == kOpFp8Long ? BN : static_cast<int32_t>((most + 31u) & ~31u);
   }
 
   __device__ __forceinline__ bool get(int32_t i, Unit& u) {

@@ -124,6 +124,10 @@ bool may_split(int64_t KB, agg::SplitPrice price) {
   return false;
 }
 
+// Rows of a product: with a tile's height beyond them, row numbers stay below 2^31.
+constexpr int64_t kMaxRows = (1LL << 31) - 256;
+static_assert(agg::kXRows <= 256 && agg::kXSub * 64 <= 256, "rows beyond the last that a tile or a stage reaches");
+
 // k-blocks of a segment where the output is fp32.
 constexpr int kSegment = 8;
 
@@ -209,8 +213,8 @@ int check_run(ag_moe_plan* p, bool fp8, int64_t rows, const int32_t* offsets, in
   if ((p->dtype == AG_MOE_E4M3) != fp8)
     return fail(AG_GEMM_ERR_INVALID, fp8 ? "ag_fp8_forward needs an AG_MOE_E4M3 plan"
                                          : "this product needs an fp16 or bf16 plan (AG_MOE_E4M3: ag_fp8_forward)");
-  if (rows < 0 || rows >= (1LL << 31))
-    return fail(AG_GEMM_ERR_INVALID, "rows must be in [0, 2^31) (got %lld)", (long long)rows);
+  if (rows < 0 || rows > kMaxRows)
+    return fail(AG_GEMM_ERR_INVALID, "rows must be in [0, %lld] (got %lld)", (long long)kMaxRows, (long long)rows);
   if (!offsets && p->E != 1)
     return fail(AG_GEMM_ERR_INVALID, "offsets may be NULL only for one expert (the plan has %d)", p->E);
   const bool ok = out_dtype == AG_MOE_F32 ||

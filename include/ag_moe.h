@@ -117,7 +117,7 @@ int ag_fp8_quantize_weights(int E, int64_t K, int64_t N, int dtype, const void *
  * offsets are the E + 1 row offsets on the device (NULL: one group of all rows,
  * E must be 1).  They must not decrease and must lie within [0, rows]; otherwise
  * the run writes nothing and the plan's status becomes AG_GEMM_ERR_INVALID.  Rows
- * of no group are not written.  rows < 2^31.  out_dtype is the operands' type (for
+ * of no group are not written.  rows <= 2^31 - 256.  out_dtype is the operands' type (for
  * AG_MOE_E4M3: AG_GEMM_F16 or AG_GEMM_BF16) or AG_MOE_F32.
  */
 enum { AG_MOE_E4M3 = 4 };
