@@ -154,7 +154,10 @@ int ag_moe_backward_weight(ag_moe_plan *plan, int64_t rows, const void *x, int64
                            int out_dtype, void *stream);
 /* y[r][n] = sum over the blocks b of K of xs[b][r] * ws[e][n / 128][b] * (the block's
  * sum of xq * wq), with the operands that ag_fp8_quantize_rows and
- * ag_fp8_quantize_weights write (an AG_MOE_E4M3 plan). */
+ * ag_fp8_quantize_weights write (an AG_MOE_E4M3 plan).  The two scales are multiplied
+ * first, in float: a product below 2^-126 costs a block's share up to 2^-125 beside the
+ * usual roundings; one beyond the largest float counts as that float (a sum of zero stays
+ * zero). */
 int ag_fp8_forward(ag_moe_plan *plan, int64_t rows, const void *xq, const float *xs,
                    const int32_t *offsets, const void *wq, const float *ws, void *y, int64_t ldy,
                    int out_dtype, void *stream);
