@@ -9,6 +9,8 @@
 
 #include <Python.h>
 
+#include <optional>
+
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -163,6 +165,15 @@ struct Pieces {
   }
 };
 
+// Makes a tensor's device current for a scope.  (A guard where it is so already takes two
+// driver calls to give back what it did not change.)
+struct Current {
+  std::optional<c10::cuda::CUDAGuard> guard;
+  explicit Current(const at::Tensor& t) {
+    if (c10::cuda::current_device() != t.device().index()) guard.emplace(t.device());
+  }
+};
+
 void* stream_of(const at::Tensor& t) {
   return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
 }
@@ -205,7 +216,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int k = to_int32(a[1], "top_k");
   if (E > AG_MOE_MAX_EXPERTS) check_rc(ag_moe_route_workspace(T, AG_MOE_MAX_EXPERTS + 1, k));
   const int64_t size = check_rc(ag_moe_route_workspace(T, static_cast<int>(E), k));
-  const c10::cuda::CUDAGuard guard(z.device());
+  const Current current(z);
   Pieces pieces(4 * Pieces::room(T * k * 4) + Pieces::room((E + 1) * 4), z);
   at::Tensor w = pieces.take({T, k}, kF32), e = pieces.take({T, k}, kI32), off = pieces.take({E + 1}, kI32),
              order = pieces.take({T * k}, kI32), slots = pieces.take({T, k}, kI32), ws;
@@ -237,7 +248,7 @@ PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float* w = plain<float>(a[1], "routing.weights", kF32, {T, k}, z);
   const int32_t* e = plain<int32_t>(a[2], "routing.experts", kI32, {T, k}, z);
   const float* dw = plain<float>(a[3], "dweights", kF32, {T, k}, z);
-  const c10::cuda::CUDAGuard guard(z.device());
+  const Current current(z);
   at::Tensor out = make({T, E}, z.scalar_type(), z);
   check_rc(ag_moe_route_backward(T, static_cast<int>(E), static_cast<int>(k), type, z.data_ptr(), ld,
                                  PyObject_IsTrue(a[4]), w, e, dw, out.data_ptr(), stream_of(z)));
@@ -255,7 +266,7 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& slots = tensor(a[2], "routing.slots", x);
   const int64_t k = slots.dim() == 2 ? slots.size(1) : 0;
   const int32_t* order = plain<int32_t>(a[1], "routing.order", kI32, {T * k}, x);
-  const c10::cuda::CUDAGuard guard(x.device());
+  const Current current(x);
   at::Tensor out = make({T * k, H}, x.scalar_type(), x);
   check_rc(ag_moe_gather(T, static_cast<int>(k), H, type, x.data_ptr(), ld, order, out.data_ptr(), stream_of(x)));
   return wrap(out);
@@ -286,7 +297,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t ld = pitch(y, "y"), H = y.size(1);
   const Choices c = choices(a[1], y);
   const float* w = a[2] == Py_None ? nullptr : plain<float>(a[2], "weights", kF32, {c.T, c.k}, y);
-  const c10::cuda::CUDAGuard guard(y.device());
+  const Current current(y);
   at::Tensor out = make({c.T, H}, y.scalar_type(), y);
   check_rc(ag_moe_combine(c.T, static_cast<int>(c.k), H, type, y.data_ptr(), ld, c.slots, w, out.data_ptr(),
                           stream_of(y)));
@@ -313,7 +324,7 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (m < 1) raise(PyExc_ValueError, "offsets must not be empty");
     end = plain<int32_t>(a[4], "offsets", kI32, {m}, y) + m - 1;
   }
-  const c10::cuda::CUDAGuard guard(y.device());
+  const Current current(y);
   at::Tensor dy = make({c.T * c.k, H}, y.scalar_type(), y), dw = make({c.T, c.k}, kF32, y);
   check_rc(ag_moe_combine_backward(c.T, static_cast<int>(c.k), H, type, d.data_ptr(), ldd, y.data_ptr(), ld,
                                    c.slots, w, end, dy.data_ptr(), static_cast<float*>(dw.data_ptr()),
@@ -337,7 +348,7 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     rows = src * k;
     order = plain<int32_t>(a[1], "routing.order", kI32, {rows}, x);
   }
-  const c10::cuda::CUDAGuard guard(x.device());
+  const Current current(x);
   Pieces pieces(Pieces::room(rows * K) + Pieces::room(blocks(K) * rows * 4), x);
   at::Tensor q = pieces.take({rows, K}, kE4m3), s = pieces.take({blocks(K), rows}, kF32);
   check_rc(ag_fp8_quantize_rows(rows, K, type, x.data_ptr(), ld, src, order, static_cast<int>(k), q.data_ptr(),
@@ -356,7 +367,7 @@ PyObject* quantize_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
     raise(PyExc_ValueError, "w must be a contiguous (E, K, N) or (K, N) tensor");
   const bool many = w.dim() == 3;
   const int64_t E = many ? w.size(0) : 1, K = w.size(-2), N = w.size(-1);
-  const c10::cuda::CUDAGuard guard(w.device());
+  const Current current(w);
   at::Tensor q = make({E, N, K}, kE4m3, w), s = make({E, blocks(N), blocks(K)}, kF32, w);
   if (E > AG_MOE_MAX_EXPERTS) raise(PyExc_ValueError, "w has too many experts");
   check_rc(ag_fp8_quantize_weights(static_cast<int>(E), K, N, type, w.data_ptr(), q.data_ptr(),
@@ -425,7 +436,7 @@ PyObject* rows_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ldw_e = w.stride(0);
   }
   const at::ScalarType ot = a[10] == Py_None ? type : dtype_of(a[10]);
-  const c10::cuda::CUDAGuard guard(x.device());
+  const Current current(x);
   at::Tensor out = output(a[9], {rows, wide}, ot, x);
   const int64_t ldo = pitch(out, "out");
   check_rc((back ? ag_moe_backward_input : ag_moe_forward)(p.plan, rows, x.data_ptr(), ld, off, w.data_ptr(), ldw,
@@ -450,7 +461,7 @@ PyObject* weight_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
           static_cast<long long>(dy.size(0)));
   const int32_t* off = offsets_of(a[7], p.E, x);
   const at::ScalarType ot = dtype_of(a[9]);
-  const c10::cuda::CUDAGuard guard(x.device());
+  const Current current(x);
   at::Tensor out = output(a[8], {p.E, p.K, p.N}, ot, x);
   if (!out.is_contiguous()) raise(PyExc_ValueError, "out must be contiguous");
   check_rc(ag_moe_backward_weight(p.plan, rows, x.data_ptr(), ldx, dy.data_ptr(), ldd, off, out.data_ptr(),
@@ -479,7 +490,7 @@ PyObject* fp8_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const int32_t* off = offsets_of(a[8], p.E, x);
   const at::ScalarType ot = dtype_of(a[10]);
-  const c10::cuda::CUDAGuard guard(x.device());
+  const Current current(x);
   at::Tensor out = output(a[9], {rows, p.N}, ot, x);
   const int64_t ldo = pitch(out, "out");
   check_rc(ag_fp8_forward(p.plan, rows, xq, xs, off, wq, ws, out.data_ptr(), ldo, type_code(ot), stream_of(x)));
