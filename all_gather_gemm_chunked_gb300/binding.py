@@ -114,6 +114,7 @@ def _load():
         "ag_moe_plan_create": (vp, [i32, i64, i64, i32]),
         "ag_moe_plan_destroy": (None, [vp]),
         "ag_moe_plan_device": (i32, [vp]),
+        "ag_moe_plan_tile_rows": (i32, [vp, i64, i32]),
         "ag_moe_plan_status": (i32, [vp]),
         "ag_moe_plan_status_word": (i64, [vp]),
         "ag_moe_plan_reset": (i32, [vp, vp]),
@@ -330,11 +331,11 @@ def _wrapped(name):
 
 (ag_moe_route_workspace, ag_moe_route, ag_moe_route_backward, ag_moe_gather, ag_moe_combine,
  ag_moe_combine_backward, ag_fp8_quantize_rows, ag_fp8_quantize_weights, ag_moe_plan_reset,
- ag_moe_plan_set_timeout_ns, ag_moe_plan_status_word, ag_moe_forward, ag_moe_backward_input,
+ ag_moe_plan_device, ag_moe_plan_tile_rows, ag_moe_plan_set_timeout_ns, ag_moe_plan_status_word, ag_moe_forward, ag_moe_backward_input,
  ag_moe_backward_weight, ag_fp8_forward) = (_wrapped("ag_" + n) for n in (
      "moe_route_workspace", "moe_route", "moe_route_backward", "moe_gather", "moe_combine",
      "moe_combine_backward", "fp8_quantize_rows", "fp8_quantize_weights", "moe_plan_reset",
-     "moe_plan_set_timeout_ns", "moe_plan_status_word", "moe_forward", "moe_backward_input",
+     "moe_plan_device", "moe_plan_tile_rows", "moe_plan_set_timeout_ns", "moe_plan_status_word", "moe_forward", "moe_backward_input",
      "moe_backward_weight", "fp8_forward"))
 
 

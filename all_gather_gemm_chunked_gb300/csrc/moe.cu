@@ -544,6 +544,15 @@ int ag_moe_plan_device(const ag_moe_plan* plan) {
   return plan->device;
 }
 
+int ag_moe_plan_tile_rows(const ag_moe_plan* plan, int64_t rows, int input_gradient) {
+  if (!plan) return fail(AG_GEMM_ERR_INVALID, "plan is NULL");
+  if (rows < 0 || rows > kMaxRows)
+    return fail(AG_GEMM_ERR_INVALID, "rows must be in [0, %lld] (got %lld)", (long long)kMaxRows, (long long)rows);
+  if (input_gradient && plan->dtype == AG_MOE_E4M3)
+    return fail(AG_GEMM_ERR_INVALID, "an AG_MOE_E4M3 plan has no input gradient");
+  return few_rows(plan, rows, input_gradient ? plan->K : plan->N) ? agg::kXFewRows : agg::kXRows;
+}
+
 int64_t ag_moe_plan_status_word(ag_moe_plan* plan) {
   if (!plan) return fail(AG_GEMM_ERR_INVALID, "plan is NULL");
   DeviceGuard dg(plan->device);

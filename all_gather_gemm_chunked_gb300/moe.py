@@ -123,6 +123,10 @@ class _ExpertsPlan:
     def __exit__(self, *exc):
         self.close()
 
+    def tile_rows(self, rows: int, input_gradient: bool = False) -> int:
+        """Rows of the tiles, 64 or 256, that a product of so many rows is cut into."""
+        return B_.ag_moe_plan_tile_rows(self.handle, rows, input_gradient)
+
     def status(self) -> int:
         """Waits for the last run; 0, or binding.ERR_TIMEOUT / ERR_INVALID (offsets)."""
         return B_.ag_moe_plan_status(self.handle)

@@ -127,6 +127,10 @@ ag_moe_plan *ag_moe_plan_create(int E, int64_t K, int64_t N, int dtype);
 void ag_moe_plan_destroy(ag_moe_plan *plan);
 /* The device that was current when the plan was made, and that its runs take place on. */
 int ag_moe_plan_device(const ag_moe_plan *plan);
+/* Rows of the tiles, 64 or 256, that a product of so many rows is cut into: the forward's
+ * (ag_moe_forward, ag_fp8_forward) or the input gradient's.  They have kernels of their
+ * own; results may differ in the order of their sums. */
+int ag_moe_plan_tile_rows(const ag_moe_plan *plan, int64_t rows, int input_gradient);
 /* Waits for the plan's runs (for the device, if some left no event).  AG_GEMM_OK;
  * AG_GEMM_ERR_TIMEOUT: a bounded wait in the kernel ran out, the results of that run and
  * of all runs until ag_moe_plan_reset are undefined; AG_GEMM_ERR_INVALID: a run had offsets
