@@ -629,11 +629,11 @@ __device__ void scale_role(const ExpertsParams& p, const Table& table,
       float x[kScaleBatch][kPer], w[kScaleBatch], largest_x = 0.0f, largest_w = 0.0f;
 #pragma unroll
       for (int j = 0; j < kScaleBatch; ++j) {
-        w[j] = j < n ? __ldg(ws + kb0 + j) : 0.0f;
+        w[j] = j < n ? ws[kb0 + j] : 0.0f;
 #pragma unroll
         for (int r = 0; r < kPer; ++r)
           x[j][r] = j < n && r * 32 + lane < u.cnt
-                        ? __ldg(xs + static_cast<int64_t>(kb0 + j) * p.rows + r * 32) : 0.0f;
+                        ? xs[static_cast<int64_t>(kb0 + j) * p.rows + r * 32] : 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < kScaleBatch; ++j) {
@@ -682,12 +682,12 @@ __device__ void scale_long_role(const ExpertsParams& p, const Table& table,
       float x[kScaleBatch][4], a[kScaleBatch], b[kScaleBatch], largest_x = 0.0f, largest_w = 0.0f;
 #pragma unroll
       for (int j = 0; j < kScaleBatch; ++j) {
-        a[j] = j < n ? __ldg(w0 + kb0 + j) : 0.0f;
-        b[j] = j < n ? __ldg(w1 + kb0 + j) : 0.0f;
+        a[j] = j < n ? w0[kb0 + j] : 0.0f;
+        b[j] = j < n ? w1[kb0 + j] : 0.0f;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           x[j][r] = j < n && first + r * 32 < u.cnt
-                        ? __ldg(xs + static_cast<int64_t>(kb0 + j) * p.rows + r * 32) : 0.0f;
+                        ? xs[static_cast<int64_t>(kb0 + j) * p.rows + r * 32] : 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < kScaleBatch; ++j) {

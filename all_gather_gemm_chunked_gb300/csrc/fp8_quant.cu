@@ -23,9 +23,9 @@ __device__ __forceinline__ float block_scale(float amax) {
 constexpr int kQuantSteps = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int64_t K,
-                                                            const T* __restrict__ x, int64_t ldx,
+                                                            const T* x, int64_t ldx,
                                                             int64_t src_rows,
-                                                            const int32_t* __restrict__ order,
+                                                            const int32_t* order,
                                                             int k, uint8_t* __restrict__ q,
                                                             float* __restrict__ scales) {
   pdl_enter();
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int64_
 template <typename T>
 struct Two {
   uint32_t u;
-  __device__ __forceinline__ void load(const T* p) { u = __ldg(reinterpret_cast<const uint32_t*>(p)); }
+  __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint32_t*>(p); }
   __device__ __forceinline__ float2 get() const {
     const T* v = reinterpret_cast<const T*>(&u);
     return make_float2(Elem<T>::get(v[0]), Elem<T>::get(v[1]));
@@ -92,7 +92,7 @@ struct Two {
 template <>
 struct Two<float> {
   float2 u;
-  __device__ __forceinline__ void load(const float* p) { u = __ldg(reinterpret_cast<const float2*>(p)); }
+  __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const float2*>(p); }
   __device__ __forceinline__ float2 get() const { return u; }
 };
 
@@ -103,7 +103,7 @@ struct Two<float> {
 constexpr int kTilePitch = kScaleBlock + 4;
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_weights_kernel(int64_t K, int64_t N,
-                                                               const T* __restrict__ w,
+                                                               const T* w,
                                                                uint8_t* __restrict__ q,
                                                                float* __restrict__ scales) {
   pdl_enter();

@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteA
 // (16384 x 128, k 8, bf16: 3.2 us, over all experts 6.5.)
 template <typename T>
 __global__ void __launch_bounds__(256) route_backward_kernel(const RouteArgs a,
-                                                             const float* __restrict__ dweights,
+                                                             const float* dweights,
                                                              T* dlogits) {
   pdl_enter();
   constexpr int V = Elem<T>::kVec;
@@ -466,7 +466,7 @@ constexpr int kRowLog = 8, kRowThreads = 1 << kRowLog;
 // A thread moves pieces of V elements, a row's threads apart: of 16 bytes, or where rows
 // are not 16-byte aligned single elements, several of them, so that as many bytes are in
 // flight.  (8192 tokens, k 4, H 4096, bf16: aligned rows combine in 52 us, their gradient
-// takes 92, gather 66; with odd pitches 81, 123 and 97, one element a thread 182, 220 and
+// takes 90, gather 65; with odd pitches 80, 120 and 91, one element a thread 182, 220 and
 // 528.)
 constexpr int kPieces = 4;
 constexpr int kGatherPieces = 8, kGatherVec = 4;  // (gather with one 16-byte piece 80 us)
@@ -492,8 +492,8 @@ RowShape row_shape(int64_t rows, int64_t H, int per_thread) {
 // 5.1 TB/s of reads and writes.)
 template <typename T, int V, int N, bool kShort>
 __global__ void __launch_bounds__(kRowThreads) gather_kernel(int64_t T_, int k, int64_t H, int log_,
-                                                             const T* __restrict__ x, int64_t ldx,
-                                                             const int32_t* __restrict__ order,
+                                                             const T* x, int64_t ldx,
+                                                             const int32_t* order,
                                                              T* __restrict__ out) {
   pdl_enter();
   const int log = kShort ? log_ : kRowLog, step = V << log;
@@ -525,9 +525,9 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(int64_t T_, int k, 
 // four blocks, 92).
 template <typename T, int V, int N, bool kShort>
 __global__ void __launch_bounds__(kRowThreads, kShort ? 5 : 6) combine_kernel(int64_t T_, int k, int64_t H, int log_,
-                                                                 const T* __restrict__ y, int64_t ldy,
-                                                                 const int32_t* __restrict__ slots,
-                                                                 const float* __restrict__ weights,
+                                                                 const T* y, int64_t ldy,
+                                                                 const int32_t* slots,
+                                                                 const float* weights,
                                                                  T* __restrict__ out) {
   pdl_enter();
   const int log = kShort ? log_ : kRowLog, step = V << log;
@@ -576,9 +576,9 @@ __global__ void __launch_bounds__(kRowThreads, kShort ? 5 : 6) combine_kernel(in
 // 90 us, 6.7 TB/s.)
 template <typename T, int V, int N, bool kShort>
 __global__ void __launch_bounds__(kRowThreads, 4) combine_backward_kernel(
-    int64_t T_, int k, int64_t H, int log_, const T* __restrict__ dout, int64_t ldd,
-    const T* __restrict__ y, int64_t ldy, const int32_t* __restrict__ slots,
-    const float* __restrict__ weights, const int32_t* __restrict__ offsets_end,
+    int64_t T_, int k, int64_t H, int log_, const T* dout, int64_t ldd,
+    const T* y, int64_t ldy, const int32_t* slots,
+    const float* weights, const int32_t* offsets_end,
     T* __restrict__ dy, float* __restrict__ dweights) {
   pdl_enter();
   __shared__ float part[kRowThreads / 32][4];

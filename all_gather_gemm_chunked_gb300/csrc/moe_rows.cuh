@@ -15,7 +15,10 @@ enum ElemType : int { kTypeF16 = 0, kTypeBf16 = 2, kTypeF32 = 3, kTypeE4m3 = 4 }
 
 // Programmatic dependent launch: a kernel of this library may start while the kernel
 // before it in the stream is still running (launch latency and set-up overlap it) and
-// waits for that one's end, and its writes, before it touches global memory.
+// waits for that one's end, and its writes, before it touches global memory.  Inputs may
+// be what that kernel writes, so they are read with plain loads: __ldg, or __restrict__ on
+// an input, would promise the compiler that they do not change while the kernel runs, and
+// let it move loads to before the wait.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // First in every kernel that touches global memory at once.

@@ -87,7 +87,7 @@ __device__ __forceinline__ void load_elems(const T* p, float (&f)[V]) {
   if constexpr (V == 1)
     f[0] = Elem<T>::get(*p);
   else
-    Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(p)), f);
+    Elem<T>::unpack(*reinterpret_cast<const uint4*>(p), f);
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_elems(T* p, const float (&f)[V]) {
@@ -102,7 +102,12 @@ __device__ __forceinline__ void store_elems(T* p, const float (&f)[V]) {
 template <typename T, int V>
 struct Raw {
   uint4 u;
-  __device__ __forceinline__ void load(const T* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  // (volatile: in the order of the source, behind a launch's wait, and none sinks to its
+  // use; as ordinary loads combine took 54 us instead of 51)
+  __device__ __forceinline__ void load(const T* p) {
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  }
   __device__ __forceinline__ void get(float (&f)[V]) const { Elem<T>::unpack(u, f); }
 };
 template <typename T>
