@@ -17,6 +17,7 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include "ag_moe.h"
 
@@ -508,4 +509,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_front", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__front() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__front() {
+  PyObject* m = PyModule_Create(&module);
+  // the torch whose objects it reaches into
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}

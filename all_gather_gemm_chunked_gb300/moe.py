@@ -20,6 +20,7 @@ torch program.
 """
 from __future__ import annotations
 
+import re
 from typing import NamedTuple, Optional
 
 import torch
@@ -27,6 +28,14 @@ import torch
 from . import binding as B_
 from . import _front
 
+
+def _same_torch(built: str, here: str) -> bool:
+    return built == re.match(r"[0-9.]*[0-9]", here).group()
+
+
+if not _same_torch(_front.torch_version, torch.__version__):
+    raise ImportError(f"the native module was built for torch {_front.torch_version}, this is {torch.__version__}: "
+                      "run the package's build again")
 _front.init(B_._err)
 _CODES = {"f16": (torch.float16, B_.F16), "bf16": (torch.bfloat16, B_.BF16)}
 
