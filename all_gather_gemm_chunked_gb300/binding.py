@@ -313,8 +313,9 @@ def ag_gemm_last_error_message() -> str:
 
 
 # -- include/ag_moe.h ---------------------------------------------------------
-# The front ends (moe.py, fp8.py) call the library's functions through these: a
-# negative code raises, the others are returned.
+# The C functions under their own names: a negative code raises, others are returned.
+# moe.py and fp8.py use the plans' functions; their operators go through _front, which
+# calls the same C functions.
 
 def _wrapped(name):
     fn = getattr(_lib, name)
@@ -329,14 +330,23 @@ def _wrapped(name):
     return call
 
 
-(ag_moe_route_workspace, ag_moe_route, ag_moe_route_backward, ag_moe_gather, ag_moe_combine,
- ag_moe_combine_backward, ag_fp8_quantize_rows, ag_fp8_quantize_weights, ag_moe_plan_reset,
- ag_moe_plan_device, ag_moe_plan_tile_rows, ag_moe_plan_set_timeout_ns, ag_moe_plan_status_word, ag_moe_forward, ag_moe_backward_input,
- ag_moe_backward_weight, ag_fp8_forward) = (_wrapped("ag_" + n) for n in (
-     "moe_route_workspace", "moe_route", "moe_route_backward", "moe_gather", "moe_combine",
-     "moe_combine_backward", "fp8_quantize_rows", "fp8_quantize_weights", "moe_plan_reset",
-     "moe_plan_device", "moe_plan_tile_rows", "moe_plan_set_timeout_ns", "moe_plan_status_word", "moe_forward", "moe_backward_input",
-     "moe_backward_weight", "fp8_forward"))
+ag_moe_route_workspace = _wrapped("ag_moe_route_workspace")
+ag_moe_route = _wrapped("ag_moe_route")
+ag_moe_route_backward = _wrapped("ag_moe_route_backward")
+ag_moe_gather = _wrapped("ag_moe_gather")
+ag_moe_combine = _wrapped("ag_moe_combine")
+ag_moe_combine_backward = _wrapped("ag_moe_combine_backward")
+ag_fp8_quantize_rows = _wrapped("ag_fp8_quantize_rows")
+ag_fp8_quantize_weights = _wrapped("ag_fp8_quantize_weights")
+ag_moe_plan_device = _wrapped("ag_moe_plan_device")
+ag_moe_plan_tile_rows = _wrapped("ag_moe_plan_tile_rows")
+ag_moe_plan_status_word = _wrapped("ag_moe_plan_status_word")
+ag_moe_plan_reset = _wrapped("ag_moe_plan_reset")
+ag_moe_plan_set_timeout_ns = _wrapped("ag_moe_plan_set_timeout_ns")
+ag_moe_forward = _wrapped("ag_moe_forward")
+ag_moe_backward_input = _wrapped("ag_moe_backward_input")
+ag_moe_backward_weight = _wrapped("ag_moe_backward_weight")
+ag_fp8_forward = _wrapped("ag_fp8_forward")
 
 
 def ag_moe_plan_create(E: int, K: int, N: int, dtype: int) -> int:
