@@ -91,7 +91,7 @@ struct ag_moe_plan {
   uint32_t* status = nullptr;    // [4], then the arrival counters
   uint32_t* arrivals = nullptr;
   int64_t arrival_count = 0;
-  float* partials = nullptr;
+  float* partials = nullptr;     // null until the first run that may split its sums
   uint64_t timeout_ns = 2000000000ull;
   cudaEvent_t done = nullptr;
   // The last run that may split its sums, and so use the workspace: `done` is recorded
@@ -110,10 +110,22 @@ struct ag_moe_plan {
 namespace {
 
 // Workspace of split sums: 40 MB hold 608 units of short tiles or 152 of long
-// ones.  Sums are split only where there are fewer than two tiles a pair.
+// ones.  Sums are split only where there are fewer than two tiles a pair.  A plan gets it
+// with its first run that may split: many plans of a model never do.
 constexpr int64_t kPartialBytes = 608 * agg::split_unit_bytes(true);
 static_assert(kPartialBytes == 152 * agg::split_unit_bytes(false), "both tile heights");
 int max_units(bool few) { return static_cast<int>(kPartialBytes / agg::split_unit_bytes(few)); }
+
+cudaError_t allocate_partials(ag_moe_plan* p) {
+  // (allowed while a stream is being captured: the allocation is no part of the graph)
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return e;
+  e = cudaMalloc(&p->partials, static_cast<size_t>(kPartialBytes));
+  if (e != cudaSuccess) p->partials = nullptr;
+  const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+  return e != cudaSuccess ? e : back;
+}
 
 // Whether a sum of so many k-blocks can be split: whether that pays in the best case, all
 // parts running at once.  (More tiles than pairs make it pay less: the parts' rounds
@@ -247,7 +259,6 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   x.E = p->E;
   x.bf16 = p->dtype == AG_GEMM_BF16;
   x.segment = x.out_type == AG_MOE_F32 ? kSegment : 1 << 30;
-  x.partials = p->partials;
   x.arrivals = p->arrivals;
   x.status = p->status;
   // (8192 x 4096 x 4096, e4m3: 125 us with 32-byte stores, 134 with rows 16 bytes off)
@@ -265,12 +276,15 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   const bool split = !plenty && may_split(kb, agg::split_price(fp8 && !few ? agg::kOpFp8Long : op,
                                                     op == agg::kOpWeight ? x.step < agg::kXRows : few));
   x.max_units = split ? max_units(few) : 0;
+  cudaError_t e = split && !p->partials ? allocate_partials(p) : cudaSuccess;
+  if (e != cudaSuccess) return cuda_fail(e, "workspace of split sums");
+  x.partials = p->partials;
   // A captured run is ordered by its graph: an event of the streams outside cannot be
   // waited on there, nor one of the graph outside.
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   unsigned long long capture_id = 0;
-  cudaError_t e = cudaStreamGetCaptureInfo(stream, &capture, &capture_id);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetCaptureInfo");
+  if ((e = cudaStreamGetCaptureInfo(stream, &capture, &capture_id)) != cudaSuccess)
+    return cuda_fail(e, "cudaStreamGetCaptureInfo");
   const bool captured = capture != cudaStreamCaptureStatusNone;
   const bool wait = captured ? p->capture_id == capture_id && p->captured_stream.other(stream)
                              : p->has_run && p->last_stream.other(stream);
@@ -518,7 +532,6 @@ ag_moe_plan* ag_moe_plan_create(int E, int64_t K, int64_t N, int dtype) {
   agg::Clearer clearer;
   if ((e = cudaMalloc(&p->status, words)) != cudaSuccess ||
       (e = clearer.clear(p->status, words)) != cudaSuccess ||
-      (e = cudaMalloc(&p->partials, static_cast<size_t>(kPartialBytes))) != cudaSuccess ||
       (e = cudaEventCreateWithFlags(&p->done, cudaEventDisableTiming)) != cudaSuccess ||
       (e = cudaEventCreateWithFlags(&p->captured, cudaEventDisableTiming)) != cudaSuccess ||
       (e = clearer.finish()) != cudaSuccess) {

@@ -108,8 +108,8 @@ int ag_fp8_quantize_weights(int E, int64_t K, int64_t N, int dtype, const void *
 /*
  * A plan serves the products of one layer's experts: E weight matrices K x N.
  * dtype AG_GEMM_F16 or AG_GEMM_BF16 (K, N multiples of 8), or AG_MOE_E4M3 (K % 16
- * == 0, N % 8 == 0).  It owns the workspace of the products that split their sums and
- * the status word; runs on one plan that may use the workspace are serialised as those
+ * == 0, N % 8 == 0).  It owns the status word and the workspace of the products that
+ * split their sums (40 MB, from the first run that may do so on); runs on one plan that may use the workspace are serialised as those
  * of ag_gemm.h are, others may overlap where their streams let them.  Runs may be
  * captured into a CUDA graph, on several branches of it too; a replay is then the caller's
  * to keep apart from the plan's other runs, and to wait for before the status is read.
