@@ -39,7 +39,7 @@
 //   fp32 outputs   8 k-blocks: the tensor core's additions lose about a last bit
 //                  each, so the error of one long accumulation grows with its length
 //                  (1.1e-6 of the result over 1024 terms, 4.5e-7 in segments),
-//   16-bit outputs the whole sum (the rounding of the output hides that error).
+//   16-bit outputs 128 k-blocks (the rounding of the output hides their error).
 //
 // Rows beyond a group's end belong to the next group: they are multiplied along and
 // not stored (rows on the N side do not mix).  In the weight gradient they would

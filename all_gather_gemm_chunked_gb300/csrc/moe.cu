@@ -140,8 +140,12 @@ bool may_split(int64_t KB, agg::SplitPrice price) {
 constexpr int64_t kMaxRows = (1LL << 31) - 256;
 static_assert(agg::kXRows <= 256 && agg::kXSub * 64 <= 256, "rows beyond the last that a tile or a stage reaches");
 
-// k-blocks of a segment where the output is fp32.
-constexpr int kSegment = 8;
+// k-blocks of a segment where the output is fp32, and where it has 16 bits: each of a
+// k-block's four additions in the tensor core loses up to 2^-23 of the sum, always towards
+// zero, so 8 k-blocks cost up to 4e-6 and 128 up to 6e-5, an eighth of fp16's half last
+// bit.  (Sums of 2^22 positive fp16 products in one segment were off by 1.6e-3, in
+// segments of 128 k-blocks by 2.2e-4, the rounding of the output.)
+constexpr int kSegment = 8, kSegment16 = 128;
 
 struct Prepared {
   cudaError_t e;
@@ -258,7 +262,7 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
   x.E = p->E;
   x.bf16 = p->dtype == AG_GEMM_BF16;
-  x.segment = x.out_type == AG_MOE_F32 ? kSegment : 1 << 30;
+  x.segment = x.out_type == AG_MOE_F32 ? kSegment : kSegment16;
   x.arrivals = p->arrivals;
   x.status = p->status;
   // (8192 x 4096 x 4096, e4m3: 125 us with 32-byte stores, 134 with rows 16 bytes off)
