@@ -52,7 +52,8 @@
 // as long as its MMAs take the tensor cores); weight gradient to fp32 175 us; 64 rows on
 // 32 experts of 4096 x 4096 131 us (the hit weights at 6.9 TB/s).  e4m3: the same product
 // 126 us (2.2 PFLOP/s; bound by the epilogue's work on each k-block), 64 rows of 16384 x
-// 7168 28 us (a bare read of the weights 27.6).  A call of one tile takes 4.4 us.
+// 7168 28 us (4.2 TB/s of weights: 28 tiles in two parts are 56 units for 76 pairs).  A
+// call of one tile, repeated, takes 4.4 us, with inputs that change 5.2.
 //
 // Every wait is bounded; on a timeout the kernel records a status word, drains what
 // it has in flight, frees TMEM and returns.

@@ -45,7 +45,8 @@ class Fp8Linear(_ExpertsPlan):
     """y[r][n] = sum over the 128-blocks b of K of xs[b][r] * ws[e][n // 128][b] * (the
     block's sum of xq * wq), for one weight matrix or, with offsets, for the rows of
     ``n_experts`` experts.  Sums of a block in the tensor core's 32 bits, over the
-    blocks in 32-bit registers.  Forward only: training goes through moe.Experts."""
+    blocks in 32-bit registers.  K is a multiple of 16, N of 8.  Forward only, without
+    autograd: training goes through moe.Experts."""
 
     def __init__(self, K: int, N: int, n_experts: int = 1):
         super().__init__(n_experts, K, N, B_.E4M3)

@@ -11,6 +11,9 @@ A layer's forward pass::
     y = down.forward(act(h), r.offsets, w_down)
     out = combine(y, r.slots, r.weights)
 
+The functions know nothing of autograd: outputs carry no gradient, whatever the inputs
+say; a backward pass calls the ``backward`` functions itself (examples/moe_layer.py).
+
 The tensors of a call, its plan and its stream are on one device, which need not be the
 current one.
 
@@ -158,8 +161,10 @@ class Experts(_ExpertsPlan):
     operands' type or float32.  Rows outside [offsets[0], offsets[-1]) are not written
     (an ``out`` of the caller's keeps them).
 
-    Serves x rows of any number from 0 on; x, dy and out may be column blocks of wider
-    matrices, w any (n_experts, K, N) tensor with contiguous rows."""
+    K and N are multiples of 8.  Rows of any number from 0 on; x, dy and out may be column
+    blocks of wider matrices, w may have its rows and its experts further apart than they
+    are long (each expert's K rows behind the last one's); pitches are multiples of 16
+    bytes."""
 
     def __init__(self, n_experts: int, K: int, N: int, dtype: str = "bf16"):
         if dtype not in _CODES:
