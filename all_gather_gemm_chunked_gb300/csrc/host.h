@@ -48,32 +48,26 @@ class Clearer {
   cudaError_t e_;
 };
 
-// The stream of a plan's last run, by the number that no other stream has: one handle
-// stands for every thread's own default stream, and a destroyed stream's may be given to a
-// new one while its work is pending.
-class LastStream {
- public:
-  bool other(cudaStream_t stream) const {
-    const unsigned long long n = id_ ? number(stream) : 0;
-    return n ? n != id_ : stream != handle_;
-  }
-  void set(cudaStream_t stream) {
-    handle_ = stream;
-    id_ = number(stream);
-  }
-
- private:
-  // The number plus 1; 0 while the stream is captured (to ask for it would end the
-  // capture): handles are compared then.
-  static unsigned long long number(cudaStream_t stream) {
-    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+// A stream by the number that no other stream has: one handle stands for every thread's
+// own default stream, and a destroyed stream's may be given to a new one while its work is
+// pending.  While the stream is captured the number is 0 (to ask for it would end the
+// capture), and handles are compared.
+struct StreamId {
+  cudaStream_t handle = nullptr;
+  unsigned long long number = 0;  // plus 1
+  StreamId() = default;
+  StreamId(cudaStream_t stream, bool captured) : handle(stream) {
     unsigned long long n = 0;
-    if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) return 0;
-    return cudaStreamGetId(stream, &n) == cudaSuccess ? n + 1 : 0;
+    if (!captured && cudaStreamGetId(stream, &n) == cudaSuccess) number = n + 1;
   }
-  cudaStream_t handle_ = nullptr;
-  unsigned long long id_ = 0;
+  bool operator!=(const StreamId& o) const {
+    return number && o.number ? number != o.number : handle != o.handle;
+  }
 };
+inline bool is_captured(cudaStream_t stream) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  return cudaStreamIsCapturing(stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone;
+}
 
 // Makes `dev` current; restores the caller's current device on scope exit.
 struct DeviceGuard {

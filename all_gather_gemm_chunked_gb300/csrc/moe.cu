@@ -98,12 +98,12 @@ struct ag_moe_plan {
   // behind it, and the next such run on another stream waits for it.  Others share
   // nothing with it but the status word; an event behind each would cost a call a
   // quarter of its host time (4.5 us against 3.4).
-  agg::LastStream last_stream;
+  agg::StreamId last_stream;
   bool has_run = false;
   bool loose = false;  // a run without an event since the last status or reset
   // The same inside a graph capture: branches of one capture are put in order.
   cudaEvent_t captured = nullptr;
-  agg::LastStream captured_stream;
+  agg::StreamId captured_stream;
   unsigned long long capture_id = 0;
 };
 
@@ -290,9 +290,10 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   if ((e = cudaStreamGetCaptureInfo(stream, &capture, &capture_id)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamGetCaptureInfo");
   const bool captured = capture != cudaStreamCaptureStatusNone;
-  const bool wait = captured ? p->capture_id == capture_id && p->captured_stream.other(stream)
-                             : p->has_run && p->last_stream.other(stream);
-  if (split && wait && (e = cudaStreamWaitEvent(stream, captured ? p->captured : p->done, 0)) != cudaSuccess)
+  const agg::StreamId id = split ? agg::StreamId(stream, captured) : agg::StreamId();
+  const bool wait = split && (captured ? p->capture_id == capture_id && p->captured_stream != id
+                                       : p->has_run && p->last_stream != id);
+  if (wait && (e = cudaStreamWaitEvent(stream, captured ? p->captured : p->done, 0)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamWaitEvent");
   // no more pairs than there can be units
   const int64_t parts = !split ? 1 : kb / agg::kMinPart < agg::kMaxSplit ? kb / agg::kMinPart : agg::kMaxSplit;
@@ -305,10 +306,10 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   } else if ((e = cudaEventRecord(captured ? p->captured : p->done, stream)) != cudaSuccess) {
     return cuda_fail(e, "cudaEventRecord");
   } else if (captured) {
-    p->captured_stream.set(stream);
+    p->captured_stream = id;
     p->capture_id = capture_id;
   } else {
-    p->last_stream.set(stream);
+    p->last_stream = id;
     p->has_run = true;
   }
   log_msg(3, "plan %p: experts product %d enqueued, %d rows", static_cast<void*>(p), op, x.rows);
@@ -599,9 +600,10 @@ int ag_moe_plan_reset(ag_moe_plan* plan, void* stream_v) {
   if (!plan) return fail(AG_GEMM_ERR_INVALID, "plan is NULL");
   DeviceGuard dg(plan->device);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+  const agg::StreamId id(stream, agg::is_captured(stream));
   cudaError_t e;
   if (plan->loose && (e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-  if (!plan->loose && plan->has_run && plan->last_stream.other(stream) &&
+  if (!plan->loose && plan->has_run && plan->last_stream != id &&
       (e = cudaStreamWaitEvent(stream, plan->done, 0)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamWaitEvent");
   plan->loose = false;
@@ -609,7 +611,7 @@ int ag_moe_plan_reset(ag_moe_plan* plan, void* stream_v) {
                            stream)) != cudaSuccess ||
       (e = cudaEventRecord(plan->done, stream)) != cudaSuccess)
     return cuda_fail(e, "plan reset");
-  plan->last_stream.set(stream);
+  plan->last_stream = id;
   plan->has_run = true;
   return AG_GEMM_OK;
 }

@@ -214,7 +214,7 @@ struct ag_gemm_plan {
   uint16_t* a16 = nullptr;  // int8 path: fp16 copy of the local shard
   uint32_t epoch = 0;
   cudaEvent_t done = nullptr;
-  agg::LastStream last_stream;
+  agg::StreamId last_stream;
   bool has_run = false;
   CUtensorMap tm_stage{};
   CUtensorMap tm_a16{}, tm_b16{};
@@ -399,7 +399,8 @@ int run_impl(ag_gemm_plan* p, const void* const* shard_ptrs, const void* B, int6
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
   cudaError_t e;
   // Runs on one plan share its staging and counters: order them.
-  if (p->has_run && p->last_stream.other(stream)) {
+  const agg::StreamId id(stream, agg::is_captured(stream));
+  if (p->has_run && p->last_stream != id) {
     e = cudaStreamWaitEvent(stream, p->done, 0);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
   }
@@ -565,7 +566,7 @@ int run_impl(ag_gemm_plan* p, const void* const* shard_ptrs, const void* B, int6
     if (runs_copy) p->epoch += 1;
     e = cudaEventRecord(p->done, stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
-    p->last_stream.set(stream);
+    p->last_stream = id;
     p->has_run = true;
     log_msg(3, "plan %p: skinny run enqueued, mode %d, epoch %u", static_cast<void*>(p), mode,
             p->epoch);
@@ -600,7 +601,7 @@ int run_impl(ag_gemm_plan* p, const void* const* shard_ptrs, const void* B, int6
   if (runs_copy) p->epoch += 1;
   e = cudaEventRecord(p->done, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
-  p->last_stream.set(stream);
+  p->last_stream = id;
   p->has_run = true;
   log_msg(3, "plan %p: fused run enqueued, mode %d, epoch %u, grid %d", static_cast<void*>(p),
           mode, p->epoch, p->grid_override > 0 ? p->grid_override : p->grid);
@@ -951,8 +952,9 @@ int ag_gemm_plan_reset(ag_gemm_plan* plan, void* stream_v) {
   if (!plan) return fail(AG_GEMM_ERR_INVALID, "plan is NULL");
   DeviceGuard dg(plan->device);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+  const agg::StreamId id(stream, agg::is_captured(stream));
   cudaError_t e;
-  if (plan->has_run && plan->last_stream.other(stream) &&
+  if (plan->has_run && plan->last_stream != id &&
       (e = cudaStreamWaitEvent(stream, plan->done, 0)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamWaitEvent");
   if ((e = cudaMemsetAsync(plan->counters, 0, sizeof(uint32_t) * plan->counter_count, stream)) != cudaSuccess ||
@@ -976,7 +978,7 @@ int ag_gemm_plan_reset(ag_gemm_plan* plan, void* stream_v) {
   plan->epoch = 0;
   plan->item_base = 0;
   plan->tile_base = 0;
-  plan->last_stream.set(stream);
+  plan->last_stream = id;
   plan->has_run = true;
   return AG_GEMM_OK;
 }
