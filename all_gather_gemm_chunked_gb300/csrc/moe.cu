@@ -101,6 +101,7 @@ struct ag_moe_plan {
   agg::StreamId last_stream;
   bool has_run = false;
   bool loose = false;  // a run without an event since the last status or reset
+  bool cleared = false;  // a reset since the last status: runs on other streams wait for `done` too
   // The same inside a graph capture: branches of one capture are put in order.
   cudaEvent_t captured = nullptr;
   agg::StreamId captured_stream;
@@ -290,9 +291,10 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   if ((e = cudaStreamGetCaptureInfo(stream, &capture, &capture_id)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamGetCaptureInfo");
   const bool captured = capture != cudaStreamCaptureStatusNone;
-  const agg::StreamId id = split ? agg::StreamId(stream, captured) : agg::StreamId();
-  const bool wait = split && (captured ? p->capture_id == capture_id && p->captured_stream != id
-                                       : p->has_run && p->last_stream != id);
+  const bool ordered = split || (p->cleared && !captured);
+  const agg::StreamId id = ordered ? agg::StreamId(stream, captured) : agg::StreamId();
+  const bool wait = ordered && (captured ? p->capture_id == capture_id && p->captured_stream != id
+                                         : p->has_run && p->last_stream != id);
   if (wait && (e = cudaStreamWaitEvent(stream, captured ? p->captured : p->done, 0)) != cudaSuccess)
     return cuda_fail(e, "cudaStreamWaitEvent");
   // no more pairs than there can be units
@@ -578,7 +580,7 @@ int64_t ag_moe_plan_status_word(ag_moe_plan* plan) {
   if (plan->loose && (e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
   if (!plan->loose && plan->has_run && (e = cudaEventSynchronize(plan->done)) != cudaSuccess)
     return cuda_fail(e, "cudaEventSynchronize");
-  plan->loose = false;
+  plan->loose = plan->cleared = false;
   uint32_t w[4] = {0, 0, 0, 0};
   if ((e = cudaMemcpy(w, plan->status, sizeof(w), cudaMemcpyDeviceToHost)) != cudaSuccess)
     return cuda_fail(e, "status read");
@@ -613,6 +615,7 @@ int ag_moe_plan_reset(ag_moe_plan* plan, void* stream_v) {
     return cuda_fail(e, "plan reset");
   plan->last_stream = id;
   plan->has_run = true;
+  plan->cleared = true;
   return AG_GEMM_OK;
 }
 

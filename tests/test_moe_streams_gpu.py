@@ -113,3 +113,19 @@ def test_branches_of_a_captured_graph_are_ordered():
                 assert all(torch.equal(g, t) for g, t in zip(got, want))
         assert all(torch.equal(p.forward(t, None, w), y) for t, y in zip(xs, want))
         assert p.status() == B_.OK
+
+
+def test_a_reset_comes_before_later_runs_on_any_stream():
+    x, w = randn(rng(1), (20, 64), torch.float16), randn(rng(2), (3, 64, 64), torch.float16)
+    bad = torch.tensor([0, 10, 5, 20], dtype=torch.int32, device="cuda")
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    with moe.Experts(3, 64, 64, "f16") as p:
+        for wait_ms in (0, 300):
+            p.reset()
+            assert p.status() == B_.OK
+            with torch.cuda.stream(a):
+                torch.cuda._sleep(wait_ms * CYCLES_PER_MS)
+            p.reset(a)
+            p.forward(x, bad, w, stream=b)  # this run's status is newer than the reset
+            torch.cuda.synchronize()
+            assert p.status() == B_.ERR_INVALID
