@@ -1,4 +1,4 @@
-"""ctypes binding of libaggemm.so (include/ag_gemm.h, include/ag_moe.h).
+"""ctypes binding of libaggemm.so (include/ag_gemm.h, include/ag_moe.h, include/ag_layer.h).
 
 Argument marshalling only: every step of the path runs in the CUDA library.
 The functions keep the C names; pointers are passed as Python ints (device
@@ -28,12 +28,13 @@ OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_OOM, ERR_TIMEOUT, ERR_STATE = 0,
 ERROR_NAMES = {ERR_INVALID: "INVALID", ERR_UNSUPPORTED: "UNSUPPORTED", ERR_CUDA: "CUDA",
                ERR_OOM: "OOM", ERR_TIMEOUT: "TIMEOUT", ERR_STATE: "STATE"}
 
-F32, E4M3 = 3, 4  # AG_MOE_F32, AG_MOE_E4M3: beside F16, I8 and BF16
+F32, E4M3, E2M1 = 3, 4, 5  # AG_MOE_F32, AG_MOE_E4M3, AG_MOE_E2M1: beside F16, I8 and BF16
 MAX_EXPERTS, MAX_TOP_K, SCALE_BLOCK = 1024, 32, 128
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                       "include", "ag_gemm.h")
 HEADER_MOE = os.path.join(os.path.dirname(HEADER), "ag_moe.h")
+HEADER_LAYER = os.path.join(os.path.dirname(HEADER), "ag_layer.h")
 
 
 class AgGemmError(RuntimeError):
@@ -123,6 +124,9 @@ def _load():
         "ag_moe_backward_input": (i32, [vp, i64, vp, i64, vp, vp, i64, i64, vp, i64, i32, vp]),
         "ag_moe_backward_weight": (i32, [vp, i64, vp, i64, vp, i64, vp, vp, i32, vp]),
         "ag_fp8_forward": (i32, [vp, i64, vp, vp, vp, vp, vp, vp, i64, i32, vp]),
+        "ag_fp4_quantize_rows": (i32, [i64, i64, i32, vp, i64, i64, vp, i32, vp, vp, vp]),
+        "ag_fp4_quantize_weights": (i32, [i32, i64, i64, i32, vp, vp, vp, vp]),
+        "ag_fp4_forward": (i32, [vp, i64, vp, vp, vp, vp, vp, vp, i64, i32, vp]),
         "ag_gemm_last_error": (i32, []),
         "ag_gemm_last_error_message": (ctypes.c_char_p, []),
     }
@@ -140,7 +144,7 @@ def header_functions(path: str = HEADER):
     """Names of the functions a header (include/ag_gemm.h) declares."""
     text = open(path).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(ag_(?:gemm|moe|fp8)_\w+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(ag_(?:gemm|moe|fp8|fp4|norm|act)_\w+)\s*\(", text)))
 
 
 def library_handle():
@@ -312,9 +316,9 @@ def ag_gemm_last_error_message() -> str:
     return (_lib.ag_gemm_last_error_message() or b"").decode()
 
 
-# -- include/ag_moe.h ---------------------------------------------------------
+# -- include/ag_moe.h, include/ag_layer.h --------------------------------------
 # The C functions under their own names: a negative code raises, others are returned.
-# moe.py and fp8.py use the plans' functions; their operators go through _front, which
+# moe.py, fp8.py and fp4.py use the plans' functions; their operators go through _front, which
 # calls the same C functions.
 
 def _wrapped(name):
@@ -347,6 +351,9 @@ ag_moe_forward = _wrapped("ag_moe_forward")
 ag_moe_backward_input = _wrapped("ag_moe_backward_input")
 ag_moe_backward_weight = _wrapped("ag_moe_backward_weight")
 ag_fp8_forward = _wrapped("ag_fp8_forward")
+ag_fp4_quantize_rows = _wrapped("ag_fp4_quantize_rows")
+ag_fp4_quantize_weights = _wrapped("ag_fp4_quantize_weights")
+ag_fp4_forward = _wrapped("ag_fp4_forward")
 
 
 def ag_moe_plan_create(E: int, K: int, N: int, dtype: int) -> int:

@@ -1,7 +1,7 @@
 // experts_kernel.cu -- matrix products grouped by expert, for ragged groups, as
 // one persistent kernel of CTA pairs for sm_103a.
 //
-// All four products have the form out[row][wide] = sum over red of W * R, where the
+// All products have the form out[row][wide] = sum over red of W * R, where the
 // wide operand W is the MMA's M and the row operand R its N:
 //
 //   forward          W = w[e] (K x N, wide contiguous: MN-major),  R = x rows (K-major)
@@ -9,6 +9,7 @@
 //   weight gradient  W = dy^T (MN-major), R = x^T (MN-major), red = the expert's rows
 //   e4m3             W = wq[e] (N x K: K-major), R = xq rows (K-major); for long
 //                    groups the other way round, rows on the M side
+//   e2m1             as e4m3, rows on the N side; 256 elements make a k-block
 //
 // Rows on the N side: a pair's N takes any multiple of 32 up to 256 where its M is
 // 256, so a group of 300 rows costs two tiles of 160 and one of 7 rows a tile of 32,
@@ -24,6 +25,7 @@
 //   warps 2-17  epilogue: TMEM lane quadrant warp % 4, a quarter of the tile's columns
 //   warp 18     weight gradient: zeros over the rows behind a group's end;
 //               e4m3: the scales of each k-block into shared memory
+//               e2m1: the rows' scales into shared memory, as the tensor core takes them
 //
 // Work: tiles in expert order, and inside an expert in groups of 8 row tiles by all
 // wide tiles, so that the tiles in flight share operands in L2.  Unit u of pair p is
@@ -40,6 +42,15 @@
 //                  each, so the error of one long accumulation grows with its length
 //                  (1.1e-6 of the result over 1024 terms, 4.5e-7 in segments),
 //   16-bit outputs 128 k-blocks (the rounding of the output hides their error).
+//
+// e2m1 operands have a scale of 2^(byte - 127) for each 32 elements along K, which the
+// tensor core multiplies in (kind::mxf4).  It takes the scales from TMEM: pieces of 128
+// rows by 4 scales, 512 bytes, that tcgen05.cp brings from shared memory, in order with
+// the MMAs that the same thread issues.  The weights' pieces lie ready in memory and come
+// by TMA with their codes.  The rows' do not: a group begins at any row, so they are kept
+// as words of four scales, [128 elements of K][row], and a warp puts the tile's words into
+// the pieces' order.  Two accumulators of 224 columns leave TMEM columns for the scales of
+// two k-blocks.
 //
 // Rows beyond a group's end belong to the next group: they are multiplied along and
 // not stored (rows on the N side do not mix).  In the weight gradient they would
@@ -79,12 +90,19 @@ constexpr int kGroupBytes = kSub * 64 * 128;  // MN-major: 64 columns of a stage
 
 __host__ __device__ constexpr int rows_per_cta(int BN) { return BN / 2; }
 __host__ __device__ constexpr int r_bytes(int BN) { return rows_per_cta(BN) * 128; }
-// Stages that fit: 3 of 64 KB, or 5 of 40 KB for short row tiles, where the bytes in
-// flight are nearly the weights' alone.
-__host__ __device__ constexpr int stages_of(int BN) { return (BN == kXRows ? 6 : 10) / kSub; }
+// Stages that fit: 3 of 64 KB, or 5 of 40 KB (e2m1, with scales: 4 of 44 KB) for short row
+// tiles, where the bytes in flight are nearly the weights' alone.
+__host__ __device__ constexpr int stages_of(int op, int BN) {
+  return (BN != kXFewRows ? 6 : op == kOpFp4 ? 8 : 10) / kSub;
+}
 constexpr int kScaleBatch = 4;  // e4m3: k-blocks whose scales are handed over at once; two such batches
+// e2m1: pieces of 128 rows x 4 scales, of a stage's weights and of its rows, [128 elements of K][128 rows]
+constexpr int kPiece = 512, kPieces = 2 * kSub;
+__host__ __device__ constexpr int row_pieces(int BN) { return (BN + 127) / 128; }
+__host__ __device__ constexpr int scale_stage(int BN) { return kPieces * (1 + row_pieces(BN)) * kPiece; }
 __host__ __device__ constexpr int scale_bytes(int op, int BN) {
-  return op == kOpFp8 ? 2 * kScaleBatch * BN * 4 : op == kOpFp8Long ? 2 * kScaleBatch * 2 * 128 * 4 : 0;
+  return op == kOpFp8 ? 2 * kScaleBatch * BN * 4 : op == kOpFp8Long ? 2 * kScaleBatch * 2 * 128 * 4
+         : op == kOpFp4 ? stages_of(op, BN) * scale_stage(BN) : 0;
 }
 // An epilogue warp's buffer for rows of output on their way: 8 of 128 bytes, or 4.
 __host__ __device__ constexpr int out_buffer(int op) { return op == kOpFp8Long ? 0 : op == kOpFp8 ? 512 : 1024; }
@@ -92,12 +110,13 @@ __host__ __device__ constexpr int out_bytes(int op) { return kXEpiWarps * out_bu
 constexpr int kTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) & ~15;
 constexpr int kUnitBytes = kXEpiWarps * 48;  // the epilogue warps' units
 __host__ __device__ constexpr int smem_bytes(int op, int BN) {
-  return stages_of(BN) * kSub * (kWBytes + r_bytes(BN)) + scale_bytes(op, BN) +
+  return stages_of(op, BN) * kSub * (kWBytes + r_bytes(BN)) + scale_bytes(op, BN) +
          out_bytes(op) + kTableBytes + kUnitBytes + 512 /*barriers*/ + 1024 /*alignment*/;
 }
 static_assert(smem_bytes(kOpForward, kXRows) <= 227 * 1024 && smem_bytes(kOpForward, kXFewRows) <= 227 * 1024 &&
                   smem_bytes(kOpWeight, kXRows) <= 227 * 1024 && smem_bytes(kOpFp8, kXFewRows) <= 227 * 1024 &&
-                  smem_bytes(kOpFp8Long, kXRows) <= 227 * 1024,
+                  smem_bytes(kOpFp8Long, kXRows) <= 227 * 1024 && smem_bytes(kOpFp4, kXRows4) <= 227 * 1024 &&
+                  smem_bytes(kOpFp4, kXFewRows) <= 227 * 1024,
               "shared memory of an SM");
 
 // After a wait has run out: how long what is in flight is waited for.
@@ -116,6 +135,31 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uin
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// The same of e2m1 operands (K = 64) with a scale for each 32 elements in TMEM.
+__device__ __forceinline__ void mma_f4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t a_scales, uint32_t b_scales, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor: e2m1 A and B (format 1), scales e8m0 (bit 23); the scales of an
+// MMA are bytes `id` and id + 1 of each word (bits [4,6) of B's, [29,31) of A's).
+__device__ __forceinline__ uint32_t idesc_f4(int n, uint32_t id) {
+  return (id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(kXWide >> 4) << 24) | (id << 29);
+}
+// A piece of scales to 4 TMEM columns, in both CTAs from each one's own shared memory:
+// 32 lanes of 16 bytes (8 of them 128 bytes apart, no swizzle), the same for the four
+// quarters of the lanes.
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint32_t saddr) {
+  const uint64_t desc = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
+                        (static_cast<uint64_t>(1) << 46);
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* map, uint32_t bar,
                                                  int32_t x, int32_t y, int32_t z, int32_t w) {
@@ -188,6 +232,11 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 // hand-over costs the epilogue about 300 cycles, as much as a k-block's sums.
 constexpr int kAccCols = 256;
 constexpr int kFewBlocks = kAccCols / kXFewRows;
+// e2m1: two of 224, behind them the scales of two k-blocks: the weights' two pieces (4
+// columns each), the rows' two by two.
+__host__ __device__ constexpr int acc_cols(int op) { return op == kOpFp4 ? kXRows4 : kAccCols; }
+constexpr int kScaleCol = 2 * kXRows4, kScaleCols = 24;
+static_assert(kScaleCol + kSub * kScaleCols <= 512, "TMEM columns");
 static_assert(kScaleBatch == kFewBlocks, "scales are handed over with the accumulators");
 
 // ------------------------------------------------------------------ work
@@ -209,7 +258,7 @@ static_assert(sizeof(Unit) <= kUnitBytes / kXEpiWarps, "an epilogue warp's unit"
 
 __host__ __device__ constexpr bool is_fp8(int op) { return op == kOpFp8 || op == kOpFp8Long; }
 template <int OP>
-__host__ __device__ constexpr int block_k() { return is_fp8(OP) ? 128 : 64; }
+__host__ __device__ constexpr int block_k() { return OP == kOpFp4 ? 256 : is_fp8(OP) ? 128 : 64; }
 
 // Division by a number that stays: n < 2^31; floor(2^32 / d) gives the quotient or one
 // less.  (A hardware division takes about a hundred cycles; a role that decodes its
@@ -295,7 +344,7 @@ struct Schedule {
     if (OP == kOpWeight) tiles = p.E * row_tiles(p);
     tiles *= wide_tiles(p);
     const int32_t split = choose_split(tiles, OP == kOpWeight ? longest / 64 : k_blocks(p), p.max_units,
-                                       split_price(OP, OP == kOpWeight ? p.step < kXRows : BN != kXRows));
+                                       split_price(OP, OP == kOpWeight ? p.step < kXRows : BN == kXFewRows));
     if ((threadIdx.x & 31) == 0) {
       head[0] = split;
       head[1] = static_cast<int32_t>(split == 1 ? 0xffffffffu : 0xffffffffu / static_cast<uint32_t>(split));
@@ -434,9 +483,11 @@ struct Ring {
   uint64_t* tempty; // on the even CTA: the epilogue warps of both
   uint64_t* tail;   // weight gradient, by stage: this CTA's part of a group's last k-block
   uint64_t* zfull;  // and, on the even CTA: both CTAs' parts zeroed behind the group's end
+                    // (e2m1: by stage, both CTAs' copies of the rows' scales)
   uint64_t* sfull;  // e4m3: scales of a k-block, by slot
   uint64_t* sempty; // e4m3: this CTA's epilogue warps are through with them
   float* scales;    // two batches: [k-block][BN], long groups [k-block][column block][128]
+                    // (e2m1: a stage's pieces, the weights' and then the rows')
   uint8_t* stage_out;  // a buffer of out_buffer(OP) bytes for each epilogue warp
   Unit* units;         // an epilogue warp's unit, beside the sums that fill its registers
   volatile int* abort;
@@ -472,14 +523,14 @@ __device__ __forceinline__ void load_k(uint8_t* dst, const CUtensorMap* map, uin
 // Box height of the row operand's loads (rows of a CTA, rounded up to its four sizes).
 template <int BN>
 __device__ __forceinline__ int32_t box_of(int32_t half) {
-  return (half + BN / 8 - 1) / (BN / 8);
+  return (half + box_step(BN) - 1) / box_step(BN);
 }
 
 template <int OP, int BN>
 __device__ void tma_role(const ExpertsParams& p, const Table& table, const Ring& ring,
                          uint32_t rank, int lane) {
   Schedule<OP, BN> sch(p, table);
-  constexpr int kStagesX = stages_of(BN);
+  constexpr int kStagesX = stages_of(OP, BN);
   const uint32_t full0 = mapa_shared(smem_u32(ring.full), 0);
   [[maybe_unused]] const uint32_t tail0 = mapa_shared(smem_u32(ring.tail), rank);
   int stage = 0;
@@ -489,8 +540,8 @@ __device__ void tma_role(const ExpertsParams& p, const Table& table, const Ring&
   for (int32_t i = 0; ok && sch.get(i, u); ++i) {
     const int32_t half = u.w / 2;
     const int32_t boxes = OP == kOpFp8Long ? kXRowBoxes : box_of<BN>(half);
-    const int32_t height = OP == kOpWeight ? half : boxes * (BN / 8);
-    const uint32_t tx = static_cast<uint32_t>(kSub * (kWBytes + height * 128));
+    const int32_t height = OP == kOpWeight ? half : box_height(BN, boxes);
+    const uint32_t tx = static_cast<uint32_t>(kSub * (kWBytes + height * 128) + (OP == kOpFp4 ? kPieces * kPiece : 0));
     const int32_t n = u.n0 + static_cast<int32_t>(rank) * 128;
     for (int32_t kb0 = u.kb0; kb0 < u.kb1; kb0 += kSub) {
       const int n_sub = u.kb1 - kb0 < kSub ? u.kb1 - kb0 : kSub;
@@ -515,6 +566,12 @@ __device__ void tma_role(const ExpertsParams& p, const Table& table, const Ring&
           load_k(wd, &p.tm_r[kXRowBoxes - 1], bar, p.r_blk, kb0, 128,
                  u.row0 + static_cast<int32_t>(rank) * 128, 0, kWBytes);
           load_k(rd, &p.tm_w, bar, p.w_blk, kb0, 128, u.n0 + mine, u.e, r_bytes(BN));
+        } else if constexpr (OP == kOpFp4) {
+          load_k(wd, &p.tm_w, bar, p.w_blk, kb0, 128, n, u.e, kWBytes);
+          load_k(rd, &p.tm_r[boxes - 1], bar, p.r_blk, kb0, 128, u.row0 + mine, 0, height * 128);
+          // (a piece is 64 8-byte elements; past the last columns' block: another's, not used)
+          tma_load_2d_pair(reinterpret_cast<uint8_t*>(ring.scales) + stage * scale_stage(BN), &p.tm_s, bar,
+                           kb0 * (2 * kPiece / 8), u.e * ((p.wide + 127) / 128) + n / 128);
         } else if constexpr (OP == kOpWeight) {
           load_mn(wd, &p.tm_w, bar, p.w_blk, n, u.row0 + kb0 * 64, 0, false);
           load_mn(rd, &p.tm_r[half == 64], bar, p.r_blk, u.kt0 + mine, u.row0 + kb0 * 64, 0, half == 64);
@@ -557,7 +614,7 @@ template <int BN>
 __device__ void zero_role(const ExpertsParams& p, const Table& table,
                           const Ring& ring, uint32_t rank, int lane) {
   Schedule<kOpWeight, BN> sch(p, table);
-  constexpr int kStagesX = stages_of(BN);
+  constexpr int kStagesX = stages_of(kOpWeight, BN);
   const uint32_t zfull0 = mapa_shared(smem_u32(ring.zfull), 0);
   uint32_t stages = 0, used = 0;  // stages so far; bit s: parity of stage s's tails
   Unit u;
@@ -721,13 +778,83 @@ __device__ void scale_long_role(const ExpertsParams& p, const Table& table,
   }
 }
 
+// ------------------------------------------------------------------ scales (e2m1)
+// The tile's rows' scales of each stage, as pieces of 128 rows: row r's word at (r % 32) *
+// 16 + (r / 32) * 4, so that a lane's four words are one store of 16 bytes.  Both CTAs
+// hold those of all rows (each multiplies its half of the columns with all of them).  The
+// next stage's words are on their way while this one's wait for their place.
+template <int BN>
+__device__ void scale4_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int lane) {
+  Schedule<kOpFp4, BN> sch(p, table);
+  constexpr int kStagesX = stages_of(kOpFp4, BN), kWords = 4 * row_pieces(BN);
+  const uint32_t zfull0 = mapa_shared(smem_u32(ring.zfull), 0);
+  const int32_t KA = (p.red + 127) / 128;
+  Unit u;
+  int32_t i = 0, kb = 0, row0 = 0, cnt = 0, kb_end = 0;
+  // The next stage's words; false behind the last stage.
+  auto next = [&](uint32_t (&v)[kPieces][kWords]) {
+    if (kb >= kb_end) {
+      do {
+        if (!sch.get(i++, u)) return false;
+      } while (u.kb0 >= u.kb1);
+      kb = u.kb0;
+      kb_end = u.kb1;
+      row0 = u.row0 + lane;
+      cnt = u.cnt - lane;
+    }
+    const uint32_t* from = p.xs4 + static_cast<int64_t>(kb) * 2 * p.rows + row0;
+    const int32_t pieces = KA - kb * 2;
+#pragma unroll
+    for (int a = 0; a < kPieces; ++a)
+#pragma unroll
+      for (int j = 0; j < kWords; ++j)
+        v[a][j] = j * 32 < BN && j * 32 < cnt && a < pieces ? from[static_cast<int64_t>(a) * p.rows + j * 32] : 0u;
+    kb += kSub;
+    return true;
+  };
+  uint32_t v[kPieces][kWords];
+  int stage = 0;
+  uint32_t phase = 0;
+  bool more = next(v), ok = true;
+  while (more) {
+    uint32_t w[kPieces][kWords];
+#pragma unroll
+    for (int a = 0; a < kPieces; ++a)
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) w[a][j] = v[a][j];
+    more = next(v);
+    ok = mbar_wait(&ring.empty[stage], phase ^ 1u, p.timeout_ns, ring.abort, p.status);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    uint8_t* to = reinterpret_cast<uint8_t*>(ring.scales) + stage * scale_stage(BN) + kPieces * kPiece + lane * 16;
+#pragma unroll
+    for (int a = 0; a < kPieces; ++a)
+#pragma unroll
+      for (int r = 0; r < row_pieces(BN); ++r)
+        *reinterpret_cast<uint4*>(to + (a * row_pieces(BN) + r) * kPiece) =
+            make_uint4(w[a][4 * r], w[a][4 * r + 1], w[a][4 * r + 2], w[a][4 * r + 3]);
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(zfull0 + stage * 8);
+    __syncwarp();
+    if (++stage == kStagesX) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  if (!ok && lane == 0) {
+    set_status(p.status, kStatusPipelineTimeout, 0x500u | rank);
+    *ring.abort = 1;
+  }
+}
+
 // ------------------------------------------------------------------ MMA (one warp)
 // The warp waits and computes together; lane 0 issues.
 template <int OP, int BN>
 __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring& ring,
                          int lane, uint32_t tmem) {
   Schedule<OP, BN> sch(p, table);
-  constexpr int kStagesX = stages_of(BN);
+  constexpr int kStagesX = stages_of(OP, BN);
   constexpr bool kWMn = OP == kOpForward || OP == kOpWeight;
   constexpr bool kRMn = OP == kOpWeight;
   // 128-byte swizzle.  K-major: groups of 8 rows 1024 B apart, 32 B further per step.
@@ -756,7 +883,7 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
                            (!is_fp8(OP) && p.bf16 ? kIdescAbBf16 : 0u);
     const uint32_t r_second = kRMn ? 64 * 128 / 16
                               : OP == kOpFp8Long ? r_bytes(BN) / 16
-                                                 : static_cast<uint32_t>(box_of<BN>(width / 2) * (BN / 8) * 128 / 16);
+                                                 : static_cast<uint32_t>(box_height(BN, box_of<BN>(width / 2)) * 128 / 16);
     const int32_t segment = OP == kOpFp8Long ? 1 : OP == kOpFp8 ? kFewBlocks : p.segment;
     int32_t left = 0;  // k-blocks left of the segment
     for (int32_t kb0 = kb_begin; kb0 < kb_end; kb0 += kSub) {
@@ -778,6 +905,9 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
       } else {
         ok = warp_wait(&ring.full[stage], (full_phase >> stage) & 1u, p.timeout_ns, ring.abort,
                        p.status);
+        if (OP == kOpFp4 && ok)  // and the rows' scales, from both CTAs' scale warps
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&ring.zfull[stage], (full_phase >> stage) & 1u,
+                                                         p.timeout_ns, ring.abort, p.status));
         full_phase ^= 1u << stage;
       }
       if (!ok) break;
@@ -788,8 +918,32 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
       for (int s = 0; s < kSub; ++s) {
         if (s >= n_sub) break;
         if (OP == kOpFp8Long && !(ok = accumulator())) break;
-        const uint32_t d = tmem + (acc & 1u) * kAccCols +
+        const uint32_t d = tmem + (acc & 1u) * acc_cols(OP) +
                            (OP == kOpFp8 ? (kFewBlocks - left + s) * kXFewRows : 0);
+        if constexpr (OP == kOpFp4) {
+          const int32_t rest = (p.red - (kb0 + s) * 256 + 63) / 64, steps = rest < 4 ? rest : 4;
+          const uint32_t sf = tmem + kScaleCol + s * kScaleCols;
+          const uint32_t from = smem_u32(ring.scales) + stage * scale_stage(BN);
+          if (elect_one()) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+              if (2 * a < steps) {
+                copy_scales_pair(sf + 4 * a, from + (2 * s + a) * kPiece);
+#pragma unroll
+                for (int r = 0; r < row_pieces(BN); ++r)
+                  if (r * 128 < width)
+                    copy_scales_pair(sf + 8 + 8 * a + 4 * r,
+                                     from + (kPieces + (2 * s + a) * row_pieces(BN) + r) * kPiece);
+              }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < steps)
+                mma_f4_pair(d, ws + (s * kWSecond + k * kWStep), rs + (s * r_second + k * kRStep),
+                            idesc_f4(width, 2 * (k & 1)), sf + 4 * (k >> 1), sf + 8 + 8 * (k >> 1),
+                            (!first || s > 0 || k > 0) ? 1u : 0u);
+          }
+          continue;
+        }
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -1118,7 +1272,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
           return;
         }
         tc_fence_after();
-        const uint32_t from = from0 + slot * kAccCols;
+        const uint32_t from = from0 + slot * acc_cols(OP);
         if constexpr (OP == kOpFp8) {
           // four k-blocks side by side: this warp's columns of each, times their scales
           const float* scale = ring.scales + slot * (kFewBlocks * BN) + c_first;
@@ -1226,7 +1380,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
 template <int OP, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     experts_kernel(const __grid_constant__ ExpertsParams p) {
-  constexpr int kStagesX = stages_of(BN);
+  constexpr int kStagesX = stages_of(OP, BN);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -1283,6 +1437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     head[Table::kInverse + lane] = static_cast<int32_t>(lane ? 0xffffffffu / static_cast<uint32_t>(lane) : 0u);
   if (warp == 2 && lane <= kXRowBoxes)  // the descriptors' first use would wait for them
     tma_prefetch_desc(lane == kXRowBoxes ? &p.tm_w : &p.tm_r[OP == kOpWeight ? lane & 1 : lane]);
+  if (OP == kOpFp4 && warp == 4 && lane == 0) tma_prefetch_desc(&p.tm_s);
   tc_fence_before();
   cluster_arrive();  // barriers initialised, TMEM allocated; the table is read meanwhile
   pdl_wait();        // from here on global memory is read
@@ -1306,6 +1461,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       scale_role<BN>(p, table, ring, rank, lane);
     } else if constexpr (OP == kOpFp8Long) {
       scale_long_role<BN>(p, table, ring, rank, lane);
+    } else if constexpr (OP == kOpFp4) {
+      scale4_role<BN>(p, table, ring, rank, lane);
     }
   } else if (threadIdx.x == 0) {
     set_status(p.status + 2, kStatusOffsets, 0);
@@ -1349,6 +1506,7 @@ Variant variant(int op, bool few) {
     case kOpForward: return few ? variant_of<kOpForward, kXFewRows>() : variant_of<kOpForward, kXRows>();
     case kOpInput: return few ? variant_of<kOpInput, kXFewRows>() : variant_of<kOpInput, kXRows>();
     case kOpWeight: return variant_of<kOpWeight, kXRows>();
+    case kOpFp4: return few ? variant_of<kOpFp4, kXFewRows>() : variant_of<kOpFp4, kXRows4>();
     default: return few ? variant_of<kOpFp8, kXFewRows>() : variant_of<kOpFp8Long, kXRows>();
   }
 }
@@ -1359,7 +1517,7 @@ cudaError_t experts_prepare(int* pairs) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   int least = sms / 2;
-  for (int op = 0; op < 4 && e == cudaSuccess; ++op)
+  for (int op : {kOpForward, kOpInput, kOpWeight, kOpFp8, kOpFp4})
     for (int few = 0; few < 2 && e == cudaSuccess; ++few) {
       const Variant v = variant(op, few != 0);
       e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);

@@ -8,7 +8,7 @@
 
 namespace agg {
 
-// The four products of the kernel.  "Wide" is the output's contiguous dimension,
+// The products of the kernel.  "Wide" is the output's contiguous dimension,
 // the MMA's M; "rows" its N.
 enum ExpertsOp : int {
   kOpForward = 0,   // y[r][n]  = sum_k x[r][k] w[e][k][n]     wide n, rows r, over k
@@ -16,24 +16,31 @@ enum ExpertsOp : int {
   kOpWeight = 2,    // dw[e][k][n] = sum_r x[r][k] dy[r][n]    wide n, rows k, over e's rows r
   kOpFp8 = 3,       // y[r][n] with e4m3 operands and scales   wide n, rows r, over k
   kOpFp8Long = 4,   // the same with rows as the MMA's M (chosen by the launcher)
+  kOpFp4 = 5,       // y[r][n] with e2m1 operands and e8m0 scales, over k
 };
 
 constexpr int kXWide = 256;    // a pair's tile: 256 of the wide dimension
 constexpr int kXRows = 256;    // and up to 256 rows,
 constexpr int kXFewRows = 64;  // or up to 64 where groups are short
-constexpr int kXRowBoxes = 4;  // box heights of the row operand: 1/4 to 4/4 of half a tile
+constexpr int kXRows4 = 224;   // e2m1: up to 224 (two accumulators of 224 leave TMEM columns for the scales)
+constexpr int kXRowBoxes = 4;  // box heights of the row operand: a quarter of half a tile, in whole 8 rows, to all of it
+__host__ __device__ constexpr int box_step(int tile_rows) { return (tile_rows / 8 + 7) / 8 * 8; }
+__host__ __device__ constexpr int box_height(int tile_rows, int boxes) {
+  return boxes * box_step(tile_rows) < tile_rows / 2 ? boxes * box_step(tile_rows) : tile_rows / 2;
+}
 constexpr int kXSub = 2;       // k-blocks of 128 bytes per stage of the ring
 constexpr int kXEpiWarps = 16;
 // TMA warp, MMA warp, epilogue warps; the weight gradient's zeroing warp, or the
-// scale warp of e4m3.
+// scale warp of e4m3 and e2m1.
 __host__ __device__ constexpr int threads_of(int op) {
-  return 32 * (2 + kXEpiWarps + (op == kOpWeight || op == kOpFp8 || op == kOpFp8Long ? 1 : 0));
+  return 32 * (2 + kXEpiWarps + (op == kOpForward || op == kOpInput ? 0 : 1));
 }
 constexpr int kXGroup = 8;     // row tiles that share the weights they read (tile order)
 
 struct ExpertsParams {
   CUtensorMap tm_w;              // the wide operand
   CUtensorMap tm_r[kXRowBoxes];  // the row operand, by box height (weight gradient: of 128 and of 64 columns)
+  CUtensorMap tm_s;              // e2m1: the weights' scales, pieces of 128 rows x 4 scales side by side
   const int32_t* offsets;        // [E + 1], or null: one group of all rows
   int32_t E;
   int32_t rows;                  // rows of the inputs
@@ -51,6 +58,7 @@ struct ExpertsParams {
   int64_t ldo;
   const float* xs;               // e4m3: row scales [KB][rows]
   const float* ws;               // e4m3: weight scales [E][NB][KB]
+  const uint32_t* xs4;           // e2m1: row scales, four to a word, [ceil(K / 128)][rows]
   float* partials;               // split sums: [unit][warps of the pair][columns][32 lanes]
   uint32_t* arrivals;            // [tile][warps of the pair], zero between runs
   int32_t max_units;             // units the workspace holds (0: never split)
@@ -72,6 +80,7 @@ struct SplitPrice {
 __host__ __device__ constexpr SplitPrice split_price(int op, bool short_tiles) {
   return op == kOpFp8 ? SplitPrice{9, 1}
          : op == kOpFp8Long ? SplitPrice{9, 3}
+         : op == kOpFp4 ? SplitPrice{9, short_tiles ? 1 : 3}
          : op == kOpWeight ? SplitPrice{14, short_tiles ? 3 : 5}  // half tiles, whole ones
                            : SplitPrice{14, short_tiles ? 2 : 5};
 }

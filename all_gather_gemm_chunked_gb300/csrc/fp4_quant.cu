@@ -1,0 +1,155 @@
+// fp4_quant.cu -- microscaled e2m1 operands (fp4_codes.cuh) of rows and of weights.
+
+#include "fp4_codes.cuh"
+#include "moe_rows.cuh"
+#include "moe_types.cuh"
+
+namespace agg {
+
+namespace {
+// Bound by memory (2 bytes in, a little above half a byte out per element).  A warp takes
+// 256 elements of a row per step, 8 per lane: 4 lanes make one block, whose maximum takes
+// two shuffles, and 16 lanes the word of four scales.  All of a lane's loads are issued
+// before the first use.  The eight warps of a block take eight neighbouring rows, so that
+// the words they write ([K / 128][row]) fill 32-byte sectors.
+constexpr int kQuantSteps = 4;
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_rows4_kernel(int64_t rows, int64_t K, const T* x, int64_t ldx,
+                                                             int64_t src_rows, const int32_t* order, int k,
+                                                             uint8_t* __restrict__ q, uint32_t* __restrict__ scales) {
+  pdl_enter();
+  constexpr int V = Elem<T>::kVec;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  if (r >= rows) return;
+  int64_t src = r;
+  bool in = true;
+  if (order) {
+    const int32_t o = order[r];
+    src = o / k;
+    in = o >= 0;
+  }
+  in = in && src < src_rows;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (256 * kQuantSteps) + lane * 8;
+  float f[kQuantSteps][8 / V][V];
+#pragma unroll
+  for (int i = 0; i < kQuantSteps; ++i) {
+    const int64_t c = c0 + i * 256;  // (K % 32 == 0: a lane's 8 elements are all in or all out)
+#pragma unroll
+    for (int h = 0; h < 8 / V; ++h) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[i][h][v] = 0.0f;
+      if (in && c < K) load_elems<T, V>(x + src * ldx + c + h * V, f[i][h]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kQuantSteps; ++i) {
+    const int64_t c = c0 + i * 256;
+    float g[8];
+    uint32_t largest = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      g[j] = f[i][j / V][j % V];
+      largest = max(largest, magnitude_bits(g[j]));
+    }
+    largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
+    largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
+    const uint32_t s = micro_scale(largest);
+    const float inv = micro_inverse(s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] *= inv;
+    uint32_t word = s << ((lane >> 2 & 3) * 8);
+    word |= __shfl_xor_sync(0xffffffffu, word, 4);
+    word |= __shfl_xor_sync(0xffffffffu, word, 8);
+    if (c < K) *reinterpret_cast<uint32_t*>(q + (r * K + c) / 2) = e2m1x8(g);
+    if ((lane & 15) == 0 && c < K) scales[(c / kScaleBlock) * rows + r] = word;
+  }
+}
+
+// Two neighbouring elements as floats.
+template <typename T>
+__device__ __forceinline__ float2 load_two(const T* p) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+  const T* v = reinterpret_cast<const T*>(&u);
+  return make_float2(Elem<T>::get(v[0]), Elem<T>::get(v[1]));
+}
+template <>
+__device__ __forceinline__ float2 load_two<float>(const float* p) {
+  return *reinterpret_cast<const float2*>(p);
+}
+
+// One block per 128 x 128 block of an expert's weights (done once per model): a thread
+// holds one block of 32 along K of two columns, all its loads in flight, and writes their
+// 16 bytes of codes each; the four threads of a column write 64 neighbouring bytes.
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_weights4_kernel(int64_t K, int64_t N, const T* w,
+                                                                uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+  pdl_enter();
+  const int64_t KB = (K + kScaleBlock - 1) / kScaleBlock, NB = (N + kScaleBlock - 1) / kScaleBlock;
+  const int64_t kb = blockIdx.x % KB, nb = (blockIdx.x / KB) % NB, e = blockIdx.x / (KB * NB);
+  const int col = (threadIdx.x & 63) * 2, part = threadIdx.x >> 6;
+  const int64_t n = nb * kScaleBlock + col, k0 = kb * kScaleBlock + part * kMicroBlock;
+  const bool in = n < N && k0 < K;  // (N is even, K a multiple of 32: all of both columns' blocks, or nothing)
+  float v[2][kMicroBlock];
+#pragma unroll
+  for (int i = 0; i < kMicroBlock; ++i) {
+    float2 f = make_float2(0.0f, 0.0f);
+    if (in) f = load_two(w + (e * K + k0 + i) * N + n);
+    v[0][i] = f.x;
+    v[1][i] = f.y;
+  }
+  uint8_t* piece = scales + ((e * NB + nb) * KB + kb) * 512 + part;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t largest = 0;
+#pragma unroll
+    for (int i = 0; i < kMicroBlock; ++i) largest = max(largest, magnitude_bits(v[h][i]));
+    const uint32_t s = micro_scale(largest);
+    const float inv = micro_inverse(s);
+    uint32_t word[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float g[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = v[h][8 * j + i] * inv;
+      word[j] = e2m1x8(g);
+    }
+    if (in) *reinterpret_cast<uint4*>(q + ((e * N + n + h) * K + k0) / 2) = make_uint4(word[0], word[1], word[2], word[3]);
+    const int c = col + h;
+    piece[(c & 31) * 16 + (c >> 5) * 4] = static_cast<uint8_t>(s);
+  }
+}
+}  // namespace
+
+cudaError_t launch_quantize_rows4(int64_t rows, int64_t K, int dtype, const void* x, int64_t ldx,
+                                  int64_t src_rows, const int32_t* order, int k, void* q,
+                                  void* scales, cudaStream_t stream) {
+  if (rows == 0) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>((rows + 7) / 8),
+                  static_cast<unsigned>((K + 256 * kQuantSteps - 1) / (256 * kQuantSteps)));
+  uint8_t* out = static_cast<uint8_t*>(q);
+  uint32_t* words = static_cast<uint32_t*>(scales);
+  if (dtype == kTypeF32)
+    return launch(quantize_rows4_kernel<float>, grid, 256, stream, rows, K, static_cast<const float*>(x), ldx,
+                  src_rows, order, k, out, words);
+  if (dtype == kTypeF16)
+    return launch(quantize_rows4_kernel<__half>, grid, 256, stream, rows, K, static_cast<const __half*>(x), ldx,
+                  src_rows, order, k, out, words);
+  return launch(quantize_rows4_kernel<__nv_bfloat16>, grid, 256, stream, rows, K,
+                static_cast<const __nv_bfloat16*>(x), ldx, src_rows, order, k, out, words);
+}
+
+cudaError_t launch_quantize_weights4(int E, int64_t K, int64_t N, int dtype, const void* w, void* q,
+                                     void* scales, cudaStream_t stream) {
+  const int64_t blocks = E * ((K + kScaleBlock - 1) / kScaleBlock) * ((N + kScaleBlock - 1) / kScaleBlock);
+  const unsigned grid = static_cast<unsigned>(blocks);
+  uint8_t *out = static_cast<uint8_t*>(q), *bytes = static_cast<uint8_t*>(scales);
+  if (dtype == kTypeF32)
+    return launch(quantize_weights4_kernel<float>, dim3(grid), 256, stream, K, N, static_cast<const float*>(w), out, bytes);
+  if (dtype == kTypeF16)
+    return launch(quantize_weights4_kernel<__half>, dim3(grid), 256, stream, K, N, static_cast<const __half*>(w), out, bytes);
+  return launch(quantize_weights4_kernel<__nv_bfloat16>, dim3(grid), 256, stream, K, N,
+                static_cast<const __nv_bfloat16*>(w), out, bytes);
+}
+
+}  // namespace agg

@@ -1,4 +1,5 @@
-// front.cpp -- native part of the torch front end of include/ag_moe.h (moe.py, fp8.py):
+// front.cpp -- native part of the torch front end of include/ag_moe.h and ag_layer.h
+// (moe.py, fp8.py, fp4.py):
 // checks tensors, allocates outputs, takes the current stream and calls the library.
 // A call's host time decides how long a small operator takes: in Python the checks,
 // the allocation and the foreign call took 10 to 18 us a call, longer than the kernels.
@@ -19,6 +20,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
+#include "ag_layer.h"
 #include "ag_moe.h"
 
 namespace {
@@ -193,6 +195,8 @@ PyObject* tuple_of(T&&... t) {
 constexpr auto kI32 = at::ScalarType::Int;
 constexpr auto kF32 = at::ScalarType::Float;
 constexpr auto kE4m3 = at::ScalarType::Float8_e4m3fn;
+constexpr auto kE8m0 = at::ScalarType::Float8_e8m0fnu;
+constexpr auto kByte = at::ScalarType::Byte;
 
 int64_t blocks(int64_t n) { return (n + AG_MOE_SCALE_BLOCK - 1) / AG_MOE_SCALE_BLOCK; }
 
@@ -334,6 +338,18 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   AGG_END
 }
 
+// The rows of x, or those that a routing gathers of them.
+struct Gathered {
+  int64_t rows, k;
+  const int32_t* order;
+};
+Gathered gathered(PyObject* order, PyObject* slots_o, const at::Tensor& x) {
+  if (order == Py_None) return {x.size(0), 1, nullptr};
+  const at::Tensor& slots = tensor(slots_o, "routing.slots", x);
+  const int64_t k = slots.dim() == 2 ? slots.size(1) : 0, rows = x.size(0) * k;
+  return {rows, k, plain<int32_t>(order, "routing.order", kI32, {rows}, x)};
+}
+
 // quantize_rows(x, order or None, slots or None) -> codes, scales
 PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   AGG_BEGIN
@@ -341,18 +357,11 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& x = tensor(a[0], "x");
   const int type = float_type(x, "x");
   const int64_t ld = pitch(x, "x"), src = x.size(0), K = x.size(1);
-  int64_t rows = src, k = 1;
-  const int32_t* order = nullptr;
-  if (a[1] != Py_None) {
-    const at::Tensor& slots = tensor(a[2], "routing.slots", x);
-    k = slots.dim() == 2 ? slots.size(1) : 0;
-    rows = src * k;
-    order = plain<int32_t>(a[1], "routing.order", kI32, {rows}, x);
-  }
+  const Gathered g = gathered(a[1], a[2], x);
   const Current current(x);
-  Pieces pieces(Pieces::room(rows * K) + Pieces::room(blocks(K) * rows * 4), x);
-  at::Tensor q = pieces.take({rows, K}, kE4m3), s = pieces.take({blocks(K), rows}, kF32);
-  check_rc(ag_fp8_quantize_rows(rows, K, type, x.data_ptr(), ld, src, order, static_cast<int>(k), q.data_ptr(),
+  Pieces pieces(Pieces::room(g.rows * K) + Pieces::room(blocks(K) * g.rows * 4), x);
+  at::Tensor q = pieces.take({g.rows, K}, kE4m3), s = pieces.take({blocks(K), g.rows}, kF32);
+  check_rc(ag_fp8_quantize_rows(g.rows, K, type, x.data_ptr(), ld, src, g.order, static_cast<int>(g.k), q.data_ptr(),
                                 static_cast<float*>(s.data_ptr()), stream_of(x)));
   return tuple_of(q, s);
   AGG_END
@@ -499,12 +508,77 @@ PyObject* fp8_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   AGG_END
 }
 
+// fp4_quantize_rows(x, order or None, slots or None) -> codes, scales
+PyObject* fp4_quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  AGG_BEGIN
+  check_args(n, 3);
+  const at::Tensor& x = tensor(a[0], "x");
+  const int type = float_type(x, "x");
+  const int64_t ld = pitch(x, "x"), src = x.size(0), K = x.size(1);
+  const Gathered g = gathered(a[1], a[2], x);
+  const Current current(x);
+  Pieces pieces(Pieces::room(g.rows * (K / 2)) + Pieces::room(blocks(K) * g.rows * 4), x);
+  at::Tensor q = pieces.take({g.rows, K / 2}, kByte), s = pieces.take({blocks(K), g.rows, 4}, kE8m0);
+  check_rc(ag_fp4_quantize_rows(g.rows, K, type, x.data_ptr(), ld, src, g.order, static_cast<int>(g.k), q.data_ptr(),
+                                s.data_ptr(), stream_of(x)));
+  return tuple_of(q, s);
+  AGG_END
+}
+
+// fp4_quantize_weights(w) -> codes, scales
+PyObject* fp4_quantize_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  AGG_BEGIN
+  check_args(n, 1);
+  const at::Tensor& w = tensor(a[0], "w");
+  const int type = float_type(w, "w");
+  if ((w.dim() != 2 && w.dim() != 3) || !w.is_contiguous())
+    raise(PyExc_ValueError, "w must be a contiguous (E, K, N) or (K, N) tensor");
+  const bool many = w.dim() == 3;
+  const int64_t E = many ? w.size(0) : 1, K = w.size(-2), N = w.size(-1);
+  if (E > AG_MOE_MAX_EXPERTS) raise(PyExc_ValueError, "w has too many experts");
+  const Current current(w);
+  at::Tensor q = make({E, N, K / 2}, kByte, w), s = make({E, blocks(N), blocks(K), 32, 4, 4}, kE8m0, w);
+  check_rc(ag_fp4_quantize_weights(static_cast<int>(E), K, N, type, w.data_ptr(), q.data_ptr(), s.data_ptr(),
+                                   stream_of(w)));
+  if (!many) {
+    q = q.squeeze(0);
+    s = s.squeeze(0);
+  }
+  return tuple_of(q, s);
+  AGG_END
+}
+
+// fp4_product(handle, E, K, N, xq, xs, wq, ws, offsets, out, out_dtype)
+PyObject* fp4_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  AGG_BEGIN
+  check_args(n, 11);
+  const PlanArgs p = plan_args(a);
+  const at::Tensor &x = tensor(a[4], "xq", p), &w = tensor(a[6], "wq", x);
+  const int64_t rows = x.dim() > 0 ? x.size(0) : 0, kb = blocks(p.K), nb = blocks(p.N);
+  const void* xq = plain(a[4], "xq", kByte, {rows, p.K / 2}, x);
+  const void* xs = plain(a[5], "xs", kE8m0, {kb, rows, 4}, x);
+  const bool one = p.E == 1 && w.dim() == 2;
+  const void* wq = one ? plain(a[6], "wq", kByte, {p.N, p.K / 2}, x) : plain(a[6], "wq", kByte, {p.E, p.N, p.K / 2}, x);
+  const void* ws = one ? plain(a[7], "ws", kE8m0, {nb, kb, 32, 4, 4}, x)
+                       : plain(a[7], "ws", kE8m0, {p.E, nb, kb, 32, 4, 4}, x);
+  const int32_t* off = offsets_of(a[8], p.E, x);
+  const at::ScalarType ot = dtype_of(a[10]);
+  const Current current(x);
+  at::Tensor out = output(a[9], {rows, p.N}, ot, x);
+  const int64_t ldo = pitch(out, "out");
+  check_rc(ag_fp4_forward(p.plan, rows, xq, xs, off, wq, ws, out.data_ptr(), ldo, type_code(ot), stream_of(x)));
+  return wrap(out);
+  AGG_END
+}
+
 #define AGG_METHOD(f) \
   { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {AGG_METHOD(init),         AGG_METHOD(route),         AGG_METHOD(route_backward),
                          AGG_METHOD(gather),       AGG_METHOD(combine),       AGG_METHOD(combine_backward),
                          AGG_METHOD(quantize_rows), AGG_METHOD(quantize_weights), AGG_METHOD(rows_product),
-                         AGG_METHOD(weight_product), AGG_METHOD(fp8_product),  {nullptr, nullptr, 0, nullptr}};
+                         AGG_METHOD(weight_product), AGG_METHOD(fp8_product),
+                         AGG_METHOD(fp4_quantize_rows), AGG_METHOD(fp4_quantize_weights), AGG_METHOD(fp4_product),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_front", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

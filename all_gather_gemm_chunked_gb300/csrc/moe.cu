@@ -7,20 +7,27 @@
 #include <mutex>
 #include <new>
 
+#include "ag_layer.h"
 #include "ag_moe.h"
+#include "checks.h"
 #include "experts_kernel.cuh"
 #include "fused_kernel.cuh"
 #include "host.h"
 #include "moe_rows.cuh"
 
 using agg::aligned16;
+using agg::check_matrix;
 using agg::cuda_fail;
 using agg::DeviceGuard;
 using agg::encode_tiled;
+using agg::esize;
 using agg::fail;
+using agg::float_type;
+using agg::kMaxRowLen;
+using agg::launched;
 using agg::log_msg;
 
-static_assert(AG_MOE_F32 == agg::kTypeF32 && AG_MOE_E4M3 == agg::kTypeE4m3 &&
+static_assert(AG_MOE_F32 == agg::kTypeF32 && AG_MOE_E4M3 == agg::kTypeE4m3 && AG_MOE_E2M1 == agg::kTypeE2m1 &&
                   AG_GEMM_F16 == agg::kTypeF16 && AG_GEMM_BF16 == agg::kTypeBf16 &&
                   AG_MOE_MAX_EXPERTS == agg::kMaxExperts && AG_MOE_MAX_TOP_K == agg::kMaxTopK &&
                   AG_MOE_SCALE_BLOCK == agg::kScaleBlock,
@@ -29,12 +36,6 @@ static_assert(AG_MOE_F32 == agg::kTypeF32 && AG_MOE_E4M3 == agg::kTypeE4m3 &&
 namespace {
 
 constexpr int64_t kMaxTokens = 1LL << 28;   // (the router then takes 4097 blocks)
-constexpr int64_t kMaxRowLen = 1LL << 24;   // columns of a moved row (grid limit)
-
-bool float_type(int dtype) {
-  return dtype == AG_GEMM_F16 || dtype == AG_GEMM_BF16 || dtype == AG_MOE_F32;
-}
-int esize(int dtype) { return dtype == AG_MOE_F32 ? 4 : dtype == AG_MOE_E4M3 ? 1 : 2; }
 
 // ------------------------------------------------------------------ router, rows
 int check_route(int64_t T, int E, int k, int dtype) {
@@ -73,10 +74,6 @@ agg::RouteArgs route_args(int64_t T, int E, int k, int dtype, const void* logits
   a.dtype = dtype;
   a.normalize = normalize;
   return a;
-}
-
-int launched(cudaError_t e, const char* what) {
-  return e == cudaSuccess ? AG_GEMM_OK : cuda_fail(e, what);
 }
 
 }  // namespace
@@ -215,34 +212,34 @@ int encode_mn_major(CUtensorMap* map, const void* base, int64_t cols, int64_t ro
   return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, 3, dims, strides, box);
 }
 
-int check_matrix(const char* name, const void* p, int64_t ld, int64_t cols, int dtype) {
-  if (!p) return fail(AG_GEMM_ERR_INVALID, "%s is NULL", name);
-  if (!aligned16(p)) return fail(AG_GEMM_ERR_INVALID, "%s must be 16-byte aligned", name);
-  if (ld < cols || ld * esize(dtype) % 16 != 0)
-    return fail(AG_GEMM_ERR_INVALID, "%s: row pitch %lld must be at least %lld and a multiple of 16 bytes",
-                name, (long long)ld, (long long)cols);
-  if (ld >= (1LL << 36)) return fail(AG_GEMM_ERR_UNSUPPORTED, "%s: row pitch too large", name);
-  return AG_GEMM_OK;
-}
+// Operands of codes with scales.
+bool scaled(int dtype) { return dtype == AG_MOE_E4M3 || dtype == AG_MOE_E2M1; }
 
-int check_run(ag_moe_plan* p, bool fp8, int64_t rows, const int32_t* offsets, int out_dtype) {
+// codes: AG_MOE_E4M3 or AG_MOE_E2M1 where the product takes those, 0 for 16-bit operands.
+int check_run(ag_moe_plan* p, int codes, int64_t rows, const int32_t* offsets, int out_dtype) {
   if (!p) return fail(AG_GEMM_ERR_INVALID, "plan is NULL");
-  if ((p->dtype == AG_MOE_E4M3) != fp8)
-    return fail(AG_GEMM_ERR_INVALID, fp8 ? "ag_fp8_forward needs an AG_MOE_E4M3 plan"
-                                         : "this product needs an fp16 or bf16 plan (AG_MOE_E4M3: ag_fp8_forward)");
+  if (codes ? p->dtype != codes : scaled(p->dtype))
+    return fail(AG_GEMM_ERR_INVALID, codes == AG_MOE_E4M3 ? "ag_fp8_forward needs an AG_MOE_E4M3 plan"
+                                     : codes ? "ag_fp4_forward needs an AG_MOE_E2M1 plan"
+                                             : "this product needs an fp16 or bf16 plan (AG_MOE_E4M3: ag_fp8_forward, "
+                                               "AG_MOE_E2M1: ag_fp4_forward)");
   if (rows < 0 || rows > kMaxRows)
     return fail(AG_GEMM_ERR_INVALID, "rows must be in [0, %lld] (got %lld)", (long long)kMaxRows, (long long)rows);
   if (!offsets && p->E != 1)
     return fail(AG_GEMM_ERR_INVALID, "offsets may be NULL only for one expert (the plan has %d)", p->E);
   const bool ok = out_dtype == AG_MOE_F32 ||
-                  (fp8 ? out_dtype == AG_GEMM_F16 || out_dtype == AG_GEMM_BF16 : out_dtype == p->dtype);
+                  (codes ? out_dtype == AG_GEMM_F16 || out_dtype == AG_GEMM_BF16 : out_dtype == p->dtype);
   if (!ok) return fail(AG_GEMM_ERR_INVALID, "out_dtype %d does not fit the plan's type %d", out_dtype, p->dtype);
   return AG_GEMM_OK;
 }
 
+int tile_rows(const ag_moe_plan* p, bool few) {
+  return few ? agg::kXFewRows : p->dtype == AG_MOE_E2M1 ? agg::kXRows4 : agg::kXRows;
+}
+
 // Row tiles that the groups of so many rows can make.
 int64_t most_row_tiles(const ag_moe_plan* p, int64_t rows, bool few) {
-  return rows / (few ? agg::kXFewRows : agg::kXRows) + (rows < p->E ? rows : p->E);
+  return rows / tile_rows(p, few) + (rows < p->E ? rows : p->E);
 }
 
 // Short row tiles where the groups are short on average: 64 rows a tile leave ten
@@ -254,7 +251,7 @@ int64_t most_row_tiles(const ag_moe_plan* p, int64_t rows, bool few) {
 // against 10.1.  In two rounds of short tiles 1200 rows of 1024 x 2048 took 10.7 against
 // 12.1 us, 600 of 2048 x 3000 18.4 against 15.0; e4m3 1088 of 4096 x 2048 22.2 against 21.2.)
 bool few_rows(const ag_moe_plan* p, int64_t rows, int64_t wide) {
-  return rows <= static_cast<int64_t>(p->dtype == AG_MOE_E4M3 ? 96 : 64) * p->E ||
+  return rows <= static_cast<int64_t>(scaled(p->dtype) ? 96 : 64) * p->E ||
          most_row_tiles(p, rows, true) * ((wide + agg::kXWide - 1) / agg::kXWide) <= p->pairs;
 }
 
@@ -275,7 +272,8 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   x.inv_group = 0xffffffffu / static_cast<uint32_t>(agg::kXGroup * wide_tiles);
   x.inv_expert = op == agg::kOpWeight ? 0xffffffffu / static_cast<uint32_t>(wide_tiles * x.row_tiles) : 0;
   const bool fp8 = op == agg::kOpFp8;
-  const int64_t kb = op == agg::kOpWeight ? x.rows / 64 : (x.red + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
+  const int block_k = op == agg::kOpFp4 ? 256 : fp8 ? 128 : 64;
+  const int64_t kb = op == agg::kOpWeight ? x.rows / 64 : (x.red + block_k - 1) / block_k;
   // (where the tiles' number does not depend on offsets, two rounds of them never split)
   const bool plenty = (op == agg::kOpWeight || !x.offsets) && (row_tiles - 1) * wide_tiles >= 2 * p->pairs;
   const bool split = !plenty && may_split(kb, agg::split_price(fp8 && !few ? agg::kOpFp8Long : op,
@@ -318,20 +316,21 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   return AG_GEMM_OK;
 }
 
-// The row operand, once for each height of box that its tiles can have.
+// The row operand, once for each height of box that its tiles of `tile` rows can have
+// (`all`: whatever the rows).
 int encode_rows(agg::ExpertsParams& x, int dtype, const void* base, int64_t len, int64_t rows,
-                int64_t ld, bool few) {
-  const int step = (few ? agg::kXFewRows : agg::kXRows) / 8;
+                int64_t ld, int tile, bool all) {
+  const int step = agg::box_step(tile);
   const int64_t half = (rows + 31) / 32 * 16;  // of a CTA, in a tile of all rows
-  const int most = (dtype == AG_MOE_E4M3 && !few) || half >= 4 * step ? agg::kXRowBoxes
-                                                                   : static_cast<int>((half + step - 1) / step);
+  const int most = all || half >= 4 * step ? agg::kXRowBoxes : static_cast<int>((half + step - 1) / step);
   x.r_blk = whole_blocks(dtype, len);
   for (int i = 0; i < agg::kXRowBoxes; ++i) {
     if (i >= most) {
       x.tm_r[i] = x.tm_r[i - 1];
       continue;
     }
-    if (int rc = encode_k_major(&x.tm_r[i], dtype, base, len, rows, ld, 1, rows * ld, (i + 1) * step)) return rc;
+    if (int rc = encode_k_major(&x.tm_r[i], dtype, base, len, rows, ld, 1, rows * ld, agg::box_height(tile, i + 1)))
+      return rc;
   }
   return AG_GEMM_OK;
 }
@@ -341,7 +340,7 @@ int run_rows(ag_moe_plan* p, int op, int64_t rows, const void* in, int64_t ld_in
              const int32_t* offsets, const void* w, int64_t ldw, int64_t ldw_e, void* out,
              int64_t ld_out, int out_dtype, void* stream) {
   const bool fwd = op == agg::kOpForward;
-  if (int rc = check_run(p, false, rows, offsets, out_dtype)) return rc;
+  if (int rc = check_run(p, 0, rows, offsets, out_dtype)) return rc;
   const int64_t red = fwd ? p->K : p->N, wide = fwd ? p->N : p->K;
   if (rows == 0) return AG_GEMM_OK;
   if (int rc = check_matrix(fwd ? "x" : "dy", in, ld_in, red, p->dtype)) return rc;
@@ -356,7 +355,7 @@ int run_rows(ag_moe_plan* p, int op, int64_t rows, const void* in, int64_t ld_in
   agg::ExpertsParams x{};
   int rc = fwd ? encode_mn_major(&x.tm_w, w, p->N, p->K, ldw, p->E, ldw_e)
                : encode_k_major(&x.tm_w, p->dtype, w, p->N, p->K, ldw, p->E, ldw_e, 128);
-  if (rc || (rc = encode_rows(x, p->dtype, in, red, rows, ld_in, few))) return rc;
+  if (rc || (rc = encode_rows(x, p->dtype, in, red, rows, ld_in, tile_rows(p, few), false))) return rc;
   x.w_blk = whole_blocks(p->dtype, p->N);
   x.offsets = offsets;
   x.rows = static_cast<int32_t>(rows);
@@ -486,16 +485,54 @@ int ag_fp8_quantize_weights(int E, int64_t K, int64_t N, int dtype, const void* 
                   "weight quantisation launch");
 }
 
+int ag_fp4_quantize_rows(int64_t rows, int64_t K, int dtype, const void* x, int64_t ldx,
+                         int64_t src_rows, const int32_t* order, int top_k, void* q,
+                         void* scales, void* stream) {
+  if (!float_type(dtype)) return fail(AG_GEMM_ERR_INVALID, "x must be fp16, bf16 or fp32 (got type %d)", dtype);
+  if (rows < 0 || rows >= (1LL << 31) || src_rows < 0 || (!order && src_rows < rows))
+    return fail(AG_GEMM_ERR_INVALID, "rows must be in [0, 2^31) and, without order, at most src_rows (got %lld of %lld)",
+                (long long)rows, (long long)src_rows);
+  if (K < 32 || K % 32 != 0 || K > kMaxRowLen)
+    return fail(AG_GEMM_ERR_INVALID, "K must be a multiple of 32, at most %lld (got %lld)", (long long)kMaxRowLen,
+                (long long)K);
+  if (order && (top_k < 1 || top_k > agg::kMaxTopK))
+    return fail(AG_GEMM_ERR_INVALID, "top_k must be in [1, %d] (got %d)", agg::kMaxTopK, top_k);
+  if (rows == 0) return AG_GEMM_OK;
+  if (int rc = check_matrix("x", x, ldx, K, dtype)) return rc;
+  if (!q || !scales) return fail(AG_GEMM_ERR_INVALID, "a pointer is NULL");
+  if (!aligned16(q) || !aligned16(scales)) return fail(AG_GEMM_ERR_INVALID, "q and scales must be 16-byte aligned");
+  return launched(agg::launch_quantize_rows4(rows, K, dtype, x, ldx, src_rows, order, top_k, q, scales,
+                                             static_cast<cudaStream_t>(stream)),
+                  "row quantisation launch");
+}
+
+int ag_fp4_quantize_weights(int E, int64_t K, int64_t N, int dtype, const void* w, void* q,
+                            void* scales, void* stream) {
+  if (!float_type(dtype)) return fail(AG_GEMM_ERR_INVALID, "w must be fp16, bf16 or fp32 (got type %d)", dtype);
+  if (E < 1 || E > agg::kMaxExperts)
+    return fail(AG_GEMM_ERR_INVALID, "experts must be in [1, %d] (got %d)", agg::kMaxExperts, E);
+  if (K < 32 || K % 32 != 0 || N < 8 || N % 8 != 0 || K > kMaxRowLen || N > kMaxRowLen)
+    return fail(AG_GEMM_ERR_INVALID, "need K %% 32 == 0 and N %% 8 == 0, at most %lld (got %lld, %lld)",
+                (long long)kMaxRowLen, (long long)K, (long long)N);
+  if (E * ((K + 127) / 128) * ((N + 127) / 128) >= (1LL << 31))
+    return fail(AG_GEMM_ERR_UNSUPPORTED, "more than 2^31 pieces of scales");
+  if (!w || !q || !scales) return fail(AG_GEMM_ERR_INVALID, "a pointer is NULL");
+  if (!aligned16(w) || !aligned16(q) || !aligned16(scales))
+    return fail(AG_GEMM_ERR_INVALID, "w, q and scales must be 16-byte aligned");
+  return launched(agg::launch_quantize_weights4(E, K, N, dtype, w, q, scales, static_cast<cudaStream_t>(stream)),
+                  "weight quantisation launch");
+}
+
 ag_moe_plan* ag_moe_plan_create(int E, int64_t K, int64_t N, int dtype) {
-  if (dtype != AG_GEMM_F16 && dtype != AG_GEMM_BF16 && dtype != AG_MOE_E4M3) {
-    fail(AG_GEMM_ERR_INVALID, "dtype must be AG_GEMM_F16, AG_GEMM_BF16 or AG_MOE_E4M3 (got %d)", dtype);
+  if (dtype != AG_GEMM_F16 && dtype != AG_GEMM_BF16 && !scaled(dtype)) {
+    fail(AG_GEMM_ERR_INVALID, "dtype must be AG_GEMM_F16, AG_GEMM_BF16, AG_MOE_E4M3 or AG_MOE_E2M1 (got %d)", dtype);
     return nullptr;
   }
   if (E < 1 || E > agg::kMaxExperts) {
     fail(AG_GEMM_ERR_INVALID, "experts must be in [1, %d] (got %d)", agg::kMaxExperts, E);
     return nullptr;
   }
-  const int kmod = dtype == AG_MOE_E4M3 ? 16 : 8;
+  const int kmod = dtype == AG_MOE_E2M1 ? 32 : dtype == AG_MOE_E4M3 ? 16 : 8;
   if (K < kmod || K % kmod != 0 || N < 8 || N % 8 != 0 || K > kMaxRowLen || N > kMaxRowLen) {
     fail(AG_GEMM_ERR_INVALID, "need K %% %d == 0 and N %% 8 == 0, both in (0, %lld] (got %lld, %lld)", kmod,
          (long long)kMaxRowLen, (long long)K, (long long)N);
@@ -568,9 +605,9 @@ int ag_moe_plan_tile_rows(const ag_moe_plan* plan, int64_t rows, int input_gradi
   if (!plan) return fail(AG_GEMM_ERR_INVALID, "plan is NULL");
   if (rows < 0 || rows > kMaxRows)
     return fail(AG_GEMM_ERR_INVALID, "rows must be in [0, %lld] (got %lld)", (long long)kMaxRows, (long long)rows);
-  if (input_gradient && plan->dtype == AG_MOE_E4M3)
-    return fail(AG_GEMM_ERR_INVALID, "an AG_MOE_E4M3 plan has no input gradient");
-  return few_rows(plan, rows, input_gradient ? plan->K : plan->N) ? agg::kXFewRows : agg::kXRows;
+  if (input_gradient && scaled(plan->dtype))
+    return fail(AG_GEMM_ERR_INVALID, "an AG_MOE_E4M3 or AG_MOE_E2M1 plan has no input gradient");
+  return tile_rows(plan, few_rows(plan, rows, input_gradient ? plan->K : plan->N));
 }
 
 int64_t ag_moe_plan_status_word(ag_moe_plan* plan) {
@@ -641,7 +678,7 @@ int ag_moe_backward_input(ag_moe_plan* plan, int64_t rows, const void* dy, int64
 int ag_moe_backward_weight(ag_moe_plan* plan, int64_t rows, const void* x, int64_t ldx,
                            const void* dy, int64_t lddy, const int32_t* offsets, void* dw,
                            int out_dtype, void* stream) {
-  if (int rc = check_run(plan, false, rows, offsets, out_dtype)) return rc;
+  if (int rc = check_run(plan, 0, rows, offsets, out_dtype)) return rc;
   if (!dw) return fail(AG_GEMM_ERR_INVALID, "dw is NULL");
   if (!aligned16(dw)) return fail(AG_GEMM_ERR_INVALID, "dw must be 16-byte aligned");
   DeviceGuard dg(plan->device);
@@ -678,7 +715,7 @@ int ag_moe_backward_weight(ag_moe_plan* plan, int64_t rows, const void* x, int64
 int ag_fp8_forward(ag_moe_plan* plan, int64_t rows, const void* xq, const float* xs,
                    const int32_t* offsets, const void* wq, const float* ws, void* y, int64_t ldy,
                    int out_dtype, void* stream) {
-  if (int rc = check_run(plan, true, rows, offsets, out_dtype)) return rc;
+  if (int rc = check_run(plan, AG_MOE_E4M3, rows, offsets, out_dtype)) return rc;
   if (rows == 0) return AG_GEMM_OK;
   if (int rc = check_matrix("xq", xq, plan->K, plan->K, AG_MOE_E4M3)) return rc;
   if (int rc = check_matrix("wq", wq, plan->K, plan->K, AG_MOE_E4M3)) return rc;
@@ -689,7 +726,7 @@ int ag_fp8_forward(ag_moe_plan* plan, int64_t rows, const void* xq, const float*
   agg::ExpertsParams p{};
   int rc;
   if ((rc = encode_k_major(&p.tm_w, AG_MOE_E4M3, wq, plan->K, plan->N, plan->K, plan->E, plan->K * plan->N, 128)) ||
-      (rc = encode_rows(p, AG_MOE_E4M3, xq, plan->K, rows, plan->K, few)))
+      (rc = encode_rows(p, AG_MOE_E4M3, xq, plan->K, rows, plan->K, tile_rows(plan, few), !few)))
     return rc;
   p.w_blk = whole_blocks(AG_MOE_E4M3, plan->K);
   p.offsets = offsets;
@@ -702,6 +739,44 @@ int ag_fp8_forward(ag_moe_plan* plan, int64_t rows, const void* xq, const float*
   p.xs = xs;
   p.ws = ws;
   return run(plan, p, agg::kOpFp8, few, most_row_tiles(plan, rows, few), stream);
+}
+
+int ag_fp4_forward(ag_moe_plan* plan, int64_t rows, const void* xq, const void* xs,
+                   const int32_t* offsets, const void* wq, const void* ws, void* y, int64_t ldy,
+                   int out_dtype, void* stream) {
+  if (int rc = check_run(plan, AG_MOE_E2M1, rows, offsets, out_dtype)) return rc;
+  if (rows == 0) return AG_GEMM_OK;
+  const int64_t bytes = plan->K / 2;  // of a row: the loads take codes as bytes
+  if (int rc = check_matrix("xq", xq, bytes, bytes, AG_MOE_E4M3)) return rc;
+  if (int rc = check_matrix("wq", wq, bytes, bytes, AG_MOE_E4M3)) return rc;
+  if (int rc = check_matrix("y", y, ldy, plan->N, out_dtype)) return rc;
+  if (!xs || !ws) return fail(AG_GEMM_ERR_INVALID, "scales are NULL");
+  if (!aligned16(xs) || !aligned16(ws)) return fail(AG_GEMM_ERR_INVALID, "scales must be 16-byte aligned");
+  DeviceGuard dg(plan->device);
+  const bool few = few_rows(plan, rows, plan->N);
+  agg::ExpertsParams p{};
+  int rc;
+  if ((rc = encode_k_major(&p.tm_w, AG_MOE_E4M3, wq, bytes, plan->N, bytes, plan->E, bytes * plan->N, 128)) ||
+      (rc = encode_rows(p, AG_MOE_E4M3, xq, bytes, rows, bytes, tile_rows(plan, few), false)))
+    return rc;
+  // the weights' scales: pieces of 512 bytes along K, a stage's four in one load
+  const cuuint64_t pieces = static_cast<cuuint64_t>((plan->K + 127) / 128);
+  const cuuint64_t dims[2] = {pieces * 64, static_cast<cuuint64_t>(plan->E) * ((plan->N + 127) / 128)};
+  const cuuint64_t strides[1] = {pieces * 512};
+  const cuuint32_t box[2] = {2 * agg::kXSub * 64, 1};
+  if ((rc = encode_tiled(&p.tm_s, CU_TENSOR_MAP_DATA_TYPE_INT64, ws, 2, dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_NONE)))
+    return rc;
+  p.w_blk = whole_blocks(AG_MOE_E4M3, bytes);
+  p.offsets = offsets;
+  p.rows = static_cast<int32_t>(rows);
+  p.wide = static_cast<int32_t>(plan->N);
+  p.red = static_cast<int32_t>(plan->K);
+  p.out_type = out_dtype;
+  p.out = y;
+  p.ldo = ldy;
+  p.xs4 = static_cast<const uint32_t*>(xs);
+  return run(plan, p, agg::kOpFp4, few, most_row_tiles(plan, rows, few), stream);
 }
 
 }  // extern "C"

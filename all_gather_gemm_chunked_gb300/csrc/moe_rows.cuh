@@ -1,6 +1,7 @@
 // moe_rows.cuh -- launchers of the router and of the kernels that move rows
-// between tokens and experts (moe_rows.cu), and of the 8-bit quantisation
-// (fp8_quant.cu).  Arguments as in ag_moe.h, checked by the caller.
+// between tokens and experts (moe_rows.cu), and of the 8-bit and 4-bit quantisation
+// (fp8_quant.cu, fp4_quant.cu).  Arguments as in ag_moe.h and ag_layer.h, checked by
+// the caller.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -11,7 +12,7 @@ namespace agg {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
 constexpr int kScaleBlock = 128;
-enum ElemType : int { kTypeF16 = 0, kTypeBf16 = 2, kTypeF32 = 3, kTypeE4m3 = 4 };
+enum ElemType : int { kTypeF16 = 0, kTypeBf16 = 2, kTypeF32 = 3, kTypeE4m3 = 4, kTypeE2m1 = 5 };
 
 // Programmatic dependent launch: a kernel of this library may start while the kernel
 // before it in the stream is still running (launch latency and set-up overlap it) and
@@ -85,5 +86,10 @@ cudaError_t launch_quantize_rows(int64_t rows, int64_t K, int dtype, const void*
                                  float* scales, cudaStream_t stream);
 cudaError_t launch_quantize_weights(int E, int64_t K, int64_t N, int dtype, const void* w,
                                     void* q, float* scales, cudaStream_t stream);
+cudaError_t launch_quantize_rows4(int64_t rows, int64_t K, int dtype, const void* x, int64_t ldx,
+                                  int64_t src_rows, const int32_t* order, int k, void* q,
+                                  void* scales, cudaStream_t stream);
+cudaError_t launch_quantize_weights4(int E, int64_t K, int64_t N, int dtype, const void* w, void* q,
+                                     void* scales, cudaStream_t stream);
 
 }  // namespace agg

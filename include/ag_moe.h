@@ -107,8 +107,8 @@ int ag_fp8_quantize_weights(int E, int64_t K, int64_t N, int dtype, const void *
 /* ---------------------------------------------------------------- products by expert */
 /*
  * A plan serves the products of one layer's experts: E weight matrices K x N.
- * dtype AG_GEMM_F16 or AG_GEMM_BF16 (K, N multiples of 8), or AG_MOE_E4M3 (K % 16
- * == 0, N % 8 == 0).  It owns the status word and the workspace of the products that
+ * dtype AG_GEMM_F16 or AG_GEMM_BF16 (K, N multiples of 8), AG_MOE_E4M3 (K % 16
+ * == 0, N % 8 == 0), or AG_MOE_E2M1 (K % 32 == 0, N % 8 == 0; ag_layer.h).  It owns the status word and the workspace of the products that
  * split their sums (40 MB, from the first run that may do so on); runs on one plan that may use the workspace are serialised as those
  * of ag_gemm.h are, others may overlap where their streams let them.  Runs may be
  * captured into a CUDA graph, on several branches of it too; a replay is then the caller's
@@ -118,17 +118,17 @@ int ag_fp8_quantize_weights(int E, int64_t K, int64_t N, int dtype, const void *
  * E must be 1).  They must not decrease and must lie within [0, rows]; otherwise
  * the run writes nothing and the plan's status becomes AG_GEMM_ERR_INVALID.  Rows
  * of no group are not written.  rows <= 2^31 - 256.  out_dtype is the operands' type (for
- * AG_MOE_E4M3: AG_GEMM_F16 or AG_GEMM_BF16) or AG_MOE_F32.
+ * AG_MOE_E4M3 and AG_MOE_E2M1: AG_GEMM_F16 or AG_GEMM_BF16) or AG_MOE_F32.
  */
-enum { AG_MOE_E4M3 = 4 };
+enum { AG_MOE_E4M3 = 4, AG_MOE_E2M1 = 5 };
 typedef struct ag_moe_plan ag_moe_plan;
 
 ag_moe_plan *ag_moe_plan_create(int E, int64_t K, int64_t N, int dtype);
 void ag_moe_plan_destroy(ag_moe_plan *plan);
 /* The device that was current when the plan was made, and that its runs take place on. */
 int ag_moe_plan_device(const ag_moe_plan *plan);
-/* Rows of the tiles, 64 or 256, that a product of so many rows is cut into: the forward's
- * (ag_moe_forward, ag_fp8_forward) or the input gradient's.  They have kernels of their
+/* Rows of the tiles, 64 or 256 (AG_MOE_E2M1: 64 or 224), that a product of so many rows is
+ * cut into: the forward's (ag_moe_forward, ag_fp8_forward, ag_fp4_forward) or the input gradient's.  They have kernels of their
  * own; results may differ in the order of their sums. */
 int ag_moe_plan_tile_rows(const ag_moe_plan *plan, int64_t rows, int input_gradient);
 /* Waits for the plan's runs (for the device, if some left no event).  AG_GEMM_OK;
