@@ -25,7 +25,8 @@
 //   warps 2-17  epilogue: TMEM lane quadrant warp % 4, a quarter of the tile's columns
 //   warp 18     weight gradient: zeros over the rows behind a group's end;
 //               e4m3: the scales of each k-block into shared memory
-//               e2m1: the rows' scales into shared memory, as the tensor core takes them
+//               e2m1: the rows' scales into shared memory, as the tensor core takes them;
+//   warp 19     e2m1: passes them on
 //
 // Work: tiles in expert order, and inside an expert in groups of 8 row tiles by all
 // wide tiles, so that the tiles in flight share operands in L2.  Unit u of pair p is
@@ -48,8 +49,8 @@
 // rows by 4 scales, 512 bytes, that tcgen05.cp brings from shared memory, in order with
 // the MMAs that the same thread issues.  The weights' pieces lie ready in memory and come
 // by TMA with their codes.  The rows' do not: a group begins at any row, so they are kept
-// as words of four scales, [128 elements of K][row], and a warp puts the tile's words into
-// the pieces' order.  Two accumulators of 224 columns leave TMEM columns for the scales of
+// as words of four scales, [128 elements of K][row], and a warp copies the tile's words
+// into the pieces' order.  Two accumulators of 224 columns leave TMEM columns for the scales of
 // two k-blocks.
 //
 // Rows beyond a group's end belong to the next group: they are multiplied along and
@@ -188,6 +189,16 @@ __device__ __forceinline__ void cluster_wait() {
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+
+// A word to shared memory (zero without `in`), counted by arrive_copied: that arrival on
+// the barrier takes place once all of this thread's copies so far have landed.
+__device__ __forceinline__ void copy_word(uint32_t to, const uint32_t* from, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void arrive_copied(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // A value that is the same in all lanes, so that the compiler knows it: what it
 // computes from such values stays in uniform registers, where the MMA and TMA
@@ -484,6 +495,7 @@ struct Ring {
   uint64_t* tail;   // weight gradient, by stage: this CTA's part of a group's last k-block
   uint64_t* zfull;  // and, on the even CTA: both CTAs' parts zeroed behind the group's end
                     // (e2m1: by stage, both CTAs' copies of the rows' scales)
+  uint64_t* sraw;   // e2m1, by stage: this CTA's copy of the rows' scales has landed
   uint64_t* sfull;  // e4m3: scales of a k-block, by slot
   uint64_t* sempty; // e4m3: this CTA's epilogue warps are through with them
   float* scales;    // two batches: [k-block][BN], long groups [k-block][column block][128]
@@ -780,70 +792,74 @@ __device__ void scale_long_role(const ExpertsParams& p, const Table& table,
 
 // ------------------------------------------------------------------ scales (e2m1)
 // The tile's rows' scales of each stage, as pieces of 128 rows: row r's word at (r % 32) *
-// 16 + (r / 32) * 4, so that a lane's four words are one store of 16 bytes.  Both CTAs
-// hold those of all rows (each multiplies its half of the columns with all of them).  The
-// next stage's words are on their way while this one's wait for their place.
+// 16 + (r / 32) * 4.  Both CTAs hold those of all rows (each multiplies its half of the
+// columns with all of them).  One warp copies the words to their places, as many stages
+// ahead as the ring has, and another passes on what has landed: a warp that loads and
+// stores them itself waits for a load once a stage (8192 x 4096 x 4096: 95 us so).
 template <int BN>
 __device__ void scale4_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int lane) {
   Schedule<kOpFp4, BN> sch(p, table);
-  constexpr int kStagesX = stages_of(kOpFp4, BN), kWords = 4 * row_pieces(BN);
-  const uint32_t zfull0 = mapa_shared(smem_u32(ring.zfull), 0);
+  constexpr int kStagesX = stages_of(kOpFp4, BN);
   const int32_t KA = (p.red + 127) / 128;
-  Unit u;
-  int32_t i = 0, kb = 0, row0 = 0, cnt = 0, kb_end = 0;
-  // The next stage's words; false behind the last stage.
-  auto next = [&](uint32_t (&v)[kPieces][kWords]) {
-    if (kb >= kb_end) {
-      do {
-        if (!sch.get(i++, u)) return false;
-      } while (u.kb0 >= u.kb1);
-      kb = u.kb0;
-      kb_end = u.kb1;
-      row0 = u.row0 + lane;
-      cnt = u.cnt - lane;
-    }
-    const uint32_t* from = p.xs4 + static_cast<int64_t>(kb) * 2 * p.rows + row0;
-    const int32_t pieces = KA - kb * 2;
-#pragma unroll
-    for (int a = 0; a < kPieces; ++a)
-#pragma unroll
-      for (int j = 0; j < kWords; ++j)
-        v[a][j] = j * 32 < BN && j * 32 < cnt && a < pieces ? from[static_cast<int64_t>(a) * p.rows + j * 32] : 0u;
-    kb += kSub;
-    return true;
-  };
-  uint32_t v[kPieces][kWords];
   int stage = 0;
   uint32_t phase = 0;
-  bool more = next(v), ok = true;
-  while (more) {
-    uint32_t w[kPieces][kWords];
+  bool ok = true;
+  Unit u;
+  for (int32_t i = 0; ok && sch.get(i, u); ++i) {
+    const int32_t words = (u.cnt + 31) / 32;  // (the accumulator's columns behind them are not stored)
+    const uint32_t* const xs = p.xs4 + u.row0 + lane;
+    for (int32_t kb = u.kb0; kb < u.kb1; kb += kSub) {
+      ok = mbar_wait(&ring.empty[stage], phase ^ 1u, p.timeout_ns, ring.abort, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t to = smem_u32(ring.scales) + stage * scale_stage(BN) + kPieces * kPiece + lane * 16;
 #pragma unroll
-    for (int a = 0; a < kPieces; ++a)
+      for (int a = 0; a < kPieces; ++a) {
+        if (kb * 2 + a >= KA) break;  // (no MMA reads the pieces past K)
+        const uint32_t* const from = xs + static_cast<int64_t>(kb * 2 + a) * p.rows;
 #pragma unroll
-      for (int j = 0; j < kWords; ++j) w[a][j] = v[a][j];
-    more = next(v);
-    ok = mbar_wait(&ring.empty[stage], phase ^ 1u, p.timeout_ns, ring.abort, p.status);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    uint8_t* to = reinterpret_cast<uint8_t*>(ring.scales) + stage * scale_stage(BN) + kPieces * kPiece + lane * 16;
-#pragma unroll
-    for (int a = 0; a < kPieces; ++a)
-#pragma unroll
-      for (int r = 0; r < row_pieces(BN); ++r)
-        *reinterpret_cast<uint4*>(to + (a * row_pieces(BN) + r) * kPiece) =
-            make_uint4(w[a][4 * r], w[a][4 * r + 1], w[a][4 * r + 2], w[a][4 * r + 3]);
-    fence_proxy_async_shared();
-    __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(zfull0 + stage * 8);
-    __syncwarp();
-    if (++stage == kStagesX) {
-      stage = 0;
-      phase ^= 1u;
+        for (int j = 0; j < BN / 32; ++j)
+          if (j < words)
+            copy_word(to + (a * row_pieces(BN) + j / 4) * kPiece + j % 4 * 4,
+                      j * 32 + lane < u.cnt ? from + j * 32 : p.xs4, j * 32 + lane < u.cnt);
+      }
+      arrive_copied(&ring.sraw[stage]);
+      if (++stage == kStagesX) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
   }
   if (!ok && lane == 0) {
     set_status(p.status, kStatusPipelineTimeout, 0x500u | rank);
+    *ring.abort = 1;
+  }
+  copies_done();
+}
+
+template <int BN>
+__device__ void pass4_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int lane) {
+  Schedule<kOpFp4, BN> sch(p, table);
+  constexpr int kStagesX = stages_of(kOpFp4, BN);
+  const uint32_t zfull0 = mapa_shared(smem_u32(ring.zfull), 0);
+  int stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  Unit u;
+  for (int32_t i = 0; ok && sch.get(i, u); ++i)
+    for (int32_t kb = u.kb0; kb < u.kb1; kb += kSub) {
+      ok = warp_wait(&ring.sraw[stage], phase, p.timeout_ns, ring.abort, p.status);
+      if (!ok) break;
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(zfull0 + stage * 8);
+      if (++stage == kStagesX) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  if (!ok && lane == 0) {
+    set_status(p.status, kStatusPipelineTimeout, 0x600u | rank);
     *ring.abort = 1;
   }
 }
@@ -1401,7 +1417,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   ring.zfull = ring.tail + kStagesX;
   ring.sfull = ring.zfull + kStagesX;
   ring.sempty = ring.sfull + 2;
-  uint64_t* drain = ring.sempty + 2;
+  ring.sraw = ring.sempty + 2;
+  uint64_t* drain = ring.sraw + kStagesX;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   ring.abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* flag = reinterpret_cast<int32_t*>(tmem_slot + 2);
@@ -1417,6 +1434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       mbar_init(&ring.empty[s], 1);
       mbar_init(&ring.tail[s], 1);
       mbar_init(&ring.zfull[s], 2);
+      mbar_init(&ring.sraw[s], 32);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ring.tfull[b], 1);
@@ -1462,7 +1480,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     } else if constexpr (OP == kOpFp8Long) {
       scale_long_role<BN>(p, table, ring, rank, lane);
     } else if constexpr (OP == kOpFp4) {
-      scale4_role<BN>(p, table, ring, rank, lane);
+      if (warp == 2 + kXEpiWarps)
+        scale4_role<BN>(p, table, ring, rank, lane);
+      else
+        pass4_role<BN>(p, table, ring, rank, lane);
     }
   } else if (threadIdx.x == 0) {
     set_status(p.status + 2, kStatusOffsets, 0);
