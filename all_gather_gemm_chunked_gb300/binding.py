@@ -73,7 +73,7 @@ def _load():
     if not os.path.exists(path):
         raise ImportError(f"libaggemm.so is not built ({path}); run __graft_entry__.build()")
     lib = ctypes.CDLL(path)
-    i32, i64, vp = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p
+    i32, i64, vp, f32 = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
     geo_p = ctypes.POINTER(Geometry)
     i64_arr = ctypes.POINTER(ctypes.c_int64)
     sig = {
@@ -127,6 +127,13 @@ def _load():
         "ag_fp4_quantize_rows": (i32, [i64, i64, i32, vp, i64, i64, vp, i32, vp, vp, vp]),
         "ag_fp4_quantize_weights": (i32, [i32, i64, i64, i32, vp, vp, vp, vp]),
         "ag_fp4_forward": (i32, [vp, i64, vp, vp, vp, vp, vp, vp, i64, i32, vp]),
+        "ag_norm_rms": (i32, [i64, i64, i32, vp, i64, vp, i64, vp, i32, f32, vp, vp, vp, vp]),
+        "ag_norm_rms_quantized": (i32, [i64, i64, i32, vp, i64, vp, i64, vp, i32, f32, i32, vp, vp, vp, vp]),
+        "ag_norm_rms_backward_workspace": (i64, [i64, i64]),
+        "ag_norm_rms_backward": (i32, [i64, i64, i32, vp, i64, vp, i64, vp, i32, vp, vp, i64, vp, vp, vp, vp]),
+        "ag_act_swiglu": (i32, [i64, i64, i32, vp, i64, vp, vp]),
+        "ag_act_swiglu_quantized": (i32, [i64, i64, i32, vp, i64, i32, vp, vp, vp]),
+        "ag_act_swiglu_backward": (i32, [i64, i64, i32, vp, i64, vp, i64, vp, vp]),
         "ag_gemm_last_error": (i32, []),
         "ag_gemm_last_error_message": (ctypes.c_char_p, []),
     }
@@ -354,6 +361,13 @@ ag_fp8_forward = _wrapped("ag_fp8_forward")
 ag_fp4_quantize_rows = _wrapped("ag_fp4_quantize_rows")
 ag_fp4_quantize_weights = _wrapped("ag_fp4_quantize_weights")
 ag_fp4_forward = _wrapped("ag_fp4_forward")
+ag_norm_rms = _wrapped("ag_norm_rms")
+ag_norm_rms_quantized = _wrapped("ag_norm_rms_quantized")
+ag_norm_rms_backward_workspace = _wrapped("ag_norm_rms_backward_workspace")
+ag_norm_rms_backward = _wrapped("ag_norm_rms_backward")
+ag_act_swiglu = _wrapped("ag_act_swiglu")
+ag_act_swiglu_quantized = _wrapped("ag_act_swiglu_quantized")
+ag_act_swiglu_backward = _wrapped("ag_act_swiglu_backward")
 
 
 def ag_moe_plan_create(E: int, K: int, N: int, dtype: int) -> int:

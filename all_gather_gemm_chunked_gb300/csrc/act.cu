@@ -1,0 +1,156 @@
+// act.cu -- gated activation: y = g s u with s = 1 / (1 + exp(-g)), for rows that hold the
+// gate g and the other factor u side by side, and its gradient
+//
+//   dg = dy u s (1 + g (1 - s)),   du = dy g s
+//
+// Bound by memory: every element is read once, in 16-byte accesses where rows are aligned,
+// with all of a thread's loads in flight before the first is used.  A team of 2^log
+// threads takes 2^log * P pieces of a row.
+
+#include "layer_rows.cuh"
+
+namespace agg {
+
+namespace {
+constexpr int kThreads = 256;
+
+// s and 1 - s from exp(-|g|), which does not overflow: far negative gates keep their s
+// (exp(-g) passes the largest float from -88.7 on, and 1 / (1 + exp(-g)) would be zero).
+__device__ __forceinline__ void sigmoid(float g, float& s, float& rest) {
+  const float e = expf(-fabsf(g)), r = __frcp_rn(1.0f + e);
+  s = g < 0.0f ? e * r : r;
+  rest = g < 0.0f ? r : e * r;
+}
+
+template <typename T, int V, int P, int OUT>
+__global__ void __launch_bounds__(kThreads) swiglu_kernel(const GateArgs a, int log) {
+  pdl_enter();
+  const int team = 1 << log, thread = threadIdx.x & (team - 1);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads >> log) + (threadIdx.x >> log);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (team * P * V) + thread * V;
+  const bool valid = row < a.rows;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx + c0;
+  Raw<T, V> g[P], u[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    g[i] = u[i] = Raw<T, V>{};
+    if (valid && c0 + i * team * V < a.N) {
+      g[i].load(x + i * team * V);
+      u[i].load(x + i * team * V + a.N);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int64_t c = c0 + i * team * V;
+    const bool in = valid && c < a.N;
+    float f[V], v[V];
+    g[i].get(f);
+    u[i].get(v);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float s, rest;
+      sigmoid(f[j], s, rest);
+      f[j] = f[j] * s * v[j];
+    }
+    if constexpr (OUT == kTypeE4m3 || OUT == kTypeE2m1) {
+      put_codes<OUT, V>(a.out, a.scales, a.rows, a.N, row, c, in, f);
+    } else {
+      if (in) store_elems<T, V>(static_cast<T*>(a.out) + row * a.N + c, f);
+    }
+  }
+}
+
+template <typename T, int V, int P>
+__global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const GateArgs a, int log) {
+  pdl_enter();
+  const int team = 1 << log, thread = threadIdx.x & (team - 1);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads >> log) + (threadIdx.x >> log);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (team * P * V) + thread * V;
+  if (row >= a.rows) return;
+  const T *x = static_cast<const T*>(a.x) + row * a.ldx + c0, *dy = static_cast<const T*>(a.dy) + row * a.lddy + c0;
+  T* dx = static_cast<T*>(a.out) + row * 2 * a.N + c0;
+  Raw<T, V> g[P], u[P], d[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (c0 + i * team * V < a.N) {
+      g[i].load(x + i * team * V);
+      u[i].load(x + i * team * V + a.N);
+      d[i].load(dy + i * team * V);
+    }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    if (c0 + i * team * V >= a.N) break;
+    float f[V], v[V], e[V];
+    g[i].get(f);
+    u[i].get(v);
+    d[i].get(e);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float s, rest;
+      sigmoid(f[j], s, rest);
+      const float es = e[j] * s;
+      v[j] = es * v[j] * fmaf(f[j], rest, 1.0f);
+      e[j] = es * f[j];
+    }
+    store_elems<T, V>(dx + i * team * V, v);
+    store_elems<T, V>(dx + i * team * V + a.N, e);
+  }
+}
+
+// A team's log, and the grid: rows, and pieces of them.
+struct Shape {
+  int log;
+  dim3 grid;
+};
+Shape shape_of(int64_t rows, int64_t N, int V, int P) {
+  const int64_t pieces = (N + V - 1) / V;
+  int log = 5;
+  while (log < 8 && (P << log) < pieces) ++log;
+  const int64_t per = kThreads >> log, cols = static_cast<int64_t>(P) << log;
+  return {log, dim3(static_cast<unsigned>((rows + per - 1) / per), static_cast<unsigned>((pieces + cols - 1) / cols))};
+}
+
+template <typename F>
+cudaError_t with_type(int dtype, const F& f) {
+  return dtype == kTypeF32 ? f(float{}) : dtype == kTypeF16 ? f(__half{}) : f(__nv_bfloat16{});
+}
+
+template <typename T, int V, int OUT>
+cudaError_t forward(const GateArgs& a, cudaStream_t stream) {
+  constexpr int P = 2;
+  const Shape s = shape_of(a.rows, a.N, V, P);
+  return launch(swiglu_kernel<T, V, P, OUT>, s.grid, kThreads, stream, a, s.log);
+}
+template <typename T, int V>
+cudaError_t backward(const GateArgs& a, cudaStream_t stream) {
+  constexpr int P = 2;
+  const Shape s = shape_of(a.rows, a.N, V, P);
+  return launch(swiglu_backward_kernel<T, V, P>, s.grid, kThreads, stream, a, s.log);
+}
+}  // namespace
+
+cudaError_t launch_swiglu(const GateArgs& a, int dtype, int out_type, cudaStream_t stream) {
+  if (a.rows == 0) return cudaSuccess;
+  const int size = dtype == kTypeF32 ? 4 : 2;
+  const bool vec = vectors(a.x, a.ldx, size) && a.N * size % 16 == 0 && vectors(a.out, 0, 1);
+  return with_type(dtype, [&](auto t) {
+    using T = decltype(t);
+    constexpr int V = Elem<T>::kVec;
+    if (out_type == kTypeE4m3) return forward<T, V, kTypeE4m3>(a, stream);
+    if (out_type == kTypeE2m1) return forward<T, V, kTypeE2m1>(a, stream);
+    return vec ? forward<T, V, kTypeF32>(a, stream) : forward<T, 1, kTypeF32>(a, stream);
+  });
+}
+
+cudaError_t launch_swiglu_backward(const GateArgs& a, int dtype, cudaStream_t stream) {
+  if (a.rows == 0) return cudaSuccess;
+  const int size = dtype == kTypeF32 ? 4 : 2;
+  const bool vec = vectors(a.x, a.ldx, size) && vectors(a.dy, a.lddy, size) && a.N * size % 16 == 0 &&
+                   vectors(a.out, 0, 1);
+  return with_type(dtype, [&](auto t) {
+    using T = decltype(t);
+    return vec ? backward<T, Elem<T>::kVec>(a, stream) : backward<T, 1>(a, stream);
+  });
+}
+
+}  // namespace agg

@@ -10,10 +10,6 @@
 namespace agg {
 
 namespace {
-__device__ __forceinline__ float block_scale(float amax) {
-  return fmaxf(__fdiv_rn(amax, 448.0f), 1.17549435e-38f);
-}
-
 // Bound by memory (2 bytes in, 1 out per element).  A warp takes 256 elements of
 // a row per step, 8 per lane: 16 lanes make one scale block, whose maximum takes
 // four shuffles.  All of a lane's loads are issued before the first use.  The

@@ -1,5 +1,5 @@
 // front.cpp -- native part of the torch front end of include/ag_moe.h and ag_layer.h
-// (moe.py, fp8.py, fp4.py):
+// (moe.py, fp8.py, fp4.py, norm.py, act.py):
 // checks tensors, allocates outputs, takes the current stream and calls the library.
 // A call's host time decides how long a small operator takes: in Python the checks,
 // the allocation and the foreign call took 10 to 18 us a call, longer than the kernels.
@@ -571,6 +571,171 @@ PyObject* fp4_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   AGG_END
 }
 
+// Codes and scales of rows x n elements, in one allocation.
+struct Codes {
+  at::Tensor q, s;
+  Codes(int code, int64_t rows, int64_t n, const at::Tensor& like) {
+    const bool e4m3 = code == AG_MOE_E4M3;
+    const int64_t bytes = e4m3 ? n : n / 2;
+    Pieces pieces(Pieces::room(rows * bytes) + Pieces::room(blocks(n) * rows * 4), like);
+    q = pieces.take({rows, bytes}, e4m3 ? kE4m3 : kByte);
+    s = e4m3 ? pieces.take({blocks(n), rows}, kF32) : pieces.take({blocks(n), rows, 4}, kE8m0);
+  }
+};
+
+// What both forms of the norm read: (x, weight, eps, residual or None).
+struct NormInputs {
+  const at::Tensor& x;
+  int type, weight_type;
+  int64_t ld, rows, H;
+  const void* weight;
+  float eps;
+  const at::Tensor* residual = nullptr;
+  const void* res = nullptr;
+  int64_t ldr = 0;
+  explicit NormInputs(PyObject* const* a)
+      : x(tensor(a[0], "x")), type(float_type(x, "x")), ld(pitch(x, "x")), rows(x.size(0)), H(x.size(1)) {
+    weight = weight_of(a[1], x, H, weight_type);
+    const double e = PyFloat_AsDouble(a[2]);
+    if (e == -1.0 && PyErr_Occurred()) throw Raised();
+    eps = static_cast<float>(e);
+    if (a[3] != Py_None) {
+      residual = &tensor(a[3], "residual", x);
+      want_type(*residual, "residual", x.scalar_type());
+      want_shape(*residual, "residual", {rows, H});
+      ldr = pitch(*residual, "residual");
+      res = residual->data_ptr();
+    }
+  }
+  static const void* weight_of(PyObject* o, const at::Tensor& x, int64_t H, int& type) {
+    const at::Tensor& w = tensor(o, "weight", x);
+    if (w.scalar_type() != x.scalar_type()) want_type(w, "weight", kF32);
+    type = type_code(w.scalar_type());
+    return plain(o, "weight", w.scalar_type(), {H}, x);
+  }
+};
+
+// rms_norm(x, weight, eps, residual or None) -> y, h, rstd
+PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  AGG_BEGIN
+  check_args(n, 4);
+  const NormInputs in(a);
+  const Current current(in.x);
+  const at::ScalarType t = in.x.scalar_type();
+  const int64_t bytes = in.rows * in.H * static_cast<int64_t>(c10::elementSize(t));
+  // (y apart where it is large: a residual stream that is kept would keep its memory too)
+  const bool apart = bytes > (int64_t{1} << 20);
+  Pieces pieces((apart ? 0 : Pieces::room(bytes)) + (in.residual ? Pieces::room(bytes) : 0) + Pieces::room(in.rows * 4),
+                in.x);
+  at::Tensor y = apart ? make({in.rows, in.H}, t, in.x) : pieces.take({in.rows, in.H}, t),
+             h = in.residual ? pieces.take({in.rows, in.H}, t) : in.x, rstd = pieces.take({in.rows}, kF32);
+  check_rc(ag_norm_rms(in.rows, in.H, in.type, in.x.data_ptr(), in.ld, in.res, in.ldr, in.weight, in.weight_type, in.eps,
+                       y.data_ptr(), in.residual ? h.data_ptr() : nullptr, static_cast<float*>(rstd.data_ptr()),
+                       stream_of(in.x)));
+  return tuple_of(y, h, rstd);
+  AGG_END
+}
+
+// rms_norm_quantized(x, weight, eps, residual or None, code type) -> codes, scales, h
+PyObject* rms_norm_quantized(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  AGG_BEGIN
+  check_args(n, 5);
+  const NormInputs in(a);
+  const int code = to_int32(a[4], "code type");
+  const Current current(in.x);
+  Codes c(code, in.rows, in.H, in.x);
+  at::Tensor h = in.residual ? make({in.rows, in.H}, in.x.scalar_type(), in.x) : in.x;
+  check_rc(ag_norm_rms_quantized(in.rows, in.H, in.type, in.x.data_ptr(), in.ld, in.res, in.ldr, in.weight,
+                                 in.weight_type, in.eps, code, c.q.data_ptr(), c.s.data_ptr(),
+                                 in.residual ? h.data_ptr() : nullptr, stream_of(in.x)));
+  return tuple_of(c.q, c.s, h);
+  AGG_END
+}
+
+// rms_norm_backward(dy, h, weight, rstd, dh or None) -> dx, dweight
+PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  AGG_BEGIN
+  check_args(n, 5);
+  const at::Tensor &dy = tensor(a[0], "dy"), &h = tensor(a[1], "h", dy);
+  const int type = float_type(dy, "dy");
+  const int64_t lddy = pitch(dy, "dy"), rows = dy.size(0), H = dy.size(1);
+  want_type(h, "h", dy.scalar_type());
+  want_shape(h, "h", {rows, H});
+  const int64_t ldh = pitch(h, "h");
+  int weight_type;
+  const void* w = NormInputs::weight_of(a[2], dy, H, weight_type);
+  const float* rstd = plain<float>(a[3], "rstd", kF32, {rows}, dy);
+  const void* dh = nullptr;
+  int64_t lddh = 0;
+  if (a[4] != Py_None) {
+    const at::Tensor& t = tensor(a[4], "dh", dy);
+    want_type(t, "dh", dy.scalar_type());
+    want_shape(t, "dh", {rows, H});
+    lddh = pitch(t, "dh");
+    dh = t.data_ptr();
+  }
+  const int64_t size = check_rc(ag_norm_rms_backward_workspace(rows, H));
+  const Current current(dy);
+  at::Tensor dx = make({rows, H}, dy.scalar_type(), dy), dw = make({H}, kF32, dy), ws = make({size}, kByte, dy);
+  check_rc(ag_norm_rms_backward(rows, H, type, dy.data_ptr(), lddy, h.data_ptr(), ldh, w, weight_type, rstd, dh, lddh,
+                                dx.data_ptr(), static_cast<float*>(dw.data_ptr()), ws.data_ptr(), stream_of(dy)));
+  return tuple_of(dx, dw);
+  AGG_END
+}
+
+// A row's two halves.
+int64_t half_of(const at::Tensor& x) {
+  if (x.size(1) % 2 != 0 || x.size(1) == 0)
+    raise(PyExc_ValueError, "x must have an even number of columns, got %s", shape_of(x.sizes()).c_str());
+  return x.size(1) / 2;
+}
+
+// swiglu(x) -> y
+PyObject* swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  AGG_BEGIN
+  check_args(n, 1);
+  const at::Tensor& x = tensor(a[0], "x");
+  const int type = float_type(x, "x");
+  const int64_t ld = pitch(x, "x"), N = half_of(x);
+  const Current current(x);
+  at::Tensor y = make({x.size(0), N}, x.scalar_type(), x);
+  check_rc(ag_act_swiglu(x.size(0), N, type, x.data_ptr(), ld, y.data_ptr(), stream_of(x)));
+  return wrap(y);
+  AGG_END
+}
+
+// swiglu_quantized(x, code type) -> codes, scales
+PyObject* swiglu_quantized(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  AGG_BEGIN
+  check_args(n, 2);
+  const at::Tensor& x = tensor(a[0], "x");
+  const int type = float_type(x, "x"), code = to_int32(a[1], "code type");
+  const int64_t ld = pitch(x, "x"), N = half_of(x);
+  const Current current(x);
+  Codes c(code, x.size(0), N, x);
+  check_rc(ag_act_swiglu_quantized(x.size(0), N, type, x.data_ptr(), ld, code, c.q.data_ptr(), c.s.data_ptr(),
+                                   stream_of(x)));
+  return tuple_of(c.q, c.s);
+  AGG_END
+}
+
+// swiglu_backward(dy, x) -> dx
+PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  AGG_BEGIN
+  check_args(n, 2);
+  const at::Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x", dy);
+  const int type = float_type(x, "x");
+  const int64_t ld = pitch(x, "x"), N = half_of(x), rows = x.size(0);
+  want_type(dy, "dy", x.scalar_type());
+  want_shape(dy, "dy", {rows, N});
+  const int64_t lddy = pitch(dy, "dy");
+  const Current current(x);
+  at::Tensor dx = make({rows, 2 * N}, x.scalar_type(), x);
+  check_rc(ag_act_swiglu_backward(rows, N, type, dy.data_ptr(), lddy, x.data_ptr(), ld, dx.data_ptr(), stream_of(x)));
+  return wrap(dx);
+  AGG_END
+}
+
 #define AGG_METHOD(f) \
   { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {AGG_METHOD(init),         AGG_METHOD(route),         AGG_METHOD(route_backward),
@@ -578,6 +743,8 @@ PyMethodDef methods[] = {AGG_METHOD(init),         AGG_METHOD(route),         AG
                          AGG_METHOD(quantize_rows), AGG_METHOD(quantize_weights), AGG_METHOD(rows_product),
                          AGG_METHOD(weight_product), AGG_METHOD(fp8_product),
                          AGG_METHOD(fp4_quantize_rows), AGG_METHOD(fp4_quantize_weights), AGG_METHOD(fp4_product),
+                         AGG_METHOD(rms_norm), AGG_METHOD(rms_norm_quantized), AGG_METHOD(rms_norm_backward),
+                         AGG_METHOD(swiglu), AGG_METHOD(swiglu_quantized), AGG_METHOD(swiglu_backward),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_front", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,139 @@
+// layer_rows.cuh -- launchers of the norm (norm.cu) and of the gated activation (act.cu),
+// and what their kernels share: a row's threads, and outputs as codes with scales.
+// Arguments as in ag_layer.h, checked by the caller.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fp4_codes.cuh"
+#include "moe_rows.cuh"
+#include "moe_types.cuh"
+
+namespace agg {
+
+struct NormArgs {
+  int64_t rows, H;
+  const void* x;
+  int64_t ldx;
+  const void* residual;  // or null
+  int64_t ldr;
+  const void* weight;
+  int weight_f32;        // weights are floats (otherwise the rows' type)
+  float eps;
+  void* out;             // y, or codes
+  void* scales;          // of the codes
+  void* h;               // with a residual
+  float* rstd;           // or null
+};
+// out_type: dtype itself, kTypeE4m3 or kTypeE2m1.
+cudaError_t launch_norm(const NormArgs& a, int dtype, int out_type, cudaStream_t stream);
+
+struct NormBackwardArgs {
+  int64_t rows, H;
+  const void* dy;
+  int64_t lddy;
+  const void* h;
+  int64_t ldh;
+  const void* weight;
+  int weight_f32;
+  const float* rstd;
+  const void* dh;  // or null
+  int64_t lddh;
+  void* dx;
+  float* dweight;
+  float* parts;    // [norm_parts][H]
+};
+// Sums of the weight's gradient that are made first and then added.
+int64_t norm_parts(int64_t rows, int64_t H);
+cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, cudaStream_t stream);
+
+struct GateArgs {
+  int64_t rows, N;
+  const void* x;   // gate, and N columns on the other factor
+  int64_t ldx;
+  const void* dy;  // backward
+  int64_t lddy;
+  void* out;       // y, codes, or the gradient of x
+  void* scales;
+};
+cudaError_t launch_swiglu(const GateArgs& a, int dtype, int out_type, cudaStream_t stream);
+cudaError_t launch_swiglu_backward(const GateArgs& a, int dtype, cudaStream_t stream);
+
+#ifdef __CUDACC__
+// V neighbouring elements of a row as codes, by the lanes of a whole warp, which hold V
+// elements each, the next lane the next V; past the row (`in` false) they are zeros.  The
+// same codes and scales as quantising the floats.
+template <int OUT, int V>
+__device__ __forceinline__ void put_codes(void* codes, void* scales, int64_t rows, int64_t H, int64_t row, int64_t c,
+                                          bool in, float (&f)[V]) {
+  static_assert(V == 8 || V == 4, "16 bytes of the rows' type");
+  const int lane = threadIdx.x & 31;
+  constexpr int kLanes = kScaleBlock / V;  // of 128 elements
+  if constexpr (OUT == kTypeE4m3) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) amax = fmaxf(amax, fabsf(f[v]));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float s = block_scale(amax), inv = __frcp_rn(s);
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int b = 0; b < V / 4; ++b)
+      w[b] = e4m3x2(__fmul_rn(f[4 * b], inv), __fmul_rn(f[4 * b + 1], inv)) |
+             (e4m3x2(__fmul_rn(f[4 * b + 2], inv), __fmul_rn(f[4 * b + 3], inv)) << 16);
+    if (!in) return;
+    uint8_t* q = static_cast<uint8_t*>(codes) + row * H + c;
+    if constexpr (V == 8)
+      *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(q) = w[0];
+    if ((lane & (kLanes - 1)) == 0) static_cast<float*>(scales)[(c / kScaleBlock) * rows + row] = s;
+  } else {
+    uint32_t largest = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) largest = max(largest, magnitude_bits(f[v]));
+#pragma unroll
+    for (int o = kMicroBlock / V / 2; o > 0; o >>= 1)
+      largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+    const uint32_t s = micro_scale(largest);
+    const float inv = micro_inverse(s);
+    float g[8] = {};
+#pragma unroll
+    for (int v = 0; v < V; ++v) g[v] = f[v] * inv;
+    const uint32_t code = e2m1x8(g);
+    uint32_t word = s << ((lane / (kMicroBlock / V) & 3) * 8);
+#pragma unroll
+    for (int o = kMicroBlock / V; o < kLanes; o <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+    if (!in) return;
+    uint8_t* q = static_cast<uint8_t*>(codes) + (row * H + c) / 2;
+    if constexpr (V == 8)
+      *reinterpret_cast<uint32_t*>(q) = code;
+    else
+      *reinterpret_cast<uint16_t*>(q) = static_cast<uint16_t>(code);
+    if ((lane & (kLanes - 1)) == 0) static_cast<uint32_t*>(scales)[(c / kScaleBlock) * rows + row] = word;
+  }
+}
+
+// The sum over a team's threads (a power of two of them, 32 or more; `part` has a float
+// for each warp of the block), the same in every thread and every call.
+__device__ __forceinline__ float team_sum(float v, int team_warps, float* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (team_warps == 1) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) part[warp] = v;
+  __syncthreads();
+  v = lane < team_warps ? part[(warp & ~(team_warps - 1)) + lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+#endif
+
+// 16-byte accesses: base and row pitch are multiples of 16 bytes.
+inline bool vectors(const void* p, int64_t ld, int size) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * size % 16 == 0;
+}
+
+}  // namespace agg

@@ -117,6 +117,10 @@ struct Raw<T, 1> {
   __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = Elem<T>::get(u); }
 };
 
+// Scale of an e4m3 block.
+__device__ __forceinline__ float block_scale(float amax) {
+  return fmaxf(__fdiv_rn(amax, 448.0f), 1.17549435e-38f);
+}
 // Two floats to e4m3 codes (nearest, ties to even, clipped to +-448; NaN stays
 // NaN), lo in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {

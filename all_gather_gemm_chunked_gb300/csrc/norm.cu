@@ -1,0 +1,461 @@
+// norm.cu -- root-mean-square norm with the residual's addition, and its gradient.
+//
+//   h = x + residual (rounded to the rows' type: that is the residual stream),
+//   rstd = 1 / sqrt(mean(h^2) + eps),  y = h rstd w
+//
+// The norm is that of the rounded h: the backward pass, which starts from the stored h,
+// is then the gradient of what ran forward.  With g = dy w and xh = h rstd,
+//
+//   dx = rstd (g - xh mean(g xh)) + dh   (of x and of the residual),  dw = sum over rows of dy xh
+//
+// Bound by memory: each row is read once and held in registers (as it was loaded: in half
+// of its floats' registers) while its sum goes through the team of threads that shares it;
+// sums and everything between the loads and the stores are floats.  y is rounded once, to
+// the rows' type or to codes (put_codes).
+
+#include "layer_rows.cuh"
+
+namespace agg {
+
+namespace {
+// V weights, as they are loaded; floats or the rows' type.
+template <typename W, int V>
+struct Weights {
+  static constexpr int kN = V == 1 ? 1 : V / Elem<W>::kVec, kV = V == 1 ? 1 : Elem<W>::kVec;
+  Raw<W, kV> r[kN];
+  __device__ __forceinline__ void load(const W* p) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) r[i].load(p + i * kV);
+  }
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      float g[kV];
+      r[i].get(g);
+#pragma unroll
+      for (int v = 0; v < kV; ++v) f[i * kV + v] = g[v];
+    }
+  }
+};
+
+// V elements of h, rounded, as they are stored.
+template <typename T, int V>
+__device__ __forceinline__ void add_residual(Raw<T, V>& x, const Raw<T, V>& r) {
+  float a[V], b[V];
+  x.get(a);
+  r.get(b);
+#pragma unroll
+  for (int v = 0; v < V; ++v) a[v] += b[v];
+  if constexpr (V == 1)
+    x.u = Elem<T>::put(a[0]);
+  else
+    x.u = Elem<T>::pack(a);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_raw(T* p, const Raw<T, V>& r) {
+  if constexpr (V == 1)
+    *p = r.u;
+  else
+    *reinterpret_cast<uint4*>(p) = r.u;
+}
+template <typename T, int V>
+__device__ __forceinline__ float squares(const Raw<T, V>& r, float scale, float sum) {
+  float f[V];
+  r.get(f);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    f[v] *= scale;
+    sum = fmaf(f[v], f[v], sum);
+  }
+  return sum;
+}
+// rstd of a row from its team's sums of squares; squares(scale) is a thread's sum of those
+// of its elements times scale.  Where elements from 10^18 on make the sum pass the largest
+// float, it is made anew of elements times 2^-80 (all threads of the block or, with teams of
+// one warp, of the warp take that way together).
+template <typename F>
+__device__ __forceinline__ float team_rstd(const NormArgs& a, int team_warps, float (*part)[32], const F& squares) {
+  constexpr float kSmall = 0x1p-80f, kLarge = 1e37f;  // (32 warps' sums up to that are finite)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = warp & ~(team_warps - 1);
+  auto over_warp = [](float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  float sum = over_warp(squares(1.0f));
+  bool large = !(sum <= kLarge);
+  if (team_warps > 1) {
+    if (lane == 0) part[0][warp] = sum;
+    large = __syncthreads_or(large);
+    sum = over_warp(lane < team_warps ? part[0][first + lane] : 0.0f);
+  }
+  float scale = 1.0f, eps = a.eps;
+  if (large) {
+    float s = over_warp(squares(kSmall));
+    if (team_warps > 1) {
+      if (lane == 0) part[1][warp] = s;
+      __syncthreads();
+      s = over_warp(lane < team_warps ? part[1][first + lane] : 0.0f);
+    }
+    if (!(sum <= kLarge)) {
+      sum = s;
+      scale = kSmall;
+      eps = 0.0f;  // (eps 2^-160)
+    }
+  }
+  return scale * __frcp_rn(__fsqrt_rn(__fdiv_rn(sum, static_cast<float>(a.H)) + eps));
+}
+
+template <int OUT, typename T, int V>
+__device__ __forceinline__ void put_row(const NormArgs& a, int64_t row, int64_t c, bool in, const Raw<T, V>& h, float rstd,
+                                        const float (&w)[V]) {
+  float f[V];
+  h.get(f);
+#pragma unroll
+  for (int v = 0; v < V; ++v) f[v] = in ? f[v] * rstd * w[v] : 0.0f;
+  if constexpr (OUT == kTypeE4m3 || OUT == kTypeE2m1) {
+    put_codes<OUT, V>(a.out, a.scales, a.rows, a.H, row, c, in, f);
+  } else {
+    if (in) store_elems<T, V>(static_cast<T*>(a.out) + row * a.H + c, f);
+  }
+}
+
+// A team of 2^log threads has a row, P pieces of V elements a thread.
+template <typename T, typename W, int V, int P, int OUT>
+__global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int log) {
+  pdl_enter();
+  __shared__ float part[2][32];
+  const int team = 1 << log, thread = threadIdx.x & (team - 1);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> log) + (threadIdx.x >> log);
+  const bool valid = row < a.rows;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* res = static_cast<const T*>(a.residual) + row * a.ldr;
+  Raw<T, V> h[P], r[P];
+  Weights<W, V> w[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int64_t c = static_cast<int64_t>(i * team + thread) * V;
+    h[i] = r[i] = Raw<T, V>{};
+    w[i] = Weights<W, V>{};
+    if (valid && c < a.H) {
+      h[i].load(x + c);
+      if (a.residual) r[i].load(res + c);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int64_t c = static_cast<int64_t>(i * team + thread) * V;
+    if (valid && c < a.H) w[i].load(static_cast<const W*>(a.weight) + c);
+  }
+  if (a.residual)
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int64_t c = static_cast<int64_t>(i * team + thread) * V;
+      add_residual(h[i], r[i]);
+      if (valid && c < a.H) store_raw(static_cast<T*>(a.h) + row * a.H + c, h[i]);
+    }
+  const float rstd = team_rstd(a, team >> 5, part, [&](float scale) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) sum = squares(h[i], scale, sum);
+    return sum;
+  });
+  if (a.rstd && thread == 0 && valid) a.rstd[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int64_t c = static_cast<int64_t>(i * team + thread) * V;
+    float f[V];
+    w[i].get(f);
+    put_row<OUT>(a, row, c, valid && c < a.H, h[i], rstd, f);
+  }
+}
+
+// A block has a row of any length, which it reads twice.
+template <typename T, typename W, int V, int OUT>
+__global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
+  pdl_enter();
+  __shared__ float part[2][32];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  T* h = static_cast<T*>(a.h) + row * a.H;
+  const float rstd = team_rstd(a, 32, part, [&](float scale) {
+    float sum = 0.0f;
+    for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < a.H; c += 1024 * V) {
+      Raw<T, V> v, r;
+      v.load(x + c);
+      if (a.residual) {
+        r.load(static_cast<const T*>(a.residual) + row * a.ldr + c);
+        add_residual(v, r);
+        store_raw(h + c, v);
+      }
+      sum = squares(v, scale, sum);
+    }
+    return sum;
+  });
+  if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+  const T* from = a.residual ? h : x;  // (each thread reads what it wrote itself)
+  const int64_t end = (a.H + 1024 * V - 1) / (1024 * V) * (1024 * V);  // (the lanes of a warp stay together)
+  for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < end; c += 1024 * V) {
+    const bool in = c < a.H;
+    Raw<T, V> v{};
+    Weights<W, V> w{};
+    float f[V];
+    if (in) {
+      v.load(from + c);
+      w.load(static_cast<const W*>(a.weight) + c);
+    }
+    w.get(f);
+    put_row<OUT>(a, row, c, in, v, rstd, f);
+  }
+}
+
+// ------------------------------------------------------------------ gradient
+constexpr int kSms = 152;
+
+// Rows whose pieces fit a team of up to 1024 threads, one a thread.  A thread keeps its
+// columns from row to row, and their share of the weight's gradient in registers; a block
+// adds its teams' and stores one part.  The next row's loads are under way while this
+// one's sum goes through the team.
+template <typename T, typename W, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 2) norm_backward_kernel(const NormBackwardArgs a, int log) {
+  pdl_enter();
+  constexpr int V = Elem<T>::kVec;
+  __shared__ float part[2][32];
+  __shared__ float sums[THREADS == 1024 ? 1 : THREADS * V];
+  const int team = 1 << log, thread = threadIdx.x & (team - 1), teams = THREADS >> log;
+  const int64_t c = static_cast<int64_t>(thread) * V, step = static_cast<int64_t>(gridDim.x) * teams;
+  const bool in = c < a.H;
+  const T *dy = static_cast<const T*>(a.dy) + c, *h = static_cast<const T*>(a.h) + c,
+          *dh = static_cast<const T*>(a.dh) + c;
+  float w[V], dw[V] = {};
+  {
+    Weights<W, V> r{};
+    if (in) r.load(static_cast<const W*>(a.weight) + c);
+    r.get(w);
+  }
+  const float inv = 1.0f / static_cast<float>(a.H);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * teams;
+  int64_t row = first + (threadIdx.x >> log);
+  Raw<T, V> rg{}, rh{}, rd{};
+  float rstd = 0.0f;
+  auto load = [&] {
+    if (row < a.rows) {
+      rstd = a.rstd[row];
+      if (in) {
+        rg.load(dy + row * a.lddy);
+        rh.load(h + row * a.ldh);
+        if (a.dh) rd.load(dh + row * a.lddh);
+      }
+    }
+  };
+  load();
+  int turn = 0;
+  for (int64_t base = first; base < a.rows; base += step, turn ^= 1) {  // (all teams: they share a barrier)
+    float g[V], x[V], d[V];
+    rg.get(g);
+    rh.get(x);
+    rd.get(d);
+    const float rs = rstd;
+    const int64_t at = row;
+    row += step;
+    load();
+    float dot = 0.0f;
+    const bool valid = at < a.rows;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x[v] *= rs;
+      if (valid) dw[v] = fmaf(g[v], x[v], dw[v]);
+      g[v] *= w[v];
+      dot = fmaf(g[v], x[v], dot);
+    }
+    dot = team_sum(dot, team >> 5, part[turn]) * inv;
+    if (valid && in) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) g[v] = fmaf(rs, fmaf(-x[v], dot, g[v]), a.dh ? d[v] : 0.0f);
+      store_elems<T, V>(static_cast<T*>(a.dx) + at * a.H + c, g);
+    }
+  }
+  float* to = a.parts + static_cast<int64_t>(blockIdx.x) * a.H;
+  if constexpr (THREADS != 1024) {
+    if (teams > 1) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) sums[threadIdx.x * V + v] = dw[v];
+      __syncthreads();
+      for (int i = threadIdx.x; i < a.H; i += THREADS) {
+        float s = 0.0f;
+        for (int t = 0; t < teams; ++t) s += sums[t * team * V + i];
+        to[i] = s;
+      }
+      return;
+    }
+  }
+  if (in)
+#pragma unroll
+    for (int v = 0; v < V; v += 4) *reinterpret_cast<float4*>(to + c + v) = make_float4(dw[v], dw[v + 1], dw[v + 2], dw[v + 3]);
+}
+
+// Rows of any length and alignment: a block has a row, which it reads twice ...
+template <typename T, typename W, int V>
+__global__ void __launch_bounds__(512) norm_backward_long_kernel(const NormBackwardArgs a) {
+  pdl_enter();
+  __shared__ float part[32];
+  const int64_t row = blockIdx.x;
+  const T *dy = static_cast<const T*>(a.dy) + row * a.lddy, *h = static_cast<const T*>(a.h) + row * a.ldh;
+  const float rs = a.rstd[row];
+  float dot = 0.0f;
+  for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < a.H; c += 512 * V) {
+    Raw<T, V> rg, rh;
+    Weights<W, V> rw;
+    rg.load(dy + c);
+    rh.load(h + c);
+    rw.load(static_cast<const W*>(a.weight) + c);
+    float g[V], x[V], w[V];
+    rg.get(g);
+    rh.get(x);
+    rw.get(w);
+#pragma unroll
+    for (int v = 0; v < V; ++v) dot = fmaf(g[v] * w[v], x[v] * rs, dot);
+  }
+  dot = team_sum(dot, 16, part) / static_cast<float>(a.H);
+  for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < a.H; c += 512 * V) {
+    Raw<T, V> rg, rh, rd{};
+    Weights<W, V> rw;
+    rg.load(dy + c);
+    rh.load(h + c);
+    rw.load(static_cast<const W*>(a.weight) + c);
+    if (a.dh) rd.load(static_cast<const T*>(a.dh) + row * a.lddh + c);
+    float g[V], x[V], w[V], d[V];
+    rg.get(g);
+    rh.get(x);
+    rw.get(w);
+    rd.get(d);
+#pragma unroll
+    for (int v = 0; v < V; ++v) g[v] = fmaf(rs, fmaf(-x[v] * rs, dot, g[v] * w[v]), a.dh ? d[v] : 0.0f);
+    store_elems<T, V>(static_cast<T*>(a.dx) + row * a.H + c, g);
+  }
+}
+// ... and the weight's gradient comes by columns, a thread for each, over a part of the rows.
+constexpr int kColumnThreads = 128;
+template <typename T>
+__global__ void __launch_bounds__(kColumnThreads) norm_columns_kernel(const NormBackwardArgs a, int64_t part_rows) {
+  pdl_enter();
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kColumnThreads + threadIdx.x;
+  if (c >= a.H) return;
+  const int64_t r0 = blockIdx.y * part_rows, r1 = r0 + part_rows < a.rows ? r0 + part_rows : a.rows;
+  const T *dy = static_cast<const T*>(a.dy) + c, *h = static_cast<const T*>(a.h) + c;
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int64_t r = r0; r < r1; ++r)
+    sum = fmaf(Elem<T>::get(dy[r * a.lddy]), Elem<T>::get(h[r * a.ldh]) * a.rstd[r], sum);
+  a.parts[blockIdx.y * a.H + c] = sum;
+}
+
+// The sum of the parts, 32 columns a block: each warp adds every 16th part, then the warps'
+// sums are added in their order.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(32 * kSumWarps) norm_sum_kernel(const float* parts, int64_t n, int64_t H, float* dweight) {
+  pdl_enter();
+  __shared__ float sums[kSumWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float s = 0.0f;
+  if (c < H)
+#pragma unroll 8
+    for (int64_t i = warp; i < n; i += kSumWarps) s += parts[i * H + c];
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < H) {
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSumWarps; ++i) s += sums[i][lane];
+    dweight[c] = s;
+  }
+}
+
+int team_log(int64_t threads) {
+  int log = 5;
+  while ((1LL << log) < threads) ++log;
+  return log;
+}
+
+constexpr int kMaxParts = 2 * kSms;
+
+template <typename F>
+cudaError_t with_types(int dtype, int weight_f32, const F& f) {
+  if (dtype == kTypeF32) return f(float{}, float{});
+  if (dtype == kTypeF16) return weight_f32 ? f(__half{}, float{}) : f(__half{}, __half{});
+  return weight_f32 ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
+}
+int size_of(int dtype) { return dtype == kTypeF32 ? 4 : 2; }
+
+template <typename T, typename W, int V, int OUT>
+cudaError_t launch_norm_v(const NormArgs& a, cudaStream_t stream) {
+  const int64_t pieces = (a.H + V - 1) / V;
+  constexpr int kMost = V == 1 ? 8 : 4;
+  if (pieces > 1024 * kMost)
+    return launch(norm_long_kernel<T, W, V, OUT>, dim3(static_cast<unsigned>(a.rows)), 1024, stream, a);
+  // One piece a thread where rows are few, two where they are many.
+  const int p = pieces > 1024 * (kMost / 2) ? kMost : pieces > 1024 || a.rows > 2 * kSms ? kMost / 2 : 1;
+  const int log = team_log((pieces + p - 1) / p);
+  const int threads = log < 8 ? 256 : 1 << log, per = threads >> log;
+  const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per));
+  if (p == 1) return launch(norm_kernel<T, W, V, 1, OUT>, grid, threads, stream, a, log);
+  if (p == kMost / 2) return launch(norm_kernel<T, W, V, kMost / 2, OUT>, grid, threads, stream, a, log);
+  return launch(norm_kernel<T, W, V, kMost, OUT>, grid, threads, stream, a, log);
+}
+
+template <typename T, typename W, int V>
+cudaError_t launch_backward_long(const NormBackwardArgs& a, int64_t parts, cudaStream_t stream) {
+  cudaError_t e = launch(norm_backward_long_kernel<T, W, V>, dim3(static_cast<unsigned>(a.rows)), 512, stream, a);
+  if (e != cudaSuccess) return e;
+  const int64_t part_rows = (a.rows + parts - 1) / parts;
+  const dim3 grid(static_cast<unsigned>((a.H + kColumnThreads - 1) / kColumnThreads), static_cast<unsigned>(parts));
+  return launch(norm_columns_kernel<T>, grid, kColumnThreads, stream, a, part_rows);
+}
+}  // namespace
+
+cudaError_t launch_norm(const NormArgs& a, int dtype, int out_type, cudaStream_t stream) {
+  if (a.rows == 0) return cudaSuccess;
+  const int size = size_of(dtype);
+  const bool vec = vectors(a.x, a.ldx, size) && vectors(a.weight, 0, 1) && a.H * size % 16 == 0 &&
+                   (!a.residual || (vectors(a.residual, a.ldr, size) && vectors(a.h, a.H, size))) &&
+                   (out_type != dtype || vectors(a.out, a.H, size));
+  return with_types(dtype, a.weight_f32, [&](auto t, auto w) {
+    using T = decltype(t);
+    using W = decltype(w);
+    constexpr int V = Elem<T>::kVec;
+    if (out_type == kTypeE4m3) return launch_norm_v<T, W, V, kTypeE4m3>(a, stream);
+    if (out_type == kTypeE2m1) return launch_norm_v<T, W, V, kTypeE2m1>(a, stream);
+    return vec ? launch_norm_v<T, W, V, kTypeF32>(a, stream) : launch_norm_v<T, W, 1, kTypeF32>(a, stream);
+  });
+}
+
+int64_t norm_parts(int64_t rows, int64_t) { return rows < kMaxParts ? rows : kMaxParts; }
+
+cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, cudaStream_t stream) {
+  if (a.rows == 0) return cudaMemsetAsync(a.dweight, 0, static_cast<size_t>(a.H) * 4, stream);
+  const int size = size_of(dtype);
+  const bool vec = vectors(a.dy, a.lddy, size) && vectors(a.h, a.ldh, size) && vectors(a.weight, 0, 1) &&
+                   vectors(a.dx, a.H, size) && a.H * size % 16 == 0 && (!a.dh || vectors(a.dh, a.lddh, size));
+  int64_t parts = norm_parts(a.rows, a.H);
+  const cudaError_t e = with_types(dtype, a.weight_f32, [&](auto t, auto w) {
+    using T = decltype(t);
+    using W = decltype(w);
+    constexpr int V = Elem<T>::kVec;
+    if (!vec) return launch_backward_long<T, W, 1>(a, parts, stream);
+    if (a.H > 1024 * V) return launch_backward_long<T, W, V>(a, parts, stream);
+    const int log = team_log(a.H / V);
+    if (log == 10) {
+      if (parts > kSms) parts = kSms;
+      return launch(norm_backward_kernel<T, W, 1024>, dim3(static_cast<unsigned>(parts)), 1024, stream, a, log);
+    }
+    const int64_t blocks = (a.rows + (512 >> log) - 1) / (512 >> log);
+    if (parts > blocks) parts = blocks;
+    return launch(norm_backward_kernel<T, W, 512>, dim3(static_cast<unsigned>(parts)), 512, stream, a, log);
+  });
+  if (e != cudaSuccess) return e;
+  return launch(norm_sum_kernel, dim3(static_cast<unsigned>((a.H + 31) / 32)), 32 * kSumWarps, stream, a.parts, parts,
+                a.H, a.dweight);
+}
+
+}  // namespace agg

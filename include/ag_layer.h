@@ -1,6 +1,7 @@
 /*
  * ag_layer.h -- C ABI of libaggemm.so's operators around a layer's products: the
- * products of microscaled 4-bit operands.
+ * root-mean-square norm before them, the gated activation between them, and the products
+ * of microscaled 4-bit operands.
  *
  * Conventions are those of ag_moe.h: row-major DEVICE matrices of the current device that
  * the caller owns, row pitches in elements, asynchronous runs on `stream`, negative
@@ -17,6 +18,56 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/* ---------------------------------------------------------------- norm */
+/*
+ * For each of the rows (rows x H, any of the three types)
+ *   h = x + residual, rounded to the rows' type (without residual, NULL: x itself),
+ *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight,
+ * in 32 bits, y rounded once.  weight: H elements of the rows' type or floats.  h
+ * (contiguous; ignored without residual) and rstd (rows floats; may be NULL) are what the
+ * gradient needs.  Outputs are contiguous and overlap no input.  eps >= 0.
+ * rows < 2^31, 1 <= H <= 2^24.
+ */
+int ag_norm_rms(int64_t rows, int64_t H, int dtype, const void *x, int64_t ldx,
+                const void *residual, int64_t ldr, const void *weight, int weight_dtype, float eps,
+                void *y, void *h, float *rstd, void *stream);
+/*
+ * The same with y as the codes and scales of a product's rows instead: what
+ * ag_fp8_quantize_rows (code_type AG_MOE_E4M3, H % 16 == 0) or ag_fp4_quantize_rows
+ * (AG_MOE_E2M1, H % 32 == 0) would make of the unrounded y.  All pointers and row pitches
+ * are multiples of 16 bytes.
+ */
+int ag_norm_rms_quantized(int64_t rows, int64_t H, int dtype, const void *x, int64_t ldx,
+                          const void *residual, int64_t ldr, const void *weight, int weight_dtype,
+                          float eps, int code_type, void *q, void *scales, void *h, void *stream);
+/*
+ * From y's gradient dy (and dh, what else arrives at h; or NULL) with h (x where there was
+ * no residual) and rstd of the forward pass: dx (rows x H, contiguous), the gradient of x and of
+ * the residual, and dweight (H floats), summed over the rows in a fixed order.
+ * workspace: ag_norm_rms_backward_workspace(rows, H) bytes, 16-byte aligned, not in use by
+ * another call.  rows may be 0: dweight becomes zeros.
+ */
+int64_t ag_norm_rms_backward_workspace(int64_t rows, int64_t H);
+int ag_norm_rms_backward(int64_t rows, int64_t H, int dtype, const void *dy, int64_t lddy,
+                         const void *h, int64_t ldh, const void *weight, int weight_dtype,
+                         const float *rstd, const void *dh, int64_t lddh, void *dx, float *dweight,
+                         void *workspace, void *stream);
+
+/* ---------------------------------------------------------------- gated activation */
+/*
+ * y = g * s * u with s = 1 / (1 + exp(-g)): x is rows x 2 N, the gate g in its first N
+ * columns, u in the others; y is rows x N, contiguous.  In 32 bits, rounded once.
+ * rows < 2^31, 1 <= N <= 2^24.
+ */
+int ag_act_swiglu(int64_t rows, int64_t N, int dtype, const void *x, int64_t ldx, void *y,
+                  void *stream);
+/* The same with y as codes and scales, as in ag_norm_rms_quantized (N for H). */
+int ag_act_swiglu_quantized(int64_t rows, int64_t N, int dtype, const void *x, int64_t ldx,
+                            int code_type, void *q, void *scales, void *stream);
+/* dx (rows x 2 N, contiguous): dg = dy u s (1 + g (1 - s)), du = dy g s. */
+int ag_act_swiglu_backward(int64_t rows, int64_t N, int dtype, const void *dy, int64_t lddy,
+                           const void *x, int64_t ldx, void *dx, void *stream);
 
 /* ---------------------------------------------------------------- 4-bit operands */
 /*
