@@ -26,7 +26,7 @@
 //   warp 18     weight gradient: zeros over the rows behind a group's end;
 //               e4m3: the scales of each k-block into shared memory
 //               e2m1: the rows' scales into shared memory, as the tensor core takes them;
-//   warp 19     e2m1: passes them on
+//   warps 19-20 e2m1: pass them on
 //
 // Work: tiles in expert order, and inside an expert in groups of 8 row tiles by all
 // wide tiles, so that the tiles in flight share operands in L2.  Unit u of pair p is
@@ -97,22 +97,27 @@ __host__ __device__ constexpr int stages_of(int op, int BN) {
   return (BN != kXFewRows ? 6 : op == kOpFp4 ? 8 : 10) / kSub;
 }
 constexpr int kScaleBatch = 4;  // e4m3: k-blocks whose scales are handed over at once; two such batches
-// e2m1: pieces of 128 rows x 4 scales, of a stage's weights and of its rows, [128 elements of K][128 rows]
+// e2m1: a stage's pieces of 128 rows x 4 scales of the weights, and in a ring of their own
+// those of the rows, [128 elements of K][128 rows]
 constexpr int kPiece = 512, kPieces = 2 * kSub;
 __host__ __device__ constexpr int row_pieces(int BN) { return (BN + 127) / 128; }
-__host__ __device__ constexpr int scale_stage(int BN) { return kPieces * (1 + row_pieces(BN)) * kPiece; }
+__host__ __device__ constexpr int row_slot(int BN) { return kPieces * row_pieces(BN) * kPiece; }
+__host__ __device__ constexpr int scale_slots(int BN) { return BN == kXFewRows ? 8 : 5; }
+constexpr int kMaxScaleSlots = 8;
 __host__ __device__ constexpr int scale_bytes(int op, int BN) {
   return op == kOpFp8 ? 2 * kScaleBatch * BN * 4 : op == kOpFp8Long ? 2 * kScaleBatch * 2 * 128 * 4
-         : op == kOpFp4 ? stages_of(op, BN) * scale_stage(BN) : 0;
+         : op == kOpFp4 ? stages_of(op, BN) * kPieces * kPiece + scale_slots(BN) * row_slot(BN) : 0;
 }
 // An epilogue warp's buffer for rows of output on their way: 8 of 128 bytes, or 4.
-__host__ __device__ constexpr int out_buffer(int op) { return op == kOpFp8Long ? 0 : op == kOpFp8 ? 512 : 1024; }
+__host__ __device__ constexpr int out_buffer(int op) {
+  return op == kOpFp8Long ? 0 : op == kOpFp8 || op == kOpFp4 ? 512 : 1024;
+}
 __host__ __device__ constexpr int out_bytes(int op) { return kXEpiWarps * out_buffer(op); }
 constexpr int kTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) & ~15;
 constexpr int kUnitBytes = kXEpiWarps * 48;  // the epilogue warps' units
 __host__ __device__ constexpr int smem_bytes(int op, int BN) {
   return stages_of(op, BN) * kSub * (kWBytes + r_bytes(BN)) + scale_bytes(op, BN) +
-         out_bytes(op) + kTableBytes + kUnitBytes + 512 /*barriers*/ + 1024 /*alignment*/;
+         out_bytes(op) + kTableBytes + kUnitBytes + 640 /*barriers*/ + 1024 /*alignment*/;
 }
 static_assert(smem_bytes(kOpForward, kXRows) <= 227 * 1024 && smem_bytes(kOpForward, kXFewRows) <= 227 * 1024 &&
                   smem_bytes(kOpWeight, kXRows) <= 227 * 1024 && smem_bytes(kOpFp8, kXFewRows) <= 227 * 1024 &&
@@ -494,12 +499,14 @@ struct Ring {
   uint64_t* tempty; // on the even CTA: the epilogue warps of both
   uint64_t* tail;   // weight gradient, by stage: this CTA's part of a group's last k-block
   uint64_t* zfull;  // and, on the even CTA: both CTAs' parts zeroed behind the group's end
-                    // (e2m1: by stage, both CTAs' copies of the rows' scales)
-  uint64_t* sraw;   // e2m1, by stage: this CTA's copy of the rows' scales has landed
+  uint64_t* praw;   // e2m1, by slot: this CTA's copy of the rows' scales has landed,
+  uint64_t* pfull;  // on the even CTA's: both CTAs' have,
+  uint64_t* pempty; // the tensor core has read them
   uint64_t* sfull;  // e4m3: scales of a k-block, by slot
   uint64_t* sempty; // e4m3: this CTA's epilogue warps are through with them
   float* scales;    // two batches: [k-block][BN], long groups [k-block][column block][128]
-                    // (e2m1: a stage's pieces, the weights' and then the rows')
+                    // (e2m1: a stage's pieces of the weights)
+  uint8_t* pieces;  // e2m1, by slot: the rows'
   uint8_t* stage_out;  // a buffer of out_buffer(OP) bytes for each epilogue warp
   Unit* units;         // an epilogue warp's unit, beside the sums that fill its registers
   volatile int* abort;
@@ -582,7 +589,7 @@ __device__ void tma_role(const ExpertsParams& p, const Table& table, const Ring&
           load_k(wd, &p.tm_w, bar, p.w_blk, kb0, 128, n, u.e, kWBytes);
           load_k(rd, &p.tm_r[boxes - 1], bar, p.r_blk, kb0, 128, u.row0 + mine, 0, height * 128);
           // (a piece is 64 8-byte elements; past the last columns' block: another's, not used)
-          tma_load_2d_pair(reinterpret_cast<uint8_t*>(ring.scales) + stage * scale_stage(BN), &p.tm_s, bar,
+          tma_load_2d_pair(reinterpret_cast<uint8_t*>(ring.scales) + stage * (kPieces * kPiece), &p.tm_s, bar,
                            kb0 * (2 * kPiece / 8), u.e * ((p.wide + 127) / 128) + n / 128);
         } else if constexpr (OP == kOpWeight) {
           load_mn(wd, &p.tm_w, bar, p.w_blk, n, u.row0 + kb0 * 64, 0, false);
@@ -793,15 +800,19 @@ __device__ void scale_long_role(const ExpertsParams& p, const Table& table,
 // ------------------------------------------------------------------ scales (e2m1)
 // The tile's rows' scales of each stage, as pieces of 128 rows: row r's word at (r % 32) *
 // 16 + (r / 32) * 4.  Both CTAs hold those of all rows (each multiplies its half of the
-// columns with all of them).  One warp copies the words to their places, as many stages
-// ahead as the ring has, and another passes on what has landed: a warp that loads and
-// stores them itself waits for a load once a stage (8192 x 4096 x 4096: 95 us so).
+// columns with all of them).  One warp copies the words to their places, and others pass on
+// what has landed, by turns: the release for the pair takes a warp about a microsecond
+// under load, as long as the MMAs of two stages.  The pieces have a ring of their own,
+// longer than the operands', which covers both ways' latencies.
+// (8192 x 16384 x 8192: 740 us where a warp loads and stores the words itself; 465 with one
+// warp that passes on, in the operands' ring; 480 to 560 with the words stored to TMEM by
+// four warps, whose stores take as long as a k-block's MMAs.)
 template <int BN>
-__device__ void scale4_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int lane) {
+__device__ void copy4_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int lane) {
   Schedule<kOpFp4, BN> sch(p, table);
-  constexpr int kStagesX = stages_of(kOpFp4, BN);
+  constexpr int kSlots = scale_slots(BN);
   const int32_t KA = (p.red + 127) / 128;
-  int stage = 0;
+  int slot = 0;
   uint32_t phase = 0;
   bool ok = true;
   Unit u;
@@ -809,10 +820,10 @@ __device__ void scale4_role(const ExpertsParams& p, const Table& table, const Ri
     const int32_t words = (u.cnt + 31) / 32;  // (the accumulator's columns behind them are not stored)
     const uint32_t* const xs = p.xs4 + u.row0 + lane;
     for (int32_t kb = u.kb0; kb < u.kb1; kb += kSub) {
-      ok = mbar_wait(&ring.empty[stage], phase ^ 1u, p.timeout_ns, ring.abort, p.status);
+      ok = mbar_wait(&ring.pempty[slot], phase ^ 1u, p.timeout_ns, ring.abort, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint32_t to = smem_u32(ring.scales) + stage * scale_stage(BN) + kPieces * kPiece + lane * 16;
+      const uint32_t to = smem_u32(ring.pieces) + slot * row_slot(BN) + lane * 16;
 #pragma unroll
       for (int a = 0; a < kPieces; ++a) {
         if (kb * 2 + a >= KA) break;  // (no MMA reads the pieces past K)
@@ -823,9 +834,9 @@ __device__ void scale4_role(const ExpertsParams& p, const Table& table, const Ri
             copy_word(to + (a * row_pieces(BN) + j / 4) * kPiece + j % 4 * 4,
                       j * 32 + lane < u.cnt ? from + j * 32 : p.xs4, j * 32 + lane < u.cnt);
       }
-      arrive_copied(&ring.sraw[stage]);
-      if (++stage == kStagesX) {
-        stage = 0;
+      arrive_copied(&ring.praw[slot]);
+      if (++slot == kSlots) {
+        slot = 0;
         phase ^= 1u;
       }
     }
@@ -838,23 +849,27 @@ __device__ void scale4_role(const ExpertsParams& p, const Table& table, const Ri
 }
 
 template <int BN>
-__device__ void pass4_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int lane) {
+__device__ void pass4_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int lane,
+                           int turn) {
   Schedule<kOpFp4, BN> sch(p, table);
-  constexpr int kStagesX = stages_of(kOpFp4, BN);
-  const uint32_t zfull0 = mapa_shared(smem_u32(ring.zfull), 0);
-  int stage = 0;
+  constexpr int kSlots = scale_slots(BN);
+  const uint32_t pfull0 = mapa_shared(smem_u32(ring.pfull), 0);
+  int slot = 0, next = turn;  // stages until this warp's next
   uint32_t phase = 0;
   bool ok = true;
   Unit u;
   for (int32_t i = 0; ok && sch.get(i, u); ++i)
     for (int32_t kb = u.kb0; kb < u.kb1; kb += kSub) {
-      ok = warp_wait(&ring.sraw[stage], phase, p.timeout_ns, ring.abort, p.status);
-      if (!ok) break;
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(zfull0 + stage * 8);
-      if (++stage == kStagesX) {
-        stage = 0;
+      if (next-- == 0) {
+        next = kPassWarps - 1;
+        ok = warp_wait(&ring.praw[slot], phase, p.timeout_ns, ring.abort, p.status);
+        if (!ok) break;
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(pfull0 + slot * 8);
+      }
+      if (++slot == kSlots) {
+        slot = 0;
         phase ^= 1u;
       }
     }
@@ -884,6 +899,8 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
   constexpr uint32_t kWSecond = (kWMn ? 64 * 128 : kWBytes) / 16;  // the second k-block
   int stage = 0;
   uint32_t acc = 0, full_phase = 0, zeroed = 0;  // bit s: parity of stage s's barriers
+  [[maybe_unused]] int slot = 0;  // e2m1: of the rows' scales
+  [[maybe_unused]] uint32_t slot_phase = 0;
   bool ok = true;
   auto accumulator = [&] {  // wait until it has been read
     const bool r = warp_wait(&ring.tempty[acc & 1u], ((acc >> 1) & 1u) ^ 1u, p.timeout_ns, ring.abort,
@@ -922,8 +939,8 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
         ok = warp_wait(&ring.full[stage], (full_phase >> stage) & 1u, p.timeout_ns, ring.abort,
                        p.status);
         if (OP == kOpFp4 && ok)  // and the rows' scales, from both CTAs' scale warps
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&ring.zfull[stage], (full_phase >> stage) & 1u,
-                                                         p.timeout_ns, ring.abort, p.status));
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&ring.pfull[slot], slot_phase, p.timeout_ns, ring.abort,
+                                                         p.status));
         full_phase ^= 1u << stage;
       }
       if (!ok) break;
@@ -939,17 +956,17 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
         if constexpr (OP == kOpFp4) {
           const int32_t rest = (p.red - (kb0 + s) * 256 + 63) / 64, steps = rest < 4 ? rest : 4;
           const uint32_t sf = tmem + kScaleCol + s * kScaleCols;
-          const uint32_t from = smem_u32(ring.scales) + stage * scale_stage(BN);
+          const uint32_t from = smem_u32(ring.scales) + (stage * kPieces + 2 * s) * kPiece;
+          const uint32_t rows_from = smem_u32(ring.pieces) + slot * row_slot(BN) + 2 * s * row_pieces(BN) * kPiece;
           if (elect_one()) {
 #pragma unroll
             for (int a = 0; a < 2; ++a)
               if (2 * a < steps) {
-                copy_scales_pair(sf + 4 * a, from + (2 * s + a) * kPiece);
+                copy_scales_pair(sf + 4 * a, from + a * kPiece);
 #pragma unroll
                 for (int r = 0; r < row_pieces(BN); ++r)
                   if (r * 128 < width)
-                    copy_scales_pair(sf + 8 + 8 * a + 4 * r,
-                                     from + (kPieces + (2 * s + a) * row_pieces(BN) + r) * kPiece);
+                    copy_scales_pair(sf + 8 + 8 * a + 4 * r, rows_from + (a * row_pieces(BN) + r) * kPiece);
               }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -976,7 +993,14 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
         if (OP == kOpFp8Long) ++acc;
       }
       if (!ok) break;
-      if (elect_one()) mma_commit_pair_both(&ring.empty[stage]);
+      if (elect_one()) {
+        mma_commit_pair_both(&ring.empty[stage]);
+        if (OP == kOpFp4) mma_commit_pair_both(&ring.pempty[slot]);
+      }
+      if (OP == kOpFp4 && ++slot == scale_slots(BN)) {
+        slot = 0;
+        slot_phase ^= 1u;
+      }
       if (++stage == kStagesX) stage = 0;
       if (OP != kOpFp8Long) {
         left -= n_sub;
@@ -1404,6 +1428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   ring.w = smem;
   ring.r = smem + kStagesX * kSub * kWBytes;
   ring.scales = reinterpret_cast<float*>(ring.r + kStagesX * kSub * r_bytes(BN));
+  ring.pieces = reinterpret_cast<uint8_t*>(ring.scales) + kStagesX * kPieces * kPiece;
   ring.stage_out = reinterpret_cast<uint8_t*>(ring.scales) + scale_bytes(OP, BN);
   int32_t* off = reinterpret_cast<int32_t*>(ring.stage_out + out_bytes(OP));
   int32_t* pre = off + kMaxExperts + 1;
@@ -1417,8 +1442,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   ring.zfull = ring.tail + kStagesX;
   ring.sfull = ring.zfull + kStagesX;
   ring.sempty = ring.sfull + 2;
-  ring.sraw = ring.sempty + 2;
-  uint64_t* drain = ring.sraw + kStagesX;
+  ring.praw = ring.sempty + 2;
+  ring.pfull = ring.praw + kMaxScaleSlots;
+  ring.pempty = ring.pfull + kMaxScaleSlots;
+  uint64_t* drain = ring.pempty + kMaxScaleSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   ring.abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* flag = reinterpret_cast<int32_t*>(tmem_slot + 2);
@@ -1434,8 +1461,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       mbar_init(&ring.empty[s], 1);
       mbar_init(&ring.tail[s], 1);
       mbar_init(&ring.zfull[s], 2);
-      mbar_init(&ring.sraw[s], 32);
     }
+    if (OP == kOpFp4)
+      for (int s = 0; s < kMaxScaleSlots; ++s) {
+        mbar_init(&ring.praw[s], 32);
+        mbar_init(&ring.pfull[s], 2);
+        mbar_init(&ring.pempty[s], 1);
+      }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ring.tfull[b], 1);
       mbar_init(&ring.tempty[b], 2 * kXEpiWarps);
@@ -1481,9 +1513,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       scale_long_role<BN>(p, table, ring, rank, lane);
     } else if constexpr (OP == kOpFp4) {
       if (warp == 2 + kXEpiWarps)
-        scale4_role<BN>(p, table, ring, rank, lane);
+        copy4_role<BN>(p, table, ring, rank, lane);
       else
-        pass4_role<BN>(p, table, ring, rank, lane);
+        pass4_role<BN>(p, table, ring, rank, lane, warp - (3 + kXEpiWarps));
     }
   } else if (threadIdx.x == 0) {
     set_status(p.status + 2, kStatusOffsets, 0);
