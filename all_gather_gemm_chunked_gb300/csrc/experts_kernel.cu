@@ -26,7 +26,7 @@
 //   warp 18     weight gradient: zeros over the rows behind a group's end;
 //               e4m3: the scales of each k-block into shared memory
 //               e2m1: the rows' scales into shared memory, as the tensor core takes them;
-//   warps 19-20 e2m1: pass them on
+//   warps 19-23 e2m1: pass them on
 //
 // Work: tiles in expert order, and inside an expert in groups of 8 row tiles by all
 // wide tiles, so that the tiles in flight share operands in L2.  Unit u of pair p is
@@ -802,8 +802,10 @@ __device__ void scale_long_role(const ExpertsParams& p, const Table& table,
 // 16 + (r / 32) * 4.  Both CTAs hold those of all rows (each multiplies its half of the
 // columns with all of them).  One warp copies the words to their places, and others pass on
 // what has landed, by turns: the release for the pair takes a warp about a microsecond
-// under load, as long as the MMAs of two stages.  The pieces have a ring of their own,
-// longer than the operands', which covers both ways' latencies.
+// under load and two where weights stream in, as long as the MMAs of several stages (64 rows
+// of 16384 x 7168 22.7 us with two such warps, 20.8 with five; 24 warps need no fewer
+// registers than 21).  The pieces have a ring of their own, longer than the operands',
+// which covers both ways' latencies.
 // (8192 x 16384 x 8192: 740 us where a warp loads and stores the words itself; 465 with one
 // warp that passes on, in the operands' ring; 480 to 560 with the words stored to TMEM by
 // four warps, whose stores take as long as a k-block's MMAs.)
