@@ -17,7 +17,7 @@ constexpr int kThreads = 256;
 // s and 1 - s from exp(-|g|), which does not overflow: far negative gates keep their s
 // (exp(-g) passes the largest float from -88.7 on, and 1 / (1 + exp(-g)) would be zero).
 __device__ __forceinline__ void sigmoid(float g, float& s, float& rest) {
-  const float e = expf(-fabsf(g)), r = __frcp_rn(1.0f + e);
+  const float e = expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + e);  // (of 1 to 2: off by at most 1 ulp)
   s = g < 0.0f ? e * r : r;
   rest = g < 0.0f ? r : e * r;
 }
@@ -30,10 +30,10 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const GateArgs a, int 
   const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (team * P * V) + thread * V;
   const bool valid = row < a.rows;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx + c0;
-  Raw<T, V> g[P], u[P];
+  Piece<T, V> g[P], u[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    g[i] = u[i] = Raw<T, V>{};
+    g[i] = u[i] = Piece<T, V>{};
     if (valid && c0 + i * team * V < a.N) {
       g[i].load(x + i * team * V);
       u[i].load(x + i * team * V + a.N);
@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const GateArgs a, int 
   for (int i = 0; i < P; ++i) {
     const int64_t c = c0 + i * team * V;
     const bool in = valid && c < a.N;
+    if (c - (thread & 31) * V >= a.N) break;  // (all of the warp)
     float f[V], v[V];
     g[i].get(f);
     u[i].get(v);
@@ -55,7 +56,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const GateArgs a, int 
     if constexpr (OUT == kTypeE4m3 || OUT == kTypeE2m1) {
       put_codes<OUT, V>(a.out, a.scales, a.rows, a.N, row, c, in, f);
     } else {
-      if (in) store_elems<T, V>(static_cast<T*>(a.out) + row * a.N + c, f);
+      if (in) store_floats(static_cast<T*>(a.out) + row * a.N + c, f);
     }
   }
 }
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const GateArg
   if (row >= a.rows) return;
   const T *x = static_cast<const T*>(a.x) + row * a.ldx + c0, *dy = static_cast<const T*>(a.dy) + row * a.lddy + c0;
   T* dx = static_cast<T*>(a.out) + row * 2 * a.N + c0;
-  Raw<T, V> g[P], u[P], d[P];
+  Piece<T, V> g[P], u[P], d[P];
 #pragma unroll
   for (int i = 0; i < P; ++i)
     if (c0 + i * team * V < a.N) {
@@ -92,8 +93,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const GateArg
       v[j] = es * v[j] * fmaf(f[j], rest, 1.0f);
       e[j] = es * f[j];
     }
-    store_elems<T, V>(dx + i * team * V, v);
-    store_elems<T, V>(dx + i * team * V + a.N, e);
+    store_floats(dx + i * team * V, v);
+    store_floats(dx + i * team * V + a.N, e);
   }
 }
 
@@ -115,41 +116,51 @@ cudaError_t with_type(int dtype, const F& f) {
   return dtype == kTypeF32 ? f(float{}) : dtype == kTypeF16 ? f(__half{}) : f(__nv_bfloat16{});
 }
 
+// Pieces a thread: more in flight where there is enough to do for all SMs.
+bool plenty(const GateArgs& a, int V) { return a.rows * ((a.N + V - 1) / V) >= 152 * 2048 && a.N >= 32 * 4 * V; }
 template <typename T, int V, int OUT>
 cudaError_t forward(const GateArgs& a, cudaStream_t stream) {
-  constexpr int P = 2;
-  const Shape s = shape_of(a.rows, a.N, V, P);
-  return launch(swiglu_kernel<T, V, P, OUT>, s.grid, kThreads, stream, a, s.log);
+  constexpr int kFew = V * sizeof(T) == 16 ? 1 : 4, kMost = V * sizeof(T) == 16 ? 4 : 8;
+  const bool most = plenty(a, V);
+  const Shape s = shape_of(a.rows, a.N, V, most ? kMost : kFew);
+  return most ? launch(swiglu_kernel<T, V, kMost, OUT>, s.grid, kThreads, stream, a, s.log)
+              : launch(swiglu_kernel<T, V, kFew, OUT>, s.grid, kThreads, stream, a, s.log);
 }
 template <typename T, int V>
 cudaError_t backward(const GateArgs& a, cudaStream_t stream) {
-  constexpr int P = 2;
-  const Shape s = shape_of(a.rows, a.N, V, P);
-  return launch(swiglu_backward_kernel<T, V, P>, s.grid, kThreads, stream, a, s.log);
+  constexpr int kFew = V * sizeof(T) == 16 ? 1 : 4, kMost = V * sizeof(T) == 16 ? 2 : 8;
+  const bool most = plenty(a, V);
+  const Shape s = shape_of(a.rows, a.N, V, most ? kMost : kFew);
+  return most ? launch(swiglu_backward_kernel<T, V, kMost>, s.grid, kThreads, stream, a, s.log)
+              : launch(swiglu_backward_kernel<T, V, kFew>, s.grid, kThreads, stream, a, s.log);
 }
 }  // namespace
 
 cudaError_t launch_swiglu(const GateArgs& a, int dtype, int out_type, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
   const int size = dtype == kTypeF32 ? 4 : 2;
-  const bool vec = vectors(a.x, a.ldx, size) && a.N * size % 16 == 0 && vectors(a.out, 0, 1);
+  Access at;  // (N too: the other factor begins N elements behind the gate)
+  at.rows(a.x, a.ldx, size).rows(a.out, a.N, out_type == dtype ? size : 16);
   return with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    constexpr int V = Elem<T>::kVec;
+    constexpr int V = Elem<T>::kVec, V4 = 4 / sizeof(T);
     if (out_type == kTypeE4m3) return forward<T, V, kTypeE4m3>(a, stream);
     if (out_type == kTypeE2m1) return forward<T, V, kTypeE2m1>(a, stream);
-    return vec ? forward<T, V, kTypeF32>(a, stream) : forward<T, 1, kTypeF32>(a, stream);
+    if (at.by(16)) return forward<T, V, kTypeF32>(a, stream);
+    return at.by(4) ? forward<T, V4, kTypeF32>(a, stream) : forward<T, 1, kTypeF32>(a, stream);
   });
 }
 
 cudaError_t launch_swiglu_backward(const GateArgs& a, int dtype, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
   const int size = dtype == kTypeF32 ? 4 : 2;
-  const bool vec = vectors(a.x, a.ldx, size) && vectors(a.dy, a.lddy, size) && a.N * size % 16 == 0 &&
-                   vectors(a.out, 0, 1);
+  Access at;
+  at.rows(a.x, a.ldx, size).rows(a.dy, a.lddy, size).rows(a.out, a.N, size);
   return with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    return vec ? backward<T, Elem<T>::kVec>(a, stream) : backward<T, 1>(a, stream);
+    constexpr int V = Elem<T>::kVec, V4 = 4 / sizeof(T);
+    if (at.by(16)) return backward<T, V>(a, stream);
+    return at.by(4) ? backward<T, V4>(a, stream) : backward<T, 1>(a, stream);
   });
 }
 

@@ -1,19 +1,35 @@
 // fp4_quant.cu -- microscaled e2m1 operands (fp4_codes.cuh) of rows and of weights.
 
 #include "fp4_codes.cuh"
-#include "moe_rows.cuh"
-#include "moe_types.cuh"
+#include "layer_rows.cuh"
 
 namespace agg {
 
 namespace {
+// The largest magnitude's bits as a float; of 16-bit elements two at a time, whose bits
+// order as the magnitudes do.
+template <typename T, int V>
+__device__ __forceinline__ uint32_t largest_of(const Piece<T, V>& p) {
+  if constexpr (sizeof(T) == 4) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) m = max(m, p.w[v] & 0x7fffffffu);
+    return m;
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < Piece<T, V>::kWords; ++i) m = __vmaxu2(m, p.w[i] & 0x7fff7fffu);
+    const uint16_t one = static_cast<uint16_t>(max(m & 0xffffu, m >> 16));
+    return __float_as_uint(Elem<T>::get(reinterpret_cast<const T&>(one)));
+  }
+}
+
 // Bound by memory (2 bytes in, a little above half a byte out per element).  A warp takes
 // 256 elements of a row per step, 8 per lane: 4 lanes make one block, whose maximum takes
 // two shuffles, and 16 lanes the word of four scales.  All of a lane's loads are issued
 // before the first use.  The eight warps of a block take eight neighbouring rows, so that
 // the words they write ([K / 128][row]) fill 32-byte sectors.
-constexpr int kQuantSteps = 4;
-template <typename T>
+template <typename T, int kSteps>
 __global__ void __launch_bounds__(256) quantize_rows4_kernel(int64_t rows, int64_t K, const T* x, int64_t ldx,
                                                              int64_t src_rows, const int32_t* order, int k,
                                                              uint8_t* __restrict__ q, uint32_t* __restrict__ scales) {
@@ -30,27 +46,30 @@ __global__ void __launch_bounds__(256) quantize_rows4_kernel(int64_t rows, int64
     in = o >= 0;
   }
   in = in && src < src_rows;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (256 * kQuantSteps) + lane * 8;
-  float f[kQuantSteps][8 / V][V];
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (256 * kSteps) + lane * 8;
+  Piece<T, V> p[kSteps][8 / V];
 #pragma unroll
-  for (int i = 0; i < kQuantSteps; ++i) {
+  for (int i = 0; i < kSteps; ++i) {
     const int64_t c = c0 + i * 256;  // (K % 32 == 0: a lane's 8 elements are all in or all out)
 #pragma unroll
     for (int h = 0; h < 8 / V; ++h) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) f[i][h][v] = 0.0f;
-      if (in && c < K) load_elems<T, V>(x + src * ldx + c + h * V, f[i][h]);
+      p[i][h] = Piece<T, V>{};
+      if (in && c < K) p[i][h].load(x + src * ldx + c + h * V);
     }
   }
 #pragma unroll
-  for (int i = 0; i < kQuantSteps; ++i) {
+  for (int i = 0; i < kSteps; ++i) {
     const int64_t c = c0 + i * 256;
+    if (c - lane * 8 >= K) break;
     float g[8];
     uint32_t largest = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      g[j] = f[i][j / V][j % V];
-      largest = max(largest, magnitude_bits(g[j]));
+    for (int h = 0; h < 8 / V; ++h) {
+      float f[V];
+      p[i][h].get(f);
+#pragma unroll
+      for (int v = 0; v < V; ++v) g[h * V + v] = f[v];
+      largest = max(largest, largest_of(p[i][h]));
     }
     largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
     largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
@@ -125,18 +144,16 @@ cudaError_t launch_quantize_rows4(int64_t rows, int64_t K, int dtype, const void
                                   int64_t src_rows, const int32_t* order, int k, void* q,
                                   void* scales, cudaStream_t stream) {
   if (rows == 0) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>((rows + 7) / 8),
-                  static_cast<unsigned>((K + 256 * kQuantSteps - 1) / (256 * kQuantSteps)));
-  uint8_t* out = static_cast<uint8_t*>(q);
-  uint32_t* words = static_cast<uint32_t*>(scales);
-  if (dtype == kTypeF32)
-    return launch(quantize_rows4_kernel<float>, grid, 256, stream, rows, K, static_cast<const float*>(x), ldx,
-                  src_rows, order, k, out, words);
-  if (dtype == kTypeF16)
-    return launch(quantize_rows4_kernel<__half>, grid, 256, stream, rows, K, static_cast<const __half*>(x), ldx,
-                  src_rows, order, k, out, words);
-  return launch(quantize_rows4_kernel<__nv_bfloat16>, grid, 256, stream, rows, K,
-                static_cast<const __nv_bfloat16*>(x), ldx, src_rows, order, k, out, words);
+  // Eight steps of 256 elements a warp where that leaves work for every SM, else one.
+  const int steps = rows * K >= int64_t{152} * 8 * 8192 && K >= 1024 ? 8 : 1;
+  const dim3 grid(static_cast<unsigned>((rows + 7) / 8), static_cast<unsigned>((K + 256 * steps - 1) / (256 * steps)));
+  auto go = [&](auto t) {
+    using T = decltype(t);
+    return launch(steps == 8 ? quantize_rows4_kernel<T, 8> : quantize_rows4_kernel<T, 1>, grid, 256, stream, rows, K,
+                  static_cast<const T*>(x), ldx, src_rows, order, k, static_cast<uint8_t*>(q),
+                  static_cast<uint32_t*>(scales));
+  };
+  return dtype == kTypeF32 ? go(float{}) : dtype == kTypeF16 ? go(__half{}) : go(__nv_bfloat16{});
 }
 
 cudaError_t launch_quantize_weights4(int E, int64_t K, int64_t N, int dtype, const void* w, void* q,

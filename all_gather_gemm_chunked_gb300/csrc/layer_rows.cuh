@@ -21,13 +21,14 @@ struct NormArgs {
   const void* weight;
   int weight_f32;        // weights are floats (otherwise the rows' type)
   float eps;
+  float inv_H;           // (made by the launcher)
   void* out;             // y, or codes
   void* scales;          // of the codes
   void* h;               // with a residual
   float* rstd;           // or null
 };
 // out_type: dtype itself, kTypeE4m3 or kTypeE2m1.
-cudaError_t launch_norm(const NormArgs& a, int dtype, int out_type, cudaStream_t stream);
+cudaError_t launch_norm(NormArgs a, int dtype, int out_type, cudaStream_t stream);
 
 struct NormBackwardArgs {
   int64_t rows, H;
@@ -61,6 +62,68 @@ cudaError_t launch_swiglu(const GateArgs& a, int dtype, int out_type, cudaStream
 cudaError_t launch_swiglu_backward(const GateArgs& a, int dtype, cudaStream_t stream);
 
 #ifdef __CUDACC__
+// V neighbouring elements as they lie in memory, 16, 4 or 2 bytes.  (Loads are volatile: in
+// the order of the source, behind a launch's wait, and none sinks to its use.)
+template <typename T, int V>
+struct Piece {
+  static constexpr int kBytes = V * static_cast<int>(sizeof(T)), kWords = kBytes < 4 ? 1 : kBytes / 4;
+  static_assert(kBytes == 16 || kBytes == 4 || kBytes == 2, "one access");
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kBytes == 16) {
+      asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+    } else if constexpr (kBytes == 4) {
+      asm volatile("ld.global.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+    } else {
+      uint16_t h;
+      asm volatile("ld.global.u16 %0, [%1];" : "=h"(h) : "l"(p));
+      w[0] = h;
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (kBytes == 16)
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (kBytes == 4)
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    else
+      *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+  }
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[v] = __uint_as_float(w[v]);
+    } else if constexpr (V == 1) {
+      const uint16_t h = static_cast<uint16_t>(w[0]);
+      f[0] = Elem<T>::get(reinterpret_cast<const T&>(h));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const float2 p = Elem<T>::unpair(w[i]);
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const float (&f)[V]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) w[v] = __float_as_uint(f[v]);
+    } else if constexpr (V == 1) {
+      const T h = Elem<T>::put(f[0]);
+      w[0] = reinterpret_cast<const uint16_t&>(h);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = Elem<T>::pair(f[2 * i], f[2 * i + 1]);
+    }
+  }
+};
+template <typename T, int V>
+__device__ __forceinline__ void store_floats(T* p, const float (&f)[V]) {
+  Piece<T, V> r;
+  r.put(f);
+  r.store(p);
+}
+
 // V neighbouring elements of a row as codes, by the lanes of a whole warp, which hold V
 // elements each, the next lane the next V; past the row (`in` false) they are zeros.  The
 // same codes and scales as quantising the floats.
@@ -131,9 +194,14 @@ __device__ __forceinline__ float team_sum(float v, int team_warps, float* part) 
 }
 #endif
 
-// 16-byte accesses: base and row pitch are multiples of 16 bytes.
-inline bool vectors(const void* p, int64_t ld, int size) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * size % 16 == 0;
-}
+// The bytes of an access that all of some rows allow: 16, 4, or one element's.
+struct Access {
+  uint64_t bits = 0;
+  Access& rows(const void* p, int64_t ld, int size) {  // (null: not there)
+    if (p) bits |= reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(ld * size);
+    return *this;
+  }
+  bool by(int bytes) const { return (bits & static_cast<uint64_t>(bytes - 1)) == 0; }
+};
 
 }  // namespace agg

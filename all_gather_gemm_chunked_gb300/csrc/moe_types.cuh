@@ -67,12 +67,17 @@ struct Elem<__nv_bfloat16> {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
+  // (a bfloat16 is the upper half of a float)
+  static __device__ __forceinline__ float2 unpair(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  }
   static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // a bfloat16 is the upper half of a float
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = unpair(w[i]);
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
     }
   }
   static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {

@@ -13,16 +13,20 @@
 // sums and everything between the loads and the stores are floats.  y is rounded once, to
 // the rows' type or to codes (put_codes).
 
+#include <type_traits>
+
 #include "layer_rows.cuh"
 
 namespace agg {
 
 namespace {
+constexpr int kSms = 152;
+
 // V weights, as they are loaded; floats or the rows' type.
 template <typename W, int V>
 struct Weights {
-  static constexpr int kN = V == 1 ? 1 : V / Elem<W>::kVec, kV = V == 1 ? 1 : Elem<W>::kVec;
-  Raw<W, kV> r[kN];
+  static constexpr int kV = V * sizeof(W) > 16 ? 16 / sizeof(W) : V == 2 && sizeof(W) == 4 ? 1 : V, kN = V / kV;
+  Piece<W, kV> r[kN];
   __device__ __forceinline__ void load(const W* p) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) r[i].load(p + i * kV);
@@ -38,28 +42,28 @@ struct Weights {
   }
 };
 
-// V elements of h, rounded, as they are stored.
+// h, rounded, in the place of x.  (Pairs of 16-bit elements are added as such: their sum in
+// floats is exact, or so far from a tie that rounding it once more gives the same.)
 template <typename T, int V>
-__device__ __forceinline__ void add_residual(Raw<T, V>& x, const Raw<T, V>& r) {
-  float a[V], b[V];
-  x.get(a);
-  r.get(b);
+__device__ __forceinline__ void add_residual(Piece<T, V>& x, const Piece<T, V>& r) {
+  if constexpr (sizeof(T) == 2 && V > 1) {
+    using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
 #pragma unroll
-  for (int v = 0; v < V; ++v) a[v] += b[v];
-  if constexpr (V == 1)
-    x.u = Elem<T>::put(a[0]);
-  else
-    x.u = Elem<T>::pack(a);
+    for (int i = 0; i < Piece<T, V>::kWords; ++i) {
+      const T2 s = __hadd2(reinterpret_cast<const T2&>(x.w[i]), reinterpret_cast<const T2&>(r.w[i]));
+      x.w[i] = reinterpret_cast<const uint32_t&>(s);
+    }
+  } else {
+    float a[V], b[V];
+    x.get(a);
+    r.get(b);
+#pragma unroll
+    for (int v = 0; v < V; ++v) a[v] += b[v];
+    x.put(a);
+  }
 }
 template <typename T, int V>
-__device__ __forceinline__ void store_raw(T* p, const Raw<T, V>& r) {
-  if constexpr (V == 1)
-    *p = r.u;
-  else
-    *reinterpret_cast<uint4*>(p) = r.u;
-}
-template <typename T, int V>
-__device__ __forceinline__ float squares(const Raw<T, V>& r, float scale, float sum) {
+__device__ __forceinline__ float squares(const Piece<T, V>& r, float scale, float sum) {
   float f[V];
   r.get(f);
 #pragma unroll
@@ -103,20 +107,23 @@ __device__ __forceinline__ float team_rstd(const NormArgs& a, int team_warps, fl
       eps = 0.0f;  // (eps 2^-160)
     }
   }
-  return scale * __frcp_rn(__fsqrt_rn(__fdiv_rn(sum, static_cast<float>(a.H)) + eps));
+  return scale * rsqrtf(fmaf(sum, a.inv_H, eps));
 }
 
 template <int OUT, typename T, int V>
-__device__ __forceinline__ void put_row(const NormArgs& a, int64_t row, int64_t c, bool in, const Raw<T, V>& h, float rstd,
-                                        const float (&w)[V]) {
+__device__ __forceinline__ void put_row(const NormArgs& a, int64_t row, int64_t c, bool in, const Piece<T, V>& h,
+                                        float rstd, const float (&w)[V]) {
   float f[V];
   h.get(f);
 #pragma unroll
-  for (int v = 0; v < V; ++v) f[v] = in ? f[v] * rstd * w[v] : 0.0f;
+  for (int v = 0; v < V; ++v) f[v] = f[v] * rstd * w[v];
   if constexpr (OUT == kTypeE4m3 || OUT == kTypeE2m1) {
+    if (!in)
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[v] = 0.0f;
     put_codes<OUT, V>(a.out, a.scales, a.rows, a.H, row, c, in, f);
   } else {
-    if (in) store_elems<T, V>(static_cast<T*>(a.out) + row * a.H + c, f);
+    if (in) store_floats(static_cast<T*>(a.out) + row * a.H + c, f);
   }
 }
 
@@ -127,46 +134,44 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int log) {
   __shared__ float part[2][32];
   const int team = 1 << log, thread = threadIdx.x & (team - 1);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> log) + (threadIdx.x >> log);
-  const bool valid = row < a.rows;
-  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-  const T* res = static_cast<const T*>(a.residual) + row * a.ldr;
-  Raw<T, V> h[P], r[P];
-  Weights<W, V> w[P];
+  const int c0 = thread * V, left = row < a.rows ? static_cast<int>(a.H) - c0 : 0;  // elements of the row from c0 on
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx + c0;
+  Piece<T, V> h[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int64_t c = static_cast<int64_t>(i * team + thread) * V;
-    h[i] = r[i] = Raw<T, V>{};
-    w[i] = Weights<W, V>{};
-    if (valid && c < a.H) {
-      h[i].load(x + c);
-      if (a.residual) r[i].load(res + c);
-    }
+    h[i] = Piece<T, V>{};
+    if (i * team * V < left) h[i].load(x + i * team * V);
   }
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int64_t c = static_cast<int64_t>(i * team + thread) * V;
-    if (valid && c < a.H) w[i].load(static_cast<const W*>(a.weight) + c);
-  }
-  if (a.residual)
+  if (a.residual) {
+    const T* res = static_cast<const T*>(a.residual) + row * a.ldr + c0;
+    Piece<T, V> r[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int64_t c = static_cast<int64_t>(i * team + thread) * V;
-      add_residual(h[i], r[i]);
-      if (valid && c < a.H) store_raw(static_cast<T*>(a.h) + row * a.H + c, h[i]);
+      r[i] = Piece<T, V>{};
+      if (i * team * V < left) r[i].load(res + i * team * V);
     }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      add_residual(h[i], r[i]);
+      if (i * team * V < left) h[i].store(static_cast<T*>(a.h) + row * a.H + c0 + i * team * V);
+    }
+  }
   const float rstd = team_rstd(a, team >> 5, part, [&](float scale) {
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < P; ++i) sum = squares(h[i], scale, sum);
     return sum;
   });
-  if (a.rstd && thread == 0 && valid) a.rstd[row] = rstd;
+  if (a.rstd && thread == 0 && left > 0) a.rstd[row] = rstd;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int64_t c = static_cast<int64_t>(i * team + thread) * V;
+    const bool in = i * team * V < left;
+    if (!__any_sync(0xffffffffu, in)) break;
+    Weights<W, V> w{};
+    if (in) w.load(static_cast<const W*>(a.weight) + c0 + i * team * V);
     float f[V];
-    w[i].get(f);
-    put_row<OUT>(a, row, c, valid && c < a.H, h[i], rstd, f);
+    w.get(f);
+    put_row<OUT>(a, row, c0 + i * team * V, in, h[i], rstd, f);
   }
 }
 
@@ -181,12 +186,12 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
   const float rstd = team_rstd(a, 32, part, [&](float scale) {
     float sum = 0.0f;
     for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < a.H; c += 1024 * V) {
-      Raw<T, V> v, r;
+      Piece<T, V> v, r;
       v.load(x + c);
       if (a.residual) {
         r.load(static_cast<const T*>(a.residual) + row * a.ldr + c);
         add_residual(v, r);
-        store_raw(h + c, v);
+        v.store(h + c);
       }
       sum = squares(v, scale, sum);
     }
@@ -197,7 +202,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
   const int64_t end = (a.H + 1024 * V - 1) / (1024 * V) * (1024 * V);  // (the lanes of a warp stay together)
   for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < end; c += 1024 * V) {
     const bool in = c < a.H;
-    Raw<T, V> v{};
+    Piece<T, V> v{};
     Weights<W, V> w{};
     float f[V];
     if (in) {
@@ -210,91 +215,125 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
 }
 
 // ------------------------------------------------------------------ gradient
-constexpr int kSms = 152;
-
-// Rows whose pieces fit a team of up to 1024 threads, one a thread.  A thread keeps its
-// columns from row to row, and their share of the weight's gradient in registers; a block
-// adds its teams' and stores one part.  The next row's loads are under way while this
-// one's sum goes through the team.
-template <typename T, typename W, int THREADS>
+// Rows whose pieces fit a team, P a thread.  A thread keeps its columns from row to row,
+// and their share of the weight's gradient in registers; a block adds its teams' and
+// stores one part.
+template <typename T, typename W, int V, int P, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 2) norm_backward_kernel(const NormBackwardArgs a, int log) {
   pdl_enter();
-  constexpr int V = Elem<T>::kVec;
+  // The next row's loads ahead of this one's sum, where registers allow.
+  constexpr bool kAhead = P * Piece<T, V>::kWords <= 4;
   __shared__ float part[2][32];
-  __shared__ float sums[THREADS == 1024 ? 1 : THREADS * V];
+  __shared__ float sums[THREADS == 1024 ? 1 : THREADS * V * P];
   const int team = 1 << log, thread = threadIdx.x & (team - 1), teams = THREADS >> log;
-  const int64_t c = static_cast<int64_t>(thread) * V, step = static_cast<int64_t>(gridDim.x) * teams;
-  const bool in = c < a.H;
-  const T *dy = static_cast<const T*>(a.dy) + c, *h = static_cast<const T*>(a.h) + c,
-          *dh = static_cast<const T*>(a.dh) + c;
-  float w[V], dw[V] = {};
-  {
-    Weights<W, V> r{};
-    if (in) r.load(static_cast<const W*>(a.weight) + c);
-    r.get(w);
+  const int c0 = thread * V;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+  const T *dy = static_cast<const T*>(a.dy) + c0, *h = static_cast<const T*>(a.h) + c0,
+          *dh = static_cast<const T*>(a.dh) + c0;
+  float dw[P][V] = {};
+  Weights<W, V> rw[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    rw[i] = Weights<W, V>{};
+    if (c0 + i * team * V < a.H) rw[i].load(static_cast<const W*>(a.weight) + c0 + i * team * V);
   }
   const float inv = 1.0f / static_cast<float>(a.H);
   const int64_t first = static_cast<int64_t>(blockIdx.x) * teams;
   int64_t row = first + (threadIdx.x >> log);
-  Raw<T, V> rg{}, rh{}, rd{};
+  Piece<T, V> rg[P], rh[P], rd[P];
   float rstd = 0.0f;
   auto load = [&] {
-    if (row < a.rows) {
-      rstd = a.rstd[row];
-      if (in) {
-        rg.load(dy + row * a.lddy);
-        rh.load(h + row * a.ldh);
-        if (a.dh) rd.load(dh + row * a.lddh);
+    const bool valid = row < a.rows;
+    if (valid) rstd = a.rstd[row];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int c = i * team * V;
+      rg[i] = rh[i] = rd[i] = Piece<T, V>{};
+      if (valid && c0 + c < a.H) {
+        rg[i].load(dy + row * a.lddy + c);
+        rh[i].load(h + row * a.ldh + c);
+        if (a.dh) rd[i].load(dh + row * a.lddh + c);
       }
     }
   };
-  load();
+  if (kAhead) load();
   int turn = 0;
   for (int64_t base = first; base < a.rows; base += step, turn ^= 1) {  // (all teams: they share a barrier)
-    float g[V], x[V], d[V];
-    rg.get(g);
-    rh.get(x);
-    rd.get(d);
+    if (!kAhead) load();
+    Piece<T, V> pg[P], ph[P], pd[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      pg[i] = rg[i];
+      ph[i] = rh[i];
+      pd[i] = rd[i];
+    }
     const float rs = rstd;
     const int64_t at = row;
-    row += step;
-    load();
-    float dot = 0.0f;
     const bool valid = at < a.rows;
+    row += step;
+    if (kAhead) load();
+    float dot = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      x[v] *= rs;
-      if (valid) dw[v] = fmaf(g[v], x[v], dw[v]);
-      g[v] *= w[v];
-      dot = fmaf(g[v], x[v], dot);
+    for (int i = 0; i < P; ++i) {
+      float g[V], x[V], w[V];
+      pg[i].get(g);
+      ph[i].get(x);
+      rw[i].get(w);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        x[v] *= rs;
+        if (valid) dw[i][v] = fmaf(g[v], x[v], dw[i][v]);
+        dot = fmaf(g[v] * w[v], x[v], dot);
+      }
     }
     dot = team_sum(dot, team >> 5, part[turn]) * inv;
-    if (valid && in) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) g[v] = fmaf(rs, fmaf(-x[v], dot, g[v]), a.dh ? d[v] : 0.0f);
-      store_elems<T, V>(static_cast<T*>(a.dx) + at * a.H + c, g);
+    for (int i = 0; i < P; ++i) {
+      const int c = i * team * V;
+      if (!valid || c0 + c >= a.H) continue;
+      float g[V], x[V], w[V], d[V];
+      pg[i].get(g);
+      ph[i].get(x);
+      rw[i].get(w);
+      pd[i].get(d);
+#pragma unroll
+      for (int v = 0; v < V; ++v) g[v] = fmaf(rs, fmaf(-x[v] * rs, dot, g[v] * w[v]), a.dh ? d[v] : 0.0f);
+      store_floats(static_cast<T*>(a.dx) + at * a.H + c0 + c, g);
     }
   }
   float* to = a.parts + static_cast<int64_t>(blockIdx.x) * a.H;
   if constexpr (THREADS != 1024) {
     if (teams > 1) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) sums[threadIdx.x * V + v] = dw[v];
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          sums[(threadIdx.x >> log) * (team * P * V) + i * team * V + c0 + v] = dw[i][v];
       __syncthreads();
-      for (int i = threadIdx.x; i < a.H; i += THREADS) {
+      for (int c = threadIdx.x; c < a.H; c += THREADS) {
         float s = 0.0f;
-        for (int t = 0; t < teams; ++t) s += sums[t * team * V + i];
-        to[i] = s;
+        for (int t = 0; t < teams; ++t) s += sums[t * (team * P * V) + c];
+        to[c] = s;
       }
       return;
     }
   }
-  if (in)
 #pragma unroll
-    for (int v = 0; v < V; v += 4) *reinterpret_cast<float4*>(to + c + v) = make_float4(dw[v], dw[v + 1], dw[v + 2], dw[v + 3]);
+  for (int i = 0; i < P; ++i) {
+    const int c = c0 + i * team * V;
+    if (c >= a.H) continue;
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+      for (int v = 0; v < V; v += 4)
+        *reinterpret_cast<float4*>(to + c + v) = make_float4(dw[i][v], dw[i][v + 1], dw[i][v + 2], dw[i][v + 3]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) to[c + v] = dw[i][v];
+    }
+  }
 }
 
-// Rows of any length and alignment: a block has a row, which it reads twice ...
+// Rows of any length: a block has a row, which it reads twice ...
 template <typename T, typename W, int V>
 __global__ void __launch_bounds__(512) norm_backward_long_kernel(const NormBackwardArgs a) {
   pdl_enter();
@@ -304,7 +343,7 @@ __global__ void __launch_bounds__(512) norm_backward_long_kernel(const NormBackw
   const float rs = a.rstd[row];
   float dot = 0.0f;
   for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < a.H; c += 512 * V) {
-    Raw<T, V> rg, rh;
+    Piece<T, V> rg, rh;
     Weights<W, V> rw;
     rg.load(dy + c);
     rh.load(h + c);
@@ -318,7 +357,7 @@ __global__ void __launch_bounds__(512) norm_backward_long_kernel(const NormBackw
   }
   dot = team_sum(dot, 16, part) / static_cast<float>(a.H);
   for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < a.H; c += 512 * V) {
-    Raw<T, V> rg, rh, rd{};
+    Piece<T, V> rg, rh, rd{};
     Weights<W, V> rw;
     rg.load(dy + c);
     rh.load(h + c);
@@ -331,7 +370,7 @@ __global__ void __launch_bounds__(512) norm_backward_long_kernel(const NormBackw
     rd.get(d);
 #pragma unroll
     for (int v = 0; v < V; ++v) g[v] = fmaf(rs, fmaf(-x[v] * rs, dot, g[v] * w[v]), a.dh ? d[v] : 0.0f);
-    store_elems<T, V>(static_cast<T*>(a.dx) + row * a.H + c, g);
+    store_floats(static_cast<T*>(a.dx) + row * a.H + c, g);
   }
 }
 // ... and the weight's gradient comes by columns, a thread for each, over a part of the rows.
@@ -388,45 +427,69 @@ cudaError_t with_types(int dtype, int weight_f32, const F& f) {
 }
 int size_of(int dtype) { return dtype == kTypeF32 ? 4 : 2; }
 
+template <typename T, typename W, int V, int P, int OUT>
+cudaError_t launch_norm_p(const NormArgs& a, int64_t pieces, cudaStream_t stream) {
+  const int log = team_log((pieces + P - 1) / P), threads = log < 7 ? 128 : 1 << log, per = threads >> log;
+  const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per));
+  return launch(norm_kernel<T, W, V, P, OUT>, grid, threads, stream, a, log);
+}
 template <typename T, typename W, int V, int OUT>
 cudaError_t launch_norm_v(const NormArgs& a, cudaStream_t stream) {
+  constexpr bool kVec = V * sizeof(T) == 16;
+  constexpr int kFew = kVec ? 1 : 4, kMost = kVec ? 4 : 8;
   const int64_t pieces = (a.H + V - 1) / V;
-  constexpr int kMost = V == 1 ? 8 : 4;
   if (pieces > 1024 * kMost)
     return launch(norm_long_kernel<T, W, V, OUT>, dim3(static_cast<unsigned>(a.rows)), 1024, stream, a);
-  // One piece a thread where rows are few, two where they are many.
-  const int p = pieces > 1024 * (kMost / 2) ? kMost : pieces > 1024 || a.rows > 2 * kSms ? kMost / 2 : 1;
-  const int log = team_log((pieces + p - 1) / p);
-  const int threads = log < 8 ? 256 : 1 << log, per = threads >> log;
-  const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per));
-  if (p == 1) return launch(norm_kernel<T, W, V, 1, OUT>, grid, threads, stream, a, log);
-  if (p == kMost / 2) return launch(norm_kernel<T, W, V, kMost / 2, OUT>, grid, threads, stream, a, log);
-  return launch(norm_kernel<T, W, V, kMost, OUT>, grid, threads, stream, a, log);
+  // Few rows are spread over more threads; of many, more of a row is in flight in a thread
+  // (8192 x 4096 bf16: 40.0 us with four pieces, 40.9 with two, without a residual 21.7 and
+  // 30.3; 64 x 7168 2.6 with one, 3.1 with two).  Rows of a few pieces have no more.
+  if (pieces > 1024 * kFew || (a.rows > 2 * kSms && pieces >= 32 * kMost)) return launch_norm_p<T, W, V, kMost, OUT>(a, pieces, stream);
+  return launch_norm_p<T, W, V, kFew, OUT>(a, pieces, stream);
 }
 
+// kWide: teams of 1024 threads (log 10) alone.
+template <typename T, typename W, int V, int P, bool kWide>
+cudaError_t launch_backward_p(const NormBackwardArgs& a, int log, int64_t& parts, cudaStream_t stream) {
+  const int64_t per = log == 10 ? 1 : 512 >> log, blocks = (a.rows + per - 1) / per;
+  const int64_t most = log == 10 ? kSms : kMaxParts;
+  parts = blocks < most ? blocks : most;
+  const dim3 grid(static_cast<unsigned>(parts));
+  if constexpr (!kWide)
+    if (log < 10) return launch(norm_backward_kernel<T, W, V, P, 512>, grid, 512, stream, a, log);
+  return launch(norm_backward_kernel<T, W, V, P, 1024>, grid, 1024, stream, a, log);
+}
 template <typename T, typename W, int V>
-cudaError_t launch_backward_long(const NormBackwardArgs& a, int64_t parts, cudaStream_t stream) {
+cudaError_t launch_backward_v(const NormBackwardArgs& a, int64_t& parts, cudaStream_t stream) {
+  constexpr bool kVec = V * sizeof(T) == 16;
+  constexpr int kFew = kVec ? 1 : 4, kMost = kVec ? 2 : 8;
+  const int64_t pieces = (a.H + V - 1) / V;
+  if (pieces <= 1024 * kFew)
+    return launch_backward_p<T, W, V, kFew, false>(a, team_log((pieces + kFew - 1) / kFew), parts, stream);
+  if (pieces <= 1024 * kMost) return launch_backward_p<T, W, V, kMost, true>(a, 10, parts, stream);
   cudaError_t e = launch(norm_backward_long_kernel<T, W, V>, dim3(static_cast<unsigned>(a.rows)), 512, stream, a);
   if (e != cudaSuccess) return e;
+  parts = norm_parts(a.rows, a.H);
   const int64_t part_rows = (a.rows + parts - 1) / parts;
   const dim3 grid(static_cast<unsigned>((a.H + kColumnThreads - 1) / kColumnThreads), static_cast<unsigned>(parts));
   return launch(norm_columns_kernel<T>, grid, kColumnThreads, stream, a, part_rows);
 }
 }  // namespace
 
-cudaError_t launch_norm(const NormArgs& a, int dtype, int out_type, cudaStream_t stream) {
+cudaError_t launch_norm(NormArgs a, int dtype, int out_type, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
+  a.inv_H = 1.0f / static_cast<float>(a.H);
   const int size = size_of(dtype);
-  const bool vec = vectors(a.x, a.ldx, size) && vectors(a.weight, 0, 1) && a.H * size % 16 == 0 &&
-                   (!a.residual || (vectors(a.residual, a.ldr, size) && vectors(a.h, a.H, size))) &&
-                   (out_type != dtype || vectors(a.out, a.H, size));
+  Access at;
+  at.rows(a.x, a.ldx, size).rows(a.weight, a.H, size).rows(a.out, a.H, out_type == dtype ? size : 16);
+  if (a.residual) at.rows(a.residual, a.ldr, size).rows(a.h, a.H, size);
   return with_types(dtype, a.weight_f32, [&](auto t, auto w) {
     using T = decltype(t);
     using W = decltype(w);
-    constexpr int V = Elem<T>::kVec;
+    constexpr int V = Elem<T>::kVec, V4 = 4 / sizeof(T);
     if (out_type == kTypeE4m3) return launch_norm_v<T, W, V, kTypeE4m3>(a, stream);
     if (out_type == kTypeE2m1) return launch_norm_v<T, W, V, kTypeE2m1>(a, stream);
-    return vec ? launch_norm_v<T, W, V, kTypeF32>(a, stream) : launch_norm_v<T, W, 1, kTypeF32>(a, stream);
+    if (at.by(16)) return launch_norm_v<T, W, V, kTypeF32>(a, stream);
+    return at.by(4) ? launch_norm_v<T, W, V4, kTypeF32>(a, stream) : launch_norm_v<T, W, 1, kTypeF32>(a, stream);
   });
 }
 
@@ -435,23 +498,15 @@ int64_t norm_parts(int64_t rows, int64_t) { return rows < kMaxParts ? rows : kMa
 cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, cudaStream_t stream) {
   if (a.rows == 0) return cudaMemsetAsync(a.dweight, 0, static_cast<size_t>(a.H) * 4, stream);
   const int size = size_of(dtype);
-  const bool vec = vectors(a.dy, a.lddy, size) && vectors(a.h, a.ldh, size) && vectors(a.weight, 0, 1) &&
-                   vectors(a.dx, a.H, size) && a.H * size % 16 == 0 && (!a.dh || vectors(a.dh, a.lddh, size));
-  int64_t parts = norm_parts(a.rows, a.H);
+  Access at;
+  at.rows(a.dy, a.lddy, size).rows(a.h, a.ldh, size).rows(a.weight, a.H, size).rows(a.dx, a.H, size).rows(a.dh, a.lddh, size);
+  int64_t parts = 0;
   const cudaError_t e = with_types(dtype, a.weight_f32, [&](auto t, auto w) {
     using T = decltype(t);
     using W = decltype(w);
-    constexpr int V = Elem<T>::kVec;
-    if (!vec) return launch_backward_long<T, W, 1>(a, parts, stream);
-    if (a.H > 1024 * V) return launch_backward_long<T, W, V>(a, parts, stream);
-    const int log = team_log(a.H / V);
-    if (log == 10) {
-      if (parts > kSms) parts = kSms;
-      return launch(norm_backward_kernel<T, W, 1024>, dim3(static_cast<unsigned>(parts)), 1024, stream, a, log);
-    }
-    const int64_t blocks = (a.rows + (512 >> log) - 1) / (512 >> log);
-    if (parts > blocks) parts = blocks;
-    return launch(norm_backward_kernel<T, W, 512>, dim3(static_cast<unsigned>(parts)), 512, stream, a, log);
+    constexpr int V = Elem<T>::kVec, V4 = 4 / sizeof(T);
+    if (at.by(16)) return launch_backward_v<T, W, V>(a, parts, stream);
+    return at.by(4) ? launch_backward_v<T, W, V4>(a, parts, stream) : launch_backward_v<T, W, 1>(a, parts, stream);
   });
   if (e != cudaSuccess) return e;
   return launch(norm_sum_kernel, dim3(static_cast<unsigned>((a.H + 31) / 32)), 32 * kSumWarps, stream, a.parts, parts,
