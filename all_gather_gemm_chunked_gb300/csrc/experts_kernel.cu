@@ -114,7 +114,7 @@ __host__ __device__ constexpr int out_buffer(int op) {
 }
 __host__ __device__ constexpr int out_bytes(int op) { return kXEpiWarps * out_buffer(op); }
 constexpr int kTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) & ~15;
-constexpr int kUnitBytes = kXEpiWarps * 48;  // the epilogue warps' units
+constexpr int kUnitBytes = kXEpiWarps * 64;  // the epilogue warps' units
 __host__ __device__ constexpr int smem_bytes(int op, int BN) {
   return stages_of(op, BN) * kSub * (kWBytes + r_bytes(BN)) + scale_bytes(op, BN) +
          out_bytes(op) + kTableBytes + kUnitBytes + 640 /*barriers*/ + 1024 /*alignment*/;
@@ -269,6 +269,7 @@ struct Unit {
   int32_t whole;     // and those that k-blocks may hold as they are: more where zeros follow
                      // (the inputs' last row) or the 16 rows of an MMA step end with the group
   int32_t tile, part;
+  int32_t parts, first;  // shares (below): parts of the tile's sum, the pair that has its first
 };
 static_assert(sizeof(Unit) <= kUnitBytes / kXEpiWarps, "an epilogue warp's unit");
 
@@ -325,11 +326,35 @@ __device__ __forceinline__ int32_t choose_split(int32_t tiles, int32_t KB, int32
   return static_cast<int32_t>(best & 31u) + 1;
 }
 
-// The units of a pair in order: unit i is number pair + i * pairs of the list.  A role
+// e2m1, short row tiles: instead, where it pays, every pair takes an equal share of the
+// stages of all tiles, which follow one another tile by tile, so that a tile's sum is cut
+// wherever a pair's share ends.  (An SM takes in about 50 GB/s of what is not in L2, so
+// weights stream at the memory's rate only where all of them read: 64 rows of 16384 x 7168,
+// 28 tiles, in two parts each 20.8 us.)  Lanes 0 to 15 try shares of a tile's stages over 1
+// to 16, lane 16 the least.  Returns the share, 0 for whole tiles in rounds.
+__device__ __forceinline__ int32_t choose_share(int32_t tiles, int32_t stages, int32_t max_units, SplitPrice price) {
+  const int32_t pairs = static_cast<int32_t>(gridDim.x / 2);
+  if (tiles == 0 || tiles >= 2 * pairs || max_units < 2 * pairs) return 0;
+  const int32_t lane = static_cast<int32_t>(threadIdx.x & 31), least = (tiles * stages + pairs - 1) / pairs;
+  const int32_t share = lane < 16 ? (stages + lane) / (lane + 1) : least;
+  const int32_t parts = (stages + share - 1) / share + (stages % share != 0 ? 1 : 0);
+  const int32_t rounds = (tiles + pairs - 1) / pairs;
+  uint32_t cost = 0x01ffffffu;
+  if (lane == 17)
+    cost = static_cast<uint32_t>(rounds * (kSub * stages + 6));
+  else if (lane < 17 && share >= least && share >= kMinPart / kSub)
+    cost = static_cast<uint32_t>(kSub * share + 6 * ((share + stages - 1) / stages) + price.once + parts * price.part);
+  const uint32_t best = __reduce_min_sync(0xffffffffu, min(cost, 0x01ffffffu) * 32 + lane) & 31u;
+  return __shfl_sync(0xffffffffu, lane == 17 ? 0 : share, static_cast<int>(best));
+}
+
+// The units of a pair in order: unit i is number pair + i * pairs of the list (with shares:
+// its part of the i-th tile that its share reaches).  A role
 // asks for them one after the other.  (Cheap to make: the epilogue makes it anew for
 // each tile, so that nothing of it takes registers while sums are added.)
 template <int OP, int BN>
 struct Schedule {
+  static constexpr bool kShares = OP == kOpFp4 && BN == kXFewRows;
   const ExpertsParams& p;
   const int32_t* off;
   const int32_t* pre;
@@ -359,6 +384,15 @@ struct Schedule {
                                                    int32_t* head) {
     if (OP == kOpWeight) tiles = p.E * row_tiles(p);
     tiles *= wide_tiles(p);
+    if constexpr (kShares) {
+      const int32_t share = choose_share(tiles, (k_blocks(p) + kSub - 1) / kSub, p.max_units, split_price(OP, true));
+      if ((threadIdx.x & 31) == 0) {
+        head[0] = share;
+        head[1] = static_cast<int32_t>(share > 1 ? 0xffffffffu / static_cast<uint32_t>(share) : 0xffffffffu);
+        head[2] = tiles;
+      }
+      return;
+    }
     const int32_t split = choose_split(tiles, OP == kOpWeight ? longest / 64 : k_blocks(p), p.max_units,
                                        split_price(OP, OP == kOpWeight ? p.step < kXRows : BN == kXFewRows));
     if ((threadIdx.x & 31) == 0) {
@@ -410,14 +444,28 @@ struct Schedule {
   }
 
   __device__ __forceinline__ bool get(int32_t i, Unit& u) {
-    const int64_t id = static_cast<int64_t>(i) * pairs + pair;
-    if (id >= units) return false;
-    const uint32_t unit = static_cast<uint32_t>(id);
     int32_t x, row_tile;
     uint32_t part = 0;
-    u.tile = static_cast<int32_t>(unit);
-    if (split > 1) u.tile = static_cast<int32_t>(by_split.div(unit, part));
-    u.part = static_cast<int32_t>(part);
+    [[maybe_unused]] int32_t begin = 0, end = 0;  // shares: stages of the tile
+    if (kShares && split > 0) {
+      const int32_t stages = (KB + kSub - 1) / kSub, s0 = pair * split;  // (below 152 * 32768)
+      uint32_t rest;
+      u.tile = static_cast<int32_t>(Divisor(static_cast<uint32_t>(stages), p.inv_stages).div(static_cast<uint32_t>(s0), rest)) + i;
+      const int32_t t0 = u.tile * stages;
+      begin = (s0 > t0 ? s0 : t0) - t0;
+      end = (s0 + split < t0 + stages ? s0 + split : t0 + stages) - t0;
+      if (u.tile >= units || begin >= end) return false;
+      u.first = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(t0), rest));
+      u.parts = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(t0 + stages - 1), rest)) - u.first + 1;
+      u.part = pair - u.first;
+    } else {
+      const int64_t id = static_cast<int64_t>(i) * pairs + pair;
+      if (id >= units) return false;
+      u.tile = static_cast<int32_t>(id);
+      if (!kShares && split > 1) u.tile = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(id), part));
+      u.part = static_cast<int32_t>(part);
+      u.parts = 1;
+    }
     int32_t blocks = KB;  // k-blocks of the whole sum
     if constexpr (OP == kOpWeight) {
       uint32_t r;
@@ -447,7 +495,12 @@ struct Schedule {
     }
     u.kb0 = 0;
     u.kb1 = blocks;
-    if (split > 1) {
+    if (kShares) {
+      if (split > 0) {
+        u.kb0 = begin * kSub;
+        u.kb1 = end * kSub < blocks ? end * kSub : blocks;
+      }
+    } else if (split > 1) {
       uint32_t rest;
       u.kb0 = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(blocks * u.part), rest));
       u.kb1 = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(blocks * (u.part + 1)), rest));
@@ -1125,8 +1178,9 @@ __device__ __forceinline__ void store_zeros(const ExpertsParams& p, int64_t at, 
 }
 
 // The sum of a split tile's parts for 8 columns, in the order of the parts, the loads of
-// four parts in flight.
-__device__ __forceinline__ void add_parts(const float* first, int64_t next, int32_t parts, float (&v)[8]) {
+// four parts in flight.  The first part is at `first`, part s at others + s * next.
+__device__ __forceinline__ void add_parts(const float* first, const float* others, int64_t next, int32_t parts,
+                                          float (&v)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = 0.0f;
   for (int32_t s0 = 0; s0 < parts; s0 += 4) {
@@ -1134,7 +1188,8 @@ __device__ __forceinline__ void add_parts(const float* first, int64_t next, int3
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[u][j] = s0 + u < parts ? __ldcg(first + (s0 + u) * next + j * 32) : 0.0f;
+      for (int j = 0; j < 8; ++j)
+        x[u][j] = s0 + u < parts ? __ldcg((s0 + u == 0 ? first : others + (s0 + u) * next) + j * 32) : 0.0f;
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (s0 + u < parts)
@@ -1272,7 +1327,7 @@ __device__ void epilogue_long(const ExpertsParams& p, const Table& table,
     if (last_part<kWarps>(p, u, split, rank, ew, lane))
       for (int c = 0; c < n; ++c) {
         float v[8];
-        add_parts(first + c * 8 * 32, kNext, split, v);
+        add_parts(first + c * 8 * 32, first + c * 8 * 32, kNext, split, v);
         if (row < u.cnt) store_row8(p.out, p.out_type, at + c * 8, v);
       }
   }
@@ -1374,7 +1429,8 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
     // 206 us, so 194; e4m3 of 4085 rows, 47 experts of 784 x 2664, 47.8 and 43.5.)
     __syncwarp();
     const Unit u = ring.units[ew];
-    const int32_t split = table.head[0];
+    constexpr bool kShares = Schedule<OP, BN>::kShares;
+    const int32_t split = kShares ? u.parts : table.head[0];
     const int n8 = u.w / 32, c_first = quarter * n8 * 8;
     const int32_t col = u.n0 + static_cast<int32_t>(rank) * 128 + quad * 32;
     const Out<out_buffer(OP)> out{p.out, p.ldo,
@@ -1397,10 +1453,14 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
     // this warp's part, [columns][32 lanes]; the warp that comes last adds the parts,
     // in their order
     constexpr int64_t kSlab = static_cast<int64_t>(kCols) * 32;
-    constexpr int64_t kNext = 2 * kXEpiWarps * kSlab;
-    float* first = p.partials +
-                   ((static_cast<int64_t>(u.tile) * split * 2 + rank) * kXEpiWarps + ew) * kSlab + lane;
-    float* part = first + u.part * kNext;
+    constexpr int64_t kUnit = 2 * kXEpiWarps * kSlab;
+    // Shares: a pair has two places, one for a part that begins a tile's sum and one for
+    // another, of which it has at most one each.
+    constexpr int64_t kNext = kShares ? 2 * kUnit : kUnit;
+    float* others = p.partials + (rank * kXEpiWarps + ew) * kSlab + lane +
+                    (kShares ? u.first * kNext : static_cast<int64_t>(u.tile) * split * kUnit);
+    float* first = kShares ? others + kUnit : others;
+    float* part = u.part == 0 ? first : others + u.part * kNext;
 #pragma unroll
     for (int c = 0; c < kCols / 8; ++c)
       if (c < n8) {
@@ -1412,7 +1472,7 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
     if (last_part<kXEpiWarps>(p, u, split, rank, ew, lane))
       for (int c = 0; c < n8; ++c) {
         float v[8];
-        add_parts(first + c * 8 * 32, kNext, split, v);
+        add_parts(first + c * 8 * 32, others + c * 8 * 32, kNext, split, v);
         out.store(c_first + c * 8, v, lane);
       }
   }

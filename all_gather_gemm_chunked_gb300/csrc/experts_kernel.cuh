@@ -50,6 +50,7 @@ struct ExpertsParams {
   int32_t out_rows;              // weight gradient: output rows per expert (K)
   int32_t step, row_tiles;       // weight gradient: output rows of a tile, 256 or 128; tiles of K
   uint32_t inv_group, inv_expert;  // floor((2^32 - 1) / n): n tiles of 8 row tiles, n of an expert (weight gradient)
+  uint32_t inv_stages;           // e2m1: the same of the stages of a sum
   int32_t w_blk, r_blk;          // operand described in blocks of 128 bytes (one load a stage), or not (two)
   int32_t segment;               // k-blocks per accumulator (e4m3: 1)
   int32_t bf16;                  // operands are bfloat16 (otherwise fp16)
@@ -81,7 +82,7 @@ struct SplitPrice {
 __host__ __device__ constexpr SplitPrice split_price(int op, bool short_tiles) {
   return op == kOpFp8 ? SplitPrice{9, 1}
          : op == kOpFp8Long ? SplitPrice{9, 3}
-         : op == kOpFp4 ? SplitPrice{9, short_tiles ? 1 : 3}
+         : op == kOpFp4 ? SplitPrice{short_tiles ? 7 : 9, short_tiles ? 1 : 3}
          : op == kOpWeight ? SplitPrice{14, short_tiles ? 3 : 5}  // half tiles, whole ones
                            : SplitPrice{14, short_tiles ? 2 : 5};
 }

@@ -274,6 +274,7 @@ int run(ag_moe_plan* p, agg::ExpertsParams& x, int op, bool few, int64_t row_til
   const bool fp8 = op == agg::kOpFp8;
   const int block_k = op == agg::kOpFp4 ? 256 : fp8 ? 128 : 64;
   const int64_t kb = op == agg::kOpWeight ? x.rows / 64 : (x.red + block_k - 1) / block_k;
+  x.inv_stages = 0xffffffffu / static_cast<uint32_t>((kb + agg::kXSub - 1) / agg::kXSub < 1 ? 1 : (kb + agg::kXSub - 1) / agg::kXSub);
   // (where the tiles' number does not depend on offsets, two rounds of them never split)
   const bool plenty = (op == agg::kOpWeight || !x.offsets) && (row_tiles - 1) * wide_tiles >= 2 * p->pairs;
   const bool split = !plenty && may_split(kb, agg::split_price(fp8 && !few ? agg::kOpFp8Long : op,

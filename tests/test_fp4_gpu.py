@@ -112,6 +112,10 @@ SHAPES = [
     ([700], 640, 136),
     ([16] * 33, 160, 328),
     ([5], 16384, 640),
+    ([64], 8192, 4096),               # sums cut between pairs, across tiles too
+    ([1] * 5, 4096, 768),
+    ([10, 0, 40, 65], 16384, 520),
+    ([17] * 9, 4640, 2560),           # more tiles than pairs, less than twice as many
     ([2000], 1088, 2312),
 ]
 
