@@ -592,6 +592,43 @@ __device__ __forceinline__ void load_k(uint8_t* dst, const CUtensorMap* map, uin
   }
 }
 
+// The same loads as prefetches into L2.
+__device__ __forceinline__ void prefetch_k(const CUtensorMap* map, int32_t blk, int32_t kb, int32_t bk, int32_t row, int32_t e) {
+  if (blk) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(kb), "r"(e) : "memory");
+  } else {
+    for (int s = 0; s < kSub; ++s)
+      asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                       reinterpret_cast<uint64_t>(map)), "r"((kb + s) * bk), "r"(row), "r"(e) : "memory");
+  }
+}
+// Before the wait for the kernel before: this CTA's first weights into L2, where they are
+// known without the offsets (one expert whose rows are all of them; where the offsets say
+// otherwise, other weights are read).  In a step of a model that kernel makes the rows, and
+// the memory has little to do meanwhile.  (A prefetch is no read: what that kernel may still
+// write of the weights is seen by the loads behind the wait.)
+template <int OP, int BN>
+__device__ void prefetch_weights(const ExpertsParams& p, uint32_t rank) {
+  const int32_t KB = Schedule<OP, BN>::k_blocks(p), stages = (KB + kSub - 1) / kSub, wt = Schedule<OP, BN>::wide_tiles(p);
+  const int32_t nt = (p.rows - 1) / BN + 1, tiles = nt * wt, pair = static_cast<int32_t>(blockIdx.x / 2);
+  const int32_t share = choose_share(tiles, stages, p.max_units, split_price(OP, true));
+  const int32_t tile = share > 0 ? pair * share / stages : pair, first = share > 0 ? pair * share - tile * stages : 0;
+  if (tile >= tiles) return;
+  const int32_t group = tile / (kXGroup * wt), gw = nt - group * kXGroup < kXGroup ? nt - group * kXGroup : kXGroup;
+  const int32_t n = (tile - group * kXGroup * wt) / gw * kXWide + static_cast<int32_t>(rank) * 128;
+  int32_t count = stages - first < stages_of(OP, BN) ? stages - first : stages_of(OP, BN);
+  if (share > 0 && share < count) count = share;
+  if (n < p.wide && elect_one())
+    for (int32_t s = 0; s < count; ++s) {
+      const int32_t kb = (first + s) * kSub;
+      prefetch_k(&p.tm_w, p.w_blk, kb, 128, n, 0);
+      asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                       reinterpret_cast<uint64_t>(&p.tm_s)), "r"(kb * (2 * kPiece / 8)), "r"(n / 128) : "memory");
+    }
+  __syncwarp();
+}
+
 // Box height of the row operand's loads (rows of a CTA, rounded up to its four sizes).
 template <int BN>
 __device__ __forceinline__ int32_t box_of(int32_t half) {
@@ -1552,6 +1589,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   if (OP == kOpFp4 && warp == 4 && lane == 0) tma_prefetch_desc(&p.tm_s);
   tc_fence_before();
   cluster_arrive();  // barriers initialised, TMEM allocated; the table is read meanwhile
+  if constexpr (Schedule<OP, BN>::kShares)
+    if (warp == 0 && p.E == 1) prefetch_weights<OP, BN>(p, rank);
   pdl_wait();        // from here on global memory is read
   const bool valid = load_table<OP, BN>(p, off, pre, head, flag);
   cluster_wait();
