@@ -326,6 +326,14 @@ __device__ __forceinline__ int32_t choose_split(int32_t tiles, int32_t KB, int32
   return static_cast<int32_t>(best & 31u) + 1;
 }
 
+// n / d for n below 2^24 (exact in a float), by its approximate quotient and one correction:
+// a hardware division takes about a hundred cycles, and choose_share has six.
+__device__ __forceinline__ int32_t quotient(int32_t n, int32_t d) {
+  int32_t q = __float2int_rz(__fdividef(static_cast<float>(n), static_cast<float>(d)));
+  const int32_t rest = n - q * d;
+  return rest < 0 ? q - 1 : rest >= d ? q + 1 : q;
+}
+
 // e2m1, short row tiles: instead, where it pays, every pair takes an equal share of the
 // stages of all tiles, which follow one another tile by tile, so that a tile's sum is cut
 // wherever a pair's share ends.  (An SM takes in about 50 GB/s of what is not in L2, so
@@ -335,15 +343,17 @@ __device__ __forceinline__ int32_t choose_split(int32_t tiles, int32_t KB, int32
 __device__ __forceinline__ int32_t choose_share(int32_t tiles, int32_t stages, int32_t max_units, SplitPrice price) {
   const int32_t pairs = static_cast<int32_t>(gridDim.x / 2);
   if (tiles == 0 || tiles >= 2 * pairs || max_units < 2 * pairs) return 0;
-  const int32_t lane = static_cast<int32_t>(threadIdx.x & 31), least = (tiles * stages + pairs - 1) / pairs;
-  const int32_t share = lane < 16 ? (stages + lane) / (lane + 1) : least;
-  const int32_t parts = (stages + share - 1) / share + (stages % share != 0 ? 1 : 0);
-  const int32_t rounds = (tiles + pairs - 1) / pairs;
+  // (numerators up to 152 * 32768)
+  const int32_t lane = static_cast<int32_t>(threadIdx.x & 31), least = quotient(tiles * stages + pairs - 1, pairs);
+  const int32_t share = lane < 16 ? quotient(stages + lane, lane + 1) : least;
+  const int32_t whole = quotient(stages, share);
+  const int32_t parts = whole + (whole * share != stages ? 2 : 0);
+  const int32_t rounds = tiles > pairs ? 2 : 1;
   uint32_t cost = 0x01ffffffu;
   if (lane == 17)
     cost = static_cast<uint32_t>(rounds * (kSub * stages + 6));
   else if (lane < 17 && share >= least && share >= kMinPart / kSub)
-    cost = static_cast<uint32_t>(kSub * share + 6 * ((share + stages - 1) / stages) + price.once + parts * price.part);
+    cost = static_cast<uint32_t>(kSub * share + 6 * (share > stages ? 2 : 1) + price.once + parts * price.part);
   const uint32_t best = __reduce_min_sync(0xffffffffu, min(cost, 0x01ffffffu) * 32 + lane) & 31u;
   return __shfl_sync(0xffffffffu, lane == 17 ? 0 : share, static_cast<int>(best));
 }
