@@ -161,6 +161,26 @@ def test_whole_numbers_are_exact(rows):
     assert torch.equal(y.double(), row_values(xq, xs) @ weight_values(wq[None], ws[None])[0].t())
 
 
+@pytest.mark.parametrize("K,rows", [(1 << 21, 5), (1 << 19, 300)])
+def test_long_sums(K, rows):
+    """Positive terms into 16-bit outputs: an accumulator takes at most 128 k-blocks of four additions, each off by up to
+    2^-23 of the running sum; the sums of up to 64 accumulators are added to nearest."""
+    g = rng(2)
+    N = 264
+    x, w = (torch.rand((rows, K), generator=g, device="cuda") + 0.1).half(), torch.rand((K, N), generator=g, device="cuda").half()
+    (xq, xs), (wq, ws) = fp4.quantize_rows(x), fp4.quantize_weights(w)
+    del x, w
+    with fp4.Fp4Linear(K, N) as p:
+        y = p.forward(xq, xs, wq, ws, out_dtype=torch.bfloat16)
+        assert p.status() == B_.OK
+    ref = torch.zeros((rows, N), dtype=torch.float64, device="cuda")
+    for a in range(0, K, 1 << 15):
+        b = a + (1 << 15)
+        xd = row_values(xq[:, a // 2:b // 2], xs[a // 128:b // 128])
+        ref += xd @ weight_values(wq[None, :, a // 2:b // 2], ws[None, :, a // 128:b // 128])[0].t()
+    check(y, ref, ((512 + 64) * 2.0 ** -23 + 1.01 * U[torch.bfloat16]) * ref)
+
+
 def test_far_scales():
     """Scales of 2^-90 and 2^80 beside one another: a product of values is their product."""
     K, N, rows = 64, 8, 40

@@ -84,6 +84,21 @@ def test_special_values():
     assert float(zero.rstd[0]) == float("inf") and bool(torch.isnan(zero.y).all())
 
 
+def test_sums_past_the_largest_float():
+    """Rows of large elements beside others, several teams in a block and rows that are read twice: no row's squares spill
+    over into another's."""
+    for T, H in ((50, 64), (40, 512), (310, 2048), (3, 40000)):
+        x, w = randn(rng(H), (T, H)), torch.ones(H, device="cuda")
+        x[::3] *= 1e25
+        r = norm.rms_norm(x, w, 1e-6)
+        _, rstd, y = forward_ref(x, None, w, 1e-6)
+        check(r.rstd, rstd, forward_error(H) * rstd, "rstd")
+        check(r.y, y, (forward_error(H) + 1.01 * F) * y.abs(), "y")
+        dy = randn(rng(H + 1), (T, H))
+        dx, dw = norm.rms_norm_backward(dy, r.h, w, r.rstd)
+        backward_check(dx, dw, dy, r.h, w, r.rstd, None)
+
+
 def backward_check(dx, dw, dy, h, w, rstd, dh):
     T, H = dy.shape
     g, xh = dy.double() * w.double(), h.double() * rstd.double()[:, None]
