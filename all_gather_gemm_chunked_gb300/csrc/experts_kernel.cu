@@ -114,7 +114,7 @@ __host__ __device__ constexpr int out_buffer(int op) {
 }
 __host__ __device__ constexpr int out_bytes(int op) { return kXEpiWarps * out_buffer(op); }
 constexpr int kTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) & ~15;
-constexpr int kUnitBytes = kXEpiWarps * 64;  // the epilogue warps' units
+constexpr int kUnitBytes = kXEpiWarps * 48;  // the epilogue warps' units
 __host__ __device__ constexpr int smem_bytes(int op, int BN) {
   return stages_of(op, BN) * kSub * (kWBytes + r_bytes(BN)) + scale_bytes(op, BN) +
          out_bytes(op) + kTableBytes + kUnitBytes + 640 /*barriers*/ + 1024 /*alignment*/;
@@ -269,7 +269,6 @@ struct Unit {
   int32_t whole;     // and those that k-blocks may hold as they are: more where zeros follow
                      // (the inputs' last row) or the 16 rows of an MMA step end with the group
   int32_t tile, part;
-  int32_t parts, first;  // shares (below): parts of the tile's sum, the pair that has its first
 };
 static_assert(sizeof(Unit) <= kUnitBytes / kXEpiWarps, "an epilogue warp's unit");
 
@@ -453,29 +452,52 @@ struct Schedule {
     height = OP == kOpFp8Long ? BN : static_cast<int32_t>((most + 31u) & ~31u);
   }
 
+  // Shares: the pairs that hold parts of a tile's sum are `first` and the parts - 1 behind it.
+  __device__ __forceinline__ int32_t stages() const { return (KB + kSub - 1) / kSub; }
+  __device__ __forceinline__ void cuts(int32_t tile, int32_t& first, int32_t& parts) const {
+    uint32_t rest;
+    const int32_t t0 = tile * stages();
+    first = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(t0), rest));
+    parts = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(t0 + stages() - 1), rest)) - first + 1;
+  }
+  __device__ __forceinline__ bool get_shared(int32_t i, Unit& u) {
+    const int32_t s0 = pair * split;  // (stages in all: below 152 * 32768)
+    uint32_t rest;
+    const int32_t tile =
+        static_cast<int32_t>(Divisor(static_cast<uint32_t>(stages()), p.inv_stages).div(static_cast<uint32_t>(s0), rest)) + i;
+    const int32_t t0 = tile * stages(), begin = s0 > t0 ? s0 - t0 : 0;
+    const int32_t end = s0 + split - t0 < stages() ? s0 + split - t0 : stages();
+    if (tile >= units || begin >= end) return false;
+    if (e < 0 || tile >= tile0 + nt * wt) enter(tile);
+    int32_t x, row_tile, first, parts;
+    place(static_cast<uint32_t>(tile - tile0), nt, x, row_tile);
+    cuts(tile, first, parts);
+    const int32_t left = off[e + 1] - off[e] - row_tile * height;
+    u.e = e;
+    u.row0 = off[e] + row_tile * height;
+    u.cnt = left < height ? left : height;
+    u.w = height;
+    u.n0 = x * kXWide;
+    u.kt0 = u.red_rows = u.whole = 0;
+    u.kb0 = begin * kSub;
+    u.kb1 = end * kSub < KB ? end * kSub : KB;
+    u.tile = tile;
+    u.part = pair - first;
+    return true;
+  }
+
   __device__ __forceinline__ bool get(int32_t i, Unit& u) {
+    if constexpr (kShares) {
+      if (split > 0) return get_shared(i, u);
+    }
+    const int64_t id = static_cast<int64_t>(i) * pairs + pair;
+    if (id >= units) return false;
+    const uint32_t unit = static_cast<uint32_t>(id);
     int32_t x, row_tile;
     uint32_t part = 0;
-    [[maybe_unused]] int32_t begin = 0, end = 0;  // shares: stages of the tile
-    if (kShares && split > 0) {
-      const int32_t stages = (KB + kSub - 1) / kSub, s0 = pair * split;  // (below 152 * 32768)
-      uint32_t rest;
-      u.tile = static_cast<int32_t>(Divisor(static_cast<uint32_t>(stages), p.inv_stages).div(static_cast<uint32_t>(s0), rest)) + i;
-      const int32_t t0 = u.tile * stages;
-      begin = (s0 > t0 ? s0 : t0) - t0;
-      end = (s0 + split < t0 + stages ? s0 + split : t0 + stages) - t0;
-      if (u.tile >= units || begin >= end) return false;
-      u.first = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(t0), rest));
-      u.parts = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(t0 + stages - 1), rest)) - u.first + 1;
-      u.part = pair - u.first;
-    } else {
-      const int64_t id = static_cast<int64_t>(i) * pairs + pair;
-      if (id >= units) return false;
-      u.tile = static_cast<int32_t>(id);
-      if (!kShares && split > 1) u.tile = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(id), part));
-      u.part = static_cast<int32_t>(part);
-      u.parts = 1;
-    }
+    u.tile = static_cast<int32_t>(unit);
+    if (!kShares && split > 1) u.tile = static_cast<int32_t>(by_split.div(unit, part));
+    u.part = static_cast<int32_t>(part);
     int32_t blocks = KB;  // k-blocks of the whole sum
     if constexpr (OP == kOpWeight) {
       uint32_t r;
@@ -505,12 +527,7 @@ struct Schedule {
     }
     u.kb0 = 0;
     u.kb1 = blocks;
-    if (kShares) {
-      if (split > 0) {
-        u.kb0 = begin * kSub;
-        u.kb1 = end * kSub < blocks ? end * kSub : blocks;
-      }
-    } else if (split > 1) {
+    if (!kShares && split > 1) {
       uint32_t rest;
       u.kb0 = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(blocks * u.part), rest));
       u.kb1 = static_cast<int32_t>(by_split.div(static_cast<uint32_t>(blocks * (u.part + 1)), rest));
@@ -1225,9 +1242,26 @@ __device__ __forceinline__ void store_zeros(const ExpertsParams& p, int64_t at, 
 }
 
 // The sum of a split tile's parts for 8 columns, in the order of the parts, the loads of
-// four parts in flight.  The first part is at `first`, part s at others + s * next.
-__device__ __forceinline__ void add_parts(const float* first, const float* others, int64_t next, int32_t parts,
-                                          float (&v)[8]) {
+// four parts in flight.
+__device__ __forceinline__ void add_parts(const float* first, int64_t next, int32_t parts, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  for (int32_t s0 = 0; s0 < parts; s0 += 4) {
+    float x[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[u][j] = s0 + u < parts ? __ldcg(first + (s0 + u) * next + j * 32) : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (s0 + u < parts)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += x[u][j];
+  }
+}
+
+// The same where part s > 0 is 2 s - 1 places behind the first (shares).
+__device__ __forceinline__ void add_shares(const float* first, int64_t next, int32_t parts, float (&v)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = 0.0f;
   for (int32_t s0 = 0; s0 < parts; s0 += 4) {
@@ -1236,7 +1270,7 @@ __device__ __forceinline__ void add_parts(const float* first, const float* other
     for (int u = 0; u < 4; ++u)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        x[u][j] = s0 + u < parts ? __ldcg((s0 + u == 0 ? first : others + (s0 + u) * next) + j * 32) : 0.0f;
+        x[u][j] = s0 + u < parts ? __ldcg(first + (s0 + u == 0 ? 0 : 2 * (s0 + u) - 1) * next + j * 32) : 0.0f;
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (s0 + u < parts)
@@ -1374,7 +1408,7 @@ __device__ void epilogue_long(const ExpertsParams& p, const Table& table,
     if (last_part<kWarps>(p, u, split, rank, ew, lane))
       for (int c = 0; c < n; ++c) {
         float v[8];
-        add_parts(first + c * 8 * 32, first + c * 8 * 32, kNext, split, v);
+        add_parts(first + c * 8 * 32, kNext, split, v);
         if (row < u.cnt) store_row8(p.out, p.out_type, at + c * 8, v);
       }
   }
@@ -1476,8 +1510,15 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
     // 206 us, so 194; e4m3 of 4085 rows, 47 experts of 784 x 2664, 47.8 and 43.5.)
     __syncwarp();
     const Unit u = ring.units[ew];
+    // (shares: the parts of this tile's sum, not of every one's)
     constexpr bool kShares = Schedule<OP, BN>::kShares;
-    const int32_t split = kShares ? u.parts : table.head[0];
+    int32_t split = table.head[0], holder = 0;
+    if constexpr (kShares) {
+      if (split > 0)
+        Schedule<OP, BN>(p, table).cuts(u.tile, holder, split);
+      else
+        split = 1;
+    }
     const int n8 = u.w / 32, c_first = quarter * n8 * 8;
     const int32_t col = u.n0 + static_cast<int32_t>(rank) * 128 + quad * 32;
     const Out<out_buffer(OP)> out{p.out, p.ldo,
@@ -1500,14 +1541,19 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
     // this warp's part, [columns][32 lanes]; the warp that comes last adds the parts,
     // in their order
     constexpr int64_t kSlab = static_cast<int64_t>(kCols) * 32;
-    constexpr int64_t kUnit = 2 * kXEpiWarps * kSlab;
-    // Shares: a pair has two places, one for a part that begins a tile's sum and one for
-    // another, of which it has at most one each.
-    constexpr int64_t kNext = kShares ? 2 * kUnit : kUnit;
-    float* others = p.partials + (rank * kXEpiWarps + ew) * kSlab + lane +
-                    (kShares ? u.first * kNext : static_cast<int64_t>(u.tile) * split * kUnit);
-    float* first = kShares ? others + kUnit : others;
-    float* part = u.part == 0 ? first : others + u.part * kNext;
+    constexpr int64_t kNext = 2 * kXEpiWarps * kSlab;
+    float* first;
+    float* part;
+    if constexpr (kShares) {
+      // Pair q has place 2 q for the first part of a sum, with which its share may end, and
+      // place 2 q - 1 for another part, with which it may begin.
+      first = p.partials + (((2 * static_cast<int64_t>(holder)) * 2 + rank) * kXEpiWarps + ew) * kSlab + lane;
+      part = first + (u.part == 0 ? 0 : 2 * u.part - 1) * kNext;
+    } else {
+      first = p.partials +
+              ((static_cast<int64_t>(u.tile) * split * 2 + rank) * kXEpiWarps + ew) * kSlab + lane;
+      part = first + u.part * kNext;
+    }
 #pragma unroll
     for (int c = 0; c < kCols / 8; ++c)
       if (c < n8) {
@@ -1519,7 +1565,10 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table,
     if (last_part<kXEpiWarps>(p, u, split, rank, ew, lane))
       for (int c = 0; c < n8; ++c) {
         float v[8];
-        add_parts(first + c * 8 * 32, others + c * 8 * 32, kNext, split, v);
+        if constexpr (kShares)
+          add_shares(first + c * 8 * 32, kNext, split, v);
+        else
+          add_parts(first + c * 8 * 32, kNext, split, v);
         out.store(c_first + c * 8, v, lane);
       }
   }

@@ -26,7 +26,8 @@ constexpr int kXRows4 = 224;   // e2m1: up to 224 (two accumulators of 224 leave
 constexpr int kXRowBoxes = 4;  // box heights of the row operand: a quarter of half a tile, in whole 8 rows, to all of it
 __host__ __device__ constexpr int box_step(int tile_rows) { return (tile_rows / 8 + 7) / 8 * 8; }
 __host__ __device__ constexpr int box_height(int tile_rows, int boxes) {
-  return boxes * box_step(tile_rows) < tile_rows / 2 ? boxes * box_step(tile_rows) : tile_rows / 2;
+  return kXRowBoxes * box_step(tile_rows) > tile_rows / 2 && boxes == kXRowBoxes ? tile_rows / 2
+                                                                               : boxes * box_step(tile_rows);
 }
 constexpr int kXSub = 2;       // k-blocks of 128 bytes per stage of the ring
 constexpr int kXEpiWarps = 16;
@@ -41,7 +42,6 @@ constexpr int kXGroup = 8;     // row tiles that share the weights they read (ti
 struct ExpertsParams {
   CUtensorMap tm_w;              // the wide operand
   CUtensorMap tm_r[kXRowBoxes];  // the row operand, by box height (weight gradient: of 128 and of 64 columns)
-  CUtensorMap tm_s;              // e2m1: the weights' scales, pieces of 128 rows x 4 scales side by side
   const int32_t* offsets;        // [E + 1], or null: one group of all rows
   int32_t E;
   int32_t rows;                  // rows of the inputs
@@ -50,7 +50,6 @@ struct ExpertsParams {
   int32_t out_rows;              // weight gradient: output rows per expert (K)
   int32_t step, row_tiles;       // weight gradient: output rows of a tile, 256 or 128; tiles of K
   uint32_t inv_group, inv_expert;  // floor((2^32 - 1) / n): n tiles of 8 row tiles, n of an expert (weight gradient)
-  uint32_t inv_stages;           // e2m1: the same of the stages of a sum
   int32_t w_blk, r_blk;          // operand described in blocks of 128 bytes (one load a stage), or not (two)
   int32_t segment;               // k-blocks per accumulator (e4m3: 1)
   int32_t bf16;                  // operands are bfloat16 (otherwise fp16)
@@ -60,13 +59,17 @@ struct ExpertsParams {
   int64_t ldo;
   const float* xs;               // e4m3: row scales [KB][rows]
   const float* ws;               // e4m3: weight scales [E][NB][KB]
-  const uint32_t* xs4;           // e2m1: row scales, four to a word, [ceil(K / 128)][rows]
   float* partials;               // split sums: [unit][warps of the pair][columns][32 lanes]
   uint32_t* arrivals;            // [tile][warps of the pair], zero between runs
   int32_t max_units;             // units the workspace holds (0: never split)
   uint32_t* status;              // [4]: status word and detail of a wait that ran out, which ends the waits
                                  // of later runs too; the same of bad offsets, which concern their run alone
   uint64_t timeout_ns;
+  // (here, so that what the other products read stays where it was: further in, the e4m3 kernel
+  // of long groups spilt more registers, and 8192 rows on 32 experts took 344 us instead of 336)
+  const uint32_t* xs4;           // e2m1: row scales, four to a word, [ceil(K / 128)][rows]
+  uint32_t inv_stages;           // e2m1: floor((2^32 - 1) / stages of a sum)
+  CUtensorMap tm_s;              // e2m1: the weights' scales, pieces of 128 rows x 4 scales side by side
 };
 
 // A unit of a split sum: each warp's columns x 32 lanes of floats.
