@@ -486,6 +486,15 @@ struct Schedule {
     return true;
   }
 
+  // The first unit of a table made anew.
+  static __device__ __forceinline__ bool again(Schedule& s, const ExpertsParams& p, const Table& t, Unit& u) {
+    s.split = t.head[0];
+    s.units = t.head[2];
+    s.by_split = Divisor(static_cast<uint32_t>(t.head[0]), static_cast<uint32_t>(t.head[1]));
+    s.e = -1;
+    return s.get(0, u);
+  }
+
   __device__ __forceinline__ bool get(int32_t i, Unit& u) {
     if constexpr (kShares) {
       if (split > 0) return get_shared(i, u);
@@ -537,12 +546,17 @@ struct Schedule {
 };
 
 // Offsets to shared memory, checked, and the row tiles before each expert.
-// Returns false (to every thread) if the offsets are no layout of the rows.
-template <int OP, int BN>
+// Returns false (to every thread) if the offsets are no layout of the rows.  kGuess: without
+// them, as if the last expert had all rows.
+template <int OP, int BN, bool kGuess = false>
 __device__ bool load_table(const ExpertsParams& p, int32_t* off, int32_t* pre, int32_t* head, int32_t* flag) {
   if (threadIdx.x == 0) *flag = 0;
-  for (int e = threadIdx.x; e <= p.E; e += blockDim.x)
-    off[e] = p.offsets ? p.offsets[e] : (e == 0 ? 0 : p.rows);
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
+    if constexpr (kGuess)
+      off[e] = e < p.E ? 0 : p.rows;
+    else
+      off[e] = p.offsets ? p.offsets[e] : (e == 0 ? 0 : p.rows);
+  }
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += blockDim.x)
     if (off[e] < 0 || off[e + 1] < off[e] || off[e + 1] > p.rows) *flag = 1;
@@ -568,6 +582,29 @@ __device__ bool load_table(const ExpertsParams& p, int32_t* off, int32_t* pre, i
   }
   __syncthreads();
   return *flag == 0;
+}
+
+// Short row tiles of e2m1 (kShares), whose calls are short: a call spends 2.4 us on its table
+// and on finding its first unit, of about 10.  With one expert, whose rows are most likely
+// all, this is done on a guess, before the wait for the kernel before, which in a step of a
+// model makes the rows; the roles then start with settle(), after which memory may be read:
+// true if the table has been made anew and the first unit has to be found again.
+struct Guess {
+  int32_t *off, *pre, *head, *flag;
+};
+template <int OP, int BN>
+__device__ bool settle(const ExpertsParams& p, const Guess& g) {
+  pdl_wait();
+  bool wrong = p.E != 1;
+  if (!wrong && p.offsets) wrong = p.offsets[0] != 0 || p.offsets[1] != p.rows;
+  if (!__syncthreads_or(wrong)) return false;
+  load_table<OP, BN>(p, g.off, g.pre, g.head, g.flag);
+  if (*g.flag != 0) {  // no units
+    __syncthreads();
+    if (threadIdx.x == 0) g.head[0] = g.head[2] = 0;
+    __syncthreads();
+  }
+  return true;
 }
 
 struct Ring {
@@ -630,32 +667,6 @@ __device__ __forceinline__ void prefetch_k(const CUtensorMap* map, int32_t blk, 
                        reinterpret_cast<uint64_t>(map)), "r"((kb + s) * bk), "r"(row), "r"(e) : "memory");
   }
 }
-// Before the wait for the kernel before: this CTA's first weights into L2, where they are
-// known without the offsets (one expert whose rows are all of them; where the offsets say
-// otherwise, other weights are read).  In a step of a model that kernel makes the rows, and
-// the memory has little to do meanwhile.  (A prefetch is no read: what that kernel may still
-// write of the weights is seen by the loads behind the wait.)
-template <int OP, int BN>
-__device__ void prefetch_weights(const ExpertsParams& p, uint32_t rank) {
-  const int32_t KB = Schedule<OP, BN>::k_blocks(p), stages = (KB + kSub - 1) / kSub, wt = Schedule<OP, BN>::wide_tiles(p);
-  const int32_t nt = (p.rows - 1) / BN + 1, tiles = nt * wt, pair = static_cast<int32_t>(blockIdx.x / 2);
-  const int32_t share = choose_share(tiles, stages, p.max_units, split_price(OP, true));
-  const int32_t tile = share > 0 ? pair * share / stages : pair, first = share > 0 ? pair * share - tile * stages : 0;
-  if (tile >= tiles) return;
-  const int32_t group = tile / (kXGroup * wt), gw = nt - group * kXGroup < kXGroup ? nt - group * kXGroup : kXGroup;
-  const int32_t n = (tile - group * kXGroup * wt) / gw * kXWide + static_cast<int32_t>(rank) * 128;
-  int32_t count = stages - first < stages_of(OP, BN) ? stages - first : stages_of(OP, BN);
-  if (share > 0 && share < count) count = share;
-  if (n < p.wide && elect_one())
-    for (int32_t s = 0; s < count; ++s) {
-      const int32_t kb = (first + s) * kSub;
-      prefetch_k(&p.tm_w, p.w_blk, kb, 128, n, 0);
-      asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                       reinterpret_cast<uint64_t>(&p.tm_s)), "r"(kb * (2 * kPiece / 8)), "r"(n / 128) : "memory");
-    }
-  __syncwarp();
-}
-
 // Box height of the row operand's loads (rows of a CTA, rounded up to its four sizes).
 template <int BN>
 __device__ __forceinline__ int32_t box_of(int32_t half) {
@@ -664,7 +675,7 @@ __device__ __forceinline__ int32_t box_of(int32_t half) {
 
 template <int OP, int BN>
 __device__ void tma_role(const ExpertsParams& p, const Table& table, const Ring& ring,
-                         uint32_t rank, int lane) {
+                         uint32_t rank, int lane, const Guess& guess) {
   Schedule<OP, BN> sch(p, table);
   constexpr int kStagesX = stages_of(OP, BN);
   const uint32_t full0 = mapa_shared(smem_u32(ring.full), 0);
@@ -673,7 +684,22 @@ __device__ void tma_role(const ExpertsParams& p, const Table& table, const Ring&
   uint32_t phase = 0, issued = 0, filled = 0;  // bit s: stage s used; its loads' parity
   bool ok = true;
   Unit u;
-  for (int32_t i = 0; ok && sch.get(i, u); ++i) {
+  bool more = false;  // (kShares: whether there is a first unit)
+  if constexpr (Schedule<OP, BN>::kShares) {
+    more = sch.get(0, u);
+    // Its first weights are asked for, too.  (A prefetch is no read: what the kernel before may
+    // still write of them is seen by the loads behind the wait.)
+    const int32_t n = u.n0 + static_cast<int32_t>(rank) * 128;
+    if (p.E == 1 && more && n < p.wide && elect_one())
+      for (int32_t kb = u.kb0; kb < u.kb1 && kb < u.kb0 + kSub * kStagesX; kb += kSub) {
+        prefetch_k(&p.tm_w, p.w_blk, kb, 128, n, 0);
+        asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                         reinterpret_cast<uint64_t>(&p.tm_s)), "r"(kb * (2 * kPiece / 8)), "r"(n / 128) : "memory");
+      }
+    __syncwarp();
+    if (settle<OP, BN>(p, guess)) more = Schedule<OP, BN>::again(sch, p, table, u);
+  }
+  for (int32_t i = 0; ok && (Schedule<OP, BN>::kShares && i == 0 ? more : sch.get(i, u)); ++i) {
     const int32_t half = u.w / 2;
     const int32_t boxes = OP == kOpFp8Long ? kXRowBoxes : box_of<BN>(half);
     const int32_t height = OP == kOpWeight ? half : box_height(BN, boxes);
@@ -927,15 +953,22 @@ __device__ void scale_long_role(const ExpertsParams& p, const Table& table,
 // warp that passes on, in the operands' ring; 480 to 560 with the words stored to TMEM by
 // four warps, whose stores take as long as a k-block's MMAs.)
 template <int BN>
-__device__ void copy4_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int lane) {
-  Schedule<kOpFp4, BN> sch(p, table);
+__device__ void copy4_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int lane,
+                           const Guess& guess) {
+  using Units = Schedule<kOpFp4, BN>;
+  Units sch(p, table);
   constexpr int kSlots = scale_slots(BN);
   const int32_t KA = (p.red + 127) / 128;
   int slot = 0;
   uint32_t phase = 0;
   bool ok = true;
   Unit u;
-  for (int32_t i = 0; ok && sch.get(i, u); ++i) {
+  bool more = false;
+  if constexpr (Units::kShares) {
+    more = sch.get(0, u);
+    if (settle<kOpFp4, BN>(p, guess)) more = Units::again(sch, p, table, u);
+  }
+  for (int32_t i = 0; ok && (Units::kShares && i == 0 ? more : sch.get(i, u)); ++i) {
     const int32_t words = (u.cnt + 31) / 32;  // (the accumulator's columns behind them are not stored)
     const uint32_t* const xs = p.xs4 + u.row0 + lane;
     for (int32_t kb = u.kb0; kb < u.kb1; kb += kSub) {
@@ -969,7 +1002,8 @@ __device__ void copy4_role(const ExpertsParams& p, const Table& table, const Rin
 
 template <int BN>
 __device__ void pass4_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int lane,
-                           int turn) {
+                           int turn, const Guess& guess) {
+  if constexpr (Schedule<kOpFp4, BN>::kShares) settle<kOpFp4, BN>(p, guess);
   Schedule<kOpFp4, BN> sch(p, table);
   constexpr int kSlots = scale_slots(BN);
   const uint32_t pfull0 = mapa_shared(smem_u32(ring.pfull), 0);
@@ -1002,7 +1036,8 @@ __device__ void pass4_role(const ExpertsParams& p, const Table& table, const Rin
 // The warp waits and computes together; lane 0 issues.
 template <int OP, int BN>
 __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring& ring,
-                         int lane, uint32_t tmem) {
+                         int lane, uint32_t tmem, const Guess& guess) {
+  if constexpr (Schedule<OP, BN>::kShares) settle<OP, BN>(p, guess);
   Schedule<OP, BN> sch(p, table);
   constexpr int kStagesX = stages_of(OP, BN);
   constexpr bool kWMn = OP == kOpForward || OP == kOpWeight;
@@ -1415,8 +1450,9 @@ __device__ void epilogue_long(const ExpertsParams& p, const Table& table,
 }
 
 template <int OP, int BN>
-__device__ void epilogue_role(const ExpertsParams& p, const Table& table,
-                              const Ring& ring, uint32_t rank, int ew, int lane, uint32_t tmem) {
+__device__ void epilogue_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int ew,
+                              int lane, uint32_t tmem, const Guess& guess) {
+  if constexpr (Schedule<OP, BN>::kShares) settle<OP, BN>(p, guess);
   constexpr int kCols = BN / 4;  // columns of a warp, at most
   const int quad = (threadIdx.x >> 5) & 3, quarter = ew >> 2;
   uint32_t acc = 0;
@@ -1648,23 +1684,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   if (OP == kOpFp4 && warp == 4 && lane == 0) tma_prefetch_desc(&p.tm_s);
   tc_fence_before();
   cluster_arrive();  // barriers initialised, TMEM allocated; the table is read meanwhile
-  if constexpr (Schedule<OP, BN>::kShares)
-    if (warp == 0 && p.E == 1) prefetch_weights<OP, BN>(p, rank);
-  pdl_wait();        // from here on global memory is read
-  const bool valid = load_table<OP, BN>(p, off, pre, head, flag);
+  constexpr bool kGuess = Schedule<OP, BN>::kShares;
+  const Guess guess{off, pre, head, flag};
+  if (!kGuess) pdl_wait();  // from here on global memory is read (a guess: from settle() on)
+  const bool valid = load_table<OP, BN, kGuess>(p, off, pre, head, flag);
   cluster_wait();
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
   if (valid) {
     if (warp == 0) {
-      tma_role<OP, BN>(p, table, ring, rank, lane);
+      tma_role<OP, BN>(p, table, ring, rank, lane, guess);
     } else if (warp == 1) {
-      if (rank == 0) mma_role<OP, BN>(p, table, ring, lane, tmem);
+      if (rank == 0)
+        mma_role<OP, BN>(p, table, ring, lane, tmem, guess);
+      else if constexpr (kGuess)
+        settle<OP, BN>(p, guess);
     } else if (warp < 2 + kXEpiWarps) {
       if constexpr (OP == kOpFp8Long)
         epilogue_long<BN>(p, table, ring, rank, warp - 2, lane, tmem);
       else
-        epilogue_role<OP, BN>(p, table, ring, rank, warp - 2, lane, tmem);
+        epilogue_role<OP, BN>(p, table, ring, rank, warp - 2, lane, tmem, guess);
     } else if constexpr (OP == kOpWeight) {
       zero_role<BN>(p, table, ring, rank, lane);
     } else if constexpr (OP == kOpFp8) {
@@ -1673,13 +1712,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       scale_long_role<BN>(p, table, ring, rank, lane);
     } else if constexpr (OP == kOpFp4) {
       if (warp == 2 + kXEpiWarps)
-        copy4_role<BN>(p, table, ring, rank, lane);
+        copy4_role<BN>(p, table, ring, rank, lane, guess);
       else
-        pass4_role<BN>(p, table, ring, rank, lane, warp - (3 + kXEpiWarps));
+        pass4_role<BN>(p, table, ring, rank, lane, warp - (3 + kXEpiWarps), guess);
     }
   } else if (threadIdx.x == 0) {
     set_status(p.status + 2, kStatusOffsets, 0);
   }
+  if constexpr (kGuess)
+    if (*flag != 0 && threadIdx.x == 0) set_status(p.status + 2, kStatusOffsets, 0);
   tc_fence_before();
   // This CTA's epilogue has waited for every accumulator of the pair, so every MMA and load
   // of the pair is through, unless a wait of this CTA ran out (a wait of the peer's alone

@@ -230,6 +230,30 @@ def test_rows_outside_the_groups_are_left():
         check(wide[a:b, 8:8 + N], ref, (K + 8) * 2.0 ** -23 * mag + 1.01 * U[torch.bfloat16] * ref.abs(), f"expert {e}")
 
 
+@pytest.mark.parametrize("K,N", [(128, 40), (8192, 2560)])
+@pytest.mark.parametrize("first,last", [(0, 50), (4, 45), (0, 0), (50, 50), (49, 50), (0, 51), (3, 2), (-1, 50)])
+def test_offsets_of_one_expert(K, N, first, last):
+    """Its rows need not be all of them, and offsets that are none leave everything as it was."""
+    g = rng(K + first)
+    x, w = randn(g, (50, K), torch.bfloat16), randn(g, (K, N), torch.bfloat16)
+    (xq, xs), (wq, ws) = fp4.quantize_rows(x), fp4.quantize_weights(w)
+    off = torch.tensor([first, last], dtype=torch.int32, device="cuda")
+    with fp4.Fp4Linear(K, N) as p:
+        want = p.forward(xq, xs, wq, ws, out_dtype=torch.float32)
+        out = torch.full_like(want, 7.0)
+        p.forward(xq, xs, wq, ws, off, out=out, out_dtype=torch.float32)
+        good = 0 <= first <= last <= 50
+        assert p.status() == (B_.OK if good else B_.ERR_INVALID)
+        if not good:
+            assert bool((out == 7).all())
+            p.reset()
+            assert torch.equal(p.forward(xq, xs, wq, ws, out_dtype=torch.float32), want) and p.status() == B_.OK
+            return
+    assert bool((out[:first] == 7).all()) and bool((out[last:] == 7).all())
+    mag = row_values(xq, xs).abs() @ weight_values(wq[None], ws[None])[0].abs().t()
+    check(out[first:last], want[first:last], 2 * (K + 8) * 2.0 ** -23 * mag[first:last])  # (tiles of other rows may add in another order)
+
+
 def test_runs_repeat_bit_for_bit():
     g = rng(7)
     x, w = randn(g, (64, 16384), torch.bfloat16), randn(g, (16384, 512), torch.bfloat16)
