@@ -14,42 +14,44 @@ namespace agg {
 namespace {
 constexpr int kThreads = 256;
 
-// s = 1 / (1 + exp(-g)) and 1 - s = exp(-g) s.
+__device__ __forceinline__ float reciprocal(float d) {  // of 1 and on; within 1 ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return r;
+}
+// exp(x) for |x| <= 100, within 2 ulps (zero from -87.3 down): with t = x / ln 2 rounded, exp(x) = 2^t exp(x - t ln 2), whose
+// second factor is 1 + (x - t ln 2) but for its square, below 2^-33.  ln 2 in two parts.
+__device__ __forceinline__ float exp_near(float x) {
+  const float t = x * 1.44269504f;
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  return fmaf(e, fmaf(t, 1.90465429e-9f, fmaf(-t, 0.693147182f, x)), e);
+}
+
+// s = 1 / (1 + exp(-g)) and 1 - s = exp(-g) s.  Below -80 s is exp(g): exp(-g) passes the largest
+// float from -88.7 on, but g s lies within floats to -103.  (Looked for once for all V.)
 //
-// kExact (floats, and codes, whose ties a last bit of y decides): the reciprocal is the
-// hardware's approximate one after one step of Newton's iteration, within 1 ulp.  Below -80 s is
-// exp(g): exp(-g) passes the largest float from -88.7 on, but g s lies within floats to -103.
-// (Looked for once for all V: a second exponential for each, taken or not, makes the kernel to
-// e4m3 17 % slower.)
-//
-// Otherwise (y rounded to 16 bits): from exp(-|g|), which does not overflow, and the approximate
-// reciprocal alone, within 4 ulps together (8192 x 2 x 2048 to bf16 18.4 us, 19.3 so).
+// kExact (floats, and codes, whose ties a last bit of y decides): to about an ulp, the reciprocal
+// after one step of Newton's iteration.  Otherwise (y rounded to 16 bits) by the approximate
+// exponential, off by |g| 2^-24 and 2 ulps.  The kernels are bound by instructions here: 8192 x 2 x 4096
+// bf16 to e4m3 takes 42 us with expf and __fdividef, its loads and stores 25.
 template <bool kExact, int V>
 __device__ __forceinline__ void sigmoid(const float (&g)[V], float (&s)[V], float (&rest)[V]) {
-  if constexpr (kExact) {
-    float least = 0.0f;
+  float least = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float e = expf(-g[v]), d = 1.0f + e, r = __fdividef(1.0f, d);
-      s[v] = fmaf(r, fmaf(-d, r, 1.0f), r);
-      rest[v] = e * s[v];
-      least = fminf(least, g[v]);
-    }
-    if (least < -80.0f) {
+  for (int v = 0; v < V; ++v) {
+    const float e = kExact ? exp_near(fmaxf(-g[v], -100.0f)) : __expf(-g[v]), d = 1.0f + e, r = reciprocal(d);
+    s[v] = kExact ? fmaf(r, fmaf(-d, r, 1.0f), r) : r;
+    rest[v] = e * s[v];
+    least = fminf(least, g[v]);
+  }
+  if (least < -80.0f) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (g[v] < -80.0f) {
-          s[v] = expf(g[v]);
-          rest[v] = 1.0f;
-        }
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float e = expf(-fabsf(g[v])), r = __fdividef(1.0f, 1.0f + e);
-      s[v] = g[v] < 0.0f ? e * r : r;
-      rest[v] = g[v] < 0.0f ? r : e * r;
-    }
+    for (int v = 0; v < V; ++v)
+      if (g[v] < -80.0f) {
+        s[v] = expf(g[v]);
+        rest[v] = 1.0f;
+      }
   }
 }
 

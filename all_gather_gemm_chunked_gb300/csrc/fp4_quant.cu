@@ -47,20 +47,22 @@ __global__ void __launch_bounds__(256) quantize_rows4_kernel(int64_t rows, int64
   }
   in = in && src < src_rows;
   const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (256 * kSteps) + lane * 8;
+  const int left = static_cast<int>(K - c0);  // (K % 32 == 0: a lane's 8 elements are all in or all out)
+  const T* from = x + src * ldx + c0;
   Piece<T, V> p[kSteps][8 / V];
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
-    const int64_t c = c0 + i * 256;  // (K % 32 == 0: a lane's 8 elements are all in or all out)
 #pragma unroll
     for (int h = 0; h < 8 / V; ++h) {
       p[i][h] = Piece<T, V>{};
-      if (in && c < K) p[i][h].load(x + src * ldx + c + h * V);
+      if (in && i * 256 < left) p[i][h].load(from + i * 256 + h * V);
     }
   }
+  uint32_t* const codes = reinterpret_cast<uint32_t*>(q + (r * K + c0) / 2);
+  uint32_t* words = scales + (c0 / kScaleBlock) * rows + r;
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int64_t c = c0 + i * 256;
-    if (c - lane * 8 >= K) break;
+  for (int i = 0; i < kSteps; ++i, words += 2 * rows) {
+    if (i * 256 >= left + lane * 8) break;  // (all of the warp)
     float g[8];
     uint32_t largest = 0;
 #pragma unroll
@@ -80,8 +82,10 @@ __global__ void __launch_bounds__(256) quantize_rows4_kernel(int64_t rows, int64
     uint32_t word = s << ((lane >> 2 & 3) * 8);
     word |= __shfl_xor_sync(0xffffffffu, word, 4);
     word |= __shfl_xor_sync(0xffffffffu, word, 8);
-    if (c < K) *reinterpret_cast<uint32_t*>(q + (r * K + c) / 2) = e2m1x8(g);
-    if ((lane & 15) == 0 && c < K) scales[(c / kScaleBlock) * rows + r] = word;
+    if (i * 256 < left) {
+      codes[i * 32] = e2m1x8(g);
+      if ((lane & 15) == 0) *words = word;
+    }
   }
 }
 

@@ -80,6 +80,26 @@ def test_special_values():
     assert bool(torch.isnan(dx[5]))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_far_gates(dtype):
+    """Gates from -110 to 110, where the exponential leaves the range of floats."""
+    n = 4096
+    x = torch.cat([torch.linspace(-110, 110, n, device="cuda"), randn(rng(3), (n,))]).to(dtype)[None]
+    dy = randn(rng(4), (1, n), dtype)
+    g, u, s = parts(x)
+    # beside the error near zero: the approximate exponential's |g| 2^-24, and where s lies among floats 2^-149
+    # apart (or is flushed to them), three and a half of those steps
+    y, grain = g * s * u, 3.5 * 2.0 ** -149 * (1 + g.abs())
+    check(act.swiglu(x), y, (S_ERROR + (4 + g.abs()) * F + 1.01 * U[dtype]) * y.abs() + grain * u.abs() + STEP[dtype], "y")
+    d, t = dy.double(), 1 + g * (1 - s)
+    ref = torch.cat([d * u * s * t, d * g * s], 1)
+    rel = S_ERROR + (6 + g.abs()) * F
+    err = torch.cat([(d * u).abs() * (s * (rel * t.abs() + rel * g.abs() * (1 - s)) + grain * t.abs()), (d * g).abs() * (rel * s) + grain * d.abs()], 1)
+    # products below 2^-126 are rounded to 2^-149, by half of it: dy s, which u t (or g) multiplies, and that times u, which t does
+    err = err + 2.0 ** -150 * torch.cat([(u * t).abs() + t.abs() + 1, g.abs() + 1], 1)
+    check(act.swiglu_backward(dy, x), ref, err + 1.01 * U[dtype] * ref.abs() + STEP[dtype], "dx")
+
+
 def test_backward_is_the_slope():
     """Differences of the formula in 64 bits along random directions."""
     gen = rng(12)
