@@ -61,32 +61,35 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const GateArgs a, int 
   const int team = 1 << log, thread = threadIdx.x & (team - 1);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads >> log) + (threadIdx.x >> log);
   const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (team * P * V) + thread * V;
-  const bool valid = row < a.rows;
-  const T* x = static_cast<const T*>(a.x) + row * a.ldx + c0;
+  const int left = row < a.rows ? static_cast<int>(a.N - c0) : 0;  // elements of the row from c0 on
+  const T *x = static_cast<const T*>(a.x) + row * a.ldx + c0, *y = x + a.N;
   Piece<T, V> g[P], u[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     g[i] = u[i] = Piece<T, V>{};
-    if (valid && c0 + i * team * V < a.N) {
+    if (i * team * V < left) {
       g[i].load(x + i * team * V);
-      u[i].load(x + i * team * V + a.N);
+      u[i].load(y + i * team * V);
     }
   }
+  constexpr bool kCodes = OUT == kTypeE4m3 || OUT == kTypeE2m1;
+  [[maybe_unused]] T* const out = static_cast<T*>(a.out) + row * a.N + c0;
+  [[maybe_unused]] CodePlace<OUT> place(a.out, a.scales, a.rows, a.N, row, c0);
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int64_t c = c0 + i * team * V;
-    const bool in = valid && c < a.N;
-    if (c - (thread & 31) * V >= a.N) break;  // (all of the warp)
+    const bool in = i * team * V < left;
+    if (!__any_sync(0xffffffffu, in)) break;
     float f[V], v[V], s[V], rest[V];
     g[i].get(f);
     u[i].get(v);
-    sigmoid<sizeof(T) == 4 || OUT == kTypeE4m3 || OUT == kTypeE2m1>(f, s, rest);
+    sigmoid<sizeof(T) == 4 || kCodes>(f, s, rest);
 #pragma unroll
     for (int j = 0; j < V; ++j) f[j] = f[j] * s[j] * v[j];
-    if constexpr (OUT == kTypeE4m3 || OUT == kTypeE2m1) {
-      put_codes<OUT, V>(a.out, a.scales, a.rows, a.N, row, c, in, f);
+    if constexpr (kCodes) {
+      put_codes<OUT, V>(place, in, f);
+      place.advance(team * V);
     } else {
-      if (in) store_floats(static_cast<T*>(a.out) + row * a.N + c, f);
+      if (in) store_floats(out + i * team * V, f);
     }
   }
 }
@@ -98,19 +101,21 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const GateArg
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads >> log) + (threadIdx.x >> log);
   const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (team * P * V) + thread * V;
   if (row >= a.rows) return;
-  const T *x = static_cast<const T*>(a.x) + row * a.ldx + c0, *dy = static_cast<const T*>(a.dy) + row * a.lddy + c0;
-  T* dx = static_cast<T*>(a.out) + row * 2 * a.N + c0;
+  const int left = static_cast<int>(a.N - c0);
+  const T *x = static_cast<const T*>(a.x) + row * a.ldx + c0, *y = x + a.N,
+          *dy = static_cast<const T*>(a.dy) + row * a.lddy + c0;
+  T *dg = static_cast<T*>(a.out) + row * 2 * a.N + c0, *du = dg + a.N;
   Piece<T, V> g[P], u[P], d[P];
 #pragma unroll
   for (int i = 0; i < P; ++i)
-    if (c0 + i * team * V < a.N) {
+    if (i * team * V < left) {
       g[i].load(x + i * team * V);
-      u[i].load(x + i * team * V + a.N);
+      u[i].load(y + i * team * V);
       d[i].load(dy + i * team * V);
     }
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    if (c0 + i * team * V >= a.N) break;
+    if (i * team * V >= left) break;
     float f[V], v[V], e[V], s[V], rest[V];
     g[i].get(f);
     u[i].get(v);
@@ -122,8 +127,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const GateArg
       v[j] = es * v[j] * fmaf(f[j], rest[j], 1.0f);
       e[j] = es * f[j];
     }
-    store_floats(dx + i * team * V, v);
-    store_floats(dx + i * team * V + a.N, e);
+    store_floats(dg + i * team * V, v);
+    store_floats(du + i * team * V, e);
   }
 }
 

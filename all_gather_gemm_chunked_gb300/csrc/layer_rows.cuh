@@ -124,12 +124,28 @@ __device__ __forceinline__ void store_floats(T* p, const float (&f)[V]) {
   r.store(p);
 }
 
+// Places of a row's codes and scales from column c on (their addresses are made once a
+// thread: at each piece, in 64 bits, they cost a tenth of the time).
+template <int OUT>
+struct CodePlace {
+  uint8_t* q;
+  uint32_t* s;     // of c's 128 elements: an e4m3 scale, or four e2m1 ones
+  int64_t blocks;  // from one 128 elements' to the next
+  __device__ __forceinline__ CodePlace(void* codes, void* scales, int64_t rows, int64_t H, int64_t row, int64_t c)
+      : q(static_cast<uint8_t*>(codes) + (OUT == kTypeE4m3 ? row * H + c : (row * H + c) / 2)),
+        s(static_cast<uint32_t*>(scales) + (c / kScaleBlock) * rows + row), blocks(rows) {}
+  // n elements on, a multiple of 128
+  __device__ __forceinline__ void advance(int n) {
+    q += OUT == kTypeE4m3 ? n : n / 2;
+    s += n / kScaleBlock * blocks;
+  }
+};
+
 // V neighbouring elements of a row as codes, by the lanes of a whole warp, which hold V
 // elements each, the next lane the next V; past the row (`in` false) they are zeros.  The
 // same codes and scales as quantising the floats.
 template <int OUT, int V>
-__device__ __forceinline__ void put_codes(void* codes, void* scales, int64_t rows, int64_t H, int64_t row, int64_t c,
-                                          bool in, float (&f)[V]) {
+__device__ __forceinline__ void put_codes(const CodePlace<OUT>& at, bool in, float (&f)[V]) {
   static_assert(V == 8 || V == 4, "16 bytes of the rows' type");
   const int lane = threadIdx.x & 31;
   constexpr int kLanes = kScaleBlock / V;  // of 128 elements
@@ -146,12 +162,11 @@ __device__ __forceinline__ void put_codes(void* codes, void* scales, int64_t row
       w[b] = e4m3x2(__fmul_rn(f[4 * b], inv), __fmul_rn(f[4 * b + 1], inv)) |
              (e4m3x2(__fmul_rn(f[4 * b + 2], inv), __fmul_rn(f[4 * b + 3], inv)) << 16);
     if (!in) return;
-    uint8_t* q = static_cast<uint8_t*>(codes) + row * H + c;
     if constexpr (V == 8)
-      *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(at.q) = make_uint2(w[0], w[1]);
     else
-      *reinterpret_cast<uint32_t*>(q) = w[0];
-    if ((lane & (kLanes - 1)) == 0) static_cast<float*>(scales)[(c / kScaleBlock) * rows + row] = s;
+      *reinterpret_cast<uint32_t*>(at.q) = w[0];
+    if ((lane & (kLanes - 1)) == 0) *at.s = __float_as_uint(s);
   } else {
     uint32_t largest = 0;
 #pragma unroll
@@ -169,12 +184,11 @@ __device__ __forceinline__ void put_codes(void* codes, void* scales, int64_t row
 #pragma unroll
     for (int o = kMicroBlock / V; o < kLanes; o <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
     if (!in) return;
-    uint8_t* q = static_cast<uint8_t*>(codes) + (row * H + c) / 2;
     if constexpr (V == 8)
-      *reinterpret_cast<uint32_t*>(q) = code;
+      *reinterpret_cast<uint32_t*>(at.q) = code;
     else
-      *reinterpret_cast<uint16_t*>(q) = static_cast<uint16_t>(code);
-    if ((lane & (kLanes - 1)) == 0) static_cast<uint32_t*>(scales)[(c / kScaleBlock) * rows + row] = word;
+      *reinterpret_cast<uint16_t*>(at.q) = static_cast<uint16_t>(code);
+    if ((lane & (kLanes - 1)) == 0) *at.s = word;
   }
 }
 

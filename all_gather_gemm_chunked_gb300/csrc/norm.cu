@@ -110,22 +110,32 @@ __device__ __forceinline__ float team_rstd(const NormArgs& a, int team_warps, fl
   return scale * rsqrtf(fmaf(sum, a.inv_H, eps));
 }
 
+// Where a thread's piece of y goes, and the next, n elements on, a multiple of 128 where y
+// becomes codes.
 template <int OUT, typename T, int V>
-__device__ __forceinline__ void put_row(const NormArgs& a, int64_t row, int64_t c, bool in, const Piece<T, V>& h,
-                                        float rstd, const float (&w)[V]) {
-  float f[V];
-  h.get(f);
+struct RowPlace {
+  static constexpr bool kCodes = OUT == kTypeE4m3 || OUT == kTypeE2m1;
+  T* y;
+  CodePlace<OUT> codes;
+  __device__ __forceinline__ RowPlace(const NormArgs& a, int64_t row, int64_t c)
+      : y(static_cast<T*>(a.out) + row * a.H + c), codes(a.out, a.scales, a.rows, a.H, row, c) {}
+  __device__ __forceinline__ void put(bool in, const Piece<T, V>& h, float rstd, const float (&w)[V], int n) {
+    float f[V];
+    h.get(f);
 #pragma unroll
-  for (int v = 0; v < V; ++v) f[v] = f[v] * rstd * w[v];
-  if constexpr (OUT == kTypeE4m3 || OUT == kTypeE2m1) {
-    if (!in)
+    for (int v = 0; v < V; ++v) f[v] = f[v] * rstd * w[v];
+    if constexpr (kCodes) {
+      if (!in)
 #pragma unroll
-      for (int v = 0; v < V; ++v) f[v] = 0.0f;
-    put_codes<OUT, V>(a.out, a.scales, a.rows, a.H, row, c, in, f);
-  } else {
-    if (in) store_floats(static_cast<T*>(a.out) + row * a.H + c, f);
+        for (int v = 0; v < V; ++v) f[v] = 0.0f;
+      put_codes<OUT, V>(codes, in, f);
+      codes.advance(n);
+    } else {
+      if (in) store_floats(y, f);
+      y += n;
+    }
   }
-}
+};
 
 // A team of 2^log threads has a row, P pieces of V elements a thread.
 template <typename T, typename W, int V, int P, int OUT>
@@ -143,7 +153,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int log) {
     if (i * team * V < left) h[i].load(x + i * team * V);
   }
   if (a.residual) {
-    const T* res = static_cast<const T*>(a.residual) + row * a.ldr + c0;
+    const T* const res = static_cast<const T*>(a.residual) + row * a.ldr + c0;
+    T* const held = static_cast<T*>(a.h) + row * a.H + c0;
     Piece<T, V> r[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -153,7 +164,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int log) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       add_residual(h[i], r[i]);
-      if (i * team * V < left) h[i].store(static_cast<T*>(a.h) + row * a.H + c0 + i * team * V);
+      if (i * team * V < left) h[i].store(held + i * team * V);
     }
   }
   const float rstd = team_rstd(a, team >> 5, part, [&](float scale) {
@@ -163,15 +174,17 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int log) {
     return sum;
   });
   if (a.rstd && thread == 0 && left > 0) a.rstd[row] = rstd;
+  RowPlace<OUT, T, V> place(a, row, c0);
+  const W* const weight = static_cast<const W*>(a.weight) + c0;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const bool in = i * team * V < left;
     if (!__any_sync(0xffffffffu, in)) break;
     Weights<W, V> w{};
-    if (in) w.load(static_cast<const W*>(a.weight) + c0 + i * team * V);
+    if (in) w.load(weight + i * team * V);
     float f[V];
     w.get(f);
-    put_row<OUT>(a, row, c0 + i * team * V, in, h[i], rstd, f);
+    place.put(in, h[i], rstd, f, team * V);
   }
 }
 
@@ -199,6 +212,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
   });
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
   const T* from = a.residual ? h : x;  // (each thread reads what it wrote itself)
+  RowPlace<OUT, T, V> place(a, row, static_cast<int64_t>(threadIdx.x) * V);
   const int64_t end = (a.H + 1024 * V - 1) / (1024 * V) * (1024 * V);  // (the lanes of a warp stay together)
   for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < end; c += 1024 * V) {
     const bool in = c < a.H;
@@ -210,7 +224,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
       w.load(static_cast<const W*>(a.weight) + c);
     }
     w.get(f);
-    put_row<OUT>(a, row, c, in, v, rstd, f);
+    place.put(in, v, rstd, f, 1024 * V);
   }
 }
 
