@@ -78,9 +78,9 @@ __device__ __forceinline__ float squares(const Piece<T, V>& r, float scale, floa
 // float, it is made anew of elements times 2^-80 (all threads of the block or, with teams of
 // one warp, of the warp take that way together).
 template <typename F>
-__device__ __forceinline__ float team_rstd(const NormArgs& a, int team_warps, float (*part)[32], const F& squares) {
+__device__ __forceinline__ float team_rstd(const NormArgs& a, int team_warps, int first, float (*part)[32], const F& squares) {
   constexpr float kSmall = 0x1p-80f, kLarge = 1e37f;  // (32 warps' sums up to that are finite)
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = warp & ~(team_warps - 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;  // first: of the team's warps
   auto over_warp = [](float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -137,13 +137,14 @@ struct RowPlace {
   }
 };
 
-// A team of 2^log threads has a row, P pieces of V elements a thread.
+// A team of threads has a row, P pieces of V elements a thread: a block's threads (log 10), or
+// 2^log of them, several teams a block.
 template <typename T, typename W, int V, int P, int OUT>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int log) {
+__global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int team, int log) {
   pdl_enter();
   __shared__ float part[2][32];
-  const int team = 1 << log, thread = threadIdx.x & (team - 1);
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> log) + (threadIdx.x >> log);
+  const int thread = threadIdx.x & ((1 << log) - 1), number = threadIdx.x >> log;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (log == 10 ? 1 : blockDim.x >> log) + number;
   const int c0 = thread * V, left = row < a.rows ? static_cast<int>(a.H) - c0 : 0;  // elements of the row from c0 on
   const T* x = static_cast<const T*>(a.x) + row * a.ldx + c0;
   Piece<T, V> h[P];
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int log) {
       if (i * team * V < left) h[i].store(held + i * team * V);
     }
   }
-  const float rstd = team_rstd(a, team >> 5, part, [&](float scale) {
+  const float rstd = team_rstd(a, team >> 5, number << (log - 5), part, [&](float scale) {
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < P; ++i) sum = squares(h[i], scale, sum);
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   T* h = static_cast<T*>(a.h) + row * a.H;
-  const float rstd = team_rstd(a, 32, part, [&](float scale) {
+  const float rstd = team_rstd(a, 32, 0, part, [&](float scale) {
     float sum = 0.0f;
     for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < a.H; c += 1024 * V) {
       Piece<T, V> v, r;
@@ -443,9 +444,12 @@ int size_of(int dtype) { return dtype == kTypeF32 ? 4 : 2; }
 
 template <typename T, typename W, int V, int P, int OUT>
 cudaError_t launch_norm_p(const NormArgs& a, int64_t pieces, cudaStream_t stream) {
-  const int log = team_log((pieces + P - 1) / P), threads = log < 7 ? 128 : 1 << log, per = threads >> log;
+  // (teams of more than 64 threads: no more warps than the row needs)
+  const int64_t need = (pieces + P - 1) / P;
+  const int log = need > 64 ? 10 : team_log(need), team = log == 10 ? static_cast<int>((need + 31) / 32 * 32) : 1 << log;
+  const int threads = log == 10 ? team : 128, per = threads / team;
   const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per));
-  return launch(norm_kernel<T, W, V, P, OUT>, grid, threads, stream, a, log);
+  return launch(norm_kernel<T, W, V, P, OUT>, grid, threads, stream, a, team, log);
 }
 template <typename T, typename W, int V, int OUT>
 cudaError_t launch_norm_v(const NormArgs& a, cudaStream_t stream) {
