@@ -192,16 +192,17 @@ __device__ __forceinline__ void put_codes(const CodePlace<OUT>& at, bool in, flo
   }
 }
 
-// The sum over a team's threads (a power of two of them, 32 or more; `part` has a float
-// for each warp of the block), the same in every thread and every call.
-__device__ __forceinline__ float team_sum(float v, int team_warps, float* part) {
+// The sum over a team's threads (whole warps, `first` of the block's on, or 8 or 16 lanes of
+// one; `part` has a float for each warp of the block), the same in every thread and every call.
+__device__ __forceinline__ float team_sum(float v, int team, int first, float* part) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (team_warps == 1) return v;
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < team) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (team <= 32) return v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) part[warp] = v;
   __syncthreads();
-  v = lane < team_warps ? part[(warp & ~(team_warps - 1)) + lane] : 0.0f;
+  v = lane < team >> 5 ? part[first + lane] : 0.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;

@@ -232,118 +232,161 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
 // ------------------------------------------------------------------ gradient
 // Rows whose pieces fit a team, P a thread.  A thread keeps its columns from row to row,
 // and their share of the weight's gradient in registers; a block adds its teams' and
-// stores one part.
-template <typename T, typename W, int V, int P, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 2) norm_backward_kernel(const NormBackwardArgs a, int log) {
+// stores one part.  The rows to come are copied to shared memory, two ahead, each piece by
+// the thread that reads it, twice: registers for what is in flight would leave room for
+// fewer columns and threads.  (8192 x 8192 bf16 83 us, with rows in registers 97; 8192 x
+// 5120 55 and 68.  Single 16-bit elements, which no such copy takes, stay in registers.)
+constexpr int kSlots = 2;
+template <typename T, int V, int P, bool kCopied = (V * sizeof(T) >= 4)>
+struct Ring {
+  static constexpr int kBytes = 3 * P * kSlots * V * static_cast<int>(sizeof(T));  // of a thread
+  using Word = std::conditional_t<V * sizeof(T) == 16, uint4, uint32_t>;
+  Word* mine;
+  int n;
+  __device__ __forceinline__ explicit Ring(uint8_t* bytes)
+      : mine(reinterpret_cast<Word*>(bytes) + threadIdx.x), n(static_cast<int>(blockDim.x)) {}
+  __device__ __forceinline__ Word* at(int slot, int operand, int i) const { return mine + ((slot * 3 + operand) * P + i) * n; }
+  __device__ __forceinline__ void clear(int slot, int operand, int i) { *at(slot, operand, i) = Word{}; }
+  __device__ __forceinline__ void ask(int slot, int operand, int i, const T* from) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(at(slot, operand, i)));
+    if constexpr (sizeof(Word) == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+  }
+  __device__ __forceinline__ void get(int slot, int operand, int i, float (&f)[V]) const {
+    Piece<T, V> p;
+    const Word w = *at(slot, operand, i);
+    __builtin_memcpy(p.w, &w, sizeof(p.w));
+    p.get(f);
+  }
+};
+template <typename T, int V, int P>
+struct Ring<T, V, P, false> {
+  static constexpr int kBytes = P * V * 4;  // (its columns' sums)
+  Piece<T, V> r[kSlots][3][P];
+  __device__ __forceinline__ explicit Ring(uint8_t*) {}
+  __device__ __forceinline__ void clear(int slot, int operand, int i) { r[slot][operand][i] = Piece<T, V>{}; }
+  __device__ __forceinline__ void ask(int slot, int operand, int i, const T* from) { r[slot][operand][i].load(from); }
+  __device__ __forceinline__ void get(int slot, int operand, int i, float (&f)[V]) const { r[slot][operand][i].get(f); }
+};
+template <typename T, typename W, int V, int P>
+__global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBackwardArgs a, int team, int teams) {
   pdl_enter();
-  // The next row's loads ahead of this one's sum, where registers allow.
-  constexpr bool kAhead = P * Piece<T, V>::kWords <= 4;
+  using R = Ring<T, V, P>;
+  extern __shared__ __align__(16) uint8_t ring_bytes[];
   __shared__ float part[2][32];
-  __shared__ float sums[THREADS == 1024 ? 1 : THREADS * V * P];
-  const int team = 1 << log, thread = threadIdx.x & (team - 1), teams = THREADS >> log;
-  const int c0 = thread * V;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
-  const T *dy = static_cast<const T*>(a.dy) + c0, *h = static_cast<const T*>(a.h) + c0,
-          *dh = static_cast<const T*>(a.dh) + c0;
+  R ring(ring_bytes);
+  const int number = threadIdx.x / team, thread = threadIdx.x - number * team, c0 = thread * V;
+  const int left = static_cast<int>(a.H) - c0;  // elements of a row from c0 on
+  const int64_t step = static_cast<int64_t>(gridDim.x) * teams, first = static_cast<int64_t>(blockIdx.x) * teams;
   float dw[P][V] = {};
   Weights<W, V> rw[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     rw[i] = Weights<W, V>{};
-    if (c0 + i * team * V < a.H) rw[i].load(static_cast<const W*>(a.weight) + c0 + i * team * V);
+    if (i * team * V < left) rw[i].load(static_cast<const W*>(a.weight) + c0 + i * team * V);
   }
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)  // what no copy fills
+#pragma unroll
+      for (int o = 0; o < 3; ++o)
+        if (i * team * V >= left || (o == 2 && !a.dh)) ring.clear(s, o, i);
   const float inv = 1.0f / static_cast<float>(a.H);
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * teams;
-  int64_t row = first + (threadIdx.x >> log);
-  Piece<T, V> rg[P], rh[P], rd[P];
-  float rstd = 0.0f;
-  auto load = [&] {
-    const bool valid = row < a.rows;
-    if (valid) rstd = a.rstd[row];
+  int64_t row = first + number, next = row;  // next: the row to ask for
+  float rstd[kSlots];
+  auto ask = [&](int slot) {
+    if (next < a.rows) {
+      const T *dy = static_cast<const T*>(a.dy) + next * a.lddy + c0, *h = static_cast<const T*>(a.h) + next * a.ldh + c0,
+              *dh = static_cast<const T*>(a.dh) + next * a.lddh + c0;
+      rstd[slot] = a.rstd[next];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int c = i * team * V;
-      rg[i] = rh[i] = rd[i] = Piece<T, V>{};
-      if (valid && c0 + c < a.H) {
-        rg[i].load(dy + row * a.lddy + c);
-        rh[i].load(h + row * a.ldh + c);
-        if (a.dh) rd[i].load(dh + row * a.lddh + c);
-      }
+      for (int i = 0; i < P; ++i)
+        if (i * team * V < left) {
+          ring.ask(slot, 0, i, dy + i * team * V);
+          ring.ask(slot, 1, i, h + i * team * V);
+          if (a.dh) ring.ask(slot, 2, i, dh + i * team * V);
+        }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    next += step;
   };
-  if (kAhead) load();
-  int turn = 0;
-  for (int64_t base = first; base < a.rows; base += step, turn ^= 1) {  // (all teams: they share a barrier)
-    if (!kAhead) load();
-    Piece<T, V> pg[P], ph[P], pd[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      pg[i] = rg[i];
-      ph[i] = rh[i];
-      pd[i] = rd[i];
-    }
-    const float rs = rstd;
-    const int64_t at = row;
-    const bool valid = at < a.rows;
-    row += step;
-    if (kAhead) load();
-    float dot = 0.0f;
+  for (int s = 0; s < kSlots; ++s) {
+    rstd[s] = 0.0f;
+    ask(s);
+  }
+  for (int64_t base = first; base < a.rows;) {  // (all teams: they share a barrier)
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      float g[V], x[V], w[V];
-      pg[i].get(g);
-      ph[i].get(x);
-      rw[i].get(w);
+    for (int s = 0; s < kSlots; ++s) {
+      if (base >= a.rows) break;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
+      const float rs = rstd[s];
+      const bool valid = row < a.rows;
+      float dot = 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        x[v] *= rs;
-        if (valid) dw[i][v] = fmaf(g[v], x[v], dw[i][v]);
-        dot = fmaf(g[v] * w[v], x[v], dot);
+      for (int i = 0; i < P; ++i) {
+        float g[V], x[V], w[V];
+        ring.get(s, 0, i, g);
+        ring.get(s, 1, i, x);
+        rw[i].get(w);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          x[v] *= rs;
+          if (valid) dw[i][v] = fmaf(g[v], x[v], dw[i][v]);
+          dot = fmaf(g[v] * w[v], x[v], dot);
+        }
       }
-    }
-    dot = team_sum(dot, team >> 5, part[turn]) * inv;
+      dot = team_sum(dot, team, number * (team >> 5), part[s]) * inv;
+      T* dx = static_cast<T*>(a.dx) + row * a.H + c0;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int c = i * team * V;
-      if (!valid || c0 + c >= a.H) continue;
-      float g[V], x[V], w[V], d[V];
-      pg[i].get(g);
-      ph[i].get(x);
-      rw[i].get(w);
-      pd[i].get(d);
+      for (int i = 0; i < P; ++i) {
+        if (!valid || i * team * V >= left) continue;
+        float g[V], x[V], w[V], d[V];
+        ring.get(s, 0, i, g);
+        ring.get(s, 1, i, x);
+        ring.get(s, 2, i, d);
+        rw[i].get(w);
 #pragma unroll
-      for (int v = 0; v < V; ++v) g[v] = fmaf(rs, fmaf(-x[v] * rs, dot, g[v] * w[v]), a.dh ? d[v] : 0.0f);
-      store_floats(static_cast<T*>(a.dx) + at * a.H + c0 + c, g);
+        for (int v = 0; v < V; ++v) g[v] = fmaf(rs, fmaf(-x[v] * rs, dot, g[v] * w[v]), d[v]);
+        store_floats(dx + i * team * V, g);
+      }
+      ask(s);
+      row += step;
+      base += step;
     }
   }
   float* to = a.parts + static_cast<int64_t>(blockIdx.x) * a.H;
-  if constexpr (THREADS != 1024) {
-    if (teams > 1) {
+  if (teams > 1) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(ring_bytes);
 #pragma unroll
-      for (int i = 0; i < P; ++i)
+    for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          sums[(threadIdx.x >> log) * (team * P * V) + i * team * V + c0 + v] = dw[i][v];
-      __syncthreads();
-      for (int c = threadIdx.x; c < a.H; c += THREADS) {
-        float s = 0.0f;
-        for (int t = 0; t < teams; ++t) s += sums[t * (team * P * V) + c];
-        to[c] = s;
-      }
-      return;
+      for (int v = 0; v < V; ++v) sums[number * (team * P * V) + i * team * V + c0 + v] = dw[i][v];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.H; c += teams * team) {
+      float s = 0.0f;
+#pragma unroll 4
+      for (int t = 0; t < teams; ++t) s += sums[t * (team * P * V) + c];
+      to[c] = s;
     }
+    return;
   }
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int c = c0 + i * team * V;
-    if (c >= a.H) continue;
+    const int c = i * team * V;
+    if (c >= left) continue;
     if constexpr (V % 4 == 0) {
 #pragma unroll
       for (int v = 0; v < V; v += 4)
-        *reinterpret_cast<float4*>(to + c + v) = make_float4(dw[i][v], dw[i][v + 1], dw[i][v + 2], dw[i][v + 3]);
+        *reinterpret_cast<float4*>(to + c0 + c + v) = make_float4(dw[i][v], dw[i][v + 1], dw[i][v + 2], dw[i][v + 3]);
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) to[c + v] = dw[i][v];
+      for (int v = 0; v < V; ++v) to[c0 + c + v] = dw[i][v];
     }
   }
 }
@@ -370,7 +413,7 @@ __global__ void __launch_bounds__(512) norm_backward_long_kernel(const NormBackw
 #pragma unroll
     for (int v = 0; v < V; ++v) dot = fmaf(g[v] * w[v], x[v] * rs, dot);
   }
-  dot = team_sum(dot, 16, part) / static_cast<float>(a.H);
+  dot = team_sum(dot, 512, 0, part) / static_cast<float>(a.H);
   for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < a.H; c += 512 * V) {
     Piece<T, V> rg, rh, rd{};
     Weights<W, V> rw;
@@ -465,25 +508,38 @@ cudaError_t launch_norm_v(const NormArgs& a, cudaStream_t stream) {
   return launch_norm_p<T, W, V, kFew, OUT>(a, pieces, stream);
 }
 
-// kWide: teams of 1024 threads (log 10) alone.
-template <typename T, typename W, int V, int P, bool kWide>
-cudaError_t launch_backward_p(const NormBackwardArgs& a, int log, int64_t& parts, cudaStream_t stream) {
-  const int64_t per = log == 10 ? 1 : 512 >> log, blocks = (a.rows + per - 1) / per;
-  const int64_t most = log == 10 ? kSms : kMaxParts;
-  parts = blocks < most ? blocks : most;
-  const dim3 grid(static_cast<unsigned>(parts));
-  if constexpr (!kWide)
-    if (log < 10) return launch(norm_backward_kernel<T, W, V, P, 512>, grid, 512, stream, a, log);
-  return launch(norm_backward_kernel<T, W, V, P, 1024>, grid, 1024, stream, a, log);
+// A team's threads: as many warps as a row needs, or 8 or 16 lanes.
+int backward_team(int64_t H, int per_thread) {
+  const int64_t need = (H + per_thread - 1) / per_thread;
+  return need <= 8 ? 8 : need <= 16 ? 16 : static_cast<int>((need + 31) / 32 * 32);
+}
+// A block an SM, of as many teams as 1024 threads hold (of few rows no more than that each has one).
+template <typename T, typename W, int V, int P>
+cudaError_t launch_backward_p(const NormBackwardArgs& a, int64_t& parts, cudaStream_t stream) {
+  const int team = backward_team(a.H, V * P);
+  const int64_t most = 1024 / team, each = (a.rows + kSms - 1) / kSms;
+  const int whole = team < 32 ? 32 / team : 1;  // teams of a warp
+  const int teams = each < most ? static_cast<int>(each + whole - 1) / whole * whole : static_cast<int>(most);
+  const int threads = team * teams;
+  const int64_t blocks = (a.rows + teams - 1) / teams;
+  parts = blocks < kSms ? blocks : kSms;
+  using R = Ring<T, V, P>;
+  const void* kernel = reinterpret_cast<const void*>(norm_backward_kernel<T, W, V, P>);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 * R::kBytes);
+  if (e != cudaSuccess) return e;
+  void* args[] = {const_cast<NormBackwardArgs*>(&a), const_cast<int*>(&team), const_cast<int*>(&teams)};
+  return launch_args(kernel, dim3(static_cast<unsigned>(parts)), threads, static_cast<size_t>(threads) * R::kBytes, stream, args);
 }
 template <typename T, typename W, int V>
 cudaError_t launch_backward_v(const NormBackwardArgs& a, int64_t& parts, cudaStream_t stream) {
-  constexpr bool kVec = V * sizeof(T) == 16;
-  constexpr int kFew = kVec ? 1 : 4, kMost = kVec ? 2 : 8;
-  const int64_t pieces = (a.H + V - 1) / V;
-  if (pieces <= 1024 * kFew)
-    return launch_backward_p<T, W, V, kFew, false>(a, team_log((pieces + kFew - 1) / kFew), parts, stream);
-  if (pieces <= 1024 * kMost) return launch_backward_p<T, W, V, kMost, true>(a, 10, parts, stream);
+  constexpr int kBytes = V * static_cast<int>(sizeof(T)), kFew = kBytes == 16 ? 1 : 4, kMost = 2 * kFew;
+  // The fewer pieces a thread where their teams fill the SM or rows are few; else the more, of
+  // smaller teams (8192 x 4096 bf16: 45.7 us with one piece, 46.1 with two, 8192 x 6144 68.9 and
+  // 64.1, 512 x 8192 12.0 and 13.0).  Rows in registers have room for no more (5000 x 777 19.1 and 31.6).
+  const int team = backward_team(a.H, V * kFew);
+  const bool few = kBytes < 4 || a.rows <= 8 * kSms || 1024 / team * team >= 960;
+  if (team <= 1024 && few) return launch_backward_p<T, W, V, kFew>(a, parts, stream);
+  if (backward_team(a.H, V * kMost) <= 1024) return launch_backward_p<T, W, V, kMost>(a, parts, stream);
   cudaError_t e = launch(norm_backward_long_kernel<T, W, V>, dim3(static_cast<unsigned>(a.rows)), 512, stream, a);
   if (e != cudaSuccess) return e;
   parts = norm_parts(a.rows, a.H);
