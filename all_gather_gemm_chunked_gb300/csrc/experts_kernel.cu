@@ -954,12 +954,12 @@ __device__ void scale_long_role(const ExpertsParams& p, const Table& table,
 // four warps, whose stores take as long as a k-block's MMAs.)
 template <int BN>
 __device__ void copy4_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int lane,
-                           const Guess& guess) {
+                           int turn, const Guess& guess) {
   using Units = Schedule<kOpFp4, BN>;
   Units sch(p, table);
   constexpr int kSlots = scale_slots(BN);
   const int32_t KA = (p.red + 127) / 128;
-  int slot = 0;
+  int slot = 0, next = turn;  // stages until this warp's next
   uint32_t phase = 0;
   bool ok = true;
   Unit u;
@@ -972,21 +972,24 @@ __device__ void copy4_role(const ExpertsParams& p, const Table& table, const Rin
     const int32_t words = (u.cnt + 31) / 32;  // (the accumulator's columns behind them are not stored)
     const uint32_t* const xs = p.xs4 + u.row0 + lane;
     for (int32_t kb = u.kb0; kb < u.kb1; kb += kSub) {
-      ok = mbar_wait(&ring.pempty[slot], phase ^ 1u, p.timeout_ns, ring.abort, p.status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t to = smem_u32(ring.pieces) + slot * row_slot(BN) + lane * 16;
+      if (next-- == 0) {
+        next = kCopyWarps - 1;
+        ok = mbar_wait(&ring.pempty[slot], phase ^ 1u, p.timeout_ns, ring.abort, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t to = smem_u32(ring.pieces) + slot * row_slot(BN) + lane * 16;
 #pragma unroll
-      for (int a = 0; a < kPieces; ++a) {
-        if (kb * 2 + a >= KA) break;  // (no MMA reads the pieces past K)
-        const uint32_t* const from = xs + static_cast<int64_t>(kb * 2 + a) * p.rows;
+        for (int a = 0; a < kPieces; ++a) {
+          if (kb * 2 + a >= KA) break;  // (no MMA reads the pieces past K)
+          const uint32_t* const from = xs + static_cast<int64_t>(kb * 2 + a) * p.rows;
 #pragma unroll
-        for (int j = 0; j < BN / 32; ++j)
-          if (j < words)
-            copy_word(to + (a * row_pieces(BN) + j / 4) * kPiece + j % 4 * 4,
-                      j * 32 + lane < u.cnt ? from + j * 32 : p.xs4, j * 32 + lane < u.cnt);
+          for (int j = 0; j < BN / 32; ++j)
+            if (j < words)
+              copy_word(to + (a * row_pieces(BN) + j / 4) * kPiece + j % 4 * 4,
+                        j * 32 + lane < u.cnt ? from + j * 32 : p.xs4, j * 32 + lane < u.cnt);
+        }
+        arrive_copied(&ring.praw[slot]);
       }
-      arrive_copied(&ring.praw[slot]);
       if (++slot == kSlots) {
         slot = 0;
         phase ^= 1u;
@@ -1711,10 +1714,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     } else if constexpr (OP == kOpFp8Long) {
       scale_long_role<BN>(p, table, ring, rank, lane);
     } else if constexpr (OP == kOpFp4) {
-      if (warp == 2 + kXEpiWarps)
-        copy4_role<BN>(p, table, ring, rank, lane, guess);
+      if (warp < 2 + kXEpiWarps + kCopyWarps)
+        copy4_role<BN>(p, table, ring, rank, lane, warp - (2 + kXEpiWarps), guess);
       else
-        pass4_role<BN>(p, table, ring, rank, lane, warp - (3 + kXEpiWarps), guess);
+        pass4_role<BN>(p, table, ring, rank, lane, warp - (2 + kXEpiWarps + kCopyWarps), guess);
     }
   } else if (threadIdx.x == 0) {
     set_status(p.status + 2, kStatusOffsets, 0);

@@ -31,11 +31,11 @@ __host__ __device__ constexpr int box_height(int tile_rows, int boxes) {
 }
 constexpr int kXSub = 2;       // k-blocks of 128 bytes per stage of the ring
 constexpr int kXEpiWarps = 16;
-constexpr int kPassWarps = 5;
+constexpr int kCopyWarps = 2, kPassWarps = 4;
 // TMA warp, MMA warp, epilogue warps; the weight gradient's zeroing warp, the scale warp
 // of e4m3, or those of e2m1, one that copies and five that pass on.
 __host__ __device__ constexpr int threads_of(int op) {
-  return 32 * (2 + kXEpiWarps + (op == kOpForward || op == kOpInput ? 0 : op == kOpFp4 ? 1 + kPassWarps : 1));
+  return 32 * (2 + kXEpiWarps + (op == kOpForward || op == kOpInput ? 0 : op == kOpFp4 ? kCopyWarps + kPassWarps : 1));
 }
 constexpr int kXGroup = 8;     // row tiles that share the weights they read (tile order)
 
