@@ -115,9 +115,13 @@ __host__ __device__ constexpr int out_buffer(int op) {
 __host__ __device__ constexpr int out_bytes(int op) { return kXEpiWarps * out_buffer(op); }
 constexpr int kTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) & ~15;
 constexpr int kUnitBytes = kXEpiWarps * 48;  // the epilogue warps' units
+// e2m1, long row tiles: the MMA warp takes its units from the TMA warp.  (Four places: the loads
+// are at most three stages ahead, a tile has one or more, and a place is filled once its first
+// stage is free.)
+__host__ __device__ constexpr bool hands_units(int op, int BN) { return op == kOpFp4 && BN == kXRows4; }
 __host__ __device__ constexpr int smem_bytes(int op, int BN) {
   return stages_of(op, BN) * kSub * (kWBytes + r_bytes(BN)) + scale_bytes(op, BN) +
-         out_bytes(op) + kTableBytes + kUnitBytes + 640 /*barriers*/ + 1024 /*alignment*/;
+         out_bytes(op) + kTableBytes + kUnitBytes + 64 + 640 /*barriers*/ + 1024 /*alignment*/;
 }
 static_assert(smem_bytes(kOpForward, kXRows) <= 227 * 1024 && smem_bytes(kOpForward, kXFewRows) <= 227 * 1024 &&
                   smem_bytes(kOpWeight, kXRows) <= 227 * 1024 && smem_bytes(kOpFp8, kXFewRows) <= 227 * 1024 &&
@@ -625,6 +629,7 @@ struct Ring {
                     // (e2m1: a stage's pieces of the weights)
   uint8_t* pieces;  // e2m1, by slot: the rows'
   uint8_t* stage_out;  // a buffer of out_buffer(OP) bytes for each epilogue warp
+  int4* tiles;         // e2m1, long row tiles: the next units, from the TMA warp to the MMA warp
   Unit* units;         // an epilogue warp's unit, beside the sums that fill its registers
   volatile int* abort;
 };
@@ -711,6 +716,7 @@ __device__ void tma_role(const ExpertsParams& p, const Table& table, const Ring&
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (elect_one()) {
+        if (hands_units(OP, BN) && rank == 0 && kb0 == u.kb0) ring.tiles[i & 3] = make_int4(u.kb0, u.kb1, u.w, 0);
         const bool tail = OP == kOpWeight && u.whole - (kb0 + n_sub) * 64 < 0;
         uint32_t bar = full0 + stage * 8;
         if (tail) {
@@ -1066,7 +1072,18 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
     return r;
   };
   Unit u;
-  for (int32_t i = 0; ok && sch.get(i, u); ++i) {
+  // (Working a unit out takes as long as the MMAs of a stage, and the tensor cores would wait.)
+  auto next_unit = [&](int32_t i) {
+    if constexpr (!hands_units(OP, BN)) return sch.get(i, u);
+    if (static_cast<int64_t>(i) * sch.pairs + sch.pair >= sch.units) return false;
+    if (!(ok = warp_wait(&ring.full[stage], (full_phase >> stage) & 1u, p.timeout_ns, ring.abort, p.status))) return false;
+    const int4 t = ring.tiles[i & 3];
+    u.kb0 = t.x;
+    u.kb1 = t.y;
+    u.w = t.z;
+    return true;
+  };
+  for (int32_t i = 0; ok && next_unit(i); ++i) {
     const int32_t kb_end = uniform(u.kb1), kb_begin = uniform(u.kb0), width = uniform(u.w);
     [[maybe_unused]] const int32_t red_rows = uniform(u.red_rows), whole = uniform(u.whole);
     const uint32_t idesc = idesc_f16_f32(kXWide, width, kWMn, kRMn) |
@@ -1630,7 +1647,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   int32_t* off = reinterpret_cast<int32_t*>(ring.stage_out + out_bytes(OP));
   int32_t* pre = off + kMaxExperts + 1;
   ring.units = reinterpret_cast<Unit*>(reinterpret_cast<uint8_t*>(off) + kTableBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ring.units) + kUnitBytes);
+  ring.tiles = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(ring.units) + kUnitBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring.tiles + 4);
   ring.full = bars;
   ring.empty = bars + kStagesX;
   ring.tfull = bars + 2 * kStagesX;
