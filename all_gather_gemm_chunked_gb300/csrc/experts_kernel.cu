@@ -146,15 +146,15 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uin
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// The same of e2m1 operands (K = 64) with a scale for each 32 elements in TMEM.
-__device__ __forceinline__ void mma_f4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+// The same of e2m1 operands (K = 64) with a scale for each 32 elements in TMEM; of the
+// operands' descriptors the low words, and the high one that they share.
+__device__ __forceinline__ void mma_f4_pair(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc,
                                             uint32_t a_scales, uint32_t b_scales, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-          d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %7, 0;\n\tmov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %4, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
       : "memory");
 }
 // Instruction descriptor: e2m1 A and B (format 1), scales e8m0 (bit 23); the scales of an
@@ -163,13 +163,13 @@ __device__ __forceinline__ uint32_t idesc_f4(int n, uint32_t id) {
   return (id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
          (static_cast<uint32_t>(kXWide >> 4) << 24) | (id << 29);
 }
-// A piece of scales to 4 TMEM columns, in both CTAs from each one's own shared memory:
+// A piece of scales (its address in units of 16) to 4 TMEM columns, in both CTAs from each one's own shared memory:
 // 32 lanes of 16 bytes (8 of them 128 bytes apart, no swizzle), the same for the four
 // quarters of the lanes.
-__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint32_t saddr) {
-  const uint64_t desc = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
-                        (static_cast<uint64_t>(1) << 46);
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint32_t from16) {
+  asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\ttcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(tmem),
+               "r"(from16), "n"((128 >> 4) | (1 << 14))
+               : "memory");
 }
 __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* map, uint32_t bar,
                                                  int32_t x, int32_t y, int32_t z, int32_t w) {
@@ -1045,8 +1045,7 @@ __device__ void pass4_role(const ExpertsParams& p, const Table& table, const Rin
 // The warp waits and computes together; lane 0 issues.
 template <int OP, int BN>
 __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring& ring,
-                         int lane, uint32_t tmem, const Guess& guess) {
-  if constexpr (Schedule<OP, BN>::kShares) settle<OP, BN>(p, guess);
+                         int lane, uint32_t tmem) {
   Schedule<OP, BN> sch(p, table);
   constexpr int kStagesX = stages_of(OP, BN);
   constexpr bool kWMn = OP == kOpForward || OP == kOpWeight;
@@ -1062,8 +1061,6 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
   constexpr uint32_t kWSecond = (kWMn ? 64 * 128 : kWBytes) / 16;  // the second k-block
   int stage = 0;
   uint32_t acc = 0, full_phase = 0, zeroed = 0;  // bit s: parity of stage s's barriers
-  [[maybe_unused]] int slot = 0;  // e2m1: of the rows' scales
-  [[maybe_unused]] uint32_t slot_phase = 0;
   bool ok = true;
   auto accumulator = [&] {  // wait until it has been read
     const bool r = warp_wait(&ring.tempty[acc & 1u], ((acc >> 1) & 1u) ^ 1u, p.timeout_ns, ring.abort,
@@ -1072,18 +1069,7 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
     return r;
   };
   Unit u;
-  // (Working a unit out takes as long as the MMAs of a stage, and the tensor cores would wait.)
-  auto next_unit = [&](int32_t i) {
-    if constexpr (!hands_units(OP, BN)) return sch.get(i, u);
-    if (static_cast<int64_t>(i) * sch.pairs + sch.pair >= sch.units) return false;
-    if (!(ok = warp_wait(&ring.full[stage], (full_phase >> stage) & 1u, p.timeout_ns, ring.abort, p.status))) return false;
-    const int4 t = ring.tiles[i & 3];
-    u.kb0 = t.x;
-    u.kb1 = t.y;
-    u.w = t.z;
-    return true;
-  };
-  for (int32_t i = 0; ok && next_unit(i); ++i) {
+  for (int32_t i = 0; ok && sch.get(i, u); ++i) {
     const int32_t kb_end = uniform(u.kb1), kb_begin = uniform(u.kb0), width = uniform(u.w);
     [[maybe_unused]] const int32_t red_rows = uniform(u.red_rows), whole = uniform(u.whole);
     const uint32_t idesc = idesc_f16_f32(kXWide, width, kWMn, kRMn) |
@@ -1112,9 +1098,6 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
       } else {
         ok = warp_wait(&ring.full[stage], (full_phase >> stage) & 1u, p.timeout_ns, ring.abort,
                        p.status);
-        if (OP == kOpFp4 && ok)  // and the rows' scales, from both CTAs' scale warps
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&ring.pfull[slot], slot_phase, p.timeout_ns, ring.abort,
-                                                         p.status));
         full_phase ^= 1u << stage;
       }
       if (!ok) break;
@@ -1127,30 +1110,6 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
         if (OP == kOpFp8Long && !(ok = accumulator())) break;
         const uint32_t d = tmem + (acc & 1u) * acc_cols(OP) +
                            (OP == kOpFp8 ? (kFewBlocks - left + s) * kXFewRows : 0);
-        if constexpr (OP == kOpFp4) {
-          const int32_t rest = (p.red - (kb0 + s) * 256 + 63) / 64, steps = rest < 4 ? rest : 4;
-          const uint32_t sf = tmem + kScaleCol + s * kScaleCols;
-          const uint32_t from = smem_u32(ring.scales) + (stage * kPieces + 2 * s) * kPiece;
-          const uint32_t rows_from = smem_u32(ring.pieces) + slot * row_slot(BN) + 2 * s * row_pieces(BN) * kPiece;
-          if (elect_one()) {
-#pragma unroll
-            for (int a = 0; a < 2; ++a)
-              if (2 * a < steps) {
-                copy_scales_pair(sf + 4 * a, from + a * kPiece);
-#pragma unroll
-                for (int r = 0; r < row_pieces(BN); ++r)
-                  if (r * 128 < width)
-                    copy_scales_pair(sf + 8 + 8 * a + 4 * r, rows_from + (a * row_pieces(BN) + r) * kPiece);
-              }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < steps)
-                mma_f4_pair(d, ws + (s * kWSecond + k * kWStep), rs + (s * r_second + k * kRStep),
-                            idesc_f4(width, 2 * (k & 1)), sf + 4 * (k >> 1), sf + 8 + 8 * (k >> 1),
-                            (!first || s > 0 || k > 0) ? 1u : 0u);
-          }
-          continue;
-        }
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -1169,11 +1128,6 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
       if (!ok) break;
       if (elect_one()) {
         mma_commit_pair_both(&ring.empty[stage]);
-        if (OP == kOpFp4) mma_commit_pair_both(&ring.pempty[slot]);
-      }
-      if (OP == kOpFp4 && ++slot == scale_slots(BN)) {
-        slot = 0;
-        slot_phase ^= 1u;
       }
       if (++stage == kStagesX) stage = 0;
       if (OP != kOpFp8Long) {
@@ -1185,6 +1139,113 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
         }
       }
       __syncwarp();
+    }
+  }
+  if (!ok && lane == 0) {
+    set_status(p.status, kStatusPipelineTimeout, 0x200u);
+    *ring.abort = 1;
+  }
+}
+
+// The same for e2m1: a stage's scales to TMEM, then its MMAs, in the order of the one thread
+// that issues both.  What bounds a stage is that thread: its 23 instructions for the tensor
+// cores and those around them take longer than the tensor cores with all but the longest row
+// tiles.  So a stage of whole k-blocks has no branch, descriptors are made by their low words,
+// and units of long row tiles come from the TMA warp.
+template <int BN>
+__device__ void mma4_role(const ExpertsParams& p, const Table& table, const Ring& ring, int lane, uint32_t tmem,
+                          const Guess& guess) {
+  constexpr bool kHanded = hands_units(kOpFp4, BN);
+  if constexpr (Schedule<kOpFp4, BN>::kShares) settle<kOpFp4, BN>(p, guess);
+  Schedule<kOpFp4, BN> sch(p, table);
+  constexpr int kStagesX = stages_of(kOpFp4, BN);
+  // K-major, 128-byte swizzle: groups of 8 rows 1024 B apart, 32 B further per step.
+  const uint64_t desc = smem_desc_sw128(smem_u32(ring.w), 16, 1024);
+  const uint32_t high = uniform(static_cast<uint32_t>(desc >> 32)), w0 = uniform(static_cast<uint32_t>(desc)),
+                 r0 = uniform(static_cast<uint32_t>(smem_desc_sw128(smem_u32(ring.r), 16, 1024))),
+                 ws0 = uniform(smem_u32(ring.scales) >> 4), rs0 = uniform(smem_u32(ring.pieces) >> 4);
+  constexpr uint32_t kRowPieces = row_pieces(BN) * kPiece / 16;  // of 128 elements
+  int stage = 0, slot = 0;
+  uint32_t acc = 0, phase = 0, slot_phase = 0;
+  bool ok = true;
+  Unit u;
+  auto next_unit = [&](int32_t i) {
+    if constexpr (!kHanded) return sch.get(i, u);
+    if (static_cast<int64_t>(i) * sch.pairs + sch.pair >= sch.units) return false;
+    if (!(ok = warp_wait(&ring.full[stage], phase, p.timeout_ns, ring.abort, p.status))) return false;
+    const int4 t = ring.tiles[i & 3];
+    u.kb0 = t.x;
+    u.kb1 = t.y;
+    u.w = t.z;
+    return true;
+  };
+  for (int32_t i = 0; ok && next_unit(i); ++i) {
+    const int32_t kb_end = uniform(u.kb1), kb_begin = uniform(u.kb0), width = uniform(u.w);
+    const uint32_t idesc0 = idesc_f4(width, 0), idesc2 = idesc_f4(width, 2);
+    const uint32_t r_second = static_cast<uint32_t>(box_height(BN, box_of<BN>(width / 2)) * 128 / 16);
+    const bool wide = BN > 128 && width > 128;
+    int32_t left = 0;  // k-blocks left of the segment
+    for (int32_t kb = kb_begin; kb < kb_end; kb += kSub) {
+      const uint32_t add = left > 0 ? 1u : 0u, d = tmem + (acc & 1u) * acc_cols(kOpFp4);
+      if (left <= 0) {  // an accumulator that has been read
+        ok = warp_wait(&ring.tempty[acc & 1u], ((acc >> 1) & 1u) ^ 1u, p.timeout_ns, ring.abort, p.status);
+        if (!ok) break;
+        left = p.segment;
+      }
+      ok = warp_wait(&ring.full[stage], phase, p.timeout_ns, ring.abort, p.status);
+      if (ok)  // and the rows' scales, from both CTAs' warps
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&ring.pfull[slot], slot_phase, p.timeout_ns, ring.abort, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t w = w0 + stage * (kSub * kWBytes / 16), r = r0 + stage * (kSub * r_bytes(BN) / 16);
+      const uint32_t ws = ws0 + stage * (kPieces * kPiece / 16), rs = rs0 + slot * (row_slot(BN) / 16);
+      const uint32_t sf = tmem + kScaleCol;
+      left = kb + kSub >= kb_end ? 0 : left - kSub;
+      if (elect_one()) {
+        auto scales = [&](int s, int a) {
+          const uint32_t to = sf + s * kScaleCols;
+          copy_scales_pair(to + 4 * a, ws + (2 * s + a) * (kPiece / 16));
+          copy_scales_pair(to + 8 + 8 * a, rs + (2 * s + a) * kRowPieces);
+          if (wide) copy_scales_pair(to + 12 + 8 * a, rs + (2 * s + a) * kRowPieces + kPiece / 16);
+        };
+        auto mma = [&](int s, int k) {
+          const uint32_t from = sf + s * kScaleCols;
+          mma_f4_pair(d, w + s * (kWBytes / 16) + 2 * k, r + s * r_second + 2 * k, high, k & 1 ? idesc2 : idesc0,
+                      from + 4 * (k >> 1), from + 8 + 8 * (k >> 1), s > 0 || k > 0 ? 1u : add);
+        };
+        const int32_t rest = p.red - kb * 256;
+        if (kb + kSub <= kb_end && rest >= kSub * 256) {
+#pragma unroll
+          for (int s = 0; s < kSub; ++s) {
+            scales(s, 0);
+            scales(s, 1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma(s, k);
+          }
+        } else {
+          for (int s = 0; s < kSub; ++s) {
+            if (kb + s >= kb_end) break;
+            const int32_t steps = (rest - s * 256 + 63) / 64;
+            for (int a = 0; a < 2; ++a)
+              if (2 * a < steps) scales(s, a);
+            for (int k = 0; k < 4; ++k)
+              if (k < steps) mma(s, k);
+          }
+        }
+        mma_commit_pair_both(&ring.empty[stage]);
+        mma_commit_pair_both(&ring.pempty[slot]);
+        if (left <= 0) mma_commit_pair_both(&ring.tfull[acc & 1u]);
+      }
+      __syncwarp();
+      if (left <= 0) ++acc;
+      if (++slot == scale_slots(BN)) {
+        slot = 0;
+        slot_phase ^= 1u;
+      }
+      if (++stage == kStagesX) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
   }
   if (!ok && lane == 0) {
@@ -1716,10 +1777,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     if (warp == 0) {
       tma_role<OP, BN>(p, table, ring, rank, lane, guess);
     } else if (warp == 1) {
-      if (rank == 0)
-        mma_role<OP, BN>(p, table, ring, lane, tmem, guess);
-      else if constexpr (kGuess)
-        settle<OP, BN>(p, guess);
+      if constexpr (OP == kOpFp4) {
+        if (rank == 0)
+          mma4_role<BN>(p, table, ring, lane, tmem, guess);
+        else if constexpr (kGuess)
+          settle<OP, BN>(p, guess);
+      } else if (rank == 0) {
+        mma_role<OP, BN>(p, table, ring, lane, tmem);
+      }
     } else if (warp < 2 + kXEpiWarps) {
       if constexpr (OP == kOpFp8Long)
         epilogue_long<BN>(p, table, ring, rank, warp - 2, lane, tmem);
