@@ -240,6 +240,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64
 }
 
 // 32 TMEM lanes x 8 columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
@@ -1303,6 +1308,32 @@ struct Out {
   }
 };
 
+// A warp's columns of 16-bit output, in eights: two rows of a column to a word.
+template <int COLS>
+__device__ __forceinline__ void store_pairs(uint8_t* stage, void* base, int64_t ldo, int64_t at, bool f16, int n8, int rows,
+                                            bool in_cols, const float (&v)[COLS], int lane) {
+  const int row = lane >> 2;
+  uint16_t* to = static_cast<uint16_t*>(base) + at + row * ldo + (lane & 3) * 8;
+  const uint32_t half = row & 1 ? 0x7632u : 0x5410u;
+#pragma unroll
+  for (int c = 0; c < COLS / 8; ++c)
+    if (c < n8) {
+      uint32_t* s = reinterpret_cast<uint32_t*>(stage) + lane;
+      __syncwarp();  // the buffer has been read
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s[i * 32] = f16 ? Elem<__half>::pair(v[c * 8 + 2 * i], v[c * 8 + 2 * i + 1])
+                        : Elem<__nv_bfloat16>::pair(v[c * 8 + 2 * i], v[c * 8 + 2 * i + 1]);
+      __syncwarp();
+      const uint4* from = reinterpret_cast<const uint4*>(stage + (row >> 1) * 128 + (lane & 3) * 32);
+      const uint4 x = from[0], y = from[1];
+      if (c * 8 + row < rows && in_cols)
+        *reinterpret_cast<uint4*>(to) = make_uint4(__byte_perm(x.x, x.y, half), __byte_perm(x.z, x.w, half),
+                                                   __byte_perm(y.x, y.y, half), __byte_perm(y.z, y.w, half));
+      to += 8 * ldo;
+    }
+}
+
 // 16 columns of an output row in one store of 32 bytes (16-bit outputs whose rows are
 // 32-byte aligned): whole sectors, half the instructions.
 __device__ __forceinline__ void store_row16(void* base, int type, int64_t at, const float (&v)[16]) {
@@ -1539,8 +1570,10 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table, const 
   uint32_t acc = 0;
   for (int32_t i = 0;; ++i) {
     float sums[kCols];
+    if (OP != kOpFp4) {
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) sums[c] = 0.0f;
+      for (int c = 0; c < kCols; ++c) sums[c] = 0.0f;
+    }
     {
       Unit u;
       if (!Schedule<OP, BN>(p, table).get(i, u)) break;
@@ -1556,7 +1589,27 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table, const 
       const uint32_t from0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c_first;
       const uint32_t tempty0 = mapa_shared(smem_u32(ring.tempty), 0);
       const int32_t seg = OP == kOpFp8 ? kFewBlocks : p.segment;
-      for (int32_t left = u.kb1 - u.kb0; left > 0; left -= seg, ++acc) {
+      int32_t left = u.kb1 - u.kb0;
+      if constexpr (OP == kOpFp4) {
+        // the first segment straight to the sums, in one wait (all columns that a tile can have:
+        // those past its width are not stored)
+        const uint32_t slot = acc & 1u;
+        if (!warp_wait(&ring.tfull[slot], (acc >> 1) & 1u, p.timeout_ns, ring.abort, p.status)) {
+          set_status(p.status, kStatusPipelineTimeout, 0x300u | rank);
+          *ring.abort = 1;
+          return;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kCols; c += 8) tmem_ld8(from0 + slot * acc_cols(OP) + c, &sums[c]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(tempty0 + slot * 8);
+        left -= seg;
+        ++acc;
+      }
+      for (; left > 0; left -= seg, ++acc) {
         const uint32_t slot = acc & 1u, phase = (acc >> 1) & 1u;
         bool ok = true;
         if constexpr (OP == kOpFp8)
@@ -1646,6 +1699,11 @@ __device__ void epilogue_role(const ExpertsParams& p, const Table& table, const 
       for (int j = 0; j < 8; ++j) v[j] = sums[c * 8 + j];
     };
     if (split == 1) {
+      if (OP == kOpFp4 && p.out_type != kTypeF32) {
+        store_pairs(out.stage, p.out, p.ldo, (static_cast<int64_t>(u.row0) + c_first) * p.ldo + col, p.out_type == kTypeF16, n8,
+                    u.cnt - c_first, (lane & 3) * 8 < p.wide - col, sums, lane);
+        continue;
+      }
 #pragma unroll
       for (int c = 0; c < kCols / 8; ++c)
         if (c < n8) {
