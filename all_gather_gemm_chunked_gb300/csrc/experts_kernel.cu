@@ -25,8 +25,8 @@
 //   warps 2-17  epilogue: TMEM lane quadrant warp % 4, a quarter of the tile's columns
 //   warp 18     weight gradient: zeros over the rows behind a group's end;
 //               e4m3: the scales of each k-block into shared memory
-//               e2m1: the rows' scales into shared memory, as the tensor core takes them;
-//   warps 19-23 e2m1: pass them on
+//   warps 18-19 e2m1: the rows' scales into shared memory, as the tensor core takes them;
+//   warps 20-23 pass them on
 //
 // Work: tiles in expert order, and inside an expert in groups of 8 row tiles by all
 // wide tiles, so that the tiles in flight share operands in L2.  Unit u of pair p is
@@ -49,7 +49,7 @@
 // rows by 4 scales, 512 bytes, that tcgen05.cp brings from shared memory, in order with
 // the MMAs that the same thread issues.  The weights' pieces lie ready in memory and come
 // by TMA with their codes.  The rows' do not: a group begins at any row, so they are kept
-// as words of four scales, [128 elements of K][row], and a warp copies the tile's words
+// as words of four scales, [128 elements of K][row], and two warps copy the tile's words
 // into the pieces' order.  Two accumulators of 224 columns leave TMEM columns for the scales of
 // two k-blocks.
 //
@@ -64,7 +64,10 @@
 // as long as its MMAs take the tensor cores); weight gradient to fp32 175 us; 64 rows on
 // 32 experts of 4096 x 4096 131 us (the hit weights at 6.9 TB/s).  e4m3: the same product
 // 126 us (2.2 PFLOP/s; bound by the epilogue's work on each k-block), 64 rows of 16384 x
-// 7168 28 us (4.2 TB/s of weights: 28 tiles in two parts are 56 units for 76 pairs).  A
+// 7168 28 us (4.2 TB/s of weights: 28 tiles in two parts are 56 units for 76 pairs).  e2m1:
+// 8192 x 4096 x 4096 54 us (5.1 PFLOP/s), 8192 x 16384 x 8192 330 us (6.7 PFLOP/s: a stage of
+// 63 KB takes 0.58 us, so that all SMs take in 16 TB/s); 64 rows on 32 experts of 4096 x 4096
+// 43 us (5.8 TB/s), of 16384 x 7168 18.3 us; 8192 on 32 experts of 4096 x 7168 140 us.  A
 // call of one tile, repeated, takes 4.4 us, with inputs that change 5.2.
 //
 // Every wait is bounded; on a timeout the kernel records a status word, drains what
@@ -115,7 +118,8 @@ __host__ __device__ constexpr int out_buffer(int op) {
 __host__ __device__ constexpr int out_bytes(int op) { return kXEpiWarps * out_buffer(op); }
 constexpr int kTableBytes = (2 * (kMaxExperts + 1) * 4 + 15) & ~15;
 constexpr int kUnitBytes = kXEpiWarps * 48;  // the epilogue warps' units
-// e2m1, long row tiles: the MMA warp takes its units from the TMA warp.  (Four places: the loads
+// e2m1, long row tiles: the MMA warp takes its units from the TMA warp (8192 rows on 32 experts of
+// 4096 x 7168 168.9 us, so 163.1: working one out takes as long as a stage).  (Four places: the loads
 // are at most three stages ahead, a tile has one or more, and a place is filled once its first
 // stage is free.)
 __host__ __device__ constexpr bool hands_units(int op, int BN) { return op == kOpFp4 && BN == kXRows4; }
@@ -346,7 +350,7 @@ __device__ __forceinline__ int32_t quotient(int32_t n, int32_t d) {
 // stages of all tiles, which follow one another tile by tile, so that a tile's sum is cut
 // wherever a pair's share ends.  (An SM takes in about 50 GB/s of what is not in L2, so
 // weights stream at the memory's rate only where all of them read: 64 rows of 16384 x 7168,
-// 28 tiles, in two parts each 20.8 us.)  Lanes 0 to 15 try shares of a tile's stages over 1
+// 28 tiles, took 20.8 us in two parts each and 18.7 in shares of 12 stages.)  Lanes 0 to 15 try shares of a tile's stages over 1
 // to 16, lane 16 the least.  Returns the share, 0 for whole tiles in rounds.
 __device__ __forceinline__ int32_t choose_share(int32_t tiles, int32_t stages, int32_t max_units, SplitPrice price) {
   const int32_t pairs = static_cast<int32_t>(gridDim.x / 2);
@@ -954,11 +958,11 @@ __device__ void scale_long_role(const ExpertsParams& p, const Table& table,
 // ------------------------------------------------------------------ scales (e2m1)
 // The tile's rows' scales of each stage, as pieces of 128 rows: row r's word at (r % 32) *
 // 16 + (r / 32) * 4.  Both CTAs hold those of all rows (each multiplies its half of the
-// columns with all of them).  One warp copies the words to their places, and others pass on
+// columns with all of them).  Two warps copy the words to their places, and four pass on
 // what has landed, by turns: the release for the pair takes a warp about a microsecond
 // under load and two where weights stream in, as long as the MMAs of several stages (64 rows
-// of 16384 x 7168 22.7 us with two such warps, 20.8 with five; 24 warps need no fewer
-// registers than 21).  The pieces have a ring of their own, longer than the operands',
+// of 16384 x 7168 took 22.7 us with two such warps, 20.8 with five; 8512 of 4096 x 4096 65.3 with
+// one and five, 62.8 with two and four, 64.2 with a warp more).  The pieces have a ring of their own, longer than the operands',
 // which covers both ways' latencies.
 // (8192 x 16384 x 8192: 740 us where a warp loads and stores the words itself; 465 with one
 // warp that passes on, in the operands' ring; 480 to 560 with the words stored to TMEM by
@@ -1153,10 +1157,11 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
 }
 
 // The same for e2m1: a stage's scales to TMEM, then its MMAs, in the order of the one thread
-// that issues both.  What bounds a stage is that thread: its 23 instructions for the tensor
-// cores and those around them take longer than the tensor cores with all but the longest row
-// tiles.  So a stage of whole k-blocks has no branch, descriptors are made by their low words,
-// and units of long row tiles come from the TMA warp.
+// that issues both.  With the general role its 23 instructions for the tensor cores and those
+// around them took 0.67 us a stage whatever the tile's width; now 0.58, where the operands' way
+// from L2 takes over (224 rows; less with fewer).  So a stage of whole k-blocks has no branch,
+// descriptors are made by their low words, and units of long row tiles come from the TMA warp.
+// (8512 x 4096 x 4096 61.7 us, so 54.4; 8192 rows on 32 experts of 4096 x 7168 162.9 and 140.3.)
 template <int BN>
 __device__ void mma4_role(const ExpertsParams& p, const Table& table, const Ring& ring, int lane, uint32_t tmem,
                           const Guess& guess) {
@@ -1308,7 +1313,9 @@ struct Out {
   }
 };
 
-// A warp's columns of 16-bit output, in eights: two rows of a column to a word.
+// A warp's columns of 16-bit output, in eights: two rows of a column to a word.  (Where sums are
+// short the epilogue bounds the kernel: 8512 x 1024 x 4096 34.8 us with single elements and a wait
+// for each eight's load, so 28.3.)
 template <int COLS>
 __device__ __forceinline__ void store_pairs(uint8_t* stage, void* base, int64_t ldo, int64_t at, bool f16, int n8, int rows,
                                             bool in_cols, const float (&v)[COLS], int lane) {

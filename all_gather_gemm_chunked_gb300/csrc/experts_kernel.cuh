@@ -33,7 +33,7 @@ constexpr int kXSub = 2;       // k-blocks of 128 bytes per stage of the ring
 constexpr int kXEpiWarps = 16;
 constexpr int kCopyWarps = 2, kPassWarps = 4;
 // TMA warp, MMA warp, epilogue warps; the weight gradient's zeroing warp, the scale warp
-// of e4m3, or those of e2m1, one that copies and five that pass on.
+// of e4m3, or those of e2m1, two that copy and four that pass on.
 __host__ __device__ constexpr int threads_of(int op) {
   return 32 * (2 + kXEpiWarps + (op == kOpForward || op == kOpInput ? 0 : op == kOpFp4 ? kCopyWarps + kPassWarps : 1));
 }

@@ -245,13 +245,15 @@ int64_t most_row_tiles(const ag_moe_plan* p, int64_t rows, bool few) {
 // Short row tiles where the groups are short on average: 64 rows a tile leave ten
 // stages for the weights in flight, 256 read the weights once where a group is longer.
 // (32 experts of 4096 x 4096, bf16: 64 rows each 166 us short, 167 long, 80 rows 177 and
-// 169; e4m3: 80 rows 118 and 130, 96 rows 130 and 131, 128 rows 155 and 135.)
+// 169; e4m3: 80 rows 118 and 130, 96 rows 130 and 131, 128 rows 155 and 135; e2m1: 64 rows 52
+// and 53, 80 rows 67 and 54.)
 // And where all of them run at once: a k-block of 256 rows takes 0.23 us, of 64 0.14.
 // (One expert, 200 rows of 1024 x 2048, 32 short tiles: 7.5 us against 10.7; e4m3 7.3
 // against 10.1.  In two rounds of short tiles 1200 rows of 1024 x 2048 took 10.7 against
-// 12.1 us, 600 of 2048 x 3000 18.4 against 15.0; e4m3 1088 of 4096 x 2048 22.2 against 21.2.)
+// 12.1 us, 600 of 2048 x 3000 18.4 against 15.0; e4m3 1088 of 4096 x 2048 22.2 against 21.2.
+// e2m1: 128 of 4096 x 4096 8.2 against 10.0, in two rounds 512 of 4096 x 4096 12.8 against 11.8.)
 bool few_rows(const ag_moe_plan* p, int64_t rows, int64_t wide) {
-  return rows <= static_cast<int64_t>(scaled(p->dtype) ? 96 : 64) * p->E ||
+  return rows <= static_cast<int64_t>(p->dtype == AG_MOE_E4M3 ? 96 : 64) * p->E ||
          most_row_tiles(p, rows, true) * ((wide + agg::kXWide - 1) / agg::kXWide) <= p->pairs;
 }
 

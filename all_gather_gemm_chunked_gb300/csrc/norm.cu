@@ -12,6 +12,10 @@
 // of its floats' registers) while its sum goes through the team of threads that shares it;
 // sums and everything between the loads and the stores are floats.  y is rounded once, to
 // the rows' type or to codes (put_codes).
+//
+// Measured, 8192 x 4096 bf16: with the residual 40.1 us (6.7 TB/s), without 22.2 (6.1), with it and
+// to e4m3 37.0 (6.4), to 4 bits 38.5 (5.7); gradient 47.0 (5.7 TB/s: its second launch and the end
+// of the first take 5 us).  64 x 7168 with the residual 2.7 us.
 
 #include <type_traits>
 
