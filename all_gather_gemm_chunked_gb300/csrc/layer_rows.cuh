@@ -192,6 +192,80 @@ __device__ __forceinline__ void put_codes(const CodePlace<OUT>& at, bool in, flo
   }
 }
 
+// Rows that begin anywhere.  A frame is 16 bytes' worth of elements, V of them; frames lie so
+// that those of the output are aligned, and lanes 0 to 30 of a warp have 31 neighbouring ones.
+// An operand's elements of a frame lie in two aligned 16-byte pieces: the lane's own, and the
+// next lane's (lane 31 has no frame, only a piece).  Pieces that are not all of the row are
+// read, and frames written, element by element.
+constexpr int kFrames = 31;
+// A frame's elements out of two neighbouring pieces, from the d-th on (the same d in all lanes).
+template <typename T>
+__device__ __forceinline__ Piece<T, 16 / sizeof(T)> from_pieces(uint32_t (&w)[8], int d) {
+  const int words = d * static_cast<int>(sizeof(T)) / 4;
+  if (words & 2)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (words & 1)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  Piece<T, 16 / sizeof(T)> p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p.w[i] = sizeof(T) == 2 ? __funnelshift_r(w[i], w[i + 1], (d & 1) * 16) : w[i];
+  return p;
+}
+template <typename T>
+struct Anywhere {
+  static constexpr int V = 16 / sizeof(T);
+  const T* row;
+  int H, d;  // elements of the row; of a frame's start past an aligned address
+  __device__ __forceinline__ Anywhere(const T* row_, int64_t H_, int c)
+      : row(row_), H(static_cast<int>(H_)),
+        d(static_cast<int>((reinterpret_cast<uintptr_t>(row_ + c) & 15) / sizeof(T))) {}
+  // The piece of the frame at column c: all of the row, or made of what is, and zeros.
+  __device__ __forceinline__ bool whole(int c) const { return c - d >= 0 && c - d + V <= H; }
+  __device__ __forceinline__ Piece<T, V> part(int c) const {
+    Piece<T, V> p{};
+    const int a = c - d;
+    if (a < H && a + V > 0) {
+      T e[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) e[v] = a + v >= 0 && a + v < H ? row[a + v] : T(0.0f);
+      __builtin_memcpy(p.w, e, 16);
+    }
+    return p;
+  }
+  __device__ __forceinline__ Piece<T, V> ask(int c) const {
+    if (!whole(c)) return part(c);
+    Piece<T, V> p;
+    p.load(row + c - d);
+    return p;
+  }
+  // The frame of the pieces (all lanes of the warp).
+  __device__ __forceinline__ Piece<T, V> frame(const Piece<T, V>& own) const {
+    if (d == 0) return own;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = own.w[i];
+      w[4 + i] = __shfl_down_sync(0xffffffffu, own.w[i], 1);
+    }
+    return from_pieces<T>(w, d);
+  }
+};
+// A frame at column c of a row of H elements, from lanes that have one.
+template <typename T, int V>
+__device__ __forceinline__ void store_frame(T* row, int H, int c, const Piece<T, V>& p) {
+  if ((reinterpret_cast<uintptr_t>(row + c) & 15) == 0 && c >= 0 && c + V <= H) {
+    p.store(row + c);
+    return;
+  }
+  T e[V];
+  __builtin_memcpy(e, p.w, 16);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (c + v >= 0 && c + v < H) row[c + v] = e[v];
+}
+
 // The sum over a team's threads (whole warps, `first` of the block's on, or 8 or 16 lanes of
 // one; `part` has a float for each warp of the block), the same in every thread and every call.
 __device__ __forceinline__ float team_sum(float v, int team, int first, float* part) {

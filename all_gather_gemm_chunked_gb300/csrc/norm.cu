@@ -193,6 +193,64 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int team, 
   }
 }
 
+// Rows of any alignment, by frames: a team of whole warps has a row, P frames a lane, several
+// teams a block.
+template <typename T, typename W, int P>
+__global__ void __launch_bounds__(1024) norm_frames_kernel(const NormArgs a, int team_warps) {
+  constexpr int V = 16 / sizeof(T);
+  pdl_enter();
+  __shared__ float part[2][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, number = warp / team_warps, first = number * team_warps;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * ((blockDim.x >> 5) / team_warps) + number;
+  const bool valid = row < a.rows;
+  const int H = valid ? static_cast<int>(a.H) : 0, step = team_warps * kFrames * V;
+  T* const y = static_cast<T*>(a.out) + row * a.H;
+  const int c0 = ((warp - first) * kFrames + lane) * V - static_cast<int>((reinterpret_cast<uintptr_t>(y) & 15) / sizeof(T));
+  const Anywhere<T> x(static_cast<const T*>(a.x) + row * a.ldx, H, c0);
+  Piece<T, V> h[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) h[i] = x.ask(c0 + i * step);
+  if (a.residual) {
+    const Anywhere<T> res(static_cast<const T*>(a.residual) + row * a.ldr, H, c0);
+    Piece<T, V> r[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) r[i] = res.ask(c0 + i * step);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      h[i] = x.frame(h[i]);
+      add_residual(h[i], res.frame(r[i]));
+      if (lane < kFrames) store_frame(static_cast<T*>(a.h) + row * a.H, H, c0 + i * step, h[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) h[i] = x.frame(h[i]);
+  }
+  // (what lies outside the row is zero; lane 31's frames are the next warp's)
+  const float rstd = team_rstd(a, team_warps, first, part, [&](float scale) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) sum = squares(h[i], scale, sum);
+    return lane < kFrames ? sum : 0.0f;
+  });
+  if (a.rstd && threadIdx.x == first * 32 && valid) a.rstd[row] = rstd;
+  if (lane >= kFrames) return;
+  const W* const weight = static_cast<const W*>(a.weight);
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int c = c0 + i * step;
+    if (c >= H) break;
+    float f[V], w[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) w[v] = c + v >= 0 && c + v < H ? Elem<W>::get(weight[c + v]) : 0.0f;
+    h[i].get(f);
+#pragma unroll
+    for (int v = 0; v < V; ++v) f[v] = f[v] * rstd * w[v];
+    Piece<T, V> p;
+    p.put(f);
+    store_frame(y, H, c, p);
+  }
+}
+
 // A block has a row of any length, which it reads twice.
 template <typename T, typename W, int V, int OUT>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
@@ -512,6 +570,23 @@ cudaError_t launch_norm_v(const NormArgs& a, cudaStream_t stream) {
   return launch_norm_p<T, W, V, kFew, OUT>(a, pieces, stream);
 }
 
+template <typename T, typename W>
+cudaError_t launch_norm_frames(const NormArgs& a, cudaStream_t stream) {
+  constexpr int V = 16 / sizeof(T), kWarp = kFrames * V;
+  const int64_t warps = (a.H + V - 1 + kWarp - 1) / kWarp;  // of one frame a lane
+  if (warps > 32 * 4)
+    return launch(norm_long_kernel<T, W, 1, kTypeF32>, dim3(static_cast<unsigned>(a.rows)), 1024, stream, a);
+  auto go = [&](auto kernel, int64_t P) {
+    const int team = static_cast<int>((warps + P - 1) / P), teams = team < 4 ? 4 / team : 1;
+    return launch(kernel, dim3(static_cast<unsigned>((a.rows + teams - 1) / teams)), 32 * team * teams, stream, a, team);
+  };
+  // (frames a lane, one, two, four: 8192 x 4099 bf16 94 us, 76, 57; 500 x 1001 4.0, 3.7, 5.5; 64 x
+  // 7001 3.7, 4.3, 4.4)
+  if (warps > 64 || (warps >= 4 && a.rows > 4 * kSms)) return go(norm_frames_kernel<T, W, 4>, 4);
+  if (warps > 32 || (warps >= 2 && a.rows > 2 * kSms)) return go(norm_frames_kernel<T, W, 2>, 2);
+  return go(norm_frames_kernel<T, W, 1>, 1);
+}
+
 // A team's threads: as many warps as a row needs, or 8 or 16 lanes.
 int backward_team(int64_t H, int per_thread) {
   const int64_t need = (H + per_thread - 1) / per_thread;
@@ -539,11 +614,12 @@ cudaError_t launch_backward_v(const NormBackwardArgs& a, int64_t& parts, cudaStr
   constexpr int kBytes = V * static_cast<int>(sizeof(T)), kFew = kBytes == 16 ? 1 : 4, kMost = 2 * kFew;
   // The fewer pieces a thread where their teams fill the SM or rows are few; else the more, of
   // smaller teams (8192 x 4096 bf16: 45.7 us with one piece, 46.1 with two, 8192 x 6144 68.9 and
-  // 64.1, 512 x 8192 12.0 and 13.0).  Rows in registers have room for no more (5000 x 777 19.1 and 31.6).
+  // 64.1, 512 x 8192 12.0 and 13.0).  Rows in registers have room for no more (5000 x 777 19.1 and 31.6,
+  // 8192 x 4099 304 and, read twice, 140).
   const int team = backward_team(a.H, V * kFew);
   const bool few = kBytes < 4 || a.rows <= 8 * kSms || 1024 / team * team >= 960;
   if (team <= 1024 && few) return launch_backward_p<T, W, V, kFew>(a, parts, stream);
-  if (backward_team(a.H, V * kMost) <= 1024) return launch_backward_p<T, W, V, kMost>(a, parts, stream);
+  if (kBytes >= 4 && backward_team(a.H, V * kMost) <= 1024) return launch_backward_p<T, W, V, kMost>(a, parts, stream);
   cudaError_t e = launch(norm_backward_long_kernel<T, W, V>, dim3(static_cast<unsigned>(a.rows)), 512, stream, a);
   if (e != cudaSuccess) return e;
   parts = norm_parts(a.rows, a.H);
@@ -563,11 +639,17 @@ cudaError_t launch_norm(NormArgs a, int dtype, int out_type, cudaStream_t stream
   return with_types(dtype, a.weight_f32, [&](auto t, auto w) {
     using T = decltype(t);
     using W = decltype(w);
-    constexpr int V = Elem<T>::kVec, V4 = 4 / sizeof(T);
+    constexpr int V = Elem<T>::kVec;
     if (out_type == kTypeE4m3) return launch_norm_v<T, W, V, kTypeE4m3>(a, stream);
     if (out_type == kTypeE2m1) return launch_norm_v<T, W, V, kTypeE2m1>(a, stream);
     if (at.by(16)) return launch_norm_v<T, W, V, kTypeF32>(a, stream);
-    return at.by(4) ? launch_norm_v<T, W, V4, kTypeF32>(a, stream) : launch_norm_v<T, W, 1, kTypeF32>(a, stream);
+    // Many rows of 16-bit elements that 4-byte accesses can take, or that are narrow, one by one; the
+    // others by frames.  (8192 rows with the residual: of 4100 49 us and, by frames, 55, of 101 4.2 and
+    // 6.3, of 4099 105 and 59; 64 of 7001 4.6 and 3.8; floats, 4096 x 4099 59 and 43.)
+    if constexpr (sizeof(T) == 2)
+      if (a.rows > 2 * kSms && (at.by(4) || a.H <= 128))
+        return at.by(4) ? launch_norm_v<T, W, 2, kTypeF32>(a, stream) : launch_norm_v<T, W, 1, kTypeF32>(a, stream);
+    return launch_norm_frames<T, W>(a, stream);
   });
 }
 
