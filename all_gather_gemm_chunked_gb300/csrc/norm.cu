@@ -604,10 +604,13 @@ cudaError_t launch_backward_p(const NormBackwardArgs& a, int64_t& parts, cudaStr
   parts = blocks < kSms ? blocks : kSms;
   using R = Ring<T, V, P>;
   const void* kernel = reinterpret_cast<const void*>(norm_backward_kernel<T, W, V, P>);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 * R::kBytes);
-  if (e != cudaSuccess) return e;
+  const size_t smem = static_cast<size_t>(threads) * R::kBytes;
+  if (smem > 47 * 1024) {  // (with the kernel's own 256 bytes: what needs no leave)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 * R::kBytes);
+    if (e != cudaSuccess) return e;
+  }
   void* args[] = {const_cast<NormBackwardArgs*>(&a), const_cast<int*>(&team), const_cast<int*>(&teams)};
-  return launch_args(kernel, dim3(static_cast<unsigned>(parts)), threads, static_cast<size_t>(threads) * R::kBytes, stream, args);
+  return launch_args(kernel, dim3(static_cast<unsigned>(parts)), threads, smem, stream, args);
 }
 template <typename T, typename W, int V>
 cudaError_t launch_backward_v(const NormBackwardArgs& a, int64_t& parts, cudaStream_t stream) {
