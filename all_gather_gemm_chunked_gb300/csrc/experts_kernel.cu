@@ -958,23 +958,24 @@ __device__ void scale_long_role(const ExpertsParams& p, const Table& table,
 // ------------------------------------------------------------------ scales (e2m1)
 // The tile's rows' scales of each stage, as pieces of 128 rows: row r's word at (r % 32) *
 // 16 + (r / 32) * 4.  Both CTAs hold those of all rows (each multiplies its half of the
-// columns with all of them).  Two warps copy the words to their places, and four pass on
-// what has landed, by turns: the release for the pair takes a warp about a microsecond
+// columns with all of them).  Two warps copy the words to their places, each of one k-block, and
+// four pass on what has landed, by turns: the release for the pair takes a warp about a microsecond
 // under load and two where weights stream in, as long as the MMAs of several stages (64 rows
 // of 16384 x 7168 took 22.7 us with two such warps, 20.8 with five; 8512 of 4096 x 4096 65.3 with
-// one and five, 62.8 with two and four, 64.2 with a warp more).  The pieces have a ring of their own, longer than the operands',
-// which covers both ways' latencies.
+// one and five, 62.8 with two and four, 64.2 with a warp more).  The pieces have a ring of their
+// own, longer than the operands', which covers both ways' latencies (four places for five: 53.2 to
+// 57.4).
 // (8192 x 16384 x 8192: 740 us where a warp loads and stores the words itself; 465 with one
 // warp that passes on, in the operands' ring; 480 to 560 with the words stored to TMEM by
 // four warps, whose stores take as long as a k-block's MMAs.)
 template <int BN>
 __device__ void copy4_role(const ExpertsParams& p, const Table& table, const Ring& ring, uint32_t rank, int lane,
-                           int turn, const Guess& guess) {
+                           int part, const Guess& guess) {
   using Units = Schedule<kOpFp4, BN>;
   Units sch(p, table);
   constexpr int kSlots = scale_slots(BN);
   const int32_t KA = (p.red + 127) / 128;
-  int slot = 0, next = turn;  // stages until this warp's next
+  int slot = 0;
   uint32_t phase = 0;
   bool ok = true;
   Unit u;
@@ -987,24 +988,22 @@ __device__ void copy4_role(const ExpertsParams& p, const Table& table, const Rin
     const int32_t words = (u.cnt + 31) / 32;  // (the accumulator's columns behind them are not stored)
     const uint32_t* const xs = p.xs4 + u.row0 + lane;
     for (int32_t kb = u.kb0; kb < u.kb1; kb += kSub) {
-      if (next-- == 0) {
-        next = kCopyWarps - 1;
-        ok = mbar_wait(&ring.pempty[slot], phase ^ 1u, p.timeout_ns, ring.abort, p.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t to = smem_u32(ring.pieces) + slot * row_slot(BN) + lane * 16;
+      ok = mbar_wait(&ring.pempty[slot], phase ^ 1u, p.timeout_ns, ring.abort, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t to = smem_u32(ring.pieces) + slot * row_slot(BN) + lane * 16;
 #pragma unroll
-        for (int a = 0; a < kPieces; ++a) {
-          if (kb * 2 + a >= KA) break;  // (no MMA reads the pieces past K)
-          const uint32_t* const from = xs + static_cast<int64_t>(kb * 2 + a) * p.rows;
+      for (int i = 0; i < kPieces / kCopyWarps; ++i) {
+        const int a = part * (kPieces / kCopyWarps) + i;
+        if (kb * 2 + a >= KA) break;  // (no MMA reads the pieces past K)
+        const uint32_t* const from = xs + static_cast<int64_t>(kb * 2 + a) * p.rows;
 #pragma unroll
-          for (int j = 0; j < BN / 32; ++j)
-            if (j < words)
-              copy_word(to + (a * row_pieces(BN) + j / 4) * kPiece + j % 4 * 4,
-                        j * 32 + lane < u.cnt ? from + j * 32 : p.xs4, j * 32 + lane < u.cnt);
-        }
-        arrive_copied(&ring.praw[slot]);
+        for (int j = 0; j < BN / 32; ++j)
+          if (j < words)
+            copy_word(to + (a * row_pieces(BN) + j / 4) * kPiece + j % 4 * 4,
+                      j * 32 + lane < u.cnt ? from + j * 32 : p.xs4, j * 32 + lane < u.cnt);
       }
+      arrive_copied(&ring.praw[slot]);
       if (++slot == kSlots) {
         slot = 0;
         phase ^= 1u;
@@ -1033,7 +1032,10 @@ __device__ void pass4_role(const ExpertsParams& p, const Table& table, const Rin
     for (int32_t kb = u.kb0; kb < u.kb1; kb += kSub) {
       if (next-- == 0) {
         next = kPassWarps - 1;
-        ok = warp_wait(&ring.praw[slot], phase, p.timeout_ns, ring.abort, p.status);
+        // (The slot's last use first: a wait tells a phase from the one before it, not from the
+        // second before, and this warp has not seen the stage in between.)
+        ok = warp_wait(&ring.pempty[slot], phase ^ 1u, p.timeout_ns, ring.abort, p.status) &&
+             warp_wait(&ring.praw[slot], phase, p.timeout_ns, ring.abort, p.status);
         if (!ok) break;
         fence_proxy_async_shared();
         __syncwarp();
@@ -1805,7 +1807,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     }
     if (OP == kOpFp4)
       for (int s = 0; s < kMaxScaleSlots; ++s) {
-        mbar_init(&ring.praw[s], 32);
+        mbar_init(&ring.praw[s], 32 * kCopyWarps);
         mbar_init(&ring.pfull[s], 2);
         mbar_init(&ring.pempty[s], 1);
       }
