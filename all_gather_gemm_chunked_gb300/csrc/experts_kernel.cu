@@ -65,9 +65,9 @@
 // 32 experts of 4096 x 4096 131 us (the hit weights at 6.9 TB/s).  e4m3: the same product
 // 126 us (2.2 PFLOP/s; bound by the epilogue's work on each k-block), 64 rows of 16384 x
 // 7168 28 us (4.2 TB/s of weights: 28 tiles in two parts are 56 units for 76 pairs).  e2m1:
-// 8192 x 4096 x 4096 54 us (5.1 PFLOP/s), 8192 x 16384 x 8192 330 us (6.7 PFLOP/s: a stage of
+// 8192 x 4096 x 4096 52 us (5.3 PFLOP/s), 8192 x 16384 x 8192 326 us (6.7 PFLOP/s: a stage of
 // 63 KB takes 0.58 us, so that all SMs take in 16 TB/s); 64 rows on 32 experts of 4096 x 4096
-// 43 us (5.8 TB/s), of 16384 x 7168 18.3 us; 8192 on 32 experts of 4096 x 7168 140 us.  A
+// 43 us (5.8 TB/s), of 16384 x 7168 17.9 us; 8192 on 32 experts of 4096 x 7168 138 us.  A
 // call of one tile, repeated, takes 4.4 us, with inputs that change 5.2.
 //
 // Every wait is bounded; on a timeout the kernel records a status word, drains what
