@@ -73,3 +73,45 @@ def test_any_row_special_values():
     h, rstd, y = forward_ref(x[clean], None, w, 1e-6)
     check(r.y[clean], y, (forward_error(1001) + 1.01 * U[torch.bfloat16]) * y.abs() + STEP[torch.bfloat16], "y")
     assert bool(r.y[1].isnan().all()) and bool(r.y[3, 0].isnan()) and bool((r.y[3, 1:] == 0).all())
+
+
+@pytest.mark.parametrize("T,H,dtype", [(700, 4096, torch.bfloat16), (700, 1001, torch.float16), (310, 4099, torch.bfloat16),
+                                       (400, 1401, torch.float32), (40, 100, torch.bfloat16)])
+def test_captured(T, H, dtype):
+    """Forward and gradient in a graph (kernels that ask for more shared memory among them), replayed on other inputs."""
+    g = rng(T * H)
+    x, res, dy, dh = (randn(g, (T, H), dtype) for _ in range(4))
+    w = randn(g, (H,), dtype)
+
+    def step():
+        n = norm.rms_norm(x, w, residual=res)
+        return (n.y, n.h, n.rstd, *norm.rms_norm_backward(dy, n.h, w, n.rstd, dh))
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(2):
+        for t in (x, res, dy, dh):
+            t.copy_(randn(g, (T, H), dtype))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, step()))
+
+
+def test_gradients_on_two_streams():
+    """Two gradients at once: each has its own workspace."""
+    g = rng(77)
+    T, H = 3000, 2056
+    sets = [[randn(g, (T, H), torch.bfloat16) for _ in range(2)] for _ in range(2)]
+    w, rstd = randn(g, (H,), torch.bfloat16), torch.rand(T, generator=g, device="cuda")
+    want = [norm.rms_norm_backward(dy, h, w, rstd) for dy, h in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for (dy, h), s in zip(sets, streams):
+            with torch.cuda.stream(s):
+                got.append(norm.rms_norm_backward(dy, h, w, rstd))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
