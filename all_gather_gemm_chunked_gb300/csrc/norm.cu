@@ -298,6 +298,12 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
 // the thread that reads it, twice: registers for what is in flight would leave room for
 // fewer columns and threads.  (8192 x 8192 bf16 83 us, with rows in registers 97; 8192 x
 // 5120 55 and 68.  Single 16-bit elements, which no such copy takes, stay in registers.)
+//
+// kShifted: rows that begin anywhere, but all operands' at the same distance from an aligned
+// address.  The rows of a team are a multiple of V apart, so that distance is the team's, and
+// its columns begin that much before the row: all pieces are aligned, and those at the row's
+// ends are written element by element.  (8192 x 4099 bf16 63 us; by single elements, with rows
+// read twice, 140.)
 constexpr int kSlots = 2;
 template <typename T, int V, int P, bool kCopied = (V * sizeof(T) >= 4)>
 struct Ring {
@@ -309,6 +315,9 @@ struct Ring {
       : mine(reinterpret_cast<Word*>(bytes) + threadIdx.x), n(static_cast<int>(blockDim.x)) {}
   __device__ __forceinline__ Word* at(int slot, int operand, int i) const { return mine + ((slot * 3 + operand) * P + i) * n; }
   __device__ __forceinline__ void clear(int slot, int operand, int i) { *at(slot, operand, i) = Word{}; }
+  __device__ __forceinline__ void put(int slot, int operand, int i, int v, T x) {  // one element
+    reinterpret_cast<T*>(at(slot, operand, i))[v] = x;
+  }
   __device__ __forceinline__ void ask(int slot, int operand, int i, const T* from) {
     const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(at(slot, operand, i)));
     if constexpr (sizeof(Word) == 16)
@@ -332,22 +341,37 @@ struct Ring<T, V, P, false> {
   __device__ __forceinline__ void ask(int slot, int operand, int i, const T* from) { r[slot][operand][i].load(from); }
   __device__ __forceinline__ void get(int slot, int operand, int i, float (&f)[V]) const { r[slot][operand][i].get(f); }
 };
-template <typename T, typename W, int V, int P>
+template <typename T, typename W, int V, int P, bool kShifted>
 __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBackwardArgs a, int team, int teams) {
   pdl_enter();
   using R = Ring<T, V, P>;
   extern __shared__ __align__(16) uint8_t ring_bytes[];
   __shared__ float part[2][32];
   R ring(ring_bytes);
-  const int number = threadIdx.x / team, thread = threadIdx.x - number * team, c0 = thread * V;
-  const int left = static_cast<int>(a.H) - c0;  // elements of a row from c0 on
+  const int number = threadIdx.x / team, thread = threadIdx.x - number * team, H = static_cast<int>(a.H);
   const int64_t step = static_cast<int64_t>(gridDim.x) * teams, first = static_cast<int64_t>(blockIdx.x) * teams;
+  // of a row of dx: elements from an aligned address to its start
+  auto shift_of = [&](int64_t r) {
+    return kShifted ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<T*>(a.dx) + r * a.H) & 15) / sizeof(T)) : 0;
+  };
+  const int c0 = thread * V - shift_of(first + number);
+  auto inside = [&](int c) { return c < H && (!kShifted || c + V > 0); };  // at least one element
+  auto whole = [&](int c) { return !kShifted || (c >= 0 && c + V <= H); };
   float dw[P][V] = {};
   Weights<W, V> rw[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
+    const int c = c0 + i * team * V;
     rw[i] = Weights<W, V>{};
-    if (i * team * V < left) rw[i].load(static_cast<const W*>(a.weight) + c0 + i * team * V);
+    if (!inside(c)) continue;
+    if (whole(c) && !kShifted) {
+      rw[i].load(static_cast<const W*>(a.weight) + c);
+    } else {
+      W w[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) w[v] = c + v >= 0 && c + v < H ? static_cast<const W*>(a.weight)[c + v] : W(0.0f);
+      __builtin_memcpy(&rw[i], w, sizeof(w));
+    }
   }
 #pragma unroll
   for (int i = 0; i < P; ++i)
@@ -355,7 +379,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBackwardA
     for (int s = 0; s < kSlots; ++s)  // what no copy fills
 #pragma unroll
       for (int o = 0; o < 3; ++o)
-        if (i * team * V >= left || (o == 2 && !a.dh)) ring.clear(s, o, i);
+        if (!inside(c0 + i * team * V) || (o == 2 && !a.dh)) ring.clear(s, o, i);
   const float inv = 1.0f / static_cast<float>(a.H);
   int64_t row = first + number, next = row;  // next: the row to ask for
   float rstd[kSlots];
@@ -365,12 +389,24 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBackwardA
               *dh = static_cast<const T*>(a.dh) + next * a.lddh + c0;
       rstd[slot] = a.rstd[next];
 #pragma unroll
-      for (int i = 0; i < P; ++i)
-        if (i * team * V < left) {
-          ring.ask(slot, 0, i, dy + i * team * V);
-          ring.ask(slot, 1, i, h + i * team * V);
-          if (a.dh) ring.ask(slot, 2, i, dh + i * team * V);
+      for (int i = 0; i < P; ++i) {
+        const int n = i * team * V, c = c0 + n;
+        if (!inside(c)) continue;
+        // (all of the operands, if not of the row)
+        if (whole(c) || ((next > 0 || c >= 0) && (next + 1 < a.rows || c + V <= H))) {
+          ring.ask(slot, 0, i, dy + n);
+          ring.ask(slot, 1, i, h + n);
+          if (a.dh) ring.ask(slot, 2, i, dh + n);
+        } else if constexpr (kShifted) {
+#pragma unroll 1
+          for (int v = 0; v < V; ++v) {
+            if (c + v < 0 || c + v >= H) continue;
+            ring.put(slot, 0, i, v, dy[n + v]);
+            ring.put(slot, 1, i, v, h[n + v]);
+            if (a.dh) ring.put(slot, 2, i, v, dh[n + v]);
+          }
         }
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     next += step;
@@ -394,6 +430,10 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBackwardA
         ring.get(s, 0, i, g);
         ring.get(s, 1, i, x);
         rw[i].get(w);
+        if (kShifted && !whole(c0 + i * team * V))  // (what is not of the row may be anything)
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            if (static_cast<unsigned>(c0 + i * team * V + v) >= static_cast<unsigned>(H)) g[v] = x[v] = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           x[v] *= rs;
@@ -405,7 +445,8 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBackwardA
       T* dx = static_cast<T*>(a.dx) + row * a.H + c0;
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        if (!valid || i * team * V >= left) continue;
+        const int c = c0 + i * team * V;
+        if (!valid || !inside(c)) continue;
         float g[V], x[V], w[V], d[V];
         ring.get(s, 0, i, g);
         ring.get(s, 1, i, x);
@@ -413,7 +454,13 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBackwardA
         rw[i].get(w);
 #pragma unroll
         for (int v = 0; v < V; ++v) g[v] = fmaf(rs, fmaf(-x[v] * rs, dot, g[v] * w[v]), d[v]);
-        store_floats(dx + i * team * V, g);
+        if (whole(c)) {
+          store_floats(dx + i * team * V, g);
+        } else if constexpr (kShifted) {
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            if (c + v >= 0 && c + v < H) dx[i * team * V + v] = Elem<T>::put(g[v]);
+        }
       }
       ask(s);
       row += step;
@@ -421,19 +468,20 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBackwardA
     }
   }
   float* to = a.parts + static_cast<int64_t>(blockIdx.x) * a.H;
-  if (teams > 1) {
+  if (kShifted || teams > 1) {
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     float* sums = reinterpret_cast<float*>(ring_bytes);
 #pragma unroll
     for (int i = 0; i < P; ++i)
 #pragma unroll
-      for (int v = 0; v < V; ++v) sums[number * (team * P * V) + i * team * V + c0 + v] = dw[i][v];
+      for (int v = 0; v < V; ++v) sums[number * (team * P * V) + (i * team + thread) * V + v] = dw[i][v];
     __syncthreads();
+    const int shift = shift_of(first);  // of the block's first team; a row on it is H more, modulo V
     for (int c = threadIdx.x; c < a.H; c += teams * team) {
       float s = 0.0f;
 #pragma unroll 4
-      for (int t = 0; t < teams; ++t) s += sums[t * (team * P * V) + c];
+      for (int t = 0; t < teams; ++t) s += sums[t * (team * P * V) + c + (kShifted ? (shift + t * H) & (V - 1) : 0)];
       to[c] = s;
     }
     return;
@@ -441,7 +489,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBackwardA
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int c = i * team * V;
-    if (c >= left) continue;
+    if (c0 + c >= H) continue;
     if constexpr (V % 4 == 0) {
 #pragma unroll
       for (int v = 0; v < V; v += 4)
@@ -593,9 +641,9 @@ int backward_team(int64_t H, int per_thread) {
   return need <= 8 ? 8 : need <= 16 ? 16 : static_cast<int>((need + 31) / 32 * 32);
 }
 // A block an SM, of as many teams as 1024 threads hold (of few rows no more than that each has one).
-template <typename T, typename W, int V, int P>
+template <typename T, typename W, int V, int P, bool kShifted>
 cudaError_t launch_backward_p(const NormBackwardArgs& a, int64_t& parts, cudaStream_t stream) {
-  const int team = backward_team(a.H, V * P);
+  const int team = backward_team(kShifted ? a.H + V - 1 : a.H, V * P);
   const int64_t most = 1024 / team, each = (a.rows + kSms - 1) / kSms;
   const int whole = team < 32 ? 32 / team : 1;  // teams of a warp
   const int teams = each < most ? static_cast<int>(each + whole - 1) / whole * whole : static_cast<int>(most);
@@ -603,7 +651,7 @@ cudaError_t launch_backward_p(const NormBackwardArgs& a, int64_t& parts, cudaStr
   const int64_t blocks = (a.rows + teams - 1) / teams;
   parts = blocks < kSms ? blocks : kSms;
   using R = Ring<T, V, P>;
-  const void* kernel = reinterpret_cast<const void*>(norm_backward_kernel<T, W, V, P>);
+  const void* kernel = reinterpret_cast<const void*>(norm_backward_kernel<T, W, V, P, kShifted>);
   const size_t smem = static_cast<size_t>(threads) * R::kBytes;
   if (smem > 47 * 1024) {  // (with the kernel's own 256 bytes: what needs no leave)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 * R::kBytes);
@@ -612,18 +660,20 @@ cudaError_t launch_backward_p(const NormBackwardArgs& a, int64_t& parts, cudaStr
   void* args[] = {const_cast<NormBackwardArgs*>(&a), const_cast<int*>(&team), const_cast<int*>(&teams)};
   return launch_args(kernel, dim3(static_cast<unsigned>(parts)), threads, smem, stream, args);
 }
-template <typename T, typename W, int V>
+template <typename T, typename W, int V, bool kShifted = false>
 cudaError_t launch_backward_v(const NormBackwardArgs& a, int64_t& parts, cudaStream_t stream) {
   constexpr int kBytes = V * static_cast<int>(sizeof(T)), kFew = kBytes == 16 ? 1 : 4, kMost = 2 * kFew;
   // The fewer pieces a thread where their teams fill the SM or rows are few; else the more, of
   // smaller teams (8192 x 4096 bf16: 45.7 us with one piece, 46.1 with two, 8192 x 6144 68.9 and
   // 64.1, 512 x 8192 12.0 and 13.0).  Rows in registers have room for no more (5000 x 777 19.1 and 31.6,
   // 8192 x 4099 304 and, read twice, 140).
-  const int team = backward_team(a.H, V * kFew);
+  const int64_t H = kShifted ? a.H + V - 1 : a.H;
+  const int team = backward_team(H, V * kFew);
   const bool few = kBytes < 4 || a.rows <= 8 * kSms || 1024 / team * team >= 960;
-  if (team <= 1024 && few) return launch_backward_p<T, W, V, kFew>(a, parts, stream);
-  if (kBytes >= 4 && backward_team(a.H, V * kMost) <= 1024) return launch_backward_p<T, W, V, kMost>(a, parts, stream);
-  cudaError_t e = launch(norm_backward_long_kernel<T, W, V>, dim3(static_cast<unsigned>(a.rows)), 512, stream, a);
+  if (team <= 1024 && few) return launch_backward_p<T, W, V, kFew, kShifted>(a, parts, stream);
+  if (kBytes >= 4 && backward_team(H, V * kMost) <= 1024) return launch_backward_p<T, W, V, kMost, kShifted>(a, parts, stream);
+  constexpr int kLong = kShifted ? 1 : V;
+  cudaError_t e = launch(norm_backward_long_kernel<T, W, kLong>, dim3(static_cast<unsigned>(a.rows)), 512, stream, a);
   if (e != cudaSuccess) return e;
   parts = norm_parts(a.rows, a.H);
   const int64_t part_rows = (a.rows + parts - 1) / parts;
@@ -669,6 +719,14 @@ cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, cudaStrea
     using W = decltype(w);
     constexpr int V = Elem<T>::kVec, V4 = 4 / sizeof(T);
     if (at.by(16)) return launch_backward_v<T, W, V>(a, parts, stream);
+    // Rows at the same distance from an aligned address in all operands (and no shorter than a
+    // piece, which then reaches no further than the next row), where there are many or they are
+    // wide; others by narrower accesses.  (bf16, shifted and narrow: 8192 x 1001 20.4 us and 31.2, 8192
+    // x 2050 38.5 and 47.1, 64 x 7001 7.8 and 11.7, but 500 x 251 6.4 and 5.4, 100 x 4001 8.9 and 7.2.)
+    auto like_dx = [&](const void* p, int64_t ld) {
+      return !p || (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(a.dx)) & 15) == 0 && (ld - a.H) % V == 0);
+    };
+    if (a.H >= V && (a.rows > 4 * kSms || a.H > 4096) && like_dx(a.dy, a.lddy) && like_dx(a.h, a.ldh) && like_dx(a.dh, a.lddh)) return launch_backward_v<T, W, V, true>(a, parts, stream);
     return at.by(4) ? launch_backward_v<T, W, V4>(a, parts, stream) : launch_backward_v<T, W, 1>(a, parts, stream);
   });
   if (e != cudaSuccess) return e;

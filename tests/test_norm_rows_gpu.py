@@ -115,3 +115,18 @@ def test_gradients_on_two_streams():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("T,H,dtype", [(700, 1001, torch.bfloat16), (700, 1002, torch.float16), (610, 9, torch.bfloat16),
+                                       (3, 4101, torch.bfloat16), (700, 501, torch.float32), (1300, 4099, torch.bfloat16)])
+def test_gradient_of_a_row_stays_apart(T, H, dtype):
+    """Pieces at a row's ends hold elements of its neighbours: not finite ones there change nothing else."""
+    g = rng(T + 7 * H)
+    dy, h, dh = (randn(g, (T, H), dtype) for _ in range(3))
+    w, rstd = randn(g, (H,), dtype), torch.rand(T, generator=g, device="cuda") + 0.5
+    want, dw = norm.rms_norm_backward(dy, h, w, rstd, dh)
+    backward_check(want, dw, dy, h, w, rstd, dh)
+    bad = list(range(1, T, 2))
+    dy[bad[0::3]], h[bad[1::3]], dh[bad[2::3]] = float("nan"), float("inf"), float("nan")
+    got = norm.rms_norm_backward(dy, h, w, rstd, dh)[0]
+    assert torch.equal(got[0::2], want[0::2])
