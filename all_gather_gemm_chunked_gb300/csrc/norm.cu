@@ -671,7 +671,8 @@ cudaError_t launch_backward_v(const NormBackwardArgs& a, int64_t& parts, cudaStr
   const int team = backward_team(H, V * kFew);
   const bool few = kBytes < 4 || a.rows <= 8 * kSms || 1024 / team * team >= 960;
   if (team <= 1024 && few) return launch_backward_p<T, W, V, kFew, kShifted>(a, parts, stream);
-  if (kBytes >= 4 && backward_team(H, V * kMost) <= 1024) return launch_backward_p<T, W, V, kMost, kShifted>(a, parts, stream);
+  if constexpr (kBytes >= 4)
+    if (backward_team(H, V * kMost) <= 1024) return launch_backward_p<T, W, V, kMost, kShifted>(a, parts, stream);
   constexpr int kLong = kShifted ? 1 : V;
   cudaError_t e = launch(norm_backward_long_kernel<T, W, kLong>, dim3(static_cast<unsigned>(a.rows)), 512, stream, a);
   if (e != cudaSuccess) return e;
