@@ -79,8 +79,8 @@ __device__ __forceinline__ float squares(const Piece<T, V>& r, float scale, floa
 }
 // rstd of a row from its team's sums of squares; squares(scale) is a thread's sum of those
 // of its elements times scale.  Where elements from 10^18 on make the sum pass the largest
-// float, it is made anew of elements times 2^-80 (all threads of the block or, with teams of
-// one warp, of the warp take that way together).
+// float, or eps may, it is made anew of elements times 2^-80, eps then times 2^-160 (all threads
+// of the block or, with teams of one warp, of the warp take that way together).
 template <typename F>
 __device__ __forceinline__ float team_rstd(const NormArgs& a, int team_warps, int first, float (*part)[32], const F& squares) {
   constexpr float kSmall = 0x1p-80f, kLarge = 1e37f;  // (32 warps' sums up to that are finite)
@@ -90,8 +90,9 @@ __device__ __forceinline__ float team_rstd(const NormArgs& a, int team_warps, in
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   };
+  auto past = [&](float sum) { return !(sum <= kLarge) || a.eps > kLarge; };
   float sum = over_warp(squares(1.0f));
-  bool large = !(sum <= kLarge);
+  bool large = past(sum);
   if (team_warps > 1) {
     if (lane == 0) part[0][warp] = sum;
     large = __syncthreads_or(large);
@@ -105,10 +106,10 @@ __device__ __forceinline__ float team_rstd(const NormArgs& a, int team_warps, in
       __syncthreads();
       s = over_warp(lane < team_warps ? part[1][first + lane] : 0.0f);
     }
-    if (!(sum <= kLarge)) {
+    if (past(sum)) {
       sum = s;
       scale = kSmall;
-      eps = 0.0f;  // (eps 2^-160)
+      eps = eps * kSmall * kSmall;
     }
   }
   return scale * rsqrtf(fmaf(sum, a.inv_H, eps));
