@@ -78,41 +78,40 @@ __device__ __forceinline__ float squares(const Piece<T, V>& r, float scale, floa
   return sum;
 }
 // rstd of a row from its team's sums of squares; squares(scale) is a thread's sum of those
-// of its elements times scale.  Where elements from 10^18 on make the sum pass the largest
-// float, or eps may, it is made anew of elements times 2^-80, eps then times 2^-160 (all threads
-// of the block or, with teams of one warp, of the warp take that way together).
+// of its elements times scale.  Where the squares, or eps, pass the largest float (elements from
+// 10^18 on), or where squares below the smallest normal one lose bits that eps does not hide
+// (elements below 10^-15, eps below 2^-80), the sum is made anew of scaled elements, eps times the
+// scale's square: of all threads of the block or, with teams of one warp, of the warp together.
+// (A sum from 2^-100 on has lost at most 2^24 halves of 2^-149, a quarter of its last bit.)
 template <typename F>
 __device__ __forceinline__ float team_rstd(const NormArgs& a, int team_warps, int first, float (*part)[32], const F& squares) {
-  constexpr float kSmall = 0x1p-80f, kLarge = 1e37f;  // (32 warps' sums up to that are finite)
+  constexpr float kMost = 1e37f, kDown = 0x1p-80f;  // (32 warps' sums up to that are finite)
+  constexpr float kLeast = 0x1p-100f, kLeastEps = 0x1p-80f, kUp = 0x1p100f;  // (2^24 squares then stay below 2^124)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;  // first: of the team's warps
   auto over_warp = [](float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   };
-  auto past = [&](float sum) { return !(sum <= kLarge) || a.eps > kLarge; };
+  auto scale_of = [&](float sum) {
+    return !(sum <= kMost) || a.eps > kMost ? kDown : sum < kLeast && a.eps < kLeastEps ? kUp : 1.0f;
+  };
   float sum = over_warp(squares(1.0f));
-  bool large = past(sum);
+  bool again = scale_of(sum) != 1.0f;  // (of a warp's share: where a row's sum is small, all its warps' are)
   if (team_warps > 1) {
     if (lane == 0) part[0][warp] = sum;
-    large = __syncthreads_or(large);
+    again = __syncthreads_or(again);
     sum = over_warp(lane < team_warps ? part[0][first + lane] : 0.0f);
   }
-  float scale = 1.0f, eps = a.eps;
-  if (large) {
-    float s = over_warp(squares(kSmall));
-    if (team_warps > 1) {
-      if (lane == 0) part[1][warp] = s;
-      __syncthreads();
-      s = over_warp(lane < team_warps ? part[1][first + lane] : 0.0f);
-    }
-    if (past(sum)) {
-      sum = s;
-      scale = kSmall;
-      eps = eps * kSmall * kSmall;
-    }
+  if (!again) return rsqrtf(fmaf(sum, a.inv_H, a.eps));
+  const float scale = scale_of(sum);
+  sum = over_warp(squares(scale));
+  if (team_warps > 1) {
+    if (lane == 0) part[1][warp] = sum;
+    __syncthreads();
+    sum = over_warp(lane < team_warps ? part[1][first + lane] : 0.0f);
   }
-  return scale * rsqrtf(fmaf(sum, a.inv_H, eps));
+  return scale * rsqrtf(fmaf(sum, a.inv_H, a.eps * scale * scale));
 }
 
 // Where a thread's piece of y goes, and the next, n elements on, a multiple of 128 where y

@@ -24,9 +24,10 @@ extern "C" {
  * For each of the rows (rows x H, any of the three types)
  *   h = x + residual, rounded to the rows' type (without residual, NULL: x itself),
  *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight,
- * in 32 bits, y rounded once.  weight: H elements of the rows' type or floats.  h
- * (contiguous; ignored without residual) and rstd (rows floats; may be NULL) are what the
- * gradient needs.  Outputs are contiguous and overlap no input.  eps >= 0.
+ * in 32 bits, y rounded once.  The squares may leave the range of floats; an rstd beyond it
+ * (rows of magnitudes below 2^-128, eps as small) is infinite.  weight: H elements of the rows'
+ * type or floats.  h (contiguous; ignored without residual) and rstd (rows floats; may be NULL)
+ * are what the gradient needs.  Outputs are contiguous and overlap no input.  eps >= 0.
  * rows < 2^31, 1 <= H <= 2^24.
  */
 int ag_norm_rms(int64_t rows, int64_t H, int dtype, const void *x, int64_t ldx,
