@@ -671,16 +671,21 @@ cudaError_t launch_backward_v(const NormBackwardArgs& a, int64_t& parts, cudaStr
   const int team = backward_team(H, V * kFew);
   const bool few = kBytes < 4 || a.rows <= 8 * kSms || 1024 / team * team >= 960;
   if (team <= 1024 && few) return launch_backward_p<T, W, V, kFew, kShifted>(a, parts, stream);
-  if constexpr (kBytes >= 4)
-    if (backward_team(H, V * kMost) <= 1024) return launch_backward_p<T, W, V, kMost, kShifted>(a, parts, stream);
-  constexpr int kLong = kShifted ? 1 : V;
-  cudaError_t e = launch(norm_backward_long_kernel<T, W, kLong>, dim3(static_cast<unsigned>(a.rows)), 512, stream, a);
-  if (e != cudaSuccess) return e;
-  parts = norm_parts(a.rows, a.H);
-  const int64_t part_rows = (a.rows + parts - 1) / parts;
-  const dim3 grid(static_cast<unsigned>((a.H + kColumnThreads - 1) / kColumnThreads), static_cast<unsigned>(parts));
-  return launch(norm_columns_kernel<T>, grid, kColumnThreads, stream, a, part_rows);
+  if constexpr (kShifted) {  // (where shifted_fits)
+    return launch_backward_p<T, W, V, kMost, true>(a, parts, stream);
+  } else {
+    if constexpr (kBytes >= 4)
+      if (backward_team(H, V * kMost) <= 1024) return launch_backward_p<T, W, V, kMost, false>(a, parts, stream);
+    cudaError_t e = launch(norm_backward_long_kernel<T, W, V>, dim3(static_cast<unsigned>(a.rows)), 512, stream, a);
+    if (e != cudaSuccess) return e;
+    parts = norm_parts(a.rows, a.H);
+    const int64_t part_rows = (a.rows + parts - 1) / parts;
+    const dim3 grid(static_cast<unsigned>((a.H + kColumnThreads - 1) / kColumnThreads), static_cast<unsigned>(parts));
+    return launch(norm_columns_kernel<T>, grid, kColumnThreads, stream, a, part_rows);
+  }
 }
+// Whether a row's shifted pieces of V elements fit a team.
+bool shifted_fits(int64_t H, int V) { return backward_team(H + V - 1, 2 * V) <= 1024; }
 }  // namespace
 
 cudaError_t launch_norm(NormArgs a, int dtype, int out_type, cudaStream_t stream) {
@@ -722,12 +727,14 @@ cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, cudaStrea
     if (at.by(16)) return launch_backward_v<T, W, V>(a, parts, stream);
     // Rows at the same distance from an aligned address in all operands (and no shorter than a
     // piece, which then reaches no further than the next row), where there are many or they are
-    // wide; others by narrower accesses.  (bf16, shifted and narrow: 8192 x 1001 20.4 us and 31.2, 8192
+    // wide, and a team holds them; others by narrower accesses.  (bf16, shifted and narrow: 8192 x 1001 20.4 us and 31.2, 8192
     // x 2050 38.5 and 47.1, 64 x 7001 7.8 and 11.7, but 500 x 251 6.4 and 5.4, 100 x 4001 8.9 and 7.2.)
     auto like_dx = [&](const void* p, int64_t ld) {
       return !p || (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(a.dx)) & 15) == 0 && (ld - a.H) % V == 0);
     };
-    if (a.H >= V && (a.rows > 4 * kSms || a.H > 4096) && like_dx(a.dy, a.lddy) && like_dx(a.h, a.ldh) && like_dx(a.dh, a.lddh)) return launch_backward_v<T, W, V, true>(a, parts, stream);
+    if (a.H >= V && (a.rows > 4 * kSms || a.H > 4096) && shifted_fits(a.H, V) && like_dx(a.dy, a.lddy) && like_dx(a.h, a.ldh) &&
+        like_dx(a.dh, a.lddh))
+      return launch_backward_v<T, W, V, true>(a, parts, stream);
     return at.by(4) ? launch_backward_v<T, W, V4>(a, parts, stream) : launch_backward_v<T, W, 1>(a, parts, stream);
   });
   if (e != cudaSuccess) return e;
