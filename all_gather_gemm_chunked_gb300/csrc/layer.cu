@@ -109,7 +109,7 @@ int ag_norm_rms_quantized(int64_t rows, int64_t H, int dtype, const void* x, int
 
 int64_t ag_norm_rms_backward_workspace(int64_t rows, int64_t H) {
   if (int rc = check_rows(rows, H, AG_MOE_F32)) return rc;
-  return agg::norm_parts(rows, H) * H * 4;
+  return agg::norm_parts(rows) * H * 4;
 }
 
 int ag_norm_rms_backward(int64_t rows, int64_t H, int dtype, const void* dy, int64_t lddy, const void* h, int64_t ldh,

@@ -46,7 +46,7 @@ struct NormBackwardArgs {
   float* parts;    // [norm_parts][H]
 };
 // Sums of the weight's gradient that are made first and then added.
-int64_t norm_parts(int64_t rows, int64_t H);
+int64_t norm_parts(int64_t rows);
 cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, cudaStream_t stream);
 
 struct GateArgs {

@@ -609,12 +609,15 @@ cudaError_t launch_norm_v(const NormArgs& a, cudaStream_t stream) {
   constexpr bool kVec = V * sizeof(T) == 16;
   constexpr int kFew = kVec ? 1 : 4, kMost = kVec ? 4 : 8;
   const int64_t pieces = (a.H + V - 1) / V;
-  if (pieces > 1024 * kMost)
-    return launch(norm_long_kernel<T, W, V, OUT>, dim3(static_cast<unsigned>(a.rows)), 1024, stream, a);
-  // Few rows are spread over more threads; of many, more of a row is in flight in a thread
-  // (8192 x 4096 bf16: 40.0 us with four pieces, 40.9 with two, without a residual 21.7 and
-  // 30.3; 64 x 7168 2.6 with one, 3.1 with two).  Rows of a few pieces have no more.
-  if (pieces > 1024 * kFew || (a.rows > 2 * kSms && pieces >= 32 * kMost)) return launch_norm_p<T, W, V, kMost, OUT>(a, pieces, stream);
+  if constexpr (V > 1) {  // (single elements: narrow rows alone)
+    if (pieces > 1024 * kMost)
+      return launch(norm_long_kernel<T, W, V, OUT>, dim3(static_cast<unsigned>(a.rows)), 1024, stream, a);
+    // Few rows are spread over more threads; of many, more of a row is in flight in a thread
+    // (8192 x 4096 bf16: 40.0 us with four pieces, 40.9 with two, without a residual 21.7 and
+    // 30.3; 64 x 7168 2.6 with one, 3.1 with two).  Rows of a few pieces have no more.
+    if (pieces > 1024 * kFew || (a.rows > 2 * kSms && pieces >= 32 * kMost))
+      return launch_norm_p<T, W, V, kMost, OUT>(a, pieces, stream);
+  }
   return launch_norm_p<T, W, V, kFew, OUT>(a, pieces, stream);
 }
 
@@ -678,7 +681,7 @@ cudaError_t launch_backward_v(const NormBackwardArgs& a, int64_t& parts, cudaStr
       if (backward_team(H, V * kMost) <= 1024) return launch_backward_p<T, W, V, kMost, false>(a, parts, stream);
     cudaError_t e = launch(norm_backward_long_kernel<T, W, V>, dim3(static_cast<unsigned>(a.rows)), 512, stream, a);
     if (e != cudaSuccess) return e;
-    parts = norm_parts(a.rows, a.H);
+    parts = norm_parts(a.rows);
     const int64_t part_rows = (a.rows + parts - 1) / parts;
     const dim3 grid(static_cast<unsigned>((a.H + kColumnThreads - 1) / kColumnThreads), static_cast<unsigned>(parts));
     return launch(norm_columns_kernel<T>, grid, kColumnThreads, stream, a, part_rows);
@@ -712,7 +715,7 @@ cudaError_t launch_norm(NormArgs a, int dtype, int out_type, cudaStream_t stream
   });
 }
 
-int64_t norm_parts(int64_t rows, int64_t) { return rows < kMaxParts ? rows : kMaxParts; }
+int64_t norm_parts(int64_t rows) { return rows < kMaxParts ? rows : kMaxParts; }
 
 cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, cudaStream_t stream) {
   if (a.rows == 0) return cudaMemsetAsync(a.dweight, 0, static_cast<size_t>(a.H) * 4, stream);
