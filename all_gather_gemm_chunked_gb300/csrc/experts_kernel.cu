@@ -1137,9 +1137,7 @@ __device__ void mma_role(const ExpertsParams& p, const Table& table, const Ring&
         if (OP == kOpFp8Long) ++acc;
       }
       if (!ok) break;
-      if (elect_one()) {
-        mma_commit_pair_both(&ring.empty[stage]);
-      }
+      if (elect_one()) mma_commit_pair_both(&ring.empty[stage]);
       if (++stage == kStagesX) stage = 0;
       if (OP != kOpFp8Long) {
         left -= n_sub;
