@@ -27,7 +27,7 @@ def swiglu(x: torch.Tensor, stream=None) -> torch.Tensor:
 def swiglu_quantized(x: torch.Tensor, codes: str, stream=None):
     """(codes, scales): what ``fp8.quantize_rows`` ("e4m3", N a multiple of 16) or
     ``fp4.quantize_rows`` ("mxfp4", of 32) would make of the unrounded y.  x is 16-byte
-    aligned."""
+    aligned, its rows a multiple of 16 bytes apart; others are refused (:func:`swiglu` takes any)."""
     if stream is not None:
         return _on(stream, swiglu_quantized, x, codes)
     if codes not in CODES:

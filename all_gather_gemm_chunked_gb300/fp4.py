@@ -29,7 +29,8 @@ E8M0 = torch.float8_e8m0fnu
 def quantize_rows(x: torch.Tensor, routing=None, stream=None):
     """(codes (rows, K / 2) uint8, scales (ceil(K / 128), rows, 4) float8_e8m0fnu) of the rows
     of x (K a multiple of 32): the scale of row r and block b of 32 at [b // 4, r, b % 4].
-    With a ``moe.Routing`` the rows are the experts' rows of x, as ``moe.gather`` gives them."""
+    With a ``moe.Routing`` the rows are the experts' rows of x, as ``moe.gather`` gives them.
+    x is 16-byte aligned, its rows a multiple of 16 bytes apart."""
     if stream is not None:
         return _on(stream, quantize_rows, x, routing)
     if routing is None:
@@ -39,7 +40,7 @@ def quantize_rows(x: torch.Tensor, routing=None, stream=None):
 
 def quantize_weights(w: torch.Tensor, stream=None):
     """(codes (..., N, K / 2) uint8, scales (..., ceil(N / 128), ceil(K / 128), 32, 4, 4)
-    float8_e8m0fnu) of weights (E, K, N) or (K, N), K a multiple of 32 and N of 8, laid out as
+    float8_e8m0fnu) of contiguous, 16-byte aligned weights (E, K, N) or (K, N), K a multiple of 32 and N of 8, laid out as
     the product reads them: the scale of column n and block b of 32 along K at
     [n // 128, b // 4, n % 32, n % 128 // 32, b % 4]."""
     if stream is not None:

@@ -49,7 +49,8 @@ def rms_norm_quantized(x: torch.Tensor, weight: torch.Tensor, codes: str, eps: f
                        residual: Optional[torch.Tensor] = None, stream=None):
     """(codes, scales, h): :func:`rms_norm` with y as the rows of a product, what
     ``fp8.quantize_rows`` ("e4m3", H a multiple of 16) or ``fp4.quantize_rows`` ("mxfp4", of
-    32) would make of the unrounded y.  x and the residual are 16-byte aligned."""
+    32) would make of the unrounded y.  x, the residual and the weight are 16-byte aligned, rows
+    a multiple of 16 bytes apart; others are refused (:func:`rms_norm` takes any)."""
     if stream is not None:
         return _on(stream, rms_norm_quantized, x, weight, codes, eps, residual)
     if codes not in CODES:
