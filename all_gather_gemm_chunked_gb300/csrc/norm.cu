@@ -731,8 +731,10 @@ cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, cudaStrea
     if (at.by(16)) return launch_backward_v<T, W, V>(a, parts, stream);
     // Rows at the same distance from an aligned address in all operands (and no shorter than a
     // piece, which then reaches no further than the next row), where there are many or they are
-    // wide, and a team holds them; others by narrower accesses.  (bf16, shifted and narrow: 8192 x 1001 20.4 us and 31.2, 8192
-    // x 2050 38.5 and 47.1, 64 x 7001 7.8 and 11.7, but 500 x 251 6.4 and 5.4, 100 x 4001 8.9 and 7.2.)
+    // wide, and a team holds them; others by narrower accesses.  (bf16, shifted and narrow: 8192 x
+    // 1001 20.4 us and 31.2, 8192 x 2050 38.5 and 47.1, 64 x 7001 7.8 and 11.7, but 500 x 251 6.4 and
+    // 5.4, 100 x 4001 8.9 and 7.2.  2000 x 16380, which no team holds shifted: read twice by single
+    // elements 165, by 4 bytes 87.)
     auto like_dx = [&](const void* p, int64_t ld) {
       return !p || (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(a.dx)) & 15) == 0 && (ld - a.H) % V == 0);
     };
