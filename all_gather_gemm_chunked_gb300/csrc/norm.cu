@@ -14,7 +14,7 @@
 // the rows' type or to codes (put_codes).
 //
 // Measured, 8192 x 4096 bf16: with the residual 40.1 us (6.7 TB/s), without 22.2 (6.1), with it and
-// to e4m3 37.0 (6.4), to 4 bits 38.5 (5.7); gradient 47.0 (5.7 TB/s: its second launch and the end
+// to e4m3 37.1 (6.4), to 4 bits 34.3 (6.4); gradient 47.0 (5.7 TB/s: its second launch and the end
 // of the first take 5 us).  64 x 7168 with the residual 2.7 us.
 
 #include <type_traits>
@@ -77,6 +77,16 @@ __device__ __forceinline__ float squares(const Piece<T, V>& r, float scale, floa
   }
   return sum;
 }
+// 1 / sqrt(m), to the nearest but for about 2^-40: the approximate root (2 ulps) after one step of
+// Newton's iteration, r + r (1 - m r^2) / 2, with m r in two parts.  It is every element's factor: by
+// the approximate root alone floats of y were off by a twelfth more, and e4m3 codes next to ties a
+// little oftener; with an exact root and division 8192 x 4096 bf16 took 41.3 us, so 40.8.  (Zero and
+// infinite m have no step.)
+__device__ __forceinline__ float inverse_root(float m) {
+  const float r = rsqrtf(m), p = m * r, rest = fmaf(m, r, -p);
+  const float better = fmaf(0.5f * r, fmaf(-rest, r, fmaf(-p, r, 1.0f)), r);
+  return better == better ? better : r;
+}
 // rstd of a row from its team's sums of squares; squares(scale) is a thread's sum of those
 // of its elements times scale.  Where the squares, or eps, pass the largest float (elements from
 // 10^18 on), or where squares below the smallest normal one lose bits that eps does not hide
@@ -103,15 +113,18 @@ __device__ __forceinline__ float team_rstd(const NormArgs& a, int team_warps, in
     again = __syncthreads_or(again);
     sum = over_warp(lane < team_warps ? part[0][first + lane] : 0.0f);
   }
-  if (!again) return rsqrtf(fmaf(sum, a.inv_H, a.eps));
-  const float scale = scale_of(sum);
-  sum = over_warp(squares(scale));
-  if (team_warps > 1) {
-    if (lane == 0) part[1][warp] = sum;
-    __syncthreads();
-    sum = over_warp(lane < team_warps ? part[1][first + lane] : 0.0f);
+  float scale = 1.0f, m = fmaf(sum, a.inv_H, a.eps);
+  if (again) {
+    scale = scale_of(sum);
+    sum = over_warp(squares(scale));
+    if (team_warps > 1) {
+      if (lane == 0) part[1][warp] = sum;
+      __syncthreads();
+      sum = over_warp(lane < team_warps ? part[1][first + lane] : 0.0f);
+    }
+    m = fmaf(sum, a.inv_H, a.eps * scale * scale);
   }
-  return scale * rsqrtf(fmaf(sum, a.inv_H, a.eps * scale * scale));
+  return scale * inverse_root(m);
 }
 
 // Where a thread's piece of y goes, and the next, n elements on, a multiple of 128 where y

@@ -80,3 +80,17 @@ def test_zeros_and_not_finite_values_without_eps():
     _, rstd, y = forward_ref(x[3:], None, w, 0.0)
     check(r.rstd[3:], rstd, forward_error(256) * rstd, "rstd")
     check(r.y[3:], y, (forward_error(256) + 1.01 * U[x.dtype]) * y.abs(), "y")
+
+
+@pytest.mark.parametrize("T,H", [(4000, 64), (900, 2048), (700, 16384), (64, 32768)])
+def test_rstd_is_rounded_once(T, H):
+    """Whole numbers whose squares' sum is a float in any order, and a mean that is one: rstd is the nearest float or, within
+    2^-10 of a tie, its neighbour."""
+    x = torch.randint(-16, 17, (T, H), generator=rng(H), device="cuda").float()  # sums of H squares: below 2^8 H <= 2^23
+    x[:, 0] = torch.randint(1, 17, (T,), generator=rng(T), device="cuda").float()
+    w = torch.ones(H, device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        got = norm.rms_norm(x.to(dtype), w.to(dtype), 0.0).rstd.double()
+        want = 1 / torch.sqrt((x.double() ** 2).sum(1) / H)
+        step = torch.exp2(torch.floor(torch.log2(want)) - 23)
+        assert float(((got - want).abs() / step).max()) <= 0.5 + 2.0 ** -10
